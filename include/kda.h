@@ -352,6 +352,121 @@ KDA_API int kda_chunk_fwd_noalloc(const void* q, const void* k, const void* v,
                                   void* out, float lower_bound, int state_dtype,
                                   kda_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Operators beside the KDA forward: the rest of a linear-attention layer.
+ * They share its conventions: packed tokens, the state pool, host checks
+ * before any work is enqueued, kda_last_error(), the caller's stream.
+ * ------------------------------------------------------------------------ */
+
+enum kda_dtype { KDA_F32 = 0, KDA_BF16 = 1, KDA_F16 = 2 };
+
+/*
+ * kda_lin_attn_fwd — linear attention with a decay for each head over packed
+ * sequences, the states in the paged pool read and written in-kernel.  For
+ * every sequence and head h, with a V-first state S in R^{V x K}, K = V = 128:
+ *
+ *     S_t = exp(g_t) S_{t-1} + v_t k_t^T,     o_t = scale * S_t q_t
+ *
+ *   q, k             device bf16 [total_tokens][num_qk_heads][128]; head h
+ *                    reads q/k head h / (num_heads / num_qk_heads).
+ *   v                device bf16 [total_tokens][num_heads][128].
+ *   *_stride_t/_h    elements between tokens and between heads of q, k and v
+ *                    (views of one projection's output, for instance);
+ *                    multiples of 8, at least 128, bases 16-byte aligned.
+ *   log_decay        device fp32 g, <= 0: [num_heads], or, with
+ *                    decay_per_token, [total_tokens][num_heads] dense.  -inf
+ *                    clears the state before the token's write; values below
+ *                    -104 act as -inf does (exp underflows in fp32).
+ *   num_qk_heads     divides num_heads.
+ *   scale            factor on the outputs (usually 1/sqrt(128)).
+ *   cu_seqlens, cu_seqlens_host, state_cache ... has_initial_state, out,
+ *   state_dtype      as in kda_chunk_fwd, with the same reports of bad slots;
+ *                    out is dense [total_tokens][num_heads][128].
+ *   workspace        at least kda_lin_attn_workspace_size() bytes, 256-byte
+ *                    aligned; kda_check_status() reads its status word.
+ *
+ * Accumulation is in fp32; an fp32 pool receives the state to fp32 accuracy.
+ * The order of summation, and so every bit of the result, depends on the
+ * bounds, the head counts and the GPU's SM count alone.  A token's output depends on its own
+ * sequence's tokens up to it alone, also where others hold infinities or NaN.
+ *
+ * Graph capture, synchronisation and bounds follow kda_chunk_fwd.
+ */
+KDA_API int kda_lin_attn_fwd(const void* q, int64_t q_stride_t, int64_t q_stride_h,
+                  const void* k, int64_t k_stride_t, int64_t k_stride_h,
+                  const void* v, int64_t v_stride_t, int64_t v_stride_h,
+                  const float* log_decay, int decay_per_token,
+                  const int32_t* cu_seqlens, const int32_t* cu_seqlens_host,
+                  int32_t num_seqs, int64_t total_tokens, int32_t num_heads,
+                  int32_t num_qk_heads,
+                  void* state_cache, int64_t state_stride0, int32_t num_slots,
+                  const int32_t* state_indices, const uint8_t* has_initial_state,
+                  void* out, float scale, int state_dtype,
+                  void* workspace, size_t workspace_bytes, kda_stream_t stream);
+
+/* Bytes of workspace a kda_lin_attn_fwd call with these sizes needs; 0 for
+ * invalid sizes. */
+KDA_API size_t kda_lin_attn_workspace_size(int64_t total_tokens, int32_t num_seqs,
+                  int32_t num_heads);
+
+/*
+ * kda_rope — rotary positions.  For each token t with position p, each head x
+ * and each pair i < rot_dim / 2, with the angle a = p * inv_freq[i]:
+ *
+ *     y[one] = factor * (x[one] cos a - x[two] sin a)
+ *     y[two] = factor * (x[two] cos a + x[one] sin a)
+ *
+ * (one, two) = (i, i + rot_dim / 2) for KDA_ROPE_HALF and (2i, 2i + 1) for
+ * KDA_ROPE_INTERLEAVED; the dimensions from rot_dim on are copied.  `inverse`
+ * turns the other way: the gradient with respect to x is the inverse rotation
+ * of the gradient with respect to y.
+ *
+ * The angle is reduced exactly: inv_freq / 2 pi is held as a 64-bit fraction
+ * of a turn and multiplied by the integer position modulo one turn, so
+ * positions of any size keep an error below 1e-6 radians up to |p| = 2^28.
+ * The tensors of one call (q and k) share the positions and the frequencies.
+ *
+ *   tensors       1 or 2 of them; num_heads 0 skips one.  `in` and `out` are
+ *                 device [total_tokens][num_heads][head_dim] of dtype, dense in
+ *                 the last dimension, strides in elements; out == in with the
+ *                 same strides works in place, any other overlap is refused.
+ *   positions     device int32 or int64 (position_bytes 4 or 8), one per token.
+ *   inv_freq      device fp64 [rot_dim / 2], radians per position, in (-2 pi, 2 pi).
+ *   head_dim      1 .. 1024; rot_dim even, 0 .. head_dim.
+ */
+enum kda_rope_layout { KDA_ROPE_HALF = 0, KDA_ROPE_INTERLEAVED = 1 };
+typedef struct kda_rope_tensor {
+    const void* in;
+    void* out;
+    int64_t in_stride_t, in_stride_h, out_stride_t, out_stride_h;
+    int32_t num_heads;
+} kda_rope_tensor;
+KDA_API int kda_rope(const kda_rope_tensor* tensors, int32_t num_tensors,
+                  const void* positions, int position_bytes, const double* inv_freq,
+                  int64_t total_tokens, int32_t head_dim, int32_t rot_dim, int layout,
+                  float factor, int inverse, int dtype, kda_stream_t stream);
+
+/*
+ * kda_gated_norm — root-mean-square norm of each row, with a weight and a gate:
+ *
+ *     y = x / sqrt(mean(x^2) + eps) * weight * act(gate)
+ *
+ *   x, gate, out   device [total_tokens][num_heads][head_dim] of dtype, dense
+ *                  in the last dimension, strides in elements; gate may be
+ *                  NULL (no gate).  out == x with the same strides works in
+ *                  place, any other overlap of out with x or gate is refused.
+ *   weight         device fp32 [head_dim], or NULL for ones.
+ *   activation     KDA_ACT_SIGMOID, KDA_ACT_SILU or KDA_ACT_NONE (the gate as it is).
+ *   head_dim       1 .. 8192;  eps >= 0.
+ */
+enum kda_activation { KDA_ACT_NONE = 0, KDA_ACT_SIGMOID = 1, KDA_ACT_SILU = 2 };
+KDA_API int kda_gated_norm(const void* x, int64_t x_stride_t, int64_t x_stride_h,
+                  const void* gate, int64_t gate_stride_t, int64_t gate_stride_h,
+                  const float* weight,
+                  void* out, int64_t out_stride_t, int64_t out_stride_h,
+                  int64_t total_tokens, int32_t num_heads, int32_t head_dim,
+                  float eps, int activation, int dtype, kda_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

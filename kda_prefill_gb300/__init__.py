@@ -1,4 +1,6 @@
-"""Python binding of the GB300 chunkwise KDA forward library (``libkda.so``).
+"""Python binding of the GB300 chunkwise KDA forward library (``libkda.so``) and
+the operators beside it (linear attention with a decay for each head, rotary
+positions, gated norm; see ``ops``).
 
 Argument marshalling only: every step of the forward runs in the CUDA kernels
 behind the C ABI declared in ``include/kda.h``.  PyTorch provides device
@@ -18,6 +20,7 @@ __all__ = [
     "release_cache", "cache_entries", "load_library", "KDAError", "STATE_DTYPES",
     "set_kernel_timing", "kernel_times", "set_fused_launch", "check_status",
     "debug_wait_timeout", "STATUS_WAIT_TIMEOUT", "STATUS_SMEM_ALIGN", "STATUS_BAD_SLOT", "STATUS_BOUNDS_MISMATCH",
+    "lin_attn_fwd", "lin_attn_workspace_size", "rope", "rope_frequencies", "gated_norm",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -38,7 +41,8 @@ EXPORTED = (
     "kda_plan_chunks", "kda_last_error", "kda_release_cache", "kda_cache_entries",
     "kda_set_kernel_timing", "kda_kernel_times", "kda_kernel_name", "kda_chunk_fwd_raw_bf16",
     "kda_chunk_fwd_noalloc", "kda_set_fused_launch", "kda_check_status",
-    "kda_debug_wait_timeout",
+    "kda_debug_wait_timeout", "kda_lin_attn_fwd", "kda_lin_attn_workspace_size", "kda_rope",
+    "kda_gated_norm",
 )
 
 
@@ -114,6 +118,29 @@ def load_library(path: str = LIB_PATH):
         _vp, _i64, _i32, _vp, _vp,      # state_cache stride0 slots indices has_init
         _vp, ctypes.c_float, ctypes.c_int,  # out lower_bound state_dtype
         _vp,                            # stream
+    ]
+    lib.kda_lin_attn_workspace_size.restype = ctypes.c_size_t
+    lib.kda_lin_attn_workspace_size.argtypes = [_i64, _i32, _i32]
+    lib.kda_lin_attn_fwd.restype = ctypes.c_int
+    lib.kda_lin_attn_fwd.argtypes = [
+        _vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _i64,  # q k v with token and head strides
+        _vp, ctypes.c_int,              # log_decay decay_per_token
+        _vp, _vp, _i32, _i64, _i32, _i32,  # cu_seqlens cu_seqlens_host N T H Hqk
+        _vp, _i64, _i32, _vp, _vp,      # state_cache stride0 slots indices has_init
+        _vp, ctypes.c_float, ctypes.c_int,  # out scale state_dtype
+        _vp, ctypes.c_size_t, _vp,      # workspace bytes stream
+    ]
+    lib.kda_rope.restype = ctypes.c_int
+    lib.kda_rope.argtypes = [
+        _vp, _i32, _vp, ctypes.c_int, _vp,  # tensors count positions position_bytes inv_freq
+        _i64, _i32, _i32, ctypes.c_int,     # T head_dim rot_dim layout
+        ctypes.c_float, ctypes.c_int, ctypes.c_int, _vp,  # factor inverse dtype stream
+    ]
+    lib.kda_gated_norm.restype = ctypes.c_int
+    lib.kda_gated_norm.argtypes = [
+        _vp, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _i64, _i64,  # x gate weight out
+        _i64, _i32, _i32, ctypes.c_float,   # T H D eps
+        ctypes.c_int, ctypes.c_int, _vp,    # activation dtype stream
     ]
     if path == LIB_PATH:
         _lib = lib
@@ -368,3 +395,7 @@ def chunk_fwd_dense(q, k, v, g_raw, beta_raw, cu_seqlens, *, final_state, out,
         _ptr(ws), ws.numel() * ws.element_size(), s.cuda_stream)
     _check(rc, lib)
     return out, final_state
+
+
+from .ops import (  # noqa: E402  (needs the names above)
+    gated_norm, lin_attn_fwd, lin_attn_workspace_size, rope, rope_frequencies)

@@ -22,6 +22,7 @@
 
 #include "kda.h"
 #include "kda_internal.h"
+#include "kda_ops.h"
 
 namespace {
 
@@ -90,6 +91,8 @@ struct MetaLayout {
     int64_t n_chunks = 0;
     int32_t n_long = 0, n_short = 0;
     int32_t max_long_chunks = 0;  // chunks of the longest sequence the chunked kernels take
+    int64_t long_tokens = 0;      // tokens of the sequences the chunked kernels take
+    int32_t max_long = 0;         // tokens of the longest of them
     size_t off_cu = 0, off_seq_off = 0, off_chunk_seq = 0, off_chunk_tok = 0;  // int32 units
     size_t off_long = 0, off_short = 0;
     size_t words = 0;
@@ -103,7 +106,13 @@ MetaLayout meta_layout(const int32_t* cu, int32_t N) {
     for (int32_t n = 0; n < N; ++n) {
         const int64_t len = (int64_t)cu[n + 1] - cu[n];
         L.n_chunks += routed_chunks(len);
-        if (is_short(len)) ++L.n_short; else ++L.n_long;
+        if (is_short(len)) {
+            ++L.n_short;
+        } else {
+            ++L.n_long;
+            L.long_tokens += len;
+            L.max_long = std::max<int32_t>(L.max_long, (int32_t)len);
+        }
         L.max_long_chunks = std::max<int32_t>(L.max_long_chunks, (int32_t)routed_chunks(len));
     }
     size_t o = 0;
@@ -455,6 +464,33 @@ struct StateArgs {
     int32_t num_slots;  // paged calls: slots are checked against it on the device; 0 = dense
 };
 
+// The call's metadata entry, with the cache locked: reads the bounds back first
+// when the host does not have them.
+int find_tables(const int32_t* cu_dev, const int32_t* cu_host, int32_t N, int64_t T,
+                cudaStream_t stream, bool capturing, MetaEntry** m) {
+    std::vector<int32_t> readback;
+    if (!cu_host) {
+        if (capturing)
+            return fail(KDA_ERR_CAPTURE_MISS,
+                        "device bounds cannot be read back while the stream is capturing; "
+                        "pass cu_seqlens_host");
+        readback.resize((size_t)N + 1);
+        cudaEvent_t* done = nullptr;
+        void* host = cache().ring.acquire(readback.size() * sizeof(int32_t), &done);
+        if (!host) return fail(KDA_ERR_CUDA, "pinned staging allocation failed");
+        cudaError_t e = cudaMemcpyAsync(host, cu_dev, readback.size() * sizeof(int32_t),
+                                        cudaMemcpyDeviceToHost, stream);
+        if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
+        if (e == cudaSuccess) std::memcpy(readback.data(), host, readback.size() * sizeof(int32_t));
+        cudaEventRecord(*done, stream);
+        if (e != cudaSuccess) return cuda_fail(e, "read-back of cu_seqlens");
+        cu_host = readback.data();
+        int rc = check_host_bounds(cu_host, N, T);
+        if (rc != KDA_OK) return rc;
+    }
+    return cache().get(cu_host, N, stream, capturing, m);
+}
+
 int run_forward(const void* q, const void* k, const void* v, const void* g_raw,
                 const void* beta_raw, int raw_bf16, const int32_t* cu_dev,
                 const int32_t* cu_host, int32_t N, int64_t T, int32_t H, const StateArgs& st,
@@ -466,29 +502,8 @@ int run_forward(const void* q, const void* k, const void* v, const void* g_raw,
     const bool capturing = (cap != cudaStreamCaptureStatusNone);
 
     std::lock_guard<std::mutex> lock(cache().mu);
-    std::vector<int32_t> readback;
-    if (!cu_host) {
-        if (capturing)
-            return fail(KDA_ERR_CAPTURE_MISS,
-                        "device bounds cannot be read back while the stream is capturing; "
-                        "pass cu_seqlens_host");
-        readback.resize((size_t)N + 1);
-        cudaEvent_t* done = nullptr;
-        void* host = cache().ring.acquire(readback.size() * sizeof(int32_t), &done);
-        if (!host) return fail(KDA_ERR_CUDA, "pinned staging allocation failed");
-        e = cudaMemcpyAsync(host, cu_dev, readback.size() * sizeof(int32_t),
-                            cudaMemcpyDeviceToHost, stream);
-        if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
-        if (e == cudaSuccess) std::memcpy(readback.data(), host, readback.size() * sizeof(int32_t));
-        cudaEventRecord(*done, stream);
-        if (e != cudaSuccess) return cuda_fail(e, "read-back of cu_seqlens");
-        cu_host = readback.data();
-        int rc = check_host_bounds(cu_host, N, T);
-        if (rc != KDA_OK) return rc;
-    }
-
     MetaEntry* m = nullptr;
-    int rc = cache().get(cu_host, N, stream, capturing, &m);
+    int rc = find_tables(cu_dev, cu_host, N, T, stream, capturing, &m);
     if (rc != KDA_OK) return rc;
 
     uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -620,6 +635,45 @@ int common_checks(const void* q, const void* k, const void* v, const void* g_raw
 int noalloc_scratch(void** out);
 
 }  // namespace
+
+// Services shared with the operators beside the KDA forward (kda_ops.h).
+namespace kda {
+
+int set_error(int code, const char* fmt, ...) {
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof(buf), fmt, ap);
+    va_end(ap);
+    g_err = buf;
+    return code;
+}
+
+int check_bounds(const int32_t* cu_host, int32_t N, int64_t T) {
+    return check_host_bounds(cu_host, N, T);
+}
+
+int with_seq_tables(const int32_t* cu_dev, const int32_t* cu_host, int32_t N, int64_t T,
+                    cudaStream_t stream, int (*enqueue)(void*, const SeqTables&), void* arg) {
+    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+    cudaError_t e = cudaStreamIsCapturing(stream, &cap);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaStreamIsCapturing");
+    const bool capturing = (cap != cudaStreamCaptureStatusNone);
+    std::lock_guard<std::mutex> lock(cache().mu);
+    MetaEntry* m = nullptr;
+    int rc = find_tables(cu_dev, cu_host, N, T, stream, capturing, &m);
+    if (rc != KDA_OK) return rc;
+    const MetaLayout& L = m->layout;
+    SeqTables t{m->dev + L.off_cu, m->dev + L.off_long, m->dev + L.off_short,
+                L.n_long,          L.n_short,           L.long_tokens,
+                L.max_long};
+    rc = enqueue(arg, t);
+    if (rc != KDA_OK) return rc;
+    cache().mark_use(m, stream, capturing);
+    return KDA_OK;
+}
+
+}  // namespace kda
 
 extern "C" {
 

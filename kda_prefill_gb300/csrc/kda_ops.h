@@ -1,0 +1,94 @@
+// Internal interface of the operators beside the KDA forward (linear attention
+// with a decay for each head, rotary positions, gated norm): the parameters
+// their host checks (kda_ops_api.cu) hand to their kernels, and the services of
+// kda_api.cu they share.
+#pragma once
+
+#include "kda.h"
+#include "kda_internal.h"
+
+namespace kda {
+
+// Records the message kda_last_error() returns and gives back `code`.
+int set_error(int code, const char* fmt, ...);
+
+// The cached tables of a call's bounds (see kda_api.cu).  The tables stay valid
+// on `stream` for work enqueued while the lock is held.
+struct SeqTables {
+    const int32_t* cu;          // [N + 1]
+    const int32_t* long_list;   // sequences of more than kShortMax tokens, longest first
+    const int32_t* short_list;  // the others
+    int n_long, n_short;
+    int64_t long_tokens;        // tokens of the long sequences
+    int max_long;               // tokens of the longest one
+};
+// Looks the bounds up (reading them back once without cu_host), calls
+// enqueue(arg, tables) with the cache locked and marks the tables' use.
+int with_seq_tables(const int32_t* cu_dev, const int32_t* cu_host, int32_t N, int64_t T,
+                    cudaStream_t stream, int (*enqueue)(void*, const SeqTables&), void* arg);
+// The bounds' host check (message set on failure).
+int check_bounds(const int32_t* cu_host, int32_t N, int64_t T);
+
+struct LinParams {
+    const __nv_bfloat16 *q, *k, *v;
+    int64_t q_st, q_sh, k_st, k_sh, v_st, v_sh;  // elements between tokens, between heads
+    const float* g;   // log decays
+    int64_t g_st;     // elements between tokens' decays: H, or 0 for one decay per head
+    __nv_bfloat16* out;
+    float scale;
+    int H, rep, N;    // heads, heads per q/k head, sequences
+    int64_t T;
+    const int32_t* cu;
+    const int32_t *long_list, *short_list;
+    int n_long, n_short;
+    int64_t long_tokens;
+    int max_long;
+    int* status;
+    void* pool;
+    int64_t stride0;  // elements between slots
+    const int32_t* idx;
+    const uint8_t* has_init;
+    int num_slots;
+    int st_dtype;
+};
+
+// Values below kMinDecay give exp() == 0 in fp32; the clamp keeps sums of them finite.
+constexpr float kMinDecay = -104.f;
+
+cudaError_t launch_lin_step(const LinParams& p, const int32_t* list, int n, cudaStream_t s);
+
+struct RopeTensor {
+    const void* in;
+    void* out;
+    int64_t in_st, in_sh, out_st, out_sh;
+    int heads;
+};
+struct RopeParams {
+    RopeTensor x[2];
+    const void* pos;
+    int pos64;
+    const double* inv_freq;
+    int64_t T;
+    int D, rot;
+    int interleaved;
+    float factor;   // on cos and sin
+    float sign;     // -1 for the inverse rotation
+    int dtype;
+};
+cudaError_t launch_rope(const RopeParams& p, cudaStream_t s);
+
+struct NormParams {
+    const void* x;
+    const void* gate;
+    const float* weight;
+    void* out;
+    int64_t x_st, x_sh, g_st, g_sh, o_st, o_sh;
+    int64_t T;
+    int H, D;
+    float eps;
+    int act;
+    int dtype;
+};
+cudaError_t launch_gated_norm(const NormParams& p, cudaStream_t s);
+
+}  // namespace kda
