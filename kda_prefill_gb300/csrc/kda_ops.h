@@ -55,6 +55,8 @@ struct LinParams {
 // Values below kMinDecay give exp() == 0 in fp32; the clamp keeps sums of them finite.
 constexpr float kMinDecay = -104.f;
 
+// Long sequences chunk by chunk (kda_lin_walk.cu); short ones token by token.
+cudaError_t launch_lin_walk(const LinParams& p, cudaStream_t s);
 cudaError_t launch_lin_step(const LinParams& p, const int32_t* list, int n, cudaStream_t s);
 
 struct RopeTensor {

@@ -77,7 +77,7 @@ int enqueue_lin(void* arg, const kda::SeqTables& t) {
     p.max_long = t.max_long;
     cudaError_t e = cudaMemsetAsync(p.status, 0, kda::kWsClearBytes, c.stream);
     if (e != cudaSuccess) return cuda_error(e, "cudaMemsetAsync (status)");
-    e = kda::launch_lin_step(p, p.long_list, p.n_long, c.stream);
+    e = kda::launch_lin_walk(p, c.stream);
     if (e == cudaSuccess) e = kda::launch_lin_step(p, p.short_list, p.n_short, c.stream);
     return e == cudaSuccess ? KDA_OK : cuda_error(e, "kernel launch");
 }
