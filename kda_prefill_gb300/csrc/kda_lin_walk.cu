@@ -7,11 +7,14 @@
 //     dS = (e^{R_j} v_j)^T k       S' = e^{G_C} S + dS
 //
 // One CTA walks one (sequence, head) at a time; its warps have roles:
-//   0-7   state: weighted v (W) into tensor memory, S in registers, S as the
-//         q S^T product's operand in shared memory
-//   8-11  scores: X to P in place, the e^{G_i} on q S^T, the output rows
-//   12    issues the MMAs     13  issues the TMA loads
-//   14    claims items and makes the decays
+//   0-7   S in registers, and as the q S^T product's operand in shared memory
+//   8-15  W, the weighted v, into tensor memory
+//   16-19 X to P, in place
+//   20-23 the e^{G_i} on q S^T, the output rows
+//   24    issues the MMAs     25  issues the TMA loads
+//   26    claims items and makes the decays
+// Each role's work on a chunk is shorter than the chunk's time; what bounds it is
+// the chain QK -> P -> PV -> next QK beside QS -> KV -> S -> next QS.
 //
 // Rounding.  Operands are bf16.  q, k and v are; P and S are carried as a sum of
 // two bf16 (16 bits: with one, a rounding as large as out's own would be added
@@ -19,11 +22,16 @@
 // every chunk and S' is formed in fp32 registers, so that S is rounded once a
 // chunk however the tensor cores round their partial sums.
 //
+// Decays of scores.  In the 32 x 32 blocks on the diagonal e^{G_i - G_j} is taken
+// as it stands.  Left of them it is e^{G_i - G_b} e^{G_b - G_j}, b the last token of
+// column j's block: both factors are at most one, the first is one a row and block
+// and the second one a token, so neither overflows and few exponentials are left.
+//
 // Infinities and NaN.  A masked score is a zero by selection, but a zero times an
-// infinite v is NaN: P v would carry it to the chunk's earlier tokens.  The state
-// warps, which read all of v for W, therefore clear such values in the tile (W
-// keeps them: the state holds them from the chunk's end on), and the score warps
-// put a NaN into their columns from their token on.
+// infinite v is NaN: P v would carry it to the chunk's earlier tokens.  The W
+// warps, which read all of v, therefore clear such values in the tile (W keeps
+// them: the state holds them from the chunk's end on), and the output warps put a
+// NaN into their columns from their token on.
 
 #include <type_traits>
 
@@ -37,29 +45,31 @@ using namespace dev;
 
 constexpr int D = kD;
 constexpr int C = 128;
-constexpr int kThreads = 15 * 32;
+constexpr int kThreads = 28 * 32;
 constexpr int kTile = C * D * 2;  // bytes of a q, k or v tile
 constexpr int kSlots = 5;         // tiles in flight or in use
-constexpr int kItems = 4;         // items the claims run ahead
+constexpr int kItems = 3;         // items the claims run ahead
 
 // Shared memory.  Tiles are two halves of 64 columns, 128-byte swizzled.
 constexpr int kSmS = 0;                        // S as bf16: high part, then low part
 constexpr int kSmTile = 2 * kTile;
-constexpr int kSmG = kSmTile + kSlots * kTile; // [2][G, prefix sums in log2; e^R]
-constexpr int kSmItem = kSmG + 2 * 2 * C * 4;
+constexpr int kSmG = kSmTile + kSlots * kTile;  // [2][G, prefix sums in log2; e^R]
+constexpr int kSmCf = kSmG + 2 * 2 * C * 4;     // [96] e^{G_b - G_j}
 struct Item {
     int t0, len, h, n, slot, flags;
-    float pad[2];
 };
+constexpr int kSmItem = kSmCf + 96 * 4;
 enum { kInit = 1, kStore = 2, kEnd = 4 };
 constexpr int kSmBar = kSmItem + kItems * (int)sizeof(Item);
+static_assert(kSmBar % 8 == 0, "barriers are 8-byte aligned");
 
 enum Bar {
     kFull = 0,                  // [5] tile loaded
     kEmpty = kFull + kSlots,    // [5] tile consumed
     kDecFull = kEmpty + kSlots, // [2] decays of a chunk made
     kDecEmpty = kDecFull + 2,   // [2] and read
-    kItemFull = kDecEmpty + 2,  // [4] item claimed
+    kCfFull = kDecEmpty + 2,    // factors of score columns made
+    kItemFull,                  // [3] item claimed
     kItemEmpty = kItemFull + kItems,
     kXFull = kItemEmpty + kItems,  // q k^T in X
     kPFull,                     // P in X
@@ -67,9 +77,9 @@ enum Bar {
     kQSScaled,                  // e^{G_i} applied
     kOFull,                     // the chunk's O complete
     kOEmpty,                    // and read
-    kWFull,                     // [2] two K steps of W written
-    kWEmpty = kWFull + 2,       // [2] and read
-    kDSFull = kWEmpty + 2,      // dS complete
+    kWFull,                     // [5] a K step of W written
+    kWEmpty = kWFull + 5,       // [5] and read
+    kDSFull = kWEmpty + 5,      // dS complete
     kDSEmpty,                   // and read
     kSFull,                     // S's operand written
     kCleared,                   // rows past a sequence's end cleared
@@ -79,14 +89,19 @@ enum Bar {
 constexpr int kSmGamma = kSmBar + kNumBars * 8;  // [2] e^{G_C}
 constexpr int kSmBad = kSmGamma + 8;             // [2][8] value columns with infinities or NaN
 constexpr int kSmMisc = kSmBad + 64;             // tensor-memory base, abort flag
-constexpr int kSmemBytes = kSmMisc + 8;
+constexpr int kSmRows = kSmMisc + 8;             // warps done with a q tile's rows
+constexpr int kSmemBytes = kSmRows + 8;
 static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
 
 // Tensor memory columns.
 constexpr uint32_t kTmX = 0;    // X; then P: per 32 tokens 16 columns high part, 16 low
 constexpr uint32_t kTmO = 128;
 constexpr uint32_t kTmDS = 256;
-constexpr uint32_t kTmW = 384;  // [2] buffers of 2 K steps x (high, middle, low) x 8 columns
+constexpr uint32_t kTmW = 384;  // [5] buffers of a K step of W: (high, middle, low) x 8 columns;
+                                // the last three take q's place once q S^T is done, so that
+                                // enough steps are under way to hide their handing over
+constexpr uint32_t kTmQ = 432;  // q: with both operands in shared memory an MMA reads all of
+                                // its bandwidth, and everything else there waits
 constexpr uint32_t kTmCols = 512;
 
 constexpr uint32_t kIdescKK = mma_idesc(1, 0, 0, 128, 128);  // B K-major
@@ -101,27 +116,28 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, u
         : "memory");
 }
 
-// 32 columns of this thread's lane.
-__device__ __forceinline__ void tmem_ld32(uint32_t a, uint32_t (&r)[32]) {
+// 128 rows x 32 bytes (a K step) from shared memory into 8 columns, in order with
+// the MMAs that this thread issues after it.
+__device__ __forceinline__ void tmem_cp_step(uint32_t d, uint64_t desc) {
+    asm volatile("tcgen05.cp.cta_group::1.128x256b [%0], %1;" ::"r"(d), "l"(desc) : "memory");
+}
+
+// 16 columns of this thread's lane.
+__device__ __forceinline__ void tmem_ld16u(uint32_t a, uint32_t (&r)[16]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
-        "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+        "%15}, [%16];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
           "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
-          "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
-          "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+          "=r"(r[14]), "=r"(r[15])
         : "r"(a));
 }
-__device__ __forceinline__ void tmem_st32(uint32_t a, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t (&r)[16]) {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
-        "%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
+        "%13,%14,%15};" ::"r"(r[0]),
         "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
-        "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
-        "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
-        "r"(r[30]), "r"(r[31]), "r"(a)
+        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(a)
         : "memory");
 }
 // 16 lanes x 8 columns: r0 holds lane t/4, column t%4; r1 lane t/4 + 8; r2, r3 the
@@ -144,19 +160,61 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ float bf_lo(uint32_t x) { return __uint_as_float(x << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t x) { return __uint_as_float(x & 0xFFFF0000u); }
 
-__device__ __forceinline__ void store32(void* p, const uint32_t* r, bool wide) {
-    if (wide) {
-        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]),
-                     "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                     : "memory");
-    } else {
-        reinterpret_cast<uint4*>(p)[0] = make_uint4(r[0], r[1], r[2], r[3]);
-        reinterpret_cast<uint4*>(p)[1] = make_uint4(r[4], r[5], r[6], r[7]);
-    }
+// Two fp32 values in one 64-bit register.
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 pack2(float a, float b) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2(f2 a) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+    return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f2 from_bf(uint32_t x) { return pack2(bf_lo(x), bf_hi(x)); }
+// The next bf16 part of a pair: returns it and leaves the exact remainder in a.
+__device__ __forceinline__ uint32_t take_bf(f2& a) {
+    const float2 v = unpack2(a);
+    const uint32_t hi = pack_bf162(v.x, v.y);
+    a = fma2(from_bf(hi), pack2(-1.f, -1.f), a);
+    return hi;
+}
+__device__ __forceinline__ uint32_t last_bf(f2 a) {
+    const float2 v = unpack2(a);
+    return pack_bf162(v.x, v.y);
+}
+template <int N>
+__device__ __forceinline__ void more_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
 }
 
+// Buffer of W's step ks (0 .. 7), and the phase of its use in chunk c: buffers 0, 1
+// and 2 are used twice a chunk.
+__device__ __forceinline__ int w_buffer(int ks) { return ks < 5 ? ks : ks - 5; }
+__device__ __forceinline__ uint32_t w_phase(int ks, int c) { return ks == 3 || ks == 4 ? c & 1 : ks >= 5; }
+
 struct Maps {
-    CUtensorMap q, k, v;
+    CUtensorMap q, k, v, out;
 };
 
 // What every role needs.
@@ -170,6 +228,7 @@ struct Ctx {
     // Waits for a barrier's phase; gives up after about a second, or once another
     // role has (the callers then leave their loops).
     __device__ __forceinline__ bool wait(int b, uint32_t parity) const {
+#pragma unroll 1
         for (uint32_t i = 0; i < kWaitLimit; ++i) {
             if (mbar_try_wait(bar + b, parity)) return true;
             if (*abort) return false;
@@ -204,7 +263,7 @@ struct Ctx {
 };
 __device__ __forceinline__ int chunks(int len) { return (len + C - 1) / C; }
 
-// ---- warp 14: items and decays ------------------------------------------------
+// ---- warp 26: items and decays ------------------------------------------------
 __device__ __forceinline__ void decay_role(const LinParams& p, const Ctx& x) {
     const int n_items = p.n_long * p.H;
     int c = 0;
@@ -274,11 +333,26 @@ __device__ __forceinline__ void decay_role(const LinParams& p, const Ctx& x) {
             if (x.lane == 0) reinterpret_cast<float*>(x.smem + kSmGamma)[c & 1] = expf(total);
             __syncwarp();
             if (x.lane == 0) x.arrive(kDecFull + (c & 1));
+            // the sums from here to the end of each 32 tokens (eight lanes)
+            float rest = pre[3];
+#pragma unroll
+            for (int w = 1; w < 8; w <<= 1) {
+                const float d = __shfl_down_sync(0xffffffffu, rest, w, 8);
+                if ((x.lane & 7) + w < 8) rest += d;
+            }
+            rest = __shfl_down_sync(0xffffffffu, rest, 1, 8);
+            if ((x.lane & 7) == 7) rest = 0.f;
+            if (c > 0 && !x.wait_all(kPFull, (c + 1) & 1)) return;
+            if (x.lane < 24)
+                reinterpret_cast<float4*>(x.smem + kSmCf)[x.lane] =
+                    make_float4(expf(rest + suf[0]), expf(rest + suf[1]), expf(rest + suf[2]), expf(rest + suf[3]));
+            __syncwarp();
+            if (x.lane == 0) x.arrive(kCfFull);
         }
     }
 }
 
-// ---- warp 13, one lane: loads -------------------------------------------------
+// ---- warp 25, one lane: loads -------------------------------------------------
 // Returns the number of tiles issued.
 __device__ __forceinline__ int load_role(const Maps& maps, const LinParams& p, const Ctx& x) {
     int tile = 0;
@@ -287,9 +361,9 @@ __device__ __forceinline__ int load_role(const Maps& maps, const LinParams& p, c
         for (int j = 0; j < chunks(item.len); ++j) {
             const int t = item.t0 + j * C;
 #pragma unroll
-            for (int m = 0; m < 3; ++m, ++tile) {  // k, q, v
+            for (int m = 0; m < 3; ++m, ++tile) {  // q, k, v, in the order that they come free
                 if (tile >= kSlots && !x.wait(kEmpty + tile % kSlots, ((tile / kSlots) + 1) & 1)) return tile;
-                const CUtensorMap* map = m == 0 ? &maps.k : m == 1 ? &maps.q : &maps.v;
+                const CUtensorMap* map = m == 0 ? &maps.q : m == 1 ? &maps.k : &maps.v;
                 const int h = m == 2 ? item.h : item.h / p.rep;
                 uint64_t* bar = x.bar + kFull + tile % kSlots;
                 uint8_t* dst = x.tile(tile);
@@ -302,130 +376,167 @@ __device__ __forceinline__ int load_role(const Maps& maps, const LinParams& p, c
     return tile;
 }
 
-// ---- warp 12, one lane: products ------------------------------------------------
+// ---- warp 24: products ----------------------------------------------------------
+// The warp runs as one (descriptors stay in uniform registers); one elected lane
+// issues.
 __device__ __forceinline__ void mma_role(const Ctx& x) {
     const uint32_t base = smem_u32(x.smem);
-    auto kmaj = [&](uint32_t a, int ks) {  // K-major: 16 columns on
-        return sw128_desc(a + (ks >> 2) * (kTile / 2) + (ks & 3) * 32, 16, 1024);
-    };
-    auto mnmaj = [&](uint32_t a, int ks) {  // MN-major: 16 rows on
-        return sw128_desc(a + ks * 2048, kTile / 2, 1024);
-    };
-    int tile = 0, c = 0, with_s = 0, wb = 0;
+    // descriptors of a tile read K-major (16 columns a step) and MN-major (16 rows)
+    auto kdesc = [&](uint32_t a) { return sw128_desc(a, 16, 1024); };
+    auto mdesc = [&](uint32_t a) { return sw128_desc(a, kTile / 2, 1024); };
+    constexpr auto kstep = [](int ks) { return (uint64_t)(((ks >> 2) * (kTile / 2) + (ks & 3) * 32) >> 4); };
+    constexpr auto mstep = [](int ks) { return (uint64_t)((ks * 2048) >> 4); };
+    const uint64_t s_hi = kdesc(base + kSmS), s_lo = kdesc(base + kSmS + kTile);
+    const bool lead = elect_one();
+    int tile = 0, c = 0, with_s = 0;
     Item item;
-    for (int it = 0; x.item(it, &item, false); ++it) {
+    for (int it = 0; x.item(it, &item, true); ++it) {
         const int nc = chunks(item.len);
         for (int j = 0; j < nc; ++j, ++c, tile += 3) {
             const bool has_s = j > 0 || (item.flags & kInit);
-            const uint32_t k = smem_u32(x.tile(tile)), q = smem_u32(x.tile(tile + 1)),
-                           v = smem_u32(x.tile(tile + 2));
-            if (!x.wait(x.full(tile), x.full_phase(tile)) || !x.wait(x.full(tile + 1), x.full_phase(tile + 1)))
-                return;
+            const uint32_t qa = smem_u32(x.tile(tile)), ka = smem_u32(x.tile(tile + 1)), va = smem_u32(x.tile(tile + 2));
+            const uint64_t k = kdesc(ka), q = kdesc(qa), km = mdesc(ka), vm = mdesc(va);
+            if (!x.wait_all(x.full(tile), x.full_phase(tile))) return;
+            if (!x.wait_all(x.full(tile + 1), x.full_phase(tile + 1))) return;
             // X is free once the previous chunk's P v has read it
-            if (c > 0 && !x.wait(kOFull, (c + 1) & 1)) return;
+            if (c > 0 && !x.wait_all(kOFull, (c + 1) & 1)) return;
             tc_fence_after();
-            for (int ks = 0; ks < 8; ++ks)
-                mma_f16_ss(x.tmem + kTmX, kmaj(q, ks), kmaj(k, ks), kIdescKK, ks > 0);
-            mma_commit(x.bar + kXFull);
+            if (lead) {
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks)
+                    tmem_cp_step(x.tmem + kTmQ + 8 * ks, q + kstep(ks));
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks)
+                    mma_f16_ts(x.tmem + kTmX, x.tmem + kTmQ + 8 * ks, k + kstep(ks), kIdescKK, ks > 0);
+                mma_commit(x.bar + kXFull);
+                mma_commit(x.bar + kEmpty + tile % kSlots);
+            }
+            __syncwarp();
             // O is free once the previous chunk's rows have been read
-            if (c > 0 && !x.wait(kOEmpty, (c + 1) & 1)) return;
+            if (c > 0 && !x.wait_all(kOEmpty, (c + 1) & 1)) return;
             if (has_s) {
-                if (!x.wait(kSFull, with_s & 1)) return;
+                if (!x.wait_all(kSFull, with_s & 1)) return;
                 tc_fence_after();
-                for (int part = 1; part >= 0; --part)  // low part first
+                if (lead) {
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)  // low part first
+                        mma_f16_ts(x.tmem + kTmO, x.tmem + kTmQ + 8 * ks, s_lo + kstep(ks), kIdescKK, ks > 0);
+#pragma unroll
                     for (int ks = 0; ks < 8; ++ks)
-                        mma_f16_ss(x.tmem + kTmO, kmaj(q, ks), kmaj(base + kSmS + part * kTile, ks), kIdescKK,
-                                   part == 0 || ks > 0);
-                mma_commit(x.bar + kQSFull);
+                        mma_f16_ts(x.tmem + kTmO, x.tmem + kTmQ + 8 * ks, s_hi + kstep(ks), kIdescKK, 1);
+                    mma_commit(x.bar + kQSFull);
+                }
+                __syncwarp();
             }
-            mma_commit(x.bar + kEmpty + (tile + 1) % kSlots);
-            if (c > 0 && !x.wait(kDSEmpty, (c + 1) & 1)) return;
-            for (int half = 0; half < 4; ++half, ++wb) {  // 32 tokens each
-                if (!x.wait(kWFull + (wb & 1), (wb >> 1) & 1)) return;
+            if (c > 0 && !x.wait_all(kDSEmpty, (c + 1) & 1)) return;
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks) {
+                if (!x.wait_all(kWFull + w_buffer(ks), w_phase(ks, c))) return;
                 tc_fence_after();
-                const uint32_t w = x.tmem + kTmW + (wb & 1) * 48;
-                for (int s = 0; s < 2; ++s)
+                if (lead) {
+#pragma unroll
                     for (int part = 2; part >= 0; --part)
-                        mma_f16_ts(x.tmem + kTmDS, w + s * 24 + part * 8, mnmaj(k, 2 * half + s), kIdescKM,
-                                   half > 0 || s > 0 || part < 2);
-                mma_commit(x.bar + kWEmpty + (wb & 1));
+                        mma_f16_ts(x.tmem + kTmDS, x.tmem + kTmW + w_buffer(ks) * 24 + part * 8, km + mstep(ks), kIdescKM,
+                                   ks > 0 || part < 2);
+                    mma_commit(x.bar + kWEmpty + w_buffer(ks));
+                }
+                __syncwarp();
             }
-            mma_commit(x.bar + kDSFull);
-            mma_commit(x.bar + kEmpty + tile % kSlots);
-            if (!x.wait(kPFull, c & 1)) return;
-            if (has_s && !x.wait(kQSScaled, with_s & 1)) return;
+            if (lead) {
+                mma_commit(x.bar + kDSFull);
+                mma_commit(x.bar + kEmpty + (tile + 1) % kSlots);
+            }
+            __syncwarp();
+            if (!x.wait_all(kPFull, c & 1)) return;
+            if (has_s && !x.wait_all(kQSScaled, with_s & 1)) return;
             tc_fence_after();
-            for (int ks = 0; ks < 8; ++ks)
-                for (int part = 1; part >= 0; --part)
-                    mma_f16_ts(x.tmem + kTmO, x.tmem + kTmX + 32 * (ks >> 1) + 16 * part + 8 * (ks & 1),
-                               mnmaj(v, ks), kIdescKM, has_s || ks > 0 || part == 0);
-            mma_commit(x.bar + kOFull);
-            mma_commit(x.bar + kEmpty + (tile + 2) % kSlots);
+            if (lead) {
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks)
+#pragma unroll
+                    for (int part = 1; part >= 0; --part)
+                        mma_f16_ts(x.tmem + kTmO, x.tmem + kTmX + 32 * (ks >> 1) + 16 * part + 8 * (ks & 1),
+                                   vm + mstep(ks), kIdescKM, has_s || ks > 0 || part == 0);
+                mma_commit(x.bar + kOFull);  // v's tile takes the output rows now
+            }
+            __syncwarp();
             with_s += has_s;
         }
     }
 }
 
-// Bit e: v holds an infinity or NaN in column col + e between tokens t0 and t1 of
-// the item, for the columns in `cols`.
-__device__ __noinline__ uint32_t nonfinite_up_to(const LinParams& p, const Item& item, int t0, int t1,
-                                                 int col, uint32_t cols) {
-    const uint16_t* v = reinterpret_cast<const uint16_t*>(p.v) + (int64_t)item.h * p.v_sh + col;
-    uint32_t hit = 0;
-    for (int t = t0; t <= t1; ++t)
-        for (uint32_t m = cols & ~hit; m; m &= m - 1) {
-            const int e = __ffs(m) - 1;
-            if ((v[(int64_t)(item.t0 + t) * p.v_st + e] & 0x7F80) == 0x7F80) hit |= 1u << e;
+// Puts a NaN into the row's columns, of those in `cols`, where v holds an infinity or
+// NaN between tokens t0 and t1 of the item.
+__device__ __noinline__ void put_nonfinite(const LinParams& p, const Item& item, int t0, int t1, int row,
+                                           uint4 cols, uint8_t* tile) {
+    const uint16_t* v = reinterpret_cast<const uint16_t*>(p.v) + (int64_t)item.h * p.v_sh;
+    for (int g = 0; g < 4; ++g)
+        for (uint32_t m = g == 0 ? cols.x : g == 1 ? cols.y : g == 2 ? cols.z : cols.w; m; m &= m - 1) {
+            const int col = 32 * g + __ffs(m) - 1;
+            for (int t = t0; t <= t1; ++t)
+                if ((v[(int64_t)(item.t0 + t) * p.v_st + col] & 0x7F80) == 0x7F80) {
+                    *reinterpret_cast<uint16_t*>(tile + sw128_off(row, col, C)) = 0x7FFF;
+                    break;
+                }
         }
-    return hit;
 }
 
-// ---- warps 8-11: scores and output rows; thread = chunk row ----------------------
+// ---- warps 16-19: scores; thread = chunk row ------------------------------------
 __device__ __forceinline__ void score_role(const LinParams& p, const Ctx& x, int w) {
     const int row = 32 * w + x.lane;
-    const uint32_t tm = x.tmem + ((uint32_t)(32 * w) << 16);
-    const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
-    int c = 0, with_s = 0;
+    const uint32_t tm = x.tmem + ((uint32_t)(32 * w) << 16) + kTmX;
+    const float* cf = reinterpret_cast<const float*>(x.smem + kSmCf);
+    int c = 0;
     Item item;
     for (int it = 0; x.item(it, &item, true); ++it) {
         for (int j = 0; j < chunks(item.len); ++j, ++c) {
-            const bool has_s = j > 0 || (item.flags & kInit);
             if (!x.wait_all(kDecFull + (c & 1), (c >> 1) & 1)) return;
             const float* G = x.decays(c);
             const float gi = G[row];
+            if (!x.wait_all(kCfFull, c & 1)) return;
             if (!x.wait_all(kXFull, c & 1)) return;
             tc_fence_after();
-#pragma unroll 1
-            for (int b = 0; b < 4; ++b) {
-                uint32_t r[32], o[32];
-                if (b <= w) {
-                    tmem_ld32(tm + kTmX + 32 * b, r);
+            // Sixteen scores become eight pairs of high parts and eight of low parts.
+            // A block of 32 is held as high 0-15, high 16-31, low 0-15, low 16-31 so
+            // that its first half is read before its place is written.
+            auto split_and_store = [&](int b, auto factor) {
+                uint32_t hi[16], lo[16];
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    uint32_t r[16];
+                    tmem_ld16u(tm + 32 * b + 16 * u, r);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        const float4 gj = *reinterpret_cast<const float4*>(G + 32 * b + e);
-                        float v[4] = {__uint_as_float(r[e]) * ex2(gi - gj.x),
-                                      __uint_as_float(r[e + 1]) * ex2(gi - gj.y),
-                                      __uint_as_float(r[e + 2]) * ex2(gi - gj.z),
-                                      __uint_as_float(r[e + 3]) * ex2(gi - gj.w)};
-                        if (b == w) {
-#pragma unroll
-                            for (int u = 0; u < 4; ++u)
-                                if (e + u > x.lane) v[u] = 0.f;
-                        }
-#pragma unroll
-                        for (int u = 0; u < 4; u += 2) {
-                            const uint32_t hi = pack_bf162(v[u], v[u + 1]);
-                            o[(e + u) / 2] = hi;
-                            o[16 + (e + u) / 2] = pack_bf162(v[u] - bf_lo(hi), v[u + 1] - bf_hi(hi));
-                        }
+                    for (int e = 0; e < 16; e += 2) {
+                        const f2 f = factor(16 * u + e, r[e], r[e + 1]);  // may clear the scores
+                        f2 v = mul2(pack2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), f);
+                        hi[8 * u + e / 2] = take_bf(v);
+                        lo[8 * u + e / 2] = last_bf(v);
                     }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = 0u;
                 }
-                tmem_st32(tm + kTmX + 32 * b, o);
+                tmem_st16(tm + 32 * b, hi);
+                tmem_st16(tm + 32 * b + 16, lo);
+            };
+#pragma unroll 1
+            for (int b = 0; b < w; ++b) {
+                const float f = ex2(gi - G[32 * b + 31]);
+                const f2 ff = pack2(f, f);
+                const float2* col = reinterpret_cast<const float2*>(cf + 32 * b);
+                split_and_store(b, [&](int e, uint32_t, uint32_t) {
+                    const float2 u = col[e / 2];
+                    return mul2(ff, pack2(u.x, u.y));
+                });
             }
+            const float2* Gw = reinterpret_cast<const float2*>(G + 32 * w);
+            split_and_store(w, [&](int e, uint32_t& a, uint32_t& b) {
+                const float2 u = Gw[e / 2];
+                if (e > x.lane) a = 0u;
+                if (e + 1 > x.lane) b = 0u;
+                return pack2(ex2(e > x.lane ? 0.f : gi - u.x), ex2(e + 1 > x.lane ? 0.f : gi - u.y));
+            });
+            const uint32_t zero[16] = {};
+#pragma unroll 1
+            for (int b = 2 * w + 2; b < 8; ++b) tmem_st16(tm + 16 * b, zero);
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -433,18 +544,41 @@ __device__ __forceinline__ void score_role(const LinParams& p, const Ctx& x, int
                 x.arrive(kPFull);
                 x.arrive(kDecEmpty + (c & 1));
             }
+        }
+    }
+}
+
+// ---- warps 20-23: output rows; thread = chunk row --------------------------------
+__device__ __forceinline__ void out_role(const Maps& maps, const LinParams& p, const Ctx& x, int w) {
+    const int row = 32 * w + x.lane;
+    const uint32_t tm = x.tmem + ((uint32_t)(32 * w) << 16) + kTmO;
+    const f2 scale = pack2(p.scale, p.scale);
+    int tile = 0, c = 0, with_s = 0;
+    Item item;
+    for (int it = 0; x.item(it, &item, true); ++it) {
+        for (int j = 0; j < chunks(item.len); ++j, ++c, tile += 3) {
+            const bool has_s = j > 0 || (item.flags & kInit);
+            if (!x.wait_all(kDecFull + (c & 1), (c >> 1) & 1)) return;
+            const float f = ex2(x.decays(c)[row]);
+            __syncwarp();
+            if (x.lane == 0) x.arrive(kDecEmpty + (c & 1));
             if (has_s) {
                 if (!x.wait_all(kQSFull, with_s & 1)) return;
                 tc_fence_after();
-                const float f = ex2(gi);
+                const f2 ff = pack2(f, f);
+                uint32_t r[16];
+                tmem_ld16u(tm, r);
 #pragma unroll 1
-                for (int b = 0; b < 4; ++b) {
-                    uint32_t r[32];
-                    tmem_ld32(tm + kTmO + 32 * b, r);
+                for (int b = 0; b < 8; ++b) {
+                    uint32_t y[16];
                     tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(f * __uint_as_float(r[e]));
-                    tmem_st32(tm + kTmO + 32 * b, r);
+                    for (int e = 0; e < 16; e += 2) {
+                        const float2 v = unpack2(mul2(ff, pack2(__uint_as_float(r[e]), __uint_as_float(r[e + 1]))));
+                        y[e] = __float_as_uint(v.x), y[e + 1] = __float_as_uint(v.y);
+                    }
+                    if (b < 7) tmem_ld16u(tm + 16 * b + 16, r);
+                    tmem_st16(tm + 16 * b, y);
                 }
                 tmem_wait_st();
                 tc_fence_before();
@@ -454,40 +588,169 @@ __device__ __forceinline__ void score_role(const LinParams& p, const Ctx& x, int
             }
             if (!x.wait_all(kOFull, c & 1)) return;
             tc_fence_after();
-            const uint32_t* bad = reinterpret_cast<const uint32_t*>(x.smem + kSmBad) + 8 * (c & 1);
-            const int t = j * C + row;
-            __nv_bfloat16* out = p.out + ((size_t)(item.t0 + t) * p.H + item.h) * D;
-            uint32_t y[64];
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                uint32_t r[32];
-                tmem_ld32(tm + kTmO + 32 * b, r);
+            // The rows go through v's tile, which has been read, so that whole rows
+            // are written to memory: lanes that each store a row of their own fill
+            // the load/store unit with single sectors and hold up everything else.
+            uint8_t* vt = x.tile(tile + 2);
+            const uint4* bad = reinterpret_cast<const uint4*>(x.smem + kSmBad) + 2 * (c & 1);
+            uint4 cols = bad[0];
+            cols.x |= bad[1].x, cols.y |= bad[1].y, cols.z |= bad[1].z, cols.w |= bad[1].w;
+            uint32_t r[16];
+            tmem_ld16u(tm, r);
+#pragma unroll 1
+            for (int b = 0; b < 8; ++b) {
+                uint32_t y[8];
                 tmem_wait_ld();
-                if (const uint32_t cols = bad[b] | bad[4 + b]) {
-                    const uint32_t hit = nonfinite_up_to(p, item, j * C, min(t, item.len - 1), 32 * b, cols);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (hit >> e & 1) r[e] = 0x7FFFFFFFu;
-                }
+                for (int e = 0; e < 16; e += 2)
+                    y[e / 2] = last_bf(mul2(scale, pack2(__uint_as_float(r[e]), __uint_as_float(r[e + 1]))));
+                if (b < 7) tmem_ld16u(tm + 16 * b + 16, r);
 #pragma unroll
-                for (int e = 0; e < 32; e += 2)
-                    y[16 * b + e / 2] = pack_bf162(p.scale * __uint_as_float(r[e]), p.scale * __uint_as_float(r[e + 1]));
+                for (int e = 0; e < 8; e += 4)
+                    *reinterpret_cast<uint4*>(vt + sw128_off(row, 16 * b + 2 * e, C)) = make_uint4(y[e], y[e + 1], y[e + 2], y[e + 3]);
             }
             tc_fence_before();
             __syncwarp();
             if (x.lane == 0) x.arrive(kOEmpty);
-            if (t < item.len) {
-#pragma unroll
-                for (int b = 0; b < 8; ++b) store32(out + 16 * b, y + 8 * b, wide);
+            if (cols.x | cols.y | cols.z | cols.w)
+                put_nonfinite(p, item, j * C, min(j * C + row, item.len - 1), row, cols, vt);
+            const int live = item.len - j * C - 32 * w;  // rows of this warp's 32
+            const int t = item.t0 + j * C + 32 * w;
+            fence_proxy_async();
+            __syncwarp();
+            if (live >= 32) {
+                if (x.lane == 0) {
+                    tma_store_3d(&maps.out, vt + 32 * w * 128, 0, item.h, t);
+                    tma_store_3d(&maps.out, vt + kTile / 2 + 32 * w * 128, 64, item.h, t);
+                    bulk_commit();
+                    bulk_wait_read_all();
+                }
+            } else {
+                // two rows at a time, 16 bytes a lane
+                const int half = x.lane >> 4, l16 = x.lane & 15;
+                __nv_bfloat16* out = p.out + ((int64_t)t * p.H + item.h) * D + 8 * l16;
+#pragma unroll 1
+                for (int r = half; r < live; r += 2)
+                    *reinterpret_cast<uint4*>(out + (int64_t)r * p.H * D) =
+                        *reinterpret_cast<const uint4*>(vt + sw128_off(32 * w + r, 8 * l16, C));
+                fence_proxy_async();
+            }
+            // the last of the four warps frees the tile
+            __syncwarp();
+            if (x.lane == 0) {
+                __threadfence_block();
+                if ((atomicAdd(reinterpret_cast<int*>(x.smem + kSmRows), 1) & 3) == 3)
+                    x.arrive(kEmpty + (tile + 2) % kSlots);
             }
         }
     }
 }
 
-// ---- warps 0-7: weighted v and the state ------------------------------------------
+// Clears infinities and NaN in a lane's column, in every other K step from `odd` on;
+// returns the warp's columns that had any.
+__device__ __noinline__ uint32_t clear_nonfinite(uint8_t* vt, int col, int odd) {
+    bool any = false;
+    for (int i = 0; i < 64; ++i) {
+        const int tok = 32 * (i >> 4) + 16 * odd + (i & 15);
+        uint16_t* at = reinterpret_cast<uint16_t*>(vt + sw128_off(tok, col, C));
+        if ((*at & 0x7F80) == 0x7F80) {
+            *at = 0;
+            any = true;
+        }
+    }
+    fence_proxy_async();
+    return __ballot_sync(0xffffffffu, any);
+}
+
+// ---- warps 8-15: weighted v ---------------------------------------------------------
+// A warp makes 32 value rows of the even K steps (warps 8-11) or of the odd ones.
+__device__ __forceinline__ void weight_role(const LinParams& p, const Ctx& x, int w8) {
+    const int w4 = w8 & 3, odd = w8 >> 2;
+    const uint32_t tm = x.tmem + ((uint32_t)(32 * w4) << 16) + kTmW;
+    // a lane's place in four 8 x 8 matrices: tokens 0-7 and 8-15, value rows 0-7 and 8-15
+    const int tok = (x.lane & 7) + ((x.lane >> 4) << 3);
+    const int col = 32 * w4 + (((x.lane >> 3) & 1) << 3);
+    int tile = 0, c = 0, with_s = 0, cleared = 0;
+    Item item;
+    for (int it = 0; x.item(it, &item, true); ++it) {
+        const int nc = chunks(item.len);
+        for (int j = 0; j < nc; ++j, ++c, tile += 3) {
+            const bool has_s = j > 0 || (item.flags & kInit);
+            const int live = min(C, item.len - j * C);
+            uint8_t* vt = x.tile(tile + 2);
+            if (!x.wait_all(x.full(tile + 2), x.full_phase(tile + 2))) return;
+            if (live < C) {
+                // rows past the sequence's end belong to others: they weigh nothing,
+                // and may hold anything, so they are cleared
+                if (!x.wait_all(x.full(tile + 1), x.full_phase(tile + 1))) return;
+                uint8_t* kt = x.tile(tile + 1);
+                for (int i = 32 * w8 + x.lane; i < (C - live) * 16; i += 256) {
+                    const uint32_t at = (i & 8 ? kTile / 2 : 0) + (live + (i >> 4)) * 128 + (i & 7) * 16;
+                    *reinterpret_cast<uint4*>(kt + at) = make_uint4(0, 0, 0, 0);
+                    *reinterpret_cast<uint4*>(vt + at) = make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async();
+                __syncwarp();
+                if (x.lane == 0) x.arrive(kCleared);
+                if (!x.wait_all(kCleared, cleared & 1)) return;
+                ++cleared;
+            }
+            if (!x.wait_all(kDecFull + (c & 1), (c >> 1) & 1)) return;
+            const float2* wt = reinterpret_cast<const float2*>(x.decays(c) + C) + (x.lane & 3);
+            const uint32_t vs = smem_u32(vt);
+            uint32_t nan2 = 0;  // becomes NaN with any part that is one
+#pragma unroll 1
+            for (int n = 0; n < 4; ++n) {
+                const int ks = 2 * n + odd;  // 16 tokens
+                const float2 wa = wt[8 * ks], wc = wt[8 * ks + 4];
+                const f2 f[2] = {pack2(wa.x, wa.y), pack2(wc.x, wc.y)};
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {  // 16 value rows
+                    uint32_t r[4], hi[4], mi[4], lo[4];
+                    ldsm_x4_t(vs + sw128_off(16 * ks + tok, col + 16 * i, C), r[0], r[1], r[2], r[3]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        f2 a = mul2(f[e >> 1], from_bf(r[e]));
+                        hi[e] = take_bf(a);
+                        mi[e] = take_bf(a);
+                        lo[e] = last_bf(a);
+                        // an infinite or NaN value leaves a NaN in its low part
+                        asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(nan2) : "r"(lo[e]), "r"(0u));
+                    }
+                    if (i == 0) {
+                        // the buffer's last step has been read, and for q's place q
+                        if ((c > 0 || ks >= 5) && !x.wait_all(kWEmpty + w_buffer(ks), w_phase(ks, c) ^ 1)) return;
+                        if (ks >= 2 && ks < 5) {
+                            if (has_s ? !x.wait_all(kQSFull, with_s & 1) : !x.wait_all(kXFull, c & 1)) return;
+                        }
+                        tc_fence_after();
+                    }
+                    const uint32_t at = tm + ((uint32_t)(16 * i) << 16) + 24 * w_buffer(ks);
+                    tmem_st_16x8(at, hi[0], hi[1], hi[2], hi[3]);
+                    tmem_st_16x8(at + 8, mi[0], mi[1], mi[2], mi[3]);
+                    tmem_st_16x8(at + 16, lo[0], lo[1], lo[2], lo[3]);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                if (n == 3) {
+                    uint32_t cols = 0;
+                    if (__any_sync(0xffffffffu, (nan2 & 0x7FFF7FFFu) != 0))
+                        cols = clear_nonfinite(vt, 32 * w4 + x.lane, odd);
+                    if (x.lane == 0) reinterpret_cast<uint32_t*>(x.smem + kSmBad)[8 * (c & 1) + w8] = cols;
+                }
+                __syncwarp();
+                if (x.lane == 0) x.arrive(kWFull + w_buffer(ks));
+            }
+            with_s += has_s;
+            if (x.lane == 0) x.arrive(kDecEmpty + (c & 1));
+        }
+    }
+}
+
+// ---- warps 0-7: the state ----------------------------------------------------------
 // Thread: value row 32 (warp % 4) + lane, key columns 64 (warp / 4) .. + 63.
-template <class S>
-__device__ __forceinline__ float4 load4(const S* s);
+template <class P>
+__device__ __forceinline__ float4 load4(const P* s);
 template <>
 __device__ __forceinline__ float4 load4(const float* s) {
     return *reinterpret_cast<const float4*>(s);
@@ -512,157 +775,105 @@ __device__ __forceinline__ void store4(__half* s, float4 v) {
     *reinterpret_cast<uint2*>(s) = make_uint2(pack_half2(v.x, v.y), pack_half2(v.z, v.w));
 }
 
-// Clears infinities and NaN in a lane's column of the warp's tokens (16 of every
-// 32); returns the warp's columns that had any.
-__device__ __noinline__ uint32_t clear_nonfinite(uint8_t* vt, int col, int sg) {
-    bool any = false;
-    for (int i = 0; i < 64; ++i) {
-        const int tok = 32 * (i >> 4) + 16 * sg + (i & 15);
-        uint16_t* at = reinterpret_cast<uint16_t*>(vt + sw128_off(tok, col, C));
-        if ((*at & 0x7F80) == 0x7F80) {
-            *at = 0;
-            any = true;
-        }
-    }
-    fence_proxy_async();
-    return __ballot_sync(0xffffffffu, any);
-}
-
 template <class P>
 __device__ __forceinline__ void state_role(const LinParams& p, const Ctx& x, int warp) {
     const int sg = warp >> 2;
     const int row = 32 * (warp & 3) + x.lane;
-    const uint32_t tm = x.tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-    int tile = 0, c = 0, with_s = 0, wb = 0, cleared = 0;
-    float S[64];
+    const uint32_t tm = x.tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kTmDS + 64 * sg;
+    int c = 0, with_s = 0;
+    f2 S[32];
     // S as the product's operand: row `row`, columns 64 sg .. + 63
     auto write_operand = [&]() {
+        uint8_t* at = x.smem + kSmS + sg * (kTile / 2) + row * 128;
 #pragma unroll
-        for (int e = 0; e < 64; e += 8) {
+        for (int e = 0; e < 8; ++e) {
             uint32_t hi[4], lo[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                hi[u] = pack_bf162(S[e + 2 * u], S[e + 2 * u + 1]);
-                lo[u] = pack_bf162(S[e + 2 * u] - bf_lo(hi[u]), S[e + 2 * u + 1] - bf_hi(hi[u]));
+                f2 a = S[4 * e + u];
+                hi[u] = take_bf(a);
+                lo[u] = last_bf(a);
             }
-            uint8_t* at = x.smem + kSmS + sw128_off(row, 64 * sg + e, C);
-            *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4*>(at + kTile) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            const uint32_t chunk = (e ^ (row & 7)) << 4;
+            *reinterpret_cast<uint4*>(at + chunk) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(at + kTile + chunk) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
         fence_proxy_async();
         __syncwarp();
         if (x.lane == 0) x.arrive(kSFull);
     };
+    // The warp's 32 x 64 fp32 values of S in the shared memory of its part of the
+    // operand (4 KB of the high, 4 KB of the low part): row r, values 4 e .. 4 e + 3.
+    // Pool rows pass through it so that memory sees whole rows, not one a lane.
+    auto staged = [&](int r, int e) {
+        return reinterpret_cast<float4*>(x.smem + kSmS + (e >> 3) * kTile + sg * (kTile / 2) +
+                                         (32 * (warp & 3) + r) * 128 + (((e & 7) ^ (r & 7)) << 4));
+    };
+    const int l16 = x.lane & 15, half = x.lane >> 4;
     Item item;
     for (int it = 0; x.item(it, &item, true); ++it) {
         const int nc = chunks(item.len);
+        // this lane's 4 columns of the warp's rows half, half + 2, ...
         P* pool = static_cast<P*>(p.pool) +
                   (item.flags & kStore ? (size_t)item.slot * p.stride0 : 0) +
-                  ((size_t)item.h * D + row) * D + 64 * sg;
+                  ((size_t)item.h * D + 32 * (warp & 3) + half) * D + 64 * sg + 4 * l16;
         if (item.flags & kInit) {
-#pragma unroll
-            for (int e = 0; e < 64; e += 4) {
-                const float4 v = load4<P>(pool + e);
-                S[e] = v.x, S[e + 1] = v.y, S[e + 2] = v.z, S[e + 3] = v.w;
-            }
-            // the last q S^T that read the operand
+            // the last q S^T has read the operand
             if (with_s > 0 && !x.wait_all(kQSFull, (with_s + 1) & 1)) return;
+#pragma unroll 8
+            for (int r = 0; r < 32; r += 2) *staged(r + half, l16) = load4<P>(pool + r * D);
+            __syncwarp();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const float4 v = *staged(x.lane, e);
+                S[2 * e] = pack2(v.x, v.y), S[2 * e + 1] = pack2(v.z, v.w);
+            }
+            __syncwarp();
             write_operand();
             ++with_s;
         } else {
 #pragma unroll
-            for (int e = 0; e < 64; ++e) S[e] = 0.f;
+            for (int e = 0; e < 32; ++e) S[e] = 0ull;
         }
-        for (int j = 0; j < nc; ++j, ++c, tile += 3) {
-            const int live = min(C, item.len - j * C);
-            uint8_t* vt = x.tile(tile + 2);
-            if (!x.wait_all(x.full(tile + 2), x.full_phase(tile + 2))) return;
-            if (live < C) {
-                // rows past the sequence's end belong to others: they weigh nothing,
-                // and may hold anything, so they are cleared
-                if (!x.wait_all(x.full(tile), x.full_phase(tile))) return;
-                uint8_t* kt = x.tile(tile);
-                for (int i = (warp * 32 + x.lane); i < (C - live) * 16; i += 256) {
-                    const uint32_t at = (i & 8 ? kTile / 2 : 0) + (live + (i >> 4)) * 128 + (i & 7) * 16;
-                    *reinterpret_cast<uint4*>(kt + at) = make_uint4(0, 0, 0, 0);
-                    *reinterpret_cast<uint4*>(vt + at) = make_uint4(0, 0, 0, 0);
-                }
-                fence_proxy_async();
-                __syncwarp();
-                if (x.lane == 0) x.arrive(kCleared);
-                if (!x.wait_all(kCleared, cleared & 1)) return;
-                ++cleared;
-            }
+        for (int j = 0; j < nc; ++j, ++c) {
             if (!x.wait_all(kDecFull + (c & 1), (c >> 1) & 1)) return;
-            const float* wt = x.decays(c) + C;
             const float gamma = x.gamma(c);
-            const uint32_t vs = smem_u32(vt);
-            uint32_t top = 0;  // largest magnitudes, as bits
-#pragma unroll 1
-            for (int half = 0; half < 4; ++half, ++wb) {
-                const int ks = 2 * half + sg;  // this warp's 16 tokens
-                const float2 wa = *reinterpret_cast<const float2*>(wt + 16 * ks + 2 * (x.lane & 3));
-                const float2 wc = *reinterpret_cast<const float2*>(wt + 16 * ks + 8 + 2 * (x.lane & 3));
-                if (wb >= 2 && !x.wait_all(kWEmpty + (wb & 1), ((wb >> 1) + 1) & 1)) return;
-                tc_fence_after();
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {  // 16 value rows each
-                    // matrices: tokens 0-7 and 8-15, value rows 0-7 and 8-15
-                    const int tok = 16 * ks + (x.lane & 7) + ((x.lane >> 4) << 3);
-                    const int col = 32 * (warp & 3) + 16 * u + (((x.lane >> 3) & 1) << 3);
-                    uint32_t r[4], hi[4], mi[4], lo[4];
-                    ldsm_x4_t(vs + sw128_off(tok, col, C), r[0], r[1], r[2], r[3]);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        top = __vmaxu2(top, r[e] & 0x7FFF7FFFu);
-                        const float2 w = e < 2 ? wa : wc;
-                        float a = w.x * bf_lo(r[e]), b = w.y * bf_hi(r[e]);
-                        hi[e] = pack_bf162(a, b);
-                        a -= bf_lo(hi[e]), b -= bf_hi(hi[e]);
-                        mi[e] = pack_bf162(a, b);
-                        a -= bf_lo(mi[e]), b -= bf_hi(mi[e]);
-                        lo[e] = pack_bf162(a, b);
-                    }
-                    const uint32_t at = tm + ((uint32_t)(16 * u) << 16) + kTmW + (wb & 1) * 48 + sg * 24;
-                    tmem_st_16x8(at, hi[0], hi[1], hi[2], hi[3]);
-                    tmem_st_16x8(at + 8, mi[0], mi[1], mi[2], mi[3]);
-                    tmem_st_16x8(at + 16, lo[0], lo[1], lo[2], lo[3]);
-                }
-                tmem_wait_st();
-                tc_fence_before();
-                if (half == 3) {
-                    const bool any = (top & 0xFFFFu) >= 0x7F80u || (top >> 16) >= 0x7F80u;
-                    uint32_t cols = 0;
-                    if (__any_sync(0xffffffffu, any)) cols = clear_nonfinite(vt, 32 * (warp & 3) + x.lane, sg);
-                    if (x.lane == 0) reinterpret_cast<uint32_t*>(x.smem + kSmBad)[8 * (c & 1) + warp] = cols;
-                }
-                __syncwarp();
-                if (x.lane == 0) x.arrive(kWFull + (wb & 1));
-            }
+            __syncwarp();
             if (x.lane == 0) x.arrive(kDecEmpty + (c & 1));
             if (!x.wait_all(kDSFull, c & 1)) return;
             tc_fence_after();
+            const f2 g2 = pack2(gamma, gamma);
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                uint32_t r[32];
-                tmem_ld32(tm + kTmDS + 64 * sg + 32 * b, r);
+            for (int b = 0; b < 4; ++b) {
+                uint32_t r[16];
+                tmem_ld16u(tm + 16 * b, r);
                 tmem_wait_ld();
+                if (b == 3) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (x.lane == 0) x.arrive(kDSEmpty);
+                }
 #pragma unroll
-                for (int e = 0; e < 32; ++e)
-                    S[32 * b + e] = fmaf(gamma, S[32 * b + e], __uint_as_float(r[e]));
+                for (int e = 0; e < 16; e += 2)
+                    S[8 * b + e / 2] = fma2(g2, S[8 * b + e / 2],
+                                             pack2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])));
             }
-            tc_fence_before();
-            __syncwarp();
-            if (x.lane == 0) x.arrive(kDSEmpty);
             if (j + 1 < nc) {
                 if (with_s > 0 && !x.wait_all(kQSFull, (with_s + 1) & 1)) return;
                 write_operand();
                 ++with_s;
             }
         }
-        if (item.flags & kStore) {
+        if (item.flags & kStore) {  // the chunk's q S^T, issued before dS, has read the operand
 #pragma unroll
-            for (int e = 0; e < 64; e += 4) store4(pool + e, make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]));
+            for (int e = 0; e < 16; ++e) {
+                const float2 a = unpack2(S[2 * e]), b = unpack2(S[2 * e + 1]);
+                *staged(x.lane, e) = make_float4(a.x, a.y, b.x, b.y);
+            }
+            __syncwarp();
+#pragma unroll 8
+            for (int r = 0; r < 32; r += 2) store4(pool + r * D, *staged(r + half, l16));
+            __syncwarp();
         }
     }
 }
@@ -684,38 +895,48 @@ __global__ void __launch_bounds__(kThreads, 1) kda_lin_walk(const __grid_constan
     if (threadIdx.x == 0) {
         for (int i = 0; i < kNumBars; ++i) {
             int n = 1;
-            if (i == kDecEmpty || i == kDecEmpty + 1) n = 12;
-            if (i >= kItemEmpty && i < kItemEmpty + kItems) n = 14;
+            if (i == kDecEmpty || i == kDecEmpty + 1) n = 24;
+            if (i >= kItemEmpty && i < kItemEmpty + kItems) n = 26;
             if (i == kPFull || i == kQSScaled || i == kOEmpty) n = 4;
-            if (i == kWFull || i == kWFull + 1 || i == kDSEmpty || i == kSFull || i == kCleared) n = 8;
+            if (i >= kWFull && i < kWFull + 5) n = 4;
+            if (i == kDSEmpty || i == kSFull || i == kCleared) n = 8;
             mbar_init(x.bar + i, n);
         }
         *x.abort = 0;
+        *reinterpret_cast<int*>(smem + kSmRows) = 0;
         fence_mbar_init();
         prefetch_tmap(&maps.q);
         prefetch_tmap(&maps.k);
         prefetch_tmap(&maps.v);
+        prefetch_tmap(&maps.out);
     }
-    if (warp == 12) tmem_alloc(slot, kTmCols);
+    if (warp == 24) tmem_alloc(slot, kTmCols);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     x.tmem = *slot;
 
+    // registers: the launch's 896 x 72 = 256 x 112 + 640 x 56
     int issued = 0;
     if (warp < 8) {
+        more_registers<112>();
         state_role<P>(p, x, warp);
-    } else if (warp < 12) {
-        score_role(p, x, warp - 8);
-    } else if (warp == 12) {
-        if (x.lane == 0) {
-            mma_role(x);
-            mma_commit(x.bar + kDone);
-        }
-    } else if (warp == 13) {
-        if (x.lane == 0) issued = load_role(maps, p, x);
     } else {
-        decay_role(p, x);
+        fewer_registers<56>();
+        if (warp < 16) {
+            weight_role(p, x, warp - 8);
+        } else if (warp < 20) {
+            score_role(p, x, warp - 16);
+        } else if (warp < 24) {
+            out_role(maps, p, x, warp - 20);
+        } else if (warp == 24) {
+            mma_role(x);
+            if (elect_one()) mma_commit(x.bar + kDone);  // the lane that issued
+        } else if (warp == 25) {
+            if (x.lane == 0) issued = load_role(maps, p, x);
+        } else if (warp == 26) {
+            decay_role(p, x);
+        }
     }
     __syncwarp();
     tc_fence_before();
@@ -724,16 +945,16 @@ __global__ void __launch_bounds__(kThreads, 1) kda_lin_walk(const __grid_constan
     if (*x.abort) {
         // a wait gave up: let the copies and products in flight end before their memory goes
         if (threadIdx.x == 0) atomicOr(p.status, 1);
-        if (warp == 13 && x.lane == 0)
+        if (warp == 25 && x.lane == 0)
             for (int i = max(0, issued - kSlots); i < issued; ++i)
                 mbar_wait(x.bar + kFull + i % kSlots, (i / kSlots) & 1);
     }
-    if (warp == 12) {
+    if (warp == 24) {
         mbar_wait(x.bar + kDone, 0);
         tc_fence_after();
     }
     __syncthreads();
-    if (warp == 12) tmem_dealloc(x.tmem, kTmCols);
+    if (warp == 24) tmem_dealloc(x.tmem, kTmCols);
 }
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
@@ -752,16 +973,16 @@ EncodeTiledFn encode_fn() {
     return fn;
 }
 
-// Boxes of 64 values x 1 head x C tokens of a [T][H][128] view; tokens past the
+// Boxes of 64 values x 1 head x `rows` tokens of a [T][H][128] view; tokens past the
 // end read as zeros.
-bool make_map(CUtensorMap* m, const void* base, int64_t T, int H, int64_t st, int64_t sh) {
+bool make_map(CUtensorMap* m, const void* base, int64_t T, int H, int64_t st, int64_t sh, int rows) {
     if (!encode_fn()) return false;
     // a dimension of one entry never steps: any stride that encodes will do
     if (T == 1) st = D;
     if (H == 1) sh = D;
     const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)T};
     const cuuint64_t strides[2] = {(cuuint64_t)sh * 2, (cuuint64_t)st * 2};
-    const cuuint32_t box[3] = {64, 1, (cuuint32_t)C};
+    const cuuint32_t box[3] = {64, 1, (cuuint32_t)rows};
     const cuuint32_t step[3] = {1, 1, 1};
     return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides,
                        box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -784,9 +1005,10 @@ cudaError_t launch_lin_walk(const LinParams& p, cudaStream_t s) {
     if (p.n_long <= 0) return cudaSuccess;
     if ((int64_t)p.n_long * p.H > INT32_MAX - 65536) return cudaErrorInvalidValue;
     Maps maps;
-    if (!make_map(&maps.q, p.q, p.T, p.H / p.rep, p.q_st, p.q_sh) ||
-        !make_map(&maps.k, p.k, p.T, p.H / p.rep, p.k_st, p.k_sh) ||
-        !make_map(&maps.v, p.v, p.T, p.H, p.v_st, p.v_sh))
+    if (!make_map(&maps.q, p.q, p.T, p.H / p.rep, p.q_st, p.q_sh, C) ||
+        !make_map(&maps.k, p.k, p.T, p.H / p.rep, p.k_st, p.k_sh, C) ||
+        !make_map(&maps.v, p.v, p.T, p.H, p.v_st, p.v_sh, C) ||
+        !make_map(&maps.out, p.out, p.T, p.H, (int64_t)p.H * D, D, 32))
         return cudaErrorInvalidValue;
     if (p.st_dtype == KDA_STATE_F32) return launch<float>(maps, p, s);
     if (p.st_dtype == KDA_STATE_BF16) return launch<__nv_bfloat16>(maps, p, s);
