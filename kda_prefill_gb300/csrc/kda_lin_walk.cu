@@ -18,7 +18,11 @@
 //
 // Rounding.  Operands are bf16.  q, k and v are; P and S are carried as a sum of
 // two bf16 (16 bits: with one, a rounding as large as out's own would be added
-// to it), W as a sum of three (24 bits, the state is fp32).  dS starts from zero
+// to it).  W has to keep 24 bits, the state being fp32: with the weight as a sum
+// of three bf16, w = w1 + w2 + w3, it is the four bf16 a = v w1, its remainder
+// v w1 - a (exact, one fused product), b = v w2 and the remainder v w2 - b + v w3.
+// Five operations on pairs of bf16 make them; the shortest sum, of three, would
+// take thirteen in fp32.  dS starts from zero
 // every chunk and S' is formed in fp32 registers, so that S is rounded once a
 // chunk however the tensor cores round their partial sums.
 //
@@ -53,8 +57,9 @@ constexpr int kItems = 3;         // items the claims run ahead
 // Shared memory.  Tiles are two halves of 64 columns, 128-byte swizzled.
 constexpr int kSmS = 0;                        // S as bf16: high part, then low part
 constexpr int kSmTile = 2 * kTile;
-constexpr int kSmG = kSmTile + kSlots * kTile;  // [2][G, prefix sums in log2; e^R]
-constexpr int kSmCf = kSmG + 2 * 2 * C * 4;     // [96] e^{G_b - G_j}
+constexpr int kSmW = kSmTile + kSlots * kTile;  // [2][64] e^R of token pairs, each in three parts
+constexpr int kSmG = kSmW + 2 * (C / 2) * 12;   // [128] G, prefix sums in log2
+constexpr int kSmCf = kSmG + C * 4;             // [96] e^{G_b - G_j}
 struct Item {
     int t0, len, h, n, slot, flags;
 };
@@ -66,9 +71,10 @@ static_assert(kSmBar % 8 == 0, "barriers are 8-byte aligned");
 enum Bar {
     kFull = 0,                  // [5] tile loaded
     kEmpty = kFull + kSlots,    // [5] tile consumed
-    kDecFull = kEmpty + kSlots, // [2] decays of a chunk made
+    kDecFull = kEmpty + kSlots, // [2] weights and e^{G_C} of a chunk made
     kDecEmpty = kDecFull + 2,   // [2] and read
-    kCfFull = kDecEmpty + 2,    // factors of score columns made
+    kGFull = kDecEmpty + 2,     // G and the factors of score columns made
+    kGEmpty,                    // and read
     kItemFull,                  // [3] item claimed
     kItemEmpty = kItemFull + kItems,
     kXFull = kItemEmpty + kItems,  // q k^T in X
@@ -77,9 +83,9 @@ enum Bar {
     kQSScaled,                  // e^{G_i} applied
     kOFull,                     // the chunk's O complete
     kOEmpty,                    // and read
-    kWFull,                     // [5] a K step of W written
-    kWEmpty = kWFull + 5,       // [5] and read
-    kDSFull = kWEmpty + 5,      // dS complete
+    kWFull,                     // [2] two K steps of W written
+    kWEmpty = kWFull + 2,       // [2] and read
+    kDSFull = kWEmpty + 2,      // dS complete
     kDSEmpty,                   // and read
     kSFull,                     // S's operand written
     kCleared,                   // rows past a sequence's end cleared
@@ -87,20 +93,22 @@ enum Bar {
     kNumBars
 };
 constexpr int kSmGamma = kSmBar + kNumBars * 8;  // [2] e^{G_C}
-constexpr int kSmBad = kSmGamma + 8;             // [2][8] value columns with infinities or NaN
+constexpr int kSmBad = (kSmGamma + 8 + 15) & ~15;  // [2][8] value columns with infinities or NaN
 constexpr int kSmMisc = kSmBad + 64;             // tensor-memory base, abort flag
 constexpr int kSmRows = kSmMisc + 8;             // warps done with a q tile's rows
 constexpr int kSmemBytes = kSmRows + 8;
 static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
+static_assert(kSmG % 16 == 0 && kSmCf % 16 == 0 && kSmBad % 16 == 0, "read by 16 bytes");
+static_assert(kSmGamma % 8 == 0 && kSmMisc % 8 == 0 && kSmRows % 8 == 0, "words");
 
 // Tensor memory columns.
 constexpr uint32_t kTmX = 0;    // X; then P: per 32 tokens 16 columns high part, 16 low
 constexpr uint32_t kTmO = 128;
 constexpr uint32_t kTmDS = 256;
-constexpr uint32_t kTmW = 384;  // [5] buffers of a K step of W: (high, middle, low) x 8 columns;
-                                // the last three take q's place once q S^T is done, so that
-                                // enough steps are under way to hide their handing over
-constexpr uint32_t kTmQ = 432;  // q: with both operands in shared memory an MMA reads all of
+constexpr uint32_t kTmW = 384;  // [4] buffers of a K step of W: four parts x 8 columns; the last
+                                // two take q's place once q S^T is done, so that enough steps
+                                // are under way to hide their handing over
+constexpr uint32_t kTmQ = 448;  // q: with both operands in shared memory an MMA reads all of
                                 // its bandwidth, and everything else there waits
 constexpr uint32_t kTmCols = 512;
 
@@ -122,7 +130,29 @@ __device__ __forceinline__ void tmem_cp_step(uint32_t d, uint64_t desc) {
     asm volatile("tcgen05.cp.cta_group::1.128x256b [%0], %1;" ::"r"(d), "l"(desc) : "memory");
 }
 
-// 16 columns of this thread's lane.
+// 32 or 16 columns of this thread's lane.
+__device__ __forceinline__ void tmem_ld32(uint32_t a, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+        "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+          "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+          "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(a));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t a, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
+        "%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+        "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
+        "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
+        "r"(r[30]), "r"(r[31]), "r"(a)
+        : "memory");
+}
 __device__ __forceinline__ void tmem_ld16u(uint32_t a, uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
@@ -194,6 +224,22 @@ __device__ __forceinline__ uint32_t last_bf(f2 a) {
     const float2 v = unpack2(a);
     return pack_bf162(v.x, v.y);
 }
+// Pairs of bf16.
+__device__ __forceinline__ uint32_t mul_bf2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t fma_bf2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t r;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+    return r;
+}
+__device__ __forceinline__ uint32_t neg_bf2(uint32_t a) {
+    uint32_t r;
+    asm("neg.bf16x2 %0, %1;" : "=r"(r) : "r"(a));
+    return r;
+}
 template <int N>
 __device__ __forceinline__ void more_registers() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -207,11 +253,6 @@ __device__ __forceinline__ bool elect_one() {
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
     return p != 0;
 }
-
-// Buffer of W's step ks (0 .. 7), and the phase of its use in chunk c: buffers 0, 1
-// and 2 are used twice a chunk.
-__device__ __forceinline__ int w_buffer(int ks) { return ks < 5 ? ks : ks - 5; }
-__device__ __forceinline__ uint32_t w_phase(int ks, int c) { return ks == 3 || ks == 4 ? c & 1 : ks >= 5; }
 
 struct Maps {
     CUtensorMap q, k, v, out;
@@ -245,8 +286,9 @@ struct Ctx {
     // Barrier and phase of tile i's load.
     static __device__ __forceinline__ int full(int i) { return kFull + i % kSlots; }
     static __device__ __forceinline__ uint32_t full_phase(int i) { return (i / kSlots) & 1; }
-    __device__ __forceinline__ const float* decays(int c) const {
-        return reinterpret_cast<const float*>(smem + kSmG) + (c & 1) * 2 * C;
+    // Parts of the weights of the token pairs of chunk c.
+    __device__ __forceinline__ const uint32_t* weights(int c) const {
+        return reinterpret_cast<const uint32_t*>(smem + kSmW) + (c & 1) * 3 * (C / 2);
     }
     __device__ __forceinline__ float gamma(int c) const {
         return reinterpret_cast<const float*>(smem + kSmGamma)[c & 1];
@@ -321,15 +363,15 @@ __device__ __forceinline__ void decay_role(const LinParams& p, const Ctx& x) {
             if (x.lane == 0) before = 0.f;
             if (x.lane == 31) after = 0.f;
             if (c >= 2 && !x.wait_all(kDecEmpty + (c & 1), ((c >> 1) + 1) & 1)) return;
-            float* dst = const_cast<float*>(x.decays(c));
-            constexpr float kLog2e = 1.4426950408889634f;
-            float4 G, w;
-            G.x = (before + pre[0]) * kLog2e, G.y = (before + pre[1]) * kLog2e;
-            G.z = (before + pre[2]) * kLog2e, G.w = (before + pre[3]) * kLog2e;
-            w.x = expf(after + suf[0]), w.y = expf(after + suf[1]);
-            w.z = expf(after + suf[2]), w.w = expf(after + suf[3]);
-            reinterpret_cast<float4*>(dst)[x.lane] = G;
-            reinterpret_cast<float4*>(dst + C)[x.lane] = w;
+            const float e[4] = {expf(after + suf[0]), expf(after + suf[1]), expf(after + suf[2]), expf(after + suf[3])};
+            uint32_t* w = const_cast<uint32_t*>(x.weights(c)) + 6 * x.lane;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                f2 v = pack2(e[2 * u], e[2 * u + 1]);
+                w[3 * u] = take_bf(v);
+                w[3 * u + 1] = take_bf(v);
+                w[3 * u + 2] = last_bf(v);
+            }
             if (x.lane == 0) reinterpret_cast<float*>(x.smem + kSmGamma)[c & 1] = expf(total);
             __syncwarp();
             if (x.lane == 0) x.arrive(kDecFull + (c & 1));
@@ -342,12 +384,16 @@ __device__ __forceinline__ void decay_role(const LinParams& p, const Ctx& x) {
             }
             rest = __shfl_down_sync(0xffffffffu, rest, 1, 8);
             if ((x.lane & 7) == 7) rest = 0.f;
-            if (c > 0 && !x.wait_all(kPFull, (c + 1) & 1)) return;
+            if (c > 0 && !x.wait_all(kGEmpty, (c + 1) & 1)) return;
+            constexpr float kLog2e = 1.4426950408889634f;
+            reinterpret_cast<float4*>(x.smem + kSmG)[x.lane] =
+                make_float4((before + pre[0]) * kLog2e, (before + pre[1]) * kLog2e,
+                            (before + pre[2]) * kLog2e, (before + pre[3]) * kLog2e);
             if (x.lane < 24)
                 reinterpret_cast<float4*>(x.smem + kSmCf)[x.lane] =
                     make_float4(expf(rest + suf[0]), expf(rest + suf[1]), expf(rest + suf[2]), expf(rest + suf[3]));
             __syncwarp();
-            if (x.lane == 0) x.arrive(kCfFull);
+            if (x.lane == 0) x.arrive(kGFull);
         }
     }
 }
@@ -430,15 +476,17 @@ __device__ __forceinline__ void mma_role(const Ctx& x) {
             }
             if (c > 0 && !x.wait_all(kDSEmpty, (c + 1) & 1)) return;
 #pragma unroll
-            for (int ks = 0; ks < 8; ++ks) {
-                if (!x.wait_all(kWFull + w_buffer(ks), w_phase(ks, c))) return;
+            for (int n = 0; n < 4; ++n) {  // 32 tokens each
+                if (!x.wait_all(kWFull + (n & 1), n >> 1)) return;
                 tc_fence_after();
                 if (lead) {
 #pragma unroll
-                    for (int part = 2; part >= 0; --part)
-                        mma_f16_ts(x.tmem + kTmDS, x.tmem + kTmW + w_buffer(ks) * 24 + part * 8, km + mstep(ks), kIdescKM,
-                                   ks > 0 || part < 2);
-                    mma_commit(x.bar + kWEmpty + w_buffer(ks));
+                    for (int ks = 2 * n; ks < 2 * n + 2; ++ks)
+#pragma unroll
+                        for (int part = 3; part >= 0; --part)
+                            mma_f16_ts(x.tmem + kTmDS, x.tmem + kTmW + (ks & 3) * 32 + part * 8, km + mstep(ks), kIdescKM,
+                                       ks > 0 || part < 3);
+                    mma_commit(x.bar + kWEmpty + (n & 1));
                 }
                 __syncwarp();
             }
@@ -485,15 +533,14 @@ __device__ __noinline__ void put_nonfinite(const LinParams& p, const Item& item,
 __device__ __forceinline__ void score_role(const LinParams& p, const Ctx& x, int w) {
     const int row = 32 * w + x.lane;
     const uint32_t tm = x.tmem + ((uint32_t)(32 * w) << 16) + kTmX;
+    const float* G = reinterpret_cast<const float*>(x.smem + kSmG);
     const float* cf = reinterpret_cast<const float*>(x.smem + kSmCf);
     int c = 0;
     Item item;
     for (int it = 0; x.item(it, &item, true); ++it) {
         for (int j = 0; j < chunks(item.len); ++j, ++c) {
-            if (!x.wait_all(kDecFull + (c & 1), (c >> 1) & 1)) return;
-            const float* G = x.decays(c);
+            if (!x.wait_all(kGFull, c & 1)) return;
             const float gi = G[row];
-            if (!x.wait_all(kCfFull, c & 1)) return;
             if (!x.wait_all(kXFull, c & 1)) return;
             tc_fence_after();
             // Sixteen scores become eight pairs of high parts and eight of low parts.
@@ -542,7 +589,7 @@ __device__ __forceinline__ void score_role(const LinParams& p, const Ctx& x, int
             __syncwarp();
             if (x.lane == 0) {
                 x.arrive(kPFull);
-                x.arrive(kDecEmpty + (c & 1));
+                x.arrive(kGEmpty);
             }
         }
     }
@@ -558,27 +605,25 @@ __device__ __forceinline__ void out_role(const Maps& maps, const LinParams& p, c
     for (int it = 0; x.item(it, &item, true); ++it) {
         for (int j = 0; j < chunks(item.len); ++j, ++c, tile += 3) {
             const bool has_s = j > 0 || (item.flags & kInit);
-            if (!x.wait_all(kDecFull + (c & 1), (c >> 1) & 1)) return;
-            const float f = ex2(x.decays(c)[row]);
+            if (!x.wait_all(kGFull, c & 1)) return;
+            const float f = ex2(reinterpret_cast<const float*>(x.smem + kSmG)[row]);
             __syncwarp();
-            if (x.lane == 0) x.arrive(kDecEmpty + (c & 1));
+            if (x.lane == 0) x.arrive(kGEmpty);
             if (has_s) {
                 if (!x.wait_all(kQSFull, with_s & 1)) return;
                 tc_fence_after();
                 const f2 ff = pack2(f, f);
-                uint32_t r[16];
-                tmem_ld16u(tm, r);
 #pragma unroll 1
-                for (int b = 0; b < 8; ++b) {
-                    uint32_t y[16];
+                for (int b = 0; b < 4; ++b) {
+                    uint32_t r[32];
+                    tmem_ld32(tm + 32 * b, r);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 16; e += 2) {
+                    for (int e = 0; e < 32; e += 2) {
                         const float2 v = unpack2(mul2(ff, pack2(__uint_as_float(r[e]), __uint_as_float(r[e + 1]))));
-                        y[e] = __float_as_uint(v.x), y[e + 1] = __float_as_uint(v.y);
+                        r[e] = __float_as_uint(v.x), r[e + 1] = __float_as_uint(v.y);
                     }
-                    if (b < 7) tmem_ld16u(tm + 16 * b + 16, r);
-                    tmem_st16(tm + 16 * b, y);
+                    tmem_st32(tm + 32 * b, r);
                 }
                 tmem_wait_st();
                 tc_fence_before();
@@ -595,19 +640,19 @@ __device__ __forceinline__ void out_role(const Maps& maps, const LinParams& p, c
             const uint4* bad = reinterpret_cast<const uint4*>(x.smem + kSmBad) + 2 * (c & 1);
             uint4 cols = bad[0];
             cols.x |= bad[1].x, cols.y |= bad[1].y, cols.z |= bad[1].z, cols.w |= bad[1].w;
-            uint32_t r[16];
-            tmem_ld16u(tm, r);
 #pragma unroll 1
-            for (int b = 0; b < 8; ++b) {
-                uint32_t y[8];
+            for (int b = 0; b < 4; ++b) {
+                uint32_t r[32];
+                tmem_ld32(tm + 32 * b, r);
                 tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 16; e += 2)
-                    y[e / 2] = last_bf(mul2(scale, pack2(__uint_as_float(r[e]), __uint_as_float(r[e + 1]))));
-                if (b < 7) tmem_ld16u(tm + 16 * b + 16, r);
+                for (int e = 0; e < 32; e += 8) {
+                    uint32_t y[4];
 #pragma unroll
-                for (int e = 0; e < 8; e += 4)
-                    *reinterpret_cast<uint4*>(vt + sw128_off(row, 16 * b + 2 * e, C)) = make_uint4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+                    for (int u = 0; u < 4; ++u)
+                        y[u] = last_bf(mul2(scale, pack2(__uint_as_float(r[e + 2 * u]), __uint_as_float(r[e + 2 * u + 1]))));
+                    *reinterpret_cast<uint4*>(vt + sw128_off(row, 32 * b + e, C)) = make_uint4(y[0], y[1], y[2], y[3]);
+                }
             }
             tc_fence_before();
             __syncwarp();
@@ -646,12 +691,12 @@ __device__ __forceinline__ void out_role(const Maps& maps, const LinParams& p, c
     }
 }
 
-// Clears infinities and NaN in a lane's column, in every other K step from `odd` on;
+// Clears infinities and NaN in a lane's column, in every other 32 tokens from `odd` on;
 // returns the warp's columns that had any.
 __device__ __noinline__ uint32_t clear_nonfinite(uint8_t* vt, int col, int odd) {
     bool any = false;
     for (int i = 0; i < 64; ++i) {
-        const int tok = 32 * (i >> 4) + 16 * odd + (i & 15);
+        const int tok = 64 * (i >> 5) + 32 * odd + (i & 31);
         uint16_t* at = reinterpret_cast<uint16_t*>(vt + sw128_off(tok, col, C));
         if ((*at & 0x7F80) == 0x7F80) {
             *at = 0;
@@ -663,10 +708,11 @@ __device__ __noinline__ uint32_t clear_nonfinite(uint8_t* vt, int col, int odd) 
 }
 
 // ---- warps 8-15: weighted v ---------------------------------------------------------
-// A warp makes 32 value rows of the even K steps (warps 8-11) or of the odd ones.
+// A warp makes 32 value rows of two K steps at a time, warps 8-11 of the first and third
+// 32 tokens, warps 12-15 of the others (whose place is q's until q S^T is done).
 __device__ __forceinline__ void weight_role(const LinParams& p, const Ctx& x, int w8) {
     const int w4 = w8 & 3, odd = w8 >> 2;
-    const uint32_t tm = x.tmem + ((uint32_t)(32 * w4) << 16) + kTmW;
+    const uint32_t tm = x.tmem + ((uint32_t)(32 * w4) << 16) + kTmW + 64 * odd;
     // a lane's place in four 8 x 8 matrices: tokens 0-7 and 8-15, value rows 0-7 and 8-15
     const int tok = (x.lane & 7) + ((x.lane >> 4) << 3);
     const int col = 32 * w4 + (((x.lane >> 3) & 1) << 3);
@@ -696,50 +742,52 @@ __device__ __forceinline__ void weight_role(const LinParams& p, const Ctx& x, in
                 ++cleared;
             }
             if (!x.wait_all(kDecFull + (c & 1), (c >> 1) & 1)) return;
-            const float2* wt = reinterpret_cast<const float2*>(x.decays(c) + C) + (x.lane & 3);
+            const uint32_t* wt = x.weights(c) + 3 * (x.lane & 3);
             const uint32_t vs = smem_u32(vt);
             uint32_t nan2 = 0;  // becomes NaN with any part that is one
 #pragma unroll 1
-            for (int n = 0; n < 4; ++n) {
-                const int ks = 2 * n + odd;  // 16 tokens
-                const float2 wa = wt[8 * ks], wc = wt[8 * ks + 4];
-                const f2 f[2] = {pack2(wa.x, wa.y), pack2(wc.x, wc.y)};
+            for (int n = 0; n < 2; ++n) {
+                const int t0 = 64 * n + 32 * odd;
+                uint32_t w[4][3];  // the weights' parts, of tokens t0 + 8 e + 2 (lane % 4) .. + 1
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {  // 16 value rows
-                    uint32_t r[4], hi[4], mi[4], lo[4];
-                    ldsm_x4_t(vs + sw128_off(16 * ks + tok, col + 16 * i, C), r[0], r[1], r[2], r[3]);
+                for (int e = 0; e < 4; ++e)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        f2 a = mul2(f[e >> 1], from_bf(r[e]));
-                        hi[e] = take_bf(a);
-                        mi[e] = take_bf(a);
-                        lo[e] = last_bf(a);
-                        // an infinite or NaN value leaves a NaN in its low part
-                        asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(nan2) : "r"(lo[e]), "r"(0u));
-                    }
-                    if (i == 0) {
-                        // the buffer's last step has been read, and for q's place q
-                        if ((c > 0 || ks >= 5) && !x.wait_all(kWEmpty + w_buffer(ks), w_phase(ks, c) ^ 1)) return;
-                        if (ks >= 2 && ks < 5) {
-                            if (has_s ? !x.wait_all(kQSFull, with_s & 1) : !x.wait_all(kXFull, c & 1)) return;
-                        }
-                        tc_fence_after();
-                    }
-                    const uint32_t at = tm + ((uint32_t)(16 * i) << 16) + 24 * w_buffer(ks);
-                    tmem_st_16x8(at, hi[0], hi[1], hi[2], hi[3]);
-                    tmem_st_16x8(at + 8, mi[0], mi[1], mi[2], mi[3]);
-                    tmem_st_16x8(at + 16, lo[0], lo[1], lo[2], lo[3]);
+                    for (int u = 0; u < 3; ++u) w[e][u] = wt[3 * (t0 / 2 + 4 * e) + u];
+                // the buffers' last steps have been read, and for q's place q
+                if ((c > 0 || n > 0) && !x.wait_all(kWEmpty + odd, n ^ 1)) return;
+                if (odd && n == 0) {
+                    if (has_s ? !x.wait_all(kQSFull, with_s & 1) : !x.wait_all(kXFull, c & 1)) return;
                 }
+                tc_fence_after();
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {  // 16 tokens, 16 value rows
+                        uint32_t r[4], t[4][4];
+                        ldsm_x4_t(vs + sw128_off(t0 + 16 * s + tok, col + 16 * i, C), r[0], r[1], r[2], r[3]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const uint32_t* u = w[2 * s + (e >> 1)];
+                            t[0][e] = mul_bf2(r[e], u[0]);
+                            t[1][e] = fma_bf2(r[e], u[0], neg_bf2(t[0][e]));  // exact
+                            t[2][e] = mul_bf2(r[e], u[1]);
+                            t[3][e] = fma_bf2(r[e], u[2], fma_bf2(r[e], u[1], neg_bf2(t[2][e])));
+                            nan2 = fma_bf2(t[1][e], 0u, nan2);  // an infinite or NaN value leaves a NaN
+                        }
+                        const uint32_t at = tm + ((uint32_t)(16 * i) << 16) + 32 * s;
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) tmem_st_16x8(at + 8 * u, t[u][0], t[u][1], t[u][2], t[u][3]);
+                    }
                 tmem_wait_st();
                 tc_fence_before();
-                if (n == 3) {
+                if (n == 1) {
                     uint32_t cols = 0;
                     if (__any_sync(0xffffffffu, (nan2 & 0x7FFF7FFFu) != 0))
                         cols = clear_nonfinite(vt, 32 * w4 + x.lane, odd);
                     if (x.lane == 0) reinterpret_cast<uint32_t*>(x.smem + kSmBad)[8 * (c & 1) + w8] = cols;
                 }
                 __syncwarp();
-                if (x.lane == 0) x.arrive(kWFull + w_buffer(ks));
+                if (x.lane == 0) x.arrive(kWFull + odd);
             }
             with_s += has_s;
             if (x.lane == 0) x.arrive(kDecEmpty + (c & 1));
@@ -780,7 +828,7 @@ __device__ __forceinline__ void state_role(const LinParams& p, const Ctx& x, int
     const int sg = warp >> 2;
     const int row = 32 * (warp & 3) + x.lane;
     const uint32_t tm = x.tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kTmDS + 64 * sg;
-    int c = 0, with_s = 0;
+    int c = 0;
     f2 S[32];
     // S as the product's operand: row `row`, columns 64 sg .. + 63
     auto write_operand = [&]() {
@@ -818,9 +866,8 @@ __device__ __forceinline__ void state_role(const LinParams& p, const Ctx& x, int
                   (item.flags & kStore ? (size_t)item.slot * p.stride0 : 0) +
                   ((size_t)item.h * D + 32 * (warp & 3) + half) * D + 64 * sg + 4 * l16;
         if (item.flags & kInit) {
-            // the last q S^T has read the operand
-            if (with_s > 0 && !x.wait_all(kQSFull, (with_s + 1) & 1)) return;
-#pragma unroll 8
+            // the last q S^T has read the operand: it was issued before the last dS
+#pragma unroll 4
             for (int r = 0; r < 32; r += 2) *staged(r + half, l16) = load4<P>(pool + r * D);
             __syncwarp();
 #pragma unroll
@@ -830,7 +877,6 @@ __device__ __forceinline__ void state_role(const LinParams& p, const Ctx& x, int
             }
             __syncwarp();
             write_operand();
-            ++with_s;
         } else {
 #pragma unroll
             for (int e = 0; e < 32; ++e) S[e] = 0ull;
@@ -858,11 +904,7 @@ __device__ __forceinline__ void state_role(const LinParams& p, const Ctx& x, int
                     S[8 * b + e / 2] = fma2(g2, S[8 * b + e / 2],
                                              pack2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])));
             }
-            if (j + 1 < nc) {
-                if (with_s > 0 && !x.wait_all(kQSFull, (with_s + 1) & 1)) return;
-                write_operand();
-                ++with_s;
-            }
+            if (j + 1 < nc) write_operand();
         }
         if (item.flags & kStore) {  // the chunk's q S^T, issued before dS, has read the operand
 #pragma unroll
@@ -871,7 +913,7 @@ __device__ __forceinline__ void state_role(const LinParams& p, const Ctx& x, int
                 *staged(x.lane, e) = make_float4(a.x, a.y, b.x, b.y);
             }
             __syncwarp();
-#pragma unroll 8
+#pragma unroll 4
             for (int r = 0; r < 32; r += 2) store4(pool + r * D, *staged(r + half, l16));
             __syncwarp();
         }
@@ -895,10 +937,11 @@ __global__ void __launch_bounds__(kThreads, 1) kda_lin_walk(const __grid_constan
     if (threadIdx.x == 0) {
         for (int i = 0; i < kNumBars; ++i) {
             int n = 1;
-            if (i == kDecEmpty || i == kDecEmpty + 1) n = 24;
+            if (i == kDecEmpty || i == kDecEmpty + 1) n = 16;
+            if (i == kGEmpty) n = 8;
             if (i >= kItemEmpty && i < kItemEmpty + kItems) n = 26;
             if (i == kPFull || i == kQSScaled || i == kOEmpty) n = 4;
-            if (i >= kWFull && i < kWFull + 5) n = 4;
+            if (i == kWFull || i == kWFull + 1) n = 4;
             if (i == kDSEmpty || i == kSFull || i == kCleared) n = 8;
             mbar_init(x.bar + i, n);
         }
@@ -916,20 +959,23 @@ __global__ void __launch_bounds__(kThreads, 1) kda_lin_walk(const __grid_constan
     tc_fence_after();
     x.tmem = *slot;
 
-    // registers: the launch's 896 x 72 = 256 x 112 + 640 x 56
+    // registers: the launch's 896 x 72 = 256 x 112 + 256 x 64 + 256 x 56 + 128 x 40
     int issued = 0;
     if (warp < 8) {
         more_registers<112>();
         state_role<P>(p, x, warp);
-    } else {
+    } else if (warp < 16) {
+        fewer_registers<64>();
+        weight_role(p, x, warp - 8);
+    } else if (warp < 20) {
         fewer_registers<56>();
-        if (warp < 16) {
-            weight_role(p, x, warp - 8);
-        } else if (warp < 20) {
-            score_role(p, x, warp - 16);
-        } else if (warp < 24) {
-            out_role(maps, p, x, warp - 20);
-        } else if (warp == 24) {
+        score_role(p, x, warp - 16);
+    } else if (warp < 24) {
+        fewer_registers<56>();
+        out_role(maps, p, x, warp - 20);
+    } else {
+        fewer_registers<40>();
+        if (warp == 24) {
             mma_role(x);
             if (elect_one()) mma_commit(x.bar + kDone);  // the lane that issued
         } else if (warp == 25) {
