@@ -13,8 +13,11 @@
 //   20-23 the e^{G_i} on q S^T, the output rows
 //   24    issues the MMAs     25  issues the TMA loads
 //   26    claims items and makes the decays
-// Each role's work on a chunk is shorter than the chunk's time; what bounds it is
-// the chain QK -> P -> PV -> next QK beside QS -> KV -> S -> next QS.
+// A chunk's products are issued as X, the first half of dS, q S^T, the other half, P v:
+// each role's work (P after X, S after dS, e^{G_i} after q S^T, the rows after P v) has
+// products that do not wait for it running beside it.  X takes q from tensor memory: an
+// MMA with both operands in shared memory reads all of its bandwidth, and every other
+// access to it waits.  q S^T has to (W needs the room); it runs when few others read.
 //
 // Rounding.  Operands are bf16.  q, k and v are; P and S are carried as a sum of
 // two bf16 (16 bits: with one, a rounding as large as out's own would be added
@@ -105,11 +108,9 @@ static_assert(kSmGamma % 8 == 0 && kSmMisc % 8 == 0 && kSmRows % 8 == 0, "words"
 constexpr uint32_t kTmX = 0;    // X; then P: per 32 tokens 16 columns high part, 16 low
 constexpr uint32_t kTmO = 128;
 constexpr uint32_t kTmDS = 256;
-constexpr uint32_t kTmW = 384;  // [4] buffers of a K step of W: four parts x 8 columns; the last
-                                // two take q's place once q S^T is done, so that enough steps
-                                // are under way to hide their handing over
-constexpr uint32_t kTmQ = 448;  // q: with both operands in shared memory an MMA reads all of
-                                // its bandwidth, and everything else there waits
+constexpr uint32_t kTmW = 384;  // [2] buffers of 32 tokens of W: two K steps x four parts x 8
+                                // columns; the second is q's place, free once X is done
+constexpr uint32_t kTmQ = 448;  // q, for X
 constexpr uint32_t kTmCols = 512;
 
 constexpr uint32_t kIdescKK = mma_idesc(1, 0, 0, 128, 128);  // B K-major
@@ -442,9 +443,25 @@ __device__ __forceinline__ void mma_role(const Ctx& x) {
             const bool has_s = j > 0 || (item.flags & kInit);
             const uint32_t qa = smem_u32(x.tile(tile)), ka = smem_u32(x.tile(tile + 1)), va = smem_u32(x.tile(tile + 2));
             const uint64_t k = kdesc(ka), q = kdesc(qa), km = mdesc(ka), vm = mdesc(va);
+            auto add_tokens = [&](int n) {  // dS over tokens 32 n .. 32 n + 31
+                if (!x.wait_all(kWFull + (n & 1), n >> 1)) return false;
+                tc_fence_after();
+                if (lead) {
+#pragma unroll
+                    for (int s = 0; s < 2; ++s)
+#pragma unroll
+                        for (int part = 3; part >= 0; --part)
+                            mma_f16_ts(x.tmem + kTmDS, x.tmem + kTmW + 64 * (n & 1) + 32 * s + 8 * part,
+                                       km + mstep(2 * n + s), kIdescKM, n > 0 || s > 0 || part < 3);
+                    mma_commit(x.bar + kWEmpty + (n & 1));
+                }
+                __syncwarp();
+                return true;
+            };
             if (!x.wait_all(x.full(tile), x.full_phase(tile))) return;
             if (!x.wait_all(x.full(tile + 1), x.full_phase(tile + 1))) return;
-            // X is free once the previous chunk's P v has read it
+            // X is free once the previous chunk's P v has read it, and W's second buffer
+            // with it: its last product was issued before
             if (c > 0 && !x.wait_all(kOFull, (c + 1) & 1)) return;
             tc_fence_after();
             if (lead) {
@@ -455,9 +472,11 @@ __device__ __forceinline__ void mma_role(const Ctx& x) {
                 for (int ks = 0; ks < 8; ++ks)
                     mma_f16_ts(x.tmem + kTmX, x.tmem + kTmQ + 8 * ks, k + kstep(ks), kIdescKK, ks > 0);
                 mma_commit(x.bar + kXFull);
-                mma_commit(x.bar + kEmpty + tile % kSlots);
+                if (!has_s) mma_commit(x.bar + kEmpty + tile % kSlots);
             }
             __syncwarp();
+            if (c > 0 && !x.wait_all(kDSEmpty, (c + 1) & 1)) return;
+            if (!add_tokens(0) || !add_tokens(1)) return;
             // O is free once the previous chunk's rows have been read
             if (c > 0 && !x.wait_all(kOEmpty, (c + 1) & 1)) return;
             if (has_s) {
@@ -466,30 +485,16 @@ __device__ __forceinline__ void mma_role(const Ctx& x) {
                 if (lead) {
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks)  // low part first
-                        mma_f16_ts(x.tmem + kTmO, x.tmem + kTmQ + 8 * ks, s_lo + kstep(ks), kIdescKK, ks > 0);
+                        mma_f16_ss(x.tmem + kTmO, q + kstep(ks), s_lo + kstep(ks), kIdescKK, ks > 0);
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks)
-                        mma_f16_ts(x.tmem + kTmO, x.tmem + kTmQ + 8 * ks, s_hi + kstep(ks), kIdescKK, 1);
+                        mma_f16_ss(x.tmem + kTmO, q + kstep(ks), s_hi + kstep(ks), kIdescKK, 1);
                     mma_commit(x.bar + kQSFull);
+                    mma_commit(x.bar + kEmpty + tile % kSlots);
                 }
                 __syncwarp();
             }
-            if (c > 0 && !x.wait_all(kDSEmpty, (c + 1) & 1)) return;
-#pragma unroll
-            for (int n = 0; n < 4; ++n) {  // 32 tokens each
-                if (!x.wait_all(kWFull + (n & 1), n >> 1)) return;
-                tc_fence_after();
-                if (lead) {
-#pragma unroll
-                    for (int ks = 2 * n; ks < 2 * n + 2; ++ks)
-#pragma unroll
-                        for (int part = 3; part >= 0; --part)
-                            mma_f16_ts(x.tmem + kTmDS, x.tmem + kTmW + (ks & 3) * 32 + part * 8, km + mstep(ks), kIdescKM,
-                                       ks > 0 || part < 3);
-                    mma_commit(x.bar + kWEmpty + (n & 1));
-                }
-                __syncwarp();
-            }
+            if (!add_tokens(2) || !add_tokens(3)) return;
             if (lead) {
                 mma_commit(x.bar + kDSFull);
                 mma_commit(x.bar + kEmpty + (tile + 1) % kSlots);
@@ -709,19 +714,18 @@ __device__ __noinline__ uint32_t clear_nonfinite(uint8_t* vt, int col, int odd) 
 
 // ---- warps 8-15: weighted v ---------------------------------------------------------
 // A warp makes 32 value rows of two K steps at a time, warps 8-11 of the first and third
-// 32 tokens, warps 12-15 of the others (whose place is q's until q S^T is done).
+// 32 tokens, warps 12-15 of the others (whose place is q's until X is done).
 __device__ __forceinline__ void weight_role(const LinParams& p, const Ctx& x, int w8) {
     const int w4 = w8 & 3, odd = w8 >> 2;
     const uint32_t tm = x.tmem + ((uint32_t)(32 * w4) << 16) + kTmW + 64 * odd;
     // a lane's place in four 8 x 8 matrices: tokens 0-7 and 8-15, value rows 0-7 and 8-15
     const int tok = (x.lane & 7) + ((x.lane >> 4) << 3);
     const int col = 32 * w4 + (((x.lane >> 3) & 1) << 3);
-    int tile = 0, c = 0, with_s = 0, cleared = 0;
+    int tile = 0, c = 0, cleared = 0;
     Item item;
     for (int it = 0; x.item(it, &item, true); ++it) {
         const int nc = chunks(item.len);
         for (int j = 0; j < nc; ++j, ++c, tile += 3) {
-            const bool has_s = j > 0 || (item.flags & kInit);
             const int live = min(C, item.len - j * C);
             uint8_t* vt = x.tile(tile + 2);
             if (!x.wait_all(x.full(tile + 2), x.full_phase(tile + 2))) return;
@@ -755,9 +759,7 @@ __device__ __forceinline__ void weight_role(const LinParams& p, const Ctx& x, in
                     for (int u = 0; u < 3; ++u) w[e][u] = wt[3 * (t0 / 2 + 4 * e) + u];
                 // the buffers' last steps have been read, and for q's place q
                 if ((c > 0 || n > 0) && !x.wait_all(kWEmpty + odd, n ^ 1)) return;
-                if (odd && n == 0) {
-                    if (has_s ? !x.wait_all(kQSFull, with_s & 1) : !x.wait_all(kXFull, c & 1)) return;
-                }
+                if (odd && n == 0 && !x.wait_all(kXFull, c & 1)) return;
                 tc_fence_after();
 #pragma unroll
                 for (int s = 0; s < 2; ++s)
@@ -789,7 +791,6 @@ __device__ __forceinline__ void weight_role(const LinParams& p, const Ctx& x, in
                 __syncwarp();
                 if (x.lane == 0) x.arrive(kWFull + odd);
             }
-            with_s += has_s;
             if (x.lane == 0) x.arrive(kDecEmpty + (c & 1));
         }
     }
