@@ -13,8 +13,8 @@
 //   20-23 the e^{G_i} on q S^T, the output rows
 //   24    issues the MMAs     25  issues the TMA loads
 //   26    claims items and makes the decays
-// A chunk's products are issued as X, the first half of dS, q S^T, the other half, P v:
-// each role's work (P after X, S after dS, e^{G_i} after q S^T, the rows after P v) has
+// A chunk's products are issued as dS of the first 32 tokens, X, q S^T, the rest of dS,
+// P v: each role's work (P after X, S after dS, e^{G_i} after q S^T, the rows after P v) has
 // products that do not wait for it running beside it.  X takes q from tensor memory: an
 // MMA with both operands in shared memory reads all of its bandwidth, and every other
 // access to it waits.  q S^T has to (W needs the room); it runs when few others read.
@@ -267,21 +267,61 @@ struct Ctx {
     uint32_t tmem;
     int lane;
 
-    // Waits for a barrier's phase; gives up after about a second, or once another
-    // role has (the callers then leave their loops).
+    // Waits for phases of barriers; gives up after about a second, or once another role
+    // has (the callers then leave their loops).  A whole warp goes on or leaves together.
+    // Waiting for several at once overlaps the looks at them, over a hundred cycles each
+    // even when the phase is over.  A role must have seen a barrier's phase before last
+    // to be over when it waits for one: parities alone do not tell them apart.
+    __device__ __forceinline__ uint32_t at(int b) const { return smem_u32(smem) + kSmBar + 8 * b; }
+#define KDA_WAIT_END                               \
+    "@p bra DONE;\n\t"                             \
+    "ld.volatile.shared.u32 f, [%1];\n\t"          \
+    "setp.ne.u32 p, f, 0;\n\t"                     \
+    "@p bra OUT;\n\t"                              \
+    "sub.u32 n, n, 1;\n\t"                         \
+    "setp.ne.u32 p, n, 0;\n\t"                     \
+    "@p bra AGAIN;\n\t"                            \
+    "st.volatile.shared.u32 [%1], 1;\n\t"          \
+    "OUT:\n\tmov.u32 %0, 0;\n\tbra END;\n\t"      \
+    "DONE:\n\tmov.u32 %0, 1;\n\tEND:\n\t}"
     __device__ __forceinline__ bool wait(int b, uint32_t parity) const {
-#pragma unroll 1
-        for (uint32_t i = 0; i < kWaitLimit; ++i) {
-            if (mbar_try_wait(bar + b, parity)) return true;
-            if (*abort) return false;
-        }
-        *abort = 1;
-        return false;
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .u32 n, f;\n\tmov.u32 n, %2;\n\tAGAIN:\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%3], %4;\n\t" KDA_WAIT_END
+            : "=r"(ok)
+            : "r"(smem_u32(smem) + kSmMisc + 4), "n"(kWaitLimit), "r"(at(b)), "r"(parity)
+            : "memory");
+        return ok != 0;
     }
-    // The same for a whole warp, which goes on or leaves together.
     __device__ __forceinline__ bool wait_all(int b, uint32_t parity) const {
         return __all_sync(0xffffffffu, wait(b, parity));
     }
+    __device__ __forceinline__ bool wait_all(int b0, uint32_t p0, int b1, uint32_t p1) const {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\t.reg .u32 n, f;\n\tmov.u32 n, %2;\n\tAGAIN:\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%3], %4;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 q, [%5], %6;\n\tand.pred p, p, q;\n\t" KDA_WAIT_END
+            : "=r"(ok)
+            : "r"(smem_u32(smem) + kSmMisc + 4), "n"(kWaitLimit), "r"(at(b0)), "r"(p0), "r"(at(b1)), "r"(p1)
+            : "memory");
+        return __all_sync(0xffffffffu, ok != 0);
+    }
+    __device__ __forceinline__ bool wait_all(int b0, uint32_t p0, int b1, uint32_t p1, int b2, uint32_t p2) const {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\t.reg .u32 n, f;\n\tmov.u32 n, %2;\n\tAGAIN:\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%3], %4;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 q, [%5], %6;\n\tand.pred p, p, q;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 q, [%7], %8;\n\tand.pred p, p, q;\n\t" KDA_WAIT_END
+            : "=r"(ok)
+            : "r"(smem_u32(smem) + kSmMisc + 4), "n"(kWaitLimit), "r"(at(b0)), "r"(p0), "r"(at(b1)), "r"(p1),
+              "r"(at(b2)), "r"(p2)
+            : "memory");
+        return __all_sync(0xffffffffu, ok != 0);
+    }
+#undef KDA_WAIT_END
     __device__ __forceinline__ void arrive(int b) const { mbar_arrive(bar + b); }
     __device__ __forceinline__ uint8_t* tile(int i) const { return smem + kSmTile + (i % kSlots) * kTile; }
     // Barrier and phase of tile i's load.
@@ -364,11 +404,10 @@ __device__ __forceinline__ void decay_role(const LinParams& p, const Ctx& x) {
             if (x.lane == 0) before = 0.f;
             if (x.lane == 31) after = 0.f;
             if (c >= 2 && !x.wait_all(kDecEmpty + (c & 1), ((c >> 1) + 1) & 1)) return;
-            const float e[4] = {expf(after + suf[0]), expf(after + suf[1]), expf(after + suf[2]), expf(after + suf[3])};
             uint32_t* w = const_cast<uint32_t*>(x.weights(c)) + 6 * x.lane;
-#pragma unroll
+#pragma unroll 1
             for (int u = 0; u < 2; ++u) {
-                f2 v = pack2(e[2 * u], e[2 * u + 1]);
+                f2 v = pack2(expf(after + (u ? suf[2] : suf[0])), expf(after + (u ? suf[3] : suf[1])));
                 w[3 * u] = take_bf(v);
                 w[3 * u + 1] = take_bf(v);
                 w[3 * u + 2] = last_bf(v);
@@ -408,10 +447,10 @@ __device__ __forceinline__ int load_role(const Maps& maps, const LinParams& p, c
         for (int j = 0; j < chunks(item.len); ++j) {
             const int t = item.t0 + j * C;
 #pragma unroll
-            for (int m = 0; m < 3; ++m, ++tile) {  // q, k, v, in the order that they come free
+            for (int m = 0; m < 3; ++m, ++tile) {  // q, v, k: in the order that they come free
                 if (tile >= kSlots && !x.wait(kEmpty + tile % kSlots, ((tile / kSlots) + 1) & 1)) return tile;
-                const CUtensorMap* map = m == 0 ? &maps.q : m == 1 ? &maps.k : &maps.v;
-                const int h = m == 2 ? item.h : item.h / p.rep;
+                const CUtensorMap* map = m == 0 ? &maps.q : m == 1 ? &maps.v : &maps.k;
+                const int h = m == 1 ? item.h : item.h / p.rep;
                 uint64_t* bar = x.bar + kFull + tile % kSlots;
                 uint8_t* dst = x.tile(tile);
                 mbar_arrive_expect_tx(bar, kTile);
@@ -441,70 +480,68 @@ __device__ __forceinline__ void mma_role(const Ctx& x) {
         const int nc = chunks(item.len);
         for (int j = 0; j < nc; ++j, ++c, tile += 3) {
             const bool has_s = j > 0 || (item.flags & kInit);
-            const uint32_t qa = smem_u32(x.tile(tile)), ka = smem_u32(x.tile(tile + 1)), va = smem_u32(x.tile(tile + 2));
+            const uint32_t qa = smem_u32(x.tile(tile)), va = smem_u32(x.tile(tile + 1)), ka = smem_u32(x.tile(tile + 2));
             const uint64_t k = kdesc(ka), q = kdesc(qa), km = mdesc(ka), vm = mdesc(va);
             auto add_tokens = [&](int n) {  // dS over tokens 32 n .. 32 n + 31
-                if (!x.wait_all(kWFull + (n & 1), n >> 1)) return false;
                 tc_fence_after();
                 if (lead) {
-#pragma unroll
+#pragma unroll 1
                     for (int s = 0; s < 2; ++s)
 #pragma unroll
-                        for (int part = 3; part >= 0; --part)
+                        for (int part = 3; part >= 0; --part)  // the smallest first
                             mma_f16_ts(x.tmem + kTmDS, x.tmem + kTmW + 64 * (n & 1) + 32 * s + 8 * part,
                                        km + mstep(2 * n + s), kIdescKM, n > 0 || s > 0 || part < 3);
                     mma_commit(x.bar + kWEmpty + (n & 1));
                 }
                 __syncwarp();
-                return true;
             };
-            if (!x.wait_all(x.full(tile), x.full_phase(tile))) return;
-            if (!x.wait_all(x.full(tile + 1), x.full_phase(tile + 1))) return;
+            const int fq = x.full(tile), fk = x.full(tile + 2);
+            const uint32_t pq = x.full_phase(tile), pk = x.full_phase(tile + 2);
+            if (c == 0 ? !x.wait_all(fk, pk, kWFull, 0) : !x.wait_all(fk, pk, kWFull, 0, kDSEmpty, (c + 1) & 1)) return;
+            add_tokens(0);
             // X is free once the previous chunk's P v has read it, and W's second buffer
             // with it: its last product was issued before
-            if (c > 0 && !x.wait_all(kOFull, (c + 1) & 1)) return;
+            if (c == 0 ? !x.wait_all(fq, pq) : !x.wait_all(fq, pq, kOFull, (c + 1) & 1)) return;
             tc_fence_after();
             if (lead) {
-#pragma unroll
+#pragma unroll 2
                 for (int ks = 0; ks < 8; ++ks)
                     tmem_cp_step(x.tmem + kTmQ + 8 * ks, q + kstep(ks));
-#pragma unroll
+#pragma unroll 2
                 for (int ks = 0; ks < 8; ++ks)
                     mma_f16_ts(x.tmem + kTmX, x.tmem + kTmQ + 8 * ks, k + kstep(ks), kIdescKK, ks > 0);
                 mma_commit(x.bar + kXFull);
                 if (!has_s) mma_commit(x.bar + kEmpty + tile % kSlots);
             }
             __syncwarp();
-            if (c > 0 && !x.wait_all(kDSEmpty, (c + 1) & 1)) return;
-            if (!add_tokens(0) || !add_tokens(1)) return;
             // O is free once the previous chunk's rows have been read
-            if (c > 0 && !x.wait_all(kOEmpty, (c + 1) & 1)) return;
             if (has_s) {
-                if (!x.wait_all(kSFull, with_s & 1)) return;
+                if (c == 0 ? !x.wait_all(kSFull, with_s & 1) : !x.wait_all(kSFull, with_s & 1, kOEmpty, (c + 1) & 1)) return;
                 tc_fence_after();
                 if (lead) {
-#pragma unroll
-                    for (int ks = 0; ks < 8; ++ks)  // low part first
-                        mma_f16_ss(x.tmem + kTmO, q + kstep(ks), s_lo + kstep(ks), kIdescKK, ks > 0);
-#pragma unroll
-                    for (int ks = 0; ks < 8; ++ks)
-                        mma_f16_ss(x.tmem + kTmO, q + kstep(ks), s_hi + kstep(ks), kIdescKK, 1);
+#pragma unroll 2
+                    for (int ks = 0; ks < 16; ++ks)  // the low part first
+                        mma_f16_ss(x.tmem + kTmO, q + kstep(ks & 7), (ks < 8 ? s_lo : s_hi) + kstep(ks & 7), kIdescKK, ks > 0);
                     mma_commit(x.bar + kQSFull);
                     mma_commit(x.bar + kEmpty + tile % kSlots);
                 }
                 __syncwarp();
             }
-            if (!add_tokens(2) || !add_tokens(3)) return;
+            if (!x.wait_all(kWFull + 1, 0)) return;
+            add_tokens(1);
+            if (!x.wait_all(kWFull, 1)) return;
+            add_tokens(2);
+            // P and O are awaited before the products that are still to come, not after
+            if (has_s ? !x.wait_all(kWFull + 1, 1, kPFull, c & 1, kQSScaled, with_s & 1)
+                      : !x.wait_all(kWFull + 1, 1, kPFull, c & 1)) return;
+            if (c > 0 && !has_s && !x.wait_all(kOEmpty, (c + 1) & 1)) return;
+            add_tokens(3);
             if (lead) {
                 mma_commit(x.bar + kDSFull);
-                mma_commit(x.bar + kEmpty + (tile + 1) % kSlots);
+                mma_commit(x.bar + kEmpty + (tile + 2) % kSlots);
             }
-            __syncwarp();
-            if (!x.wait_all(kPFull, c & 1)) return;
-            if (has_s && !x.wait_all(kQSScaled, with_s & 1)) return;
-            tc_fence_after();
             if (lead) {
-#pragma unroll
+#pragma unroll 1
                 for (int ks = 0; ks < 8; ++ks)
 #pragma unroll
                     for (int part = 1; part >= 0; --part)
@@ -523,9 +560,12 @@ __device__ __forceinline__ void mma_role(const Ctx& x) {
 __device__ __noinline__ void put_nonfinite(const LinParams& p, const Item& item, int t0, int t1, int row,
                                            uint4 cols, uint8_t* tile) {
     const uint16_t* v = reinterpret_cast<const uint16_t*>(p.v) + (int64_t)item.h * p.v_sh;
+#pragma unroll 1
     for (int g = 0; g < 4; ++g)
+#pragma unroll 1
         for (uint32_t m = g == 0 ? cols.x : g == 1 ? cols.y : g == 2 ? cols.z : cols.w; m; m &= m - 1) {
             const int col = 32 * g + __ffs(m) - 1;
+#pragma unroll 1
             for (int t = t0; t <= t1; ++t)
                 if ((v[(int64_t)(item.t0 + t) * p.v_st + col] & 0x7F80) == 0x7F80) {
                     *reinterpret_cast<uint16_t*>(tile + sw128_off(row, col, C)) = 0x7FFF;
@@ -544,9 +584,8 @@ __device__ __forceinline__ void score_role(const LinParams& p, const Ctx& x, int
     Item item;
     for (int it = 0; x.item(it, &item, true); ++it) {
         for (int j = 0; j < chunks(item.len); ++j, ++c) {
-            if (!x.wait_all(kGFull, c & 1)) return;
+            if (!x.wait_all(kGFull, c & 1, kXFull, c & 1)) return;
             const float gi = G[row];
-            if (!x.wait_all(kXFull, c & 1)) return;
             tc_fence_after();
             // Sixteen scores become eight pairs of high parts and eight of low parts.
             // A block of 32 is held as high 0-15, high 16-31, low 0-15, low 16-31 so
@@ -641,7 +680,7 @@ __device__ __forceinline__ void out_role(const Maps& maps, const LinParams& p, c
             // The rows go through v's tile, which has been read, so that whole rows
             // are written to memory: lanes that each store a row of their own fill
             // the load/store unit with single sectors and hold up everything else.
-            uint8_t* vt = x.tile(tile + 2);
+            uint8_t* vt = x.tile(tile + 1);
             const uint4* bad = reinterpret_cast<const uint4*>(x.smem + kSmBad) + 2 * (c & 1);
             uint4 cols = bad[0];
             cols.x |= bad[1].x, cols.y |= bad[1].y, cols.z |= bad[1].z, cols.w |= bad[1].w;
@@ -690,7 +729,7 @@ __device__ __forceinline__ void out_role(const Maps& maps, const LinParams& p, c
             if (x.lane == 0) {
                 __threadfence_block();
                 if ((atomicAdd(reinterpret_cast<int*>(x.smem + kSmRows), 1) & 3) == 3)
-                    x.arrive(kEmpty + (tile + 2) % kSlots);
+                    x.arrive(kEmpty + (tile + 1) % kSlots);
             }
         }
     }
@@ -700,6 +739,7 @@ __device__ __forceinline__ void out_role(const Maps& maps, const LinParams& p, c
 // returns the warp's columns that had any.
 __device__ __noinline__ uint32_t clear_nonfinite(uint8_t* vt, int col, int odd) {
     bool any = false;
+#pragma unroll 1
     for (int i = 0; i < 64; ++i) {
         const int tok = 64 * (i >> 5) + 32 * odd + (i & 31);
         uint16_t* at = reinterpret_cast<uint16_t*>(vt + sw128_off(tok, col, C));
@@ -727,13 +767,14 @@ __device__ __forceinline__ void weight_role(const LinParams& p, const Ctx& x, in
         const int nc = chunks(item.len);
         for (int j = 0; j < nc; ++j, ++c, tile += 3) {
             const int live = min(C, item.len - j * C);
-            uint8_t* vt = x.tile(tile + 2);
-            if (!x.wait_all(x.full(tile + 2), x.full_phase(tile + 2))) return;
+            uint8_t* vt = x.tile(tile + 1);
+            if (!x.wait_all(x.full(tile + 1), x.full_phase(tile + 1))) return;
             if (live < C) {
                 // rows past the sequence's end belong to others: they weigh nothing,
                 // and may hold anything, so they are cleared
-                if (!x.wait_all(x.full(tile + 1), x.full_phase(tile + 1))) return;
-                uint8_t* kt = x.tile(tile + 1);
+                if (!x.wait_all(x.full(tile + 2), x.full_phase(tile + 2))) return;
+                uint8_t* kt = x.tile(tile + 2);
+#pragma unroll 1
                 for (int i = 32 * w8 + x.lane; i < (C - live) * 16; i += 256) {
                     const uint32_t at = (i & 8 ? kTile / 2 : 0) + (live + (i >> 4)) * 128 + (i & 7) * 16;
                     *reinterpret_cast<uint4*>(kt + at) = make_uint4(0, 0, 0, 0);
@@ -752,24 +793,25 @@ __device__ __forceinline__ void weight_role(const LinParams& p, const Ctx& x, in
 #pragma unroll 1
             for (int n = 0; n < 2; ++n) {
                 const int t0 = 64 * n + 32 * odd;
-                uint32_t w[4][3];  // the weights' parts, of tokens t0 + 8 e + 2 (lane % 4) .. + 1
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-#pragma unroll
-                    for (int u = 0; u < 3; ++u) w[e][u] = wt[3 * (t0 / 2 + 4 * e) + u];
                 // the buffers' last steps have been read, and for q's place q
                 if ((c > 0 || n > 0) && !x.wait_all(kWEmpty + odd, n ^ 1)) return;
                 if (odd && n == 0 && !x.wait_all(kXFull, c & 1)) return;
                 tc_fence_after();
+#pragma unroll 1
+                for (int s = 0; s < 2; ++s) {  // 16 tokens
+                    uint32_t w[2][3];  // the weights' parts, of tokens 2 (lane % 4) .. + 1 and those 8 on
 #pragma unroll
-                for (int s = 0; s < 2; ++s)
+                    for (int u = 0; u < 3; ++u) {
+                        w[0][u] = wt[3 * (t0 / 2 + 8 * s) + u];
+                        w[1][u] = wt[3 * (t0 / 2 + 8 * s + 4) + u];
+                    }
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {  // 16 tokens, 16 value rows
+                    for (int i = 0; i < 2; ++i) {  // 16 value rows
                         uint32_t r[4], t[4][4];
                         ldsm_x4_t(vs + sw128_off(t0 + 16 * s + tok, col + 16 * i, C), r[0], r[1], r[2], r[3]);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const uint32_t* u = w[2 * s + (e >> 1)];
+                            const uint32_t* u = w[e >> 1];
                             t[0][e] = mul_bf2(r[e], u[0]);
                             t[1][e] = fma_bf2(r[e], u[0], neg_bf2(t[0][e]));  // exact
                             t[2][e] = mul_bf2(r[e], u[1]);
@@ -780,6 +822,7 @@ __device__ __forceinline__ void weight_role(const LinParams& p, const Ctx& x, in
 #pragma unroll
                         for (int u = 0; u < 4; ++u) tmem_st_16x8(at + 8 * u, t[u][0], t[u][1], t[u][2], t[u][3]);
                     }
+                }
                 tmem_wait_st();
                 tc_fence_before();
                 if (n == 1) {
