@@ -91,8 +91,7 @@ struct MetaLayout {
     int64_t n_chunks = 0;
     int32_t n_long = 0, n_short = 0;
     int32_t max_long_chunks = 0;  // chunks of the longest sequence the chunked kernels take
-    int64_t long_tokens = 0;      // tokens of the sequences the chunked kernels take
-    int32_t max_long = 0;         // tokens of the longest of them
+    std::vector<int32_t> long_lens;  // lengths of the sequences the chunked kernels take, longest first
     size_t off_cu = 0, off_seq_off = 0, off_chunk_seq = 0, off_chunk_tok = 0;  // int32 units
     size_t off_long = 0, off_short = 0;
     size_t words = 0;
@@ -110,11 +109,11 @@ MetaLayout meta_layout(const int32_t* cu, int32_t N) {
             ++L.n_short;
         } else {
             ++L.n_long;
-            L.long_tokens += len;
-            L.max_long = std::max<int32_t>(L.max_long, (int32_t)len);
+            L.long_lens.push_back((int32_t)len);
         }
         L.max_long_chunks = std::max<int32_t>(L.max_long_chunks, (int32_t)routed_chunks(len));
     }
+    std::sort(L.long_lens.begin(), L.long_lens.end(), [](int32_t a, int32_t b) { return a > b; });
     size_t o = 0;
     L.off_cu = o;        o = align4(o + (size_t)N + 1);
     L.off_seq_off = o;   o = align4(o + (size_t)N + 1);
@@ -665,8 +664,7 @@ int with_seq_tables(const int32_t* cu_dev, const int32_t* cu_host, int32_t N, in
     if (rc != KDA_OK) return rc;
     const MetaLayout& L = m->layout;
     SeqTables t{m->dev + L.off_cu, m->dev + L.off_long, m->dev + L.off_short,
-                L.n_long,          L.n_short,           L.long_tokens,
-                L.max_long};
+                L.n_long,          L.n_short,           L.long_lens.data()};
     rc = enqueue(arg, t);
     if (rc != KDA_OK) return rc;
     cache().mark_use(m, stream, capturing);

@@ -65,9 +65,11 @@ constexpr int kSmG = kSmW + 2 * (C / 2) * 12;   // [128] G, prefix sums in log2
 constexpr int kSmCf = kSmG + C * 4;             // [96] e^{G_b - G_j}
 struct Item {
     int t0, len, h, n, slot, flags;
+    int plane;  // of the workspace: the segment's state
+    int unused;
 };
 constexpr int kSmItem = kSmCf + 96 * 4;
-enum { kInit = 1, kStore = 2, kEnd = 4 };
+enum { kInit = 1, kStore = 2, kEnd = 4, kPlane = 8 };
 constexpr int kSmBar = kSmItem + kItems * (int)sizeof(Item);
 static_assert(kSmBar % 8 == 0, "barriers are 8-byte aligned");
 
@@ -255,6 +257,11 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 
+// Tiles of a chunk, in the order of their loads: q, v, k; Local: v, k.
+template <bool Local> constexpr int kPerChunk = Local ? 2 : 3;
+template <bool Local> constexpr int kV = Local ? 0 : 1;
+template <bool Local> constexpr int kK = Local ? 1 : 2;
+
 struct Maps {
     CUtensorMap q, k, v, out;
 };
@@ -347,27 +354,76 @@ struct Ctx {
 __device__ __forceinline__ int chunks(int len) { return (len + C - 1) / C; }
 
 // ---- warp 26: items and decays ------------------------------------------------
+// Item i of the call.  The first p.n_cut sequences (the longest) are cut into segments of
+// p.seg_len tokens, whose items come first; Local: their segments but the last.
+template <bool Local>
+__device__ __forceinline__ Item make_item(const LinParams& p, int i, int lane) {
+    Item item{};
+    const int k = i / p.H;
+    item.h = i - k * p.H;
+    int r = 0, s = 0, first = 0;  // sequence, segment, segments of the sequences before
+    const int n_seg = Local ? p.n_seg - p.n_cut : p.n_seg;
+    if (k < n_seg) {
+        for (;; r += 32) {
+            int segs = 0;
+            if (r + lane < p.n_cut) {
+                const int n = p.long_list[r + lane];
+                segs = (p.cu[n + 1] - p.cu[n] + p.seg_len - 1) / p.seg_len - (Local ? 1 : 0);
+            }
+            int upto = segs;
+#pragma unroll
+            for (int w = 1; w < 32; w <<= 1) {
+                const int u = __shfl_up_sync(0xffffffffu, upto, w);
+                if (lane >= w) upto += u;
+            }
+            upto += first;
+            const uint32_t past = __ballot_sync(0xffffffffu, upto > k);
+            if (past || r + 32 >= p.n_cut) {
+                const int at = past ? __ffs(past) - 1 : 31;
+                first = __shfl_sync(0xffffffffu, upto - segs, at);
+                r += at;
+                break;
+            }
+            first = __shfl_sync(0xffffffffu, upto, 31);
+        }
+        s = k - first;
+        item.plane = ((Local ? first + r : first) + s) * p.H + item.h;
+    } else {
+        r = p.n_cut + k - n_seg;
+    }
+    item.n = p.long_list[r];
+    const int len = p.cu[item.n + 1] - p.cu[item.n];
+    item.t0 = p.cu[item.n];
+    item.len = len;
+    bool last = true;
+    if (k < n_seg) {
+        item.t0 += s * p.seg_len;
+        item.len = min(p.seg_len, len - s * p.seg_len);
+        last = (s + 1) * p.seg_len >= len;
+    }
+    if (Local) return item;
+    item.slot = p.idx[item.n];
+    const bool ok = item.slot >= 0 && item.slot < p.num_slots;
+    if (!ok && lane == 0) atomicOr(p.status, 4);
+    item.flags = (ok && last ? kStore : 0) | (k < n_seg ? kPlane : ok && p.has_init[item.n] ? kInit : 0);
+    return item;
+}
+
+template <bool Local>
 __device__ __forceinline__ void decay_role(const LinParams& p, const Ctx& x) {
-    const int n_items = p.n_long * p.H;
+    const int n_items = (Local ? p.n_seg - p.n_cut : p.n_seg + p.n_long - p.n_cut) * p.H;
+    int* queue = reinterpret_cast<int*>(reinterpret_cast<char*>(p.status) + (Local ? kWsDecodeOff : kWsQueueOff));
     int c = 0;
     for (int it = 0;; ++it) {
         if (it >= kItems && !x.wait_all(kItemEmpty + it % kItems, ((it / kItems) + 1) & 1)) return;
         int i = 0;
-        if (x.lane == 0) i = atomicAdd(reinterpret_cast<int*>(reinterpret_cast<char*>(p.status) + kWsQueueOff), 1);
+        if (x.lane == 0) i = atomicAdd(queue, 1);
         i = __shfl_sync(0xffffffffu, i, 0);
         Item item{};
-        if (i < n_items) {
-            item.n = p.long_list[i / p.H];
-            item.h = i % p.H;
-            item.t0 = p.cu[item.n];
-            item.len = p.cu[item.n + 1] - item.t0;
-            item.slot = p.idx[item.n];
-            const bool ok = item.slot >= 0 && item.slot < p.num_slots;
-            if (!ok && x.lane == 0) atomicOr(p.status, 4);
-            item.flags = (ok ? kStore : 0) | (ok && p.has_init[item.n] ? kInit : 0);
-        } else {
+        if (i < n_items)
+            item = make_item<Local>(p, i, x.lane);
+        else
             item.flags = kEnd;
-        }
         if (x.lane == 0) {
             reinterpret_cast<Item*>(x.smem + kSmItem)[it % kItems] = item;
             x.arrive(kItemFull + it % kItems);  // releases the write
@@ -415,6 +471,7 @@ __device__ __forceinline__ void decay_role(const LinParams& p, const Ctx& x) {
             if (x.lane == 0) reinterpret_cast<float*>(x.smem + kSmGamma)[c & 1] = expf(total);
             __syncwarp();
             if (x.lane == 0) x.arrive(kDecFull + (c & 1));
+            if (Local) continue;
             // the sums from here to the end of each 32 tokens (eight lanes)
             float rest = pre[3];
 #pragma unroll
@@ -440,6 +497,7 @@ __device__ __forceinline__ void decay_role(const LinParams& p, const Ctx& x) {
 
 // ---- warp 25, one lane: loads -------------------------------------------------
 // Returns the number of tiles issued.
+template <bool Local>
 __device__ __forceinline__ int load_role(const Maps& maps, const LinParams& p, const Ctx& x) {
     int tile = 0;
     Item item;
@@ -447,7 +505,7 @@ __device__ __forceinline__ int load_role(const Maps& maps, const LinParams& p, c
         for (int j = 0; j < chunks(item.len); ++j) {
             const int t = item.t0 + j * C;
 #pragma unroll
-            for (int m = 0; m < 3; ++m, ++tile) {  // q, v, k: in the order that they come free
+            for (int m = Local ? 1 : 0; m < 3; ++m, ++tile) {  // q, v, k: in the order that they come free
                 if (tile >= kSlots && !x.wait(kEmpty + tile % kSlots, ((tile / kSlots) + 1) & 1)) return tile;
                 const CUtensorMap* map = m == 0 ? &maps.q : m == 1 ? &maps.v : &maps.k;
                 const int h = m == 1 ? item.h : item.h / p.rep;
@@ -465,6 +523,7 @@ __device__ __forceinline__ int load_role(const Maps& maps, const LinParams& p, c
 // ---- warp 24: products ----------------------------------------------------------
 // The warp runs as one (descriptors stay in uniform registers); one elected lane
 // issues.
+template <bool Local>
 __device__ __forceinline__ void mma_role(const Ctx& x) {
     const uint32_t base = smem_u32(x.smem);
     // descriptors of a tile read K-major (16 columns a step) and MN-major (16 rows)
@@ -478,9 +537,10 @@ __device__ __forceinline__ void mma_role(const Ctx& x) {
     Item item;
     for (int it = 0; x.item(it, &item, true); ++it) {
         const int nc = chunks(item.len);
-        for (int j = 0; j < nc; ++j, ++c, tile += 3) {
-            const bool has_s = j > 0 || (item.flags & kInit);
-            const uint32_t qa = smem_u32(x.tile(tile)), va = smem_u32(x.tile(tile + 1)), ka = smem_u32(x.tile(tile + 2));
+        for (int j = 0; j < nc; ++j, ++c, tile += kPerChunk<Local>) {
+            const bool has_s = j > 0 || (item.flags & (kInit | kPlane));
+            const uint32_t qa = smem_u32(x.tile(tile)), va = smem_u32(x.tile(tile + kV<Local>)),
+                           ka = smem_u32(x.tile(tile + kK<Local>));
             const uint64_t k = kdesc(ka), q = kdesc(qa), km = mdesc(ka), vm = mdesc(va);
             auto add_tokens = [&](int n) {  // dS over tokens 32 n .. 32 n + 31
                 tc_fence_after();
@@ -495,10 +555,24 @@ __device__ __forceinline__ void mma_role(const Ctx& x) {
                 }
                 __syncwarp();
             };
-            const int fq = x.full(tile), fk = x.full(tile + 2);
-            const uint32_t pq = x.full_phase(tile), pk = x.full_phase(tile + 2);
+            const int fq = x.full(tile), fk = x.full(tile + kK<Local>);
+            const uint32_t pq = x.full_phase(tile), pk = x.full_phase(tile + kK<Local>);
             if (c == 0 ? !x.wait_all(fk, pk, kWFull, 0) : !x.wait_all(fk, pk, kWFull, 0, kDSEmpty, (c + 1) & 1)) return;
             add_tokens(0);
+            if constexpr (Local) {
+#pragma unroll 1
+                for (int n = 1; n < 4; ++n) {
+                    if (!x.wait_all(kWFull + (n & 1), n >> 1)) return;
+                    add_tokens(n);
+                }
+                if (lead) {
+                    x.arrive(kEmpty + tile % kSlots);  // v, read by the W warps alone
+                    mma_commit(x.bar + kDSFull);
+                    mma_commit(x.bar + kEmpty + (tile + 1) % kSlots);
+                }
+                __syncwarp();
+                continue;
+            }
             // X is free once the previous chunk's P v has read it, and W's second buffer
             // with it: its last product was issued before
             if (c == 0 ? !x.wait_all(fq, pq) : !x.wait_all(fq, pq, kOFull, (c + 1) & 1)) return;
@@ -648,7 +722,7 @@ __device__ __forceinline__ void out_role(const Maps& maps, const LinParams& p, c
     Item item;
     for (int it = 0; x.item(it, &item, true); ++it) {
         for (int j = 0; j < chunks(item.len); ++j, ++c, tile += 3) {
-            const bool has_s = j > 0 || (item.flags & kInit);
+            const bool has_s = j > 0 || (item.flags & (kInit | kPlane));
             if (!x.wait_all(kGFull, c & 1)) return;
             const float f = ex2(reinterpret_cast<const float*>(x.smem + kSmG)[row]);
             __syncwarp();
@@ -755,6 +829,7 @@ __device__ __noinline__ uint32_t clear_nonfinite(uint8_t* vt, int col, int odd) 
 // ---- warps 8-15: weighted v ---------------------------------------------------------
 // A warp makes 32 value rows of two K steps at a time, warps 8-11 of the first and third
 // 32 tokens, warps 12-15 of the others (whose place is q's until X is done).
+template <bool Local>
 __device__ __forceinline__ void weight_role(const LinParams& p, const Ctx& x, int w8) {
     const int w4 = w8 & 3, odd = w8 >> 2;
     const uint32_t tm = x.tmem + ((uint32_t)(32 * w4) << 16) + kTmW + 64 * odd;
@@ -765,15 +840,15 @@ __device__ __forceinline__ void weight_role(const LinParams& p, const Ctx& x, in
     Item item;
     for (int it = 0; x.item(it, &item, true); ++it) {
         const int nc = chunks(item.len);
-        for (int j = 0; j < nc; ++j, ++c, tile += 3) {
+        for (int j = 0; j < nc; ++j, ++c, tile += kPerChunk<Local>) {
             const int live = min(C, item.len - j * C);
-            uint8_t* vt = x.tile(tile + 1);
-            if (!x.wait_all(x.full(tile + 1), x.full_phase(tile + 1))) return;
+            uint8_t* vt = x.tile(tile + kV<Local>);
+            if (!x.wait_all(x.full(tile + kV<Local>), x.full_phase(tile + kV<Local>))) return;
             if (live < C) {
                 // rows past the sequence's end belong to others: they weigh nothing,
                 // and may hold anything, so they are cleared
-                if (!x.wait_all(x.full(tile + 2), x.full_phase(tile + 2))) return;
-                uint8_t* kt = x.tile(tile + 2);
+                if (!x.wait_all(x.full(tile + kK<Local>), x.full_phase(tile + kK<Local>))) return;
+                uint8_t* kt = x.tile(tile + kK<Local>);
 #pragma unroll 1
                 for (int i = 32 * w8 + x.lane; i < (C - live) * 16; i += 256) {
                     const uint32_t at = (i & 8 ? kTile / 2 : 0) + (live + (i >> 4)) * 128 + (i & 7) * 16;
@@ -795,7 +870,7 @@ __device__ __forceinline__ void weight_role(const LinParams& p, const Ctx& x, in
                 const int t0 = 64 * n + 32 * odd;
                 // the buffers' last steps have been read, and for q's place q
                 if ((c > 0 || n > 0) && !x.wait_all(kWEmpty + odd, n ^ 1)) return;
-                if (odd && n == 0 && !x.wait_all(kXFull, c & 1)) return;
+                if (!Local && odd && n == 0 && !x.wait_all(kXFull, c & 1)) return;
                 tc_fence_after();
 #pragma unroll 1
                 for (int s = 0; s < 2; ++s) {  // 16 tokens
@@ -825,7 +900,7 @@ __device__ __forceinline__ void weight_role(const LinParams& p, const Ctx& x, in
                 }
                 tmem_wait_st();
                 tc_fence_before();
-                if (n == 1) {
+                if (!Local && n == 1) {
                     uint32_t cols = 0;
                     if (__any_sync(0xffffffffu, (nan2 & 0x7FFF7FFFu) != 0))
                         cols = clear_nonfinite(vt, 32 * w4 + x.lane, odd);
@@ -867,7 +942,7 @@ __device__ __forceinline__ void store4(__half* s, float4 v) {
     *reinterpret_cast<uint2*>(s) = make_uint2(pack_half2(v.x, v.y), pack_half2(v.z, v.w));
 }
 
-template <class P>
+template <class P, bool Local>
 __device__ __forceinline__ void state_role(const LinParams& p, const Ctx& x, int warp) {
     const int sg = warp >> 2;
     const int row = 32 * (warp & 3) + x.lane;
@@ -909,7 +984,17 @@ __device__ __forceinline__ void state_role(const LinParams& p, const Ctx& x, int
         P* pool = static_cast<P*>(p.pool) +
                   (item.flags & kStore ? (size_t)item.slot * p.stride0 : 0) +
                   ((size_t)item.h * D + 32 * (warp & 3) + half) * D + 64 * sg + 4 * l16;
-        if (item.flags & kInit) {
+        // a segment's state in the workspace: this thread's 4 columns 4 e .. every 256 x 4 values
+        float4* plane = reinterpret_cast<float4*>(p.planes) + (size_t)item.plane * (D * D / 4) + 32 * warp + x.lane;
+        float kept = 1.f;  // Local: what is left of the state after the segment
+        if (!Local && (item.flags & kPlane)) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const float4 v = plane[256 * e];
+                S[2 * e] = pack2(v.x, v.y), S[2 * e + 1] = pack2(v.z, v.w);
+            }
+            write_operand();
+        } else if (!Local && (item.flags & kInit)) {
             // the last q S^T has read the operand: it was issued before the last dS
 #pragma unroll 4
             for (int r = 0; r < 32; r += 2) *staged(r + half, l16) = load4<P>(pool + r * D);
@@ -933,6 +1018,7 @@ __device__ __forceinline__ void state_role(const LinParams& p, const Ctx& x, int
             if (!x.wait_all(kDSFull, c & 1)) return;
             tc_fence_after();
             const f2 g2 = pack2(gamma, gamma);
+            if (Local) kept *= gamma;
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
                 uint32_t r[16];
@@ -948,9 +1034,16 @@ __device__ __forceinline__ void state_role(const LinParams& p, const Ctx& x, int
                     S[8 * b + e / 2] = fma2(g2, S[8 * b + e / 2],
                                              pack2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])));
             }
-            if (j + 1 < nc) write_operand();
+            if (!Local && j + 1 < nc) write_operand();
         }
-        if (item.flags & kStore) {  // the chunk's q S^T, issued before dS, has read the operand
+        if (Local) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const float2 a = unpack2(S[2 * e]), b = unpack2(S[2 * e + 1]);
+                plane[256 * e] = make_float4(a.x, a.y, b.x, b.y);
+            }
+            if (threadIdx.x == 0) p.kept[item.plane] = kept;
+        } else if (item.flags & kStore) {  // the chunk's q S^T, issued before dS, has read the operand
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
                 const float2 a = unpack2(S[2 * e]), b = unpack2(S[2 * e + 1]);
@@ -964,7 +1057,8 @@ __device__ __forceinline__ void state_role(const LinParams& p, const Ctx& x, int
     }
 }
 
-template <class P>
+// Local: the segments' states from zero, nothing else (the q, score and output parts idle).
+template <class P, bool Local>
 __global__ void __launch_bounds__(kThreads, 1) kda_lin_walk(const __grid_constant__ Maps maps, LinParams p) {
     extern __shared__ __align__(1024) uint8_t smem[];
     const int warp = threadIdx.x >> 5;
@@ -983,7 +1077,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_lin_walk(const __grid_constan
             int n = 1;
             if (i == kDecEmpty || i == kDecEmpty + 1) n = 16;
             if (i == kGEmpty) n = 8;
-            if (i >= kItemEmpty && i < kItemEmpty + kItems) n = 26;
+            if (i >= kItemEmpty && i < kItemEmpty + kItems) n = Local ? 18 : 26;
             if (i == kPFull || i == kQSScaled || i == kOEmpty) n = 4;
             if (i == kWFull || i == kWFull + 1) n = 4;
             if (i == kDSEmpty || i == kSFull || i == kCleared) n = 8;
@@ -1007,25 +1101,25 @@ __global__ void __launch_bounds__(kThreads, 1) kda_lin_walk(const __grid_constan
     int issued = 0;
     if (warp < 8) {
         more_registers<112>();
-        state_role<P>(p, x, warp);
+        state_role<P, Local>(p, x, warp);
     } else if (warp < 16) {
         fewer_registers<64>();
-        weight_role(p, x, warp - 8);
+        weight_role<Local>(p, x, warp - 8);
     } else if (warp < 20) {
         fewer_registers<56>();
-        score_role(p, x, warp - 16);
+        if (!Local) score_role(p, x, warp - 16);
     } else if (warp < 24) {
         fewer_registers<56>();
-        out_role(maps, p, x, warp - 20);
+        if (!Local) out_role(maps, p, x, warp - 20);
     } else {
         fewer_registers<40>();
         if (warp == 24) {
-            mma_role(x);
+            mma_role<Local>(x);
             if (elect_one()) mma_commit(x.bar + kDone);  // the lane that issued
         } else if (warp == 25) {
-            if (x.lane == 0) issued = load_role(maps, p, x);
+            if (x.lane == 0) issued = load_role<Local>(maps, p, x);
         } else if (warp == 26) {
-            decay_role(p, x);
+            decay_role<Local>(p, x);
         }
     }
     __syncwarp();
@@ -1045,6 +1139,55 @@ __global__ void __launch_bounds__(kThreads, 1) kda_lin_walk(const __grid_constan
     }
     __syncthreads();
     if (warp == 24) tmem_dealloc(x.tmem, kTmCols);
+}
+
+// From the states that segments make from zero to the states they start from, in place:
+// with S the sequence's initial state, plane s takes S and S becomes kept_s S + (what
+// plane s held).  The first segment's is taken from the pool here, too: the last
+// segment's walk writes the pool, perhaps before the first one's has started.  A thread
+// takes four columns of a row through all segments; its reads run eight segments ahead.
+template <class P>
+__global__ void __launch_bounds__(256) kda_lin_chain(LinParams p) {
+    const int r = blockIdx.y / p.H, h = blockIdx.y % p.H;
+    __shared__ int before[2];  // segments of the sequences before, and of this one
+    if (threadIdx.x < 32) {
+        int sum = 0, own = 0;
+        for (int i = threadIdx.x; i <= r; i += 32) {
+            const int n = p.long_list[i];
+            const int m = (p.cu[n + 1] - p.cu[n] + p.seg_len - 1) / p.seg_len;
+            if (i < r) sum += m; else own = m;
+        }
+        sum = __reduce_add_sync(0xffffffffu, sum);
+        own = __reduce_add_sync(0xffffffffu, own);
+        if (threadIdx.x == 0) before[0] = sum, before[1] = own;
+    }
+    __syncthreads();
+    const int first = before[0], segs = before[1];
+    const int n = p.long_list[r], slot = p.idx[n];
+    const int warp = threadIdx.x >> 5, e = blockIdx.x;  // as the state warps hold it
+    float4 S = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (slot >= 0 && slot < p.num_slots && p.has_init[n])
+        S = load4<P>(static_cast<const P*>(p.pool) + (size_t)slot * p.stride0 +
+                     ((size_t)h * D + 32 * (warp & 3) + (threadIdx.x & 31)) * D + 64 * (warp >> 2) + 4 * e);
+    const size_t step = (size_t)p.H * (D * D / 4);
+    float4* plane = reinterpret_cast<float4*>(p.planes) + ((size_t)first * p.H + h) * (D * D / 4) + 256 * e + threadIdx.x;
+    const float* kept = p.kept + (size_t)first * p.H + h;
+    constexpr int kAhead = 8;
+    for (int s = 0; s < segs; s += kAhead) {
+        float4 v[kAhead];
+        float k[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (s + i < segs - 1) v[i] = plane[(s + i) * step], k[i] = kept[(size_t)(s + i) * p.H];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (s + i < segs) {
+                plane[(s + i) * step] = S;
+                if (s + i < segs - 1)
+                    S = make_float4(fmaf(k[i], S.x, v[i].x), fmaf(k[i], S.y, v[i].y), fmaf(k[i], S.z, v[i].z),
+                                    fmaf(k[i], S.w, v[i].w));
+            }
+    }
 }
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
@@ -1079,17 +1222,78 @@ bool make_map(CUtensorMap* m, const void* base, int64_t T, int H, int64_t st, in
                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <class P>
-cudaError_t launch(const Maps& maps, const LinParams& p, cudaStream_t s) {
-    cudaError_t e = cudaFuncSetAttribute(kda_lin_walk<P>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+template <class P, bool Local>
+cudaError_t launch_one(const Maps& maps, const LinParams& p, int64_t items, cudaStream_t s) {
+    cudaError_t e = cudaFuncSetAttribute(kda_lin_walk<P, Local>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     if (e != cudaSuccess) return e;
-    const int64_t items = (int64_t)p.n_long * p.H;
     const int grid = (int)(items < num_sms() ? items : num_sms());
-    kda_lin_walk<P><<<grid, kThreads, kSmemBytes, s>>>(maps, p);
+    kda_lin_walk<P, Local><<<grid, kThreads, kSmemBytes, s>>>(maps, p);
     return cudaGetLastError();
 }
 
+template <class P>
+cudaError_t launch(const Maps& maps, const LinParams& p, cudaStream_t s) {
+    cudaError_t e = cudaSuccess;
+    if (p.n_cut > 0) {
+        // the segments' states do not depend on the pool's type
+        e = launch_one<float, true>(maps, p, (int64_t)(p.n_seg - p.n_cut) * p.H, s);
+        if (e == cudaSuccess) {
+            kda_lin_chain<P><<<dim3(16, (unsigned)(p.n_cut * p.H)), 256, 0, s>>>(p);
+            e = cudaGetLastError();
+        }
+    }
+    if (e == cudaSuccess) e = launch_one<P, false>(maps, p, (int64_t)(p.n_seg + p.n_long - p.n_cut) * p.H, s);
+    return e;
+}
+
+// How the longest sequences are cut, from the long sequences' lengths (longest first).
+// Uncut, the walk takes as long as its longest sequence or as all chunks shared out,
+// whichever is more.  Cut, a segment's walk has to wait for the states of those before it,
+// which are made first from k and v alone, in about half of a walk's time; a few chunks'
+// time goes into the two more launches and the states' way through memory.  The segments
+// are as long as lets one wave of CTAs take all items, or, where there are more sequences
+// than that, as an even share of the chunks.
+struct Cut {
+    int seg_len = 0, n_cut = 0, n_seg = 0;
+};
+Cut cut_rule(const int32_t* lens, int n, int H, int sms) {
+    auto chunks_of = [](int len) { return (len + C - 1) / C; };
+    Cut cut;
+    if (n <= 0) return cut;
+    int64_t total = 0;
+    for (int i = 0; i < n; ++i) total += chunks_of(lens[i]);
+    const int longest = chunks_of(lens[0]);
+    const int64_t share = (total * H + sms - 1) / sms;
+    int seg = (int)(share < longest ? share : longest);
+    auto items = [&](int L) {
+        int64_t m = 0;
+        for (int i = 0; i < n; ++i) m += (chunks_of(lens[i]) + L - 1) / L;
+        return m * H;
+    };
+    if ((int64_t)n * H <= sms) {  // the shortest segments that fit
+        int hi = longest;
+        while (seg < hi) {
+            const int mid = seg + (hi - seg) / 2;
+            if (items(mid) <= sms) hi = mid; else seg = mid + 1;
+        }
+    }
+    if (seg < 2) seg = 2;
+    if (longest <= seg + (seg + 1) / 2 + 4) return cut;
+    cut.seg_len = seg * C;
+    for (; cut.n_cut < n && chunks_of(lens[cut.n_cut]) > seg; ++cut.n_cut)
+        cut.n_seg += (chunks_of(lens[cut.n_cut]) + seg - 1) / seg;
+    if ((int64_t)cut.n_seg * H > kLinPlanes) return Cut();
+    return cut;
+}
+
 }  // namespace
+
+void lin_cut(LinParams& p, const int32_t* long_lens) {
+    const Cut c = cut_rule(long_lens, p.n_long, p.H, num_sms());
+    p.seg_len = c.seg_len;
+    p.n_cut = c.n_cut;
+    p.n_seg = c.n_seg;
+}
 
 cudaError_t launch_lin_walk(const LinParams& p, cudaStream_t s) {
     if (p.n_long <= 0) return cudaSuccess;

@@ -19,8 +19,7 @@ struct SeqTables {
     const int32_t* long_list;   // sequences of more than kShortMax tokens, longest first
     const int32_t* short_list;  // the others
     int n_long, n_short;
-    int64_t long_tokens;        // tokens of the long sequences
-    int max_long;               // tokens of the longest one
+    const int32_t* long_lens;   // host: their lengths, longest first
 };
 // Looks the bounds up (reading them back once without cu_host), calls
 // enqueue(arg, tables) with the cache locked and marks the tables' use.
@@ -41,8 +40,10 @@ struct LinParams {
     const int32_t* cu;
     const int32_t *long_list, *short_list;
     int n_long, n_short;
-    int64_t long_tokens;
-    int max_long;
+    // the first n_cut long sequences are cut into n_seg segments of seg_len tokens
+    int n_cut, n_seg, seg_len;
+    float* planes;  // [kLinPlanes][128 x 128] states of the segments
+    float* kept;    // [kLinPlanes] decays over them
     int* status;
     void* pool;
     int64_t stride0;  // elements between slots
@@ -55,6 +56,10 @@ struct LinParams {
 // Values below kMinDecay give exp() == 0 in fp32; the clamp keeps sums of them finite.
 constexpr float kMinDecay = -104.f;
 
+// Segment states a call's workspace holds: a cut needs at most two for each SM.
+constexpr int kLinPlanes = 2 * 152;
+// Chooses n_cut, n_seg and seg_len.
+void lin_cut(LinParams& p, const int32_t* long_lens);
 // Long sequences chunk by chunk (kda_lin_walk.cu); short ones token by token.
 cudaError_t launch_lin_walk(const LinParams& p, cudaStream_t s);
 cudaError_t launch_lin_step(const LinParams& p, const int32_t* list, int n, cudaStream_t s);

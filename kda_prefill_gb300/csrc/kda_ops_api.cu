@@ -73,8 +73,7 @@ int enqueue_lin(void* arg, const kda::SeqTables& t) {
     p.short_list = t.short_list;
     p.n_long = t.n_long;
     p.n_short = t.n_short;
-    p.long_tokens = t.long_tokens;
-    p.max_long = t.max_long;
+    kda::lin_cut(p, t.long_lens);
     cudaError_t e = cudaMemsetAsync(p.status, 0, kda::kWsClearBytes, c.stream);
     if (e != cudaSuccess) return cuda_error(e, "cudaMemsetAsync (status)");
     e = kda::launch_lin_walk(p, c.stream);
@@ -88,7 +87,9 @@ extern "C" {
 
 size_t kda_lin_attn_workspace_size(int64_t total_tokens, int32_t num_seqs, int32_t num_heads) {
     if (total_tokens < 0 || num_seqs <= 0 || num_heads <= 0) return 0;
-    return kda::kWsHeader;
+    // no sequence is cut below seven chunks
+    if (total_tokens <= 6 * 128) return kda::kWsHeader;
+    return kda::kWsHeader + (size_t)kda::kLinPlanes * (kda::kD * kda::kD + 64) * sizeof(float);
 }
 
 int kda_lin_attn_fwd(const void* q, int64_t q_stride_t, int64_t q_stride_h, const void* k,
@@ -192,6 +193,8 @@ int kda_lin_attn_fwd(const void* q, int64_t q_stride_t, int64_t q_stride_h, cons
     p.scale = scale;
     p.H = H, p.rep = H / Hk, p.N = N, p.T = T;
     p.status = static_cast<int*>(workspace);
+    p.kept = reinterpret_cast<float*>(static_cast<char*>(workspace) + kda::kWsHeader);
+    p.planes = p.kept + 64 * kda::kLinPlanes;
     p.pool = state_cache;
     p.stride0 = state_stride0;
     p.idx = state_indices;

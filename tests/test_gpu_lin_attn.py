@@ -125,6 +125,24 @@ def test_several_segments_of_one_prompt():
     run_and_check(make([2500], 1, decay="token", seed=6, init=[1]))
 
 
+@pytest.mark.parametrize("lengths,H", [([1025], 2), ([3000], 1), ([4096, 40], 3), ([2500, 1400, 1300, 20, 0, 900], 4),
+                                       ([6000] + [130] * 30, 6), ([2048] * 40, 4)])
+@pytest.mark.parametrize("decay", ["head", "token"])
+def test_cut_sequences(lengths, H, decay):
+    """Long sequences that are walked in segments, alone and beside others."""
+    run_and_check(make(lengths, H, 1, decay=decay, seed=len(lengths), fused=True,
+                       init=[i % 2 == 0 for i in range(len(lengths))]))
+
+
+def test_cut_sequences_extreme_decays():
+    gen = torch.Generator().manual_seed(3)
+    g = -0.01 * torch.rand(1, 3333, 2, generator=gen)
+    g[0, 700, 0] = -float("inf")
+    g[0, 1500:1800, 1] = -50.0
+    g[0, 3000, 1] = -float("inf")
+    run_and_check(make([3333], 2, g=g, seed=4, init=[1]))
+
+
 def test_decode_batch():
     run_and_check(make([1] * 200, 4, 2, seed=7, pool=torch.bfloat16, init=[1] * 200))
 
