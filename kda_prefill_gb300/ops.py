@@ -35,25 +35,45 @@ def _rows(x: torch.Tensor, name: str, dtype=None):
     """(T, H, D, token stride, head stride) of a [1, T, H, D] or [T, H, D] CUDA view,
     dense in its last dimension."""
     shape, stride = x.shape, x.stride()
-    if len(shape) == 4:
-        if shape[0] != 1:
-            raise ValueError(f"{name}: packed input must have batch dim 1")
-        shape, stride = shape[1:], stride[1:]
-    if len(shape) != 3:
+    if len(shape) == 4 and shape[0] == 1:
+        _, T, H, D = shape
+        _, st, sh, s1 = stride
+    elif len(shape) == 3:
+        T, H, D = shape
+        st, sh, s1 = stride
+    elif len(shape) == 4:
+        raise ValueError(f"{name}: packed input must have batch dim 1")
+    else:
         raise ValueError(f"{name} must be [1, T, H, D] or [T, H, D], got {tuple(x.shape)}")
     if dtype is not None and x.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {x.dtype}")
     if not x.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    T, H, D = shape
-    if D > 1 and stride[2] != 1:
+    if s1 != 1 and D > 1:
         raise ValueError(f"{name} must be dense in its last dimension")
     # the stride of a dimension of one entry says nothing
-    return T, H, D, stride[0] if T > 1 else H * D, stride[1] if H > 1 else D
+    return T, H, D, st if T > 1 else H * D, sh if H > 1 else D
+
+
+# The current stream's handle by device index, without a Stream object around it.
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream(stream, device):
-    return (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _current_stream is not None and device.index is not None:
+        return _current_stream(device.index)
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _host_int32(cu_seqlens_cpu, N: int):
+    """_host_bounds, without its conversions where nothing has to be converted."""
+    h = cu_seqlens_cpu
+    if (isinstance(h, torch.Tensor) and h.dtype is torch.int32 and h.numel() == N + 1
+            and h.is_contiguous() and h.device.type == "cpu"):
+        return h
+    return _host_bounds(h, N)
 
 
 def lin_attn_workspace_size(total_tokens: int, num_seqs: int, num_heads: int) -> int:
@@ -74,6 +94,68 @@ def lin_attn_fwd(q, k, v, log_decay, cu_seqlens, *, state_cache, state_indices,
     pool arguments are those of ``chunk_fwd``.  Writes ``out`` and the selected
     pool slots in place and returns ``out``."""
     lib = load_library()
+    bf16, dev = torch.bfloat16, q.device
+    at = q.get_device()
+    qs, vs, ps, gs = q.shape, v.shape, state_cache.shape, log_decay.shape
+    N = cu_seqlens.numel() - 1
+    hs = has_initial_state
+    # One look at the usual forms; _lin_args looks at each argument, takes the others and
+    # says what is wrong.
+    if (len(qs) == len(vs) == 4 and qs[0] == vs[0] == 1 and qs[3] == vs[3] == 128
+            and qs[1] == vs[1] and k.shape == qs and qs[2] > 0 and vs[2] % qs[2] == 0
+            and q.dtype is k.dtype is v.dtype is out.dtype is bf16
+            and q.is_cuda and k.is_cuda and v.is_cuda and out.is_cuda
+            and k.get_device() == v.get_device() == out.get_device() == at
+            and out.shape == vs and out.is_contiguous()
+            and log_decay.dtype is torch.float32 and log_decay.is_cuda
+            and log_decay.get_device() == at and log_decay.is_contiguous()
+            and (gs == vs[2:3] or gs == vs[:3])
+            and cu_seqlens.dtype is state_indices.dtype is torch.int32
+            and cu_seqlens.is_cuda and cu_seqlens.get_device() == at and cu_seqlens.dim() == 1
+            and N >= 0 and cu_seqlens.is_contiguous()
+            and state_indices.is_cuda and state_indices.get_device() == at
+            and state_indices.numel() == N and state_indices.is_contiguous()
+            and (hs.dtype is torch.bool or hs.dtype is torch.uint8) and hs.is_cuda
+            and hs.get_device() == at and hs.numel() == N and hs.is_contiguous()
+            and state_cache.dtype in STATE_DTYPES and state_cache.is_cuda
+            and state_cache.get_device() == at and len(ps) == 4 and ps[1] == vs[2]
+            and ps[2] == ps[3] == 128 and state_cache.stride()[1:] == (16384, 128, 1)
+            and q.stride(3) == k.stride(3) == v.stride(3) == 1):
+        T, Hk, H = qs[1], qs[2], vs[2]
+        strides = []
+        for x, heads in ((q, Hk), (k, Hk), (v, H)):
+            st = x.stride()
+            strides += (st[1] if T > 1 else heads * 128, st[2] if heads > 1 else 128)
+        q_st, q_sh, k_st, k_sh, v_st, v_sh = strides
+    else:
+        T, Hk, H, N, (q_st, q_sh, k_st, k_sh, v_st, v_sh) = _lin_args(
+            q, k, v, log_decay, cu_seqlens, state_cache, state_indices, hs, out)
+    host = None if cu_seqlens_cpu is None else _host_int32(cu_seqlens_cpu, N)
+    need = lib.kda_lin_attn_workspace_size(T, N, H)
+    if workspace is None:
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+        given = need
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    else:
+        given = workspace.numel() * workspace.element_size()
+        if given < need:
+            raise ValueError(f"workspace too small: {need} bytes needed")
+    rc = lib.kda_lin_attn_fwd(
+        q.data_ptr(), q_st, q_sh, k.data_ptr(), k_st, k_sh, v.data_ptr(), v_st, v_sh,
+        log_decay.data_ptr(), len(gs) > 1, cu_seqlens.data_ptr(),
+        None if host is None else host.data_ptr(), N, T, H, Hk,
+        state_cache.data_ptr(), state_cache.stride(0), ps[0],
+        state_indices.data_ptr(), hs.data_ptr(), out.data_ptr(),
+        0.08838834764831845 if scale is None else float(scale), STATE_DTYPES[state_cache.dtype],
+        workspace.data_ptr(), given, _stream(stream, dev))
+    if rc != KDA_OK:
+        _check(rc, lib)
+    return out
+
+
+def _lin_args(q, k, v, log_decay, cu_seqlens, state_cache, state_indices, hs, out):
+    """(T, Hqk, H, N, strides of q, k and v), every argument checked for itself."""
     bf16 = torch.bfloat16
     T, Hk, D, q_st, q_sh = _rows(q, "q", bf16)
     Tk, Hk2, Dk, k_st, k_sh = _rows(k, "k", bf16)
@@ -84,7 +166,6 @@ def lin_attn_fwd(q, k, v, log_decay, cu_seqlens, *, state_cache, state_indices,
         raise ValueError(f"{H} heads of v are not a multiple of {Hk} heads of q and k")
     if log_decay.dtype != torch.float32 or not log_decay.is_cuda:
         raise TypeError("log_decay must be a float32 CUDA tensor")
-    per_token = log_decay.dim() > 1
     if not log_decay.is_contiguous() or tuple(log_decay.shape) not in ((H,), (T, H), (1, T, H)):
         raise ValueError(f"log_decay must be a contiguous [H] or [1, T, H] tensor; got shape "
                          f"{tuple(log_decay.shape)}")
@@ -97,41 +178,21 @@ def lin_attn_fwd(q, k, v, log_decay, cu_seqlens, *, state_cache, state_indices,
         raise TypeError("out must be a bfloat16 CUDA tensor")
     if tuple(out.shape) != tuple(v.shape) or not out.is_contiguous():
         raise ValueError("out must be contiguous and have the shape of v")
-    if state_cache.dtype not in STATE_DTYPES:
-        raise TypeError(f"state_cache dtype {state_cache.dtype} not supported")
+    if state_cache.dtype not in STATE_DTYPES or not state_cache.is_cuda:
+        raise TypeError(f"state_cache dtype {state_cache.dtype} on {state_cache.device} not supported")
     if state_cache.dim() != 4 or tuple(state_cache.shape[1:]) != (H, 128, 128):
         raise ValueError("state_cache must be [slots, H, 128, 128]")
     if tuple(state_cache.stride()[1:]) != (128 * 128, 128, 1):
         raise ValueError("each slot plane of state_cache must be dense (only stride(0) may pad)")
     if state_indices.dtype != torch.int32 or not state_indices.is_cuda:
         raise TypeError("state_indices must be an int32 CUDA tensor")
-    hs = has_initial_state
     if hs.dtype not in (torch.bool, torch.uint8) or not hs.is_cuda:
         raise TypeError("has_initial_state must be a bool/uint8 CUDA tensor")
     _per_sequence(state_indices, "state_indices", N)
     _per_sequence(hs, "has_initial_state", N)
-    dev = q.device
-    _same_device(dev, k=k, v=v, log_decay=log_decay, cu_seqlens=cu_seqlens, out=out,
+    _same_device(q.device, k=k, v=v, log_decay=log_decay, cu_seqlens=cu_seqlens, out=out,
                  state_cache=state_cache, state_indices=state_indices, has_initial_state=hs)
-    host = _host_bounds(cu_seqlens_cpu, N)
-    need = lib.kda_lin_attn_workspace_size(T, N, H)
-    if workspace is None:
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
-    elif workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
-    elif workspace.numel() * workspace.element_size() < need:
-        raise ValueError(f"workspace too small: {need} bytes needed")
-    rc = lib.kda_lin_attn_fwd(
-        q.data_ptr(), q_st, q_sh, k.data_ptr(), k_st, k_sh, v.data_ptr(), v_st, v_sh,
-        log_decay.data_ptr(), 1 if per_token else 0,
-        cu_seqlens.data_ptr(), None if host is None else host.data_ptr(), N, T, H, Hk,
-        state_cache.data_ptr(), state_cache.stride(0), state_cache.shape[0],
-        state_indices.data_ptr(), hs.data_ptr(), out.data_ptr(),
-        128 ** -0.5 if scale is None else float(scale), STATE_DTYPES[state_cache.dtype],
-        workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream, dev))
-    if rc != KDA_OK:
-        _check(rc, lib)
-    return out
+    return T, Hk, H, N, (q_st, q_sh, k_st, k_sh, v_st, v_sh)
 
 
 def rope_frequencies(rot_dim: int, base: float = 10000.0, *, scaling: Optional[str] = None,
@@ -206,10 +267,10 @@ def rope(q, k, positions, inv_freq, *, layout: str = "half", factor: float = 1.0
         if x is None:
             continue
         Tx, H, Dx, st, sh = _rows(x, name, q.dtype)
-        To, Ho, Do, ost, osh = _rows(y, name + "_out", q.dtype)
-        if (Tx, Dx) != (T, D) or (To, Ho, Do) != (Tx, H, Dx):
+        To, Ho, Do, ost, osh = (Tx, H, Dx, st, sh) if y is x else _rows(y, name + "_out", q.dtype)
+        if Tx != T or Dx != D or To != Tx or Ho != H or Do != Dx:
             raise ValueError(f"{name} and {name}_out must be [1, T, H, D] with q's T and D")
-        arr[n] = _RopeTensor(x.data_ptr(), y.data_ptr(), st, sh, ost, osh, H)
+        arr[n] = (x.data_ptr(), y.data_ptr(), st, sh, ost, osh, H)
         n += 1
     if positions.dtype not in (torch.int32, torch.int64) or not positions.is_cuda:
         raise TypeError("positions must be an int32 or int64 CUDA tensor")
@@ -219,8 +280,10 @@ def rope(q, k, positions, inv_freq, *, layout: str = "half", factor: float = 1.0
         raise TypeError("inv_freq must be a float64 CUDA tensor")
     if inv_freq.dim() != 1 or not inv_freq.is_contiguous() or 2 * inv_freq.numel() > D:
         raise ValueError("inv_freq must be a contiguous 1-D tensor of at most D / 2 frequencies")
-    dev = q.device
-    _same_device(dev, k=k, q_out=q_out, k_out=k_out, positions=positions, inv_freq=inv_freq)
+    dev, at = q.device, q.get_device()
+    if not (q_out.get_device() == positions.get_device() == inv_freq.get_device() == at
+            and (k is None or k.get_device() == k_out.get_device() == at)):
+        _same_device(dev, k=k, q_out=q_out, k_out=k_out, positions=positions, inv_freq=inv_freq)
     rc = lib.kda_rope(arr, n, positions.data_ptr(), positions.element_size(),
                       inv_freq.data_ptr(), T, D, 2 * inv_freq.numel(), _LAYOUTS[layout],
                       float(factor), 1 if inverse else 0, _DTYPES[q.dtype], _stream(stream, dev))
@@ -257,7 +320,10 @@ def gated_norm(x, weight=None, *, gate=None, activation: str = "sigmoid", eps: f
             raise TypeError("weight must be a float32 CUDA tensor")
         if weight.dim() != 1 or weight.numel() != D or not weight.is_contiguous():
             raise ValueError(f"weight must be a contiguous 1-D tensor of {D} values")
-    _same_device(x.device, gate=gate, weight=weight, out=out)
+    at = x.get_device()
+    if not (out.get_device() == at and (gate is None or gate.get_device() == at)
+            and (weight is None or weight.get_device() == at)):
+        _same_device(x.device, gate=gate, weight=weight, out=out)
     rc = lib.kda_gated_norm(
         x.data_ptr(), x_st, x_sh, None if gate is None else gate.data_ptr(), g_st, g_sh,
         None if weight is None else weight.data_ptr(), out.data_ptr(), o_st, o_sh, T, H, D,
