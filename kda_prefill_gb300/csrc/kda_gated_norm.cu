@@ -2,37 +2,37 @@
 //
 //     y = x / sqrt(mean(x^2) + eps) * weight * act(gate)
 //
-// Bound by reading x and the gate and writing y once.  A group of lanes takes a
-// row.  Rows of at most one 16-byte vector a lane stay in registers between the
-// sum of squares and the product; longer ones are read again, from the caches.
+// Bound by reading x and the gate and writing y once.  A group of lanes takes a row.
+// Rows of at most one 16-byte piece a lane stay in registers between the sum of squares
+// and the product, and where there are enough of them a group has two in flight, with
+// their gates.  Longer rows are read again, from the caches.
 
 #include "kda_ops.h"
+#include "kda_rows.cuh"
 
 namespace kda {
 namespace {
 
 constexpr int kThreads = 256;
+enum Gate { kNoGate, kPlain, kSigmoid, kSilu };
 
-__device__ __forceinline__ float to_f(float x) { return x; }
-__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
-template <class E> __device__ __forceinline__ E from_f(float x);
-template <> __device__ __forceinline__ float from_f<float>(float x) { return x; }
-template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) {
-    return __float2bfloat16_rn(x);
+// 1 / (1 + e^-z).  For fp32 rows to fp32's last bits; 16-bit rows take exp and the
+// quotient from the special function unit (within 2^-21 for |z| < 16, then rounded to
+// 2^-11 or 2^-8): otherwise they are bound by instructions (36 a value instead of 11).
+template <class E>
+__device__ __forceinline__ float sigmoid(float z) {
+    if (sizeof(E) == 4) return 1.f / (1.f + expf(-z));
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    return r;
 }
-template <> __device__ __forceinline__ __half from_f<__half>(float x) { return __float2half_rn(x); }
-
-template <class E, int VE>
-struct alignas(sizeof(E) * VE) Vec {
-    E e[VE];
-};
-
-__device__ __forceinline__ float gate_of(float z, int act) {
-    if (act == KDA_ACT_NONE) return z;
-    const float s = 1.f / (1.f + expf(-z));
-    // z s for z at -inf is 0, its limit
-    return act == KDA_ACT_SIGMOID ? s : (s > 0.f ? z * s : (z < 0.f ? 0.f : z));
+template <class E, int GATE>
+__device__ __forceinline__ float gate_of(float z) {
+    if (GATE == kPlain) return z;
+    const float s = sigmoid<E>(z);
+    if (GATE == kSigmoid) return s;
+    return s > 0.f ? z * s : (z < 0.f ? 0.f : z);  // z s at z = -inf is 0, its limit
 }
 
 template <int LANES>
@@ -42,75 +42,139 @@ __device__ __forceinline__ float group_sum(float x) {
     return x;
 }
 
-// LANES lanes a row, `steps` vectors of VE elements a lane.
-template <class E, int VE, int LANES>
-__global__ void __launch_bounds__(kThreads) kda_gated_norm(NormParams p, int64_t rows) {
-    const int lane = threadIdx.x % LANES;
-    const int64_t step = (int64_t)gridDim.x * (kThreads / LANES);
-    // the same number of rounds for all lanes: the sums are taken by whole warps
-    for (int64_t base = (int64_t)blockIdx.x * (kThreads / LANES); base < rows; base += step) {
-        const int64_t row = base + threadIdx.x / LANES;
-        const bool live = row < rows;
-        const int64_t t = live ? row / p.H : 0;
-        const int h = live ? (int)(row - t * p.H) : 0;
-        const E* x = static_cast<const E*>(p.x) + t * p.x_st + (int64_t)h * p.x_sh;
-        const E* g = static_cast<const E*>(p.gate) + (p.gate ? t * p.g_st + (int64_t)h * p.g_sh : 0);
-        E* y = static_cast<E*>(p.out) + t * p.o_st + (int64_t)h * p.o_sh;
-        const int end = live ? p.D : 0;
-        Vec<E, VE> first{};
-        float sum = 0.f;
-        for (int c = lane * VE; c < end; c += LANES * VE) {
-            const Vec<E, VE> a = *reinterpret_cast<const Vec<E, VE>*>(x + c);
-            if (c == lane * VE) first = a;
+// Rows of at most one piece a lane, ROWS of them at a time.
+template <class E, int VE, int LANES, int ROWS, int GATE>
+__global__ void __launch_bounds__(kThreads, ROWS == 1 ? 6 : 4) kda_gated_norm_short(NormParams p, int64_t rows) {
+    const int c = (threadIdx.x % LANES) * VE;
+    const bool in_row = c < p.D;
+    constexpr int kGroups = kThreads / LANES;
+    const int64_t first = (int64_t)blockIdx.x * (kGroups * ROWS) + threadIdx.x / LANES;
+    rows::Piece<E, VE> x[ROWS] = {}, z[ROWS] = {};
+    E* out[ROWS];
 #pragma unroll
-            for (int j = 0; j < VE; ++j) sum = fmaf(to_f(a.e[j]), to_f(a.e[j]), sum);
+    for (int i = 0; i < ROWS; ++i) {
+        const int64_t row = first + i * kGroups;
+        out[i] = nullptr;
+        if (row < rows && in_row) {
+            const int64_t t = row / p.H;
+            const int64_t h = row - t * p.H;
+            x[i] = rows::load<E, VE>(static_cast<const E*>(p.x) + t * p.x_st + h * p.x_sh + c);
+            if (GATE != kNoGate) z[i] = rows::load<E, VE>(static_cast<const E*>(p.gate) + t * p.g_st + h * p.g_sh + c);
+            out[i] = static_cast<E*>(p.out) + t * p.o_st + h * p.o_sh + c;
         }
+    }
+    float w[VE];
+#pragma unroll
+    for (int j = 0; j < VE; ++j) w[j] = p.weight && in_row ? p.weight[c + j] : 1.f;
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        float f[VE];
+        x[i].get(f);
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < VE; ++j) sum = fmaf(f[j], f[j], sum);
         sum = group_sum<LANES>(sum);
         const float inv = 1.f / sqrtf(sum / (float)p.D + p.eps);
-        for (int c = lane * VE; c < end; c += LANES * VE) {
-            const Vec<E, VE> a = c == lane * VE ? first : *reinterpret_cast<const Vec<E, VE>*>(x + c);
-            Vec<E, VE> z{}, b;
-            if (p.gate) z = *reinterpret_cast<const Vec<E, VE>*>(g + c);
+#pragma unroll
+        for (int j = 0; j < VE; ++j) f[j] *= inv * w[j];
+        if (GATE != kNoGate) {
+            float g[VE];
+            z[i].get(g);
+#pragma unroll
+            for (int j = 0; j < VE; ++j) f[j] *= gate_of<E, GATE>(g[j]);
+        }
+        x[i].set(f);
+        if (out[i]) rows::store<E, VE>(out[i], x[i]);
+    }
+}
+
+// Longer rows, and rows that are not whole pieces: a warp each.
+template <class E, int VE, int GATE>
+__global__ void __launch_bounds__(kThreads) kda_gated_norm(NormParams p, int64_t rows) {
+    const int lane = threadIdx.x % 32;
+    const int64_t step = (int64_t)gridDim.x * (kThreads / 32);
+    for (int64_t row = (int64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32; row < rows; row += step) {
+        const int64_t t = row / p.H;
+        const int64_t h = row - t * p.H;
+        const E* x = static_cast<const E*>(p.x) + t * p.x_st + h * p.x_sh;
+        const E* g = static_cast<const E*>(p.gate) + (GATE != kNoGate ? t * p.g_st + h * p.g_sh : 0);
+        E* y = static_cast<E*>(p.out) + t * p.o_st + h * p.o_sh;
+        float sum = 0.f;
+        for (int c = lane * VE; c < p.D; c += 32 * VE) {
+            float f[VE];
+            rows::load<E, VE>(x + c).get(f);
+#pragma unroll
+            for (int j = 0; j < VE; ++j) sum = fmaf(f[j], f[j], sum);
+        }
+        sum = group_sum<32>(sum);
+        const float inv = 1.f / sqrtf(sum / (float)p.D + p.eps);
+        for (int c = lane * VE; c < p.D; c += 32 * VE) {
+            float f[VE], z[VE];
+            rows::load<E, VE>(x + c).get(f);
+            if (GATE != kNoGate) rows::load<E, VE>(g + c).get(z);
 #pragma unroll
             for (int j = 0; j < VE; ++j) {
-                float r = to_f(a.e[j]) * inv;
-                if (p.weight) r *= p.weight[c + j];
-                if (p.gate) r *= gate_of(to_f(z.e[j]), p.act);
-                b.e[j] = from_f<E>(r);
+                f[j] *= inv * (p.weight ? p.weight[c + j] : 1.f);
+                if (GATE != kNoGate) f[j] *= gate_of<E, GATE>(z[j]);
             }
-            *reinterpret_cast<Vec<E, VE>*>(y + c) = b;
+            rows::Piece<E, VE> b;
+            b.set(f);
+            rows::store<E, VE>(y + c, b);
         }
     }
 }
 
-template <class E, int VE, int LANES>
-cudaError_t launch(const NormParams& p, cudaStream_t s) {
+template <class E, int VE, int LANES, int GATE>
+cudaError_t launch_short(const NormParams& p, cudaStream_t s) {
     const int64_t rows = p.T * p.H;
-    const int64_t per_cta = kThreads / LANES;
-    const int64_t grid = (rows + per_cta - 1) / per_cta;
-    kda_gated_norm<E, VE, LANES><<<(unsigned)(grid < INT32_MAX ? grid : INT32_MAX), kThreads, 0, s>>>(p, rows);
+    constexpr int kGroups = kThreads / LANES;
+    // two rows a group where that still gives each SM eight CTAs
+    if (rows >= (int64_t)16 * kGroups * num_sms())
+        kda_gated_norm_short<E, VE, LANES, 2, GATE>
+            <<<(unsigned)((rows + 2 * kGroups - 1) / (2 * kGroups)), kThreads, 0, s>>>(p, rows);
+    else
+        kda_gated_norm_short<E, VE, LANES, 1, GATE>
+            <<<(unsigned)((rows + kGroups - 1) / kGroups), kThreads, 0, s>>>(p, rows);
     return cudaGetLastError();
 }
 
-template <class E>
+template <class E, int VE, int GATE>
+cudaError_t launch_long(const NormParams& p, cudaStream_t s) {
+    const int64_t rows = p.T * p.H;
+    const int64_t grid = (rows + kThreads / 32 - 1) / (kThreads / 32);
+    kda_gated_norm<E, VE, GATE><<<(unsigned)(grid < INT32_MAX ? grid : INT32_MAX), kThreads, 0, s>>>(p, rows);
+    return cudaGetLastError();
+}
+
+template <class E, int GATE>
 cudaError_t dispatch(const NormParams& p, cudaStream_t s) {
     constexpr int VE = 16 / sizeof(E);
-    // 16-byte vectors when the row length, strides and bases allow them
+    // 16-byte pieces when the row length, strides and bases allow them
     const uintptr_t bases = reinterpret_cast<uintptr_t>(p.x) | reinterpret_cast<uintptr_t>(p.out) |
                             reinterpret_cast<uintptr_t>(p.gate);
     const int64_t strides = p.x_st | p.x_sh | p.o_st | p.o_sh | (p.gate ? p.g_st | p.g_sh : 0);
-    if (p.D % VE != 0 || (bases & 15) != 0 || strides % VE != 0) return launch<E, 1, 32>(p, s);
-    if (p.D <= 8 * VE) return launch<E, VE, 8>(p, s);
-    if (p.D <= 16 * VE) return launch<E, VE, 16>(p, s);
-    return launch<E, VE, 32>(p, s);
+    if (p.D % VE != 0 || (bases & 15) != 0 || strides % VE != 0) return launch_long<E, 1, GATE>(p, s);
+    // (a CTA of the short forms takes at least 4 KB of rows: the grid stays within 2^31)
+    if (p.D <= 8 * VE) return launch_short<E, VE, 8, GATE>(p, s);
+    if (p.D <= 16 * VE) return launch_short<E, VE, 16, GATE>(p, s);
+    if (p.D <= 32 * VE) return launch_short<E, VE, 32, GATE>(p, s);
+    return launch_long<E, VE, GATE>(p, s);
+}
+
+template <class E>
+cudaError_t by_gate(const NormParams& p, cudaStream_t s) {
+    if (!p.gate) return dispatch<E, kNoGate>(p, s);
+    if (p.act == KDA_ACT_SIGMOID) return dispatch<E, kSigmoid>(p, s);
+    if (p.act == KDA_ACT_SILU) return dispatch<E, kSilu>(p, s);
+    return dispatch<E, kPlain>(p, s);
 }
 
 }  // namespace
 
 cudaError_t launch_gated_norm(const NormParams& p, cudaStream_t s) {
-    if (p.dtype == KDA_F32) return dispatch<float>(p, s);
-    if (p.dtype == KDA_BF16) return dispatch<__nv_bfloat16>(p, s);
-    return dispatch<__half>(p, s);
+    if (p.dtype == KDA_F32) return by_gate<float>(p, s);
+    if (p.dtype == KDA_BF16) return by_gate<__nv_bfloat16>(p, s);
+    return by_gate<__half>(p, s);
 }
 
 }  // namespace kda

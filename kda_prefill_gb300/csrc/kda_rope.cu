@@ -6,12 +6,14 @@
 // product (two's complement wraps as turns do), and its top 32 bits give the
 // argument of sincospi.  A fp32 product p f would be off by p 2^-25 radians.
 //
-// Bound by reading and writing the heads once.  A CTA takes a few tokens,
-// writes their (c, s) to shared memory, then its threads walk the tokens' units:
-// 16 bytes of a head and their partners (half layout: the 16 bytes rot / 2
-// further), or 16 bytes to copy.
+// Bound by reading and writing the heads once.  A token's heads are cut into units of
+// 16 bytes and their partners (half layout: the 16 bytes rot / 2 further), or of 16
+// bytes to copy.  A CTA takes a few tokens; a thread keeps its unit of its head and goes
+// through the tokens, so that addresses only advance, four of them in flight, the
+// first four read before the tokens' (c, s) are made.
 
 #include "kda_ops.h"
+#include "kda_rows.cuh"
 
 namespace kda {
 namespace {
@@ -19,81 +21,112 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMaxTable = 2048;  // pairs times tokens a CTA holds (16 KB)
 
-__device__ __forceinline__ float to_f(float x) { return x; }
-__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
-template <class E> __device__ __forceinline__ E from_f(float x);
-template <> __device__ __forceinline__ float from_f<float>(float x) { return x; }
-template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) {
-    return __float2bfloat16_rn(x);
-}
-template <> __device__ __forceinline__ __half from_f<__half>(float x) { return __float2half_rn(x); }
+// One unit of a row: 16 bytes, and for pairs of the half layout (and for the narrow
+// form's pairs) the partner's.
+template <class E, int VE, bool IL>
+struct Unit {
+    rows::Piece<E, VE> a, b;
+    static constexpr bool kPaired = !IL || VE == 1;
 
-template <class E, int VE>
-struct alignas(sizeof(E) * VE) Vec {
-    E e[VE];
+    // Offsets of the two in a row; units from rot_units on are copied.
+    static __device__ __forceinline__ int one(const RopeParams& p, int u, int rot_units) {
+        if (u >= rot_units) return p.rot + (u - rot_units) * VE;
+        return IL && VE == 1 ? 2 * u : u * VE;
+    }
+    static __device__ __forceinline__ int two(const RopeParams& p, int u) {
+        return IL ? 2 * u + 1 : (p.rot >> 1) + u * VE;
+    }
+    __device__ __forceinline__ void load(const E* in, int at, int at2, bool turned) {
+        a = rows::load<E, VE>(in + at);
+        if (kPaired && turned) b = rows::load<E, VE>(in + at2);
+    }
+    __device__ __forceinline__ void turn(const float2* cs) {
+        float f[VE], g[VE];
+        a.get(f);
+        if constexpr (kPaired) {
+            b.get(g);
+#pragma unroll
+            for (int j = 0; j < VE; ++j) {
+                const float2 w = cs[j];
+                const float x1 = f[j], x2 = g[j];
+                f[j] = x1 * w.x - x2 * w.y;
+                g[j] = x2 * w.x + x1 * w.y;
+            }
+            b.set(g);
+        } else {
+#pragma unroll
+            for (int j = 0; j < VE; j += 2) {
+                const float2 w = cs[j / 2];
+                const float x1 = f[j], x2 = f[j + 1];
+                f[j] = x1 * w.x - x2 * w.y;
+                f[j + 1] = x2 * w.x + x1 * w.y;
+            }
+        }
+        a.set(f);
+    }
+    __device__ __forceinline__ void store(E* out, int at, int at2, bool turned) const {
+        rows::store<E, VE>(out + at, a);
+        if (kPaired && turned) rows::store<E, VE>(out + at2, b);
+    }
 };
 
-// Units of one head's row: `rot_units` of them turn, the others copy.
+// `units` units a row, the first rot_units of them turned.
 template <class E, int VE, bool IL>
-__global__ void __launch_bounds__(kThreads) kda_rope(RopeParams p, int tokens, int rot_units,
-                                                     int units) {
+__global__ void __launch_bounds__(kThreads, 4) kda_rope(RopeParams p, int tokens, int rot_units, int units) {
     __shared__ float2 table[kMaxTable];
+    constexpr int kAhead = 4;
     const int half = p.rot >> 1;
     const int64_t t0 = (int64_t)blockIdx.x * tokens;
     const int nt = (int)min((int64_t)tokens, p.T - t0);
-    for (int i = threadIdx.x; i < nt * half; i += kThreads) {
-        const int t = i / half, j = i - t * half;
-        const int64_t pos = p.pos64 ? static_cast<const int64_t*>(p.pos)[t0 + t]
-                                    : (int64_t) static_cast<const int32_t*>(p.pos)[t0 + t];
-        const double turns = p.inv_freq[j] * 0.15915494309189533577;  // 1 / 2 pi
-        const long long F = __double2ll_rn((turns - rint(turns)) * 18446744073709551616.0);
-        const unsigned long long phase = (unsigned long long)pos * (unsigned long long)F;
-        const float a = (float)(int)(phase >> 32) * 4.656612873077392578125e-10f;  // 2^-31
-        float s, c;
-        sincospif(a, &s, &c);
-        table[i] = make_float2(c * p.factor, s * p.factor * p.sign);
-    }
-    __syncthreads();
-    const int h0 = p.x[0].heads, heads = h0 + p.x[1].heads;
-    const int per_token = heads * units;
-    for (int i = threadIdx.x; i < nt * per_token; i += kThreads) {
-        const int t = i / per_token, r = i - t * per_token;
-        int h = r / units;
-        const int u = r - h * units;
-        const RopeTensor& x = p.x[h >= h0];
+    const int h0 = p.x[0].heads, items = (h0 + p.x[1].heads) * units;
+    bool made = false;
+    for (int item = threadIdx.x; item < items || !made; item += kThreads) {
+        const bool live = item < items;
+        int h = live ? item / units : 0;
+        const int u = live ? item - h * units : 0;
+        const RopeTensor& r = p.x[h >= h0];
         if (h >= h0) h -= h0;
-        const E* in = static_cast<const E*>(x.in) + (t0 + t) * x.in_st + (int64_t)h * x.in_sh;
-        E* out = static_cast<E*>(x.out) + (t0 + t) * x.out_st + (int64_t)h * x.out_sh;
-        const float2* cs = table + t * half;
-        if (u >= rot_units) {
-            if (in != out) {
-                const int at = p.rot + (u - rot_units) * VE;
-                *reinterpret_cast<Vec<E, VE>*>(out + at) = *reinterpret_cast<const Vec<E, VE>*>(in + at);
-            }
-        } else if (IL && VE > 1) {
-            Vec<E, VE> a = *reinterpret_cast<const Vec<E, VE>*>(in + u * VE);
+        const bool turned = u < rot_units;
+        const int at = Unit<E, VE, IL>::one(p, u, rot_units), at2 = Unit<E, VE, IL>::two(p, u);
+        const int64_t in_st = r.in_st, out_st = r.out_st;
+        const E* in = static_cast<const E*>(r.in) + t0 * in_st + (int64_t)h * r.in_sh;
+        E* out = static_cast<E*>(r.out) + t0 * out_st + (int64_t)h * r.out_sh;
+        const bool write = turned || in != out;
+        Unit<E, VE, IL> x[kAhead];
+        const int n = live ? nt : 0;
 #pragma unroll
-            for (int j = 0; j + 1 < VE; j += 2) {
-                const float2 w = cs[u * (VE / 2) + j / 2];
-                const float x1 = to_f(a.e[j]), x2 = to_f(a.e[j + 1]);
-                a.e[j] = from_f<E>(x1 * w.x - x2 * w.y);
-                a.e[j + 1] = from_f<E>(x2 * w.x + x1 * w.y);
+        for (int i = 0; i < kAhead; ++i)
+            if (i < n) x[i].load(in + i * in_st, at, at2, turned);
+        if (!made) {
+            for (int i = threadIdx.x; i < nt * half; i += kThreads) {
+                const int t = i / half, j = i - t * half;
+                const int64_t pos = p.pos64 ? static_cast<const int64_t*>(p.pos)[t0 + t]
+                                            : (int64_t) static_cast<const int32_t*>(p.pos)[t0 + t];
+                const double turns = p.inv_freq[j] * 0.15915494309189533577;  // 1 / 2 pi
+                const long long F = __double2ll_rn((turns - rint(turns)) * 18446744073709551616.0);
+                const unsigned long long phase = (unsigned long long)pos * (unsigned long long)F;
+                const float a = (float)(int)(phase >> 32) * 4.656612873077392578125e-10f;  // 2^-31
+                float s, c;
+                sincospif(a, &s, &c);
+                table[i] = make_float2(c * p.factor, s * p.factor * p.sign);
             }
-            *reinterpret_cast<Vec<E, VE>*>(out + u * VE) = a;
-        } else {
-            const int one = IL ? 2 * u : u * VE, two = IL ? 2 * u + 1 : half + u * VE;
-            Vec<E, VE> a = *reinterpret_cast<const Vec<E, VE>*>(in + one);
-            Vec<E, VE> b = *reinterpret_cast<const Vec<E, VE>*>(in + two);
+            __syncthreads();
+            made = true;
+        }
+        const float2* cs = table + (Unit<E, VE, IL>::kPaired ? u * VE : u * VE / 2);
+        for (int t = 0; t < n; t += kAhead) {
 #pragma unroll
-            for (int j = 0; j < VE; ++j) {
-                const float2 w = cs[u * VE + j];
-                const float x1 = to_f(a.e[j]), x2 = to_f(b.e[j]);
-                a.e[j] = from_f<E>(x1 * w.x - x2 * w.y);
-                b.e[j] = from_f<E>(x2 * w.x + x1 * w.y);
-            }
-            *reinterpret_cast<Vec<E, VE>*>(out + one) = a;
-            *reinterpret_cast<Vec<E, VE>*>(out + two) = b;
+            for (int i = 0; i < kAhead; ++i)
+                if (t + i < n) {
+                    if (turned) x[i].turn(cs + i * half);
+                    if (write) x[i].store(out + i * out_st, at, at2, turned);
+                }
+            cs += kAhead * half;
+            in += kAhead * in_st;
+            out += kAhead * out_st;
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i)
+                if (t + kAhead + i < n) x[i].load(in + i * in_st, at, at2, turned);
         }
     }
 }
@@ -103,12 +136,10 @@ cudaError_t launch(const RopeParams& p, cudaStream_t s) {
     const int half = p.rot / 2;
     const int rot_units = IL && VE > 1 ? p.rot / VE : half / VE;
     const int units = rot_units + (p.D - p.rot) / VE;
-    const int heads = p.x[0].heads + p.x[1].heads;
-    // tokens per CTA: about eight units for each thread, at most what the table holds
-    int tokens = kThreads * 8 / max(1, heads * units);
-    tokens = max(1, min(tokens, kMaxTable / max(1, half)));
-    // and at least four CTAs for each SM, where there are so many tokens
-    tokens = (int)max((int64_t)1, min((int64_t)tokens, p.T / (4 * num_sms())));
+    // tokens per CTA: eight, at most what the table holds, and few enough that each SM
+    // has eight CTAs where there are so many tokens
+    int tokens = max(1, min(8, kMaxTable / max(1, half)));
+    tokens = (int)max((int64_t)1, min((int64_t)tokens, p.T / (8 * num_sms())));
     const int64_t grid = (p.T + tokens - 1) / tokens;
     kda_rope<E, VE, IL><<<(unsigned)grid, kThreads, 0, s>>>(p, tokens, rot_units, units);
     return cudaGetLastError();

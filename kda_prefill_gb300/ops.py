@@ -11,6 +11,7 @@ describes each call).
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 from typing import Optional
 
@@ -76,7 +77,9 @@ def _host_int32(cu_seqlens_cpu, N: int):
     return _host_bounds(h, N)
 
 
+@functools.lru_cache(maxsize=1024)
 def lin_attn_workspace_size(total_tokens: int, num_seqs: int, num_heads: int) -> int:
+    """Bytes of workspace a ``lin_attn_fwd`` call with these sizes needs."""
     return int(load_library().kda_lin_attn_workspace_size(total_tokens, num_seqs, num_heads))
 
 
@@ -131,7 +134,7 @@ def lin_attn_fwd(q, k, v, log_decay, cu_seqlens, *, state_cache, state_indices,
         T, Hk, H, N, (q_st, q_sh, k_st, k_sh, v_st, v_sh) = _lin_args(
             q, k, v, log_decay, cu_seqlens, state_cache, state_indices, hs, out)
     host = None if cu_seqlens_cpu is None else _host_int32(cu_seqlens_cpu, N)
-    need = lib.kda_lin_attn_workspace_size(T, N, H)
+    need = lin_attn_workspace_size(T, N, H)
     if workspace is None:
         workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
         given = need
