@@ -13,7 +13,7 @@
 namespace kda {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 enum Gate { kNoGate, kPlain, kSigmoid, kSilu };
 
 // 1 / (1 + e^-z).  For fp32 rows to fp32's last bits; 16-bit rows take exp and the
@@ -44,7 +44,7 @@ __device__ __forceinline__ float group_sum(float x) {
 
 // Rows of at most one piece a lane, ROWS of them at a time.
 template <class E, int VE, int LANES, int ROWS, int GATE>
-__global__ void __launch_bounds__(kThreads, ROWS == 1 ? 6 : 4) kda_gated_norm_short(NormParams p, int64_t rows) {
+__global__ void __launch_bounds__(kThreads, ROWS == 1 ? 12 : 10) kda_gated_norm_short(NormParams p, int64_t rows) {
     const int c = (threadIdx.x % LANES) * VE;
     const bool in_row = c < p.D;
     constexpr int kGroups = kThreads / LANES;
@@ -56,7 +56,7 @@ __global__ void __launch_bounds__(kThreads, ROWS == 1 ? 6 : 4) kda_gated_norm_sh
         const int64_t row = first + i * kGroups;
         out[i] = nullptr;
         if (row < rows && in_row) {
-            const int64_t t = row / p.H;
+            const int64_t t = rows <= INT32_MAX ? (int64_t)((uint32_t)row / (uint32_t)p.H) : row / p.H;
             const int64_t h = row - t * p.H;
             x[i] = rows::load<E, VE>(static_cast<const E*>(p.x) + t * p.x_st + h * p.x_sh + c);
             if (GATE != kNoGate) z[i] = rows::load<E, VE>(static_cast<const E*>(p.gate) + t * p.g_st + h * p.g_sh + c);
@@ -128,8 +128,8 @@ template <class E, int VE, int LANES, int GATE>
 cudaError_t launch_short(const NormParams& p, cudaStream_t s) {
     const int64_t rows = p.T * p.H;
     constexpr int kGroups = kThreads / LANES;
-    // two rows a group where that still gives each SM eight CTAs
-    if (rows >= (int64_t)16 * kGroups * num_sms())
+    // two rows a group where that still gives each SM sixteen CTAs
+    if (rows >= (int64_t)32 * kGroups * num_sms())
         kda_gated_norm_short<E, VE, LANES, 2, GATE>
             <<<(unsigned)((rows + 2 * kGroups - 1) / (2 * kGroups)), kThreads, 0, s>>>(p, rows);
     else
@@ -154,7 +154,7 @@ cudaError_t dispatch(const NormParams& p, cudaStream_t s) {
                             reinterpret_cast<uintptr_t>(p.gate);
     const int64_t strides = p.x_st | p.x_sh | p.o_st | p.o_sh | (p.gate ? p.g_st | p.g_sh : 0);
     if (p.D % VE != 0 || (bases & 15) != 0 || strides % VE != 0) return launch_long<E, 1, GATE>(p, s);
-    // (a CTA of the short forms takes at least 4 KB of rows: the grid stays within 2^31)
+    // (a CTA of the short forms takes at least a KB of rows: the grid stays within 2^31)
     if (p.D <= 8 * VE) return launch_short<E, VE, 8, GATE>(p, s);
     if (p.D <= 16 * VE) return launch_short<E, VE, 16, GATE>(p, s);
     if (p.D <= 32 * VE) return launch_short<E, VE, 32, GATE>(p, s);

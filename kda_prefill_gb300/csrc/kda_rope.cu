@@ -18,7 +18,7 @@
 namespace kda {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kMaxThreads = 512;
 constexpr int kMaxTable = 2048;  // pairs times tokens a CTA holds (16 KB)
 
 // One unit of a row: 16 bytes, and for pairs of the half layout (and for the narrow
@@ -72,7 +72,7 @@ struct Unit {
 
 // `units` units a row, the first rot_units of them turned.
 template <class E, int VE, bool IL>
-__global__ void __launch_bounds__(kThreads, 4) kda_rope(RopeParams p, int tokens, int rot_units, int units) {
+__global__ void __maxnreg__(56) kda_rope(RopeParams p, int tokens, int rot_units, int units) {
     __shared__ float2 table[kMaxTable];
     constexpr int kAhead = 4;
     const int half = p.rot >> 1;
@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(kThreads, 4) kda_rope(RopeParams p, int tokens
     const int nt = (int)min((int64_t)tokens, p.T - t0);
     const int h0 = p.x[0].heads, items = (h0 + p.x[1].heads) * units;
     bool made = false;
-    for (int item = threadIdx.x; item < items || !made; item += kThreads) {
+    for (int item = threadIdx.x; item < items || !made; item += blockDim.x) {
         const bool live = item < items;
         int h = live ? item / units : 0;
         const int u = live ? item - h * units : 0;
@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(kThreads, 4) kda_rope(RopeParams p, int tokens
         for (int i = 0; i < kAhead; ++i)
             if (i < n) x[i].load(in + i * in_st, at, at2, turned);
         if (!made) {
-            for (int i = threadIdx.x; i < nt * half; i += kThreads) {
+            for (int i = threadIdx.x; i < nt * half; i += blockDim.x) {
                 const int t = i / half, j = i - t * half;
                 const int64_t pos = p.pos64 ? static_cast<const int64_t*>(p.pos)[t0 + t]
                                             : (int64_t) static_cast<const int32_t*>(p.pos)[t0 + t];
@@ -141,7 +141,11 @@ cudaError_t launch(const RopeParams& p, cudaStream_t s) {
     int tokens = max(1, min(8, kMaxTable / max(1, half)));
     tokens = (int)max((int64_t)1, min((int64_t)tokens, p.T / (8 * num_sms())));
     const int64_t grid = (p.T + tokens - 1) / tokens;
-    kda_rope<E, VE, IL><<<(unsigned)grid, kThreads, 0, s>>>(p, tokens, rot_units, units);
+    // threads: as many as a token's units in the fewest rounds, in whole warps
+    const int items = (p.x[0].heads + p.x[1].heads) * units;
+    const int rounds = (items + kMaxThreads - 1) / kMaxThreads;
+    const int threads = max(128, ((items + rounds - 1) / rounds + 31) / 32 * 32);
+    kda_rope<E, VE, IL><<<(unsigned)grid, threads, 0, s>>>(p, tokens, rot_units, units);
     return cudaGetLastError();
 }
 
