@@ -91,7 +91,8 @@ struct MetaLayout {
     int64_t n_chunks = 0;
     int32_t n_long = 0, n_short = 0;
     int32_t max_long_chunks = 0;  // chunks of the longest sequence the chunked kernels take
-    std::vector<int32_t> long_lens;  // lengths of the sequences the chunked kernels take, longest first
+    // the sequences the chunked kernels take and their lengths, longest first
+    std::vector<int32_t> long_seqs, long_lens;
     size_t off_cu = 0, off_seq_off = 0, off_chunk_seq = 0, off_chunk_tok = 0;  // int32 units
     size_t off_long = 0, off_short = 0;
     size_t words = 0;
@@ -109,11 +110,14 @@ MetaLayout meta_layout(const int32_t* cu, int32_t N) {
             ++L.n_short;
         } else {
             ++L.n_long;
-            L.long_lens.push_back((int32_t)len);
+            L.long_seqs.push_back(n);
         }
         L.max_long_chunks = std::max<int32_t>(L.max_long_chunks, (int32_t)routed_chunks(len));
     }
-    std::sort(L.long_lens.begin(), L.long_lens.end(), [](int32_t a, int32_t b) { return a > b; });
+    std::stable_sort(L.long_seqs.begin(), L.long_seqs.end(), [&](int32_t a, int32_t b) {
+        return cu[a + 1] - cu[a] > cu[b + 1] - cu[b];
+    });
+    for (int32_t n : L.long_seqs) L.long_lens.push_back(cu[n + 1] - cu[n]);
     size_t o = 0;
     L.off_cu = o;        o = align4(o + (size_t)N + 1);
     L.off_seq_off = o;   o = align4(o + (size_t)N + 1);
@@ -134,12 +138,12 @@ void meta_fill(const int32_t* cu, int32_t N, const MetaLayout& L, int32_t* buf) 
     int32_t* lng = buf + L.off_long;
     int32_t* sht = buf + L.off_short;
     int64_t j = 0;
-    int32_t nl = 0, ns = 0;
+    int32_t ns = 0;
     for (int32_t n = 0; n < N; ++n) {
         mcu[n] = cu[n];
         off[n] = (int32_t)j;
         const int64_t len = (int64_t)cu[n + 1] - cu[n];
-        if (is_short(len)) sht[ns++] = n; else lng[nl++] = n;
+        if (is_short(len)) sht[ns++] = n;
         const int64_t nc = routed_chunks(len);
         for (int64_t c = 0; c < nc; ++c, ++j) {
             cseq[j] = n;
@@ -150,9 +154,7 @@ void meta_fill(const int32_t* cu, int32_t N, const MetaLayout& L, int32_t* buf) 
     off[N] = (int32_t)j;
     // longest first: the scan launches its walks in this order, so that the long
     // walks start in the first wave and the short ones fill the last
-    std::stable_sort(lng, lng + nl, [&](int32_t a, int32_t b) {
-        return cu[a + 1] - cu[a] > cu[b + 1] - cu[b];
-    });
+    std::copy(L.long_seqs.begin(), L.long_seqs.end(), lng);
 }
 
 // ---------------------------------------------------------------------------
@@ -664,7 +666,8 @@ int with_seq_tables(const int32_t* cu_dev, const int32_t* cu_host, int32_t N, in
     if (rc != KDA_OK) return rc;
     const MetaLayout& L = m->layout;
     SeqTables t{m->dev + L.off_cu, m->dev + L.off_long, m->dev + L.off_short,
-                L.n_long,          L.n_short,           L.long_lens.data()};
+                L.n_long,          L.n_short,           m->key.data() + 3,
+                L.long_seqs.data(), L.long_lens.data()};
     rc = enqueue(arg, t);
     if (rc != KDA_OK) return rc;
     cache().mark_use(m, stream, capturing);

@@ -88,9 +88,9 @@ enum Bar {
     kQSScaled,                  // e^{G_i} applied
     kOFull,                     // the chunk's O complete
     kOEmpty,                    // and read
-    kWFull,                     // [2] two K steps of W written
-    kWEmpty = kWFull + 2,       // [2] and read
-    kDSFull = kWEmpty + 2,      // dS complete
+    kWFull,                     // [4] 32 tokens of W written, by buffer (two; Local: four)
+    kWEmpty = kWFull + 4,       // [4] and read
+    kDSFull = kWEmpty + 4,      // dS complete
     kDSEmpty,                   // and read
     kSFull,                     // S's operand written
     kCleared,                   // rows past a sequence's end cleared
@@ -110,8 +110,12 @@ static_assert(kSmGamma % 8 == 0 && kSmMisc % 8 == 0 && kSmRows % 8 == 0, "words"
 constexpr uint32_t kTmX = 0;    // X; then P: per 32 tokens 16 columns high part, 16 low
 constexpr uint32_t kTmO = 128;
 constexpr uint32_t kTmDS = 256;
-constexpr uint32_t kTmW = 384;  // [2] buffers of 32 tokens of W: two K steps x four parts x 8
-                                // columns; the second is q's place, free once X is done
+// W's buffers of 32 tokens: two K steps x four parts x 8 columns.  The second is q's
+// place, free once X is done; Local has four, X's and O's places being free.
+constexpr uint32_t kTmW = 384;
+__host__ __device__ constexpr uint32_t w_column(bool local, int n) {
+    return local && n >= 2 ? 64 * (n - 2) : kTmW + 64 * (n & 1);
+}
 constexpr uint32_t kTmQ = 448;  // q, for X
 constexpr uint32_t kTmCols = 512;
 
@@ -354,74 +358,60 @@ struct Ctx {
 __device__ __forceinline__ int chunks(int len) { return (len + C - 1) / C; }
 
 // ---- warp 26: items and decays ------------------------------------------------
-// Item i of the call.  The first p.n_cut sequences (the longest) are cut into segments of
-// p.seg_len tokens, whose items come first; Local: their segments but the last.
+// Item i of the call.  The cut sequences' segments come first; Local: all but their last.
 template <bool Local>
-__device__ __forceinline__ Item make_item(const LinParams& p, int i, int lane) {
+__device__ __forceinline__ Item make_item(const LinParams& p, const LinCuts& cuts, int i, int lane) {
     Item item{};
     const int k = i / p.H;
     item.h = i - k * p.H;
-    int r = 0, s = 0, first = 0;  // sequence, segment, segments of the sequences before
     const int n_seg = Local ? p.n_seg - p.n_cut : p.n_seg;
-    if (k < n_seg) {
-        for (;; r += 32) {
-            int segs = 0;
-            if (r + lane < p.n_cut) {
-                const int n = p.long_list[r + lane];
-                segs = (p.cu[n + 1] - p.cu[n] + p.seg_len - 1) / p.seg_len - (Local ? 1 : 0);
-            }
-            int upto = segs;
-#pragma unroll
-            for (int w = 1; w < 32; w <<= 1) {
-                const int u = __shfl_up_sync(0xffffffffu, upto, w);
-                if (lane >= w) upto += u;
-            }
-            upto += first;
-            const uint32_t past = __ballot_sync(0xffffffffu, upto > k);
-            if (past || r + 32 >= p.n_cut) {
-                const int at = past ? __ffs(past) - 1 : 31;
-                first = __shfl_sync(0xffffffffu, upto - segs, at);
-                r += at;
-                break;
-            }
-            first = __shfl_sync(0xffffffffu, upto, 31);
-        }
-        s = k - first;
-        item.plane = ((Local ? first + r : first) + s) * p.H + item.h;
-    } else {
-        r = p.n_cut + k - n_seg;
-    }
-    item.n = p.long_list[r];
-    const int len = p.cu[item.n + 1] - p.cu[item.n];
-    item.t0 = p.cu[item.n];
-    item.len = len;
     bool last = true;
     if (k < n_seg) {
-        item.t0 += s * p.seg_len;
-        item.len = min(p.seg_len, len - s * p.seg_len);
-        last = (s + 1) * p.seg_len >= len;
+        int r = 0;
+        for (;; r += 32) {  // the sequence whose segments k is among
+            const int m = r + lane;
+            const uint32_t past = __ballot_sync(0xffffffffu, m < p.n_cut && cuts.first[m + 1] - (Local ? m + 1 : 0) > k);
+            if (past || r + 32 >= p.n_cut) {
+                r += past ? __ffs(past) - 1 : 0;
+                break;
+            }
+        }
+        const int s = k - (cuts.first[r] - (Local ? r : 0));
+        item.n = cuts.seq[r];
+        item.t0 = cuts.t0[r] + s * p.seg_len;
+        item.len = min(p.seg_len, cuts.len[r] - s * p.seg_len);
+        item.plane = (cuts.first[r] + s) * p.H + item.h;
+        item.flags = kPlane;
+        last = cuts.first[r] + s + 1 == cuts.first[r + 1];
+    } else {
+        item.n = p.long_list[p.n_cut + k - n_seg];
+        item.t0 = p.cu[item.n];
+        item.len = p.cu[item.n + 1] - item.t0;
     }
     if (Local) return item;
     item.slot = p.idx[item.n];
     const bool ok = item.slot >= 0 && item.slot < p.num_slots;
     if (!ok && lane == 0) atomicOr(p.status, 4);
-    item.flags = (ok && last ? kStore : 0) | (k < n_seg ? kPlane : ok && p.has_init[item.n] ? kInit : 0);
+    if (ok && last) item.flags |= kStore;
+    if (ok && k >= n_seg && p.has_init[item.n]) item.flags |= kInit;
     return item;
 }
 
 template <bool Local>
-__device__ __forceinline__ void decay_role(const LinParams& p, const Ctx& x) {
+__device__ __forceinline__ void decay_role(const LinParams& p, const LinCuts& cuts, const Ctx& x) {
     const int n_items = (Local ? p.n_seg - p.n_cut : p.n_seg + p.n_long - p.n_cut) * p.H;
     int* queue = reinterpret_cast<int*>(reinterpret_cast<char*>(p.status) + (Local ? kWsDecodeOff : kWsQueueOff));
     int c = 0;
     for (int it = 0;; ++it) {
         if (it >= kItems && !x.wait_all(kItemEmpty + it % kItems, ((it / kItems) + 1) & 1)) return;
-        int i = 0;
-        if (x.lane == 0) i = atomicAdd(queue, 1);
-        i = __shfl_sync(0xffffffffu, i, 0);
+        int i = blockIdx.x;  // the first item by place, the others in the order of their claims
+        if (it > 0) {
+            if (x.lane == 0) i = gridDim.x + atomicAdd(queue, 1);
+            i = __shfl_sync(0xffffffffu, i, 0);
+        }
         Item item{};
         if (i < n_items)
-            item = make_item<Local>(p, i, x.lane);
+            item = make_item<Local>(p, cuts, i, x.lane);
         else
             item.flags = kEnd;
         if (x.lane == 0) {
@@ -549,20 +539,21 @@ __device__ __forceinline__ void mma_role(const Ctx& x) {
                     for (int s = 0; s < 2; ++s)
 #pragma unroll
                         for (int part = 3; part >= 0; --part)  // the smallest first
-                            mma_f16_ts(x.tmem + kTmDS, x.tmem + kTmW + 64 * (n & 1) + 32 * s + 8 * part,
+                            mma_f16_ts(x.tmem + kTmDS, x.tmem + w_column(Local, n) + 32 * s + 8 * part,
                                        km + mstep(2 * n + s), kIdescKM, n > 0 || s > 0 || part < 3);
-                    mma_commit(x.bar + kWEmpty + (n & 1));
+                    mma_commit(x.bar + kWEmpty + (Local ? n : n & 1));
                 }
                 __syncwarp();
             };
             const int fq = x.full(tile), fk = x.full(tile + kK<Local>);
             const uint32_t pq = x.full_phase(tile), pk = x.full_phase(tile + kK<Local>);
-            if (c == 0 ? !x.wait_all(fk, pk, kWFull, 0) : !x.wait_all(fk, pk, kWFull, 0, kDSEmpty, (c + 1) & 1)) return;
+            const uint32_t w0 = Local ? c & 1 : 0;  // the phase of W's first tokens
+            if (c == 0 ? !x.wait_all(fk, pk, kWFull, w0) : !x.wait_all(fk, pk, kWFull, w0, kDSEmpty, (c + 1) & 1)) return;
             add_tokens(0);
             if constexpr (Local) {
 #pragma unroll 1
                 for (int n = 1; n < 4; ++n) {
-                    if (!x.wait_all(kWFull + (n & 1), n >> 1)) return;
+                    if (!x.wait_all(kWFull + n, c & 1)) return;
                     add_tokens(n);
                 }
                 if (lead) {
@@ -827,12 +818,13 @@ __device__ __noinline__ uint32_t clear_nonfinite(uint8_t* vt, int col, int odd) 
 }
 
 // ---- warps 8-15: weighted v ---------------------------------------------------------
-// A warp makes 32 value rows of two K steps at a time, warps 8-11 of the first and third
-// 32 tokens, warps 12-15 of the others (whose place is q's until X is done).
+// A warp makes 32 value rows of 32 tokens at a time: warps 8-11 of the first and third 32,
+// warps 12-15 of the others (whose place is q's until X is done); Local: each four warps
+// of warps 8-23 of one 32.
 template <bool Local>
 __device__ __forceinline__ void weight_role(const LinParams& p, const Ctx& x, int w8) {
-    const int w4 = w8 & 3, odd = w8 >> 2;
-    const uint32_t tm = x.tmem + ((uint32_t)(32 * w4) << 16) + kTmW + 64 * odd;
+    const int w4 = w8 & 3, group = w8 >> 2;
+    const uint32_t tm = x.tmem + ((uint32_t)(32 * w4) << 16);
     // a lane's place in four 8 x 8 matrices: tokens 0-7 and 8-15, value rows 0-7 and 8-15
     const int tok = (x.lane & 7) + ((x.lane >> 4) << 3);
     const int col = 32 * w4 + (((x.lane >> 3) & 1) << 3);
@@ -844,7 +836,7 @@ __device__ __forceinline__ void weight_role(const LinParams& p, const Ctx& x, in
             const int live = min(C, item.len - j * C);
             uint8_t* vt = x.tile(tile + kV<Local>);
             if (!x.wait_all(x.full(tile + kV<Local>), x.full_phase(tile + kV<Local>))) return;
-            if (live < C) {
+            if (!Local && live < C) {  // (a segment but the last is full)
                 // rows past the sequence's end belong to others: they weigh nothing,
                 // and may hold anything, so they are cleared
                 if (!x.wait_all(x.full(tile + kK<Local>), x.full_phase(tile + kK<Local>))) return;
@@ -866,11 +858,13 @@ __device__ __forceinline__ void weight_role(const LinParams& p, const Ctx& x, in
             const uint32_t vs = smem_u32(vt);
             uint32_t nan2 = 0;  // becomes NaN with any part that is one
 #pragma unroll 1
-            for (int n = 0; n < 2; ++n) {
-                const int t0 = 64 * n + 32 * odd;
+            for (int n = group; n < 4; n += Local ? 4 : 2) {
+                const int b = Local ? n : group, t0 = 32 * n;
+                const uint32_t column = w_column(Local, n);
                 // the buffers' last steps have been read, and for q's place q
-                if ((c > 0 || n > 0) && !x.wait_all(kWEmpty + odd, n ^ 1)) return;
-                if (!Local && odd && n == 0 && !x.wait_all(kXFull, c & 1)) return;
+                if (Local ? c > 0 && !x.wait_all(kWEmpty + b, (c + 1) & 1)
+                          : (c > 0 || n >= 2) && !x.wait_all(kWEmpty + b, n < 2)) return;
+                if (!Local && n == 1 && !x.wait_all(kXFull, c & 1)) return;
                 tc_fence_after();
 #pragma unroll 1
                 for (int s = 0; s < 2; ++s) {  // 16 tokens
@@ -893,21 +887,21 @@ __device__ __forceinline__ void weight_role(const LinParams& p, const Ctx& x, in
                             t[3][e] = fma_bf2(r[e], u[2], fma_bf2(r[e], u[1], neg_bf2(t[2][e])));
                             nan2 = fma_bf2(t[1][e], 0u, nan2);  // an infinite or NaN value leaves a NaN
                         }
-                        const uint32_t at = tm + ((uint32_t)(16 * i) << 16) + 32 * s;
+                        const uint32_t at = tm + ((uint32_t)(16 * i) << 16) + column + 32 * s;
 #pragma unroll
                         for (int u = 0; u < 4; ++u) tmem_st_16x8(at + 8 * u, t[u][0], t[u][1], t[u][2], t[u][3]);
                     }
                 }
                 tmem_wait_st();
                 tc_fence_before();
-                if (!Local && n == 1) {
+                if (!Local && n >= 2) {
                     uint32_t cols = 0;
                     if (__any_sync(0xffffffffu, (nan2 & 0x7FFF7FFFu) != 0))
-                        cols = clear_nonfinite(vt, 32 * w4 + x.lane, odd);
+                        cols = clear_nonfinite(vt, 32 * w4 + x.lane, group);
                     if (x.lane == 0) reinterpret_cast<uint32_t*>(x.smem + kSmBad)[8 * (c & 1) + w8] = cols;
                 }
                 __syncwarp();
-                if (x.lane == 0) x.arrive(kWFull + odd);
+                if (x.lane == 0) x.arrive(kWFull + b);
             }
             if (x.lane == 0) x.arrive(kDecEmpty + (c & 1));
         }
@@ -988,6 +982,7 @@ __device__ __forceinline__ void state_role(const LinParams& p, const Ctx& x, int
         float4* plane = reinterpret_cast<float4*>(p.planes) + (size_t)item.plane * (D * D / 4) + 32 * warp + x.lane;
         float kept = 1.f;  // Local: what is left of the state after the segment
         if (!Local && (item.flags & kPlane)) {
+            grid_dep_wait();  // the chain kernel may still run
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
                 const float4 v = plane[256 * e];
@@ -1059,7 +1054,8 @@ __device__ __forceinline__ void state_role(const LinParams& p, const Ctx& x, int
 
 // Local: the segments' states from zero, nothing else (the q, score and output parts idle).
 template <class P, bool Local>
-__global__ void __launch_bounds__(kThreads, 1) kda_lin_walk(const __grid_constant__ Maps maps, LinParams p) {
+__global__ void __launch_bounds__(kThreads, 1) kda_lin_walk(const __grid_constant__ Maps maps, const __grid_constant__ LinParams p,
+                                                             const __grid_constant__ LinCuts cuts) {
     extern __shared__ __align__(1024) uint8_t smem[];
     const int warp = threadIdx.x >> 5;
     Ctx x;
@@ -1075,11 +1071,11 @@ __global__ void __launch_bounds__(kThreads, 1) kda_lin_walk(const __grid_constan
     if (threadIdx.x == 0) {
         for (int i = 0; i < kNumBars; ++i) {
             int n = 1;
-            if (i == kDecEmpty || i == kDecEmpty + 1) n = 16;
+            if (i == kDecEmpty || i == kDecEmpty + 1) n = Local ? 24 : 16;
             if (i == kGEmpty) n = 8;
-            if (i >= kItemEmpty && i < kItemEmpty + kItems) n = Local ? 18 : 26;
+            if (i >= kItemEmpty && i < kItemEmpty + kItems) n = 26;
             if (i == kPFull || i == kQSScaled || i == kOEmpty) n = 4;
-            if (i == kWFull || i == kWFull + 1) n = 4;
+            if (i >= kWFull && i < kWFull + 4) n = 4;
             if (i == kDSEmpty || i == kSFull || i == kCleared) n = 8;
             mbar_init(x.bar + i, n);
         }
@@ -1097,29 +1093,36 @@ __global__ void __launch_bounds__(kThreads, 1) kda_lin_walk(const __grid_constan
     tc_fence_after();
     x.tmem = *slot;
 
-    // registers: the launch's 896 x 72 = 256 x 112 + 256 x 64 + 256 x 56 + 128 x 40
+    // what follows in the stream may be set up; it waits for this grid where it has to
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    // registers: the launch's 896 x 72 = 256 x 112 + 256 x 64 + 256 x 56 + 128 x 40,
+    // Local: 256 x 112 + 640 x 56
     int issued = 0;
     if (warp < 8) {
         more_registers<112>();
         state_role<P, Local>(p, x, warp);
     } else if (warp < 16) {
-        fewer_registers<64>();
+        fewer_registers<Local ? 56 : 64>();
         weight_role<Local>(p, x, warp - 8);
-    } else if (warp < 20) {
-        fewer_registers<56>();
-        if (!Local) score_role(p, x, warp - 16);
     } else if (warp < 24) {
         fewer_registers<56>();
-        if (!Local) out_role(maps, p, x, warp - 20);
+        if constexpr (Local) {
+            weight_role<Local>(p, x, warp - 8);
+        } else if (warp < 20) {
+            score_role(p, x, warp - 16);
+        } else {
+            out_role(maps, p, x, warp - 20);
+        }
     } else {
-        fewer_registers<40>();
+        fewer_registers<Local ? 56 : 40>();
         if (warp == 24) {
             mma_role<Local>(x);
             if (elect_one()) mma_commit(x.bar + kDone);  // the lane that issued
         } else if (warp == 25) {
             if (x.lane == 0) issued = load_role<Local>(maps, p, x);
         } else if (warp == 26) {
-            decay_role<Local>(p, x);
+            decay_role<Local>(p, cuts, x);
         }
     }
     __syncwarp();
@@ -1145,25 +1148,14 @@ __global__ void __launch_bounds__(kThreads, 1) kda_lin_walk(const __grid_constan
 // with S the sequence's initial state, plane s takes S and S becomes kept_s S + (what
 // plane s held).  The first segment's is taken from the pool here, too: the last
 // segment's walk writes the pool, perhaps before the first one's has started.  A thread
-// takes four columns of a row through all segments; its reads run eight segments ahead.
+// takes four columns of a row through all segments; its reads run sixteen segments ahead.
 template <class P>
-__global__ void __launch_bounds__(256) kda_lin_chain(LinParams p) {
+__global__ void __launch_bounds__(256) kda_lin_chain(const __grid_constant__ LinParams p,
+                                                     const __grid_constant__ LinCuts cuts) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int r = blockIdx.y / p.H, h = blockIdx.y % p.H;
-    __shared__ int before[2];  // segments of the sequences before, and of this one
-    if (threadIdx.x < 32) {
-        int sum = 0, own = 0;
-        for (int i = threadIdx.x; i <= r; i += 32) {
-            const int n = p.long_list[i];
-            const int m = (p.cu[n + 1] - p.cu[n] + p.seg_len - 1) / p.seg_len;
-            if (i < r) sum += m; else own = m;
-        }
-        sum = __reduce_add_sync(0xffffffffu, sum);
-        own = __reduce_add_sync(0xffffffffu, own);
-        if (threadIdx.x == 0) before[0] = sum, before[1] = own;
-    }
-    __syncthreads();
-    const int first = before[0], segs = before[1];
-    const int n = p.long_list[r], slot = p.idx[n];
+    const int first = cuts.first[r], segs = cuts.first[r + 1] - first;
+    const int n = cuts.seq[r], slot = p.idx[n];
     const int warp = threadIdx.x >> 5, e = blockIdx.x;  // as the state warps hold it
     float4 S = make_float4(0.f, 0.f, 0.f, 0.f);
     if (slot >= 0 && slot < p.num_slots && p.has_init[n])
@@ -1172,7 +1164,8 @@ __global__ void __launch_bounds__(256) kda_lin_chain(LinParams p) {
     const size_t step = (size_t)p.H * (D * D / 4);
     float4* plane = reinterpret_cast<float4*>(p.planes) + ((size_t)first * p.H + h) * (D * D / 4) + 256 * e + threadIdx.x;
     const float* kept = p.kept + (size_t)first * p.H + h;
-    constexpr int kAhead = 8;
+    constexpr int kAhead = 16;
+    grid_dep_wait();  // the segments' states are made
     for (int s = 0; s < segs; s += kAhead) {
         float4 v[kAhead];
         float k[kAhead];
@@ -1222,27 +1215,52 @@ bool make_map(CUtensorMap* m, const void* base, int64_t T, int H, int64_t st, in
                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Launches with programmatic stream serialization where `early`: set up while the kernel
+// before still runs, whose results it then waits for.
+template <class... A>
+cudaError_t launch_after(bool early, void (*kernel)(A...), dim3 grid, int threads, size_t smem, cudaStream_t s,
+                         const A&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = early ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 template <class P, bool Local>
-cudaError_t launch_one(const Maps& maps, const LinParams& p, int64_t items, cudaStream_t s) {
-    cudaError_t e = cudaFuncSetAttribute(kda_lin_walk<P, Local>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+cudaError_t launch_one(bool early, const Maps& maps, const LinParams& p, const LinCuts& cuts, int64_t items,
+                       cudaStream_t s) {
+    static bool ready[32] = {};  // per device: the shared memory is allowed
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    if (dev >= 32 || !ready[dev]) {
+        e = cudaFuncSetAttribute(kda_lin_walk<P, Local>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+        if (e != cudaSuccess) return e;
+        if (dev < 32) ready[dev] = true;
+    }
     const int grid = (int)(items < num_sms() ? items : num_sms());
-    kda_lin_walk<P, Local><<<grid, kThreads, kSmemBytes, s>>>(maps, p);
-    return cudaGetLastError();
+    return launch_after(early, kda_lin_walk<P, Local>, dim3(grid), kThreads, kSmemBytes, s, maps, p, cuts);
 }
 
 template <class P>
-cudaError_t launch(const Maps& maps, const LinParams& p, cudaStream_t s) {
+cudaError_t launch(const Maps& maps, const LinParams& p, const LinCuts& cuts, cudaStream_t s) {
     cudaError_t e = cudaSuccess;
-    if (p.n_cut > 0) {
+    const bool cut = p.n_cut > 0;
+    if (cut) {
         // the segments' states do not depend on the pool's type
-        e = launch_one<float, true>(maps, p, (int64_t)(p.n_seg - p.n_cut) * p.H, s);
-        if (e == cudaSuccess) {
-            kda_lin_chain<P><<<dim3(16, (unsigned)(p.n_cut * p.H)), 256, 0, s>>>(p);
-            e = cudaGetLastError();
-        }
+        e = launch_one<float, true>(false, maps, p, cuts, (int64_t)(p.n_seg - p.n_cut) * p.H, s);
+        if (e == cudaSuccess)
+            e = launch_after(true, kda_lin_chain<P>, dim3(16, (unsigned)(p.n_cut * p.H)), 256, 0, s, p, cuts);
     }
-    if (e == cudaSuccess) e = launch_one<P, false>(maps, p, (int64_t)(p.n_seg + p.n_long - p.n_cut) * p.H, s);
+    if (e == cudaSuccess)
+        e = launch_one<P, false>(cut, maps, p, cuts, (int64_t)(p.n_seg + p.n_long - p.n_cut) * p.H, s);
     return e;
 }
 
@@ -1282,20 +1300,27 @@ Cut cut_rule(const int32_t* lens, int n, int H, int sms) {
     cut.seg_len = seg * C;
     for (; cut.n_cut < n && chunks_of(lens[cut.n_cut]) > seg; ++cut.n_cut)
         cut.n_seg += (chunks_of(lens[cut.n_cut]) + seg - 1) / seg;
-    if ((int64_t)cut.n_seg * H > kLinPlanes) return Cut();
+    if (cut.n_cut > kLinCuts || (int64_t)cut.n_seg * H > kLinPlanes) return Cut();
     return cut;
 }
 
 }  // namespace
 
-void lin_cut(LinParams& p, const int32_t* long_lens) {
-    const Cut c = cut_rule(long_lens, p.n_long, p.H, num_sms());
+void lin_cut(LinParams& p, LinCuts& cuts, const SeqTables& t) {
+    const Cut c = cut_rule(t.long_lens, p.n_long, p.H, num_sms());
     p.seg_len = c.seg_len;
     p.n_cut = c.n_cut;
     p.n_seg = c.n_seg;
+    cuts.first[0] = 0;
+    for (int r = 0; r < c.n_cut; ++r) {
+        cuts.seq[r] = t.long_seqs[r];
+        cuts.t0[r] = t.bounds[t.long_seqs[r]];
+        cuts.len[r] = t.long_lens[r];
+        cuts.first[r + 1] = cuts.first[r] + (t.long_lens[r] + c.seg_len - 1) / c.seg_len;
+    }
 }
 
-cudaError_t launch_lin_walk(const LinParams& p, cudaStream_t s) {
+cudaError_t launch_lin_walk(const LinParams& p, const LinCuts& cuts, cudaStream_t s) {
     if (p.n_long <= 0) return cudaSuccess;
     if ((int64_t)p.n_long * p.H > INT32_MAX - 65536) return cudaErrorInvalidValue;
     Maps maps;
@@ -1304,9 +1329,9 @@ cudaError_t launch_lin_walk(const LinParams& p, cudaStream_t s) {
         !make_map(&maps.v, p.v, p.T, p.H, p.v_st, p.v_sh, C) ||
         !make_map(&maps.out, p.out, p.T, p.H, (int64_t)p.H * D, D, 32))
         return cudaErrorInvalidValue;
-    if (p.st_dtype == KDA_STATE_F32) return launch<float>(maps, p, s);
-    if (p.st_dtype == KDA_STATE_BF16) return launch<__nv_bfloat16>(maps, p, s);
-    return launch<__half>(maps, p, s);
+    if (p.st_dtype == KDA_STATE_F32) return launch<float>(maps, p, cuts, s);
+    if (p.st_dtype == KDA_STATE_BF16) return launch<__nv_bfloat16>(maps, p, cuts, s);
+    return launch<__half>(maps, p, cuts, s);
 }
 
 }  // namespace kda

@@ -19,7 +19,10 @@ struct SeqTables {
     const int32_t* long_list;   // sequences of more than kShortMax tokens, longest first
     const int32_t* short_list;  // the others
     int n_long, n_short;
-    const int32_t* long_lens;   // host: their lengths, longest first
+    // host: the bounds, and the long sequences and their lengths in long_list's order
+    const int32_t* bounds;
+    const int32_t* long_seqs;
+    const int32_t* long_lens;
 };
 // Looks the bounds up (reading them back once without cu_host), calls
 // enqueue(arg, tables) with the cache locked and marks the tables' use.
@@ -58,11 +61,18 @@ constexpr float kMinDecay = -104.f;
 
 // Segment states a call's workspace holds: a cut needs at most two for each SM.
 constexpr int kLinPlanes = 2 * 152;
-// Chooses n_cut, n_seg and seg_len.
-void lin_cut(LinParams& p, const int32_t* long_lens);
+// The cut sequences, by value in the kernels' parameters: of sequence seq[r], which has
+// len[r] tokens from t0[r] on, the segments are first[r] .. first[r + 1] - 1.
+constexpr int kLinCuts = kLinPlanes / 2;
+struct LinCuts {
+    int seq[kLinCuts], t0[kLinCuts], len[kLinCuts], first[kLinCuts + 1];
+};
+// Chooses n_cut, n_seg, seg_len and the cuts.
+void lin_cut(LinParams& p, LinCuts& cuts, const SeqTables& t);
 // Long sequences chunk by chunk (kda_lin_walk.cu); short ones token by token.
-cudaError_t launch_lin_walk(const LinParams& p, cudaStream_t s);
-cudaError_t launch_lin_step(const LinParams& p, const int32_t* list, int n, cudaStream_t s);
+cudaError_t launch_lin_walk(const LinParams& p, const LinCuts& cuts, cudaStream_t s);
+// `beside`: right after the walk, beside its last CTAs.
+cudaError_t launch_lin_step(const LinParams& p, bool beside, cudaStream_t s);
 
 struct RopeTensor {
     const void* in;

@@ -73,11 +73,12 @@ int enqueue_lin(void* arg, const kda::SeqTables& t) {
     p.short_list = t.short_list;
     p.n_long = t.n_long;
     p.n_short = t.n_short;
-    kda::lin_cut(p, t.long_lens);
+    kda::LinCuts cuts;
+    kda::lin_cut(p, cuts, t);
     cudaError_t e = cudaMemsetAsync(p.status, 0, kda::kWsClearBytes, c.stream);
     if (e != cudaSuccess) return cuda_error(e, "cudaMemsetAsync (status)");
-    e = kda::launch_lin_walk(p, c.stream);
-    if (e == cudaSuccess) e = kda::launch_lin_step(p, p.short_list, p.n_short, c.stream);
+    e = kda::launch_lin_walk(p, cuts, c.stream);
+    if (e == cudaSuccess) e = kda::launch_lin_step(p, p.n_long > 0, c.stream);
     return e == cudaSuccess ? KDA_OK : cuda_error(e, "kernel launch");
 }
 
