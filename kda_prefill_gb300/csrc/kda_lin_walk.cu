@@ -54,7 +54,12 @@ constexpr int D = kD;
 constexpr int C = 128;
 constexpr int kThreads = 28 * 32;
 constexpr int kTile = C * D * 2;  // bytes of a q, k or v tile
-constexpr int kSlots = 5;         // tiles in flight or in use
+// Tiles in flight or in use: q's, and two of v and of k, used by turns.  A chunk's q is
+// free after q S^T, its v after P v, its k after dS and once the chunk's output rows,
+// which pass through it, have left; so the next v is on its way a chunk ahead and the next
+// q and k half a chunk (with one ring for all, v's loads waited for the rows: 7.4 K cycles
+// a chunk instead of 5.9 K on 16384 tokens x 12 heads).
+constexpr int kSlots = 5;
 constexpr int kItems = 3;         // items the claims run ahead
 
 // Shared memory.  Tiles are two halves of 64 columns, 128-byte swizzled.
@@ -64,9 +69,8 @@ constexpr int kSmW = kSmTile + kSlots * kTile;  // [2][64] e^R of token pairs, e
 constexpr int kSmG = kSmW + 2 * (C / 2) * 12;   // [128] G, prefix sums in log2
 constexpr int kSmCf = kSmG + C * 4;             // [96] e^{G_b - G_j}
 struct Item {
-    int t0, len, h, n, slot, flags;
+    int t0, len, h, n, flags;
     int plane;  // of the workspace: the segment's state
-    int unused;
 };
 constexpr int kSmItem = kSmCf + 96 * 4;
 enum { kInit = 1, kStore = 2, kEnd = 4, kPlane = 8 };
@@ -261,10 +265,12 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 
-// Tiles of a chunk, in the order of their loads: q, v, k; Local: v, k.
-template <bool Local> constexpr int kPerChunk = Local ? 2 : 3;
-template <bool Local> constexpr int kV = Local ? 0 : 1;
-template <bool Local> constexpr int kK = Local ? 1 : 2;
+// Slots of a chunk's tiles, and the phase of their barriers.
+constexpr int kQ = 0;
+__device__ __forceinline__ int v_slot(int c) { return 1 + (c & 1); }
+__device__ __forceinline__ int k_slot(int c) { return 3 + (c & 1); }
+__device__ __forceinline__ uint32_t q_phase(int c) { return c & 1; }
+__device__ __forceinline__ uint32_t vk_phase(int c) { return (c >> 1) & 1; }
 
 struct Maps {
     CUtensorMap q, k, v, out;
@@ -334,10 +340,7 @@ struct Ctx {
     }
 #undef KDA_WAIT_END
     __device__ __forceinline__ void arrive(int b) const { mbar_arrive(bar + b); }
-    __device__ __forceinline__ uint8_t* tile(int i) const { return smem + kSmTile + (i % kSlots) * kTile; }
-    // Barrier and phase of tile i's load.
-    static __device__ __forceinline__ int full(int i) { return kFull + i % kSlots; }
-    static __device__ __forceinline__ uint32_t full_phase(int i) { return (i / kSlots) & 1; }
+    __device__ __forceinline__ uint8_t* tile(int slot) const { return smem + kSmTile + slot * kTile; }
     // Parts of the weights of the token pairs of chunk c.
     __device__ __forceinline__ const uint32_t* weights(int c) const {
         return reinterpret_cast<const uint32_t*>(smem + kSmW) + (c & 1) * 3 * (C / 2);
@@ -389,11 +392,12 @@ __device__ __forceinline__ Item make_item(const LinParams& p, const LinCuts& cut
         item.len = p.cu[item.n + 1] - item.t0;
     }
     if (Local) return item;
-    item.slot = p.idx[item.n];
-    const bool ok = item.slot >= 0 && item.slot < p.num_slots;
-    if (!ok && lane == 0) atomicOr(p.status, 4);
-    if (ok && last) item.flags |= kStore;
-    if (ok && k >= n_seg && p.has_init[item.n]) item.flags |= kInit;
+    if (last) item.flags |= kStore;
+    // a segment's initial state is in the workspace, and the state warps look its slot up
+    if (k >= n_seg) {
+        const int slot = p.idx[item.n];
+        if (p.has_init[item.n] && slot >= 0 && slot < p.num_slots) item.flags |= kInit;
+    }
     return item;
 }
 
@@ -486,28 +490,32 @@ __device__ __forceinline__ void decay_role(const LinParams& p, const LinCuts& cu
 }
 
 // ---- warp 25, one lane: loads -------------------------------------------------
-// Returns the number of tiles issued.
+// Returns the numbers of q, v and k tiles issued.
 template <bool Local>
-__device__ __forceinline__ int load_role(const Maps& maps, const LinParams& p, const Ctx& x) {
-    int tile = 0;
+__device__ __forceinline__ int3 load_role(const Maps& maps, const LinParams& p, const Ctx& x) {
+    int c = 0;
+    auto load = [&](int slot, const CUtensorMap* map, int h, int t) {
+        uint64_t* bar = x.bar + kFull + slot;
+        uint8_t* dst = x.tile(slot);
+        mbar_arrive_expect_tx(bar, kTile);
+        tma_load_3d(dst, map, bar, 0, h, t);
+        tma_load_3d(dst + kTile / 2, map, bar, 64, h, t);
+    };
     Item item;
     for (int it = 0; x.item(it, &item, false); ++it) {
-        for (int j = 0; j < chunks(item.len); ++j) {
+        for (int j = 0; j < chunks(item.len); ++j, ++c) {
             const int t = item.t0 + j * C;
-#pragma unroll
-            for (int m = Local ? 1 : 0; m < 3; ++m, ++tile) {  // q, v, k: in the order that they come free
-                if (tile >= kSlots && !x.wait(kEmpty + tile % kSlots, ((tile / kSlots) + 1) & 1)) return tile;
-                const CUtensorMap* map = m == 0 ? &maps.q : m == 1 ? &maps.v : &maps.k;
-                const int h = m == 1 ? item.h : item.h / p.rep;
-                uint64_t* bar = x.bar + kFull + tile % kSlots;
-                uint8_t* dst = x.tile(tile);
-                mbar_arrive_expect_tx(bar, kTile);
-                tma_load_3d(dst, map, bar, 0, h, t);
-                tma_load_3d(dst + kTile / 2, map, bar, 64, h, t);
+            if (c >= 2 && !x.wait(kEmpty + v_slot(c), vk_phase(c) ^ 1)) return make_int3(c, c, c);
+            load(v_slot(c), &maps.v, item.h, t);
+            if constexpr (!Local) {
+                if (c >= 1 && !x.wait(kEmpty + kQ, q_phase(c) ^ 1)) return make_int3(c, c + 1, c);
+                load(kQ, &maps.q, item.h / p.rep, t);
             }
+            if (c >= 2 && !x.wait(kEmpty + k_slot(c), vk_phase(c) ^ 1)) return make_int3(c + 1, c + 1, c);
+            load(k_slot(c), &maps.k, item.h / p.rep, t);
         }
     }
-    return tile;
+    return make_int3(c, c, c);
 }
 
 // ---- warp 24: products ----------------------------------------------------------
@@ -523,14 +531,14 @@ __device__ __forceinline__ void mma_role(const Ctx& x) {
     constexpr auto mstep = [](int ks) { return (uint64_t)((ks * 2048) >> 4); };
     const uint64_t s_hi = kdesc(base + kSmS), s_lo = kdesc(base + kSmS + kTile);
     const bool lead = elect_one();
-    int tile = 0, c = 0, with_s = 0;
+    int c = 0, with_s = 0;
     Item item;
     for (int it = 0; x.item(it, &item, true); ++it) {
         const int nc = chunks(item.len);
-        for (int j = 0; j < nc; ++j, ++c, tile += kPerChunk<Local>) {
+        for (int j = 0; j < nc; ++j, ++c) {
             const bool has_s = j > 0 || (item.flags & (kInit | kPlane));
-            const uint32_t qa = smem_u32(x.tile(tile)), va = smem_u32(x.tile(tile + kV<Local>)),
-                           ka = smem_u32(x.tile(tile + kK<Local>));
+            const uint32_t qa = smem_u32(x.tile(kQ)), va = smem_u32(x.tile(v_slot(c))),
+                           ka = smem_u32(x.tile(k_slot(c)));
             const uint64_t k = kdesc(ka), q = kdesc(qa), km = mdesc(ka), vm = mdesc(va);
             auto add_tokens = [&](int n) {  // dS over tokens 32 n .. 32 n + 31
                 tc_fence_after();
@@ -545,8 +553,8 @@ __device__ __forceinline__ void mma_role(const Ctx& x) {
                 }
                 __syncwarp();
             };
-            const int fq = x.full(tile), fk = x.full(tile + kK<Local>);
-            const uint32_t pq = x.full_phase(tile), pk = x.full_phase(tile + kK<Local>);
+            const int fq = kFull + kQ, fk = kFull + k_slot(c);
+            const uint32_t pq = q_phase(c), pk = vk_phase(c);
             const uint32_t w0 = Local ? c & 1 : 0;  // the phase of W's first tokens
             if (c == 0 ? !x.wait_all(fk, pk, kWFull, w0) : !x.wait_all(fk, pk, kWFull, w0, kDSEmpty, (c + 1) & 1)) return;
             add_tokens(0);
@@ -557,9 +565,9 @@ __device__ __forceinline__ void mma_role(const Ctx& x) {
                     add_tokens(n);
                 }
                 if (lead) {
-                    x.arrive(kEmpty + tile % kSlots);  // v, read by the W warps alone
+                    x.arrive(kEmpty + v_slot(c));  // read by the W warps alone
                     mma_commit(x.bar + kDSFull);
-                    mma_commit(x.bar + kEmpty + (tile + 1) % kSlots);
+                    mma_commit(x.bar + kEmpty + k_slot(c));
                 }
                 __syncwarp();
                 continue;
@@ -576,7 +584,7 @@ __device__ __forceinline__ void mma_role(const Ctx& x) {
                 for (int ks = 0; ks < 8; ++ks)
                     mma_f16_ts(x.tmem + kTmX, x.tmem + kTmQ + 8 * ks, k + kstep(ks), kIdescKK, ks > 0);
                 mma_commit(x.bar + kXFull);
-                if (!has_s) mma_commit(x.bar + kEmpty + tile % kSlots);
+                if (!has_s) mma_commit(x.bar + kEmpty + kQ);
             }
             __syncwarp();
             // O is free once the previous chunk's rows have been read
@@ -588,7 +596,7 @@ __device__ __forceinline__ void mma_role(const Ctx& x) {
                     for (int ks = 0; ks < 16; ++ks)  // the low part first
                         mma_f16_ss(x.tmem + kTmO, q + kstep(ks & 7), (ks < 8 ? s_lo : s_hi) + kstep(ks & 7), kIdescKK, ks > 0);
                     mma_commit(x.bar + kQSFull);
-                    mma_commit(x.bar + kEmpty + tile % kSlots);
+                    mma_commit(x.bar + kEmpty + kQ);
                 }
                 __syncwarp();
             }
@@ -603,16 +611,14 @@ __device__ __forceinline__ void mma_role(const Ctx& x) {
             add_tokens(3);
             if (lead) {
                 mma_commit(x.bar + kDSFull);
-                mma_commit(x.bar + kEmpty + (tile + 2) % kSlots);
-            }
-            if (lead) {
 #pragma unroll 1
                 for (int ks = 0; ks < 8; ++ks)
 #pragma unroll
                     for (int part = 1; part >= 0; --part)
                         mma_f16_ts(x.tmem + kTmO, x.tmem + kTmX + 32 * (ks >> 1) + 16 * part + 8 * (ks & 1),
                                    vm + mstep(ks), kIdescKM, has_s || ks > 0 || part == 0);
-                mma_commit(x.bar + kOFull);  // v's tile takes the output rows now
+                mma_commit(x.bar + kOFull);  // k's tile takes the output rows now
+                mma_commit(x.bar + kEmpty + v_slot(c));
             }
             __syncwarp();
             with_s += has_s;
@@ -709,10 +715,10 @@ __device__ __forceinline__ void out_role(const Maps& maps, const LinParams& p, c
     const int row = 32 * w + x.lane;
     const uint32_t tm = x.tmem + ((uint32_t)(32 * w) << 16) + kTmO;
     const f2 scale = pack2(p.scale, p.scale);
-    int tile = 0, c = 0, with_s = 0;
+    int c = 0, with_s = 0;
     Item item;
     for (int it = 0; x.item(it, &item, true); ++it) {
-        for (int j = 0; j < chunks(item.len); ++j, ++c, tile += 3) {
+        for (int j = 0; j < chunks(item.len); ++j, ++c) {
             const bool has_s = j > 0 || (item.flags & (kInit | kPlane));
             if (!x.wait_all(kGFull, c & 1)) return;
             const float f = ex2(reinterpret_cast<const float*>(x.smem + kSmG)[row]);
@@ -742,10 +748,10 @@ __device__ __forceinline__ void out_role(const Maps& maps, const LinParams& p, c
             }
             if (!x.wait_all(kOFull, c & 1)) return;
             tc_fence_after();
-            // The rows go through v's tile, which has been read, so that whole rows
+            // The rows go through k's tile, which has been read, so that whole rows
             // are written to memory: lanes that each store a row of their own fill
             // the load/store unit with single sectors and hold up everything else.
-            uint8_t* vt = x.tile(tile + 1);
+            uint8_t* kt = x.tile(k_slot(c));
             const uint4* bad = reinterpret_cast<const uint4*>(x.smem + kSmBad) + 2 * (c & 1);
             uint4 cols = bad[0];
             cols.x |= bad[1].x, cols.y |= bad[1].y, cols.z |= bad[1].z, cols.w |= bad[1].w;
@@ -760,22 +766,22 @@ __device__ __forceinline__ void out_role(const Maps& maps, const LinParams& p, c
 #pragma unroll
                     for (int u = 0; u < 4; ++u)
                         y[u] = last_bf(mul2(scale, pack2(__uint_as_float(r[e + 2 * u]), __uint_as_float(r[e + 2 * u + 1]))));
-                    *reinterpret_cast<uint4*>(vt + sw128_off(row, 32 * b + e, C)) = make_uint4(y[0], y[1], y[2], y[3]);
+                    *reinterpret_cast<uint4*>(kt + sw128_off(row, 32 * b + e, C)) = make_uint4(y[0], y[1], y[2], y[3]);
                 }
             }
             tc_fence_before();
             __syncwarp();
             if (x.lane == 0) x.arrive(kOEmpty);
             if (cols.x | cols.y | cols.z | cols.w)
-                put_nonfinite(p, item, j * C, min(j * C + row, item.len - 1), row, cols, vt);
+                put_nonfinite(p, item, j * C, min(j * C + row, item.len - 1), row, cols, kt);
             const int live = item.len - j * C - 32 * w;  // rows of this warp's 32
             const int t = item.t0 + j * C + 32 * w;
             fence_proxy_async();
             __syncwarp();
             if (live >= 32) {
                 if (x.lane == 0) {
-                    tma_store_3d(&maps.out, vt + 32 * w * 128, 0, item.h, t);
-                    tma_store_3d(&maps.out, vt + kTile / 2 + 32 * w * 128, 64, item.h, t);
+                    tma_store_3d(&maps.out, kt + 32 * w * 128, 0, item.h, t);
+                    tma_store_3d(&maps.out, kt + kTile / 2 + 32 * w * 128, 64, item.h, t);
                     bulk_commit();
                     bulk_wait_read_all();
                 }
@@ -786,7 +792,7 @@ __device__ __forceinline__ void out_role(const Maps& maps, const LinParams& p, c
 #pragma unroll 1
                 for (int r = half; r < live; r += 2)
                     *reinterpret_cast<uint4*>(out + (int64_t)r * p.H * D) =
-                        *reinterpret_cast<const uint4*>(vt + sw128_off(32 * w + r, 8 * l16, C));
+                        *reinterpret_cast<const uint4*>(kt + sw128_off(32 * w + r, 8 * l16, C));
                 fence_proxy_async();
             }
             // the last of the four warps frees the tile
@@ -794,7 +800,7 @@ __device__ __forceinline__ void out_role(const Maps& maps, const LinParams& p, c
             if (x.lane == 0) {
                 __threadfence_block();
                 if ((atomicAdd(reinterpret_cast<int*>(x.smem + kSmRows), 1) & 3) == 3)
-                    x.arrive(kEmpty + (tile + 1) % kSlots);
+                    x.arrive(kEmpty + k_slot(c));
             }
         }
     }
@@ -828,19 +834,19 @@ __device__ __forceinline__ void weight_role(const LinParams& p, const Ctx& x, in
     // a lane's place in four 8 x 8 matrices: tokens 0-7 and 8-15, value rows 0-7 and 8-15
     const int tok = (x.lane & 7) + ((x.lane >> 4) << 3);
     const int col = 32 * w4 + (((x.lane >> 3) & 1) << 3);
-    int tile = 0, c = 0, cleared = 0;
+    int c = 0, cleared = 0;
     Item item;
     for (int it = 0; x.item(it, &item, true); ++it) {
         const int nc = chunks(item.len);
-        for (int j = 0; j < nc; ++j, ++c, tile += kPerChunk<Local>) {
+        for (int j = 0; j < nc; ++j, ++c) {
             const int live = min(C, item.len - j * C);
-            uint8_t* vt = x.tile(tile + kV<Local>);
-            if (!x.wait_all(x.full(tile + kV<Local>), x.full_phase(tile + kV<Local>))) return;
+            uint8_t* vt = x.tile(v_slot(c));
+            if (!x.wait_all(kFull + v_slot(c), vk_phase(c))) return;
             if (!Local && live < C) {  // (a segment but the last is full)
                 // rows past the sequence's end belong to others: they weigh nothing,
                 // and may hold anything, so they are cleared
-                if (!x.wait_all(x.full(tile + kK<Local>), x.full_phase(tile + kK<Local>))) return;
-                uint8_t* kt = x.tile(tile + kK<Local>);
+                if (!x.wait_all(kFull + k_slot(c), vk_phase(c))) return;
+                uint8_t* kt = x.tile(k_slot(c));
 #pragma unroll 1
                 for (int i = 32 * w8 + x.lane; i < (C - live) * 16; i += 256) {
                     const uint32_t at = (i & 8 ? kTile / 2 : 0) + (live + (i >> 4)) * 128 + (i & 7) * 16;
@@ -975,8 +981,10 @@ __device__ __forceinline__ void state_role(const LinParams& p, const Ctx& x, int
     for (int it = 0; x.item(it, &item, true); ++it) {
         const int nc = chunks(item.len);
         // this lane's 4 columns of the warp's rows half, half + 2, ...
-        P* pool = static_cast<P*>(p.pool) +
-                  (item.flags & kStore ? (size_t)item.slot * p.stride0 : 0) +
+        const int slot = Local ? 0 : p.idx[item.n];
+        const bool ok = slot >= 0 && slot < p.num_slots;
+        if (!Local && !ok && threadIdx.x == 0) atomicOr(p.status, 4);
+        P* pool = static_cast<P*>(p.pool) + (ok ? (size_t)slot * p.stride0 : 0) +
                   ((size_t)item.h * D + 32 * (warp & 3) + half) * D + 64 * sg + 4 * l16;
         // a segment's state in the workspace: this thread's 4 columns 4 e .. every 256 x 4 values
         float4* plane = reinterpret_cast<float4*>(p.planes) + (size_t)item.plane * (D * D / 4) + 32 * warp + x.lane;
@@ -1038,7 +1046,7 @@ __device__ __forceinline__ void state_role(const LinParams& p, const Ctx& x, int
                 plane[256 * e] = make_float4(a.x, a.y, b.x, b.y);
             }
             if (threadIdx.x == 0) p.kept[item.plane] = kept;
-        } else if (item.flags & kStore) {  // the chunk's q S^T, issued before dS, has read the operand
+        } else if (ok && (item.flags & kStore)) {  // the chunk's q S^T, issued before dS, has read the operand
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
                 const float2 a = unpack2(S[2 * e]), b = unpack2(S[2 * e + 1]);
@@ -1068,24 +1076,22 @@ __global__ void __launch_bounds__(kThreads, 1) kda_lin_walk(const __grid_constan
         if (threadIdx.x == 0) atomicOr(p.status, 2);
         return;
     }
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < kNumBars; ++i) {
-            int n = 1;
-            if (i == kDecEmpty || i == kDecEmpty + 1) n = Local ? 24 : 16;
-            if (i == kGEmpty) n = 8;
-            if (i >= kItemEmpty && i < kItemEmpty + kItems) n = 26;
-            if (i == kPFull || i == kQSScaled || i == kOEmpty) n = 4;
-            if (i >= kWFull && i < kWFull + 4) n = 4;
-            if (i == kDSEmpty || i == kSFull || i == kCleared) n = 8;
-            mbar_init(x.bar + i, n);
-        }
+    if (threadIdx.x < kNumBars) {
+        const int i = threadIdx.x;
+        int n = 1;
+        if (i == kDecEmpty || i == kDecEmpty + 1) n = Local ? 24 : 16;
+        if (i == kGEmpty) n = 8;
+        if (i >= kItemEmpty && i < kItemEmpty + kItems) n = 26;
+        if (i == kPFull || i == kQSScaled || i == kOEmpty) n = 4;
+        if (i >= kWFull && i < kWFull + 4) n = 4;
+        if (i == kDSEmpty || i == kSFull || i == kCleared) n = 8;
+        mbar_init(x.bar + i, n);
+        fence_mbar_init();
+    } else if (threadIdx.x == 64) {
         *x.abort = 0;
         *reinterpret_cast<int*>(smem + kSmRows) = 0;
-        fence_mbar_init();
-        prefetch_tmap(&maps.q);
-        prefetch_tmap(&maps.k);
-        prefetch_tmap(&maps.v);
-        prefetch_tmap(&maps.out);
+    } else if (threadIdx.x >= 96 && threadIdx.x < 100) {
+        prefetch_tmap(threadIdx.x == 96 ? &maps.v : threadIdx.x == 97 ? &maps.q : threadIdx.x == 98 ? &maps.k : &maps.out);
     }
     if (warp == 24) tmem_alloc(slot, kTmCols);
     tc_fence_before();
@@ -1098,7 +1104,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_lin_walk(const __grid_constan
 
     // registers: the launch's 896 x 72 = 256 x 112 + 256 x 64 + 256 x 56 + 128 x 40,
     // Local: 256 x 112 + 640 x 56
-    int issued = 0;
+    int3 issued = make_int3(0, 0, 0);
     if (warp < 8) {
         more_registers<112>();
         state_role<P, Local>(p, x, warp);
@@ -1132,9 +1138,11 @@ __global__ void __launch_bounds__(kThreads, 1) kda_lin_walk(const __grid_constan
     if (*x.abort) {
         // a wait gave up: let the copies and products in flight end before their memory goes
         if (threadIdx.x == 0) atomicOr(p.status, 1);
-        if (warp == 25 && x.lane == 0)
-            for (int i = max(0, issued - kSlots); i < issued; ++i)
-                mbar_wait(x.bar + kFull + i % kSlots, (i / kSlots) & 1);
+        if (warp == 25 && x.lane == 0) {
+            if (!Local && issued.x > 0) mbar_wait(x.bar + kFull + kQ, q_phase(issued.x - 1));
+            for (int i = max(0, issued.y - 2); i < issued.y; ++i) mbar_wait(x.bar + kFull + v_slot(i), vk_phase(i));
+            for (int i = max(0, issued.z - 2); i < issued.z; ++i) mbar_wait(x.bar + kFull + k_slot(i), vk_phase(i));
+        }
     }
     if (warp == 24) {
         mbar_wait(x.bar + kDone, 0);
