@@ -13,11 +13,9 @@
 //   20-23 the e^{G_i} on q S^T, the output rows
 //   24    issues the MMAs     25  issues the TMA loads
 //   26    claims items and makes the decays
-// A chunk's products are issued as dS of the first 32 tokens, X, q S^T, the rest of dS,
-// P v: each role's work (P after X, S after dS, e^{G_i} after q S^T, the rows after P v) has
-// products that do not wait for it running beside it.  X takes q from tensor memory: an
-// MMA with both operands in shared memory reads all of its bandwidth, and every other
-// access to it waits.  q S^T has to (W needs the room); it runs when few others read.
+// A chunk's products are issued as the first half of dS, X, q S^T, the other half, P v:
+// what a role needs time for (P after X, S after dS, e^{G_i} after q S^T, the rows after
+// P v) has products beside it that do not wait for it.
 //
 // Rounding.  Operands are bf16.  q, k and v are; P and S are carried as a sum of
 // two bf16 (16 bits: with one, a rounding as large as out's own would be added
@@ -114,13 +112,12 @@ static_assert(kSmGamma % 8 == 0 && kSmMisc % 8 == 0 && kSmRows % 8 == 0, "words"
 constexpr uint32_t kTmX = 0;    // X; then P: per 32 tokens 16 columns high part, 16 low
 constexpr uint32_t kTmO = 128;
 constexpr uint32_t kTmDS = 256;
-// W's buffers of 32 tokens: two K steps x four parts x 8 columns.  The second is q's
-// place, free once X is done; Local has four, X's and O's places being free.
+// W's buffers of 32 tokens: two K steps x four parts x 8 columns, two of them; Local has
+// four, X's and O's places being free.
 constexpr uint32_t kTmW = 384;
 __host__ __device__ constexpr uint32_t w_column(bool local, int n) {
     return local && n >= 2 ? 64 * (n - 2) : kTmW + 64 * (n & 1);
 }
-constexpr uint32_t kTmQ = 448;  // q, for X
 constexpr uint32_t kTmCols = 512;
 
 constexpr uint32_t kIdescKK = mma_idesc(1, 0, 0, 128, 128);  // B K-major
@@ -133,12 +130,6 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, u
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
         "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
-}
-
-// 128 rows x 32 bytes (a K step) from shared memory into 8 columns, in order with
-// the MMAs that this thread issues after it.
-__device__ __forceinline__ void tmem_cp_step(uint32_t d, uint64_t desc) {
-    asm volatile("tcgen05.cp.cta_group::1.128x256b [%0], %1;" ::"r"(d), "l"(desc) : "memory");
 }
 
 // 32 or 16 columns of this thread's lane.
@@ -572,17 +563,15 @@ __device__ __forceinline__ void mma_role(const Ctx& x) {
                 __syncwarp();
                 continue;
             }
-            // X is free once the previous chunk's P v has read it, and W's second buffer
-            // with it: its last product was issued before
+            if (!x.wait_all(kWFull + 1, 0)) return;
+            add_tokens(1);
+            // X is free once the previous chunk's P v has read it
             if (c == 0 ? !x.wait_all(fq, pq) : !x.wait_all(fq, pq, kOFull, (c + 1) & 1)) return;
             tc_fence_after();
             if (lead) {
 #pragma unroll 2
                 for (int ks = 0; ks < 8; ++ks)
-                    tmem_cp_step(x.tmem + kTmQ + 8 * ks, q + kstep(ks));
-#pragma unroll 2
-                for (int ks = 0; ks < 8; ++ks)
-                    mma_f16_ts(x.tmem + kTmX, x.tmem + kTmQ + 8 * ks, k + kstep(ks), kIdescKK, ks > 0);
+                    mma_f16_ss(x.tmem + kTmX, q + kstep(ks), k + kstep(ks), kIdescKK, ks > 0);
                 mma_commit(x.bar + kXFull);
                 if (!has_s) mma_commit(x.bar + kEmpty + kQ);
             }
@@ -600,8 +589,6 @@ __device__ __forceinline__ void mma_role(const Ctx& x) {
                 }
                 __syncwarp();
             }
-            if (!x.wait_all(kWFull + 1, 0)) return;
-            add_tokens(1);
             if (!x.wait_all(kWFull, 1)) return;
             add_tokens(2);
             // P and O are awaited before the products that are still to come, not after
@@ -825,8 +812,7 @@ __device__ __noinline__ uint32_t clear_nonfinite(uint8_t* vt, int col, int odd) 
 
 // ---- warps 8-15: weighted v ---------------------------------------------------------
 // A warp makes 32 value rows of 32 tokens at a time: warps 8-11 of the first and third 32,
-// warps 12-15 of the others (whose place is q's until X is done); Local: each four warps
-// of warps 8-23 of one 32.
+// warps 12-15 of the others; Local: each four warps of warps 8-23 of one 32.
 template <bool Local>
 __device__ __forceinline__ void weight_role(const LinParams& p, const Ctx& x, int w8) {
     const int w4 = w8 & 3, group = w8 >> 2;
@@ -867,10 +853,9 @@ __device__ __forceinline__ void weight_role(const LinParams& p, const Ctx& x, in
             for (int n = group; n < 4; n += Local ? 4 : 2) {
                 const int b = Local ? n : group, t0 = 32 * n;
                 const uint32_t column = w_column(Local, n);
-                // the buffers' last steps have been read, and for q's place q
+                // the buffer's last steps have been read
                 if (Local ? c > 0 && !x.wait_all(kWEmpty + b, (c + 1) & 1)
                           : (c > 0 || n >= 2) && !x.wait_all(kWEmpty + b, n < 2)) return;
-                if (!Local && n == 1 && !x.wait_all(kXFull, c & 1)) return;
                 tc_fence_after();
 #pragma unroll 1
                 for (int s = 0; s < 2; ++s) {  // 16 tokens
