@@ -13,7 +13,7 @@
 //   20-23 the e^{G_i} on q S^T, the output rows
 //   24    issues the MMAs     25  issues the TMA loads
 //   26    claims items and makes the decays
-// A chunk's products are issued as the first half of dS, X, q S^T, the other half, P v:
+// A chunk's products are issued as a quarter of dS, X, q S^T, the rest of dS, P v:
 // what a role needs time for (P after X, S after dS, e^{G_i} after q S^T, the rows after
 // P v) has products beside it that do not wait for it.
 //
@@ -563,8 +563,6 @@ __device__ __forceinline__ void mma_role(const Ctx& x) {
                 __syncwarp();
                 continue;
             }
-            if (!x.wait_all(kWFull + 1, 0)) return;
-            add_tokens(1);
             // X is free once the previous chunk's P v has read it
             if (c == 0 ? !x.wait_all(fq, pq) : !x.wait_all(fq, pq, kOFull, (c + 1) & 1)) return;
             tc_fence_after();
@@ -589,15 +587,18 @@ __device__ __forceinline__ void mma_role(const Ctx& x) {
                 }
                 __syncwarp();
             }
+            if (!x.wait_all(kWFull + 1, 0)) return;
+            add_tokens(1);
             if (!x.wait_all(kWFull, 1)) return;
             add_tokens(2);
-            // P and O are awaited before the products that are still to come, not after
-            if (has_s ? !x.wait_all(kWFull + 1, 1, kPFull, c & 1, kQSScaled, with_s & 1)
-                      : !x.wait_all(kWFull + 1, 1, kPFull, c & 1)) return;
-            if (c > 0 && !has_s && !x.wait_all(kOEmpty, (c + 1) & 1)) return;
+            if (!x.wait_all(kWFull + 1, 1)) return;
             add_tokens(3);
+            if (lead) mma_commit(x.bar + kDSFull);
+            __syncwarp();
+            if (has_s ? !x.wait_all(kPFull, c & 1, kQSScaled, with_s & 1)
+                      : c == 0 ? !x.wait_all(kPFull, 0) : !x.wait_all(kPFull, c & 1, kOEmpty, (c + 1) & 1)) return;
+            tc_fence_after();
             if (lead) {
-                mma_commit(x.bar + kDSFull);
 #pragma unroll 1
                 for (int ks = 0; ks < 8; ++ks)
 #pragma unroll
