@@ -9,11 +9,11 @@
 // One CTA walks one (sequence, head) at a time; its warps have roles:
 //   0-7   S in registers, and as the q S^T product's operand in shared memory
 //   8-15  W, the weighted v, into tensor memory
-//   16-19 X to P, in place
-//   20-23 the e^{G_i} on q S^T, the output rows
-//   24    issues the MMAs     25  issues the TMA loads
-//   26    claims items and makes the decays
-// A chunk's products are issued as a quarter of dS, X, q S^T, the rest of dS, P v:
+//   16-23 X to P, in place
+//   24-27 the e^{G_i} on q S^T, the output rows
+//   28    issues the MMAs     29  issues the TMA loads
+//   30    claims items and makes the decays
+// A chunk's products are issued as a quarter of dS, X, another, q S^T, the rest of dS, P v:
 // what a role needs time for (P after X, S after dS, e^{G_i} after q S^T, the rows after
 // P v) has products beside it that do not wait for it.
 //
@@ -50,7 +50,7 @@ using namespace dev;
 
 constexpr int D = kD;
 constexpr int C = 128;
-constexpr int kThreads = 28 * 32;
+constexpr int kThreads = 32 * 32;
 constexpr int kTile = C * D * 2;  // bytes of a q, k or v tile
 // Tiles in flight or in use: q's, and two of v and of k, used by turns.  A chunk's q is
 // free after q S^T, its v after P v, its k after dS and once the chunk's output rows,
@@ -109,7 +109,7 @@ static_assert(kSmG % 16 == 0 && kSmCf % 16 == 0 && kSmBad % 16 == 0, "read by 16
 static_assert(kSmGamma % 8 == 0 && kSmMisc % 8 == 0 && kSmRows % 8 == 0, "words");
 
 // Tensor memory columns.
-constexpr uint32_t kTmX = 0;    // X; then P: per 32 tokens 16 columns high part, 16 low
+constexpr uint32_t kTmX = 0;    // X; then P: per 16 tokens 8 columns high part, 8 low
 constexpr uint32_t kTmO = 128;
 constexpr uint32_t kTmDS = 256;
 // W's buffers of 32 tokens: two K steps x four parts x 8 columns, two of them; Local has
@@ -351,7 +351,7 @@ struct Ctx {
 };
 __device__ __forceinline__ int chunks(int len) { return (len + C - 1) / C; }
 
-// ---- warp 26: items and decays ------------------------------------------------
+// ---- warp 30: items and decays ------------------------------------------------
 // Item i of the call.  The cut sequences' segments come first; Local: all but their last.
 template <bool Local>
 __device__ __forceinline__ Item make_item(const LinParams& p, const LinCuts& cuts, int i, int lane) {
@@ -480,7 +480,7 @@ __device__ __forceinline__ void decay_role(const LinParams& p, const LinCuts& cu
     }
 }
 
-// ---- warp 25, one lane: loads -------------------------------------------------
+// ---- warp 29, one lane: loads -------------------------------------------------
 // Returns the numbers of q, v and k tiles issued.
 template <bool Local>
 __device__ __forceinline__ int3 load_role(const Maps& maps, const LinParams& p, const Ctx& x) {
@@ -509,7 +509,7 @@ __device__ __forceinline__ int3 load_role(const Maps& maps, const LinParams& p, 
     return make_int3(c, c, c);
 }
 
-// ---- warp 24: products ----------------------------------------------------------
+// ---- warp 28: products ----------------------------------------------------------
 // The warp runs as one (descriptors stay in uniform registers); one elected lane
 // issues.
 template <bool Local>
@@ -574,6 +574,8 @@ __device__ __forceinline__ void mma_role(const Ctx& x) {
                 if (!has_s) mma_commit(x.bar + kEmpty + kQ);
             }
             __syncwarp();
+            if (!x.wait_all(kWFull + 1, 0)) return;
+            add_tokens(1);
             // O is free once the previous chunk's rows have been read
             if (has_s) {
                 if (c == 0 ? !x.wait_all(kSFull, with_s & 1) : !x.wait_all(kSFull, with_s & 1, kOEmpty, (c + 1) & 1)) return;
@@ -587,8 +589,6 @@ __device__ __forceinline__ void mma_role(const Ctx& x) {
                 }
                 __syncwarp();
             }
-            if (!x.wait_all(kWFull + 1, 0)) return;
-            add_tokens(1);
             if (!x.wait_all(kWFull, 1)) return;
             add_tokens(2);
             if (!x.wait_all(kWFull + 1, 1)) return;
@@ -603,7 +603,7 @@ __device__ __forceinline__ void mma_role(const Ctx& x) {
                 for (int ks = 0; ks < 8; ++ks)
 #pragma unroll
                     for (int part = 1; part >= 0; --part)
-                        mma_f16_ts(x.tmem + kTmO, x.tmem + kTmX + 32 * (ks >> 1) + 16 * part + 8 * (ks & 1),
+                        mma_f16_ts(x.tmem + kTmO, x.tmem + kTmX + 16 * ks + 8 * part,
                                    vm + mstep(ks), kIdescKM, has_s || ks > 0 || part == 0);
                 mma_commit(x.bar + kOFull);  // k's tile takes the output rows now
                 mma_commit(x.bar + kEmpty + v_slot(c));
@@ -633,12 +633,14 @@ __device__ __noinline__ void put_nonfinite(const LinParams& p, const Item& item,
         }
 }
 
-// ---- warps 16-19: scores; thread = chunk row ------------------------------------
-__device__ __forceinline__ void score_role(const LinParams& p, const Ctx& x, int w) {
+// ---- warps 16-23: scores; thread = chunk row ------------------------------------
+// Warps 16-19 take the even groups of 16 columns, warps 20-23 the odd ones.
+__device__ __forceinline__ void score_role(const LinParams& p, const Ctx& x, int w8) {
+    const int w = w8 & 3, odd = w8 >> 2;
     const int row = 32 * w + x.lane;
-    const uint32_t tm = x.tmem + ((uint32_t)(32 * w) << 16) + kTmX;
+    const uint32_t tm = x.tmem + ((uint32_t)(32 * w) << 16) + kTmX + 16 * odd;
     const float* G = reinterpret_cast<const float*>(x.smem + kSmG);
-    const float* cf = reinterpret_cast<const float*>(x.smem + kSmCf);
+    const float2* cf = reinterpret_cast<const float2*>(x.smem + kSmCf) + 8 * odd;
     int c = 0;
     Item item;
     for (int it = 0; x.item(it, &item, true); ++it) {
@@ -646,47 +648,43 @@ __device__ __forceinline__ void score_role(const LinParams& p, const Ctx& x, int
             if (!x.wait_all(kGFull, c & 1, kXFull, c & 1)) return;
             const float gi = G[row];
             tc_fence_after();
-            // Sixteen scores become eight pairs of high parts and eight of low parts.
-            // A block of 32 is held as high 0-15, high 16-31, low 0-15, low 16-31 so
-            // that its first half is read before its place is written.
+            // Sixteen scores become eight pairs of high parts and eight of low parts, in place.
+            uint32_t r[16];
             auto split_and_store = [&](int b, auto factor) {
-                uint32_t hi[16], lo[16];
+                uint32_t o[16];
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    uint32_t r[16];
-                    tmem_ld16u(tm + 32 * b + 16 * u, r);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int e = 0; e < 16; e += 2) {
-                        const f2 f = factor(16 * u + e, r[e], r[e + 1]);  // may clear the scores
-                        f2 v = mul2(pack2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), f);
-                        hi[8 * u + e / 2] = take_bf(v);
-                        lo[8 * u + e / 2] = last_bf(v);
-                    }
+                for (int e = 0; e < 16; e += 2) {
+                    f2 v = mul2(pack2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), factor(e));
+                    o[e / 2] = take_bf(v);
+                    o[8 + e / 2] = last_bf(v);
                 }
-                tmem_st16(tm + 32 * b, hi);
-                tmem_st16(tm + 32 * b + 16, lo);
+                tmem_st16(tm + 32 * b, o);
             };
 #pragma unroll 1
             for (int b = 0; b < w; ++b) {
+                tmem_ld16u(tm + 32 * b, r);
                 const float f = ex2(gi - G[32 * b + 31]);
                 const f2 ff = pack2(f, f);
-                const float2* col = reinterpret_cast<const float2*>(cf + 32 * b);
-                split_and_store(b, [&](int e, uint32_t, uint32_t) {
-                    const float2 u = col[e / 2];
+                tmem_wait_ld();
+                split_and_store(b, [&](int e) {
+                    const float2 u = cf[16 * b + e / 2];
                     return mul2(ff, pack2(u.x, u.y));
                 });
             }
-            const float2* Gw = reinterpret_cast<const float2*>(G + 32 * w);
-            split_and_store(w, [&](int e, uint32_t& a, uint32_t& b) {
+            tmem_ld16u(tm + 32 * w, r);
+            const float2* Gw = reinterpret_cast<const float2*>(G + 32 * w + 16 * odd);
+            const int last = x.lane - 16 * odd;  // of this row, in the group
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                if (e > last) r[e] = 0u;
+            split_and_store(w, [&](int e) {
                 const float2 u = Gw[e / 2];
-                if (e > x.lane) a = 0u;
-                if (e + 1 > x.lane) b = 0u;
-                return pack2(ex2(e > x.lane ? 0.f : gi - u.x), ex2(e + 1 > x.lane ? 0.f : gi - u.y));
+                return pack2(ex2(e > last ? 0.f : gi - u.x), ex2(e + 1 > last ? 0.f : gi - u.y));
             });
             const uint32_t zero[16] = {};
 #pragma unroll 1
-            for (int b = 2 * w + 2; b < 8; ++b) tmem_st16(tm + 16 * b, zero);
+            for (int b = w + 1; b < 4; ++b) tmem_st16(tm + 32 * b, zero);
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -698,7 +696,7 @@ __device__ __forceinline__ void score_role(const LinParams& p, const Ctx& x, int
     }
 }
 
-// ---- warps 20-23: output rows; thread = chunk row --------------------------------
+// ---- warps 24-27: output rows; thread = chunk row --------------------------------
 __device__ __forceinline__ void out_role(const Maps& maps, const LinParams& p, const Ctx& x, int w) {
     const int row = 32 * w + x.lane;
     const uint32_t tm = x.tmem + ((uint32_t)(32 * w) << 16) + kTmO;
@@ -1066,11 +1064,11 @@ __global__ void __launch_bounds__(kThreads, 1) kda_lin_walk(const __grid_constan
         const int i = threadIdx.x;
         int n = 1;
         if (i == kDecEmpty || i == kDecEmpty + 1) n = Local ? 24 : 16;
-        if (i == kGEmpty) n = 8;
-        if (i >= kItemEmpty && i < kItemEmpty + kItems) n = 26;
-        if (i == kPFull || i == kQSScaled || i == kOEmpty) n = 4;
+        if (i == kGEmpty) n = 12;
+        if (i >= kItemEmpty && i < kItemEmpty + kItems) n = Local ? 26 : 30;
+        if (i == kQSScaled || i == kOEmpty) n = 4;
         if (i >= kWFull && i < kWFull + 4) n = 4;
-        if (i == kDSEmpty || i == kSFull || i == kCleared) n = 8;
+        if (i == kDSEmpty || i == kSFull || i == kCleared || i == kPFull) n = 8;
         mbar_init(x.bar + i, n);
         fence_mbar_init();
     } else if (threadIdx.x == 64) {
@@ -1079,7 +1077,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_lin_walk(const __grid_constan
     } else if (threadIdx.x >= 96 && threadIdx.x < 100) {
         prefetch_tmap(threadIdx.x == 96 ? &maps.v : threadIdx.x == 97 ? &maps.q : threadIdx.x == 98 ? &maps.k : &maps.out);
     }
-    if (warp == 24) tmem_alloc(slot, kTmCols);
+    if (warp == 28) tmem_alloc(slot, kTmCols);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -1088,32 +1086,32 @@ __global__ void __launch_bounds__(kThreads, 1) kda_lin_walk(const __grid_constan
     // what follows in the stream may be set up; it waits for this grid where it has to
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    // registers: the launch's 896 x 72 = 256 x 112 + 256 x 64 + 256 x 56 + 128 x 40,
-    // Local: 256 x 112 + 640 x 56
+    // registers: the launch's 1024 x 64 = 256 x 104 + 256 x 56 + 256 x 48 + 128 x 56 + 128 x 40,
+    // Local: 256 x 104 + 512 x 56 + 256 x 40
     int3 issued = make_int3(0, 0, 0);
     if (warp < 8) {
-        more_registers<112>();
+        more_registers<104>();
         state_role<P, Local>(p, x, warp);
     } else if (warp < 16) {
-        fewer_registers<Local ? 56 : 64>();
+        fewer_registers<56>();
         weight_role<Local>(p, x, warp - 8);
     } else if (warp < 24) {
-        fewer_registers<56>();
-        if constexpr (Local) {
+        fewer_registers<Local ? 56 : 48>();
+        if constexpr (Local)
             weight_role<Local>(p, x, warp - 8);
-        } else if (warp < 20) {
+        else
             score_role(p, x, warp - 16);
-        } else {
-            out_role(maps, p, x, warp - 20);
-        }
+    } else if (warp < 28) {
+        fewer_registers<Local ? 40 : 56>();
+        if constexpr (!Local) out_role(maps, p, x, warp - 24);
     } else {
-        fewer_registers<Local ? 56 : 40>();
-        if (warp == 24) {
+        fewer_registers<40>();
+        if (warp == 28) {
             mma_role<Local>(x);
             if (elect_one()) mma_commit(x.bar + kDone);  // the lane that issued
-        } else if (warp == 25) {
+        } else if (warp == 29) {
             if (x.lane == 0) issued = load_role<Local>(maps, p, x);
-        } else if (warp == 26) {
+        } else if (warp == 30) {
             decay_role<Local>(p, cuts, x);
         }
     }
@@ -1124,18 +1122,18 @@ __global__ void __launch_bounds__(kThreads, 1) kda_lin_walk(const __grid_constan
     if (*x.abort) {
         // a wait gave up: let the copies and products in flight end before their memory goes
         if (threadIdx.x == 0) atomicOr(p.status, 1);
-        if (warp == 25 && x.lane == 0) {
+        if (warp == 29 && x.lane == 0) {
             if (!Local && issued.x > 0) mbar_wait(x.bar + kFull + kQ, q_phase(issued.x - 1));
             for (int i = max(0, issued.y - 2); i < issued.y; ++i) mbar_wait(x.bar + kFull + v_slot(i), vk_phase(i));
             for (int i = max(0, issued.z - 2); i < issued.z; ++i) mbar_wait(x.bar + kFull + k_slot(i), vk_phase(i));
         }
     }
-    if (warp == 24) {
+    if (warp == 28) {
         mbar_wait(x.bar + kDone, 0);
         tc_fence_after();
     }
     __syncthreads();
-    if (warp == 24) tmem_dealloc(x.tmem, kTmCols);
+    if (warp == 28) tmem_dealloc(x.tmem, kTmCols);
 }
 
 // From the states that segments make from zero to the states they start from, in place:
