@@ -13,7 +13,7 @@
 //   24-27 the e^{G_i} on q S^T, the output rows
 //   28    issues the MMAs     29  issues the TMA loads
 //   30    claims items and makes the decays
-// A chunk's products are issued as a quarter of dS, X, another, q S^T, the rest of dS, P v:
+// A chunk's products are issued as X, the first half of dS, q S^T, the other half, P v:
 // what a role needs time for (P after X, S after dS, e^{G_i} after q S^T, the rows after
 // P v) has products beside it that do not wait for it.
 //
@@ -57,7 +57,9 @@ constexpr int kTile = C * D * 2;  // bytes of a q, k or v tile
 // which pass through it, have left; so the next v is on its way a chunk ahead and the next
 // q and k half a chunk (with one ring for all, v's loads waited for the rows: 7.4 K cycles
 // a chunk instead of 5.9 K on 16384 tokens x 12 heads).
-constexpr int kSlots = 5;
+// Local has S's place too: four of v and three of k, whose loads then cover their latency
+// (two of each: 4.2 K cycles a chunk).
+constexpr int kSlots = 5, kLocalSlots = 7;
 constexpr int kItems = 3;         // items the claims run ahead
 
 // Shared memory.  Tiles are two halves of 64 columns, 128-byte swizzled.
@@ -76,9 +78,9 @@ constexpr int kSmBar = kSmItem + kItems * (int)sizeof(Item);
 static_assert(kSmBar % 8 == 0, "barriers are 8-byte aligned");
 
 enum Bar {
-    kFull = 0,                  // [5] tile loaded
-    kEmpty = kFull + kSlots,    // [5] tile consumed
-    kDecFull = kEmpty + kSlots, // [2] weights and e^{G_C} of a chunk made
+    kFull = 0,                       // [7] tile loaded
+    kEmpty = kFull + kLocalSlots,    // [7] tile consumed
+    kDecFull = kEmpty + kLocalSlots, // [2] weights and e^{G_C} of a chunk made
     kDecEmpty = kDecFull + 2,   // [2] and read
     kGFull = kDecEmpty + 2,     // G and the factors of score columns made
     kGEmpty,                    // and read
@@ -172,13 +174,17 @@ __device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t (&r)[16]) {
         "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(a)
         : "memory");
 }
-// 16 lanes x 8 columns: r0 holds lane t/4, column t%4; r1 lane t/4 + 8; r2, r3 the
-// same four columns on.  The layout of ldmatrix fragments.
-__device__ __forceinline__ void tmem_st_16x8(uint32_t a, uint32_t r0, uint32_t r1, uint32_t r2,
-                                             uint32_t r3) {
-    asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(r0),
-                 "r"(r1), "r"(r2), "r"(r3)
-                 : "memory");
+// 16 lanes x 32 columns: per four columns two registers, of lane t/4 and lane t/4 + 8,
+// column t%4.  The layout of ldmatrix fragments.  (A store of 8 columns takes as long as
+// one of 32: W's stores were the bound of the segments' states, 3.1 K cycles a chunk.)
+__device__ __forceinline__ void tmem_st_16x32(uint32_t a, const uint32_t (&r)[4][4]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x128b.x8.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+        "%15};" ::"r"(r[0][0]),
+        "r"(r[0][1]), "r"(r[0][2]), "r"(r[0][3]), "r"(r[1][0]), "r"(r[1][1]), "r"(r[1][2]), "r"(r[1][3]),
+        "r"(r[2][0]), "r"(r[2][1]), "r"(r[2][2]), "r"(r[2][3]), "r"(r[3][0]), "r"(r[3][1]), "r"(r[3][2]),
+        "r"(r[3][3]), "r"(a)
+        : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() {
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -258,10 +264,18 @@ __device__ __forceinline__ bool elect_one() {
 
 // Slots of a chunk's tiles, and the phase of their barriers.
 constexpr int kQ = 0;
-__device__ __forceinline__ int v_slot(int c) { return 1 + (c & 1); }
-__device__ __forceinline__ int k_slot(int c) { return 3 + (c & 1); }
+template <bool Local> __device__ __forceinline__ uint8_t* tile(int slot) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    return smem + (Local ? kSmS : kSmTile) + slot * kTile;
+}
 __device__ __forceinline__ uint32_t q_phase(int c) { return c & 1; }
-__device__ __forceinline__ uint32_t vk_phase(int c) { return (c >> 1) & 1; }
+template <bool Local> constexpr int kVs = Local ? 4 : 2;  // slots of v, and of k
+template <bool Local> constexpr int kKs = Local ? 3 : 2;
+template <bool Local> __device__ __forceinline__ int v_slot(int c) { return (Local ? 0 : 1) + c % kVs<Local>; }
+template <bool Local> __device__ __forceinline__ int k_slot(int c) { return (Local ? 4 : 3) + c % kKs<Local>; }
+template <bool Local> __device__ __forceinline__ uint32_t v_phase(int c) { return (c / kVs<Local>) & 1; }
+template <bool Local> __device__ __forceinline__ uint32_t k_phase(int c) { return (c / kKs<Local>) & 1; }
+static_assert(kSmS + kLocalSlots * kTile == kSmTile + kSlots * kTile, "the same room");
 
 struct Maps {
     CUtensorMap q, k, v, out;
@@ -330,8 +344,19 @@ struct Ctx {
         return __all_sync(0xffffffffu, ok != 0);
     }
 #undef KDA_WAIT_END
+    template <int N>
+    __device__ __forceinline__ bool wait_all(const int (&b)[N], const uint32_t (&parity)[N]) const {
+#pragma unroll 1
+        for (uint32_t n = 0;; ++n) {
+            bool ok = true;
+#pragma unroll
+            for (int i = 0; i < N; ++i) ok = mbar_try_wait(bar + b[i], parity[i]) && ok;
+            if (__all_sync(0xffffffffu, ok)) return true;
+            if (n == kWaitLimit) *abort = 1;
+            if (__any_sync(0xffffffffu, *abort != 0)) return false;
+        }
+    }
     __device__ __forceinline__ void arrive(int b) const { mbar_arrive(bar + b); }
-    __device__ __forceinline__ uint8_t* tile(int slot) const { return smem + kSmTile + slot * kTile; }
     // Parts of the weights of the token pairs of chunk c.
     __device__ __forceinline__ const uint32_t* weights(int c) const {
         return reinterpret_cast<const uint32_t*>(smem + kSmW) + (c & 1) * 3 * (C / 2);
@@ -487,7 +512,7 @@ __device__ __forceinline__ int3 load_role(const Maps& maps, const LinParams& p, 
     int c = 0;
     auto load = [&](int slot, const CUtensorMap* map, int h, int t) {
         uint64_t* bar = x.bar + kFull + slot;
-        uint8_t* dst = x.tile(slot);
+        uint8_t* dst = tile<Local>(slot);
         mbar_arrive_expect_tx(bar, kTile);
         tma_load_3d(dst, map, bar, 0, h, t);
         tma_load_3d(dst + kTile / 2, map, bar, 64, h, t);
@@ -496,14 +521,14 @@ __device__ __forceinline__ int3 load_role(const Maps& maps, const LinParams& p, 
     for (int it = 0; x.item(it, &item, false); ++it) {
         for (int j = 0; j < chunks(item.len); ++j, ++c) {
             const int t = item.t0 + j * C;
-            if (c >= 2 && !x.wait(kEmpty + v_slot(c), vk_phase(c) ^ 1)) return make_int3(c, c, c);
-            load(v_slot(c), &maps.v, item.h, t);
+            if (c >= kVs<Local> && !x.wait(kEmpty + v_slot<Local>(c), v_phase<Local>(c) ^ 1)) return make_int3(c, c, c);
+            load(v_slot<Local>(c), &maps.v, item.h, t);
             if constexpr (!Local) {
                 if (c >= 1 && !x.wait(kEmpty + kQ, q_phase(c) ^ 1)) return make_int3(c, c + 1, c);
                 load(kQ, &maps.q, item.h / p.rep, t);
             }
-            if (c >= 2 && !x.wait(kEmpty + k_slot(c), vk_phase(c) ^ 1)) return make_int3(c + 1, c + 1, c);
-            load(k_slot(c), &maps.k, item.h / p.rep, t);
+            if (c >= kKs<Local> && !x.wait(kEmpty + k_slot<Local>(c), k_phase<Local>(c) ^ 1)) return make_int3(c + 1, c + 1, c);
+            load(k_slot<Local>(c), &maps.k, item.h / p.rep, t);
         }
     }
     return make_int3(c, c, c);
@@ -528,8 +553,8 @@ __device__ __forceinline__ void mma_role(const Ctx& x) {
         const int nc = chunks(item.len);
         for (int j = 0; j < nc; ++j, ++c) {
             const bool has_s = j > 0 || (item.flags & (kInit | kPlane));
-            const uint32_t qa = smem_u32(x.tile(kQ)), va = smem_u32(x.tile(v_slot(c))),
-                           ka = smem_u32(x.tile(k_slot(c)));
+            const uint32_t qa = smem_u32(tile<Local>(kQ)), va = smem_u32(tile<Local>(v_slot<Local>(c))),
+                           ka = smem_u32(tile<Local>(k_slot<Local>(c)));
             const uint64_t k = kdesc(ka), q = kdesc(qa), km = mdesc(ka), vm = mdesc(va);
             auto add_tokens = [&](int n) {  // dS over tokens 32 n .. 32 n + 31
                 tc_fence_after();
@@ -544,27 +569,30 @@ __device__ __forceinline__ void mma_role(const Ctx& x) {
                 }
                 __syncwarp();
             };
-            const int fq = kFull + kQ, fk = kFull + k_slot(c);
-            const uint32_t pq = q_phase(c), pk = vk_phase(c);
-            const uint32_t w0 = Local ? c & 1 : 0;  // the phase of W's first tokens
-            if (c == 0 ? !x.wait_all(fk, pk, kWFull, w0) : !x.wait_all(fk, pk, kWFull, w0, kDSEmpty, (c + 1) & 1)) return;
-            add_tokens(0);
             if constexpr (Local) {
+                if (c == 0 ? !x.wait_all(kFull + k_slot<Local>(c), k_phase<Local>(c))
+                           : !x.wait_all(kFull + k_slot<Local>(c), k_phase<Local>(c), kDSEmpty, (c + 1) & 1)) return;
 #pragma unroll 1
-                for (int n = 1; n < 4; ++n) {
+                for (int n = 0; n < 4; ++n) {
                     if (!x.wait_all(kWFull + n, c & 1)) return;
                     add_tokens(n);
                 }
                 if (lead) {
-                    x.arrive(kEmpty + v_slot(c));  // read by the W warps alone
+                    x.arrive(kEmpty + v_slot<Local>(c));  // read by the W warps alone
                     mma_commit(x.bar + kDSFull);
-                    mma_commit(x.bar + kEmpty + k_slot(c));
+                    mma_commit(x.bar + kEmpty + k_slot<Local>(c));
                 }
                 __syncwarp();
                 continue;
             }
             // X is free once the previous chunk's P v has read it
-            if (c == 0 ? !x.wait_all(fq, pq) : !x.wait_all(fq, pq, kOFull, (c + 1) & 1)) return;
+            if (c == 0) {
+                if (!x.wait_all({kFull + kQ, kFull + k_slot<Local>(c), kWFull}, {q_phase(c), k_phase<Local>(c), 0u})) return;
+            } else {
+                const uint32_t before = (c + 1) & 1;
+                if (!x.wait_all({kFull + kQ, kFull + k_slot<Local>(c), kWFull, kDSEmpty, kOFull},
+                                {q_phase(c), k_phase<Local>(c), 0u, before, before})) return;
+            }
             tc_fence_after();
             if (lead) {
 #pragma unroll 2
@@ -574,6 +602,7 @@ __device__ __forceinline__ void mma_role(const Ctx& x) {
                 if (!has_s) mma_commit(x.bar + kEmpty + kQ);
             }
             __syncwarp();
+            add_tokens(0);
             if (!x.wait_all(kWFull + 1, 0)) return;
             add_tokens(1);
             // O is free once the previous chunk's rows have been read
@@ -606,7 +635,7 @@ __device__ __forceinline__ void mma_role(const Ctx& x) {
                         mma_f16_ts(x.tmem + kTmO, x.tmem + kTmX + 16 * ks + 8 * part,
                                    vm + mstep(ks), kIdescKM, has_s || ks > 0 || part == 0);
                 mma_commit(x.bar + kOFull);  // k's tile takes the output rows now
-                mma_commit(x.bar + kEmpty + v_slot(c));
+                mma_commit(x.bar + kEmpty + v_slot<Local>(c));
             }
             __syncwarp();
             with_s += has_s;
@@ -737,7 +766,7 @@ __device__ __forceinline__ void out_role(const Maps& maps, const LinParams& p, c
             // The rows go through k's tile, which has been read, so that whole rows
             // are written to memory: lanes that each store a row of their own fill
             // the load/store unit with single sectors and hold up everything else.
-            uint8_t* kt = x.tile(k_slot(c));
+            uint8_t* kt = tile<false>(k_slot<false>(c));
             const uint4* bad = reinterpret_cast<const uint4*>(x.smem + kSmBad) + 2 * (c & 1);
             uint4 cols = bad[0];
             cols.x |= bad[1].x, cols.y |= bad[1].y, cols.z |= bad[1].z, cols.w |= bad[1].w;
@@ -786,7 +815,7 @@ __device__ __forceinline__ void out_role(const Maps& maps, const LinParams& p, c
             if (x.lane == 0) {
                 __threadfence_block();
                 if ((atomicAdd(reinterpret_cast<int*>(x.smem + kSmRows), 1) & 3) == 3)
-                    x.arrive(kEmpty + k_slot(c));
+                    x.arrive(kEmpty + k_slot<false>(c));
             }
         }
     }
@@ -825,13 +854,13 @@ __device__ __forceinline__ void weight_role(const LinParams& p, const Ctx& x, in
         const int nc = chunks(item.len);
         for (int j = 0; j < nc; ++j, ++c) {
             const int live = min(C, item.len - j * C);
-            uint8_t* vt = x.tile(v_slot(c));
-            if (!x.wait_all(kFull + v_slot(c), vk_phase(c))) return;
+            uint8_t* vt = tile<Local>(v_slot<Local>(c));
+            if (!x.wait_all(kFull + v_slot<Local>(c), v_phase<Local>(c))) return;
             if (!Local && live < C) {  // (a segment but the last is full)
                 // rows past the sequence's end belong to others: they weigh nothing,
                 // and may hold anything, so they are cleared
-                if (!x.wait_all(kFull + k_slot(c), vk_phase(c))) return;
-                uint8_t* kt = x.tile(k_slot(c));
+                if (!x.wait_all(kFull + k_slot<Local>(c), k_phase<Local>(c))) return;
+                uint8_t* kt = tile<Local>(k_slot<Local>(c));
 #pragma unroll 1
                 for (int i = 32 * w8 + x.lane; i < (C - live) * 16; i += 256) {
                     const uint32_t at = (i & 8 ? kTile / 2 : 0) + (live + (i >> 4)) * 128 + (i & 7) * 16;
@@ -878,8 +907,7 @@ __device__ __forceinline__ void weight_role(const LinParams& p, const Ctx& x, in
                             nan2 = fma_bf2(t[1][e], 0u, nan2);  // an infinite or NaN value leaves a NaN
                         }
                         const uint32_t at = tm + ((uint32_t)(16 * i) << 16) + column + 32 * s;
-#pragma unroll
-                        for (int u = 0; u < 4; ++u) tmem_st_16x8(at + 8 * u, t[u][0], t[u][1], t[u][2], t[u][3]);
+                        tmem_st_16x32(at, t);
                     }
                 }
                 tmem_wait_st();
@@ -1124,8 +1152,10 @@ __global__ void __launch_bounds__(kThreads, 1) kda_lin_walk(const __grid_constan
         if (threadIdx.x == 0) atomicOr(p.status, 1);
         if (warp == 29 && x.lane == 0) {
             if (!Local && issued.x > 0) mbar_wait(x.bar + kFull + kQ, q_phase(issued.x - 1));
-            for (int i = max(0, issued.y - 2); i < issued.y; ++i) mbar_wait(x.bar + kFull + v_slot(i), vk_phase(i));
-            for (int i = max(0, issued.z - 2); i < issued.z; ++i) mbar_wait(x.bar + kFull + k_slot(i), vk_phase(i));
+            for (int i = max(0, issued.y - kVs<Local>); i < issued.y; ++i)
+                mbar_wait(x.bar + kFull + v_slot<Local>(i), v_phase<Local>(i));
+            for (int i = max(0, issued.z - kKs<Local>); i < issued.z; ++i)
+                mbar_wait(x.bar + kFull + k_slot<Local>(i), k_phase<Local>(i));
         }
     }
     if (warp == 28) {
