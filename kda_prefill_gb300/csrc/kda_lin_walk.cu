@@ -13,7 +13,7 @@
 //   24-27 the e^{G_i} on q S^T, the output rows
 //   28    issues the MMAs     29  issues the TMA loads
 //   30    claims items and makes the decays
-// A chunk's products are issued as X, the first half of dS, q S^T, the other half, P v:
+// A chunk's products are issued as a quarter of dS, X, another, q S^T, the rest of dS, P v:
 // what a role needs time for (P after X, S after dS, e^{G_i} after q S^T, the rows after
 // P v) has products beside it that do not wait for it.
 //
@@ -279,6 +279,8 @@ static_assert(kSmS + kLocalSlots * kTile == kSmTile + kSlots * kTile, "the same 
 
 struct Maps {
     CUtensorMap q, k, v, out;
+    CUtensorMap pool;  // boxes of 128 bytes of 32 rows
+    int store_states;  // the pool has a map
 };
 
 // What every role needs.
@@ -344,18 +346,6 @@ struct Ctx {
         return __all_sync(0xffffffffu, ok != 0);
     }
 #undef KDA_WAIT_END
-    template <int N>
-    __device__ __forceinline__ bool wait_all(const int (&b)[N], const uint32_t (&parity)[N]) const {
-#pragma unroll 1
-        for (uint32_t n = 0;; ++n) {
-            bool ok = true;
-#pragma unroll
-            for (int i = 0; i < N; ++i) ok = mbar_try_wait(bar + b[i], parity[i]) && ok;
-            if (__all_sync(0xffffffffu, ok)) return true;
-            if (n == kWaitLimit) *abort = 1;
-            if (__any_sync(0xffffffffu, *abort != 0)) return false;
-        }
-    }
     __device__ __forceinline__ void arrive(int b) const { mbar_arrive(bar + b); }
     // Parts of the weights of the token pairs of chunk c.
     __device__ __forceinline__ const uint32_t* weights(int c) const {
@@ -412,7 +402,15 @@ __device__ __forceinline__ Item make_item(const LinParams& p, const LinCuts& cut
     // a segment's initial state is in the workspace, and the state warps look its slot up
     if (k >= n_seg) {
         const int slot = p.idx[item.n];
-        if (p.has_init[item.n] && slot >= 0 && slot < p.num_slots) item.flags |= kInit;
+        if (p.has_init[item.n] && slot >= 0 && slot < p.num_slots) {
+            item.flags |= kInit;
+            // into the L2 cache: the state warps get there when the item before is done
+            const int bytes = D * D * (p.st_dtype == KDA_STATE_F32 ? 4 : 2);
+            const char* from = static_cast<const char*>(p.pool) +
+                               ((size_t)slot * p.stride0 + (size_t)item.h * D * D) * (bytes / (D * D));
+            if (lane == 0)
+                asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"(bytes) : "memory");
+        }
     }
     return item;
 }
@@ -585,14 +583,12 @@ __device__ __forceinline__ void mma_role(const Ctx& x) {
                 __syncwarp();
                 continue;
             }
+            if (c == 0 ? !x.wait_all(kFull + k_slot<Local>(c), k_phase<Local>(c), kWFull, 0)
+                       : !x.wait_all(kFull + k_slot<Local>(c), k_phase<Local>(c), kWFull, 0, kDSEmpty, (c + 1) & 1)) return;
+            add_tokens(0);
             // X is free once the previous chunk's P v has read it
-            if (c == 0) {
-                if (!x.wait_all({kFull + kQ, kFull + k_slot<Local>(c), kWFull}, {q_phase(c), k_phase<Local>(c), 0u})) return;
-            } else {
-                const uint32_t before = (c + 1) & 1;
-                if (!x.wait_all({kFull + kQ, kFull + k_slot<Local>(c), kWFull, kDSEmpty, kOFull},
-                                {q_phase(c), k_phase<Local>(c), 0u, before, before})) return;
-            }
+            if (c == 0 ? !x.wait_all(kFull + kQ, q_phase(c))
+                       : !x.wait_all(kFull + kQ, q_phase(c), kOFull, (c + 1) & 1)) return;
             tc_fence_after();
             if (lead) {
 #pragma unroll 2
@@ -602,7 +598,6 @@ __device__ __forceinline__ void mma_role(const Ctx& x) {
                 if (!has_s) mma_commit(x.bar + kEmpty + kQ);
             }
             __syncwarp();
-            add_tokens(0);
             if (!x.wait_all(kWFull + 1, 0)) return;
             add_tokens(1);
             // O is free once the previous chunk's rows have been read
@@ -955,7 +950,7 @@ __device__ __forceinline__ void store4(__half* s, float4 v) {
 }
 
 template <class P, bool Local>
-__device__ __forceinline__ void state_role(const LinParams& p, const Ctx& x, int warp) {
+__device__ __forceinline__ void state_role(const Maps& maps, const LinParams& p, const Ctx& x, int warp) {
     const int sg = warp >> 2;
     const int row = 32 * (warp & 3) + x.lane;
     const uint32_t tm = x.tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kTmDS + 64 * sg;
@@ -989,6 +984,14 @@ __device__ __forceinline__ void state_role(const LinParams& p, const Ctx& x, int
                                          (32 * (warp & 3) + r) * 128 + (((e & 7) ^ (r & 7)) << 4));
     };
     const int l16 = x.lane & 15, half = x.lane >> 4;
+    bool leaving = false;  // a state on its way from the operand's place to the pool
+    auto place_free = [&]() {
+        if (leaving) {
+            if (x.lane == 0) bulk_wait_read_all();
+            __syncwarp();
+            leaving = false;
+        }
+    };
     Item item;
     for (int it = 0; x.item(it, &item, true); ++it) {
         const int nc = chunks(item.len);
@@ -1001,6 +1004,7 @@ __device__ __forceinline__ void state_role(const LinParams& p, const Ctx& x, int
         // a segment's state in the workspace: this thread's 4 columns 4 e .. every 256 x 4 values
         float4* plane = reinterpret_cast<float4*>(p.planes) + (size_t)item.plane * (D * D / 4) + 32 * warp + x.lane;
         float kept = 1.f;  // Local: what is left of the state after the segment
+        if (!Local && (item.flags & (kPlane | kInit))) place_free();
         if (!Local && (item.flags & kPlane)) {
             grid_dep_wait();  // the chain kernel may still run
 #pragma unroll
@@ -1049,7 +1053,10 @@ __device__ __forceinline__ void state_role(const LinParams& p, const Ctx& x, int
                     S[8 * b + e / 2] = fma2(g2, S[8 * b + e / 2],
                                              pack2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])));
             }
-            if (!Local && j + 1 < nc) write_operand();
+            if (!Local && j + 1 < nc) {
+                place_free();
+                write_operand();
+            }
         }
         if (Local) {
 #pragma unroll
@@ -1059,17 +1066,53 @@ __device__ __forceinline__ void state_role(const LinParams& p, const Ctx& x, int
             }
             if (threadIdx.x == 0) p.kept[item.plane] = kept;
         } else if (ok && (item.flags & kStore)) {  // the chunk's q S^T, issued before dS, has read the operand
+            place_free();
+            if (maps.store_states) {
+                // as the pool's type in rows of 128 bytes, swizzled as its map's boxes are:
+                // fp32 columns 0-31 in the high part's place, 32-63 in the low part's
+                uint8_t* mine = x.smem + kSmS + sg * (kTile / 2) + 32 * (warp & 3) * 128;
+                if constexpr (sizeof(P) == 4) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const float2 a = unpack2(S[2 * e]), b = unpack2(S[2 * e + 1]);
-                *staged(x.lane, e) = make_float4(a.x, a.y, b.x, b.y);
-            }
-            __syncwarp();
+                    for (int e = 0; e < 16; ++e) {
+                        const float2 a = unpack2(S[2 * e]), b = unpack2(S[2 * e + 1]);
+                        *staged(x.lane, e) = make_float4(a.x, a.y, b.x, b.y);
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        uint2 u[2];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const float2 a = unpack2(S[4 * e + 2 * i]), b = unpack2(S[4 * e + 2 * i + 1]);
+                            store4(reinterpret_cast<P*>(&u[i]), make_float4(a.x, a.y, b.x, b.y));
+                        }
+                        *reinterpret_cast<uint4*>(mine + x.lane * 128 + ((e ^ (x.lane & 7)) << 4)) =
+                            make_uint4(u[0].x, u[0].y, u[1].x, u[1].y);
+                    }
+                }
+                fence_proxy_async();
+                __syncwarp();
+                if (x.lane == 0) {
+                    const int y = item.h * D + 32 * (warp & 3);
+                    tma_store_3d(&maps.pool, mine, 64 * sg, y, slot);
+                    if (sizeof(P) == 4) tma_store_3d(&maps.pool, mine + kTile, 64 * sg + 32, y, slot);
+                    bulk_commit();
+                }
+                leaving = true;
+            } else {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const float2 a = unpack2(S[2 * e]), b = unpack2(S[2 * e + 1]);
+                    *staged(x.lane, e) = make_float4(a.x, a.y, b.x, b.y);
+                }
+                __syncwarp();
 #pragma unroll 4
-            for (int r = 0; r < 32; r += 2) store4(pool + r * D, *staged(r + half, l16));
-            __syncwarp();
+                for (int r = 0; r < 32; r += 2) store4(pool + r * D, *staged(r + half, l16));
+                __syncwarp();
+            }
         }
     }
+    if (x.lane == 0) bulk_wait_all();
 }
 
 // Local: the segments' states from zero, nothing else (the q, score and output parts idle).
@@ -1119,7 +1162,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_lin_walk(const __grid_constan
     int3 issued = make_int3(0, 0, 0);
     if (warp < 8) {
         more_registers<104>();
-        state_role<P, Local>(p, x, warp);
+        state_role<P, Local>(maps, p, x, warp);
     } else if (warp < 16) {
         fewer_registers<56>();
         weight_role<Local>(p, x, warp - 8);
@@ -1221,20 +1264,26 @@ EncodeTiledFn encode_fn() {
     return fn;
 }
 
-// Boxes of 64 values x 1 head x `rows` tokens of a [T][H][128] view; tokens past the
-// end read as zeros.
-bool make_map(CUtensorMap* m, const void* base, int64_t T, int H, int64_t st, int64_t sh, int rows) {
+// Boxes of 128 bytes x 1 x `rows` of a 3-D tensor, 128-byte swizzled; rows past the end
+// read as zeros.  The middle dimension's boxes are one wide, or with rows_in_middle the
+// last one's.
+bool make_map(CUtensorMap* m, CUtensorMapDataType type, int elt, const void* base, const int64_t (&dim)[3],
+              const int64_t (&stride)[2], int rows, bool rows_in_middle) {
     if (!encode_fn()) return false;
-    // a dimension of one entry never steps: any stride that encodes will do
-    if (T == 1) st = D;
-    if (H == 1) sh = D;
-    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)T};
-    const cuuint64_t strides[2] = {(cuuint64_t)sh * 2, (cuuint64_t)st * 2};
-    const cuuint32_t box[3] = {64, 1, (cuuint32_t)rows};
+    const cuuint64_t dims[3] = {(cuuint64_t)dim[0], (cuuint64_t)dim[1], (cuuint64_t)dim[2]};
+    const cuuint64_t strides[2] = {(cuuint64_t)stride[0] * elt, (cuuint64_t)stride[1] * elt};
+    const cuuint32_t box[3] = {(cuuint32_t)(128 / elt), rows_in_middle ? (cuuint32_t)rows : 1,
+                               rows_in_middle ? 1 : (cuuint32_t)rows};
     const cuuint32_t step[3] = {1, 1, 1};
-    return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides,
-                       box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+    return encode_fn()(m, type, 3, const_cast<void*>(base), dims, strides, box, step,
+                       CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// A [T][H][128] view of bf16.
+bool make_rows_map(CUtensorMap* m, const void* base, int64_t T, int H, int64_t st, int64_t sh, int rows) {
+    // a dimension of one entry never steps: any stride that encodes will do
+    return make_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, {D, H, T}, {H == 1 ? D : sh, T == 1 ? D : st}, rows,
+                    false);
 }
 
 // Launches with programmatic stream serialization where `early`: set up while the kernel
@@ -1346,11 +1395,15 @@ cudaError_t launch_lin_walk(const LinParams& p, const LinCuts& cuts, cudaStream_
     if (p.n_long <= 0) return cudaSuccess;
     if ((int64_t)p.n_long * p.H > INT32_MAX - 65536) return cudaErrorInvalidValue;
     Maps maps;
-    if (!make_map(&maps.q, p.q, p.T, p.H / p.rep, p.q_st, p.q_sh, C) ||
-        !make_map(&maps.k, p.k, p.T, p.H / p.rep, p.k_st, p.k_sh, C) ||
-        !make_map(&maps.v, p.v, p.T, p.H, p.v_st, p.v_sh, C) ||
-        !make_map(&maps.out, p.out, p.T, p.H, (int64_t)p.H * D, D, 32))
+    if (!make_rows_map(&maps.q, p.q, p.T, p.H / p.rep, p.q_st, p.q_sh, C) ||
+        !make_rows_map(&maps.k, p.k, p.T, p.H / p.rep, p.k_st, p.k_sh, C) ||
+        !make_rows_map(&maps.v, p.v, p.T, p.H, p.v_st, p.v_sh, C) ||
+        !make_rows_map(&maps.out, p.out, p.T, p.H, (int64_t)p.H * D, D, 32))
         return cudaErrorInvalidValue;
+    // the pool as [slots][H x 128][128]; one too large for a map is written without
+    const bool wide = p.st_dtype == KDA_STATE_F32;
+    maps.store_states = make_map(&maps.pool, wide ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16,
+                                 wide ? 4 : 2, p.pool, {D, (int64_t)p.H * D, p.num_slots}, {D, p.stride0}, 32, true);
     if (p.st_dtype == KDA_STATE_F32) return launch<float>(maps, p, cuts, s);
     if (p.st_dtype == KDA_STATE_BF16) return launch<__nv_bfloat16>(maps, p, cuts, s);
     return launch<__half>(maps, p, cuts, s);
