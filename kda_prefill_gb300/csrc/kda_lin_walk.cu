@@ -1212,40 +1212,58 @@ __global__ void __launch_bounds__(kThreads, 1) kda_lin_walk(const __grid_constan
 // From the states that segments make from zero to the states they start from, in place:
 // with S the sequence's initial state, plane s takes S and S becomes kept_s S + (what
 // plane s held).  The first segment's is taken from the pool here, too: the last
-// segment's walk writes the pool, perhaps before the first one's has started.  A thread
-// takes four columns of a row through all segments; its reads run sixteen segments ahead.
-template <class P>
-__global__ void __launch_bounds__(256) kda_lin_chain(const __grid_constant__ LinParams p,
-                                                     const __grid_constant__ LinCuts cuts) {
+// segment's walk writes the pool, perhaps before the first one's has started.
+//
+// Bound by the reads' latency, so they all go out at once: a thread has four columns of a
+// row in up to AHEAD segments, threads side by side (in y) have the segments that follow,
+// and the states between their runs are handed on through shared memory.
+constexpr int kChainAhead = 8, kChainRuns = 20;  // 160 segments at most
+template <class P, int AHEAD, int X, int RUNS>
+__global__ void __launch_bounds__(X* RUNS) kda_lin_chain(const __grid_constant__ LinParams p,
+                                                                     const __grid_constant__ LinCuts cuts) {
+    __shared__ float4 sum[RUNS][X];
+    __shared__ float left[RUNS];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int r = blockIdx.y / p.H, h = blockIdx.y % p.H;
     const int first = cuts.first[r], segs = cuts.first[r + 1] - first;
     const int n = cuts.seq[r], slot = p.idx[n];
-    const int warp = threadIdx.x >> 5, e = blockIdx.x;  // as the state warps hold it
+    const int at = blockIdx.x * X + threadIdx.x;  // as the state warps hold it: e, warp, lane
+    const int e = at >> 8, warp = (at >> 5) & 7;
     float4 S = make_float4(0.f, 0.f, 0.f, 0.f);
     if (slot >= 0 && slot < p.num_slots && p.has_init[n])
         S = load4<P>(static_cast<const P*>(p.pool) + (size_t)slot * p.stride0 +
-                     ((size_t)h * D + 32 * (warp & 3) + (threadIdx.x & 31)) * D + 64 * (warp >> 2) + 4 * e);
+                     ((size_t)h * D + 32 * (warp & 3) + (at & 31)) * D + 64 * (warp >> 2) + 4 * e);
     const size_t step = (size_t)p.H * (D * D / 4);
-    float4* plane = reinterpret_cast<float4*>(p.planes) + ((size_t)first * p.H + h) * (D * D / 4) + 256 * e + threadIdx.x;
-    const float* kept = p.kept + (size_t)first * p.H + h;
-    constexpr int kAhead = 16;
+    const int s0 = threadIdx.y * AHEAD, run = min(AHEAD, segs - s0);  // this thread's segments
+    float4* plane = reinterpret_cast<float4*>(p.planes) + (size_t)h * (D * D / 4) + at + (first + s0) * step;
+    const float* kept = p.kept + (size_t)(first + s0) * p.H + h;
+    auto next = [](float4 a, float k, float4 v) {
+        return make_float4(fmaf(k, a.x, v.x), fmaf(k, a.y, v.y), fmaf(k, a.z, v.z), fmaf(k, a.w, v.w));
+    };
     grid_dep_wait();  // the segments' states are made
-    for (int s = 0; s < segs; s += kAhead) {
-        float4 v[kAhead];
-        float k[kAhead];
+    float4 v[AHEAD];
+    float k[AHEAD];
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i)
-            if (s + i < segs - 1) v[i] = plane[(s + i) * step], k[i] = kept[(size_t)(s + i) * p.H];
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i)
-            if (s + i < segs) {
-                plane[(s + i) * step] = S;
-                if (s + i < segs - 1)
-                    S = make_float4(fmaf(k[i], S.x, v[i].x), fmaf(k[i], S.y, v[i].y), fmaf(k[i], S.z, v[i].z),
-                                    fmaf(k[i], S.w, v[i].w));
-            }
+    for (int i = 0; i < AHEAD; ++i) {
+        v[i] = make_float4(0.f, 0.f, 0.f, 0.f), k[i] = 1.f;
+        if (i < run && s0 + i < segs - 1) v[i] = plane[i * step], k[i] = kept[(size_t)i * p.H];
     }
+    if (RUNS > 1) {
+        float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+        float all = 1.f;
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) t = next(t, k[i], v[i]), all *= k[i];
+        sum[threadIdx.y][threadIdx.x] = t;
+        if (threadIdx.x == 0) left[threadIdx.y] = all;
+        __syncthreads();
+        for (int i = 0; i < threadIdx.y; ++i) S = next(S, left[i], sum[i][threadIdx.x]);
+    }
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)
+        if (i < run) {
+            plane[i * step] = S;
+            S = next(S, k[i], v[i]);
+        }
 }
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
@@ -1289,11 +1307,11 @@ bool make_rows_map(CUtensorMap* m, const void* base, int64_t T, int H, int64_t s
 // Launches with programmatic stream serialization where `early`: set up while the kernel
 // before still runs, whose results it then waits for.
 template <class... A>
-cudaError_t launch_after(bool early, void (*kernel)(A...), dim3 grid, int threads, size_t smem, cudaStream_t s,
+cudaError_t launch_after(bool early, void (*kernel)(A...), dim3 grid, dim3 threads, size_t smem, cudaStream_t s,
                          const A&... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
+    cfg.blockDim = threads;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -1317,7 +1335,22 @@ cudaError_t launch_one(bool early, const Maps& maps, const LinParams& p, const L
         if (dev < 32) ready[dev] = true;
     }
     const int grid = (int)(items < num_sms() ? items : num_sms());
-    return launch_after(early, kda_lin_walk<P, Local>, dim3(grid), kThreads, kSmemBytes, s, maps, p, cuts);
+    return launch_after(early, kda_lin_walk<P, Local>, dim3(grid), dim3(kThreads), kSmemBytes, s, maps, p, cuts);
+}
+
+template <class P>
+cudaError_t launch_chain(const LinParams& p, const LinCuts& cuts, cudaStream_t s) {
+    int most = 0;
+    for (int r = 0; r < p.n_cut; ++r) most = max(most, cuts.first[r + 1] - cuts.first[r]);
+    // Runs of 8 need no more registers than three such blocks an SM leave, and 152 segments
+    // are still one trip to memory: 33.8 us of 37.8 for a prompt of 16384 x 2 heads, against
+    // one run of up to 16 at a time.  Up to four segments need no joining: 119.1 us of 122.1
+    // for five prompts of 128 segments in all beside 512 of one token.
+    const unsigned y = (unsigned)(p.n_cut * p.H), columns = D * D / 4;
+    if (most <= 4)
+        return launch_after(true, kda_lin_chain<P, 4, 128, 1>, dim3(columns / 128, y), dim3(128), 0, s, p, cuts);
+    return launch_after(true, kda_lin_chain<P, kChainAhead, 32, kChainRuns>, dim3(columns / 32, y),
+                        dim3(32, (most + kChainAhead - 1) / kChainAhead), 0, s, p, cuts);
 }
 
 template <class P>
@@ -1328,7 +1361,7 @@ cudaError_t launch(const Maps& maps, const LinParams& p, const LinCuts& cuts, cu
         // the segments' states do not depend on the pool's type
         e = launch_one<float, true>(false, maps, p, cuts, (int64_t)(p.n_seg - p.n_cut) * p.H, s);
         if (e == cudaSuccess)
-            e = launch_after(true, kda_lin_chain<P>, dim3(16, (unsigned)(p.n_cut * p.H)), 256, 0, s, p, cuts);
+            e = launch_chain<P>(p, cuts, s);
     }
     if (e == cudaSuccess)
         e = launch_one<P, false>(cut, maps, p, cuts, (int64_t)(p.n_seg + p.n_long - p.n_cut) * p.H, s);
@@ -1371,7 +1404,8 @@ Cut cut_rule(const int32_t* lens, int n, int H, int sms) {
     cut.seg_len = seg * C;
     for (; cut.n_cut < n && chunks_of(lens[cut.n_cut]) > seg; ++cut.n_cut)
         cut.n_seg += (chunks_of(lens[cut.n_cut]) + seg - 1) / seg;
-    if (cut.n_cut > kLinCuts || (int64_t)cut.n_seg * H > kLinPlanes) return Cut();
+    if (cut.n_cut > kLinCuts || (int64_t)cut.n_seg * H > kLinPlanes ||
+        (longest + seg - 1) / seg > kChainAhead * kChainRuns) return Cut();
     return cut;
 }
 
