@@ -299,3 +299,43 @@ def test_slots_past_32_bits_of_elements():
     d = dict(c, cache=big, idx=at.to(torch.int32))
     assert torch.equal(run(c), run(d))
     assert torch.equal(big[at], c["cache"][c["idx"].long().cuda()])
+
+
+def test_cut_sequences_captured():
+    """Sequences walked in segments, in a captured call that is replayed twice."""
+    c, d = (make([2600, 1, 1300, 200], 2, seed=19, decay="token", init=[1, 1, 0, 1]) for _ in range(2))
+    want = run(c)
+    cu, idx, has = d["cu"].cuda(), d["idx"].cuda(), d["has"].cuda()
+    ws = torch.empty(kda.lin_attn_workspace_size(4101, 4, 2), dtype=torch.uint8, device="cuda")
+    out = torch.empty_like(want)
+    start = d["storage"].clone()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        kda.lin_attn_fwd(d["q"], d["k"], d["v"], d["g"], cu, state_cache=d["cache"], state_indices=idx,
+                         has_initial_state=has, out=out, cu_seqlens_cpu=d["cu"], workspace=ws)
+    for _ in range(2):
+        d["storage"].copy_(start)
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(d["cache"], c["cache"])
+    assert kda.check_status(ws) == 0
+
+
+def test_nonfinite_values_in_cut_sequences():
+    """As within a chunk: the value's column from its token on, in every later segment."""
+    c, clean = (make([3100, 20], 2, seed=20, init=[1, 0]) for _ in range(2))
+    c["v"][0, 1700, 1, 9] = float("inf")
+    c["v"][0, 100, 0, 64] = float("nan")
+    out, good = run(c), run(clean)
+    bad = torch.zeros(good.shape, dtype=torch.bool, device="cuda")
+    bad[0, 1700:3100, 1, 9] = True
+    bad[0, 100:3100, 0, 64] = True
+    assert bool((~torch.isfinite(out[bad])).all())
+    assert torch.equal(out[~bad], good[~bad])
+    S, T = c["cache"][c["idx"].long().cuda()], clean["cache"][clean["idx"].long().cuda()]
+    hit = torch.zeros(S.shape, dtype=torch.bool, device="cuda")
+    hit[0, 1, 9] = hit[0, 0, 64] = True
+    assert bool((~torch.isfinite(S[hit])).all())
+    assert torch.equal(S[~hit], T[~hit])
