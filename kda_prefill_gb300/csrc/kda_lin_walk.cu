@@ -1004,7 +1004,6 @@ __device__ __forceinline__ void state_role(const Maps& maps, const LinParams& p,
         // a segment's state in the workspace: this thread's 4 columns 4 e .. every 256 x 4 values
         float4* plane = reinterpret_cast<float4*>(p.planes) + (size_t)item.plane * (D * D / 4) + 32 * warp + x.lane;
         float kept = 1.f;  // Local: what is left of the state after the segment
-        if (!Local && (item.flags & (kPlane | kInit))) place_free();
         if (!Local && (item.flags & kPlane)) {
             grid_dep_wait();  // the chain kernel may still run
 #pragma unroll
@@ -1012,11 +1011,16 @@ __device__ __forceinline__ void state_role(const Maps& maps, const LinParams& p,
                 const float4 v = plane[256 * e];
                 S[2 * e] = pack2(v.x, v.y), S[2 * e + 1] = pack2(v.z, v.w);
             }
+            place_free();
             write_operand();
         } else if (!Local && (item.flags & kInit)) {
+            float4 rows[16];  // all in flight at once
+#pragma unroll
+            for (int r = 0; r < 16; ++r) rows[r] = load4<P>(pool + 2 * r * D);
+            place_free();
             // the last q S^T has read the operand: it was issued before the last dS
-#pragma unroll 4
-            for (int r = 0; r < 32; r += 2) *staged(r + half, l16) = load4<P>(pool + r * D);
+#pragma unroll
+            for (int r = 0; r < 16; ++r) *staged(2 * r + half, l16) = rows[r];
             __syncwarp();
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
