@@ -94,9 +94,9 @@ enum Bar {
     kOEmpty,                    // and read
     kWFull,                     // [4] 32 tokens of W written, by buffer (two; Local: four)
     kWEmpty = kWFull + 4,       // [4] and read
-    kDSFull = kWEmpty + 4,      // dS complete
-    kDSEmpty,                   // and read
-    kSFull,                     // S's operand written
+    kDSFull = kWEmpty + 4,      // [2] dS complete (Local has two, by turns)
+    kDSEmpty = kDSFull + 2,     // [2] and read
+    kSFull = kDSEmpty + 2,      // S's operand written
     kCleared,                   // rows past a sequence's end cleared
     kDone,                      // everything issued has completed
     kNumBars
@@ -121,6 +121,12 @@ __host__ __device__ constexpr uint32_t w_column(bool local, int n) {
     return local && n >= 2 ? 64 * (n - 2) : kTmW + 64 * (n & 1);
 }
 constexpr uint32_t kTmCols = 512;
+// dS's place, barrier and phase for chunk c.  Local has two, the other in O's place: with
+// one, a chunk's products waited for the chunk before to be read (16384 tokens x 12 heads: 80.6 us
+// instead of 82.0).
+template <bool Local> __device__ __forceinline__ uint32_t ds_column(int c) { return Local && (c & 1) ? kTmO : kTmDS; }
+template <bool Local> __device__ __forceinline__ int ds_bar(int c) { return Local ? c & 1 : 0; }
+template <bool Local> __device__ __forceinline__ uint32_t ds_phase(int c) { return (Local ? c >> 1 : c) & 1; }
 
 constexpr uint32_t kIdescKK = mma_idesc(1, 0, 0, 128, 128);  // B K-major
 constexpr uint32_t kIdescKM = mma_idesc(1, 0, 1, 128, 128);  // B MN-major
@@ -561,15 +567,16 @@ __device__ __forceinline__ void mma_role(const Ctx& x) {
                     for (int s = 0; s < 2; ++s)
 #pragma unroll
                         for (int part = 3; part >= 0; --part)  // the smallest first
-                            mma_f16_ts(x.tmem + kTmDS, x.tmem + w_column(Local, n) + 32 * s + 8 * part,
+                            mma_f16_ts(x.tmem + ds_column<Local>(c), x.tmem + w_column(Local, n) + 32 * s + 8 * part,
                                        km + mstep(2 * n + s), kIdescKM, n > 0 || s > 0 || part < 3);
                     mma_commit(x.bar + kWEmpty + (Local ? n : n & 1));
                 }
                 __syncwarp();
             };
             if constexpr (Local) {
-                if (c == 0 ? !x.wait_all(kFull + k_slot<Local>(c), k_phase<Local>(c))
-                           : !x.wait_all(kFull + k_slot<Local>(c), k_phase<Local>(c), kDSEmpty, (c + 1) & 1)) return;
+                if (c < 2 ? !x.wait_all(kFull + k_slot<Local>(c), k_phase<Local>(c))
+                          : !x.wait_all(kFull + k_slot<Local>(c), k_phase<Local>(c),
+                                        kDSEmpty + ds_bar<Local>(c), ds_phase<Local>(c) ^ 1)) return;
 #pragma unroll 1
                 for (int n = 0; n < 4; ++n) {
                     if (!x.wait_all(kWFull + n, c & 1)) return;
@@ -577,7 +584,7 @@ __device__ __forceinline__ void mma_role(const Ctx& x) {
                 }
                 if (lead) {
                     x.arrive(kEmpty + v_slot<Local>(c));  // read by the W warps alone
-                    mma_commit(x.bar + kDSFull);
+                    mma_commit(x.bar + kDSFull + ds_bar<Local>(c));
                     mma_commit(x.bar + kEmpty + k_slot<Local>(c));
                 }
                 __syncwarp();
@@ -953,7 +960,7 @@ template <class P, bool Local>
 __device__ __forceinline__ void state_role(const Maps& maps, const LinParams& p, const Ctx& x, int warp) {
     const int sg = warp >> 2;
     const int row = 32 * (warp & 3) + x.lane;
-    const uint32_t tm = x.tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kTmDS + 64 * sg;
+    const uint32_t tm = x.tmem + ((uint32_t)(32 * (warp & 3)) << 16) + 64 * sg;
     int c = 0;
     f2 S[32];
     // S as the product's operand: row `row`, columns 64 sg .. + 63
@@ -1038,19 +1045,19 @@ __device__ __forceinline__ void state_role(const Maps& maps, const LinParams& p,
             const float gamma = x.gamma(c);
             __syncwarp();
             if (x.lane == 0) x.arrive(kDecEmpty + (c & 1));
-            if (!x.wait_all(kDSFull, c & 1)) return;
+            if (!x.wait_all(kDSFull + ds_bar<Local>(c), ds_phase<Local>(c))) return;
             tc_fence_after();
             const f2 g2 = pack2(gamma, gamma);
             if (Local) kept *= gamma;
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
                 uint32_t r[16];
-                tmem_ld16u(tm + 16 * b, r);
+                tmem_ld16u(tm + ds_column<Local>(c) + 16 * b, r);
                 tmem_wait_ld();
                 if (b == 3) {
                     tc_fence_before();
                     __syncwarp();
-                    if (x.lane == 0) x.arrive(kDSEmpty);
+                    if (x.lane == 0) x.arrive(kDSEmpty + ds_bar<Local>(c));
                 }
 #pragma unroll
                 for (int e = 0; e < 16; e += 2)
@@ -1143,7 +1150,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_lin_walk(const __grid_constan
         if (i >= kItemEmpty && i < kItemEmpty + kItems) n = Local ? 26 : 30;
         if (i == kQSScaled || i == kOEmpty) n = 4;
         if (i >= kWFull && i < kWFull + 4) n = 4;
-        if (i == kDSEmpty || i == kSFull || i == kCleared || i == kPFull) n = 8;
+        if (i == kDSEmpty || i == kDSEmpty + 1 || i == kSFull || i == kCleared || i == kPFull) n = 8;
         mbar_init(x.bar + i, n);
         fence_mbar_init();
     } else if (threadIdx.x == 64) {
