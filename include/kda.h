@@ -388,7 +388,13 @@ enum kda_dtype { KDA_F32 = 0, KDA_BF16 = 1, KDA_F16 = 2 };
  * Accumulation is in fp32; an fp32 pool receives the state to fp32 accuracy.
  * The order of summation, and so every bit of the result, depends on the
  * bounds, the head counts and the GPU's SM count alone.  A token's output depends on its own
- * sequence's tokens up to it alone, also where others hold infinities or NaN.
+ * sequence's tokens up to it alone, also where others hold infinities or NaN:
+ * one in v makes its value column NaN or infinite from its token on (in out and
+ * in the state), one in q its own token's row.
+ *
+ * Where few long sequences would leave SMs idle they are worked on in segments
+ * at once, through about 20 MB of the workspace (part of its size beyond 768
+ * tokens).
  *
  * Graph capture, synchronisation and bounds follow kda_chunk_fwd.
  */

@@ -17,6 +17,18 @@
 // what a role needs time for (P after X, S after dS, e^{G_i} after q S^T, the rows after
 // P v) has products beside it that do not wait for it.
 //
+// The products are the bound: 72 of 128 x 128 x 16, 64 cycles each, 4.6 K cycles a chunk,
+// of which the tensor pipe reaches about three quarters while it shares shared and tensor
+// memory with the operands' makers (6.2 K cycles a chunk; 128 sequences of 117,555 tokens
+// x 12 heads: 323 us, tensor pipe active 62 % of the time, 46 % of the memory's rate).
+// Chunks of 128 fill the products' M: with 64, q S^T would run at half rate, and S would
+// be read, rounded and written as an operand twice as often.
+//
+// A few long sequences would leave most SMs idle.  They are cut into segments: a first
+// launch makes each segment's state from zero (Local), kda_lin_chain the states that the
+// segments start from, and the walk takes them as items.  1 x 16384 tokens x 12 heads:
+// 80.6 us (26 Local, 52 the walk), 412 us uncut.
+//
 // Rounding.  Operands are bf16.  q, k and v are; P and S are carried as a sum of
 // two bf16 (16 bits: with one, a rounding as large as out's own would be added
 // to it).  W has to keep 24 bits, the state being fp32: with the weight as a sum
@@ -55,10 +67,8 @@ constexpr int kTile = C * D * 2;  // bytes of a q, k or v tile
 // Tiles in flight or in use: q's, and two of v and of k, used by turns.  A chunk's q is
 // free after q S^T, its v after P v, its k after dS and once the chunk's output rows,
 // which pass through it, have left; so the next v is on its way a chunk ahead and the next
-// q and k half a chunk (with one ring for all, v's loads waited for the rows: 7.4 K cycles
-// a chunk instead of 5.9 K on 16384 tokens x 12 heads).
-// Local has S's place too: four of v and three of k, whose loads then cover their latency
-// (two of each: 4.2 K cycles a chunk).
+// q and k half a chunk (in one ring for all, v's loads would wait for the rows).
+// Local has S's place too: four of v and three of k, whose loads then cover their latency.
 constexpr int kSlots = 5, kLocalSlots = 7;
 constexpr int kItems = 3;         // items the claims run ahead
 
@@ -104,7 +114,7 @@ enum Bar {
 constexpr int kSmGamma = kSmBar + kNumBars * 8;  // [2] e^{G_C}
 constexpr int kSmBad = (kSmGamma + 8 + 15) & ~15;  // [2][8] value columns with infinities or NaN
 constexpr int kSmMisc = kSmBad + 64;             // tensor-memory base, abort flag
-constexpr int kSmRows = kSmMisc + 8;             // warps done with a q tile's rows
+constexpr int kSmRows = kSmMisc + 8;             // warps done with a chunk's output rows
 constexpr int kSmemBytes = kSmRows + 8;
 static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
 static_assert(kSmG % 16 == 0 && kSmCf % 16 == 0 && kSmBad % 16 == 0, "read by 16 bytes");
@@ -182,7 +192,7 @@ __device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t (&r)[16]) {
 }
 // 16 lanes x 32 columns: per four columns two registers, of lane t/4 and lane t/4 + 8,
 // column t%4.  The layout of ldmatrix fragments.  (A store of 8 columns takes as long as
-// one of 32: W's stores were the bound of the segments' states, 3.1 K cycles a chunk.)
+// one of 32; with this one and seven slots 16384 tokens x 12 heads went from 83.6 to 82.4 us.)
 __device__ __forceinline__ void tmem_st_16x32(uint32_t a, const uint32_t (&r)[4][4]) {
     asm volatile(
         "tcgen05.st.sync.aligned.16x128b.x8.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
@@ -1231,7 +1241,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_lin_walk(const __grid_constan
 constexpr int kChainAhead = 8, kChainRuns = 20;  // 160 segments at most
 template <class P, int AHEAD, int X, int RUNS>
 __global__ void __launch_bounds__(X* RUNS) kda_lin_chain(const __grid_constant__ LinParams p,
-                                                                     const __grid_constant__ LinCuts cuts) {
+                                                         const __grid_constant__ LinCuts cuts) {
     __shared__ float4 sum[RUNS][X];
     __shared__ float left[RUNS];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -1353,10 +1363,9 @@ template <class P>
 cudaError_t launch_chain(const LinParams& p, const LinCuts& cuts, cudaStream_t s) {
     int most = 0;
     for (int r = 0; r < p.n_cut; ++r) most = max(most, cuts.first[r + 1] - cuts.first[r]);
-    // Runs of 8 need no more registers than three such blocks an SM leave, and 152 segments
-    // are still one trip to memory: 33.8 us of 37.8 for a prompt of 16384 x 2 heads, against
-    // one run of up to 16 at a time.  Up to four segments need no joining: 119.1 us of 122.1
-    // for five prompts of 128 segments in all beside 512 of one token.
+    // Runs of 8: 152 segments are one trip to memory (a prompt of 16384 x 2 heads 33.8 us;
+    // one thread's run of all of them, 16 at a time, 37.8 us).  Up to four segments need no
+    // joining: 119.1 us instead of 122.1 for four prompts of 2048 beside 512 of one token.
     const unsigned y = (unsigned)(p.n_cut * p.H), columns = D * D / 4;
     if (most <= 4)
         return launch_after(true, kda_lin_chain<P, 4, 128, 1>, dim3(columns / 128, y), dim3(128), 0, s, p, cuts);
@@ -1385,7 +1394,10 @@ cudaError_t launch(const Maps& maps, const LinParams& p, const LinCuts& cuts, cu
 // which are made first from k and v alone, in about half of a walk's time; a few chunks'
 // time goes into the two more launches and the states' way through memory.  The segments
 // are as long as lets one wave of CTAs take all items, or, where there are more sequences
-// than that, as an even share of the chunks.
+// than that, as an even share of the chunks.  Cut and uncut, 12 heads: 29.2 and 36.9 us for
+// 1024 tokens, 30.6 and 61.6 us for 2048, 38.9 and 116 us for 4097, 80.6 and 412 us for
+// 16384; 118.5 and 122.8 us for four of 2048 beside 512 of one token; 768 tokens stay
+// uncut, 30.8 us.
 struct Cut {
     int seg_len = 0, n_cut = 0, n_seg = 0;
 };

@@ -254,8 +254,6 @@ int kda_rope(const kda_rope_tensor* tensors, int32_t num_tensors, const void* po
         return set_error(KDA_ERR_INVALID_ARG, "positions and inv_freq are required");
     if (!aligned(positions, (size_t)position_bytes) || !aligned(inv_freq, 8))
         return set_error(KDA_ERR_UNSUPPORTED, "positions or inv_freq is not aligned to its type");
-    // q and k may be views of one buffer (a projection's output): then their
-    // rows interleave, which the spans cannot tell from an overlap
     const Span sp = span("positions", positions, (size_t)T * position_bytes);
     const Span sf = span("inv_freq", inv_freq, (size_t)(rot_dim / 2) * 8);
     for (int i = 0; i < num_tensors; ++i)
