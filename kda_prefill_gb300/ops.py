@@ -22,6 +22,7 @@ from . import (KDA_OK, STATE_DTYPES, _check, _host_bounds, _per_sequence, _same_
 
 _DTYPES = STATE_DTYPES  # kda_dtype has the same values as kda_state_dtype
 _LAYOUTS = {"half": 0, "interleaved": 1}
+_FLAGS = (torch.bool, torch.uint8)
 _ACTIVATIONS = {"none": 0, "sigmoid": 1, "silu": 2}
 
 
@@ -68,6 +69,15 @@ def _stream(stream, device):
     return torch.cuda.current_stream(device).cuda_stream
 
 
+def _empty(shape, dtype, device, stream):
+    """New memory of the stream that the call runs on: another stream's could be given
+    out again, once the caller has dropped it, while the call still uses it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _host_int32(cu_seqlens_cpu, N: int):
     """_host_bounds, without its conversions where nothing has to be converted."""
     h = cu_seqlens_cpu
@@ -94,49 +104,51 @@ def lin_attn_fwd(q, k, v, log_decay, cu_seqlens, *, state_cache, state_indices,
     their own are taken as they are), H a multiple of Hqk; ``log_decay`` is fp32
     [H], or [1, T, H] for a decay of each token.  ``scale`` defaults to
     128 ** -0.5.  Prompts, ragged batches and single tokens go in one call; the
-    pool arguments are those of ``chunk_fwd``.  Writes ``out`` and the selected
-    pool slots in place and returns ``out``."""
+    pool arguments are those of ``chunk_fwd``.  ``workspace`` (uint8, at least
+    ``lin_attn_workspace_size`` bytes; one for each stream) saves the call its
+    allocation, about 5 us of the 20 that a call takes on the host.  Writes ``out``
+    and the selected pool slots in place and returns ``out``."""
     lib = load_library()
     bf16, dev = torch.bfloat16, q.device
-    at = q.get_device()
+    at = q.get_device()  # -1 without a GPU
     qs, vs, ps, gs = q.shape, v.shape, state_cache.shape, log_decay.shape
+    (_, q_st, q_sh, q_1), (_, k_st, k_sh, k_1), (_, v_st, v_sh, v_1), (p_st, *plane) = (
+        x.stride() if x.dim() == 4 else (0, 0, 0, 0) for x in (q, k, v, state_cache))
     N = cu_seqlens.numel() - 1
     hs = has_initial_state
     # One look at the usual forms; _lin_args looks at each argument, takes the others and
     # says what is wrong.
-    if (len(qs) == len(vs) == 4 and qs[0] == vs[0] == 1 and qs[3] == vs[3] == 128
+    if (at >= 0 and q_1 == k_1 == v_1 == 1 and plane == [16384, 128, 1]
+            and qs[0] == vs[0] == 1 and qs[3] == vs[3] == 128
             and qs[1] == vs[1] and k.shape == qs and qs[2] > 0 and vs[2] % qs[2] == 0
             and q.dtype is k.dtype is v.dtype is out.dtype is bf16
-            and q.is_cuda and k.is_cuda and v.is_cuda and out.is_cuda
-            and k.get_device() == v.get_device() == out.get_device() == at
+            and k.get_device() == v.get_device() == out.get_device() == log_decay.get_device()
+            == cu_seqlens.get_device() == state_indices.get_device() == hs.get_device()
+            == state_cache.get_device() == at
             and out.shape == vs and out.is_contiguous()
-            and log_decay.dtype is torch.float32 and log_decay.is_cuda
-            and log_decay.get_device() == at and log_decay.is_contiguous()
+            and log_decay.dtype is torch.float32 and log_decay.is_contiguous()
             and (gs == vs[2:3] or gs == vs[:3])
             and cu_seqlens.dtype is state_indices.dtype is torch.int32
-            and cu_seqlens.is_cuda and cu_seqlens.get_device() == at and cu_seqlens.dim() == 1
-            and N >= 0 and cu_seqlens.is_contiguous()
-            and state_indices.is_cuda and state_indices.get_device() == at
+            and cu_seqlens.dim() == 1 and N >= 0 and cu_seqlens.is_contiguous()
             and state_indices.numel() == N and state_indices.is_contiguous()
-            and (hs.dtype is torch.bool or hs.dtype is torch.uint8) and hs.is_cuda
-            and hs.get_device() == at and hs.numel() == N and hs.is_contiguous()
-            and state_cache.dtype in STATE_DTYPES and state_cache.is_cuda
-            and state_cache.get_device() == at and len(ps) == 4 and ps[1] == vs[2]
-            and ps[2] == ps[3] == 128 and state_cache.stride()[1:] == (16384, 128, 1)
-            and q.stride(3) == k.stride(3) == v.stride(3) == 1):
-        T, Hk, H = qs[1], qs[2], vs[2]
-        strides = []
-        for x, heads in ((q, Hk), (k, Hk), (v, H)):
-            st = x.stride()
-            strides += (st[1] if T > 1 else heads * 128, st[2] if heads > 1 else 128)
-        q_st, q_sh, k_st, k_sh, v_st, v_sh = strides
+            and hs.dtype in _FLAGS and hs.numel() == N and hs.is_contiguous()
+            and state_cache.dtype in STATE_DTYPES and ps[1] == vs[2] and ps[2] == ps[3] == 128):
+        _, T, Hk, _ = qs
+        H = vs[2]
+        if T == 1:  # the stride of a dimension of one entry says nothing
+            q_st = k_st = Hk * 128
+            v_st = H * 128
+        if Hk == 1:
+            q_sh = k_sh = 128
+        if H == 1:
+            v_sh = 128
     else:
         T, Hk, H, N, (q_st, q_sh, k_st, k_sh, v_st, v_sh) = _lin_args(
             q, k, v, log_decay, cu_seqlens, state_cache, state_indices, hs, out)
     host = None if cu_seqlens_cpu is None else _host_int32(cu_seqlens_cpu, N)
     need = lin_attn_workspace_size(T, N, H)
     if workspace is None:
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+        workspace = _empty(max(need, 256), torch.uint8, dev, stream)
         given = need
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {dev}")
@@ -148,7 +160,7 @@ def lin_attn_fwd(q, k, v, log_decay, cu_seqlens, *, state_cache, state_indices,
         q.data_ptr(), q_st, q_sh, k.data_ptr(), k_st, k_sh, v.data_ptr(), v_st, v_sh,
         log_decay.data_ptr(), len(gs) > 1, cu_seqlens.data_ptr(),
         None if host is None else host.data_ptr(), N, T, H, Hk,
-        state_cache.data_ptr(), state_cache.stride(0), ps[0],
+        state_cache.data_ptr(), p_st, ps[0],
         state_indices.data_ptr(), hs.data_ptr(), out.data_ptr(),
         0.08838834764831845 if scale is None else float(scale), STATE_DTYPES[state_cache.dtype],
         workspace.data_ptr(), given, _stream(stream, dev))
@@ -189,7 +201,7 @@ def _lin_args(q, k, v, log_decay, cu_seqlens, state_cache, state_indices, hs, ou
         raise ValueError("each slot plane of state_cache must be dense (only stride(0) may pad)")
     if state_indices.dtype != torch.int32 or not state_indices.is_cuda:
         raise TypeError("state_indices must be an int32 CUDA tensor")
-    if hs.dtype not in (torch.bool, torch.uint8) or not hs.is_cuda:
+    if hs.dtype not in _FLAGS or not hs.is_cuda:
         raise TypeError("has_initial_state must be a bool/uint8 CUDA tensor")
     _per_sequence(state_indices, "state_indices", N)
     _per_sequence(hs, "has_initial_state", N)
@@ -309,7 +321,7 @@ def gated_norm(x, weight=None, *, gate=None, activation: str = "sigmoid", eps: f
         raise TypeError(f"x dtype {x.dtype} not supported")
     T, H, D, x_st, x_sh = _rows(x, "x")
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = _empty(x.shape, x.dtype, x.device, stream)
     To, Ho, Do, o_st, o_sh = _rows(out, "out", x.dtype)
     if (To, Ho, Do) != (T, H, D):
         raise ValueError("out must have the shape of x")

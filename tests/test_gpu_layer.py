@@ -70,3 +70,30 @@ def test_between_the_projections(heads, qk_heads, state_dtype):
         assert example.difference(by_token[i], at_once[i]) < 3 * 2.0 ** -8 + 2 * round_pool
         assert example.difference(states[i], S[0]) < 2.0 ** -8 + round_pool
         assert example.difference(layer.pool[i], S[0]) < 2.0 ** -8 + round_pool
+
+
+def test_memory_made_by_a_call_belongs_to_its_stream(monkeypatch):
+    """Workspace and output that a call makes for itself come from the pool of the stream
+    it runs on, so that they are not given out again while it runs."""
+    s = torch.cuda.Stream()
+    made, empty = [], torch.empty
+
+    def spy(*args, **kw):
+        made.append(torch.cuda.current_stream())
+        return empty(*args, **kw)
+
+    q = torch.randn(1, 5, 2, D, device="cuda").bfloat16()
+    pool = torch.zeros(1, 2, D, D, device="cuda")
+    cu, idx = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([0, 5], [0]))
+    out = torch.empty_like(q)
+    torch.cuda.synchronize()
+    monkeypatch.setattr(torch, "empty", spy)
+    example.kda.lin_attn_fwd(q, q, q, -torch.ones(2, device="cuda"), cu, state_cache=pool, state_indices=idx,
+                             has_initial_state=idx.bool(), out=out,
+                             cu_seqlens_cpu=torch.tensor([0, 5], dtype=torch.int32), stream=s)
+    example.kda.gated_norm(q, stream=s)
+    assert made == [s, s]
+    example.kda.gated_norm(q)
+    assert made[2:] == [torch.cuda.current_stream()]
+    monkeypatch.undo()
+    torch.cuda.synchronize()
