@@ -106,7 +106,7 @@ def lin_attn_fwd(q, k, v, log_decay, cu_seqlens, *, state_cache, state_indices,
     128 ** -0.5.  Prompts, ragged batches and single tokens go in one call; the
     pool arguments are those of ``chunk_fwd``.  ``workspace`` (uint8, at least
     ``lin_attn_workspace_size`` bytes; one for each stream) saves the call its
-    allocation, about 5 us of the 20 that a call takes on the host.  Writes ``out``
+    allocation, about 5 us of the 18 that a call takes on the host.  Writes ``out``
     and the selected pool slots in place and returns ``out``."""
     lib = load_library()
     bf16, dev = torch.bfloat16, q.device

@@ -255,6 +255,24 @@ def test_bad_slots_are_reported():
     assert kda.check_status(ws) == 0
 
 
+def test_bad_slots_of_short_sequences_are_reported():
+    """Batches of short sequences alone write the status themselves, whatever it held."""
+    lengths = [1, 8, 0, 3] + [1] * 300
+    c = make(lengths, 2, seed=21, init=[1] * len(lengths))
+    ws = torch.full((kda.lin_attn_workspace_size(312, len(lengths), 2),), 255, dtype=torch.uint8, device="cuda")
+    good = c["idx"].clone()
+    for n, slot in ((0, -1), (2, 999), (303, len(lengths) + 2)):
+        c["idx"] = good.clone()
+        c["idx"][n] = slot
+        before = c["storage"].clone()
+        run(c, workspace=ws)
+        assert kda.check_status(ws) == kda.STATUS_BAD_SLOT
+        c["storage"].copy_(before)
+        c["idx"] = good
+        run(c, workspace=ws)
+        assert kda.check_status(ws) == 0
+
+
 def test_on_another_stream_and_captured():
     c, d = (make([260, 1, 12], 2, seed=17, decay="token") for _ in range(2))
     want = run(c)
