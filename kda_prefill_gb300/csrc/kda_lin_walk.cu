@@ -439,7 +439,9 @@ __device__ __forceinline__ void decay_role(const LinParams& p, const LinCuts& cu
     for (int it = 0;; ++it) {
         if (it >= kItems && !x.wait_all(kItemEmpty + it % kItems, ((it / kItems) + 1) & 1)) return;
         int i = blockIdx.x;  // the first item by place, the others in the order of their claims
-        if (it > 0) {
+        if (it > 0 && n_items <= (int)gridDim.x) {
+            i = n_items;
+        } else if (it > 0) {
             if (x.lane == 0) i = gridDim.x + atomicAdd(queue, 1);
             i = __shfl_sync(0xffffffffu, i, 0);
         }
@@ -1015,7 +1017,6 @@ __device__ __forceinline__ void state_role(const Maps& maps, const LinParams& p,
         // this lane's 4 columns of the warp's rows half, half + 2, ...
         const int slot = Local ? 0 : p.idx[item.n];
         const bool ok = slot >= 0 && slot < p.num_slots;
-        if (!Local && !ok && threadIdx.x == 0) atomicOr(p.status, 4);
         P* pool = static_cast<P*>(p.pool) + (ok ? (size_t)slot * p.stride0 : 0) +
                   ((size_t)item.h * D + 32 * (warp & 3) + half) * D + 64 * sg + 4 * l16;
         // a segment's state in the workspace: this thread's 4 columns 4 e .. every 256 x 4 values
@@ -1149,7 +1150,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_lin_walk(const __grid_constan
     uint32_t* slot = reinterpret_cast<uint32_t*>(smem + kSmMisc);
     x.abort = reinterpret_cast<volatile int*>(smem + kSmMisc + 4);
     if ((smem_u32(smem) & 1023) != 0) {  // swizzled tiles need 1 KB alignment
-        if (threadIdx.x == 0) atomicOr(p.status, 2);
+        if (threadIdx.x == 0) *p.status = 2;
         return;
     }
     if (threadIdx.x < kNumBars) {
@@ -1205,6 +1206,8 @@ __global__ void __launch_bounds__(kThreads, 1) kda_lin_walk(const __grid_constan
             if (x.lane == 0) issued = load_role<Local>(maps, p, x);
         } else if (warp == 30) {
             decay_role<Local>(p, cuts, x);
+        } else if (blockIdx.x == 0 && (Local || p.n_cut == 0)) {
+            write_status(p, x.lane);
         }
     }
     __syncwarp();
@@ -1377,14 +1380,16 @@ template <class P>
 cudaError_t launch(const Maps& maps, const LinParams& p, const LinCuts& cuts, cudaStream_t s) {
     cudaError_t e = cudaSuccess;
     const bool cut = p.n_cut > 0;
-    if (cut) {
+    const int64_t items = (int64_t)(p.n_seg + p.n_long - p.n_cut) * p.H;  // Local has fewer
+    if (items > num_sms()) e = cudaMemsetAsync(p.status, 0, kWsClearBytes, s);  // the queues
+    if (cut && e == cudaSuccess) {
         // the segments' states do not depend on the pool's type
         e = launch_one<float, true>(false, maps, p, cuts, (int64_t)(p.n_seg - p.n_cut) * p.H, s);
         if (e == cudaSuccess)
             e = launch_chain<P>(p, cuts, s);
     }
     if (e == cudaSuccess)
-        e = launch_one<P, false>(cut, maps, p, cuts, (int64_t)(p.n_seg + p.n_long - p.n_cut) * p.H, s);
+        e = launch_one<P, false>(cut, maps, p, cuts, items, s);
     return e;
 }
 

@@ -56,6 +56,23 @@ struct LinParams {
     int st_dtype;
 };
 
+#ifdef __CUDACC__
+// The call's status word, by one warp of the first CTA of its first kernel, whichever that
+// is: whether a sequence's slot is outside the pool.  So nothing has to clear the word
+// before (a memset ahead of the kernel: 512 single tokens x 12 heads 123.2 us instead of
+// 121.5).
+__device__ __forceinline__ void write_status(const LinParams& p, int lane) {
+    bool bad = false;
+#pragma unroll 4
+    for (int i = lane; i < p.N; i += 32) {
+        const int slot = p.idx[i];
+        bad |= slot < 0 || slot >= p.num_slots;
+    }
+    bad = __any_sync(0xffffffffu, bad);
+    if (lane == 0) *p.status = bad ? 4 : 0;
+}
+#endif
+
 // Values below kMinDecay give exp() == 0 in fp32; the clamp keeps sums of them finite.
 constexpr float kMinDecay = -104.f;
 

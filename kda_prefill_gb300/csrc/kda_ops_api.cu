@@ -75,12 +75,7 @@ int enqueue_lin(void* arg, const kda::SeqTables& t) {
     p.n_short = t.n_short;
     kda::LinCuts cuts;
     kda::lin_cut(p, cuts, t);
-    cudaError_t e = cudaSuccess;
-    if (p.n_long > 0) {  // the walk's counters, too; alone, the step kernel writes the status
-        e = cudaMemsetAsync(p.status, 0, kda::kWsClearBytes, c.stream);
-        if (e != cudaSuccess) return cuda_error(e, "cudaMemsetAsync (status)");
-    }
-    e = kda::launch_lin_walk(p, cuts, c.stream);
+    cudaError_t e = kda::launch_lin_walk(p, cuts, c.stream);
     if (e == cudaSuccess) e = kda::launch_lin_step(p, p.n_long > 0, c.stream);
     return e == cudaSuccess ? KDA_OK : cuda_error(e, "kernel launch");
 }

@@ -273,6 +273,26 @@ def test_bad_slots_of_short_sequences_are_reported():
         assert kda.check_status(ws) == 0
 
 
+@pytest.mark.parametrize("lengths", [[1500, 3], [40, 50], [20] * 200 + [1]])
+def test_bad_slots_of_long_sequences_are_reported(lengths):
+    """Cut, in one wave of CTAs and in several, whatever the status word held."""
+    c = make(lengths, 2, seed=22, init=[1] * len(lengths))
+    ws = torch.full((kda.lin_attn_workspace_size(sum(lengths), len(lengths), 2),), 255, dtype=torch.uint8,
+                    device="cuda")
+    good = c["idx"].clone()
+    for n in (0, len(lengths) - 1):
+        c["idx"] = good.clone()
+        c["idx"][n] = -1
+        before = c["storage"].clone()
+        run(c, workspace=ws)
+        assert kda.check_status(ws) == kda.STATUS_BAD_SLOT
+        c["storage"].copy_(before)
+        c["idx"] = good
+        want = expected(c)
+        check(c, run(c, workspace=ws), want, before)
+        assert kda.check_status(ws) == 0
+
+
 def test_on_another_stream_and_captured():
     c, d = (make([260, 1, 12], 2, seed=17, decay="token") for _ in range(2))
     want = run(c)
