@@ -1396,13 +1396,15 @@ cudaError_t launch(const Maps& maps, const LinParams& p, const LinCuts& cuts, cu
 // How the longest sequences are cut, from the long sequences' lengths (longest first).
 // Uncut, the walk takes as long as its longest sequence or as all chunks shared out,
 // whichever is more.  Cut, a segment's walk has to wait for the states of those before it,
-// which are made first from k and v alone, in about half of a walk's time; a few chunks'
-// time goes into the two more launches and the states' way through memory.  The segments
-// are as long as lets one wave of CTAs take all items, or, where there are more sequences
-// than that, as an even share of the chunks.  Cut and uncut, 12 heads: 29.2 and 36.9 us for
-// 1024 tokens, 30.6 and 61.6 us for 2048, 38.9 and 116 us for 4097, 80.6 and 412 us for
-// 16384; 118.5 and 122.8 us for four of 2048 beside 512 of one token; 768 tokens stay
-// uncut, 30.8 us.
+// which are made first from k and v alone, in about half of a walk's time; `start` chunks'
+// time goes into the two more launches and the states' way through memory, more of it the
+// more states there are.  The segments are as long as lets one wave of CTAs take all
+// items, or, where there are more sequences than that, as an even share of the chunks.
+// Cut and uncut, 12 heads: 24.6 and 26.6 us for 640 tokens, 24.6 and 32.8 us for 896, 28.7
+// and 60.8 us for 2048, 37.3 and 115 us for 4097, 80.0 and 410 us for 16384; 28.4 and 32.8
+// us for two of 896; 117.4 and 122.0 us for four of 2048 beside 512 of one token.  Left
+// uncut: 512 tokens (22.6 us, cut 26.6), four of 640 (26.7 us, cut 32.6), four of 1024
+// (36.9 us, cut 37.9), six of 900 to 1600 (51.6 us, cut 54.1).
 struct Cut {
     int seg_len = 0, n_cut = 0, n_seg = 0;
 };
@@ -1428,7 +1430,8 @@ Cut cut_rule(const int32_t* lens, int n, int H, int sms) {
         }
     }
     if (seg < 2) seg = 2;
-    if (longest <= seg + (seg + 1) / 2 + 4) return cut;
+    const int64_t pairs = (int64_t)n * H, start = pairs < 48 ? 1 + pairs / 16 : 4;
+    if (longest < kLinMinCut || longest <= seg + (seg + 1) / 2 + start) return cut;
     cut.seg_len = seg * C;
     for (; cut.n_cut < n && chunks_of(lens[cut.n_cut]) > seg; ++cut.n_cut)
         cut.n_seg += (chunks_of(lens[cut.n_cut]) + seg - 1) / seg;

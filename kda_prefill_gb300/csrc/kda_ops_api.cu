@@ -86,8 +86,7 @@ extern "C" {
 
 size_t kda_lin_attn_workspace_size(int64_t total_tokens, int32_t num_seqs, int32_t num_heads) {
     if (total_tokens < 0 || num_seqs <= 0 || num_heads <= 0) return 0;
-    // no sequence is cut below seven chunks
-    if (total_tokens <= 6 * 128) return kda::kWsHeader;
+    if (total_tokens <= (kda::kLinMinCut - 1) * 128) return kda::kWsHeader;  // nothing is cut
     return kda::kWsHeader + (size_t)kda::kLinPlanes * (kda::kD * kda::kD + 64) * sizeof(float);
 }
 

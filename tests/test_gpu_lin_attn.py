@@ -134,6 +134,14 @@ def test_cut_sequences(lengths, H, decay):
                        init=[i % 2 == 0 for i in range(len(lengths))]))
 
 
+@pytest.mark.parametrize("lengths", [[512], [513], [641], [767], [769], [897], [640, 640], [897, 800], [700, 1100, 513]])
+@pytest.mark.parametrize("H", [1, 12])
+def test_shortest_cut_sequences(lengths, H):
+    """Around the lengths from which sequences are cut, for few and more heads."""
+    run_and_check(make(lengths, H, 1, decay="token", seed=sum(lengths),
+                       init=[i % 2 == 0 for i in range(len(lengths))]))
+
+
 def test_cut_sequences_extreme_decays():
     gen = torch.Generator().manual_seed(3)
     g = -0.01 * torch.rand(1, 3333, 2, generator=gen)
