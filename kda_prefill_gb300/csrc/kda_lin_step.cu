@@ -9,8 +9,8 @@
 // halving butterfly.  The next token's values are read while one is worked on.  For single
 // tokens the state's two trips through memory are the bound: 512 tokens x 12 heads with
 // fp32 states take 121.5 us, 98 % of a plain copy's rate.  Further tokens are bound by
-// instructions, about 20 us each there: 512 sequences of 8 tokens take 266 us, as long as
-// the chunk kernel takes for 9 (257 us), which is where the two change over.
+// instructions, about 20 us each there: 512 sequences of 8 tokens take 260 us, as long as
+// the chunk kernel takes for 9 (256 us), which is where the two change over.
 
 #include "kda_ops.h"
 #include "kda_rows.cuh"

@@ -20,14 +20,14 @@
 // The products are the bound: 72 of 128 x 128 x 16, 64 cycles each, 4.6 K cycles a chunk,
 // of which the tensor pipe reaches about three quarters while it shares shared and tensor
 // memory with the operands' makers (6.2 K cycles a chunk; 128 sequences of 117,555 tokens
-// x 12 heads: 323 us, tensor pipe active 62 % of the time, 46 % of the memory's rate).
+// x 12 heads: 319 us, tensor pipe active 62 % of the time, 46 % of the memory's rate).
 // Chunks of 128 fill the products' M: with 64, q S^T would run at half rate, and S would
 // be read, rounded and written as an operand twice as often.
 //
 // A few long sequences would leave most SMs idle.  They are cut into segments: a first
 // launch makes each segment's state from zero (Local), kda_lin_chain the states that the
 // segments start from, and the walk takes them as items.  1 x 16384 tokens x 12 heads:
-// 80.6 us (26 Local, 52 the walk), 412 us uncut.
+// 80.0 us (26 Local, 52 the walk), 410 us uncut.
 //
 // Rounding.  Operands are bf16.  q, k and v are; P and S are carried as a sum of
 // two bf16 (16 bits: with one, a rounding as large as out's own would be added
