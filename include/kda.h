@@ -393,7 +393,7 @@ enum kda_dtype { KDA_F32 = 0, KDA_BF16 = 1, KDA_F16 = 2 };
  * in the state), one in q its own token's row.
  *
  * Where few long sequences would leave SMs idle they are worked on in segments
- * at once, through about 20 MB of the workspace (part of its size beyond 512
+ * at once, through about 20 MB of the workspace (part of its size beyond 256
  * tokens).
  *
  * Graph capture, synchronisation and bounds follow kda_chunk_fwd.

@@ -27,7 +27,7 @@
 // A few long sequences would leave most SMs idle.  They are cut into segments: a first
 // launch makes each segment's state from zero (Local), kda_lin_chain the states that the
 // segments start from, and the walk takes them as items.  1 x 16384 tokens x 12 heads:
-// 80.0 us (26 Local, 52 the walk), 410 us uncut.
+// 79.8 us (26 Local, 52 the walk), 410 us uncut.
 //
 // Rounding.  Operands are bf16.  q, k and v are; P and S are carried as a sum of
 // two bf16 (16 bits: with one, a rounding as large as out's own would be added
@@ -1400,11 +1400,12 @@ cudaError_t launch(const Maps& maps, const LinParams& p, const LinCuts& cuts, cu
 // time goes into the two more launches and the states' way through memory, more of it the
 // more states there are.  The segments are as long as lets one wave of CTAs take all
 // items, or, where there are more sequences than that, as an even share of the chunks.
-// Cut and uncut, 12 heads: 24.6 and 26.6 us for 640 tokens, 24.6 and 32.8 us for 896, 28.7
-// and 60.8 us for 2048, 37.3 and 115 us for 4097, 80.0 and 410 us for 16384; 28.4 and 32.8
-// us for two of 896; 117.4 and 122.0 us for four of 2048 beside 512 of one token.  Left
-// uncut: 512 tokens (22.6 us, cut 26.6), four of 640 (26.7 us, cut 32.6), four of 1024
-// (36.9 us, cut 37.9), six of 900 to 1600 (51.6 us, cut 54.1).
+// Cut and uncut, 12 heads: 22.6 and 26.6 us for 640 tokens, 22.6 and 32.8 us for 896, 28.7
+// and 60.8 us for 2048, 37.2 and 115 us for 4097, 79.8 and 410 us for 16384; 27.5 and 32.8
+// us for two of 896; 117.0 and 122.0 us for four of 2048 beside 512 of one token.  Two
+// heads: 18.5 and 22.6 us for 512 tokens.  Left uncut, 12 heads: 384 tokens (20.5 us, cut
+// 22.6), three of 768 (28.7 us, cut 29.6), four of 640 (26.7 us, cut 32.6), four of 1024
+// (36.9 us, cut 37.9), six of 900 to 1600 (51.3 us, cut 54.1).
 struct Cut {
     int seg_len = 0, n_cut = 0, n_seg = 0;
 };
@@ -1429,8 +1430,7 @@ Cut cut_rule(const int32_t* lens, int n, int H, int sms) {
             if (items(mid) <= sms) hi = mid; else seg = mid + 1;
         }
     }
-    if (seg < 2) seg = 2;
-    const int64_t pairs = (int64_t)n * H, start = pairs < 48 ? 1 + pairs / 16 : 4;
+    const int64_t pairs = (int64_t)n * H, start = pairs < 52 ? (pairs + 12) / 16 : 4;
     if (longest < kLinMinCut || longest <= seg + (seg + 1) / 2 + start) return cut;
     cut.seg_len = seg * C;
     for (; cut.n_cut < n && chunks_of(lens[cut.n_cut]) > seg; ++cut.n_cut)

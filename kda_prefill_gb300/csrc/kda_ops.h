@@ -79,7 +79,7 @@ constexpr float kMinDecay = -104.f;
 // Segment states a call's workspace holds: a cut needs at most two for each SM.
 constexpr int kLinPlanes = 2 * 152;
 // Chunks of 128 tokens of the shortest sequence that is cut.
-constexpr int kLinMinCut = 5;
+constexpr int kLinMinCut = 3;
 // The cut sequences, by value in the kernels' parameters: of sequence seq[r], which has
 // len[r] tokens from t0[r] on, the segments are first[r] .. first[r + 1] - 1.
 constexpr int kLinCuts = kLinPlanes / 2;

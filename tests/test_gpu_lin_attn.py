@@ -134,7 +134,7 @@ def test_cut_sequences(lengths, H, decay):
                        init=[i % 2 == 0 for i in range(len(lengths))]))
 
 
-@pytest.mark.parametrize("lengths", [[512], [513], [641], [767], [769], [897], [640, 640], [897, 800], [700, 1100, 513]])
+@pytest.mark.parametrize("lengths", [[257], [384], [385, 20], [512], [513], [641], [767], [769], [897], [640, 640], [897, 800], [700, 1100, 513]])
 @pytest.mark.parametrize("H", [1, 12])
 def test_shortest_cut_sequences(lengths, H):
     """Around the lengths from which sequences are cut, for few and more heads."""
