@@ -39,10 +39,14 @@
 // every chunk and S' is formed in fp32 registers, so that S is rounded once a
 // chunk however the tensor cores round their partial sums.
 //
-// Decays of scores.  In the 32 x 32 blocks on the diagonal e^{G_i - G_j} is taken
-// as it stands.  Left of them it is e^{G_i - G_b} e^{G_b - G_j}, b the last token of
-// column j's block: both factors are at most one, the first is one a row and block
-// and the second one a token, so neither overflows and few exponentials are left.
+// Decays of scores.  G_i - G_j is a sum of the decays between the two and is made as one:
+// a difference of sums over the chunk would lose the bits of weak decays behind strong
+// ones (32 tokens of -0.01 behind 96 of -inf: off by 1.4e-3).  In the 32 x 32 blocks on
+// the diagonal the sum grows token by token from the row to the left.  Left of them
+// e^{G_i - G_j} is e^{G_i - G_b} e^{G_b - G_j}, b the last token of column j's block: both
+// factors are at most one, the first is one a row and block and the second one a token,
+// so neither overflows and few exponentials are left; G_i - G_b is the row's sum within
+// its block and whole blocks' sums.
 //
 // Infinities and NaN.  A masked score is a zero by selection, but a zero times an
 // infinite v is NaN: P v would carry it to the chunk's earlier tokens.  The W
@@ -76,8 +80,9 @@ constexpr int kItems = 3;         // items the claims run ahead
 constexpr int kSmS = 0;                        // S as bf16: high part, then low part
 constexpr int kSmTile = 2 * kTile;
 constexpr int kSmW = kSmTile + kSlots * kTile;  // [2][64] e^R of token pairs, each in three parts
-constexpr int kSmG = kSmW + 2 * (C / 2) * 12;   // [128] G, prefix sums in log2
-constexpr int kSmCf = kSmG + C * 4;             // [96] e^{G_b - G_j}
+constexpr int kSmA = kSmW + 2 * (C / 2) * 12;   // [128] decays in log2
+constexpr int kSmT = kSmA + C * 4;              // [4] their sums over each 32 tokens
+constexpr int kSmCf = kSmT + 16;                // [96] e^{G_b - G_j}
 struct Item {
     int t0, len, h, n, flags;
     int plane;  // of the workspace: the segment's state
@@ -92,7 +97,7 @@ enum Bar {
     kEmpty = kFull + kLocalSlots,    // [7] tile consumed
     kDecFull = kEmpty + kLocalSlots, // [2] weights and e^{G_C} of a chunk made
     kDecEmpty = kDecFull + 2,   // [2] and read
-    kGFull = kDecEmpty + 2,     // G and the factors of score columns made
+    kGFull = kDecEmpty + 2,     // decays, their sums and the factors of score columns made
     kGEmpty,                    // and read
     kItemFull,                  // [3] item claimed
     kItemEmpty = kItemFull + kItems,
@@ -117,7 +122,7 @@ constexpr int kSmMisc = kSmBad + 64;             // tensor-memory base, abort fl
 constexpr int kSmRows = kSmMisc + 8;             // warps done with a chunk's output rows
 constexpr int kSmemBytes = kSmRows + 8;
 static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
-static_assert(kSmG % 16 == 0 && kSmCf % 16 == 0 && kSmBad % 16 == 0, "read by 16 bytes");
+static_assert(kSmA % 16 == 0 && kSmT % 16 == 0 && kSmCf % 16 == 0 && kSmBad % 16 == 0, "read by 16 bytes");
 static_assert(kSmGamma % 8 == 0 && kSmMisc % 8 == 0 && kSmRows % 8 == 0, "words");
 
 // Tensor memory columns.
@@ -458,7 +463,7 @@ __device__ __forceinline__ void decay_role(const LinParams& p, const LinCuts& cu
         const float* g = p.g + item.h;
         for (int j = 0; j < chunks(item.len); ++j, ++c) {
             // four tokens a lane; tokens past the end decay nothing
-            float a[4], pre[4], suf[4];
+            float a[4], suf[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int t = j * C + 4 * x.lane + e;
@@ -466,24 +471,18 @@ __device__ __forceinline__ void decay_role(const LinParams& p, const LinCuts& cu
                 if (t < item.len) v = g[(int64_t)(item.t0 + t) * p.g_st];
                 a[e] = v < kMinDecay ? kMinDecay : v;
             }
-            pre[0] = a[0];
-#pragma unroll
-            for (int e = 1; e < 4; ++e) pre[e] = pre[e - 1] + a[e];
             suf[3] = 0.f;
 #pragma unroll
             for (int e = 2; e >= 0; --e) suf[e] = suf[e + 1] + a[e + 1];
-            float up = pre[3], down = pre[3];  // sums over the lanes up to here, from here on
+            const float sum = suf[0] + a[0];
+            float down = sum;  // over the lanes from here on
 #pragma unroll
             for (int w = 1; w < 32; w <<= 1) {
-                const float u = __shfl_up_sync(0xffffffffu, up, w);
                 const float d = __shfl_down_sync(0xffffffffu, down, w);
-                if (x.lane >= w) up += u;
                 if (x.lane + w < 32) down += d;
             }
-            const float total = __shfl_sync(0xffffffffu, up, 31);
-            float before = __shfl_up_sync(0xffffffffu, up, 1);
+            const float total = __shfl_sync(0xffffffffu, down, 0);
             float after = __shfl_down_sync(0xffffffffu, down, 1);
-            if (x.lane == 0) before = 0.f;
             if (x.lane == 31) after = 0.f;
             if (c >= 2 && !x.wait_all(kDecEmpty + (c & 1), ((c >> 1) + 1) & 1)) return;
             uint32_t* w = const_cast<uint32_t*>(x.weights(c)) + 6 * x.lane;
@@ -499,19 +498,20 @@ __device__ __forceinline__ void decay_role(const LinParams& p, const LinCuts& cu
             if (x.lane == 0) x.arrive(kDecFull + (c & 1));
             if (Local) continue;
             // the sums from here to the end of each 32 tokens (eight lanes)
-            float rest = pre[3];
+            float rest = sum;
 #pragma unroll
             for (int w = 1; w < 8; w <<= 1) {
                 const float d = __shfl_down_sync(0xffffffffu, rest, w, 8);
                 if ((x.lane & 7) + w < 8) rest += d;
             }
+            const float sum32 = rest;  // of the eight lanes, in their first one
             rest = __shfl_down_sync(0xffffffffu, rest, 1, 8);
             if ((x.lane & 7) == 7) rest = 0.f;
             if (c > 0 && !x.wait_all(kGEmpty, (c + 1) & 1)) return;
             constexpr float kLog2e = 1.4426950408889634f;
-            reinterpret_cast<float4*>(x.smem + kSmG)[x.lane] =
-                make_float4((before + pre[0]) * kLog2e, (before + pre[1]) * kLog2e,
-                            (before + pre[2]) * kLog2e, (before + pre[3]) * kLog2e);
+            reinterpret_cast<float4*>(x.smem + kSmA)[x.lane] =
+                make_float4(a[0] * kLog2e, a[1] * kLog2e, a[2] * kLog2e, a[3] * kLog2e);
+            if ((x.lane & 7) == 0) reinterpret_cast<float*>(x.smem + kSmT)[x.lane >> 3] = sum32 * kLog2e;
             if (x.lane < 24)
                 reinterpret_cast<float4*>(x.smem + kSmCf)[x.lane] =
                     make_float4(expf(rest + suf[0]), expf(rest + suf[1]), expf(rest + suf[2]), expf(rest + suf[3]));
@@ -682,21 +682,33 @@ __device__ __forceinline__ void score_role(const LinParams& p, const Ctx& x, int
     const int w = w8 & 3, odd = w8 >> 2;
     const int row = 32 * w + x.lane;
     const uint32_t tm = x.tmem + ((uint32_t)(32 * w) << 16) + kTmX + 16 * odd;
-    const float* G = reinterpret_cast<const float*>(x.smem + kSmG);
+    const float* A = reinterpret_cast<const float*>(x.smem + kSmA);
+    const float* T = reinterpret_cast<const float*>(x.smem + kSmT);
     const float2* cf = reinterpret_cast<const float2*>(x.smem + kSmCf) + 8 * odd;
     int c = 0;
     Item item;
     for (int it = 0; x.item(it, &item, true); ++it) {
         for (int j = 0; j < chunks(item.len); ++j, ++c) {
-            if (!x.wait_all(kGFull, c & 1, kXFull, c & 1)) return;
-            const float gi = G[row];
+            // The decays are there long before the scores.  Their sums up to this row from the
+            // first token of its 16, and from that of its 32.
+            if (!x.wait_all(kGFull, c & 1)) return;
+            float from16 = A[row];
+#pragma unroll
+            for (int u = 1; u < 16; u <<= 1) {
+                const float up = __shfl_up_sync(0xffffffffu, from16, u, 16);
+                if ((x.lane & 15) >= u) from16 += up;
+            }
+            const float first16 = __shfl_sync(0xffffffffu, from16, 15);
+            float left = x.lane & 16 ? first16 + from16 : from16;
+            if (!x.wait_all(kXFull, c & 1)) return;
             tc_fence_after();
-            // Sixteen scores become eight pairs of high parts and eight of low parts, in place.
+            // Sixteen scores become eight pairs of high parts and eight of low parts, in place,
+            // the last columns first.
             uint32_t r[16];
             auto split_and_store = [&](int b, auto factor) {
                 uint32_t o[16];
 #pragma unroll
-                for (int e = 0; e < 16; e += 2) {
+                for (int e = 14; e >= 0; e -= 2) {
                     f2 v = mul2(pack2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), factor(e));
                     o[e / 2] = take_bf(v);
                     o[8 + e / 2] = last_bf(v);
@@ -704,9 +716,10 @@ __device__ __forceinline__ void score_role(const LinParams& p, const Ctx& x, int
                 tmem_st16(tm + 32 * b, o);
             };
 #pragma unroll 1
-            for (int b = 0; b < w; ++b) {
+            for (int b = w - 1; b >= 0; --b) {
                 tmem_ld16u(tm + 32 * b, r);
-                const float f = ex2(gi - G[32 * b + 31]);
+                const float f = ex2(left);
+                left += T[b];
                 const f2 ff = pack2(f, f);
                 tmem_wait_ld();
                 split_and_store(b, [&](int e) {
@@ -715,15 +728,20 @@ __device__ __forceinline__ void score_role(const LinParams& p, const Ctx& x, int
                 });
             }
             tmem_ld16u(tm + 32 * w, r);
-            const float2* Gw = reinterpret_cast<const float2*>(G + 32 * w + 16 * odd);
+            const float2* Aw = reinterpret_cast<const float2*>(A + 32 * w + 16 * odd);
             const int last = x.lane - 16 * odd;  // of this row, in the group
+            float d = last > 15 ? from16 : 0.f;
             tmem_wait_ld();
 #pragma unroll
             for (int e = 0; e < 16; ++e)
                 if (e > last) r[e] = 0u;
             split_and_store(w, [&](int e) {
-                const float2 u = Gw[e / 2];
-                return pack2(ex2(e > last ? 0.f : gi - u.x), ex2(e + 1 > last ? 0.f : gi - u.y));
+                const float2 u = Aw[e / 2];
+                const float f1 = ex2(d);
+                if (e + 1 <= last) d += u.y;
+                const float f0 = ex2(d);
+                if (e <= last) d += u.x;
+                return pack2(f0, f1);
             });
             const uint32_t zero[16] = {};
 #pragma unroll 1
@@ -750,7 +768,17 @@ __device__ __forceinline__ void out_role(const Maps& maps, const LinParams& p, c
         for (int j = 0; j < chunks(item.len); ++j, ++c) {
             const bool has_s = j > 0 || (item.flags & (kInit | kPlane));
             if (!x.wait_all(kGFull, c & 1)) return;
-            const float f = ex2(reinterpret_cast<const float*>(x.smem + kSmG)[row]);
+            float sum = reinterpret_cast<const float*>(x.smem + kSmA)[row];  // from the chunk's start on
+#pragma unroll
+            for (int u = 1; u < 32; u <<= 1) {
+                const float up = __shfl_up_sync(0xffffffffu, sum, u);
+                if (x.lane >= u) sum += up;
+            }
+            const float4 T = *reinterpret_cast<const float4*>(x.smem + kSmT);
+            if (w > 2) sum += T.z;
+            if (w > 1) sum += T.y;
+            if (w > 0) sum += T.x;
+            const float f = ex2(sum);
             __syncwarp();
             if (x.lane == 0) x.arrive(kGEmpty);
             if (has_s) {
