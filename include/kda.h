@@ -375,8 +375,9 @@ enum kda_dtype { KDA_F32 = 0, KDA_BF16 = 1, KDA_F16 = 2 };
  *                    multiples of 8, at least 128, bases 16-byte aligned.
  *   log_decay        device fp32 g, <= 0: [num_heads], or, with
  *                    decay_per_token, [total_tokens][num_heads] dense.  -inf
- *                    clears the state before the token's write; values below
- *                    -104 act as -inf does (exp underflows in fp32).
+ *                    clears the state before the token's write, whatever it
+ *                    held (infinities and NaN too); values below -104 act as
+ *                    -inf does (exp underflows in fp32).
  *   num_qk_heads     divides num_heads.
  *   scale            factor on the outputs (usually 1/sqrt(128)).
  *   cu_seqlens, cu_seqlens_host, state_cache ... has_initial_state, out,
@@ -390,7 +391,8 @@ enum kda_dtype { KDA_F32 = 0, KDA_BF16 = 1, KDA_F16 = 2 };
  * bounds, the head counts and the GPU's SM count alone.  A token's output depends on its own
  * sequence's tokens up to it alone, also where others hold infinities or NaN:
  * one in v makes its value column NaN or infinite from its token on (in out and
- * in the state), one in q its own token's row.
+ * in the state), one in k every column, until a token clears the state; one in q
+ * its own token's row.
  *
  * Where few long sequences would leave SMs idle they are worked on in segments
  * at once, through about 20 MB of the workspace (part of its size beyond 256

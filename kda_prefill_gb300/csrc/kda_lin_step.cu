@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(kWarps * 32, 8) kda_lin_step(const __grid_cons
         const bool slow = g > -0.5f;
         const float d = slow ? expm1f(g) : expf(g);
         const float one = slow ? 1.f : 0.f;
-        if (!slow && d == 0.f) {  // cleared, whatever it held
+        if (g < kMinDecay) {  // cleared, whatever it held
 #pragma unroll
             for (int r = 0; r < R; ++r)
 #pragma unroll

@@ -53,6 +53,15 @@
 // warps, which read all of v, therefore clear such values in the tile (W keeps
 // them: the state holds them from the chunk's end on), and the output warps put a
 // NaN into their columns from their token on.
+//
+// Clearing.  A decay below kMinDecay clears the state whatever it held, so nothing from
+// before it may be multiplied by its zero: the scores of a row with columns before its last
+// clearing token, q S^T of the rows from a chunk's first one on and S at the chunk's end
+// are zero by selection.  dS can take a NaN from a token before the last clearing one, its
+// weight being zero: where a cleared chunk's dS is not finite, the state warps sum the
+// tokens from that one on themselves.  Chunks without a clearing token only look at a flag,
+// and the rare work is out of line: inline it took registers of all (16384 tokens x 12
+// heads 96 us instead of 80 to 81).
 
 #include <type_traits>
 
@@ -82,7 +91,8 @@ constexpr int kSmTile = 2 * kTile;
 constexpr int kSmW = kSmTile + kSlots * kTile;  // [2][64] e^R of token pairs, each in three parts
 constexpr int kSmA = kSmW + 2 * (C / 2) * 12;   // [128] decays in log2
 constexpr int kSmT = kSmA + C * 4;              // [4] their sums over each 32 tokens
-constexpr int kSmCf = kSmT + 16;                // [96] e^{G_b - G_j}
+constexpr int kSmM = kSmT + 16;                 // [4] which of each 32 tokens clear the state
+constexpr int kSmCf = kSmM + 16;                // [96] e^{G_b - G_j}
 struct Item {
     int t0, len, h, n, flags;
     int plane;  // of the workspace: the segment's state
@@ -116,13 +126,13 @@ enum Bar {
     kDone,                      // everything issued has completed
     kNumBars
 };
-constexpr int kSmGamma = kSmBar + kNumBars * 8;  // [2] e^{G_C}
+constexpr int kSmGamma = kSmBar + kNumBars * 8;  // [2] e^{G_C}, or kClearing
 constexpr int kSmBad = (kSmGamma + 8 + 15) & ~15;  // [2][8] value columns with infinities or NaN
 constexpr int kSmMisc = kSmBad + 64;             // tensor-memory base, abort flag
 constexpr int kSmRows = kSmMisc + 8;             // warps done with a chunk's output rows
 constexpr int kSmemBytes = kSmRows + 8;
 static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
-static_assert(kSmA % 16 == 0 && kSmT % 16 == 0 && kSmCf % 16 == 0 && kSmBad % 16 == 0, "read by 16 bytes");
+static_assert(kSmA % 16 == 0 && kSmT % 16 == 0 && kSmM % 16 == 0 && kSmCf % 16 == 0 && kSmBad % 16 == 0, "read by 16 bytes");
 static_assert(kSmGamma % 8 == 0 && kSmMisc % 8 == 0 && kSmRows % 8 == 0, "words");
 
 // Tensor memory columns.
@@ -142,6 +152,9 @@ constexpr uint32_t kTmCols = 512;
 template <bool Local> __device__ __forceinline__ uint32_t ds_column(int c) { return Local && (c & 1) ? kTmO : kTmDS; }
 template <bool Local> __device__ __forceinline__ int ds_bar(int c) { return Local ? c & 1 : 0; }
 template <bool Local> __device__ __forceinline__ uint32_t ds_phase(int c) { return (Local ? c >> 1 : c) & 1; }
+
+// In place of a decay over tokens of which one clears the state.
+constexpr float kClearing = -1.f;
 
 constexpr uint32_t kIdescKK = mma_idesc(1, 0, 0, 128, 128);  // B K-major
 constexpr uint32_t kIdescKM = mma_idesc(1, 0, 1, 128, 128);  // B MN-major
@@ -372,6 +385,11 @@ struct Ctx {
     __device__ __forceinline__ const uint32_t* weights(int c) const {
         return reinterpret_cast<const uint32_t*>(smem + kSmW) + (c & 1) * 3 * (C / 2);
     }
+    // Whether the chunk whose decays are there has a clearing token.
+    __device__ __forceinline__ bool clears() const {
+        const uint4 m = *reinterpret_cast<const uint4*>(smem + kSmM);
+        return (m.x | m.y | m.z | m.w) != 0;
+    }
     __device__ __forceinline__ float gamma(int c) const {
         return reinterpret_cast<const float*>(smem + kSmGamma)[c & 1];
     }
@@ -386,6 +404,17 @@ struct Ctx {
     }
 };
 __device__ __forceinline__ int chunks(int len) { return (len + C - 1) / C; }
+// The last clearing token up to a row of the chunk, or -1.
+__device__ __forceinline__ int last_clearing(const uint4 m, int row) {
+    const uint32_t words[4] = {m.x, m.y, m.z, m.w};
+    int at = -1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t up_to = row < 32 * i ? 0u : row >= 32 * i + 31 ? ~0u : (2u << (row - 32 * i)) - 1u;
+        if (words[i] & up_to) at = 32 * i + 31 - __clz(words[i] & up_to);
+    }
+    return at;
+}
 
 // ---- warp 30: items and decays ------------------------------------------------
 // Item i of the call.  The cut sequences' segments come first; Local: all but their last.
@@ -464,12 +493,14 @@ __device__ __forceinline__ void decay_role(const LinParams& p, const LinCuts& cu
         for (int j = 0; j < chunks(item.len); ++j, ++c) {
             // four tokens a lane; tokens past the end decay nothing
             float a[4], suf[4];
+            uint32_t clear = 0;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int t = j * C + 4 * x.lane + e;
                 float v = 0.f;
                 if (t < item.len) v = g[(int64_t)(item.t0 + t) * p.g_st];
                 a[e] = v < kMinDecay ? kMinDecay : v;
+                clear |= v < kMinDecay ? 1u << e : 0u;
             }
             suf[3] = 0.f;
 #pragma unroll
@@ -493,7 +524,9 @@ __device__ __forceinline__ void decay_role(const LinParams& p, const LinCuts& cu
                 w[3 * u + 1] = take_bf(v);
                 w[3 * u + 2] = last_bf(v);
             }
-            if (x.lane == 0) reinterpret_cast<float*>(x.smem + kSmGamma)[c & 1] = expf(total);
+            const bool clears = __any_sync(0xffffffffu, clear != 0);
+            if (x.lane == 0)
+                reinterpret_cast<float*>(x.smem + kSmGamma)[c & 1] = clears ? kClearing : expf(total);
             __syncwarp();
             if (x.lane == 0) x.arrive(kDecFull + (c & 1));
             if (Local) continue;
@@ -505,13 +538,21 @@ __device__ __forceinline__ void decay_role(const LinParams& p, const LinCuts& cu
                 if ((x.lane & 7) + w < 8) rest += d;
             }
             const float sum32 = rest;  // of the eight lanes, in their first one
+            uint32_t clear32 = clear << (4 * (x.lane & 7));
+            if (clears) {
+#pragma unroll
+                for (int w = 1; w < 8; w <<= 1) clear32 |= __shfl_xor_sync(0xffffffffu, clear32, w);
+            }
             rest = __shfl_down_sync(0xffffffffu, rest, 1, 8);
             if ((x.lane & 7) == 7) rest = 0.f;
             if (c > 0 && !x.wait_all(kGEmpty, (c + 1) & 1)) return;
             constexpr float kLog2e = 1.4426950408889634f;
             reinterpret_cast<float4*>(x.smem + kSmA)[x.lane] =
                 make_float4(a[0] * kLog2e, a[1] * kLog2e, a[2] * kLog2e, a[3] * kLog2e);
-            if ((x.lane & 7) == 0) reinterpret_cast<float*>(x.smem + kSmT)[x.lane >> 3] = sum32 * kLog2e;
+            if ((x.lane & 7) == 0) {
+                reinterpret_cast<float*>(x.smem + kSmT)[x.lane >> 3] = sum32 * kLog2e;
+                reinterpret_cast<uint32_t*>(x.smem + kSmM)[x.lane >> 3] = clear32;
+            }
             if (x.lane < 24)
                 reinterpret_cast<float4*>(x.smem + kSmCf)[x.lane] =
                     make_float4(expf(rest + suf[0]), expf(rest + suf[1]), expf(rest + suf[2]), expf(rest + suf[3]));
@@ -658,10 +699,13 @@ __device__ __forceinline__ void mma_role(const Ctx& x) {
 }
 
 // Puts a NaN into the row's columns, of those in `cols`, where v holds an infinity or
-// NaN between tokens t0 and t1 of the item.
+// NaN between tokens t0 and t1 of the item, from the last clearing one on.
 __device__ __noinline__ void put_nonfinite(const LinParams& p, const Item& item, int t0, int t1, int row,
                                            uint4 cols, uint8_t* tile) {
     const uint16_t* v = reinterpret_cast<const uint16_t*>(p.v) + (int64_t)item.h * p.v_sh;
+#pragma unroll 1
+    for (int t = t1; t > t0; --t)
+        if (p.g[(int64_t)(item.t0 + t) * p.g_st + item.h] < kMinDecay) t0 = t;
 #pragma unroll 1
     for (int g = 0; g < 4; ++g)
 #pragma unroll 1
@@ -674,6 +718,23 @@ __device__ __noinline__ void put_nonfinite(const LinParams& p, const Item& item,
                     break;
                 }
         }
+}
+
+// Zeroes the scores of columns before the row's last clearing token, which may be NaN.
+__device__ __noinline__ void drop_scores(uint32_t tm, int warp) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const int w = warp & 3, n = last_clearing(*reinterpret_cast<const uint4*>(smem + kSmM), 32 * w + (threadIdx.x & 31)) - 16 * (warp >> 2);
+#pragma unroll 1
+    for (int b = 0; b <= w; ++b) {
+        uint32_t r[16];
+        tmem_ld16u(tm + 32 * b, r);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+            if (32 * b + e < n) r[e] = 0u;
+        tmem_st16(tm + 32 * b, r);
+    }
+    tmem_wait_st();
 }
 
 // ---- warps 16-23: scores; thread = chunk row ------------------------------------
@@ -700,8 +761,10 @@ __device__ __forceinline__ void score_role(const LinParams& p, const Ctx& x, int
             }
             const float first16 = __shfl_sync(0xffffffffu, from16, 15);
             float left = x.lane & 16 ? first16 + from16 : from16;
+            const bool clears = x.clears();
             if (!x.wait_all(kXFull, c & 1)) return;
             tc_fence_after();
+            if (clears) drop_scores(tm, w8);
             // Sixteen scores become eight pairs of high parts and eight of low parts, in place,
             // the last columns first.
             uint32_t r[16];
@@ -778,18 +841,24 @@ __device__ __forceinline__ void out_role(const Maps& maps, const LinParams& p, c
             if (w > 2) sum += T.z;
             if (w > 1) sum += T.y;
             if (w > 0) sum += T.x;
-            const float f = ex2(sum);
+            float f = ex2(sum);
+            if (x.clears() && last_clearing(*reinterpret_cast<const uint4*>(x.smem + kSmM), row) >= 0) f = kClearing;
             __syncwarp();
             if (x.lane == 0) x.arrive(kGEmpty);
             if (has_s) {
                 if (!x.wait_all(kQSFull, with_s & 1)) return;
                 tc_fence_after();
                 const f2 ff = pack2(f, f);
+                const bool dead = f == kClearing, some = __any_sync(0xffffffffu, dead);
 #pragma unroll 1
                 for (int b = 0; b < 4; ++b) {
                     uint32_t r[32];
                     tmem_ld32(tm + 32 * b, r);
                     tmem_wait_ld();
+                    if (some) {  // may be NaN
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) r[e] = dead ? 0u : r[e];
+                    }
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
                         const float2 v = unpack2(mul2(ff, pack2(__uint_as_float(r[e]), __uint_as_float(r[e + 1]))));
@@ -996,6 +1065,50 @@ __device__ __forceinline__ void store4(__half* s, float4 v) {
     *reinterpret_cast<uint2*>(s) = make_uint2(pack_half2(v.x, v.y), pack_half2(v.z, v.w));
 }
 
+// Where this warp's part of the dS of a cleared chunk (`live` tokens from t0 on) is not
+// finite, makes it anew in place: sums the tokens from the last clearing one on.
+__device__ __noinline__ void mend_ds(const LinParams& p, int t0, int live, int h, uint32_t tm, int row, int col) {
+    uint32_t r[16];
+    float nan = 0.f;
+#pragma unroll 1
+    for (int b = 0; b < 4; ++b) {
+        tmem_ld16u(tm + 16 * b, r);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) nan = fmaf(__uint_as_float(r[e]), 0.f, nan);
+    }
+    if (!__any_sync(0xffffffffu, nan != 0.f)) return;
+    const __nv_bfloat16* v = p.v + (int64_t)h * p.v_sh + row;
+#pragma unroll 1
+    for (int b = 0; b < 4; ++b) {
+        const __nv_bfloat16* k = p.k + (int64_t)(h / p.rep) * p.k_sh + col + 16 * b;
+        float decay = 0.f;  // after token t
+#pragma unroll
+        for (int e = 0; e < 16; ++e) r[e] = 0u;
+#pragma unroll 1
+        for (int t = t0 + live - 1; t >= t0; --t) {
+            const float w = expf(decay) * __bfloat162float(v[(int64_t)t * p.v_st]);
+            const uint4* kt = reinterpret_cast<const uint4*>(k + (int64_t)t * p.k_st);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint4 u = kt[i];
+                const uint32_t pair[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    uint32_t* at = r + 8 * i + 2 * e;
+                    at[0] = __float_as_uint(fmaf(w, bf_lo(pair[e]), __uint_as_float(at[0])));
+                    at[1] = __float_as_uint(fmaf(w, bf_hi(pair[e]), __uint_as_float(at[1])));
+                }
+            }
+            const float g = p.g[(int64_t)t * p.g_st + h];
+            if (g < kMinDecay) break;
+            decay += g;
+        }
+        tmem_st16(tm + 16 * b, r);
+    }
+    tmem_wait_st();
+}
+
 template <class P, bool Local>
 __device__ __forceinline__ void state_role(const Maps& maps, const LinParams& p, const Ctx& x, int warp) {
     const int sg = warp >> 2;
@@ -1049,7 +1162,7 @@ __device__ __forceinline__ void state_role(const Maps& maps, const LinParams& p,
                   ((size_t)item.h * D + 32 * (warp & 3) + half) * D + 64 * sg + 4 * l16;
         // a segment's state in the workspace: this thread's 4 columns 4 e .. every 256 x 4 values
         float4* plane = reinterpret_cast<float4*>(p.planes) + (size_t)item.plane * (D * D / 4) + 32 * warp + x.lane;
-        float kept = 1.f;  // Local: what is left of the state after the segment
+        float kept = 1.f;  // Local: what is left of the state after the segment, or kClearing
         if (!Local && (item.flags & kPlane)) {
             grid_dep_wait();  // the chain kernel may still run
 #pragma unroll
@@ -1087,7 +1200,13 @@ __device__ __forceinline__ void state_role(const Maps& maps, const LinParams& p,
             if (!x.wait_all(kDSFull + ds_bar<Local>(c), ds_phase<Local>(c))) return;
             tc_fence_after();
             const f2 g2 = pack2(gamma, gamma);
-            if (Local) kept *= gamma;
+            const bool clears = gamma == kClearing;
+            if (clears) {
+                mend_ds(p, item.t0 + j * C, min(C, item.len - j * C), item.h, tm + ds_column<Local>(c), row, 64 * sg);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) S[e] = 0ull;
+            }
+            if (Local) kept = clears || kept == kClearing ? kClearing : kept * gamma;
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
                 uint32_t r[16];
@@ -1290,6 +1409,7 @@ __global__ void __launch_bounds__(X* RUNS) kda_lin_chain(const __grid_constant__
     float4* plane = reinterpret_cast<float4*>(p.planes) + (size_t)h * (D * D / 4) + at + (first + s0) * step;
     const float* kept = p.kept + (size_t)(first + s0) * p.H + h;
     auto next = [](float4 a, float k, float4 v) {
+        if (k == kClearing) a = make_float4(0.f, 0.f, 0.f, 0.f);
         return make_float4(fmaf(k, a.x, v.x), fmaf(k, a.y, v.y), fmaf(k, a.z, v.z), fmaf(k, a.w, v.w));
     };
     grid_dep_wait();  // the segments' states are made
@@ -1304,7 +1424,8 @@ __global__ void __launch_bounds__(X* RUNS) kda_lin_chain(const __grid_constant__
         float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
         float all = 1.f;
 #pragma unroll
-        for (int i = 0; i < AHEAD; ++i) t = next(t, k[i], v[i]), all *= k[i];
+        for (int i = 0; i < AHEAD; ++i)
+            t = next(t, k[i], v[i]), all = all == kClearing || k[i] == kClearing ? kClearing : all * k[i];
         sum[threadIdx.y][threadIdx.x] = t;
         if (threadIdx.x == 0) left[threadIdx.y] = all;
         __syncthreads();

@@ -73,7 +73,8 @@ __device__ __forceinline__ void write_status(const LinParams& p, int lane) {
 }
 #endif
 
-// Values below kMinDecay give exp() == 0 in fp32; the clamp keeps sums of them finite.
+// Values below kMinDecay, where exp() is 0 in fp32, clear the state whatever it held; the
+// clamp keeps sums of them finite.
 constexpr float kMinDecay = -104.f;
 
 // Segment states a call's workspace holds: a cut needs at most two for each SM.
