@@ -1281,7 +1281,6 @@ __device__ __forceinline__ void state_role(const Maps& maps, const LinParams& p,
             }
         }
     }
-    if (x.lane == 0) bulk_wait_all();
 }
 
 // Local: the segments' states from zero, nothing else (the q, score and output parts idle).
@@ -1332,6 +1331,8 @@ __global__ void __launch_bounds__(kThreads, 1) kda_lin_walk(const __grid_constan
     if (warp < 8) {
         more_registers<104>();
         state_role<P, Local>(maps, p, x, warp);
+        // a state may be on its way to the pool, also where a wait gave up
+        if (x.lane == 0) bulk_wait_all();
     } else if (warp < 16) {
         fewer_registers<56>();
         weight_role<Local>(p, x, warp - 8);
@@ -1362,7 +1363,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_lin_walk(const __grid_constan
     __syncthreads();
     tc_fence_after();
     if (*x.abort) {
-        // a wait gave up: let the copies and products in flight end before their memory goes
+        // a wait gave up: let the loads and products in flight end, too, before their memory goes
         if (threadIdx.x == 0) atomicOr(p.status, 1);
         if (warp == 29 && x.lane == 0) {
             if (!Local && issued.x > 0) mbar_wait(x.bar + kFull + kQ, q_phase(issued.x - 1));
