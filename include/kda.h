@@ -437,7 +437,9 @@ KDA_API size_t kda_lin_attn_workspace_size(int64_t total_tokens, int32_t num_seq
  *   tensors       1 or 2 of them; num_heads 0 skips one.  `in` and `out` are
  *                 device [total_tokens][num_heads][head_dim] of dtype, dense in
  *                 the last dimension, strides in elements; out == in with the
- *                 same strides works in place, any other overlap is refused.
+ *                 same strides works in place, any other overlap of an out with
+ *                 an in, of its own tensor or the other, or with the other out
+ *                 is refused (views of one buffer that share no row are taken).
  *   positions     device int32 or int64 (position_bytes 4 or 8), one per token.
  *   inv_freq      device fp64 [rot_dim / 2], radians per position, in (-2 pi, 2 pi).
  *   head_dim      1 .. 1024; rot_dim even, 0 .. head_dim.

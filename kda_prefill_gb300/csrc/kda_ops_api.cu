@@ -1,5 +1,7 @@
 // Host side of the operators beside the KDA forward: argument checks and launches.
 
+#include <numeric>
+
 #include "kda_ops.h"
 
 namespace {
@@ -28,6 +30,33 @@ Span view(const char* name, const void* p, int64_t T, int64_t H, int64_t D, int6
 }
 bool overlap(const Span& a, const Span& b) {
     return a.lo < a.hi && b.lo < b.hi && a.lo < b.hi && b.lo < a.hi;
+}
+
+// A [T][H][D] view of rows in memory, in bytes.
+struct Rows {
+    uintptr_t lo;
+    int64_t T, H, D, st, sh;
+};
+Rows rows_of(const void* p, int64_t T, int64_t H, int64_t D, int64_t st, int64_t sh, size_t elt) {
+    const int64_t e = (int64_t)elt;
+    return Rows{reinterpret_cast<uintptr_t>(p), T, H, D * e, T > 1 ? st * e : 0, H > 1 ? sh * e : 0};
+}
+// Whether two views may share a byte.  They do not where their extents lie apart, or where
+// both consist of blocks (rows, tokens with all heads, or heads with all tokens) that
+// begin a multiple of one step apart and fit beside each other in that step: so views of
+// one projection's output are told apart.
+bool may_share(const Rows& a, const Rows& b) {
+    if (a.T <= 0 || a.H <= 0 || b.T <= 0 || b.H <= 0) return false;
+    const auto apart = [&](int64_t step, int64_t in_a, int64_t in_b) {
+        if (step == 0) return a.lo + in_a <= b.lo || b.lo + in_b <= a.lo;
+        const int64_t gap = a.lo <= b.lo ? (int64_t)((b.lo - a.lo) % step) : (step - (int64_t)((a.lo - b.lo) % step)) % step;
+        return in_a <= gap && in_b <= step - gap;
+    };
+    const int64_t heads_a = (a.H - 1) * a.sh + a.D, heads_b = (b.H - 1) * b.sh + b.D;
+    const int64_t tokens_a = (a.T - 1) * a.st + a.D, tokens_b = (b.T - 1) * b.st + b.D;
+    return !(apart(0, tokens_a + heads_a - a.D, tokens_b + heads_b - b.D) ||
+             apart(std::gcd(a.st, b.st), heads_a, heads_b) || apart(std::gcd(a.sh, b.sh), tokens_a, tokens_b) ||
+             apart(std::gcd(std::gcd(a.st, b.st), std::gcd(a.sh, b.sh)), a.D, b.D));
 }
 
 size_t dtype_size(int dtype) { return dtype == KDA_F32 ? 4 : 2; }
@@ -225,6 +254,7 @@ int kda_rope(const kda_rope_tensor* tensors, int32_t num_tensors, const void* po
     const size_t elt = dtype_size(dtype);
     kda::RopeParams p{};
     Span in[2] = {}, out[2] = {};
+    Rows from[2] = {}, to[2] = {};
     for (int i = 0; i < num_tensors; ++i) {
         const kda_rope_tensor& x = tensors[i];
         if (x.num_heads < 0 || x.num_heads > 65535)
@@ -243,10 +273,17 @@ int kda_rope(const kda_rope_tensor* tensors, int32_t num_tensors, const void* po
                           x.in_stride_h == x.out_stride_h;
         if (!same && overlap(in[i], out[i]))
             return set_error(KDA_ERR_INVALID_ARG, "out of tensor %d overlaps its in", i);
+        from[i] = rows_of(x.in, T, x.num_heads, head_dim, x.in_stride_t, x.in_stride_h, elt);
+        to[i] = rows_of(x.out, T, x.num_heads, head_dim, x.out_stride_t, x.out_stride_h, elt);
         p.x[i] = kda::RopeTensor{x.in, x.out, x.in_stride_t, x.in_stride_h,
                                  x.out_stride_t, x.out_stride_h, x.num_heads};
     }
     if (p.x[0].heads + p.x[1].heads == 0 || T == 0) return KDA_OK;
+    // one launch reads and writes both tensors in any order
+    for (int i = 0; i < 2; ++i)
+        if (may_share(to[i], from[1 - i]))
+            return set_error(KDA_ERR_INVALID_ARG, "out of tensor %d overlaps the in of tensor %d", i, 1 - i);
+    if (may_share(to[0], to[1])) return set_error(KDA_ERR_INVALID_ARG, "the outs of the two tensors overlap");
     if (!positions || (rot_dim > 0 && !inv_freq))
         return set_error(KDA_ERR_INVALID_ARG, "positions and inv_freq are required");
     if (!aligned(positions, (size_t)position_bytes) || !aligned(inv_freq, 8))
