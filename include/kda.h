@@ -464,7 +464,8 @@ KDA_API int kda_rope(const kda_rope_tensor* tensors, int32_t num_tensors,
  *   x, gate, out   device [total_tokens][num_heads][head_dim] of dtype, dense
  *                  in the last dimension, strides in elements; gate may be
  *                  NULL (no gate).  out == x with the same strides works in
- *                  place, any other overlap of out with x or gate is refused.
+ *                  place, any other overlap of out with x or gate is refused
+ *                  (views of one buffer that share no row are taken).
  *   weight         device fp32 [head_dim], or NULL for ones.
  *   activation     KDA_ACT_SIGMOID, KDA_ACT_SILU or KDA_ACT_NONE (the gate as it is).
  *   head_dim       1 .. 8192;  eps >= 0.

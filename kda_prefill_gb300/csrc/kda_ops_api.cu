@@ -41,6 +41,8 @@ Rows rows_of(const void* p, int64_t T, int64_t H, int64_t D, int64_t st, int64_t
     const int64_t e = (int64_t)elt;
     return Rows{reinterpret_cast<uintptr_t>(p), T, H, D * e, T > 1 ? st * e : 0, H > 1 ? sh * e : 0};
 }
+// The same rows in the same places, as where out is in.
+bool same_rows(const Rows& a, const Rows& b) { return a.lo == b.lo && a.st == b.st && a.sh == b.sh; }
 // Whether two views may share a byte.  They do not where their extents lie apart, or where
 // both consist of blocks (rows, tokens with all heads, or heads with all tokens) that
 // begin a multiple of one step apart and fit beside each other in that step: so views of
@@ -253,7 +255,7 @@ int kda_rope(const kda_rope_tensor* tensors, int32_t num_tensors, const void* po
         return set_error(KDA_ERR_UNSUPPORTED, "positions of %d bytes (4 or 8)", position_bytes);
     const size_t elt = dtype_size(dtype);
     kda::RopeParams p{};
-    Span in[2] = {}, out[2] = {};
+    Span out[2] = {};
     Rows from[2] = {}, to[2] = {};
     for (int i = 0; i < num_tensors; ++i) {
         const kda_rope_tensor& x = tensors[i];
@@ -267,14 +269,11 @@ int kda_rope(const kda_rope_tensor* tensors, int32_t num_tensors, const void* po
         if (rc == KDA_OK) rc = check_view("out", T, x.num_heads, head_dim, x.out_stride_t, x.out_stride_h);
         if (rc == KDA_OK) rc = check_written("out", T, x.num_heads, head_dim, x.out_stride_t, x.out_stride_h);
         if (rc != KDA_OK) return rc;
-        in[i] = view("in", x.in, T, x.num_heads, head_dim, x.in_stride_t, x.in_stride_h, elt);
         out[i] = view("out", x.out, T, x.num_heads, head_dim, x.out_stride_t, x.out_stride_h, elt);
-        const bool same = x.in == x.out && x.in_stride_t == x.out_stride_t &&
-                          x.in_stride_h == x.out_stride_h;
-        if (!same && overlap(in[i], out[i]))
-            return set_error(KDA_ERR_INVALID_ARG, "out of tensor %d overlaps its in", i);
         from[i] = rows_of(x.in, T, x.num_heads, head_dim, x.in_stride_t, x.in_stride_h, elt);
         to[i] = rows_of(x.out, T, x.num_heads, head_dim, x.out_stride_t, x.out_stride_h, elt);
+        if (!same_rows(from[i], to[i]) && may_share(from[i], to[i]))
+            return set_error(KDA_ERR_INVALID_ARG, "out of tensor %d overlaps its in", i);
         p.x[i] = kda::RopeTensor{x.in, x.out, x.in_stride_t, x.in_stride_h,
                                  x.out_stride_t, x.out_stride_h, x.num_heads};
     }
@@ -333,13 +332,13 @@ int kda_gated_norm(const void* x, int64_t x_stride_t, int64_t x_stride_h, const 
     if (rc == KDA_OK) rc = check_view("out", T, H, D, out_stride_t, out_stride_h);
     if (rc == KDA_OK) rc = check_written("out", T, H, D, out_stride_t, out_stride_h);
     if (rc != KDA_OK) return rc;
-    const Span sx = view("x", x, T, H, D, x_stride_t, x_stride_h, elt);
-    const Span sg = view("gate", gate, T, H, D, gate_stride_t, gate_stride_h, gate ? elt : 0);
+    const Rows rx = rows_of(x, T, H, D, x_stride_t, x_stride_h, elt);
+    const Rows ro = rows_of(out, T, H, D, out_stride_t, out_stride_h, elt);
     const Span so = view("out", out, T, H, D, out_stride_t, out_stride_h, elt);
     const Span sw = span("weight", weight, (size_t)D * 4);
-    const bool same = x == out && x_stride_t == out_stride_t && x_stride_h == out_stride_h;
-    if (!same && overlap(so, sx)) return set_error(KDA_ERR_INVALID_ARG, "out overlaps x");
-    if (gate && overlap(so, sg)) return set_error(KDA_ERR_INVALID_ARG, "out overlaps gate");
+    if (!same_rows(rx, ro) && may_share(rx, ro)) return set_error(KDA_ERR_INVALID_ARG, "out overlaps x");
+    if (gate && may_share(rows_of(gate, T, H, D, gate_stride_t, gate_stride_h, elt), ro))
+        return set_error(KDA_ERR_INVALID_ARG, "out overlaps gate");
     if (weight && overlap(so, sw)) return set_error(KDA_ERR_INVALID_ARG, "out overlaps weight");
     const kda::NormParams p{x,           gate,         weight,        out,
                             x_stride_t,  x_stride_h,   gate_stride_t, gate_stride_h,

@@ -64,3 +64,48 @@ def test_rope_refuses_tensors_in_each_other(lib, q, k, message):  # noqa: F811
 def test_rope_takes_tensors_beside_each_other(lib, q, k):  # noqa: F811
     rc, err = rope(lib, q, k)
     assert rc == -1 and "are required" in err, (rc, err)
+
+
+# Views of one buffer and one-entry dimensions in a single tensor.  gated_norm goes on to
+# the weight, which overlaps the out here, where it finds no other overlap.
+def norm(lib, **over):  # noqa: F811
+    return norm_abi(lib, **dict(dict(w=over.get("out", BASE)), **over))
+
+
+@pytest.mark.parametrize("over", [
+    # in place on one half of a fused [x | gate], and of [gate | x]
+    dict(x=BASE, gate=BASE + 4 * ROW, out=BASE, x_st=1024, g_st=1024, o_st=1024),
+    dict(x=BASE + 4 * ROW, gate=BASE, out=BASE + 4 * ROW, x_st=1024, g_st=1024, o_st=1024),
+    # x and gate by turns in each head
+    dict(x=BASE, gate=BASE + ROW, out=BASE, x_st=1024, g_st=1024, o_st=1024, x_sh=256, g_sh=256, o_sh=256),
+    # out in a third part of the buffer
+    dict(x=BASE, gate=BASE + 4 * ROW, out=BASE + 8 * ROW, x_st=1536, g_st=1536, o_st=1536),
+    # the stride of a dimension of one entry says nothing
+    dict(x=BASE, out=BASE, T=1, x_st=512, o_st=4096),
+    dict(x=BASE, out=BASE, H=1, x_sh=128, o_sh=640),
+])
+def test_gated_norm_takes_views_beside_each_other(lib, over):  # noqa: F811
+    rc, err = norm(lib, **over)
+    assert rc == -1 and "out overlaps weight" in err, (rc, err)
+
+
+@pytest.mark.parametrize("over,message", [
+    (dict(x=BASE, gate=BASE + 3 * ROW, out=BASE, x_st=1024, g_st=1024, o_st=1024), "out overlaps gate"),
+    (dict(x=BASE, gate=BASE + 4 * ROW, out=BASE, x_st=1024, g_st=768, o_st=1024), "out overlaps gate"),
+    (dict(x=BASE, gate=BASE, out=BASE), "out overlaps gate"),
+    (dict(x=BASE, gate=BASE + M, out=BASE + 2 * ROW, x_st=1024, o_st=1024), "out overlaps x"),
+    (dict(x=BASE, gate=BASE + M, out=BASE, x_st=1024, o_st=512), "out overlaps x"),
+])
+def test_gated_norm_refuses_rows_in_each_other(lib, over, message):  # noqa: F811
+    rc, err = norm(lib, **over)
+    assert rc == -1 and message in err, (rc, err)
+
+
+@pytest.mark.parametrize("x,y", [
+    # from one part of a fused buffer to another, and over a dimension of one entry
+    (view(BASE, 2, 768), view(BASE + 2 * ROW, 2, 768)),
+    (view(BASE, 1, 512, 128), view(BASE, 1, 512, 640)),
+])
+def test_rope_takes_views_beside_each_other(lib, x, y):  # noqa: F811
+    rc, err = rope_abi(lib, [pair(x, y)], pos=None)
+    assert rc == -1 and "are required" in err, (rc, err)
