@@ -281,6 +281,13 @@ def _same_device(device, **tensors) -> None:
             raise ValueError(f"{name} is on {x.device}, q on {device}")
 
 
+def _on_current_device(index: int) -> None:
+    """The library runs on the current GPU; tensors of another one are refused."""
+    if index >= 0 and index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on cuda:{index}, and the current device is "
+                         f"cuda:{torch.cuda.current_device()}: call under torch.cuda.device({index})")
+
+
 def _per_sequence(x: torch.Tensor, name: str, N: int) -> None:
     """One entry per sequence, contiguous (the kernels index it by sequence)."""
     if x.numel() != N or not x.is_contiguous():
@@ -341,6 +348,7 @@ def chunk_fwd(q, k, v, g_raw, beta_raw, cu_seqlens, *, state_cache, state_indice
     _per_sequence(hs, "has_initial_state", N)
     _same_device(q.device, out=out, state_cache=state_cache, state_indices=state_indices,
                  has_initial_state=hs)
+    _on_current_device(q.get_device())
     host = _host_bounds(cu_seqlens_cpu, N)
     ws = _workspace(workspace, T, N, H, q.device)
     s = stream if stream is not None else torch.cuda.current_stream(q.device)
@@ -384,6 +392,7 @@ def chunk_fwd_dense(q, k, v, g_raw, beta_raw, cu_seqlens, *, final_state, out,
         _per_sequence(hs, "has_initial_state", N)
     _same_device(q.device, out=out, final_state=final_state, initial_state=initial_state,
                  has_initial_state=hs)
+    _on_current_device(q.get_device())
     host = _host_bounds(cu_seqlens_cpu, N)
     ws = _workspace(workspace, T, N, H, q.device)
     s = stream if stream is not None else torch.cuda.current_stream(q.device)

@@ -6,7 +6,8 @@ linear-attention layer, in the order it runs them.
     kda.gated_norm(o, weight, gate=z, ...)        norm and gate of the output
 
 Argument marshalling only; the kernels are in ``libkda.so`` (``include/kda.h``
-describes each call).
+describes each call).  Every call runs on the current GPU, where its tensors have to
+be.
 """
 from __future__ import annotations
 
@@ -17,8 +18,8 @@ from typing import Optional
 
 import torch
 
-from . import (KDA_OK, STATE_DTYPES, _check, _host_bounds, _per_sequence, _same_device,
-               load_library)
+from . import (KDA_OK, STATE_DTYPES, _check, _host_bounds, _on_current_device, _per_sequence,
+               _same_device, load_library)
 
 _DTYPES = STATE_DTYPES  # kda_dtype has the same values as kda_state_dtype
 _LAYOUTS = {"half": 0, "interleaved": 1}
@@ -145,6 +146,7 @@ def lin_attn_fwd(q, k, v, log_decay, cu_seqlens, *, state_cache, state_indices,
     else:
         T, Hk, H, N, (q_st, q_sh, k_st, k_sh, v_st, v_sh) = _lin_args(
             q, k, v, log_decay, cu_seqlens, state_cache, state_indices, hs, out)
+    _on_current_device(at)
     host = None if cu_seqlens_cpu is None else _host_int32(cu_seqlens_cpu, N)
     need = lin_attn_workspace_size(T, N, H)
     if workspace is None:
@@ -299,6 +301,7 @@ def rope(q, k, positions, inv_freq, *, layout: str = "half", factor: float = 1.0
     if not (q_out.get_device() == positions.get_device() == inv_freq.get_device() == at
             and (k is None or k.get_device() == k_out.get_device() == at)):
         _same_device(dev, k=k, q_out=q_out, k_out=k_out, positions=positions, inv_freq=inv_freq)
+    _on_current_device(at)
     rc = lib.kda_rope(arr, n, positions.data_ptr(), positions.element_size(),
                       inv_freq.data_ptr(), T, D, 2 * inv_freq.numel(), _LAYOUTS[layout],
                       float(factor), 1 if inverse else 0, _DTYPES[q.dtype], _stream(stream, dev))
@@ -339,6 +342,7 @@ def gated_norm(x, weight=None, *, gate=None, activation: str = "sigmoid", eps: f
     if not (out.get_device() == at and (gate is None or gate.get_device() == at)
             and (weight is None or weight.get_device() == at)):
         _same_device(x.device, gate=gate, weight=weight, out=out)
+    _on_current_device(at)
     rc = lib.kda_gated_norm(
         x.data_ptr(), x_st, x_sh, None if gate is None else gate.data_ptr(), g_st, g_sh,
         None if weight is None else weight.data_ptr(), out.data_ptr(), o_st, o_sh, T, H, D,
