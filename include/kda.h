@@ -387,8 +387,11 @@ enum kda_dtype { KDA_F32 = 0, KDA_BF16 = 1, KDA_F16 = 2 };
  *                    aligned; kda_check_status() reads its status word.
  *
  * Accumulation is in fp32; an fp32 pool receives the state to fp32 accuracy.
+ * In sequences of more than 8 tokens the outputs' terms, decayed scores and the
+ * state they are made from, carry 16 significant bits (out itself has 8).
  * The order of summation, and so every bit of the result, depends on the
- * bounds, the head counts and the GPU's SM count alone.  A token's output depends on its own
+ * bounds, the head counts and the GPU's SM count alone (in a state cleared of
+ * infinities or NaN also on their place).  A token's output depends on its own
  * sequence's tokens up to it alone, also where others hold infinities or NaN:
  * one in v makes its value column NaN or infinite from its token on (in out and
  * in the state), one in k every column, until a token clears the state; one in q

@@ -5,9 +5,12 @@
 // Bound by reading x and the gate and writing y once.  A group of lanes takes a row.
 // Rows of at most one 16-byte piece a lane stay in registers between the sum of squares
 // and the product, and where there are enough of them a group has two in flight, with
-// their gates.  Longer rows are read again, from the caches.  16384 tokens x 12 heads of
-// 128 in bf16: 28.8 us, 77 % of a plain copy's rate; the rest is the start and the end of
-// a launch and the conversions' instructions (63 % of the issue rate).
+// their gates.  Longer rows are read again, from the caches, by a warp each, with few loads
+// in flight: 3000 rows of 8192 in bf16 47.3 us, 46 % of a plain copy's rate, 49152 of 512
+// 39.0 us, 57 %.
+// 16384 tokens x 12 heads of 128: 28.7 us in bf16, 77 % of a plain copy's rate, 53.3 us in
+// fp32, 83 %; the rest is the start and the end of a launch and, in 16 bits, the
+// conversions' instructions (63 % of the issue rate).
 
 #include "kda_ops.h"
 #include "kda_rows.cuh"

@@ -19,15 +19,15 @@
 //
 // The products are the bound: 72 of 128 x 128 x 16, 64 cycles each, 4.6 K cycles a chunk,
 // of which the tensor pipe reaches about three quarters while it shares shared and tensor
-// memory with the operands' makers (6.2 K cycles a chunk; 128 sequences of 117,555 tokens
-// x 12 heads: 319 us, tensor pipe active 62 % of the time, 46 % of the memory's rate).
+// memory with the operands' makers (6.3 K cycles a chunk; 128 sequences of 117,555 tokens
+// x 12 heads: 331 to 342 us, tensor pipe active 61 % of the time, 48 % of a copy's rate).
 // Chunks of 128 fill the products' M: with 64, q S^T would run at half rate, and S would
 // be read, rounded and written as an operand twice as often.
 //
 // A few long sequences would leave most SMs idle.  They are cut into segments: a first
 // launch makes each segment's state from zero (Local), kda_lin_chain the states that the
 // segments start from, and the walk takes them as items.  1 x 16384 tokens x 12 heads:
-// 79.8 us (26 Local, 52 the walk), 410 us uncut.
+// 80 to 81 us (27 Local, 53 the walk), 418 us uncut.
 //
 // Rounding.  Operands are bf16.  q, k and v are; P and S are carried as a sum of
 // two bf16 (16 bits: with one, a rounding as large as out's own would be added
@@ -1548,14 +1548,18 @@ cudaError_t launch(const Maps& maps, const LinParams& p, const LinCuts& cuts, cu
 // whichever is more.  Cut, a segment's walk has to wait for the states of those before it,
 // which are made first from k and v alone, in about half of a walk's time; `start` chunks'
 // time goes into the two more launches and the states' way through memory, more of it the
-// more states there are.  The segments are as long as lets one wave of CTAs take all
-// items, or, where there are more sequences than that, as an even share of the chunks.
-// Cut and uncut, 12 heads: 22.6 and 26.6 us for 640 tokens, 22.6 and 32.8 us for 896, 28.7
-// and 60.8 us for 2048, 37.2 and 115 us for 4097, 79.8 and 410 us for 16384; 27.5 and 32.8
-// us for two of 896; 117.0 and 122.0 us for four of 2048 beside 512 of one token.  Two
-// heads: 18.5 and 22.6 us for 512 tokens.  Left uncut, 12 heads: 384 tokens (20.5 us, cut
-// 22.6), three of 768 (28.7 us, cut 29.6), four of 640 (26.7 us, cut 32.6), four of 1024
-// (36.9 us, cut 37.9), six of 900 to 1600 (51.3 us, cut 54.1).
+// more states there are: none for up to three (sequence, head) pairs, and from there on one
+// more chunk for every sixteen, up to four.  That is a fit to the times below, no more.  The
+// segments are as long as lets one wave of CTAs take all items, or, where there are more
+// sequences than that, as an even share of the chunks.
+// Cut and uncut, 12 heads: 22.6 and 26.7 us for 640 tokens, 22.6 and 32.8 us for 896, 28.7
+// and 61.5 us for 2048, 37.1 and 116 us for 4097, 80.1 and 418 us for 16384; 26.7 and 32.8
+// us for two of 896; 128.3 and 131.2 us for four of 2048 beside 512 of one token (all from
+// their states).  Two heads: 18.5 and 22.6 us for 512 tokens.  Left uncut, 12 heads: 384
+// tokens (20.5 us, cut 22.4), three of 768 (30.1 us, cut 28.7), four of 640 (26.7 us, cut
+// 31.1), four of 1024 (36.9 us, cut 37.4), six of 900 to 1600 (51.3 us, cut 53.1).  Only the
+// longest sequence is compared: where all are alike and just exceed one wave of CTAs (13
+// prompts of 2048: 123.8 us, 12 of them 74.3), nothing is cut.
 struct Cut {
     int seg_len = 0, n_cut = 0, n_seg = 0;
 };

@@ -11,8 +11,9 @@
 // bytes to copy.  A CTA takes a few tokens; a thread keeps its unit of its head and goes
 // through the tokens, so that addresses only advance, four of them in flight, the
 // first four read before the tokens' (c, s) are made.  16384 tokens, 12 + 12 heads of 128,
-// half of each turned: 34.8 us, 85 % of a plain copy's rate; the rest is the start and the
-// end of a launch.
+// half of each turned by interleaved pairs: 34.8 us, 85 % of a plain copy's rate; the rest is
+// the start and the end of a launch.  All of each turned in the half layout: 46.4 us in bf16,
+// 64 %, and 66.0 us in fp32, 90 %.
 
 #include "kda_ops.h"
 #include "kda_rows.cuh"
