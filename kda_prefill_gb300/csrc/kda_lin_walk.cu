@@ -20,7 +20,7 @@
 // The products are the bound: 72 of 128 x 128 x 16, 64 cycles each, 4.6 K cycles a chunk,
 // of which the tensor pipe reaches about three quarters while it shares shared and tensor
 // memory with the operands' makers (6.3 K cycles a chunk; 128 sequences of 117,555 tokens
-// x 12 heads: 331 to 342 us, tensor pipe active 61 % of the time, 48 % of a copy's rate).
+// x 12 heads: 340 to 343 us, tensor pipe active 61 % of the time, 48 % of a copy's rate).
 // Chunks of 128 fill the products' M: with 64, q S^T would run at half rate, and S would
 // be read, rounded and written as an operand twice as often.
 //
