@@ -421,6 +421,43 @@ KDA_API size_t kda_lin_attn_workspace_size(int64_t total_tokens, int32_t num_seq
                   int32_t num_heads);
 
 /*
+ * kda_gated_delta_fwd — the gated delta rule with a decay for each head over
+ * packed sequences, the states in the paged pool read and written in-kernel.
+ * For every sequence and head, with a V-first state S in R^{V x K}, K = V = 128:
+ *
+ *     q^ = q / sqrt(|q|^2 + 1e-6),   k^ = k / sqrt(|k|^2 + 1e-6)
+ *     S_t = exp(g_t) S_{t-1} (I - beta_t k^_t k^_t^T) + beta_t v_t k^_t^T
+ *     o_t = scale * S_t q^_t
+ *
+ *   q, k, v, strides, log_decay, num_qk_heads, scale, cu_seqlens ... out,
+ *   state_dtype      as in kda_lin_attn_fwd.
+ *   beta             device fp32 [total_tokens][num_heads] dense, 0 .. 2: the
+ *                    strength of a token's write (with 1 the state then gives
+ *                    v_t for k^_t).
+ *   workspace        at least kda_gated_delta_workspace_size() bytes, 256-byte
+ *                    aligned; kda_check_status() reads its status word.
+ *
+ * Accumulation is in fp32; an fp32 pool receives the state to fp32 accuracy.
+ * Graph capture, synchronisation and bounds follow kda_chunk_fwd.
+ */
+KDA_API int kda_gated_delta_fwd(const void* q, int64_t q_stride_t, int64_t q_stride_h,
+                  const void* k, int64_t k_stride_t, int64_t k_stride_h,
+                  const void* v, int64_t v_stride_t, int64_t v_stride_h,
+                  const float* log_decay, int decay_per_token, const float* beta,
+                  const int32_t* cu_seqlens, const int32_t* cu_seqlens_host,
+                  int32_t num_seqs, int64_t total_tokens, int32_t num_heads,
+                  int32_t num_qk_heads,
+                  void* state_cache, int64_t state_stride0, int32_t num_slots,
+                  const int32_t* state_indices, const uint8_t* has_initial_state,
+                  void* out, float scale, int state_dtype,
+                  void* workspace, size_t workspace_bytes, kda_stream_t stream);
+
+/* Bytes of workspace a kda_gated_delta_fwd call with these sizes needs; 0 for
+ * invalid sizes. */
+KDA_API size_t kda_gated_delta_workspace_size(int64_t total_tokens, int32_t num_seqs,
+                  int32_t num_heads);
+
+/*
  * kda_rope — rotary positions.  For each token t with position p, each head x
  * and each pair i < rot_dim / 2, with the angle a = p * inv_freq[i]:
  *
@@ -458,6 +495,30 @@ KDA_API int kda_rope(const kda_rope_tensor* tensors, int32_t num_tensors,
                   const void* positions, int position_bytes, const double* inv_freq,
                   int64_t total_tokens, int32_t head_dim, int32_t rot_dim, int layout,
                   float factor, int inverse, int dtype, kda_stream_t stream);
+
+/*
+ * kda_qk_norm_rope — norms of queries and keys for each head, and the rotary
+ * positions, in one pass.  Each row x (a token's head) is divided by its root
+ * mean square and multiplied by a weight, then turned as in kda_rope:
+ *
+ *     y = x / sqrt(mean(x^2) + eps) * weight,   y's first rot_dim dimensions turned
+ *
+ *   tensors       1 or 2 of them (q and k), their `x` as in kda_rope.  `weight`
+ *                 is device fp32 [head_dim], or [num_heads][head_dim] with
+ *                 weight_stride_h elements between heads (0: one for all), or
+ *                 NULL for ones.
+ *   eps           >= 0.
+ *   positions ... factor, dtype   as in kda_rope.
+ */
+typedef struct kda_norm_rope_tensor {
+    kda_rope_tensor x;
+    const float* weight;
+    int64_t weight_stride_h;
+} kda_norm_rope_tensor;
+KDA_API int kda_qk_norm_rope(const kda_norm_rope_tensor* tensors, int32_t num_tensors, float eps,
+                  const void* positions, int position_bytes, const double* inv_freq,
+                  int64_t total_tokens, int32_t head_dim, int32_t rot_dim, int layout,
+                  float factor, int dtype, kda_stream_t stream);
 
 /*
  * kda_gated_norm — root-mean-square norm of each row, with a weight and a gate:

@@ -20,7 +20,8 @@ __all__ = [
     "release_cache", "cache_entries", "load_library", "KDAError", "STATE_DTYPES",
     "set_kernel_timing", "kernel_times", "set_fused_launch", "check_status",
     "debug_wait_timeout", "STATUS_WAIT_TIMEOUT", "STATUS_SMEM_ALIGN", "STATUS_BAD_SLOT", "STATUS_BOUNDS_MISMATCH",
-    "lin_attn_fwd", "lin_attn_workspace_size", "rope", "rope_frequencies", "gated_norm",
+    "lin_attn_fwd", "lin_attn_workspace_size", "gated_delta_fwd", "gated_delta_workspace_size",
+    "qk_norm_rope", "rope", "rope_frequencies", "gated_norm",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -42,7 +43,7 @@ EXPORTED = (
     "kda_set_kernel_timing", "kda_kernel_times", "kda_kernel_name", "kda_chunk_fwd_raw_bf16",
     "kda_chunk_fwd_noalloc", "kda_set_fused_launch", "kda_check_status",
     "kda_debug_wait_timeout", "kda_lin_attn_fwd", "kda_lin_attn_workspace_size", "kda_rope",
-    "kda_gated_norm",
+    "kda_gated_norm", "kda_gated_delta_fwd", "kda_gated_delta_workspace_size", "kda_qk_norm_rope",
 )
 
 
@@ -130,11 +131,23 @@ def load_library(path: str = LIB_PATH):
         _vp, ctypes.c_float, ctypes.c_int,  # out scale state_dtype
         _vp, ctypes.c_size_t, _vp,      # workspace bytes stream
     ]
+    lib.kda_gated_delta_workspace_size.restype = ctypes.c_size_t
+    lib.kda_gated_delta_workspace_size.argtypes = [_i64, _i32, _i32]
+    lib.kda_gated_delta_fwd.restype = ctypes.c_int
+    lib.kda_gated_delta_fwd.argtypes = [
+        *lib.kda_lin_attn_fwd.argtypes[:11], _vp,  # beta
+        *lib.kda_lin_attn_fwd.argtypes[11:]]
     lib.kda_rope.restype = ctypes.c_int
     lib.kda_rope.argtypes = [
         _vp, _i32, _vp, ctypes.c_int, _vp,  # tensors count positions position_bytes inv_freq
         _i64, _i32, _i32, ctypes.c_int,     # T head_dim rot_dim layout
         ctypes.c_float, ctypes.c_int, ctypes.c_int, _vp,  # factor inverse dtype stream
+    ]
+    lib.kda_qk_norm_rope.restype = ctypes.c_int
+    lib.kda_qk_norm_rope.argtypes = [
+        _vp, _i32, ctypes.c_float, _vp, ctypes.c_int, _vp,  # tensors count eps positions bytes inv_freq
+        _i64, _i32, _i32, ctypes.c_int,     # T head_dim rot_dim layout
+        ctypes.c_float, ctypes.c_int, _vp,  # factor dtype stream
     ]
     lib.kda_gated_norm.restype = ctypes.c_int
     lib.kda_gated_norm.argtypes = [
@@ -407,4 +420,5 @@ def chunk_fwd_dense(q, k, v, g_raw, beta_raw, cu_seqlens, *, final_state, out,
 
 
 from .ops import (  # noqa: E402  (needs the names above)
-    gated_norm, lin_attn_fwd, lin_attn_workspace_size, rope, rope_frequencies)
+    gated_delta_fwd, gated_delta_workspace_size, gated_norm, lin_attn_fwd,
+    lin_attn_workspace_size, qk_norm_rope, rope, rope_frequencies)

@@ -1,5 +1,6 @@
-// Internal interface of the operators beside the KDA forward (linear attention
-// with a decay for each head, rotary positions, gated norm): the parameters
+// Internal interface of the operators beside the KDA forward (linear attention and the
+// gated delta rule with a decay for each head, rotary positions alone and behind a norm of
+// q and k, gated norm): the parameters
 // their host checks (kda_ops_api.cu) hand to their kernels, and the services of
 // kda_api.cu they share.
 #pragma once
@@ -94,6 +95,13 @@ cudaError_t launch_lin_walk(const LinParams& p, const LinCuts& cuts, cudaStream_
 // `beside`: right after the walk, beside its last CTAs.
 cudaError_t launch_lin_step(const LinParams& p, bool beside, cudaStream_t s);
 
+// The gated delta rule: linear attention's parameters, and the strengths of the writes.
+struct DeltaParams : LinParams {
+    const float* beta;  // [T][H]
+};
+// The listed sequences token by token (kda_delta_step.cu).
+cudaError_t launch_delta_step(const DeltaParams& p, const int32_t* list, int n, cudaStream_t s);
+
 struct RopeTensor {
     const void* in;
     void* out;
@@ -113,6 +121,14 @@ struct RopeParams {
     int dtype;
 };
 cudaError_t launch_rope(const RopeParams& p, cudaStream_t s);
+// Each row divided by the root of its mean square plus eps and multiplied by its head's
+// weight before it is turned.
+struct NormRopeParams : RopeParams {
+    const float* weight[2];  // of the tensors' heads, or nullptr for ones
+    int64_t weight_sh[2];    // elements between heads' weights, 0 for one of all
+    float eps;
+};
+cudaError_t launch_qk_norm_rope(const NormRopeParams& p, cudaStream_t s);
 
 struct NormParams {
     const void* x;

@@ -91,6 +91,137 @@ int check_tokens(int64_t T) {
     return KDA_OK;
 }
 
+// A call over packed sequences and the pool of their states: linear attention's and the
+// gated delta rule's.
+struct PackedCall {
+    const void *q, *k, *v;
+    int64_t q_st, q_sh, k_st, k_sh, v_st, v_sh;
+    const float* g;
+    int per_token;
+    const float* beta;
+    bool has_beta;
+    const int32_t *cu, *cu_host;
+    int N;
+    int64_t T;
+    int H, Hk;
+    void* pool;
+    int64_t stride0;
+    int slots;
+    const int32_t* idx;
+    const uint8_t* has_init;
+    void* out;
+    float scale;
+    int state_dtype;
+    void* ws;
+    size_t ws_bytes;
+};
+
+// Its checks; `need` bytes of workspace.  (A call without sequences is right and has nothing
+// to do.)
+int check_packed(const PackedCall& a, size_t need) {
+    constexpr int D = kda::kD;
+    const int64_t T = a.T;
+    const int H = a.H, Hk = a.Hk, N = a.N;
+    int rc = check_tokens(T);
+    if (rc != KDA_OK) return rc;
+    if (N < 0) return set_error(KDA_ERR_INVALID_ARG, "num_seqs = %d < 0", N);
+    if (H <= 0 || H > 65535) return set_error(KDA_ERR_INVALID_ARG, "num_heads = %d out of range", H);
+    if (Hk <= 0 || H % Hk != 0)
+        return set_error(KDA_ERR_INVALID_ARG, "num_qk_heads = %d does not divide num_heads = %d", Hk, H);
+    if (N == 0 && T != 0) return set_error(KDA_ERR_INVALID_ARG, "tokens without sequences");
+    if (a.state_dtype < KDA_STATE_F32 || a.state_dtype > KDA_STATE_F16)
+        return set_error(KDA_ERR_UNSUPPORTED, "state_dtype %d not supported (0 fp32, 1 bf16, 2 fp16)",
+                         a.state_dtype);
+    if (!a.cu && !a.cu_host)
+        return set_error(KDA_ERR_INVALID_ARG, "cu_seqlens and cu_seqlens_host are both NULL");
+    if (a.cu_host) {
+        rc = kda::check_bounds(a.cu_host, N, T);
+        if (rc != KDA_OK) return rc;
+    }
+    const size_t g_bytes = sizeof(float) * (size_t)H * (a.per_token ? (size_t)T : 1);
+    const Span so = view("out", a.out, T, H, D, (int64_t)H * D, D, 2);
+    Span ins[5] = {span("q", a.q, 0), span("k", a.k, 0), span("v", a.v, 0), span("log_decay", a.g, 0),
+                   span("beta", a.beta, 0)};
+    if (T > 0) {
+        if (!a.q || !a.k || !a.v || !a.g || !a.out)
+            return set_error(KDA_ERR_INVALID_ARG, "a q/k/v/log_decay/out pointer is NULL");
+        if (a.has_beta && !a.beta) return set_error(KDA_ERR_INVALID_ARG, "beta is NULL");
+        const void* base[3] = {a.q, a.k, a.v};
+        const char* name[3] = {"q", "k", "v"};
+        const int64_t st[3] = {a.q_st, a.k_st, a.v_st};
+        const int64_t sh[3] = {a.q_sh, a.k_sh, a.v_sh};
+        for (int i = 0; i < 3; ++i) {
+            const int heads = i == 2 ? H : Hk;
+            rc = check_view(name[i], T, heads, D, st[i], sh[i]);
+            if (rc != KDA_OK) return rc;
+            if (!aligned(base[i], 16) || st[i] % 8 != 0 || sh[i] % 8 != 0)
+                return set_error(KDA_ERR_UNSUPPORTED,
+                                 "%s and its strides must be 16-byte aligned", name[i]);
+            ins[i] = view(name[i], base[i], T, heads, D, st[i], sh[i], 2);
+        }
+        if (!aligned(a.out, 16)) return set_error(KDA_ERR_UNSUPPORTED, "out is not 16-byte aligned");
+        if (!aligned(a.g, 4))
+            return set_error(KDA_ERR_UNSUPPORTED, "log_decay is not 4-byte aligned");
+        if (!aligned(a.beta, 4)) return set_error(KDA_ERR_UNSUPPORTED, "beta is not 4-byte aligned");
+        ins[3] = span("log_decay", a.g, g_bytes);
+        ins[4] = span("beta", a.beta, sizeof(float) * (size_t)H * (size_t)T);
+        for (const Span& r : ins)
+            if (overlap(so, r)) return set_error(KDA_ERR_INVALID_ARG, "out overlaps %s", r.name);
+    }
+    if (N == 0) return KDA_OK;
+    if (!a.ws || a.ws_bytes < need)
+        return set_error(KDA_ERR_WORKSPACE, "workspace of %zu bytes given, %zu needed",
+                         a.ws ? a.ws_bytes : (size_t)0, need);
+    if (!aligned(a.ws, 256))
+        return set_error(KDA_ERR_UNSUPPORTED, "workspace is not 256-byte aligned");
+    const int64_t plane = (int64_t)H * D * D;
+    if (!a.pool || !a.idx || !a.has_init)
+        return set_error(KDA_ERR_INVALID_ARG,
+                         "state_cache, state_indices and has_initial_state are required");
+    if (a.slots < N)
+        return set_error(KDA_ERR_INVALID_ARG, "num_slots %d < num_seqs %d (slots are distinct)",
+                         a.slots, N);
+    if (a.stride0 < plane || a.stride0 > (int64_t(1) << 58) / a.slots)
+        return set_error(KDA_ERR_INVALID_ARG,
+                         "state_stride0 %lld is smaller than the slot plane H*V*K = %lld, or out of range",
+                         (long long)a.stride0, (long long)plane);
+    const size_t elt = dtype_size(a.state_dtype);
+    if (!aligned(a.pool, 16) || ((size_t)a.stride0 * elt) % 16 != 0)
+        return set_error(KDA_ERR_UNSUPPORTED,
+                         "state_cache and its slot stride must be 16-byte aligned");
+    const Span sp = span("state_cache", a.pool,
+                         ((size_t)(a.slots - 1) * (size_t)a.stride0 + (size_t)plane) * elt);
+    const Span sw = span("workspace", a.ws, need);
+    const Span with_pool[] = {ins[0], ins[1], ins[2], ins[3], ins[4], so, sw};
+    for (const Span& r : with_pool)
+        if (overlap(sp, r)) return set_error(KDA_ERR_INVALID_ARG, "state_cache overlaps %s", r.name);
+    const Span with_ws[] = {ins[0], ins[1], ins[2], ins[3], ins[4], so};
+    for (const Span& r : with_ws)
+        if (overlap(sw, r)) return set_error(KDA_ERR_INVALID_ARG, "workspace overlaps %s", r.name);
+    return KDA_OK;
+}
+
+void set_params(const PackedCall& a, kda::LinParams& p) {
+    p.q = static_cast<const __nv_bfloat16*>(a.q);
+    p.k = static_cast<const __nv_bfloat16*>(a.k);
+    p.v = static_cast<const __nv_bfloat16*>(a.v);
+    p.q_st = a.q_st, p.q_sh = a.q_sh;
+    p.k_st = a.k_st, p.k_sh = a.k_sh;
+    p.v_st = a.v_st, p.v_sh = a.v_sh;
+    p.g = a.g;
+    p.g_st = a.per_token ? a.H : 0;
+    p.out = static_cast<__nv_bfloat16*>(a.out);
+    p.scale = a.scale;
+    p.H = a.H, p.rep = a.H / a.Hk, p.N = a.N, p.T = a.T;
+    p.status = static_cast<int*>(a.ws);
+    p.pool = a.pool;
+    p.stride0 = a.stride0;
+    p.idx = a.idx;
+    p.has_init = a.has_init;
+    p.num_slots = a.slots;
+    p.st_dtype = a.state_dtype;
+}
+
 struct LinCall {
     kda::LinParams p;
     cudaStream_t stream;
@@ -111,137 +242,33 @@ int enqueue_lin(void* arg, const kda::SeqTables& t) {
     return e == cudaSuccess ? KDA_OK : cuda_error(e, "kernel launch");
 }
 
-}  // namespace
+struct DeltaCall {
+    kda::DeltaParams p;
+    cudaStream_t stream;
+};
 
-extern "C" {
-
-size_t kda_lin_attn_workspace_size(int64_t total_tokens, int32_t num_seqs, int32_t num_heads) {
-    if (total_tokens < 0 || num_seqs <= 0 || num_heads <= 0) return 0;
-    if (total_tokens <= (kda::kLinMinCut - 1) * 128) return kda::kWsHeader;  // nothing is cut
-    return kda::kWsHeader + (size_t)kda::kLinPlanes * (kda::kD * kda::kD + 64) * sizeof(float);
+int enqueue_delta(void* arg, const kda::SeqTables& t) {
+    DeltaCall& c = *static_cast<DeltaCall*>(arg);
+    kda::DeltaParams& p = c.p;
+    p.cu = t.cu;
+    p.n_long = t.n_long;
+    p.n_short = t.n_short;
+    cudaError_t e = kda::launch_delta_step(p, t.long_list, t.n_long, c.stream);
+    if (e == cudaSuccess) e = kda::launch_delta_step(p, t.short_list, t.n_short, c.stream);
+    return e == cudaSuccess ? KDA_OK : cuda_error(e, "kernel launch");
 }
 
-int kda_lin_attn_fwd(const void* q, int64_t q_stride_t, int64_t q_stride_h, const void* k,
-                     int64_t k_stride_t, int64_t k_stride_h, const void* v, int64_t v_stride_t,
-                     int64_t v_stride_h, const float* log_decay, int decay_per_token,
-                     const int32_t* cu_seqlens, const int32_t* cu_seqlens_host, int32_t num_seqs,
-                     int64_t total_tokens, int32_t num_heads, int32_t num_qk_heads,
-                     void* state_cache, int64_t state_stride0, int32_t num_slots,
-                     const int32_t* state_indices, const uint8_t* has_initial_state, void* out,
-                     float scale, int state_dtype, void* workspace, size_t workspace_bytes,
-                     kda_stream_t stream) {
-    constexpr int D = kda::kD;
-    const int64_t T = total_tokens;
-    const int H = num_heads, Hk = num_qk_heads, N = num_seqs;
-    int rc = check_tokens(T);
-    if (rc != KDA_OK) return rc;
-    if (N < 0) return set_error(KDA_ERR_INVALID_ARG, "num_seqs = %d < 0", N);
-    if (H <= 0 || H > 65535) return set_error(KDA_ERR_INVALID_ARG, "num_heads = %d out of range", H);
-    if (Hk <= 0 || H % Hk != 0)
-        return set_error(KDA_ERR_INVALID_ARG, "num_qk_heads = %d does not divide num_heads = %d", Hk, H);
-    if (N == 0 && T != 0) return set_error(KDA_ERR_INVALID_ARG, "tokens without sequences");
-    if (state_dtype < KDA_STATE_F32 || state_dtype > KDA_STATE_F16)
-        return set_error(KDA_ERR_UNSUPPORTED, "state_dtype %d not supported (0 fp32, 1 bf16, 2 fp16)",
-                         state_dtype);
-    if (!cu_seqlens && !cu_seqlens_host)
-        return set_error(KDA_ERR_INVALID_ARG, "cu_seqlens and cu_seqlens_host are both NULL");
-    if (cu_seqlens_host) {
-        rc = kda::check_bounds(cu_seqlens_host, N, T);
-        if (rc != KDA_OK) return rc;
-    }
-    const size_t g_bytes = sizeof(float) * (size_t)H * (decay_per_token ? (size_t)T : 1);
-    const Span so = view("out", out, T, H, D, (int64_t)H * D, D, 2);
-    Span ins[4] = {span("q", q, 0), span("k", k, 0), span("v", v, 0), span("log_decay", log_decay, 0)};
-    if (T > 0) {
-        if (!q || !k || !v || !log_decay || !out)
-            return set_error(KDA_ERR_INVALID_ARG, "a q/k/v/log_decay/out pointer is NULL");
-        const void* base[3] = {q, k, v};
-        const char* name[3] = {"q", "k", "v"};
-        const int64_t st[3] = {q_stride_t, k_stride_t, v_stride_t};
-        const int64_t sh[3] = {q_stride_h, k_stride_h, v_stride_h};
-        for (int i = 0; i < 3; ++i) {
-            const int heads = i == 2 ? H : Hk;
-            rc = check_view(name[i], T, heads, D, st[i], sh[i]);
-            if (rc != KDA_OK) return rc;
-            if (!aligned(base[i], 16) || st[i] % 8 != 0 || sh[i] % 8 != 0)
-                return set_error(KDA_ERR_UNSUPPORTED,
-                                 "%s and its strides must be 16-byte aligned", name[i]);
-            ins[i] = view(name[i], base[i], T, heads, D, st[i], sh[i], 2);
-        }
-        if (!aligned(out, 16)) return set_error(KDA_ERR_UNSUPPORTED, "out is not 16-byte aligned");
-        if (!aligned(log_decay, 4))
-            return set_error(KDA_ERR_UNSUPPORTED, "log_decay is not 4-byte aligned");
-        ins[3] = span("log_decay", log_decay, g_bytes);
-        for (const Span& r : ins)
-            if (overlap(so, r)) return set_error(KDA_ERR_INVALID_ARG, "out overlaps %s", r.name);
-    }
-    if (N == 0) return KDA_OK;
-    const size_t need = kda_lin_attn_workspace_size(T, N, H);
-    if (!workspace || workspace_bytes < need)
-        return set_error(KDA_ERR_WORKSPACE, "workspace of %zu bytes given, %zu needed",
-                         workspace ? workspace_bytes : (size_t)0, need);
-    if (!aligned(workspace, 256))
-        return set_error(KDA_ERR_UNSUPPORTED, "workspace is not 256-byte aligned");
-    const int64_t plane = (int64_t)H * D * D;
-    if (!state_cache || !state_indices || !has_initial_state)
-        return set_error(KDA_ERR_INVALID_ARG,
-                         "state_cache, state_indices and has_initial_state are required");
-    if (num_slots < N)
-        return set_error(KDA_ERR_INVALID_ARG, "num_slots %d < num_seqs %d (slots are distinct)",
-                         num_slots, N);
-    if (state_stride0 < plane || state_stride0 > (int64_t(1) << 58) / num_slots)
-        return set_error(KDA_ERR_INVALID_ARG,
-                         "state_stride0 %lld is smaller than the slot plane H*V*K = %lld, or out of range",
-                         (long long)state_stride0, (long long)plane);
-    const size_t elt = dtype_size(state_dtype);
-    if (!aligned(state_cache, 16) || ((size_t)state_stride0 * elt) % 16 != 0)
-        return set_error(KDA_ERR_UNSUPPORTED,
-                         "state_cache and its slot stride must be 16-byte aligned");
-    const Span sp = span("state_cache", state_cache,
-                         ((size_t)(num_slots - 1) * (size_t)state_stride0 + (size_t)plane) * elt);
-    const Span sw = span("workspace", workspace, need);
-    const Span with_pool[] = {ins[0], ins[1], ins[2], ins[3], so, sw};
-    for (const Span& r : with_pool)
-        if (overlap(sp, r)) return set_error(KDA_ERR_INVALID_ARG, "state_cache overlaps %s", r.name);
-    const Span with_ws[] = {ins[0], ins[1], ins[2], ins[3], so};
-    for (const Span& r : with_ws)
-        if (overlap(sw, r)) return set_error(KDA_ERR_INVALID_ARG, "workspace overlaps %s", r.name);
-
-    LinCall c{};
-    c.stream = reinterpret_cast<cudaStream_t>(stream);
-    kda::LinParams& p = c.p;
-    p.q = static_cast<const __nv_bfloat16*>(q);
-    p.k = static_cast<const __nv_bfloat16*>(k);
-    p.v = static_cast<const __nv_bfloat16*>(v);
-    p.q_st = q_stride_t, p.q_sh = q_stride_h;
-    p.k_st = k_stride_t, p.k_sh = k_stride_h;
-    p.v_st = v_stride_t, p.v_sh = v_stride_h;
-    p.g = log_decay;
-    p.g_st = decay_per_token ? H : 0;
-    p.out = static_cast<__nv_bfloat16*>(out);
-    p.scale = scale;
-    p.H = H, p.rep = H / Hk, p.N = N, p.T = T;
-    p.status = static_cast<int*>(workspace);
-    p.kept = reinterpret_cast<float*>(static_cast<char*>(workspace) + kda::kWsHeader);
-    p.planes = p.kept + 64 * kda::kLinPlanes;
-    p.pool = state_cache;
-    p.stride0 = state_stride0;
-    p.idx = state_indices;
-    p.has_init = has_initial_state;
-    p.num_slots = num_slots;
-    p.st_dtype = state_dtype;
-    return kda::with_seq_tables(cu_seqlens, cu_seqlens_host, N, T, c.stream, enqueue_lin, &c);
-}
-
-int kda_rope(const kda_rope_tensor* tensors, int32_t num_tensors, const void* positions,
-             int position_bytes, const double* inv_freq, int64_t total_tokens, int32_t head_dim,
-             int32_t rot_dim, int layout, float factor, int inverse, int dtype,
-             kda_stream_t stream) {
+// The checks of kda_rope and kda_qk_norm_rope, and their parameters; p.T stays 0 where there
+// is nothing to do.  `weights` are read beside the tensors (two, empty ones where there are none).
+int check_rope(const char* what, const kda_rope_tensor* tensors, int32_t num_tensors, const Span* weights,
+               const void* positions, int position_bytes, const double* inv_freq, int64_t total_tokens,
+               int32_t head_dim, int32_t rot_dim, int layout, float factor, int inverse, int dtype,
+               kda::RopeParams& p) {
     const int64_t T = total_tokens;
     int rc = check_tokens(T);
     if (rc != KDA_OK) return rc;
     if (!tensors || num_tensors < 1 || num_tensors > 2)
-        return set_error(KDA_ERR_INVALID_ARG, "kda_rope takes 1 or 2 tensors, got %d", num_tensors);
+        return set_error(KDA_ERR_INVALID_ARG, "%s takes 1 or 2 tensors, got %d", what, num_tensors);
     if (head_dim < 1 || head_dim > 1024)
         return set_error(KDA_ERR_UNSUPPORTED, "head_dim %d outside [1, 1024]", head_dim);
     if (rot_dim < 0 || rot_dim > head_dim || rot_dim % 2 != 0)
@@ -254,7 +281,6 @@ int kda_rope(const kda_rope_tensor* tensors, int32_t num_tensors, const void* po
     if (position_bytes != 4 && position_bytes != 8)
         return set_error(KDA_ERR_UNSUPPORTED, "positions of %d bytes (4 or 8)", position_bytes);
     const size_t elt = dtype_size(dtype);
-    kda::RopeParams p{};
     Span out[2] = {};
     Rows from[2] = {}, to[2] = {};
     for (int i = 0; i < num_tensors; ++i) {
@@ -289,9 +315,13 @@ int kda_rope(const kda_rope_tensor* tensors, int32_t num_tensors, const void* po
         return set_error(KDA_ERR_UNSUPPORTED, "positions or inv_freq is not aligned to its type");
     const Span sp = span("positions", positions, (size_t)T * position_bytes);
     const Span sf = span("inv_freq", inv_freq, (size_t)(rot_dim / 2) * 8);
-    for (int i = 0; i < num_tensors; ++i)
+    for (int i = 0; i < num_tensors; ++i) {
         if (overlap(out[i], sp) || overlap(out[i], sf))
             return set_error(KDA_ERR_INVALID_ARG, "out of tensor %d overlaps the positions or inv_freq", i);
+        for (int j = 0; j < num_tensors; ++j)
+            if (overlap(out[i], weights[j]))
+                return set_error(KDA_ERR_INVALID_ARG, "out of tensor %d overlaps a weight", i);
+    }
     p.pos = positions;
     p.pos64 = position_bytes == 8;
     p.inv_freq = inv_freq;
@@ -302,8 +332,110 @@ int kda_rope(const kda_rope_tensor* tensors, int32_t num_tensors, const void* po
     p.factor = factor;
     p.sign = inverse ? -1.f : 1.f;
     p.dtype = dtype;
+    return KDA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t kda_lin_attn_workspace_size(int64_t total_tokens, int32_t num_seqs, int32_t num_heads) {
+    if (total_tokens < 0 || num_seqs <= 0 || num_heads <= 0) return 0;
+    if (total_tokens <= (kda::kLinMinCut - 1) * 128) return kda::kWsHeader;  // nothing is cut
+    return kda::kWsHeader + (size_t)kda::kLinPlanes * (kda::kD * kda::kD + 64) * sizeof(float);
+}
+
+int kda_lin_attn_fwd(const void* q, int64_t q_stride_t, int64_t q_stride_h, const void* k,
+                     int64_t k_stride_t, int64_t k_stride_h, const void* v, int64_t v_stride_t,
+                     int64_t v_stride_h, const float* log_decay, int decay_per_token,
+                     const int32_t* cu_seqlens, const int32_t* cu_seqlens_host, int32_t num_seqs,
+                     int64_t total_tokens, int32_t num_heads, int32_t num_qk_heads,
+                     void* state_cache, int64_t state_stride0, int32_t num_slots,
+                     const int32_t* state_indices, const uint8_t* has_initial_state, void* out,
+                     float scale, int state_dtype, void* workspace, size_t workspace_bytes,
+                     kda_stream_t stream) {
+    const PackedCall a{q, k, v, q_stride_t, q_stride_h, k_stride_t, k_stride_h, v_stride_t, v_stride_h,
+                       log_decay, decay_per_token, nullptr, false, cu_seqlens, cu_seqlens_host, num_seqs,
+                       total_tokens, num_heads, num_qk_heads, state_cache, state_stride0, num_slots,
+                       state_indices, has_initial_state, out, scale, state_dtype, workspace, workspace_bytes};
+    const int rc = check_packed(a, kda_lin_attn_workspace_size(total_tokens, num_seqs, num_heads));
+    if (rc != KDA_OK || num_seqs == 0) return rc;
+    LinCall c{};
+    c.stream = reinterpret_cast<cudaStream_t>(stream);
+    set_params(a, c.p);
+    c.p.kept = reinterpret_cast<float*>(static_cast<char*>(workspace) + kda::kWsHeader);
+    c.p.planes = c.p.kept + 64 * kda::kLinPlanes;
+    return kda::with_seq_tables(cu_seqlens, cu_seqlens_host, num_seqs, total_tokens, c.stream, enqueue_lin, &c);
+}
+
+size_t kda_gated_delta_workspace_size(int64_t total_tokens, int32_t num_seqs, int32_t num_heads) {
+    if (total_tokens < 0 || num_seqs <= 0 || num_heads <= 0) return 0;
+    return kda::kWsHeader;
+}
+
+int kda_gated_delta_fwd(const void* q, int64_t q_stride_t, int64_t q_stride_h, const void* k,
+                        int64_t k_stride_t, int64_t k_stride_h, const void* v, int64_t v_stride_t,
+                        int64_t v_stride_h, const float* log_decay, int decay_per_token, const float* beta,
+                        const int32_t* cu_seqlens, const int32_t* cu_seqlens_host, int32_t num_seqs,
+                        int64_t total_tokens, int32_t num_heads, int32_t num_qk_heads,
+                        void* state_cache, int64_t state_stride0, int32_t num_slots,
+                        const int32_t* state_indices, const uint8_t* has_initial_state, void* out,
+                        float scale, int state_dtype, void* workspace, size_t workspace_bytes,
+                        kda_stream_t stream) {
+    const PackedCall a{q, k, v, q_stride_t, q_stride_h, k_stride_t, k_stride_h, v_stride_t, v_stride_h,
+                       log_decay, decay_per_token, beta, true, cu_seqlens, cu_seqlens_host, num_seqs,
+                       total_tokens, num_heads, num_qk_heads, state_cache, state_stride0, num_slots,
+                       state_indices, has_initial_state, out, scale, state_dtype, workspace, workspace_bytes};
+    const int rc = check_packed(a, kda_gated_delta_workspace_size(total_tokens, num_seqs, num_heads));
+    if (rc != KDA_OK || num_seqs == 0) return rc;
+    DeltaCall c{};
+    c.stream = reinterpret_cast<cudaStream_t>(stream);
+    set_params(a, c.p);
+    c.p.beta = beta;
+    return kda::with_seq_tables(cu_seqlens, cu_seqlens_host, num_seqs, total_tokens, c.stream, enqueue_delta, &c);
+}
+
+int kda_rope(const kda_rope_tensor* tensors, int32_t num_tensors, const void* positions,
+             int position_bytes, const double* inv_freq, int64_t total_tokens, int32_t head_dim,
+             int32_t rot_dim, int layout, float factor, int inverse, int dtype,
+             kda_stream_t stream) {
+    kda::RopeParams p{};
+    const Span none[2] = {};
+    const int rc = check_rope("kda_rope", tensors, num_tensors, none, positions, position_bytes, inv_freq,
+                              total_tokens, head_dim, rot_dim, layout, factor, inverse, dtype, p);
+    if (rc != KDA_OK || p.T == 0) return rc;
     const cudaError_t e = kda::launch_rope(p, reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? KDA_OK : cuda_error(e, "kda_rope");
+}
+
+int kda_qk_norm_rope(const kda_norm_rope_tensor* tensors, int32_t num_tensors, float eps,
+                     const void* positions, int position_bytes, const double* inv_freq,
+                     int64_t total_tokens, int32_t head_dim, int32_t rot_dim, int layout, float factor,
+                     int dtype, kda_stream_t stream) {
+    if (!tensors || num_tensors < 1 || num_tensors > 2)
+        return set_error(KDA_ERR_INVALID_ARG, "kda_qk_norm_rope takes 1 or 2 tensors, got %d", num_tensors);
+    if (!(eps >= 0.f)) return set_error(KDA_ERR_INVALID_ARG, "eps %g is negative", (double)eps);
+    kda::NormRopeParams p{};
+    kda_rope_tensor x[2] = {};
+    Span weights[2] = {};
+    for (int i = 0; i < num_tensors; ++i) {
+        const kda_norm_rope_tensor& t = tensors[i];
+        x[i] = t.x;
+        if (!t.weight || t.x.num_heads <= 0 || head_dim < 1) continue;
+        if (!aligned(t.weight, 4)) return set_error(KDA_ERR_UNSUPPORTED, "weight %d is not 4-byte aligned", i);
+        const int64_t sh = t.x.num_heads > 1 ? t.weight_stride_h : 0;
+        if (sh < 0 || sh > (int64_t(1) << 40))
+            return set_error(KDA_ERR_INVALID_ARG, "weight_stride_h %lld is out of range", (long long)sh);
+        weights[i] = span("weight", t.weight, (size_t)((t.x.num_heads - 1) * sh + head_dim) * 4);
+        p.weight[i] = t.weight;
+        p.weight_sh[i] = sh;
+    }
+    p.eps = eps;
+    const int rc = check_rope("kda_qk_norm_rope", x, num_tensors, weights, positions, position_bytes, inv_freq,
+                              total_tokens, head_dim, rot_dim, layout, factor, 0, dtype, p);
+    if (rc != KDA_OK || p.T == 0) return rc;
+    const cudaError_t e = kda::launch_qk_norm_rope(p, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? KDA_OK : cuda_error(e, "kda_qk_norm_rope");
 }
 
 int kda_gated_norm(const void* x, int64_t x_stride_t, int64_t x_stride_h, const void* gate,

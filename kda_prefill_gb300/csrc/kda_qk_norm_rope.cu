@@ -1,0 +1,231 @@
+// Norms of queries and keys for each head with the rotary positions in the same pass:
+//
+//     y = x / sqrt(mean(x^2) + eps) * weight,   pairs of y's first rot dimensions turned
+//
+// Bound by reading and writing the heads once.  As in kda_rope a row is cut into units, 16
+// bytes and their partners of the half layout, and a thread keeps its unit of its head and
+// goes through a CTA's tokens, so that it reads its weights once.  A row's lanes lie beside
+// each other in a warp and sum its squares by shuffles; the row stays in registers.  Longer
+// rows, and rows that are not whole pieces, take a warp each, which reads them twice.
+
+#include "kda_rope.cuh"
+
+namespace kda {
+namespace {
+
+using rope::Unit;
+
+constexpr int kMaxThreads = 512;
+constexpr int kMaxTable = 2048;  // pairs times tokens a CTA holds (16 KB)
+
+template <int LANES>
+__device__ __forceinline__ float group_sum(float x) {
+#pragma unroll
+    for (int w = LANES / 2; w >= 1; w >>= 1) x += __shfl_xor_sync(0xffffffffu, x, w);
+    return x;
+}
+
+template <int VE>
+__device__ __forceinline__ void load_weights(float (&w)[VE], const float* p) {
+#pragma unroll
+    for (int j = 0; j < VE; ++j) w[j] = p ? p[j] : 1.f;
+}
+
+// `units` units a row, at most LANES, the first rot_units of them turned.
+template <class E, int VE, bool IL, int LANES>
+__global__ void __launch_bounds__(kMaxThreads)
+kda_qk_norm_rope(const __grid_constant__ NormRopeParams p, int tokens, int rot_units, int units) {
+    using U = Unit<E, VE, IL>;
+    __shared__ float2 table[kMaxTable];
+    constexpr int kAhead = 2;
+    const int half = p.rot >> 1;
+    const int64_t t0 = (int64_t)blockIdx.x * tokens;
+    const int nt = (int)min((int64_t)tokens, p.T - t0);
+    const int h0 = p.x[0].heads, items = (h0 + p.x[1].heads) * LANES;
+    const float per = 1.f / (float)p.D;
+    bool made = false;
+    // whole warps go on together
+    for (int item = threadIdx.x; (item & ~31) < items || !made; item += blockDim.x) {
+        int h = item / LANES;
+        const int u = item % LANES;
+        const bool live = item < items && u < units;
+        const int which = h >= h0;
+        const RopeTensor& r = p.x[which];
+        if (which) h -= h0;
+        const bool turned = live && u < rot_units;
+        const bool two = U::kPaired && turned;
+        const int at = U::one(p, u, rot_units), at2 = U::two(p, u);
+        const int64_t in_st = r.in_st, out_st = r.out_st;
+        const E* in = static_cast<const E*>(r.in) + t0 * in_st + (int64_t)h * r.in_sh;
+        E* out = static_cast<E*>(r.out) + t0 * out_st + (int64_t)h * r.out_sh;
+        const int n = live ? nt : 0;
+        U x[kAhead] = {};
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (i < n) x[i].load(in + i * in_st, at, at2, turned);
+        float w1[VE], w2[VE];
+        const float* weight = live && p.weight[which] ? p.weight[which] + (int64_t)h * p.weight_sh[which] : nullptr;
+        load_weights<VE>(w1, weight ? weight + at : nullptr);
+        load_weights<VE>(w2, weight && two ? weight + at2 : nullptr);
+        if (!made) {
+            for (int i = threadIdx.x; i < nt * half; i += blockDim.x) {
+                const int t = i / half, j = i - t * half;
+                table[i] = rope::turn_of(p, t0 + t, j);
+            }
+            __syncthreads();
+            made = true;
+        }
+        const float2* cs = table + (U::kPaired ? u * VE : u * VE / 2);
+        for (int t = 0; t < nt; t += kAhead) {
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                float f[VE], g[VE];
+                x[i].a.get(f);
+                if constexpr (U::kPaired) x[i].b.get(g);
+                float sum = 0.f;
+#pragma unroll
+                for (int j = 0; j < VE; ++j) sum = fmaf(f[j], f[j], sum);
+                if constexpr (U::kPaired) {
+                    if (two) {
+#pragma unroll
+                        for (int j = 0; j < VE; ++j) sum = fmaf(g[j], g[j], sum);
+                    }
+                }
+                sum = group_sum<LANES>(live ? sum : 0.f);
+                const float inv = 1.f / sqrtf(fmaf(sum, per, p.eps));
+                if (t + i < n) {
+#pragma unroll
+                    for (int j = 0; j < VE; ++j) f[j] *= inv * w1[j];
+                    if constexpr (U::kPaired) {
+#pragma unroll
+                        for (int j = 0; j < VE; ++j) g[j] *= inv * w2[j];
+                    }
+                    if (turned) U::turn(f, g, cs + i * half);
+                    x[i].a.set(f);
+                    if constexpr (U::kPaired) x[i].b.set(g);
+                    x[i].store(out + i * out_st, at, at2, turned);
+                }
+            }
+            cs += kAhead * half;
+            in += kAhead * in_st;
+            out += kAhead * out_st;
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i)
+                if (t + kAhead + i < n) x[i].load(in + i * in_st, at, at2, turned);
+        }
+    }
+}
+
+// Rows of more units: a warp each, the row read again for its products.
+template <class E, int VE, bool IL>
+__global__ void __launch_bounds__(kMaxThreads)
+kda_qk_norm_rope_long(const __grid_constant__ NormRopeParams p, int tokens, int rot_units, int units) {
+    using U = Unit<E, VE, IL>;
+    __shared__ float2 table[kMaxTable];
+    const int half = p.rot >> 1;
+    const int64_t t0 = (int64_t)blockIdx.x * tokens;
+    const int nt = (int)min((int64_t)tokens, p.T - t0);
+    for (int i = threadIdx.x; i < nt * half; i += blockDim.x) {
+        const int t = i / half, j = i - t * half;
+        table[i] = rope::turn_of(p, t0 + t, j);
+    }
+    __syncthreads();
+    const int h0 = p.x[0].heads, heads = h0 + p.x[1].heads, lane = threadIdx.x & 31;
+    for (int row = threadIdx.x >> 5; row < nt * heads; row += blockDim.x >> 5) {
+        const int t = row / heads;
+        int h = row - t * heads;
+        const int which = h >= h0;
+        const RopeTensor& r = p.x[which];
+        if (which) h -= h0;
+        const E* in = static_cast<const E*>(r.in) + (t0 + t) * r.in_st + (int64_t)h * r.in_sh;
+        E* out = static_cast<E*>(r.out) + (t0 + t) * r.out_st + (int64_t)h * r.out_sh;
+        const float* weight = p.weight[which] ? p.weight[which] + (int64_t)h * p.weight_sh[which] : nullptr;
+        float sum = 0.f;
+        for (int c = lane * VE; c < p.D; c += 32 * VE) {
+            float f[VE];
+            rows::load<E, VE>(in + c).get(f);
+#pragma unroll
+            for (int j = 0; j < VE; ++j) sum = fmaf(f[j], f[j], sum);
+        }
+        const float inv = 1.f / sqrtf(group_sum<32>(sum) / (float)p.D + p.eps);
+        __syncwarp();  // in place: all lanes have read the row
+        for (int u = lane; u < units; u += 32) {
+            const bool turned = u < rot_units;
+            const int at = U::one(p, u, rot_units), at2 = U::two(p, u);
+            U x = {};
+            x.load(in, at, at2, turned);
+            float f[VE], g[VE], w1[VE], w2[VE];
+            load_weights<VE>(w1, weight ? weight + at : nullptr);
+            load_weights<VE>(w2, weight && U::kPaired && turned ? weight + at2 : nullptr);
+            x.a.get(f);
+            if constexpr (U::kPaired) x.b.get(g);
+#pragma unroll
+            for (int j = 0; j < VE; ++j) f[j] *= inv * w1[j];
+            if constexpr (U::kPaired) {
+#pragma unroll
+                for (int j = 0; j < VE; ++j) g[j] *= inv * w2[j];
+            }
+            if (turned) U::turn(f, g, table + t * half + (U::kPaired ? u * VE : u * VE / 2));
+            x.a.set(f);
+            if constexpr (U::kPaired) x.b.set(g);
+            x.store(out, at, at2, turned);
+        }
+    }
+}
+
+template <class E, int VE, bool IL, int LANES>
+cudaError_t launch(const NormRopeParams& p, int rot_units, int units, cudaStream_t s) {
+    const int half = p.rot / 2;
+    // tokens per CTA: eight, at most what the table holds, and few enough that each SM
+    // has eight CTAs where there are so many tokens
+    int tokens = max(1, min(8, kMaxTable / max(1, half)));
+    tokens = (int)max((int64_t)1, min((int64_t)tokens, p.T / (8 * num_sms())));
+    const int64_t grid = (p.T + tokens - 1) / tokens;
+    const int heads = p.x[0].heads + p.x[1].heads;
+    if constexpr (LANES == 0) {
+        const int threads = (int)min((int64_t)kMaxThreads, (int64_t)heads * tokens * 32);
+        kda_qk_norm_rope_long<E, VE, IL><<<(unsigned)grid, max(128, threads), 0, s>>>(p, tokens, rot_units, units);
+    } else {
+        // threads: as many as a token's units in the fewest rounds, in whole warps
+        const int items = heads * LANES;
+        const int rounds = (items + kMaxThreads - 1) / kMaxThreads;
+        const int threads = max(128, ((items + rounds - 1) / rounds + 31) / 32 * 32);
+        kda_qk_norm_rope<E, VE, IL, LANES><<<(unsigned)grid, threads, 0, s>>>(p, tokens, rot_units, units);
+    }
+    return cudaGetLastError();
+}
+
+template <class E, int VE, bool IL>
+cudaError_t by_units(const NormRopeParams& p, cudaStream_t s) {
+    const int rot_units = IL && VE > 1 ? p.rot / VE : p.rot / 2 / VE;
+    const int units = rot_units + (p.D - p.rot) / VE;
+    if constexpr (VE > 1) {
+        if (units <= 8) return launch<E, VE, IL, 8>(p, rot_units, units, s);
+        if (units <= 16) return launch<E, VE, IL, 16>(p, rot_units, units, s);
+        if (units <= 32) return launch<E, VE, IL, 32>(p, rot_units, units, s);
+    }
+    return launch<E, VE, IL, 0>(p, rot_units, units, s);
+}
+
+template <class E>
+cudaError_t dispatch(const NormRopeParams& p, cudaStream_t s) {
+    constexpr int VE = 16 / sizeof(E);
+    // 16-byte units when the dimensions, strides and bases allow them
+    bool vec = (p.interleaved ? p.rot : p.rot / 2) % VE == 0 && (p.D - p.rot) % VE == 0;
+    for (const RopeTensor& x : p.x)
+        if (x.heads)
+            vec = vec && ((reinterpret_cast<uintptr_t>(x.in) | reinterpret_cast<uintptr_t>(x.out)) & 15) == 0 &&
+                  (x.in_st | x.in_sh | x.out_st | x.out_sh) % VE == 0;
+    if (p.interleaved) return vec ? by_units<E, VE, true>(p, s) : by_units<E, 1, true>(p, s);
+    return vec ? by_units<E, VE, false>(p, s) : by_units<E, 1, false>(p, s);
+}
+
+}  // namespace
+
+cudaError_t launch_qk_norm_rope(const NormRopeParams& p, cudaStream_t s) {
+    if (p.dtype == KDA_F32) return dispatch<float>(p, s);
+    if (p.dtype == KDA_BF16) return dispatch<__nv_bfloat16>(p, s);
+    return dispatch<__half>(p, s);
+}
+
+}  // namespace kda

@@ -1,11 +1,6 @@
 // Rotary positions: y1 = c x1 - s x2, y2 = c x2 + s x1 for each pair of a head's
 // first rot dimensions, with (c, s) of one token and pair shared by all heads.
 //
-// The angle p f is wanted modulo one turn.  f / 2 pi is rounded to a 64-bit
-// fraction of a turn F; then p F mod 2^64 is the phase, exactly, in one integer
-// product (two's complement wraps as turns do), and its top 32 bits give the
-// argument of sincospi.  A fp32 product p f would be off by p 2^-25 radians.
-//
 // Bound by reading and writing the heads once.  A token's heads are cut into units of
 // 16 bytes and their partners (half layout: the 16 bytes rot / 2 further), or of 16
 // bytes to copy.  A CTA takes a few tokens; a thread keeps its unit of its head and goes
@@ -15,63 +10,15 @@
 // the start and the end of a launch.  All of each turned in the half layout: 46.4 us in bf16,
 // 64 %, and 66.0 us in fp32, 90 %.
 
-#include "kda_ops.h"
-#include "kda_rows.cuh"
+#include "kda_rope.cuh"
 
 namespace kda {
 namespace {
 
+using rope::Unit;
+
 constexpr int kMaxThreads = 512;
 constexpr int kMaxTable = 2048;  // pairs times tokens a CTA holds (16 KB)
-
-// One unit of a row: 16 bytes, and for pairs of the half layout (and for the narrow
-// form's pairs) the partner's.
-template <class E, int VE, bool IL>
-struct Unit {
-    rows::Piece<E, VE> a, b;
-    static constexpr bool kPaired = !IL || VE == 1;
-
-    // Offsets of the two in a row; units from rot_units on are copied.
-    static __device__ __forceinline__ int one(const RopeParams& p, int u, int rot_units) {
-        if (u >= rot_units) return p.rot + (u - rot_units) * VE;
-        return IL && VE == 1 ? 2 * u : u * VE;
-    }
-    static __device__ __forceinline__ int two(const RopeParams& p, int u) {
-        return IL ? 2 * u + 1 : (p.rot >> 1) + u * VE;
-    }
-    __device__ __forceinline__ void load(const E* in, int at, int at2, bool turned) {
-        a = rows::load<E, VE>(in + at);
-        if (kPaired && turned) b = rows::load<E, VE>(in + at2);
-    }
-    __device__ __forceinline__ void turn(const float2* cs) {
-        float f[VE], g[VE];
-        a.get(f);
-        if constexpr (kPaired) {
-            b.get(g);
-#pragma unroll
-            for (int j = 0; j < VE; ++j) {
-                const float2 w = cs[j];
-                const float x1 = f[j], x2 = g[j];
-                f[j] = x1 * w.x - x2 * w.y;
-                g[j] = x2 * w.x + x1 * w.y;
-            }
-            b.set(g);
-        } else {
-#pragma unroll
-            for (int j = 0; j < VE; j += 2) {
-                const float2 w = cs[j / 2];
-                const float x1 = f[j], x2 = f[j + 1];
-                f[j] = x1 * w.x - x2 * w.y;
-                f[j + 1] = x2 * w.x + x1 * w.y;
-            }
-        }
-        a.set(f);
-    }
-    __device__ __forceinline__ void store(E* out, int at, int at2, bool turned) const {
-        rows::store<E, VE>(out + at, a);
-        if (kPaired && turned) rows::store<E, VE>(out + at2, b);
-    }
-};
 
 // `units` units a row, the first rot_units of them turned.
 template <class E, int VE, bool IL>
@@ -103,15 +50,7 @@ __global__ void __maxnreg__(56) kda_rope(RopeParams p, int tokens, int rot_units
         if (!made) {
             for (int i = threadIdx.x; i < nt * half; i += blockDim.x) {
                 const int t = i / half, j = i - t * half;
-                const int64_t pos = p.pos64 ? static_cast<const int64_t*>(p.pos)[t0 + t]
-                                            : (int64_t) static_cast<const int32_t*>(p.pos)[t0 + t];
-                const double turns = p.inv_freq[j] * 0.15915494309189533577;  // 1 / 2 pi
-                const long long F = __double2ll_rn((turns - rint(turns)) * 18446744073709551616.0);
-                const unsigned long long phase = (unsigned long long)pos * (unsigned long long)F;
-                const float a = (float)(int)(phase >> 32) * 4.656612873077392578125e-10f;  // 2^-31
-                float s, c;
-                sincospif(a, &s, &c);
-                table[i] = make_float2(c * p.factor, s * p.factor * p.sign);
+                table[i] = rope::turn_of(p, t0 + t, j);
             }
             __syncthreads();
             made = true;

@@ -2,7 +2,11 @@
 linear-attention layer, in the order it runs them.
 
     kda.rope(q, k, positions, inv_freq, ...)      rotary positions
+    kda.qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, ...)
+                                                  the same behind a norm of q and k
     kda.lin_attn_fwd(q, k, v, log_decay, ...)     linear attention over a paged pool
+    kda.gated_delta_fwd(q, k, v, log_decay, beta, ...)
+                                                  the gated delta rule over the pool
     kda.gated_norm(o, weight, gate=z, ...)        norm and gate of the output
 
 Argument marshalling only; the kernels are in ``libkda.so`` (``include/kda.h``
@@ -32,6 +36,10 @@ class _RopeTensor(ctypes.Structure):
                 ("in_stride_t", ctypes.c_int64), ("in_stride_h", ctypes.c_int64),
                 ("out_stride_t", ctypes.c_int64), ("out_stride_h", ctypes.c_int64),
                 ("num_heads", ctypes.c_int32)]
+
+
+class _NormRopeTensor(ctypes.Structure):
+    _fields_ = [("x", _RopeTensor), ("weight", ctypes.c_void_p), ("weight_stride_h", ctypes.c_int64)]
 
 
 def _rows(x: torch.Tensor, name: str, dtype=None):
@@ -110,14 +118,79 @@ def lin_attn_fwd(q, k, v, log_decay, cu_seqlens, *, state_cache, state_indices,
     allocation, about 5 us of the 18 that a call takes on the host.  Writes ``out``
     and the selected pool slots in place and returns ``out``."""
     lib = load_library()
-    bf16, dev = torch.bfloat16, q.device
+    dev = q.device
+    T, Hk, H, N, (q_st, q_sh, k_st, k_sh, v_st, v_sh) = _packed(
+        q, k, v, log_decay, cu_seqlens, state_cache, state_indices, has_initial_state, out)
+    _on_current_device(q.get_device())
+    host = None if cu_seqlens_cpu is None else _host_int32(cu_seqlens_cpu, N)
+    workspace, given = _packed_workspace(lin_attn_workspace_size(T, N, H), workspace, dev, stream)
+    rc = lib.kda_lin_attn_fwd(
+        q.data_ptr(), q_st, q_sh, k.data_ptr(), k_st, k_sh, v.data_ptr(), v_st, v_sh,
+        log_decay.data_ptr(), log_decay.dim() > 1, cu_seqlens.data_ptr(),
+        None if host is None else host.data_ptr(), N, T, H, Hk,
+        state_cache.data_ptr(), state_cache.stride(0), state_cache.shape[0],
+        state_indices.data_ptr(), has_initial_state.data_ptr(), out.data_ptr(),
+        0.08838834764831845 if scale is None else float(scale), STATE_DTYPES[state_cache.dtype],
+        workspace.data_ptr(), given, _stream(stream, dev))
+    if rc != KDA_OK:
+        _check(rc, lib)
+    return out
+
+
+@functools.lru_cache(maxsize=1024)
+def gated_delta_workspace_size(total_tokens: int, num_seqs: int, num_heads: int) -> int:
+    """Bytes of workspace a ``gated_delta_fwd`` call with these sizes needs."""
+    return int(load_library().kda_gated_delta_workspace_size(total_tokens, num_seqs, num_heads))
+
+
+def gated_delta_fwd(q, k, v, log_decay, beta, cu_seqlens, *, state_cache, state_indices,
+                    has_initial_state, out, scale: Optional[float] = None, cu_seqlens_cpu=None,
+                    workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The gated delta rule with a decay for each head (``kda_gated_delta_fwd``):
+
+        S_t = exp(g_t) S_{t-1} (I - beta_t k_t k_t^T) + beta_t v_t k_t^T,  o_t = scale * S_t q_t
+
+    with q and k divided by their lengths.  Tensors, pool and options are those of
+    ``lin_attn_fwd``; ``beta`` is contiguous fp32 [1, T, H] (or [T, H]), from 0 to 2.
+    Prompts, ragged batches and single tokens go in one call.  Writes ``out`` and
+    the selected pool slots in place and returns ``out``."""
+    lib = load_library()
+    dev, at = q.device, q.get_device()
+    T, Hk, H, N, (q_st, q_sh, k_st, k_sh, v_st, v_sh) = _packed(
+        q, k, v, log_decay, cu_seqlens, state_cache, state_indices, has_initial_state, out)
+    if beta.dtype is not torch.float32 or not beta.is_cuda:
+        raise TypeError("beta must be a float32 CUDA tensor")
+    if beta.get_device() != at:
+        _same_device(dev, beta=beta)
+    bs = beta.shape
+    if not beta.is_contiguous() or not (bs == (1, T, H) or bs == (T, H)):
+        raise ValueError(f"beta must be a contiguous [1, T, H] tensor; got shape {tuple(bs)}")
+    _on_current_device(at)
+    host = None if cu_seqlens_cpu is None else _host_int32(cu_seqlens_cpu, N)
+    workspace, given = _packed_workspace(gated_delta_workspace_size(T, N, H), workspace, dev, stream)
+    rc = lib.kda_gated_delta_fwd(
+        q.data_ptr(), q_st, q_sh, k.data_ptr(), k_st, k_sh, v.data_ptr(), v_st, v_sh,
+        log_decay.data_ptr(), log_decay.dim() > 1, beta.data_ptr(), cu_seqlens.data_ptr(),
+        None if host is None else host.data_ptr(), N, T, H, Hk,
+        state_cache.data_ptr(), state_cache.stride(0), state_cache.shape[0],
+        state_indices.data_ptr(), has_initial_state.data_ptr(), out.data_ptr(),
+        0.08838834764831845 if scale is None else float(scale), STATE_DTYPES[state_cache.dtype],
+        workspace.data_ptr(), given, _stream(stream, dev))
+    if rc != KDA_OK:
+        _check(rc, lib)
+    return out
+
+
+def _packed(q, k, v, log_decay, cu_seqlens, state_cache, state_indices, hs, out):
+    """(T, Hqk, H, N, strides of q, k and v) of a call over packed sequences and the pool
+    of their states, its arguments checked."""
+    bf16 = torch.bfloat16
     at = q.get_device()  # -1 without a GPU
     qs, vs, ps, gs = q.shape, v.shape, state_cache.shape, log_decay.shape
-    (_, q_st, q_sh, q_1), (_, k_st, k_sh, k_1), (_, v_st, v_sh, v_1), (p_st, *plane) = (
+    (_, q_st, q_sh, q_1), (_, k_st, k_sh, k_1), (_, v_st, v_sh, v_1), (_, *plane) = (
         x.stride() if x.dim() == 4 else (0, 0, 0, 0) for x in (q, k, v, state_cache))
     N = cu_seqlens.numel() - 1
-    hs = has_initial_state
-    # One look at the usual forms; _lin_args looks at each argument, takes the others and
+    # One look at the usual forms; _packed_args looks at each argument, takes the others and
     # says what is wrong.
     if (at >= 0 and q_1 == k_1 == v_1 == 1 and plane == [16384, 128, 1]
             and qs[0] == vs[0] == 1 and qs[3] == vs[3] == 128
@@ -144,34 +217,24 @@ def lin_attn_fwd(q, k, v, log_decay, cu_seqlens, *, state_cache, state_indices,
         if H == 1:
             v_sh = 128
     else:
-        T, Hk, H, N, (q_st, q_sh, k_st, k_sh, v_st, v_sh) = _lin_args(
+        T, Hk, H, N, (q_st, q_sh, k_st, k_sh, v_st, v_sh) = _packed_args(
             q, k, v, log_decay, cu_seqlens, state_cache, state_indices, hs, out)
-    _on_current_device(at)
-    host = None if cu_seqlens_cpu is None else _host_int32(cu_seqlens_cpu, N)
-    need = lin_attn_workspace_size(T, N, H)
+    return T, Hk, H, N, (q_st, q_sh, k_st, k_sh, v_st, v_sh)
+
+
+def _packed_workspace(need, workspace, dev, stream):
+    """(workspace, its bytes): a new one, or the caller's once it is checked."""
     if workspace is None:
-        workspace = _empty(max(need, 256), torch.uint8, dev, stream)
-        given = need
-    elif workspace.device != dev or not workspace.is_contiguous():
+        return _empty(max(need, 256), torch.uint8, dev, stream), need
+    if workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {dev}")
-    else:
-        given = workspace.numel() * workspace.element_size()
-        if given < need:
-            raise ValueError(f"workspace too small: {need} bytes needed")
-    rc = lib.kda_lin_attn_fwd(
-        q.data_ptr(), q_st, q_sh, k.data_ptr(), k_st, k_sh, v.data_ptr(), v_st, v_sh,
-        log_decay.data_ptr(), len(gs) > 1, cu_seqlens.data_ptr(),
-        None if host is None else host.data_ptr(), N, T, H, Hk,
-        state_cache.data_ptr(), p_st, ps[0],
-        state_indices.data_ptr(), hs.data_ptr(), out.data_ptr(),
-        0.08838834764831845 if scale is None else float(scale), STATE_DTYPES[state_cache.dtype],
-        workspace.data_ptr(), given, _stream(stream, dev))
-    if rc != KDA_OK:
-        _check(rc, lib)
-    return out
+    given = workspace.numel() * workspace.element_size()
+    if given < need:
+        raise ValueError(f"workspace too small: {need} bytes needed")
+    return workspace, given
 
 
-def _lin_args(q, k, v, log_decay, cu_seqlens, state_cache, state_indices, hs, out):
+def _packed_args(q, k, v, log_decay, cu_seqlens, state_cache, state_indices, hs, out):
     """(T, Hqk, H, N, strides of q, k and v), every argument checked for itself."""
     bf16 = torch.bfloat16
     T, Hk, D, q_st, q_sh = _rows(q, "q", bf16)
@@ -260,15 +323,8 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, *, scaling: Optional[s
     return torch.tensor(freq, dtype=torch.float64, device=device), amplitude
 
 
-def rope(q, k, positions, inv_freq, *, layout: str = "half", factor: float = 1.0,
-         q_out=None, k_out=None, inverse: bool = False, stream=None):
-    """Rotary positions on q [1, T, Hq, D] and, unless None, k [1, T, Hk, D]
-    (``kda_rope``): the first 2 * len(inv_freq) dimensions of each head turn by
-    position * inv_freq, the others are kept.  ``positions`` is int32 or int64
-    [T], ``inv_freq`` fp64, as from ``rope_frequencies``.  Without ``q_out`` and
-    ``k_out`` it works in place.  ``inverse`` turns back (times ``factor`` again):
-    the gradient of the inputs from that of the outputs.  Returns (q_out, k_out)."""
-    lib = load_library()
+def _rope_rows(q, k, positions, inv_freq, layout, q_out, k_out):
+    """(the fields of q's and k's ``_RopeTensor``, D), every argument checked."""
     if layout not in _LAYOUTS:
         raise ValueError(f"layout {layout!r} is not one of {sorted(_LAYOUTS)}")
     if q.dtype not in _DTYPES:
@@ -278,8 +334,7 @@ def rope(q, k, positions, inv_freq, *, layout: str = "half", factor: float = 1.0
         raise ValueError("k_out is given without k")
     k_out = k if k_out is None else k_out
     T, _, D, _, _ = _rows(q, "q")
-    arr = (_RopeTensor * 2)()
-    n = 0
+    rows = []
     for name, x, y in (("q", q, q_out), ("k", k, k_out)):
         if x is None:
             continue
@@ -287,8 +342,7 @@ def rope(q, k, positions, inv_freq, *, layout: str = "half", factor: float = 1.0
         To, Ho, Do, ost, osh = (Tx, H, Dx, st, sh) if y is x else _rows(y, name + "_out", q.dtype)
         if Tx != T or Dx != D or To != Tx or Ho != H or Do != Dx:
             raise ValueError(f"{name} and {name}_out must be [1, T, H, D] with q's T and D")
-        arr[n] = (x.data_ptr(), y.data_ptr(), st, sh, ost, osh, H)
-        n += 1
+        rows.append((x.data_ptr(), y.data_ptr(), st, sh, ost, osh, H))
     if positions.dtype not in (torch.int32, torch.int64) or not positions.is_cuda:
         raise TypeError("positions must be an int32 or int64 CUDA tensor")
     if positions.numel() != T or not positions.is_contiguous():
@@ -302,12 +356,65 @@ def rope(q, k, positions, inv_freq, *, layout: str = "half", factor: float = 1.0
             and (k is None or k.get_device() == k_out.get_device() == at)):
         _same_device(dev, k=k, q_out=q_out, k_out=k_out, positions=positions, inv_freq=inv_freq)
     _on_current_device(at)
+    return rows, D
+
+
+def rope(q, k, positions, inv_freq, *, layout: str = "half", factor: float = 1.0,
+         q_out=None, k_out=None, inverse: bool = False, stream=None):
+    """Rotary positions on q [1, T, Hq, D] and, unless None, k [1, T, Hk, D]
+    (``kda_rope``): the first 2 * len(inv_freq) dimensions of each head turn by
+    position * inv_freq, the others are kept.  ``positions`` is int32 or int64
+    [T], ``inv_freq`` fp64, as from ``rope_frequencies``.  Without ``q_out`` and
+    ``k_out`` it works in place.  ``inverse`` turns back (times ``factor`` again):
+    the gradient of the inputs from that of the outputs.  Returns (q_out, k_out)."""
+    lib = load_library()
+    rows, D = _rope_rows(q, k, positions, inv_freq, layout, q_out, k_out)
+    q_out, k_out = q if q_out is None else q_out, k if k_out is None else k_out
+    T, n = positions.numel(), len(rows)
+    arr = (_RopeTensor * 2)(*rows)
     rc = lib.kda_rope(arr, n, positions.data_ptr(), positions.element_size(),
                       inv_freq.data_ptr(), T, D, 2 * inv_freq.numel(), _LAYOUTS[layout],
-                      float(factor), 1 if inverse else 0, _DTYPES[q.dtype], _stream(stream, dev))
+                      float(factor), 1 if inverse else 0, _DTYPES[q.dtype], _stream(stream, q.device))
     if rc != KDA_OK:
         _check(rc, lib)
     return q_out, k_out
+
+
+def _head_weight(w, name, H, D):
+    """(address, elements between heads) of a norm's weights."""
+    if w is None:
+        return None, 0
+    if w.dtype != torch.float32 or not w.is_cuda:
+        raise TypeError(f"{name} must be a float32 CUDA tensor")
+    if tuple(w.shape) not in ((D,), (H, D)) or not w.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous [{D}] or [{H}, {D}] tensor; got shape "
+                         f"{tuple(w.shape)}")
+    return w.data_ptr(), D if w.dim() == 2 else 0
+
+
+def qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, *, layout: str = "half",
+                 factor: float = 1.0, eps: float = 1e-6, q_out=None, k_out=None, stream=None):
+    """Norms of queries and keys for each head and the rotary positions in one pass
+    (``kda_qk_norm_rope``): each row of q [1, T, Hq, D] and, unless None, k [1, T, Hk, D]
+    becomes x / sqrt(mean(x^2) + eps) * weight and is then turned as by ``rope``.
+    ``q_weight`` and ``k_weight`` are fp32 [D], [H, D] for a weight of each head, or
+    None.  The other arguments are those of ``rope``; without ``q_out`` and ``k_out``
+    it works in place.  Returns (q_out, k_out)."""
+    lib = load_library()
+    rows, D = _rope_rows(q, k, positions, inv_freq, layout, q_out, k_out)
+    if k is None and k_weight is not None:
+        raise ValueError("k_weight is given without k")
+    arr = (_NormRopeTensor * 2)()
+    for i, (w, name) in enumerate(((q_weight, "q_weight"), (k_weight, "k_weight"))[:len(rows)]):
+        arr[i] = (rows[i], *_head_weight(w, name, rows[i][6], D))
+        if w is not None and w.get_device() != q.get_device():
+            _same_device(q.device, **{name: w})
+    rc = lib.kda_qk_norm_rope(arr, len(rows), float(eps), positions.data_ptr(), positions.element_size(),
+                              inv_freq.data_ptr(), positions.numel(), D, 2 * inv_freq.numel(),
+                              _LAYOUTS[layout], float(factor), _DTYPES[q.dtype], _stream(stream, q.device))
+    if rc != KDA_OK:
+        _check(rc, lib)
+    return q if q_out is None else q_out, k if k_out is None else k_out
 
 
 def gated_norm(x, weight=None, *, gate=None, activation: str = "sigmoid", eps: float = 1e-6,
