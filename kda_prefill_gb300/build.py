@@ -14,7 +14,8 @@ LIB = os.path.join(PKG, "libkda.so")
 
 SOURCES = ["kda_api.cu", "kda_kernels.cu", "kda_intra.cu", "kda_intra_tc.cu", "kda_scan.cu",
            "kda_decode.cu", "kda_ops_api.cu", "kda_lin_step.cu", "kda_lin_walk.cu", "kda_rope.cu",
-           "kda_gated_norm.cu", "kda_delta_step.cu", "kda_qk_norm_rope.cu"]
+           "kda_gated_norm.cu", "kda_delta_step.cu", "kda_delta_chunk.cu",
+           "kda_delta_walk.cu", "kda_qk_norm_rope.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC = os.environ.get("NVCC", "nvcc")
 

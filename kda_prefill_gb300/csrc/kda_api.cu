@@ -666,7 +666,8 @@ int with_seq_tables(const int32_t* cu_dev, const int32_t* cu_host, int32_t N, in
     if (rc != KDA_OK) return rc;
     const MetaLayout& L = m->layout;
     SeqTables t{m->dev + L.off_cu, m->dev + L.off_long, m->dev + L.off_short,
-                L.n_long,          L.n_short,           m->key.data() + 3,
+                L.n_long,          L.n_short,           m->dev + L.off_seq_off,
+                m->dev + L.off_chunk_seq, m->dev + L.off_chunk_tok, L.n_chunks, m->key.data() + 3,
                 L.long_seqs.data(), L.long_lens.data()};
     rc = enqueue(arg, t);
     if (rc != KDA_OK) return rc;

@@ -73,10 +73,10 @@ __device__ __forceinline__ float row_sum(float x) {  // over the lanes of a row
 
 template <class S>
 __global__ void __launch_bounds__(kWarps * 32, 5)
-kda_delta_step(const __grid_constant__ DeltaParams p, const int32_t* list) {
+kda_delta_step(const __grid_constant__ DeltaParams p) {
     using C = Cols<S>;
     const int h = blockIdx.y;
-    const int n = list[blockIdx.x / kSplit];
+    const int n = p.short_list[blockIdx.x / kSplit];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int at = lane % kAcross, part = lane / kAcross;  // rows part, part + 2, ... of the eight
     const int own = at % kHeld;                            // the held row whose output this lane makes
@@ -176,22 +176,22 @@ kda_delta_step(const __grid_constant__ DeltaParams p, const int32_t* list) {
 #pragma unroll
         for (int r = 0; r < kHeld; ++r) C::store(state + r * (32 / kAcross) * D, at, s[r]);
     }
-    if (blockIdx.x == 0 && blockIdx.y == 0 && warp == 0) write_status(p, lane);
+    if (p.n_long == 0 && blockIdx.x == 0 && blockIdx.y == 0 && warp == 0) write_status(p, lane);
 }
 
 template <class S>
-cudaError_t launch(const DeltaParams& p, const int32_t* list, int n, cudaStream_t s) {
-    kda_delta_step<S><<<dim3((unsigned)n * kSplit, (unsigned)p.H), kWarps * 32, 0, s>>>(p, list);
+cudaError_t launch(const DeltaParams& p, cudaStream_t s) {
+    kda_delta_step<S><<<dim3((unsigned)p.n_short * kSplit, (unsigned)p.H), kWarps * 32, 0, s>>>(p);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_delta_step(const DeltaParams& p, const int32_t* list, int n, cudaStream_t s) {
-    if (n <= 0) return cudaSuccess;
-    if (p.st_dtype == KDA_STATE_F32) return launch<float>(p, list, n, s);
-    if (p.st_dtype == KDA_STATE_BF16) return launch<__nv_bfloat16>(p, list, n, s);
-    return launch<__half>(p, list, n, s);
+cudaError_t launch_delta_step(const DeltaParams& p, cudaStream_t s) {
+    if (p.n_short <= 0) return cudaSuccess;
+    if (p.st_dtype == KDA_STATE_F32) return launch<float>(p, s);
+    if (p.st_dtype == KDA_STATE_BF16) return launch<__nv_bfloat16>(p, s);
+    return launch<__half>(p, s);
 }
 
 }  // namespace kda

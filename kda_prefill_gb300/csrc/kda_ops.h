@@ -20,6 +20,10 @@ struct SeqTables {
     const int32_t* long_list;   // sequences of more than kShortMax tokens, longest first
     const int32_t* short_list;  // the others
     int n_long, n_short;
+    // chunks of kC tokens of the long sequences: the first of each sequence [N + 1], and
+    // each one's sequence and first token
+    const int32_t *seq_off, *chunk_seq, *chunk_tok;
+    int64_t n_chunks;
     // host: the bounds, and the long sequences and their lengths in long_list's order
     const int32_t* bounds;
     const int32_t* long_seqs;
@@ -95,12 +99,50 @@ cudaError_t launch_lin_walk(const LinParams& p, const LinCuts& cuts, cudaStream_
 // `beside`: right after the walk, beside its last CTAs.
 cudaError_t launch_lin_step(const LinParams& p, bool beside, cudaStream_t s);
 
-// The gated delta rule: linear attention's parameters, and the strengths of the writes.
+// The gated delta rule: linear attention's parameters, the strengths of the writes, and the
+// long sequences' chunks of kC tokens.
 struct DeltaParams : LinParams {
     const float* beta;  // [T][H]
+    const int32_t *seq_off, *chunk_seq, *chunk_tok;
+    int64_t n_chunks;
+    uint8_t* blocks;  // [n_chunks][H] of kDeltaBlock bytes
 };
-// The listed sequences token by token (kda_delta_step.cu).
-cudaError_t launch_delta_step(const DeltaParams& p, const int32_t* list, int n, cudaStream_t s);
+// What kda_delta_chunk leaves for the walk of a chunk and head: fp16 tiles in the swizzled
+// layout of kda_device.cuh and fp32 scalars.
+//   k   [64][128]  k times a power of two for each row
+//   t   [2][64][64] the triangular inverse's high and low part
+//   scalars         see DeltaScalars
+//   q   [64][128]  q^ e^G, each row times up
+//   pt  [64][64]   the scores times the inverse, each row times up
+constexpr int kDeltaK = 0;
+constexpr int kDeltaScal = 16384;
+struct DeltaScalars {
+    float c[kC];      // e^{G_i} and k's length: k^ e^{G_i} = c k
+    float beta[kC];
+    float w[kC];      // half of e^{G_C - G_i} and k's length
+    float down[kC];   // 1 / up
+    float gamma;      // e^{G_C}
+    int first_clear;  // first token that clears the state, kC if none
+    unsigned clears[2];  // all of them
+    float strongest;     // largest beta
+    float unused[3];
+};
+constexpr int kDeltaScalBytes = 1152;
+constexpr int kDeltaT = kDeltaScal + kDeltaScalBytes;
+constexpr int kDeltaQ = kDeltaT + 16384;
+constexpr int kDeltaPT = kDeltaQ + 16384;
+constexpr int kDeltaBlock = kDeltaPT + 8192;
+static_assert(sizeof(DeltaScalars) <= kDeltaScalBytes && sizeof(DeltaScalars) % 16 == 0, "room for the scalars");
+// At most so many chunks: only sequences of more than kShortMax tokens have any.
+inline int64_t delta_chunks(int64_t T, int64_t N) {
+    return T / kC + (T / (kShortMax + 1) < N ? T / (kShortMax + 1) : N);
+}
+// The short sequences token by token (kda_delta_step.cu).
+cudaError_t launch_delta_step(const DeltaParams& p, cudaStream_t s);
+// The long sequences' chunks, each for itself (kda_delta_chunk.cu), and the walk over them
+// (kda_delta_walk.cu).
+cudaError_t launch_delta_chunk(const DeltaParams& p, cudaStream_t s);
+cudaError_t launch_delta_walk(const DeltaParams& p, cudaStream_t s);
 
 struct RopeTensor {
     const void* in;

@@ -251,10 +251,17 @@ int enqueue_delta(void* arg, const kda::SeqTables& t) {
     DeltaCall& c = *static_cast<DeltaCall*>(arg);
     kda::DeltaParams& p = c.p;
     p.cu = t.cu;
+    p.long_list = t.long_list;
+    p.short_list = t.short_list;
     p.n_long = t.n_long;
     p.n_short = t.n_short;
-    cudaError_t e = kda::launch_delta_step(p, t.long_list, t.n_long, c.stream);
-    if (e == cudaSuccess) e = kda::launch_delta_step(p, t.short_list, t.n_short, c.stream);
+    p.seq_off = t.seq_off;
+    p.chunk_seq = t.chunk_seq;
+    p.chunk_tok = t.chunk_tok;
+    p.n_chunks = t.n_chunks;
+    cudaError_t e = kda::launch_delta_chunk(p, c.stream);
+    if (e == cudaSuccess) e = kda::launch_delta_walk(p, c.stream);
+    if (e == cudaSuccess) e = kda::launch_delta_step(p, c.stream);
     return e == cudaSuccess ? KDA_OK : cuda_error(e, "kernel launch");
 }
 
@@ -370,7 +377,7 @@ int kda_lin_attn_fwd(const void* q, int64_t q_stride_t, int64_t q_stride_h, cons
 
 size_t kda_gated_delta_workspace_size(int64_t total_tokens, int32_t num_seqs, int32_t num_heads) {
     if (total_tokens < 0 || num_seqs <= 0 || num_heads <= 0) return 0;
-    return kda::kWsHeader;
+    return kda::kWsHeader + (size_t)kda::delta_chunks(total_tokens, num_seqs) * num_heads * kda::kDeltaBlock;
 }
 
 int kda_gated_delta_fwd(const void* q, int64_t q_stride_t, int64_t q_stride_h, const void* k,
@@ -392,6 +399,7 @@ int kda_gated_delta_fwd(const void* q, int64_t q_stride_t, int64_t q_stride_h, c
     c.stream = reinterpret_cast<cudaStream_t>(stream);
     set_params(a, c.p);
     c.p.beta = beta;
+    c.p.blocks = static_cast<uint8_t*>(workspace) + kda::kWsHeader;
     return kda::with_seq_tables(cu_seqlens, cu_seqlens_host, num_seqs, total_tokens, c.stream, enqueue_delta, &c);
 }
 
