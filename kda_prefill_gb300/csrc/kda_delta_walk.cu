@@ -13,7 +13,8 @@
 //
 // One CTA walks one (sequence, head); two share an SM, and one's products run while the
 // other's threads make operands.  Warps 0-7 make operands, two for each 32 rows, and write
-// the outputs; warp 8 issues the copies and the products.
+// the outputs; warp 8 issues the products and most copies; warps 9-11 turn v over, so that a
+// value row's tokens lie beside each other, and find its largest.
 //
 // Rounding.  Operands are fp16: k exactly, up to its row's power of two; S, R, U and T as
 // the sum of two (22 bits; with one, a state would be off by 2^-12).  The outputs' own terms,
@@ -40,40 +41,42 @@ using namespace dev;
 
 constexpr int D = kD;
 constexpr int C = kC;
-constexpr int kThreads = 288;
-constexpr int kMakers = 8;  // warps 0 .. 7
+constexpr int kThreads = 384;
+constexpr int kMakers = 8;   // warps 0 .. 7
+constexpr int kTurners = 3;  // warps 9 .. 11
 
 // Shared memory.
-constexpr int kTileK = C * D * 2;
+constexpr int kTile = C * D * 2;
 constexpr int kSmK = 0;                          // [2] k
-constexpr int kSmQ = kSmK + 2 * kTileK;
-constexpr int kSmT = kSmQ + kTileK;              // [2] T's parts, then P T
-constexpr int kSmV = kSmT + 3 * C * C * 2;       // [2] v, rows of 128
-constexpr int kSmScal = kSmV + 2 * kTileK;       // [2] scalars
-constexpr int kSmVMax = kSmScal + 2 * kDeltaScalBytes;      // [2][128] largest |v| of a value row
-constexpr int kSmSMax = kSmVMax + 2 * D * 4;     // [2][2][128] largest |S| of half a row
+constexpr int kSmQ = kSmK + 2 * kTile;
+constexpr int kSmT = kSmQ + kTile;               // T's parts, then P T
+constexpr int kSmV = kSmT + 3 * C * C * 2;       // v as it comes
+constexpr int kSmVT = kSmV + kTile;              // [128][64] v by value rows, 16-byte pieces swizzled
+constexpr int kSmScal = kSmVT + kTile;           // [2] scalars
+constexpr int kSmVMax = kSmScal + 2 * kDeltaScalBytes;  // [128] largest |v| of a value row
+constexpr int kSmSMax = kSmVMax + D * 4;         // [2][2][128] largest |S| of half a row
 constexpr int kSmBad = kSmSMax + 4 * D * 4;      // [2][128] tokens whose R is not finite
 constexpr int kSmBar = kSmBad + 2 * D * 4;
 enum Bar {
     kFullK = 0,             // [2] k and scalars
-    kFullV = kFullK + 2,    // [2]
-    kFullQ = kFullV + 2,
+    kFullV = kFullK + 2,
+    kFullQ,
     kFullT,
     kXDone,
     kUDone,
     kODone,
     kDDone,
+    kEnd,
+    kTurned,                // v turned over, its largest found
     kSReady,
     kRReady,
     kUReady,
-    kVMax,                  // [2]
-    kEnd = kVMax + 2,
     kNumBars
 };
-constexpr int kSmMisc = kSmBar + kNumBars * 8;
+constexpr int kSmMisc = kSmBar + kNumBars * 8;   // abort flag, tensor-memory base
 constexpr int kSmemBytes = kSmMisc + 16;
 static_assert(2 * (kSmemBytes + 1024) <= 233472, "two CTAs on an SM");
-static_assert(kSmT % 1024 == 0 && kSmV % 1024 == 0 && kSmBar % 8 == 0, "alignment");
+static_assert(kSmT % 1024 == 0 && kSmV % 1024 == 0 && kSmVT % 1024 == 0 && kSmBar % 8 == 0, "alignment");
 
 // Tensor memory columns.  Operands have, for 16 of their K, 8 columns of the high part and 8
 // of the low one.  Half of S's operand, and then of dS, lies where a half's warps alone write.
@@ -88,6 +91,8 @@ __host__ __device__ constexpr uint32_t ds_column(int half) { return half ? kTmX 
 constexpr uint32_t kIdescKK = mma_idesc(0, 0, 0, 128, 64);  // B K-major
 constexpr uint32_t kIdescKM = mma_idesc(0, 0, 1, 128, 64);  // B MN-major
 
+extern __shared__ __align__(1024) uint8_t smem[];
+
 __device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
@@ -95,23 +100,50 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, u
         "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-__device__ __forceinline__ void tmem_ld32(uint32_t a, float (&v)[32]) {
-    uint32_t r[32];
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+__device__ __forceinline__ uint64_t* bar(int i) { return reinterpret_cast<uint64_t*>(smem + kSmBar) + i; }
+__device__ __forceinline__ volatile int& abort_flag() { return *reinterpret_cast<volatile int*>(smem + kSmMisc); }
+
+// Two fp32 values in one 64-bit register.
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 pack2(float a, float b) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2(f2 a) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+    return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+// Sixteen columns of this thread's lane, there on return.
+__device__ __forceinline__ void load16(uint32_t a, f2 (&v)[8]) {
+    uint32_t r[16];
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
-        "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+        "%15}, [%16];\n\ttcgen05.wait::ld.sync.aligned;"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
           "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
-          "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
-          "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(a));
-    tmem_wait_ld();
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(a)
+        : "memory");
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        asm volatile("" : "+r"(r[i]));  // read after the wait
-        v[i] = __uint_as_float(r[i]);
-    }
+    for (int i = 0; i < 8; ++i) v[i] = pack2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
 }
 __device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t (&r)[16]) {
     asm volatile(
@@ -124,18 +156,28 @@ __device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t (&r)[16]) {
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // Sixteen values as the sum of two fp16 each, as an operand's columns.
-__device__ __forceinline__ void store_split(uint32_t a, const float* x) {
+__device__ __forceinline__ void store_split(uint32_t a, const f2 (&x)[8]) {
     uint32_t r[16];
+    const f2 minus = pack2(-1.f, -1.f);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const __half2 hi = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
-        const float2 f = __half22float2(hi);
+        const float2 f = unpack2(x[i]);
+        const __half2 hi = __floats2half2_rn(f.x, f.y);
         r[i] = reinterpret_cast<const uint32_t&>(hi);
-        r[8 + i] = pack_half2(x[2 * i] - f.x, x[2 * i + 1] - f.y);
+        const float2 h = __half22float2(hi);
+        const float2 lo = unpack2(fma2(pack2(h.x, h.y), minus, x[i]));
+        r[8 + i] = pack_half2(lo.x, lo.y);
     }
     tmem_st16(a, r);
 }
 
+// max(m, |a|, |b|), NaN if one is.
+__device__ __forceinline__ float max_abs(float m, f2 x) {
+    const float2 f = unpack2(x);
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(f.x), "f"(f.y));
+    return r;
+}
 __device__ __forceinline__ float max_nan(float a, float b) {
     float r;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
@@ -150,204 +192,229 @@ __device__ __forceinline__ float scale_of(float bound, float& inverse) {
     return __uint_as_float((uint32_t)(267 - e) << 23);
 }
 
+// Waits for a phase; gives up after about a second, or once another warp has.  A whole
+// warp goes on or leaves together.
+__device__ __forceinline__ bool wait(int b, uint32_t parity) {
+#pragma unroll 1
+    for (uint32_t i = 0; i < kWaitLimit; ++i) {
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar(b), parity & 1))) return true;
+        if (__any_sync(0xffffffffu, abort_flag())) return false;
+    }
+    abort_flag() = 1;
+    return false;
+}
+// One arrival of a whole warp, its tensor-memory accesses before it.
+__device__ __forceinline__ void arrive_warp(int b, int lane) {
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(b));
+}
+__device__ __forceinline__ const DeltaScalars* scalars(int c) {
+    return reinterpret_cast<const DeltaScalars*>(smem + kSmScal + (c & 1) * kDeltaScalBytes);
+}
+__device__ __forceinline__ volatile float* vmax() { return reinterpret_cast<volatile float*>(smem + kSmVMax); }
+__device__ __forceinline__ volatile float* smax_of(int c, int half) {
+    return reinterpret_cast<volatile float*>(smem + kSmSMax) + ((c & 1) * 2 + half) * D;
+}
+__device__ __forceinline__ volatile unsigned* bad_of(int half) {
+    return reinterpret_cast<volatile unsigned*>(smem + kSmBad) + half * D;
+}
+
 struct Walk {
-    uint8_t* smem;
-    uint64_t* bar;
-    volatile int* abort;
-    uint32_t tmem;
-    int n, h, slot, t0, len, chunks;
+    int h, slot, t0, len, chunks;
     const uint8_t* blocks;  // of the first chunk
     int64_t step;           // bytes between chunks' blocks
     bool init;
-
-    // Waits for a phase; gives up after about a second, or once another warp has.  A whole
-    // warp goes on or leaves together.
-    __device__ bool wait(int b, uint32_t parity) const {
-#pragma unroll 1
-        for (uint32_t i = 0; i < kWaitLimit; ++i) {
-            if (__all_sync(0xffffffffu, mbar_try_wait(bar + b, parity & 1))) return true;
-            if (__any_sync(0xffffffffu, *abort)) return false;
-        }
-        *abort = 1;
-        return false;
-    }
-    // One arrival of a whole warp, its tensor-memory accesses before it.
-    __device__ void arrive_warp(int b, int lane) const {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar + b);
-    }
-    __device__ const DeltaScalars* scalars(int c) const {
-        return reinterpret_cast<const DeltaScalars*>(smem + kSmScal + (c & 1) * kDeltaScalBytes);
-    }
-    __device__ float* vmax(int c) const { return reinterpret_cast<float*>(smem + kSmVMax) + (c & 1) * D; }
-    __device__ volatile float* smax(int c, int half) const {
-        return reinterpret_cast<volatile float*>(smem + kSmSMax) + ((c & 1) * 2 + half) * D;
-    }
-    __device__ volatile unsigned* bad(int half) const {
-        return reinterpret_cast<volatile unsigned*>(smem + kSmBad) + half * D;
-    }
 };
 
-// Warp 8: copies, products and the largest |v|.
+// Warp 8: products, and the copies of a chunk's block.
 struct Issuer {
     const Walk& w;
-    const DeltaParams& p;
-    const int lane;
-    int k_loads = 0, v_loads = 0, q_loads = 0, t_loads = 0;
+    const bool lead;
+    int k_loads = 0, q_loads = 0, t_loads = 0;
 
-    __device__ const uint8_t* block(int c) const { return w.blocks + c * w.step; }
-    __device__ void load_k(int c) {
-        if (lane == 0) {
-            uint64_t* b = w.bar + kFullK + (c & 1);
-            mbar_arrive_expect_tx(b, kTileK + (uint32_t)sizeof(DeltaScalars));
-            bulk_g2s(w.smem + kSmK + (c & 1) * kTileK, block(c) + kDeltaK, kTileK, b);
-            bulk_g2s(w.smem + kSmScal + (c & 1) * kDeltaScalBytes, block(c) + kDeltaScal, sizeof(DeltaScalars), b);
+    __device__ __forceinline__ void load_k(int c) {
+        if (lead) {
+            uint64_t* b = bar(kFullK + (c & 1));
+            mbar_arrive_expect_tx(b, kTile + (uint32_t)sizeof(DeltaScalars));
+            bulk_g2s(smem + kSmK + (c & 1) * kTile, w.blocks + c * w.step + kDeltaK, kTile, b);
+            bulk_g2s(smem + kSmScal + (c & 1) * kDeltaScalBytes, w.blocks + c * w.step + kDeltaScal, sizeof(DeltaScalars), b);
         }
+        __syncwarp();
         ++k_loads;
     }
-    __device__ void load_v(int c) {
-        const int rows = min(C, w.len - c * C);
-        uint64_t* b = w.bar + kFullV + (c & 1);
-        if (lane == 0) mbar_arrive_expect_tx(b, rows * D * 2);
-        __syncwarp();
-        const __nv_bfloat16* v = p.v + (int64_t)(w.t0 + c * C) * p.v_st + (int64_t)w.h * p.v_sh;
-        for (int r = lane; r < rows; r += 32)
-            bulk_g2s(w.smem + kSmV + (c & 1) * kTileK + r * (D * 2), v + r * p.v_st, D * 2, b);
-        ++v_loads;
-    }
-    __device__ void load_q(int c) {
-        if (lane == 0) {
-            mbar_arrive_expect_tx(w.bar + kFullQ, kTileK);
-            bulk_g2s(w.smem + kSmQ, block(c) + kDeltaQ, kTileK, w.bar + kFullQ);
+    __device__ __forceinline__ void load_q(int c) {
+        if (lead) {
+            mbar_arrive_expect_tx(bar(kFullQ), kTile);
+            bulk_g2s(smem + kSmQ, w.blocks + c * w.step + kDeltaQ, kTile, bar(kFullQ));
         }
+        __syncwarp();
         ++q_loads;
     }
-    __device__ void load_t(int c) {
-        if (lane == 0) {
-            mbar_arrive_expect_tx(w.bar + kFullT, 3 * C * C * 2);
-            bulk_g2s(w.smem + kSmT, block(c) + kDeltaT, 2 * C * C * 2, w.bar + kFullT);
-            bulk_g2s(w.smem + kSmT + 2 * C * C * 2, block(c) + kDeltaPT, C * C * 2, w.bar + kFullT);
+    __device__ __forceinline__ void load_t(int c) {
+        if (lead) {
+            mbar_arrive_expect_tx(bar(kFullT), 3 * C * C * 2);
+            bulk_g2s(smem + kSmT, w.blocks + c * w.step + kDeltaT, 2 * C * C * 2, bar(kFullT));
+            bulk_g2s(smem + kSmT + 2 * C * C * 2, w.blocks + c * w.step + kDeltaPT, C * C * 2, bar(kFullT));
         }
+        __syncwarp();
         ++t_loads;
     }
-    // The largest finite |v| of each value row of chunk c.
-    __device__ bool largest_v(int c) {
-        if (!w.wait(kFullV + (c & 1), c >> 1)) return false;
-        const int rows = min(C, w.len - c * C);
-        const uint2* v = reinterpret_cast<const uint2*>(w.smem + kSmV + (c & 1) * kTileK) + lane;
-        __nv_bfloat162 a = __float2bfloat162_rn(0.f), b = a;
-#pragma unroll 8
-        for (int r = 0; r < rows; ++r) {
-            const uint2 x = v[r * (D / 4)];
-            a = __hmax2_nan(a, __habs2(reinterpret_cast<const __nv_bfloat162&>(x.x)));
-            b = __hmax2_nan(b, __habs2(reinterpret_cast<const __nv_bfloat162&>(x.y)));
-        }
-        float4 m = make_float4(__low2float(a), __high2float(a), __low2float(b), __high2float(b));
-        if (__any_sync(0xffffffffu, !(finite(m.x) && finite(m.y) && finite(m.z) && finite(m.w)))) {
-            m = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int r = 0; r < rows; ++r) {
-                const uint2 x = v[r * (D / 4)];
-                const float f[4] = {fabsf(__uint_as_float(x.x << 16)), fabsf(__uint_as_float(x.x & 0xFFFF0000u)),
-                                    fabsf(__uint_as_float(x.y << 16)), fabsf(__uint_as_float(x.y & 0xFFFF0000u))};
-                m.x = finite(f[0]) ? fmaxf(m.x, f[0]) : m.x;
-                m.y = finite(f[1]) ? fmaxf(m.y, f[1]) : m.y;
-                m.z = finite(f[2]) ? fmaxf(m.z, f[2]) : m.z;
-                m.w = finite(f[3]) ? fmaxf(m.w, f[3]) : m.w;
-            }
-        }
-        reinterpret_cast<float4*>(w.vmax(c))[lane] = m;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(w.bar + kVMax + (c & 1));
-        return true;
-    }
-
-    __device__ bool go() {
-        const uint32_t tm = w.tmem;
-        const uint32_t ks = smem_u32(w.smem + kSmK), qs = smem_u32(w.smem + kSmQ), ts = smem_u32(w.smem + kSmT);
+    __device__ __forceinline__ bool go(uint32_t tm) {
+        // descriptors; their addresses count 16 bytes
+        constexpr uint64_t kHalf = kTile / 2 >> 4;
         load_k(0);
-        load_v(0);
         load_q(0);
         load_t(0);
-        if (w.chunks > 1) {
-            load_k(1);
-            load_v(1);
-        }
-        if (!largest_v(0)) return false;
+        if (w.chunks > 1) load_k(1);
 #pragma unroll 1
         for (int c = 0; c < w.chunks; ++c) {
-            const uint32_t kt = ks + (c & 1) * kTileK;
-            if (!w.wait(kFullK + (c & 1), c >> 1) || !w.wait(kFullQ, c) || !w.wait(kSReady, c)) return false;
+            const uint32_t kt = smem_u32(smem + kSmK) + (c & 1) * kTile;
+            if (!wait(kFullK + (c & 1), c >> 1) || !wait(kFullQ, c) || !wait(kSReady, c)) return false;
             tc_fence_after();
-            if (lane == 0) {
+            if (lead) {
+                const uint64_t kd = sw128_desc(kt, 0, 1024), qd = sw128_desc(smem_u32(smem + kSmQ), 0, 1024);
 #pragma unroll
                 for (int s = 0; s < 8; ++s)
 #pragma unroll
                     for (int part = 0; part < 2; ++part)
-                        mma_f16_ts(tm + kTmX, tm + kTmS + 16 * s + 8 * part,
-                                   sw128_desc(kt + (s >> 2) * (kTileK / 2) + (s & 3) * 32, 0, 1024), kIdescKK, s > 0 || part > 0);
+                        mma_f16_ts(tm + kTmX, tm + kTmS + 16 * s + 8 * part, kd + (s >> 2) * kHalf + (s & 3) * 2, kIdescKK,
+                                   s > 0 || part > 0);
 #pragma unroll
                 for (int s = 0; s < 8; ++s)
-                    mma_f16_ts(tm + kTmO, tm + kTmS + 16 * s,
-                               sw128_desc(qs + (s >> 2) * (kTileK / 2) + (s & 3) * 32, 0, 1024), kIdescKK, s > 0);
-                mma_commit(w.bar + kXDone);
+                    mma_f16_ts(tm + kTmO, tm + kTmS + 16 * s, qd + (s >> 2) * kHalf + (s & 3) * 2, kIdescKK, s > 0);
+                mma_commit(bar(kXDone));
             }
             __syncwarp();
             // the chunk before's k has been used
             if (c >= 1 && c + 1 < w.chunks) load_k(c + 1);
-            if (c + 1 < w.chunks && !largest_v(c + 1)) return false;
-            if (!w.wait(kFullT, c) || !w.wait(kRReady, c)) return false;
+            if (!wait(kFullT, c) || !wait(kRReady, c)) return false;
             tc_fence_after();
-            if (lane == 0) {
+            if (lead) {
+                const uint64_t td = sw128_desc(smem_u32(smem + kSmT), 0, 1024);
 #pragma unroll
                 for (int s = 0; s < 4; ++s) {
-                    const uint64_t hi = sw128_desc(ts + s * 32, 0, 1024), lo = sw128_desc(ts + C * C * 2 + s * 32, 0, 1024);
+                    const uint64_t hi = td + 2 * s, lo = hi + (C * C * 2 >> 4);
                     mma_f16_ts(tm + kTmX, tm + kTmR + 16 * s, lo, kIdescKK, s > 0);
                     mma_f16_ts(tm + kTmX, tm + kTmR + 16 * s + 8, hi, kIdescKK, 1);
                     mma_f16_ts(tm + kTmX, tm + kTmR + 16 * s, hi, kIdescKK, 1);
                 }
-                mma_commit(w.bar + kUDone);
+                mma_commit(bar(kUDone));
 #pragma unroll
                 for (int s = 0; s < 4; ++s)
-                    mma_f16_ts(tm + kTmO, tm + kTmR + 16 * s, sw128_desc(ts + 2 * C * C * 2 + s * 32, 0, 1024), kIdescKK, 1);
-                mma_commit(w.bar + kODone);
+                    mma_f16_ts(tm + kTmO, tm + kTmR + 16 * s, td + (2 * C * C * 2 >> 4) + 2 * s, kIdescKK, 1);
+                mma_commit(bar(kODone));
             }
             __syncwarp();
-            // the makers have read v, and X's products q
-            if (c + 2 < w.chunks) load_v(c + 2);
+            // X's products have read q
             if (c + 1 < w.chunks) load_q(c + 1);
-            if (!w.wait(kUReady, c)) return false;
+            if (!wait(kUReady, c)) return false;
             tc_fence_after();
-            if (lane == 0) {
+            if (lead) {
+                const uint64_t km = sw128_desc(kt, kTile / 2, 1024);
 #pragma unroll
                 for (int half = 0; half < 2; ++half)
 #pragma unroll
                     for (int s = 0; s < 4; ++s) {
-                        const uint64_t b = sw128_desc(kt + half * (kTileK / 2) + s * 2048, 8192, 1024);
+                        const uint64_t b = km + half * kHalf + s * (2048 >> 4);
                         mma_f16_ts(tm + ds_column(half), tm + kTmU + 16 * s + 8, b, kIdescKM, s > 0);
                         mma_f16_ts(tm + ds_column(half), tm + kTmU + 16 * s, b, kIdescKM, 1);
                     }
-                mma_commit(w.bar + kDDone);
+                mma_commit(bar(kDDone));
             }
             __syncwarp();
-            if (!w.wait(kODone, c)) return false;
+            if (!wait(kODone, c)) return false;
             if (c + 1 < w.chunks) load_t(c + 1);
         }
         return true;
     }
-    // Copies and products in flight end before the CTA does.
-    __device__ void finish() {
-        if (lane == 0) mma_commit(w.bar + kEnd);
-        bool ok = mbar_wait(w.bar + kEnd, 0);
+    // Its copies and products in flight end before the CTA does.
+    __device__ __forceinline__ void finish() {
+        if (lead) mma_commit(bar(kEnd));
+        __syncwarp();
+        bool ok = mbar_wait(bar(kEnd), 0);
         for (int i = 0; i < 2; ++i) {
-            // loads of slot i: chunks i, i + 2, ...
-            const int nk = (k_loads + 1 - i) / 2, nv = (v_loads + 1 - i) / 2;
-            if (nk > 0) ok = mbar_wait(w.bar + kFullK + i, (nk - 1) & 1) && ok;
-            if (nv > 0) ok = mbar_wait(w.bar + kFullV + i, (nv - 1) & 1) && ok;
+            const int n = (k_loads + 1 - i) / 2;  // loads of slot i
+            if (n > 0) ok = mbar_wait(bar(kFullK + i), (n - 1) & 1) && ok;
         }
-        if (q_loads > 0) ok = mbar_wait(w.bar + kFullQ, (q_loads - 1) & 1) && ok;
-        if (t_loads > 0) ok = mbar_wait(w.bar + kFullT, (t_loads - 1) & 1) && ok;
-        if (!ok) *w.abort = 1;
+        if (q_loads > 0) ok = mbar_wait(bar(kFullQ), (q_loads - 1) & 1) && ok;
+        if (t_loads > 0) ok = mbar_wait(bar(kFullT), (t_loads - 1) & 1) && ok;
+        if (!ok) abort_flag() = 1;
+    }
+};
+
+// Warps 9-11: v by value rows, and each row's largest finite |v|.  Tokens past the sequence's
+// end are zeros.
+struct Turner {
+    const Walk& w;
+    const CUtensorMap* map;
+    const int which, lane;
+    int loads = 0;
+
+    __device__ __forceinline__ void load_v(int c) {
+        if (lane == 0) {
+            mbar_arrive_expect_tx(bar(kFullV), kTile);
+            tma_load_3d(smem + kSmV, map, bar(kFullV), 0, w.h, w.t0 + c * C);
+            tma_load_3d(smem + kSmV + kTile / 2, map, bar(kFullV), 64, w.h, w.t0 + c * C);
+        }
+        __syncwarp();
+        ++loads;
+    }
+    __device__ __forceinline__ bool go() {
+        if (which == 0) load_v(0);
+#pragma unroll 1
+        for (int c = 0; c < w.chunks; ++c) {
+            // the makers have read the chunk before's
+            if (!wait(kFullV, c) || (c > 0 && !wait(kRReady, c - 1))) return false;
+            const int live = w.len - c * C;
+            const uint32_t from = smem_u32(smem + kSmV), to = smem_u32(smem + kSmVT);
+#pragma unroll 1
+            for (int g = which; g < D / 8; g += kTurners) {
+                uint32_t r[8];
+                const int piece = ((g & 7) ^ (lane & 7)) << 4;
+                const uint32_t a = from + (g >> 3) * (kTile / 2) + lane * 128 + piece;
+                ldsm_x4_t(a, r[0], r[1], r[2], r[3]);
+                ldsm_x4_t(a + 32 * 128, r[4], r[5], r[6], r[7]);
+                const int t = 2 * (lane & 3);
+                if (live < C) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        if (8 * i + t >= live) r[i] &= 0xFFFF0000u;
+                        if (8 * i + t + 1 >= live) r[i] &= 0x0000FFFFu;
+                    }
+                }
+                const int row = 8 * g + (lane & 7);
+                const uint32_t b = to + row * 128;
+                stsm_x4(b + (((lane >> 3) ^ (lane & 7)) << 4), r[0], r[1], r[2], r[3]);
+                stsm_x4(b + (((4 + (lane >> 3)) ^ (lane & 7)) << 4), r[4], r[5], r[6], r[7]);
+                __nv_bfloat162 m = __float2bfloat162_rn(0.f);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) m = __hmax2_nan(m, __habs2(reinterpret_cast<const __nv_bfloat162&>(r[i])));
+                float f = max_nan(__low2float(m), __high2float(m));
+                if (__any_sync(0xffffffffu, !finite(f))) {
+                    f = 0.f;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float x = fabsf(__uint_as_float(r[i] << 16)), y = fabsf(__uint_as_float(r[i] & 0xFFFF0000u));
+                        f = fmaxf(f, finite(x) ? x : 0.f);
+                        f = fmaxf(f, finite(y) ? y : 0.f);
+                    }
+                }
+                f = fmaxf(f, __shfl_xor_sync(0xffffffffu, f, 1));
+                f = fmaxf(f, __shfl_xor_sync(0xffffffffu, f, 2));
+                if ((lane & 3) == 0) vmax()[8 * g + (lane >> 2)] = f;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kTurned));
+            if (which == 0 && c + 1 < w.chunks) {
+                if (!wait(kTurned, c)) return false;
+                load_v(c + 1);
+            }
+        }
+        return true;
+    }
+    __device__ __forceinline__ void finish() {
+        if (loads > 0 && !mbar_wait(bar(kFullV), (loads - 1) & 1)) abort_flag() = 1;
     }
 };
 
@@ -367,188 +434,225 @@ __device__ __noinline__ uint2 poisoned(uint2 bad, uint2 clears) {
 
 // Warps 0-7: a thread has half of value row `row`: 64 keys, 32 of a chunk's tokens.
 template <class S>
-__device__ bool make(const Walk& w, const DeltaParams& p, int warp, int lane) {
+__device__ __forceinline__ bool make(const Walk& w, const DeltaParams& p, uint32_t base, int warp, int lane) {
     const int half = warp >> 2, row = 32 * (warp & 3) + lane;
-    const uint32_t tm = w.tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+    const uint32_t tm = base + ((uint32_t)(32 * (warp & 3)) << 16);
     constexpr int N = 16 / sizeof(S);
-    S* const state = static_cast<S*>(p.pool) + (w.slot >= 0 ? (size_t)w.slot * p.stride0 : 0) +
-                     ((size_t)w.h * D + row) * D + half * 64;
-    float s[64];
-#pragma unroll
-    for (int i = 0; i < 64; ++i) s[i] = 0.f;
-    if (w.init) {
+    f2 s[32];
+    {
+        const S* state = static_cast<const S*>(p.pool) + (w.init ? (size_t)w.slot * p.stride0 : 0) +
+                         ((size_t)w.h * D + row) * D + half * 64;
 #pragma unroll
         for (int i = 0; i < 64; i += N) {
-            float f[N];
-            rows::load<S, N>(state + i).get(f);
+            float f[N] = {};
+            if (w.init) rows::load<S, N>(state + i).get(f);
 #pragma unroll
-            for (int j = 0; j < N; ++j) s[i + j] = f[j];
+            for (int j = 0; j < N; j += 2) s[(i + j) / 2] = pack2(f[j], f[j + 1]);
         }
     }
     float smax = 0.f;
 #pragma unroll
-    for (int i = 0; i < 64; ++i) smax = max_nan(smax, fabsf(s[i]));
-    w.smax(0, half)[row] = smax;
+    for (int i = 0; i < 32; ++i) smax = max_abs(smax, s[i]);
+    smax_of(0, half)[row] = smax;
     asm volatile("bar.sync 1, %0;" ::"n"(kMakers * 32) : "memory");
     // the largest |S| a chunk ago; what the chunk adds to |S| at most
-    float was = max_nan(smax, w.smax(0, half ^ 1)[row]), adds, scale, inv;
-    if (!w.wait(kVMax, 0) || !w.wait(kFullK, 0)) return false;
+    float was = max_nan(smax, smax_of(0, half ^ 1)[row]), adds, scale, inv;
     auto rescale = [&](int c, float grown) {
-        const float s = 11.32f * (finite(was) ? was : 0.f) + grown;  // |S| <= sqrt(128) max
-        const float b = w.scalars(c)->strongest, m = w.vmax(c)[row];
+        const float at = 11.32f * (finite(was) ? was : 0.f) + grown;  // |S| <= sqrt(128) max
+        const float b = scalars(c)->strongest, m = vmax()[row];
         adds = 64.f * b * m;
         // (v itself has to stay finite when it is scaled)
-        scale = scale_of(fmaxf(fmaxf(s, b * (m + s + adds)), 0x1p-60f * m), inv);
+        scale = scale_of(fmaxf(fmaxf(at, b * (m + at + adds)), 0x1p-60f * m), inv);
     };
+    // 16 keys of S's operand; of a row with infinities or NaN as zeros
+    auto store_s = [&](int b, bool live) {
+        f2 x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = live ? mul2(s[8 * b + i], pack2(scale, scale)) : 0;
+        store_split(tm + kTmS + 64 * half + 16 * b, x);
+    };
+    if (!wait(kTurned, 0) || !wait(kFullK, 0)) return false;
     rescale(0, 0.f);
-    // S's operand; a row with infinities or NaN as zeros
-    auto store_s = [&]() {
-        const bool live = finite(smax);
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            float x[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] = s[16 * b + i] * scale;
-            if (!live) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) x[i] = 0.f;
-            }
-            store_split(tm + kTmS + 64 * half + 16 * b, x);
-        }
-        tmem_wait_st();
-    };
-    store_s();
-    w.arrive_warp(kSReady, lane);
+    for (int b = 0; b < 4; ++b) store_s(b, finite(smax));
+    tmem_wait_st();
+    arrive_warp(kSReady, lane);
 
-    __nv_bfloat16* out = p.out + ((int64_t)w.t0 * p.H + w.h) * D + row;
 #pragma unroll 1
     for (int c = 0; c < w.chunks; ++c) {
-        const DeltaScalars* sc = w.scalars(c);
-        const int live = min(C, w.len - c * C) - half * 32;  // of this half's tokens
-        float x[32];
+        const DeltaScalars* sc = scalars(c);
         // R
-        if (!w.wait(kXDone, c) || !w.wait(kFullV + (c & 1), c >> 1)) return false;
+        if (!wait(kXDone, c)) return false;
         tc_fence_after();
-        tmem_ld32(tm + kTmX + 32 * half, x);
-        if (c > 0) {
-            // both halves' largest of the state that the chunk starts from
-            was = max_nan(smax, w.smax(c, half ^ 1)[row]);
-        }
-        const int clear = sc->first_clear;
-        if (clear < C) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = 32 * half + i < clear ? x[i] : 0.f;
-        }
-        const __nv_bfloat16* v = reinterpret_cast<const __nv_bfloat16*>(w.smem + kSmV + (c & 1) * kTileK) + half * 32 * D + row;
-        float check = 0.f;
-#pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-            const float4 ci = *reinterpret_cast<const float4*>(sc->c + 32 * half + i);
-            const float4 bi = *reinterpret_cast<const float4*>(sc->beta + 32 * half + i);
-            const float cc[4] = {ci.x, ci.y, ci.z, ci.w}, bb[4] = {bi.x, bi.y, bi.z, bi.w};
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const float vv = i + u < live ? __bfloat162float(v[(i + u) * D]) * scale : 0.f;
-                x[i + u] = bb[u] * fmaf(-cc[u], x[i + u], vv);
-                check = fmaf(x[i + u], 0.f, check);
-            }
-        }
-        unsigned bad = 0;
+        // both halves' largest of the state that the chunk starts from
+        if (c > 0) was = max_nan(smax, smax_of(c, half ^ 1)[row]);
+        const int clear = sc->first_clear - 32 * half;  // among this half's tokens
         const bool dead = !finite(was);
-        if (__any_sync(0xffffffffu, check != 0.f || dead)) {
+        unsigned bad = 0;
+#pragma unroll 1
+        for (int b = 0; b < 32; b += 16) {
+            f2 x[8];
+            load16(tm + kTmX + 32 * half + b, x);
+            if (clear < b + 16) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                if (!finite(x[i]) || (dead && 32 * half + i < clear)) {
-                    bad |= 1u << i;
-                    x[i] = 0.f;
+                for (int i = 0; i < 8; ++i) {
+                    const float2 f = unpack2(x[i]);
+                    x[i] = pack2(b + 2 * i < clear ? f.x : 0.f, b + 2 * i + 1 < clear ? f.y : 0.f);
                 }
             }
+            f2 check = 0;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint4 v = *reinterpret_cast<const uint4*>(smem + kSmVT + row * 128 + (((4 * half + b / 8 + j) ^ (row & 7)) << 4));
+                const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int i = 0; i < 4; i += 2) {
+                    const float4 ci = *reinterpret_cast<const float4*>(sc->c + 32 * half + b + 8 * j + 2 * i);
+                    const float4 bi = *reinterpret_cast<const float4*>(sc->beta + 32 * half + b + 8 * j + 2 * i);
+                    const f2 cc[2] = {pack2(-ci.x, -ci.y), pack2(-ci.z, -ci.w)};
+                    const f2 bb[2] = {pack2(bi.x, bi.y), pack2(bi.z, bi.w)};
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const f2 vv = pack2(__uint_as_float(vw[i + u] << 16), __uint_as_float(vw[i + u] & 0xFFFF0000u));
+                        f2& y = x[4 * j + i + u];
+                        y = mul2(bb[u], fma2(cc[u], y, mul2(vv, pack2(scale, scale))));
+                        check = fma2(y, 0, check);
+                    }
+                }
+            }
+            const float2 ch = unpack2(check);
+            if (__any_sync(0xffffffffu, ch.x + ch.y != 0.f || dead)) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    float2 f = unpack2(x[i]);
+                    if (!finite(f.x) || (dead && b + 2 * i < clear)) bad |= 1u << (b + 2 * i), f.x = 0.f;
+                    if (!finite(f.y) || (dead && b + 2 * i + 1 < clear)) bad |= 2u << (b + 2 * i), f.y = 0.f;
+                    x[i] = pack2(f.x, f.y);
+                }
+            }
+            store_split(tm + kTmR + 32 * half + b, x);
         }
-        w.bad(half)[row] = bad;
-        store_split(tm + kTmR + 32 * half, x);
-        store_split(tm + kTmR + 32 * half + 16, x + 16);
+        bad_of(half)[row] = bad;
         tmem_wait_st();
-        w.arrive_warp(kRReady, lane);
+        arrive_warp(kRReady, lane);
         // U
-        if (!w.wait(kUDone, c)) return false;
+        if (!wait(kUDone, c)) return false;
         tc_fence_after();
-        tmem_ld32(tm + kTmX + 32 * half, x);
+#pragma unroll 1
+        for (int b = 0; b < 32; b += 16) {
+            f2 x[8];
+            load16(tm + kTmX + 32 * half + b, x);
 #pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-            const float4 wi = *reinterpret_cast<const float4*>(sc->w + 32 * half + i);
-            x[i] *= wi.x, x[i + 1] *= wi.y, x[i + 2] *= wi.z, x[i + 3] *= wi.w;
+            for (int i = 0; i < 8; i += 2) {
+                const float4 wi = *reinterpret_cast<const float4*>(sc->w + 32 * half + b + 2 * i);
+                x[i] = mul2(x[i], pack2(wi.x, wi.y));
+                x[i + 1] = mul2(x[i + 1], pack2(wi.z, wi.w));
+            }
+            store_split(tm + kTmU + 32 * half + b, x);
         }
-        store_split(tm + kTmU + 32 * half, x);
-        store_split(tm + kTmU + 32 * half + 16, x + 16);
         tmem_wait_st();
-        w.arrive_warp(kUReady, lane);
+        arrive_warp(kUReady, lane);
         // outputs
-        if (!w.wait(kODone, c)) return false;
+        if (!wait(kODone, c)) return false;
         tc_fence_after();
-        tmem_ld32(tm + kTmO + 32 * half, x);
-        const unsigned other = w.bad(half ^ 1)[row];
-        uint2 spoilt = make_uint2(0, 0);
+        const unsigned other = bad_of(half ^ 1)[row];
+        unsigned spoils = 0, lost = 0;
         if (__any_sync(0xffffffffu, (bad | other) != 0)) {
-            spoilt = poisoned(half ? make_uint2(other, bad) : make_uint2(bad, other), make_uint2(sc->clears[0], sc->clears[1]));
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-                if ((half ? spoilt.y : spoilt.x) >> i & 1) x[i] = NAN;
+            const uint2 r = poisoned(half ? make_uint2(other, bad) : make_uint2(bad, other), make_uint2(sc->clears[0], sc->clears[1]));
+            spoils = half ? r.y : r.x;
+            lost = r.y >> 31;
         }
         {
-            const float f = inv * p.scale;
-            __nv_bfloat16* o = out + (int64_t)(c * C + half * 32) * p.H * D;
+            const int live = w.len - c * C - half * 32;  // of this half's tokens
+            const f2 f = pack2(inv * p.scale, inv * p.scale);
             const int64_t st = (int64_t)p.H * D;
+            __nv_bfloat16* o = p.out + ((int64_t)(w.t0 + c * C + half * 32) * p.H + w.h) * D + row;
+#pragma unroll 1
+            for (int b = 0; b < 32; b += 16) {
+                f2 x[8];
+                load16(tm + kTmO + 32 * half + b, x);
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-                const float4 di = *reinterpret_cast<const float4*>(sc->down + 32 * half + i);
-                const float dd[4] = {di.x, di.y, di.z, di.w};
+                for (int i = 0; i < 8; i += 2) {
+                    const float4 di = *reinterpret_cast<const float4*>(sc->down + 32 * half + b + 2 * i);
+                    x[i] = mul2(mul2(x[i], pack2(di.x, di.y)), f);
+                    x[i + 1] = mul2(mul2(x[i + 1], pack2(di.z, di.w)), f);
+                }
+                if (spoils) {
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    if (i + u < live) *o = __float2bfloat16_rn(x[i + u] * dd[u] * f);
-                    o += st;
+                    for (int i = 0; i < 8; ++i) {
+                        const float2 y = unpack2(x[i]);
+                        x[i] = pack2(spoils >> (b + 2 * i) & 1 ? NAN : y.x, spoils >> (b + 2 * i + 1) & 1 ? NAN : y.y);
+                    }
+                }
+                if (live >= b + 16) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float2 y = unpack2(x[i]);
+                        o[0] = __float2bfloat16_rn(y.x);
+                        o[st] = __float2bfloat16_rn(y.y);
+                        o += 2 * st;
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float2 y = unpack2(x[i]);
+                        if (b + 2 * i < live) o[0] = __float2bfloat16_rn(y.x);
+                        if (b + 2 * i + 1 < live) o[st] = __float2bfloat16_rn(y.y);
+                        o += 2 * st;
+                    }
                 }
             }
         }
         // S
-        const float gamma = sc->gamma, back = 2.f * inv;
-        if (clear < C) {
-#pragma unroll
-            for (int i = 0; i < 64; ++i) s[i] = 0.f;
-        }
         const bool more = c + 1 < w.chunks;
+        const f2 gamma = pack2(sc->gamma, sc->gamma), back = pack2(2.f * inv, 2.f * inv);
+        if (sc->first_clear < C) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) s[i] = 0;
+        }
         if (more) {
-            if (!w.wait(kVMax + ((c + 1) & 1), (c + 1) >> 1) || !w.wait(kFullK + ((c + 1) & 1), (c + 1) >> 1)) return false;
+            if (!wait(kTurned, c + 1) || !wait(kFullK + ((c + 1) & 1), (c + 1) >> 1)) return false;
             rescale(c + 1, adds);
         }
-        if (!w.wait(kDDone, c)) return false;
+        if (!wait(kDDone, c)) return false;
         tc_fence_after();
         smax = 0.f;
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            tmem_ld32(tm + ds_column(half) + 32 * b, x);
+        for (int b = 0; b < 4; ++b) {
+            f2 x[8];
+            load16(tm + ds_column(half) + 16 * b, x);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                s[32 * b + i] = fmaf(gamma, s[32 * b + i], x[i] * back);
-                smax = max_nan(smax, fabsf(s[32 * b + i]));
+            for (int i = 0; i < 8; ++i) {
+                s[8 * b + i] = fma2(gamma, s[8 * b + i], mul2(x[i], back));
+                smax = max_abs(smax, s[8 * b + i]);
             }
+            if (more) store_s(b, true);
         }
-        if (spoilt.y >> 31) {
+        if (lost) {
             smax = NAN;
 #pragma unroll
-            for (int i = 0; i < 64; ++i) s[i] = NAN;
+            for (int i = 0; i < 32; ++i) s[i] = pack2(NAN, NAN);
         }
         if (more) {
-            w.smax(c + 1, half)[row] = smax;
-            store_s();
-            w.arrive_warp(kSReady, lane);
+            if (__any_sync(0xffffffffu, !finite(smax))) {
+#pragma unroll
+                for (int b = 0; b < 4; ++b) store_s(b, finite(smax));
+            }
+            smax_of(c + 1, half)[row] = smax;
+            tmem_wait_st();
+            arrive_warp(kSReady, lane);
         }
     }
     if (w.slot >= 0) {
+        S* state = static_cast<S*>(p.pool) + (size_t)w.slot * p.stride0 + ((size_t)w.h * D + row) * D + half * 64;
 #pragma unroll
         for (int i = 0; i < 64; i += N) {
             float f[N];
 #pragma unroll
-            for (int j = 0; j < N; ++j) f[j] = s[i + j];
+            for (int j = 0; j < N; j += 2) {
+                const float2 y = unpack2(s[(i + j) / 2]);
+                f[j] = y.x, f[j + 1] = y.y;
+            }
             rows::Piece<S, N> x;
             x.set(f);
             rows::store<S, N>(state + i, x);
@@ -558,52 +662,83 @@ __device__ bool make(const Walk& w, const DeltaParams& p, int warp, int lane) {
 }
 
 template <class S>
-__global__ void __launch_bounds__(kThreads, 2) kda_delta_walk(const __grid_constant__ DeltaParams p) {
-    extern __shared__ __align__(1024) uint8_t smem[];
+__global__ void __launch_bounds__(kThreads, 2)
+kda_delta_walk(const __grid_constant__ DeltaParams p, const __grid_constant__ CUtensorMap v_map) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    Walk w;
-    w.smem = smem;
-    w.bar = reinterpret_cast<uint64_t*>(smem + kSmBar);
-    w.abort = reinterpret_cast<volatile int*>(smem + kSmMisc);
     uint32_t* const base = reinterpret_cast<uint32_t*>(smem + kSmMisc + 8);
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kNumBars; ++i) mbar_init(w.bar + i, i >= kSReady && i <= kUReady ? kMakers : 1);
-        *w.abort = 0;
+        for (int i = 0; i < kNumBars; ++i) mbar_init(bar(i), i == kTurned ? kTurners : i >= kSReady ? kMakers : 1);
+        abort_flag() = 0;
         fence_mbar_init();
     }
-    if (warp == 8) tmem_alloc(base, kTmCols);
+    if (warp == kMakers) tmem_alloc(base, kTmCols);
+    Walk w;
     w.h = blockIdx.x % p.H;
-    w.n = p.long_list[blockIdx.x / p.H];
-    w.t0 = p.cu[w.n];
-    w.len = p.cu[w.n + 1] - w.t0;
+    const int n = p.long_list[blockIdx.x / p.H];
+    w.t0 = p.cu[n];
+    w.len = p.cu[n + 1] - w.t0;
     w.chunks = (w.len + C - 1) / C;
     w.step = (int64_t)p.H * kDeltaBlock;
-    w.blocks = p.blocks + ((int64_t)p.seq_off[w.n] * p.H + w.h) * kDeltaBlock;
-    const int slot = p.idx[w.n];
+    w.blocks = p.blocks + ((int64_t)p.seq_off[n] * p.H + w.h) * kDeltaBlock;
+    const int slot = p.idx[n];
     w.slot = slot >= 0 && slot < p.num_slots ? slot : -1;
-    w.init = w.slot >= 0 && p.has_init[w.n] != 0;
+    w.init = w.slot >= 0 && p.has_init[n] != 0;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    w.tmem = *base;
+    const uint32_t tm = *base;
+    // registers: 2 x 128 x 104 + 128 x 32 of the launch's 384 x 80
     if (warp < kMakers) {
-        make<S>(w, p, warp, lane);
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+        make<S>(w, p, tm, warp, lane);
         tc_fence_before();
         __syncthreads();
     } else {
-        Issuer i{w, p, lane};
-        i.go();
-        i.finish();
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 32;");
+        if (warp == kMakers) {
+            Issuer i{w, elect_one()};
+            i.go(tm);
+            i.finish();
+        } else {
+            Turner t{w, &v_map, warp - kMakers - 1, lane};
+            t.go();
+            t.finish();
+        }
         __syncthreads();
         __syncwarp();
-        tc_fence_after();
-        if (*w.abort && lane == 0) atomicOr(p.status, 1);
-        tmem_dealloc(w.tmem, kTmCols);
+        if (warp == kMakers) {
+            tc_fence_after();
+            if (abort_flag() && lane == 0) atomicOr(p.status, 1);
+            tmem_dealloc(tm, kTmCols);
+        }
     }
 }
 
+// A [T][H][128] view of bf16 in boxes of 64 values x 1 head x 64 tokens, swizzled; tokens past
+// the end read as zeros.
+bool make_v_map(CUtensorMap* m, const DeltaParams& p) {
+    typedef CUresult (*Encode)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                               const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                               CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static const Encode encode = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+                        q == cudaDriverEntryPointSuccess;
+        return ok ? reinterpret_cast<Encode>(f) : nullptr;
+    }();
+    if (!encode) return false;
+    const cuuint64_t dims[3] = {D, (cuuint64_t)p.H, (cuuint64_t)p.T};
+    // a dimension of one entry never steps: any stride that encodes will do
+    const cuuint64_t strides[2] = {(cuuint64_t)(p.H == 1 ? D : p.v_sh) * 2, (cuuint64_t)(p.T == 1 ? D : p.v_st) * 2};
+    const cuuint32_t box[3] = {64, 1, C}, step[3] = {1, 1, 1};
+    return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<__nv_bfloat16*>(p.v), dims, strides, box, step,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <class S>
-cudaError_t launch(const DeltaParams& p, cudaStream_t s) {
+cudaError_t launch(const DeltaParams& p, const CUtensorMap& v_map, cudaStream_t s) {
     static unsigned configured = 0;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -613,7 +748,7 @@ cudaError_t launch(const DeltaParams& p, cudaStream_t s) {
         if (e != cudaSuccess) return e;
         if (dev < 32) configured |= 1u << dev;
     }
-    kda_delta_walk<S><<<(unsigned)(p.n_long * p.H), kThreads, kSmemBytes, s>>>(p);
+    kda_delta_walk<S><<<(unsigned)(p.n_long * p.H), kThreads, kSmemBytes, s>>>(p, v_map);
     return cudaGetLastError();
 }
 
@@ -621,9 +756,11 @@ cudaError_t launch(const DeltaParams& p, cudaStream_t s) {
 
 cudaError_t launch_delta_walk(const DeltaParams& p, cudaStream_t s) {
     if (p.n_long <= 0) return cudaSuccess;
-    if (p.st_dtype == KDA_STATE_F32) return launch<float>(p, s);
-    if (p.st_dtype == KDA_STATE_BF16) return launch<__nv_bfloat16>(p, s);
-    return launch<__half>(p, s);
+    CUtensorMap v_map;
+    if (!make_v_map(&v_map, p)) return cudaErrorInvalidValue;
+    if (p.st_dtype == KDA_STATE_F32) return launch<float>(p, v_map, s);
+    if (p.st_dtype == KDA_STATE_BF16) return launch<__nv_bfloat16>(p, v_map, s);
+    return launch<__half>(p, v_map, s);
 }
 
 }  // namespace kda
