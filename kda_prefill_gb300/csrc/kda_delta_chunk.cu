@@ -120,11 +120,12 @@ __global__ void __launch_bounds__(kThreads, 3) kda_delta_chunk(const __grid_cons
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t chunk = blockIdx.x / p.H;
     const int h = blockIdx.x % p.H;
+    if (tid == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (blockIdx.x == 0 && warp == 0) write_status(p, lane);
     const int n = p.chunk_seq[chunk], t0 = p.chunk_tok[chunk];
     const int len = min(C, p.cu[n + 1] - t0);
     uint8_t* const blk = p.blocks + (chunk * p.H + h) * (int64_t)kDeltaBlock;
-    DeltaScalars* const scal = reinterpret_cast<DeltaScalars*>(blk + kDeltaScal);
+    DeltaScalars* const scal = reinterpret_cast<DeltaScalars*>(blk);
 
     // k and q
     {

@@ -7,14 +7,19 @@
 //     U = R T^T,  O = X_q + R (P T)^T 128 x 64 x 64
 //     S' = e^{G_C} S + (w U) k        128 x 128 x 64
 //
-// All products have the value rows as their M: a thread keeps half a row of S in fp32
-// registers, and everything it rounds, scales or stores belongs to that row.  Rows are
-// independent of each other but for the keys, so nothing has to be summed across threads.
+// All products have the value rows as their M: a thread keeps a quarter of a row of S in fp32
+// registers, and everything it rounds or scales belongs to that row.  Rows are independent of
+// each other but for the keys, so nothing has to be summed across threads.
 //
-// One CTA walks one (sequence, head); two share an SM, and one's products run while the
-// other's threads make operands.  Warps 0-7 make operands, two for each 32 rows, and write
-// the outputs; warp 8 issues the products and most copies; warps 9-11 turn v over, so that a
-// value row's tokens lie beside each other, and find its largest.
+// A CTA walks one (sequence, head), its warps in roles:
+//   0-15   operands: four warps for each 32 rows
+//   16-19  the output rows
+//   20     issues the products and the blocks' copies
+//   21-23  turn v over, so that a value row's tokens lie beside each other, and find its
+//          largest
+// The chain X, R, U, dS, S of one chunk after the other is the bound: the roles keep all
+// else off it, and an SM has one CTA, whose registers then let a warp have all its values of a step
+// in flight (two CTAs of half as many registers took 10.7 K cycles a chunk).
 //
 // Rounding.  Operands are fp16: k exactly, up to its row's power of two; S, R, U and T as
 // the sum of two (22 bits; with one, a state would be off by 2^-12).  The outputs' own terms,
@@ -41,55 +46,57 @@ using namespace dev;
 
 constexpr int D = kD;
 constexpr int C = kC;
-constexpr int kThreads = 384;
-constexpr int kMakers = 8;   // warps 0 .. 7
-constexpr int kTurners = 3;  // warps 9 .. 11
+constexpr int kThreads = 768;
+constexpr int kMakers = 16;  // warps 0 .. 15, four parts of each row
+constexpr int kWriters = 4;  // warps 16 .. 19
+constexpr int kIssuer = 20;
+constexpr int kTurners = 3;  // warps 21 .. 23
+constexpr int kKeys = D / 4, kToks = C / 4;  // of a maker
 
 // Shared memory.
 constexpr int kTile = C * D * 2;
-constexpr int kSmK = 0;                          // [2] k
-constexpr int kSmQ = kSmK + 2 * kTile;
-constexpr int kSmT = kSmQ + kTile;               // T's parts, then P T
-constexpr int kSmV = kSmT + 3 * C * C * 2;       // v as it comes
-constexpr int kSmVT = kSmV + kTile;              // [128][64] v by value rows, 16-byte pieces swizzled
-constexpr int kSmScal = kSmVT + kTile;           // [2] scalars
-constexpr int kSmVMax = kSmScal + 2 * kDeltaScalBytes;  // [128] largest |v| of a value row
-constexpr int kSmSMax = kSmVMax + D * 4;         // [2][2][128] largest |S| of half a row
-constexpr int kSmBad = kSmSMax + 4 * D * 4;      // [2][128] tokens whose R is not finite
-constexpr int kSmBar = kSmBad + 2 * D * 4;
+constexpr int kSmBlock = 0;                      // [2] blocks of kda_delta_chunk
+constexpr int kSmV = kSmBlock + 2 * kDeltaBlock; // v as it comes
+constexpr int kSmVT = kSmV + kTile;              // [2][128][64] v by value rows, 16-byte pieces swizzled
+constexpr int kSmVMax = kSmVT + 2 * kTile;       // [2][128] largest |v| of a value row
+constexpr int kSmSMax = kSmVMax + 2 * D * 4;     // [2][4][128] largest |S| of a quarter of a row
+constexpr int kSmBad = kSmSMax + 8 * D * 4;      // [2][128][4] tokens whose R is not finite, 16 bits a maker
+constexpr int kSmInv = kSmBad + 2 * D * 8;       // [2][128] the rows' scales undone
+constexpr int kSmBar = kSmInv + 2 * D * 4;
 enum Bar {
-    kFullK = 0,             // [2] k and scalars
-    kFullV = kFullK + 2,
-    kFullQ,
-    kFullT,
+    kFull = 0,              // [2] block there
+    kFullV = kFull + 2,
     kXDone,
     kUDone,
-    kODone,
     kDDone,
-    kEnd,
-    kTurned,                // v turned over, its largest found
-    kSReady,
+    kODone,                 // [2] by the place of O
+    kEnd = kODone + 2,
+    kTurned,                // [2] v turned over, its largest found
+    kOEmpty = kTurned + 2,  // [2] O read
+    kVEmpty = kOEmpty + 2,  // [2] v's rows read
+    kSReady = kVEmpty + 2,
     kRReady,
     kUReady,
     kNumBars
 };
 constexpr int kSmMisc = kSmBar + kNumBars * 8;   // abort flag, tensor-memory base
 constexpr int kSmemBytes = kSmMisc + 16;
-static_assert(2 * (kSmemBytes + 1024) <= 233472, "two CTAs on an SM");
-static_assert(kSmT % 1024 == 0 && kSmV % 1024 == 0 && kSmVT % 1024 == 0 && kSmBar % 8 == 0, "alignment");
+static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
+static_assert(kDeltaBlock % 1024 == 0 && kDeltaK % 1024 == 0 && kSmV % 1024 == 0 && kSmVT % 1024 == 0 && kSmBar % 8 == 0, "alignment");
 
 // Tensor memory columns.  Operands have, for 16 of their K, 8 columns of the high part and 8
-// of the low one.  Half of S's operand, and then of dS, lies where a half's warps alone write.
-constexpr uint32_t kTmCols = 256;
-constexpr uint32_t kTmS = 0;      // S: keys 0-63, 64-127; R in its first half, U in its second
-constexpr uint32_t kTmR = 0;
-constexpr uint32_t kTmU = 64;
-constexpr uint32_t kTmX = 128;    // X_k; then R T^T; then dS of keys 64-127
-constexpr uint32_t kTmO = 192;
-__host__ __device__ constexpr uint32_t ds_column(int half) { return half ? kTmX : 0; }
+// of the low one.
+constexpr uint32_t kTmCols = 512;
+constexpr uint32_t kTmS = 0;
+constexpr uint32_t kTmR = 128;
+constexpr uint32_t kTmU = 192;
+constexpr uint32_t kTmX = 256;    // X_k; then, with U's place, dS
+constexpr uint32_t kTmUAcc = 320;
+constexpr uint32_t kTmDS = 256;
+constexpr uint32_t kTmO = 384;    // [2]
 
 constexpr uint32_t kIdescKK = mma_idesc(0, 0, 0, 128, 64);  // B K-major
-constexpr uint32_t kIdescKM = mma_idesc(0, 0, 1, 128, 64);  // B MN-major
+constexpr uint32_t kIdescKM = mma_idesc(0, 0, 1, 128, 128); // B MN-major
 
 extern __shared__ __align__(1024) uint8_t smem[];
 
@@ -209,122 +216,106 @@ __device__ __forceinline__ void arrive_warp(int b, int lane) {
     __syncwarp();
     if (lane == 0) mbar_arrive(bar(b));
 }
-__device__ __forceinline__ const DeltaScalars* scalars(int c) {
-    return reinterpret_cast<const DeltaScalars*>(smem + kSmScal + (c & 1) * kDeltaScalBytes);
+__device__ __forceinline__ uint8_t* block(int c) { return smem + kSmBlock + (c & 1) * kDeltaBlock; }
+__device__ __forceinline__ const DeltaScalars* scalars(int c) { return reinterpret_cast<const DeltaScalars*>(block(c)); }
+__device__ __forceinline__ volatile float* vmax(int c) { return reinterpret_cast<volatile float*>(smem + kSmVMax) + (c & 1) * D; }
+__device__ __forceinline__ volatile float* smax_of(int c, int part) {
+    return reinterpret_cast<volatile float*>(smem + kSmSMax) + ((c & 1) * 4 + part) * D;
 }
-__device__ __forceinline__ volatile float* vmax() { return reinterpret_cast<volatile float*>(smem + kSmVMax); }
-__device__ __forceinline__ volatile float* smax_of(int c, int half) {
-    return reinterpret_cast<volatile float*>(smem + kSmSMax) + ((c & 1) * 2 + half) * D;
+__device__ __forceinline__ volatile uint2* bad_of(int c, int row) {
+    return reinterpret_cast<volatile uint2*>(smem + kSmBad) + (c & 1) * D + row;
 }
-__device__ __forceinline__ volatile unsigned* bad_of(int half) {
-    return reinterpret_cast<volatile unsigned*>(smem + kSmBad) + half * D;
-}
+__device__ __forceinline__ volatile float* inv_of(int c) { return reinterpret_cast<volatile float*>(smem + kSmInv) + (c & 1) * D; }
 
 struct Walk {
-    int h, slot, t0, len, chunks;
+    int h, t0, len, chunks;
     const uint8_t* blocks;  // of the first chunk
     int64_t step;           // bytes between chunks' blocks
-    bool init;
+    bool outputs, values;   // makes outputs; has values (not the rows of a transition)
 };
 
-// Warp 8: products, and the copies of a chunk's block.
+// Warp 20: products, and the copies of the chunks' blocks.
 struct Issuer {
     const Walk& w;
     const bool lead;
-    int k_loads = 0, q_loads = 0, t_loads = 0;
+    int loads = 0;
 
-    __device__ __forceinline__ void load_k(int c) {
+    __device__ __forceinline__ void load(int c) {
         if (lead) {
-            uint64_t* b = bar(kFullK + (c & 1));
-            mbar_arrive_expect_tx(b, kTile + (uint32_t)sizeof(DeltaScalars));
-            bulk_g2s(smem + kSmK + (c & 1) * kTile, w.blocks + c * w.step + kDeltaK, kTile, b);
-            bulk_g2s(smem + kSmScal + (c & 1) * kDeltaScalBytes, w.blocks + c * w.step + kDeltaScal, sizeof(DeltaScalars), b);
+            const uint32_t bytes = w.outputs ? kDeltaBlock : kDeltaQ;
+            mbar_arrive_expect_tx(bar(kFull + (c & 1)), bytes);
+            bulk_g2s(block(c), w.blocks + c * w.step, bytes, bar(kFull + (c & 1)));
         }
         __syncwarp();
-        ++k_loads;
-    }
-    __device__ __forceinline__ void load_q(int c) {
-        if (lead) {
-            mbar_arrive_expect_tx(bar(kFullQ), kTile);
-            bulk_g2s(smem + kSmQ, w.blocks + c * w.step + kDeltaQ, kTile, bar(kFullQ));
-        }
-        __syncwarp();
-        ++q_loads;
-    }
-    __device__ __forceinline__ void load_t(int c) {
-        if (lead) {
-            mbar_arrive_expect_tx(bar(kFullT), 3 * C * C * 2);
-            bulk_g2s(smem + kSmT, w.blocks + c * w.step + kDeltaT, 2 * C * C * 2, bar(kFullT));
-            bulk_g2s(smem + kSmT + 2 * C * C * 2, w.blocks + c * w.step + kDeltaPT, C * C * 2, bar(kFullT));
-        }
-        __syncwarp();
-        ++t_loads;
+        ++loads;
     }
     __device__ __forceinline__ bool go(uint32_t tm) {
-        // descriptors; their addresses count 16 bytes
-        constexpr uint64_t kHalf = kTile / 2 >> 4;
-        load_k(0);
-        load_q(0);
-        load_t(0);
-        if (w.chunks > 1) load_k(1);
+        constexpr uint64_t kHalf = kTile / 2 >> 4;  // descriptors' addresses count 16 bytes
+        grid_dep_wait();                            // the blocks are written
+        load(0);
+        if (w.chunks > 1) load(1);
 #pragma unroll 1
         for (int c = 0; c < w.chunks; ++c) {
-            const uint32_t kt = smem_u32(smem + kSmK) + (c & 1) * kTile;
-            if (!wait(kFullK + (c & 1), c >> 1) || !wait(kFullQ, c) || !wait(kSReady, c)) return false;
+            const uint32_t at = smem_u32(block(c)), o = tm + kTmO + (c & 1) * C;
+            if (!wait(kFull + (c & 1), c >> 1) || !wait(kSReady, c)) return false;
             tc_fence_after();
             if (lead) {
-                const uint64_t kd = sw128_desc(kt, 0, 1024), qd = sw128_desc(smem_u32(smem + kSmQ), 0, 1024);
+                const uint64_t kd = sw128_desc(at + kDeltaK, 0, 1024);
 #pragma unroll
                 for (int s = 0; s < 8; ++s)
 #pragma unroll
                     for (int part = 0; part < 2; ++part)
                         mma_f16_ts(tm + kTmX, tm + kTmS + 16 * s + 8 * part, kd + (s >> 2) * kHalf + (s & 3) * 2, kIdescKK,
                                    s > 0 || part > 0);
-#pragma unroll
-                for (int s = 0; s < 8; ++s)
-                    mma_f16_ts(tm + kTmO, tm + kTmS + 16 * s, qd + (s >> 2) * kHalf + (s & 3) * 2, kIdescKK, s > 0);
                 mma_commit(bar(kXDone));
             }
             __syncwarp();
-            // the chunk before's k has been used
-            if (c >= 1 && c + 1 < w.chunks) load_k(c + 1);
-            if (!wait(kFullT, c) || !wait(kRReady, c)) return false;
+            // the chunk before's products are over, and its outputs read
+            if (w.outputs && c >= 1 && !wait(kOEmpty + ((c - 1) & 1), (c - 1) >> 1)) return false;
+            if (c >= 1 && c + 1 < w.chunks) load(c + 1);
+            if (w.outputs) {
+                tc_fence_after();
+                if (lead) {
+                    const uint64_t qd = sw128_desc(at + kDeltaQ, 0, 1024);
+#pragma unroll
+                    for (int s = 0; s < 8; ++s)
+                        mma_f16_ts(o, tm + kTmS + 16 * s, qd + (s >> 2) * kHalf + (s & 3) * 2, kIdescKK, s > 0);
+                }
+                __syncwarp();
+            }
+            if (!wait(kRReady, c)) return false;
             tc_fence_after();
             if (lead) {
-                const uint64_t td = sw128_desc(smem_u32(smem + kSmT), 0, 1024);
+                const uint64_t td = sw128_desc(at + kDeltaT, 0, 1024);
 #pragma unroll
                 for (int s = 0; s < 4; ++s) {
                     const uint64_t hi = td + 2 * s, lo = hi + (C * C * 2 >> 4);
-                    mma_f16_ts(tm + kTmX, tm + kTmR + 16 * s, lo, kIdescKK, s > 0);
-                    mma_f16_ts(tm + kTmX, tm + kTmR + 16 * s + 8, hi, kIdescKK, 1);
-                    mma_f16_ts(tm + kTmX, tm + kTmR + 16 * s, hi, kIdescKK, 1);
+                    mma_f16_ts(tm + kTmUAcc, tm + kTmR + 16 * s, lo, kIdescKK, s > 0);
+                    mma_f16_ts(tm + kTmUAcc, tm + kTmR + 16 * s + 8, hi, kIdescKK, 1);
+                    mma_f16_ts(tm + kTmUAcc, tm + kTmR + 16 * s, hi, kIdescKK, 1);
                 }
                 mma_commit(bar(kUDone));
+                if (w.outputs) {
+                    const uint64_t pd = sw128_desc(at + kDeltaPT, 0, 1024);
 #pragma unroll
-                for (int s = 0; s < 4; ++s)
-                    mma_f16_ts(tm + kTmO, tm + kTmR + 16 * s, td + (2 * C * C * 2 >> 4) + 2 * s, kIdescKK, 1);
-                mma_commit(bar(kODone));
+                    for (int s = 0; s < 4; ++s) mma_f16_ts(o, tm + kTmR + 16 * s, pd + 2 * s, kIdescKK, 1);
+                    mma_commit(bar(kODone + (c & 1)));
+                }
             }
             __syncwarp();
-            // X's products have read q
-            if (c + 1 < w.chunks) load_q(c + 1);
             if (!wait(kUReady, c)) return false;
             tc_fence_after();
             if (lead) {
-                const uint64_t km = sw128_desc(kt, kTile / 2, 1024);
+                const uint64_t km = sw128_desc(at + kDeltaK, kTile / 2, 1024);
 #pragma unroll
-                for (int half = 0; half < 2; ++half)
-#pragma unroll
-                    for (int s = 0; s < 4; ++s) {
-                        const uint64_t b = km + half * kHalf + s * (2048 >> 4);
-                        mma_f16_ts(tm + ds_column(half), tm + kTmU + 16 * s + 8, b, kIdescKM, s > 0);
-                        mma_f16_ts(tm + ds_column(half), tm + kTmU + 16 * s, b, kIdescKM, 1);
-                    }
+                for (int s = 0; s < 4; ++s) {
+                    const uint64_t b = km + s * (2048 >> 4);
+                    mma_f16_ts(tm + kTmDS, tm + kTmU + 16 * s + 8, b, kIdescKM, s > 0);
+                    mma_f16_ts(tm + kTmDS, tm + kTmU + 16 * s, b, kIdescKM, 1);
+                }
                 mma_commit(bar(kDDone));
             }
             __syncwarp();
-            if (!wait(kODone, c)) return false;
-            if (c + 1 < w.chunks) load_t(c + 1);
         }
         return true;
     }
@@ -334,16 +325,14 @@ struct Issuer {
         __syncwarp();
         bool ok = mbar_wait(bar(kEnd), 0);
         for (int i = 0; i < 2; ++i) {
-            const int n = (k_loads + 1 - i) / 2;  // loads of slot i
-            if (n > 0) ok = mbar_wait(bar(kFullK + i), (n - 1) & 1) && ok;
+            const int n = (loads + 1 - i) / 2;  // loads of slot i
+            if (n > 0) ok = mbar_wait(bar(kFull + i), (n - 1) & 1) && ok;
         }
-        if (q_loads > 0) ok = mbar_wait(bar(kFullQ), (q_loads - 1) & 1) && ok;
-        if (t_loads > 0) ok = mbar_wait(bar(kFullT), (t_loads - 1) & 1) && ok;
         if (!ok) abort_flag() = 1;
     }
 };
 
-// Warps 9-11: v by value rows, and each row's largest finite |v|.  Tokens past the sequence's
+// Warps 21-23: v by value rows, and each row's largest finite |v|.  Tokens past the sequence's
 // end are zeros.
 struct Turner {
     const Walk& w;
@@ -364,10 +353,9 @@ struct Turner {
         if (which == 0) load_v(0);
 #pragma unroll 1
         for (int c = 0; c < w.chunks; ++c) {
-            // the makers have read the chunk before's
-            if (!wait(kFullV, c) || (c > 0 && !wait(kRReady, c - 1))) return false;
+            if (!wait(kFullV, c) || (c > 1 && !wait(kVEmpty + (c & 1), (c >> 1) - 1))) return false;
             const int live = w.len - c * C;
-            const uint32_t from = smem_u32(smem + kSmV), to = smem_u32(smem + kSmVT);
+            const uint32_t from = smem_u32(smem + kSmV), to = smem_u32(smem + kSmVT) + (c & 1) * kTile;
 #pragma unroll 1
             for (int g = which; g < D / 8; g += kTurners) {
                 uint32_t r[8];
@@ -402,12 +390,12 @@ struct Turner {
                 }
                 f = fmaxf(f, __shfl_xor_sync(0xffffffffu, f, 1));
                 f = fmaxf(f, __shfl_xor_sync(0xffffffffu, f, 2));
-                if ((lane & 3) == 0) vmax()[8 * g + (lane >> 2)] = f;
+                if ((lane & 3) == 0) vmax(c)[8 * g + (lane >> 2)] = f;
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(kTurned));
+            if (lane == 0) mbar_arrive(bar(kTurned + (c & 1)));
             if (which == 0 && c + 1 < w.chunks) {
-                if (!wait(kTurned, c)) return false;
+                if (!wait(kTurned + (c & 1), c >> 1)) return false;
                 load_v(c + 1);
             }
         }
@@ -432,49 +420,107 @@ __device__ __noinline__ uint2 poisoned(uint2 bad, uint2 clears) {
     return r;
 }
 
-// Warps 0-7: a thread has half of value row `row`: 64 keys, 32 of a chunk's tokens.
-template <class S>
-__device__ __forceinline__ bool make(const Walk& w, const DeltaParams& p, uint32_t base, int warp, int lane) {
-    const int half = warp >> 2, row = 32 * (warp & 3) + lane;
-    const uint32_t tm = base + ((uint32_t)(32 * (warp & 3)) << 16);
-    constexpr int N = 16 / sizeof(S);
-    f2 s[32];
-    {
-        const S* state = static_cast<const S*>(p.pool) + (w.init ? (size_t)w.slot * p.stride0 : 0) +
-                         ((size_t)w.h * D + row) * D + half * 64;
+// Warps 16-19: a thread has an output row's 64 tokens.
+__device__ __forceinline__ bool write(const Walk& w, const DeltaParams& p, uint32_t base, int warp, int lane) {
+    const int row = 32 * (warp & 3) + lane;
+    const uint32_t tm = base + ((uint32_t)(32 * (warp & 3)) << 16) + kTmO;
+    const int64_t st = (int64_t)p.H * D;
+#pragma unroll 1
+    for (int c = 0; c < w.chunks; ++c) {
+        if (!wait(kODone + (c & 1), c >> 1)) return false;
+        tc_fence_after();
+        const DeltaScalars* sc = scalars(c);
+        uint2 spoils = make_uint2(bad_of(c, row)->x, bad_of(c, row)->y);
+        if (__any_sync(0xffffffffu, (spoils.x | spoils.y) != 0)) spoils = poisoned(spoils, make_uint2(sc->clears[0], sc->clears[1]));
+        const int live = w.len - c * C;
+        const float f = inv_of(c)[row] * p.scale;
+        __nv_bfloat16* o = p.out + ((int64_t)(w.t0 + c * C) * p.H + w.h) * D + row;
+#pragma unroll 1
+        for (int b = 0; b < C; b += 16) {
+            f2 x[8];
+            load16(tm + (c & 1) * C + b, x);
 #pragma unroll
-        for (int i = 0; i < 64; i += N) {
-            float f[N] = {};
-            if (w.init) rows::load<S, N>(state + i).get(f);
+            for (int i = 0; i < 8; i += 2) {
+                const float4 d = *reinterpret_cast<const float4*>(sc->down + b + 2 * i);
+                x[i] = mul2(mul2(x[i], pack2(d.x, d.y)), pack2(f, f));
+                x[i + 1] = mul2(mul2(x[i + 1], pack2(d.z, d.w)), pack2(f, f));
+            }
+            const unsigned lost = (b < 32 ? spoils.x : spoils.y) >> (b & 31);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float2 y = unpack2(x[i]);
+                if (b + 2 * i < live) o[0] = __float2bfloat16_rn(lost >> (2 * i) & 1 ? NAN : y.x);
+                if (b + 2 * i + 1 < live) o[st] = __float2bfloat16_rn(lost >> (2 * i + 1) & 1 ? NAN : y.y);
+                o += 2 * st;
+            }
+        }
+        arrive_warp(kOEmpty + (c & 1), lane);
+    }
+    return true;
+}
+
+// Warps 0-15: a thread has a quarter of value row `row`: 32 keys, 16 of a chunk's tokens.
+// Starts from `state` (fp32 values if it is a plane, S if of the pool; 0: from zero, or from
+// the identity) and leaves the state there.
+template <class S>
+__device__ __forceinline__ bool make(const Walk& w, const DeltaParams& p, uint32_t base, int warp, int lane, const S* from,
+                                     const float* plane, f2 (&s)[kKeys / 2], bool& cleared) {
+    const int part = warp >> 2, row = 32 * (warp & 3) + lane;
+    const uint32_t tm = base + ((uint32_t)(32 * (warp & 3)) << 16);
+    const int at = row * D + part * kKeys;
+    constexpr int N = 16 / sizeof(S);
+#pragma unroll
+    for (int i = 0; i < kKeys / 2; ++i) s[i] = 0;
+    if (from) {
+#pragma unroll
+        for (int i = 0; i < kKeys; i += N) {
+            float f[N];
+            rows::load<S, N>(from + at + i).get(f);
 #pragma unroll
             for (int j = 0; j < N; j += 2) s[(i + j) / 2] = pack2(f[j], f[j + 1]);
         }
+    } else if (plane) {
+#pragma unroll
+        for (int i = 0; i < kKeys; i += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(plane + at + i);
+            s[i / 2] = pack2(f.x, f.y), s[i / 2 + 1] = pack2(f.z, f.w);
+        }
+    } else if (!w.values) {
+#pragma unroll
+        for (int i = 0; i < kKeys; i += 2) {
+            const int key = part * kKeys + i;
+            s[i / 2] = pack2(key == row ? 1.f : 0.f, key + 1 == row ? 1.f : 0.f);
+        }
     }
+    cleared = false;
     float smax = 0.f;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) smax = max_abs(smax, s[i]);
-    smax_of(0, half)[row] = smax;
+    for (int i = 0; i < kKeys / 2; ++i) smax = max_abs(smax, s[i]);
+    smax_of(0, part)[row] = smax;
     asm volatile("bar.sync 1, %0;" ::"n"(kMakers * 32) : "memory");
-    // the largest |S| a chunk ago; what the chunk adds to |S| at most
-    float was = max_nan(smax, smax_of(0, half ^ 1)[row]), adds, scale, inv;
+    // the largest |S| of the row a chunk ago; what a chunk adds to |S| at most
+    auto of_row = [&](int c) {
+        return max_nan(max_nan(smax_of(c, 0)[row], smax_of(c, 1)[row]), max_nan(smax_of(c, 2)[row], smax_of(c, 3)[row]));
+    };
+    float was = of_row(0), adds, scale, inv;
     auto rescale = [&](int c, float grown) {
-        const float at = 11.32f * (finite(was) ? was : 0.f) + grown;  // |S| <= sqrt(128) max
-        const float b = scalars(c)->strongest, m = vmax()[row];
+        const float l = 11.32f * (finite(was) ? was : 0.f) + grown;  // |S| <= sqrt(128) max
+        const float b = scalars(c)->strongest, m = w.values ? vmax(c)[row] : 0.f;
         adds = 64.f * b * m;
         // (v itself has to stay finite when it is scaled)
-        scale = scale_of(fmaxf(fmaxf(at, b * (m + at + adds)), 0x1p-60f * m), inv);
+        scale = scale_of(fmaxf(fmaxf(l, b * (m + l + adds)), 0x1p-60f * m), inv);
     };
     // 16 keys of S's operand; of a row with infinities or NaN as zeros
     auto store_s = [&](int b, bool live) {
         f2 x[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = live ? mul2(s[8 * b + i], pack2(scale, scale)) : 0;
-        store_split(tm + kTmS + 64 * half + 16 * b, x);
+        store_split(tm + kTmS + kKeys * part + 16 * b, x);
     };
-    if (!wait(kTurned, 0) || !wait(kFullK, 0)) return false;
+    if ((w.values && !wait(kTurned, 0)) || !wait(kFull, 0)) return false;
     rescale(0, 0.f);
-#pragma unroll
-    for (int b = 0; b < 4; ++b) store_s(b, finite(smax));
+    store_s(0, finite(smax));
+    store_s(1, finite(smax));
     tmem_wait_st();
     arrive_warp(kSReady, lane);
 
@@ -482,145 +528,102 @@ __device__ __forceinline__ bool make(const Walk& w, const DeltaParams& p, uint32
     for (int c = 0; c < w.chunks; ++c) {
         const DeltaScalars* sc = scalars(c);
         // R
+        const int clear = sc->first_clear;
+        cleared = cleared || clear < C;
+        uint4 v[2] = {};
+        if (w.values) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                v[j] = *reinterpret_cast<const uint4*>(smem + kSmVT + (c & 1) * kTile + row * 128 + (((2 * part + j) ^ (row & 7)) << 4));
+        }
         if (!wait(kXDone, c)) return false;
         tc_fence_after();
-        // both halves' largest of the state that the chunk starts from
-        if (c > 0) was = max_nan(smax, smax_of(c, half ^ 1)[row]);
-        const int clear = sc->first_clear - 32 * half;  // among this half's tokens
-        const bool dead = !finite(was);
-        unsigned bad = 0;
-#pragma unroll 1
-        for (int b = 0; b < 32; b += 16) {
+        {
             f2 x[8];
-            load16(tm + kTmX + 32 * half + b, x);
-            if (clear < b + 16) {
+            load16(tm + kTmX + kToks * part, x);
+            if (c > 0) was = of_row(c);
+            const bool dead = !finite(was);
+            const int mine = clear - kToks * part;  // among this thread's tokens
+            if (mine < kToks) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const float2 f = unpack2(x[i]);
-                    x[i] = pack2(b + 2 * i < clear ? f.x : 0.f, b + 2 * i + 1 < clear ? f.y : 0.f);
+                    x[i] = pack2(2 * i < mine ? f.x : 0.f, 2 * i + 1 < mine ? f.y : 0.f);
                 }
             }
             f2 check = 0;
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const uint4 v = *reinterpret_cast<const uint4*>(smem + kSmVT + row * 128 + (((4 * half + b / 8 + j) ^ (row & 7)) << 4));
-                const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
+            for (int i = 0; i < 8; i += 2) {
+                const float4 ci = *reinterpret_cast<const float4*>(sc->c + kToks * part + 2 * i);
+                const float4 bi = *reinterpret_cast<const float4*>(sc->beta + kToks * part + 2 * i);
+                const f2 cc[2] = {pack2(-ci.x, -ci.y), pack2(-ci.z, -ci.w)};
+                const f2 bb[2] = {pack2(bi.x, bi.y), pack2(bi.z, bi.w)};
+                const uint4 vq = v[i / 4];
+                const uint32_t vw[2] = {i % 4 ? vq.z : vq.x, i % 4 ? vq.w : vq.y};
 #pragma unroll
-                for (int i = 0; i < 4; i += 2) {
-                    const float4 ci = *reinterpret_cast<const float4*>(sc->c + 32 * half + b + 8 * j + 2 * i);
-                    const float4 bi = *reinterpret_cast<const float4*>(sc->beta + 32 * half + b + 8 * j + 2 * i);
-                    const f2 cc[2] = {pack2(-ci.x, -ci.y), pack2(-ci.z, -ci.w)};
-                    const f2 bb[2] = {pack2(bi.x, bi.y), pack2(bi.z, bi.w)};
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const f2 vv = pack2(__uint_as_float(vw[i + u] << 16), __uint_as_float(vw[i + u] & 0xFFFF0000u));
-                        f2& y = x[4 * j + i + u];
-                        y = mul2(bb[u], fma2(cc[u], y, mul2(vv, pack2(scale, scale))));
-                        check = fma2(y, 0, check);
-                    }
+                for (int u = 0; u < 2; ++u) {
+                    const f2 vv = pack2(__uint_as_float(vw[u] << 16), __uint_as_float(vw[u] & 0xFFFF0000u));
+                    x[i + u] = mul2(bb[u], fma2(cc[u], x[i + u], mul2(vv, pack2(scale, scale))));
+                    check = fma2(x[i + u], 0, check);
                 }
             }
+            unsigned bad = 0;
             const float2 ch = unpack2(check);
             if (__any_sync(0xffffffffu, ch.x + ch.y != 0.f || dead)) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     float2 f = unpack2(x[i]);
-                    if (!finite(f.x) || (dead && b + 2 * i < clear)) bad |= 1u << (b + 2 * i), f.x = 0.f;
-                    if (!finite(f.y) || (dead && b + 2 * i + 1 < clear)) bad |= 2u << (b + 2 * i), f.y = 0.f;
+                    if (!finite(f.x) || (dead && 2 * i < mine)) bad |= 1u << (2 * i), f.x = 0.f;
+                    if (!finite(f.y) || (dead && 2 * i + 1 < mine)) bad |= 2u << (2 * i), f.y = 0.f;
                     x[i] = pack2(f.x, f.y);
                 }
             }
-            store_split(tm + kTmR + 32 * half + b, x);
+            store_split(tm + kTmR + kToks * part, x);
+            reinterpret_cast<volatile uint16_t*>(bad_of(c, row))[part] = (uint16_t)bad;
+            if (part == 0) inv_of(c)[row] = inv;
         }
-        bad_of(half)[row] = bad;
         tmem_wait_st();
         arrive_warp(kRReady, lane);
+        if (w.values && lane == 0) mbar_arrive(bar(kVEmpty + (c & 1)));
         // U
         if (!wait(kUDone, c)) return false;
         tc_fence_after();
-#pragma unroll 1
-        for (int b = 0; b < 32; b += 16) {
+        {
             f2 x[8];
-            load16(tm + kTmX + 32 * half + b, x);
+            load16(tm + kTmUAcc + kToks * part, x);
 #pragma unroll
             for (int i = 0; i < 8; i += 2) {
-                const float4 wi = *reinterpret_cast<const float4*>(sc->w + 32 * half + b + 2 * i);
+                const float4 wi = *reinterpret_cast<const float4*>(sc->w + kToks * part + 2 * i);
                 x[i] = mul2(x[i], pack2(wi.x, wi.y));
                 x[i + 1] = mul2(x[i + 1], pack2(wi.z, wi.w));
             }
-            store_split(tm + kTmU + 32 * half + b, x);
+            store_split(tm + kTmU + kToks * part, x);
         }
         tmem_wait_st();
         arrive_warp(kUReady, lane);
-        // outputs
-        if (!wait(kODone, c)) return false;
-        tc_fence_after();
-        const unsigned other = bad_of(half ^ 1)[row];
-        unsigned spoils = 0, lost = 0;
-        if (__any_sync(0xffffffffu, (bad | other) != 0)) {
-            const uint2 r = poisoned(half ? make_uint2(other, bad) : make_uint2(bad, other), make_uint2(sc->clears[0], sc->clears[1]));
-            spoils = half ? r.y : r.x;
-            lost = r.y >> 31;
-        }
-        {
-            const int live = w.len - c * C - half * 32;  // of this half's tokens
-            const f2 f = pack2(inv * p.scale, inv * p.scale);
-            const int64_t st = (int64_t)p.H * D;
-            __nv_bfloat16* o = p.out + ((int64_t)(w.t0 + c * C + half * 32) * p.H + w.h) * D + row;
-#pragma unroll 1
-            for (int b = 0; b < 32; b += 16) {
-                f2 x[8];
-                load16(tm + kTmO + 32 * half + b, x);
-#pragma unroll
-                for (int i = 0; i < 8; i += 2) {
-                    const float4 di = *reinterpret_cast<const float4*>(sc->down + 32 * half + b + 2 * i);
-                    x[i] = mul2(mul2(x[i], pack2(di.x, di.y)), f);
-                    x[i + 1] = mul2(mul2(x[i + 1], pack2(di.z, di.w)), f);
-                }
-                if (spoils) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float2 y = unpack2(x[i]);
-                        x[i] = pack2(spoils >> (b + 2 * i) & 1 ? NAN : y.x, spoils >> (b + 2 * i + 1) & 1 ? NAN : y.y);
-                    }
-                }
-                if (live >= b + 16) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float2 y = unpack2(x[i]);
-                        o[0] = __float2bfloat16_rn(y.x);
-                        o[st] = __float2bfloat16_rn(y.y);
-                        o += 2 * st;
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float2 y = unpack2(x[i]);
-                        if (b + 2 * i < live) o[0] = __float2bfloat16_rn(y.x);
-                        if (b + 2 * i + 1 < live) o[st] = __float2bfloat16_rn(y.y);
-                        o += 2 * st;
-                    }
-                }
-            }
-        }
         // S
         const bool more = c + 1 < w.chunks;
         const f2 gamma = pack2(sc->gamma, sc->gamma), back = pack2(2.f * inv, 2.f * inv);
-        if (sc->first_clear < C) {
+        if (clear < C) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) s[i] = 0;
+            for (int i = 0; i < kKeys / 2; ++i) s[i] = 0;
+        }
+        bool lost = false;
+        {
+            const uint2 bad = make_uint2(bad_of(c, row)->x, bad_of(c, row)->y);
+            if (__any_sync(0xffffffffu, (bad.x | bad.y) != 0)) lost = poisoned(bad, make_uint2(sc->clears[0], sc->clears[1])).y >> 31;
         }
         if (more) {
-            if (!wait(kTurned, c + 1) || !wait(kFullK + ((c + 1) & 1), (c + 1) >> 1)) return false;
+            if ((w.values && !wait(kTurned + ((c + 1) & 1), (c + 1) >> 1)) || !wait(kFull + ((c + 1) & 1), (c + 1) >> 1)) return false;
             rescale(c + 1, adds);
         }
         if (!wait(kDDone, c)) return false;
         tc_fence_after();
         smax = 0.f;
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
+        for (int b = 0; b < kKeys / 16; ++b) {
             f2 x[8];
-            load16(tm + ds_column(half) + 16 * b, x);
+            load16(tm + kTmDS + kKeys * part + 16 * b, x);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 s[8 * b + i] = fma2(gamma, s[8 * b + i], mul2(x[i], back));
@@ -631,47 +634,33 @@ __device__ __forceinline__ bool make(const Walk& w, const DeltaParams& p, uint32
         if (lost) {
             smax = NAN;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) s[i] = pack2(NAN, NAN);
+            for (int i = 0; i < kKeys / 2; ++i) s[i] = pack2(NAN, NAN);
         }
         if (more) {
             if (__any_sync(0xffffffffu, !finite(smax))) {
-#pragma unroll
-                for (int b = 0; b < 4; ++b) store_s(b, finite(smax));
+                store_s(0, finite(smax));
+                store_s(1, finite(smax));
             }
-            smax_of(c + 1, half)[row] = smax;
+            smax_of(c + 1, part)[row] = smax;
             tmem_wait_st();
             arrive_warp(kSReady, lane);
-        }
-    }
-    if (w.slot >= 0) {
-        S* state = static_cast<S*>(p.pool) + (size_t)w.slot * p.stride0 + ((size_t)w.h * D + row) * D + half * 64;
-#pragma unroll
-        for (int i = 0; i < 64; i += N) {
-            float f[N];
-#pragma unroll
-            for (int j = 0; j < N; j += 2) {
-                const float2 y = unpack2(s[(i + j) / 2]);
-                f[j] = y.x, f[j + 1] = y.y;
-            }
-            rows::Piece<S, N> x;
-            x.set(f);
-            rows::store<S, N>(state + i, x);
         }
     }
     return true;
 }
 
 template <class S>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, 1)
 kda_delta_walk(const __grid_constant__ DeltaParams p, const __grid_constant__ CUtensorMap v_map) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint32_t* const base = reinterpret_cast<uint32_t*>(smem + kSmMisc + 8);
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kNumBars; ++i) mbar_init(bar(i), i == kTurned ? kTurners : i >= kSReady ? kMakers : 1);
+        for (int i = 0; i < kNumBars; ++i)
+            mbar_init(bar(i), i >= kVEmpty ? kMakers : i >= kOEmpty ? kWriters : i >= kTurned ? kTurners : 1);
         abort_flag() = 0;
         fence_mbar_init();
     }
-    if (warp == kMakers) tmem_alloc(base, kTmCols);
+    if (warp == kIssuer) tmem_alloc(base, kTmCols);
     Walk w;
     w.h = blockIdx.x % p.H;
     const int n = p.long_list[blockIdx.x / p.H];
@@ -680,33 +669,57 @@ kda_delta_walk(const __grid_constant__ DeltaParams p, const __grid_constant__ CU
     w.chunks = (w.len + C - 1) / C;
     w.step = (int64_t)p.H * kDeltaBlock;
     w.blocks = p.blocks + ((int64_t)p.seq_off[n] * p.H + w.h) * kDeltaBlock;
+    w.outputs = w.values = true;
     const int slot = p.idx[n];
-    w.slot = slot >= 0 && slot < p.num_slots ? slot : -1;
-    w.init = w.slot >= 0 && p.has_init[n] != 0;
+    S* const state = slot >= 0 && slot < p.num_slots
+                         ? static_cast<S*>(p.pool) + (size_t)slot * p.stride0 + (size_t)w.h * D * D : nullptr;
+    const bool init = state && p.has_init[n] != 0;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = *base;
-    // registers: 2 x 128 x 104 + 128 x 32 of the launch's 384 x 80
+    // registers: 512 x 96 + 128 x 64 + 128 x 32 of the launch's 768 x 80
     if (warp < kMakers) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
-        make<S>(w, p, tm, warp, lane);
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
+        f2 s[kKeys / 2];
+        bool cleared;
+        if (make<S>(w, p, tm, warp, lane, init ? state : nullptr, nullptr, s, cleared) && state) {
+            constexpr int N = 16 / sizeof(S);
+            S* to = state + (32 * (warp & 3) + lane) * D + (warp >> 2) * kKeys;
+#pragma unroll
+            for (int i = 0; i < kKeys; i += N) {
+                float f[N];
+#pragma unroll
+                for (int j = 0; j < N; j += 2) {
+                    const float2 y = unpack2(s[(i + j) / 2]);
+                    f[j] = y.x, f[j + 1] = y.y;
+                }
+                rows::Piece<S, N> x;
+                x.set(f);
+                rows::store<S, N>(to + i, x);
+            }
+        }
+        tc_fence_before();
+        __syncthreads();
+    } else if (warp < kIssuer) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        if (w.outputs) write(w, p, tm, warp, lane);
         tc_fence_before();
         __syncthreads();
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 32;");
-        if (warp == kMakers) {
+        if (warp == kIssuer) {
             Issuer i{w, elect_one()};
             i.go(tm);
             i.finish();
-        } else {
-            Turner t{w, &v_map, warp - kMakers - 1, lane};
+        } else if (w.values) {
+            Turner t{w, &v_map, warp - kIssuer - 1, lane};
             t.go();
             t.finish();
         }
         __syncthreads();
         __syncwarp();
-        if (warp == kMakers) {
+        if (warp == kIssuer) {
             tc_fence_after();
             if (abort_flag() && lane == 0) atomicOr(p.status, 1);
             tmem_dealloc(tm, kTmCols);
@@ -748,8 +761,18 @@ cudaError_t launch(const DeltaParams& p, const CUtensorMap& v_map, cudaStream_t 
         if (e != cudaSuccess) return e;
         if (dev < 32) configured |= 1u << dev;
     }
-    kda_delta_walk<S><<<(unsigned)(p.n_long * p.H), kThreads, kSmemBytes, s>>>(p, v_map);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(p.n_long * p.H));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.stream = s;
+    // set up while the chunks' last CTAs still run
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kda_delta_walk<S>, p, v_map);
 }
 
 }  // namespace

@@ -107,15 +107,13 @@ struct DeltaParams : LinParams {
     int64_t n_chunks;
     uint8_t* blocks;  // [n_chunks][H] of kDeltaBlock bytes
 };
-// What kda_delta_chunk leaves for the walk of a chunk and head: fp16 tiles in the swizzled
-// layout of kda_device.cuh and fp32 scalars.
+// What kda_delta_chunk leaves for the walk of a chunk and head: fp32 scalars, and fp16 tiles in
+// the swizzled layout of kda_device.cuh.
 //   k   [64][128]  k times a power of two for each row
 //   t   [2][64][64] the triangular inverse's high and low part
-//   scalars         see DeltaScalars
 //   q   [64][128]  q^ e^G, each row times up
 //   pt  [64][64]   the scores times the inverse, each row times up
-constexpr int kDeltaK = 0;
-constexpr int kDeltaScal = 16384;
+// A walk without outputs needs the first kDeltaQ bytes.
 struct DeltaScalars {
     float c[kC];      // e^{G_i} and k's length: k^ e^{G_i} = c k
     float beta[kC];
@@ -127,12 +125,12 @@ struct DeltaScalars {
     float strongest;     // largest beta
     float unused[3];
 };
-constexpr int kDeltaScalBytes = 1152;
-constexpr int kDeltaT = kDeltaScal + kDeltaScalBytes;
+constexpr int kDeltaK = 2048;
+constexpr int kDeltaT = kDeltaK + 16384;
 constexpr int kDeltaQ = kDeltaT + 16384;
 constexpr int kDeltaPT = kDeltaQ + 16384;
 constexpr int kDeltaBlock = kDeltaPT + 8192;
-static_assert(sizeof(DeltaScalars) <= kDeltaScalBytes && sizeof(DeltaScalars) % 16 == 0, "room for the scalars");
+static_assert(sizeof(DeltaScalars) <= kDeltaK, "room for the scalars");
 // At most so many chunks: only sequences of more than kShortMax tokens have any.
 inline int64_t delta_chunks(int64_t T, int64_t N) {
     return T / kC + (T / (kShortMax + 1) < N ? T / (kShortMax + 1) : N);
