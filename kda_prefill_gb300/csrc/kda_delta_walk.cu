@@ -80,7 +80,13 @@ enum Bar {
     kNumBars
 };
 constexpr int kSmMisc = kSmBar + kNumBars * 8;   // abort flag, tensor-memory base
-constexpr int kSmemBytes = kSmMisc + 16;
+struct End {  // what happens to the state in the end
+    void* state;   // of the pool, or nullptr
+    float* plane;  // a segment's
+    float* kept;   // whether a transition is of cleared states, or nullptr
+};
+constexpr int kSmEnd = kSmMisc + 16;
+constexpr int kSmemBytes = kSmEnd + (int)sizeof(End);
 static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
 static_assert(kDeltaBlock % 1024 == 0 && kDeltaK % 1024 == 0 && kSmV % 1024 == 0 && kSmVT % 1024 == 0 && kSmBar % 8 == 0, "alignment");
 
@@ -151,6 +157,22 @@ __device__ __forceinline__ void load16(uint32_t a, f2 (&v)[8]) {
         : "memory");
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = pack2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+}
+__device__ __forceinline__ void load32(uint32_t a, f2 (&v)[16]) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+        "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+          "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+          "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(a)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = pack2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
 }
 __device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t (&r)[16]) {
     asm volatile(
@@ -530,11 +552,29 @@ __device__ __forceinline__ bool make(const Walk& w, const DeltaParams& p, uint32
         // R
         const int clear = sc->first_clear;
         cleared = cleared || clear < C;
-        uint4 v[2] = {};
-        if (w.values) {
+        // y0 + bc X, made of all but X while its products run
+        f2 y0[8], bc[8];
+        {
+            uint4 v[2] = {};
+            if (w.values) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-                v[j] = *reinterpret_cast<const uint4*>(smem + kSmVT + (c & 1) * kTile + row * 128 + (((2 * part + j) ^ (row & 7)) << 4));
+                for (int j = 0; j < 2; ++j)
+                    v[j] = *reinterpret_cast<const uint4*>(smem + kSmVT + (c & 1) * kTile + row * 128 + (((2 * part + j) ^ (row & 7)) << 4));
+            }
+            const uint32_t vw[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+                const float4 ci = *reinterpret_cast<const float4*>(sc->c + kToks * part + 2 * i);
+                const float4 bi = *reinterpret_cast<const float4*>(sc->beta + kToks * part + 2 * i);
+                const f2 cc[2] = {pack2(-ci.x, -ci.y), pack2(-ci.z, -ci.w)};
+                const f2 bb[2] = {pack2(bi.x, bi.y), pack2(bi.z, bi.w)};
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const f2 vv = pack2(__uint_as_float(vw[i + u] << 16), __uint_as_float(vw[i + u] & 0xFFFF0000u));
+                    y0[i + u] = mul2(bb[u], mul2(vv, pack2(scale, scale)));
+                    bc[i + u] = mul2(bb[u], cc[u]);
+                }
+            }
         }
         if (!wait(kXDone, c)) return false;
         tc_fence_after();
@@ -553,19 +593,9 @@ __device__ __forceinline__ bool make(const Walk& w, const DeltaParams& p, uint32
             }
             f2 check = 0;
 #pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-                const float4 ci = *reinterpret_cast<const float4*>(sc->c + kToks * part + 2 * i);
-                const float4 bi = *reinterpret_cast<const float4*>(sc->beta + kToks * part + 2 * i);
-                const f2 cc[2] = {pack2(-ci.x, -ci.y), pack2(-ci.z, -ci.w)};
-                const f2 bb[2] = {pack2(bi.x, bi.y), pack2(bi.z, bi.w)};
-                const uint4 vq = v[i / 4];
-                const uint32_t vw[2] = {i % 4 ? vq.z : vq.x, i % 4 ? vq.w : vq.y};
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const f2 vv = pack2(__uint_as_float(vw[u] << 16), __uint_as_float(vw[u] & 0xFFFF0000u));
-                    x[i + u] = mul2(bb[u], fma2(cc[u], x[i + u], mul2(vv, pack2(scale, scale))));
-                    check = fma2(x[i + u], 0, check);
-                }
+            for (int i = 0; i < 8; ++i) {
+                x[i] = fma2(bc[i], x[i], y0[i]);
+                check = fma2(x[i], 0, check);
             }
             unsigned bad = 0;
             const float2 ch = unpack2(check);
@@ -620,16 +650,18 @@ __device__ __forceinline__ bool make(const Walk& w, const DeltaParams& p, uint32
         if (!wait(kDDone, c)) return false;
         tc_fence_after();
         smax = 0.f;
+        {
+            f2 x[16];
+            load32(tm + kTmDS + kKeys * part, x);
 #pragma unroll
-        for (int b = 0; b < kKeys / 16; ++b) {
-            f2 x[8];
-            load16(tm + kTmDS + kKeys * part + 16 * b, x);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                s[8 * b + i] = fma2(gamma, s[8 * b + i], mul2(x[i], back));
-                smax = max_abs(smax, s[8 * b + i]);
+            for (int i = 0; i < 16; ++i) {
+                s[i] = fma2(gamma, s[i], mul2(x[i], back));
+                smax = max_abs(smax, s[i]);
             }
-            if (more) store_s(b, true);
+        }
+        if (more) {
+            store_s(0, true);
+            store_s(1, true);
         }
         if (lost) {
             smax = NAN;
@@ -651,29 +683,59 @@ __device__ __forceinline__ bool make(const Walk& w, const DeltaParams& p, uint32
 
 template <class S>
 __global__ void __launch_bounds__(kThreads, 1)
-kda_delta_walk(const __grid_constant__ DeltaParams p, const __grid_constant__ CUtensorMap v_map) {
+kda_delta_walk(const __grid_constant__ DeltaParams p, const __grid_constant__ CUtensorMap v_map,
+               const __grid_constant__ LinCuts cuts, bool local) {
+    if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // the item: a long sequence, or a segment of one that is cut
+    Walk w;
+    w.h = blockIdx.x % p.H;
+    int i = blockIdx.x / p.H;
+    bool first = true, last = true;
+    int n, at = 0, plane = 0;
+    w.outputs = w.values = true;
+    if (local) {  // all segments but the last: from zero, and from the identity
+        w.values = (i & 1) == 0;
+        i >>= 1;
+    }
+    int r = 0;  // cut sequence r's segments after its first follow those of the ones before
+    if (i < p.n_seg - p.n_cut) {
+        while (i >= cuts.first[r + 1] - (r + 1)) ++r;
+        int g = i - (cuts.first[r] - r) + (local ? 0 : 1);
+        n = cuts.seq[r];
+        w.t0 = cuts.t0[r] + g * p.seg_len;
+        w.len = min(p.seg_len, cuts.len[r] - g * p.seg_len);
+        at = g * (p.seg_len / C);
+        first = g == 0;
+        last = g + 1 == cuts.first[r + 1] - cuts.first[r];
+        plane = ((cuts.first[r] + g) * p.H + w.h) * 2;
+        w.outputs = first || !local;
+    } else {
+        n = p.long_list[p.n_cut + i - (p.n_seg - p.n_cut)];
+        w.t0 = p.cu[n];
+        w.len = p.cu[n + 1] - w.t0;
+    }
+    w.chunks = (w.len + C - 1) / C;
+    w.step = (int64_t)p.H * kDeltaBlock;
+    w.blocks = p.blocks + (((int64_t)p.seq_off[n] + at) * p.H + w.h) * kDeltaBlock;
+    if (local && first && !w.values) return;  // its state is its sequence's
+    const int slot = p.idx[n];
+    S* const state = slot >= 0 && slot < p.num_slots
+                         ? static_cast<S*>(p.pool) + (size_t)slot * p.stride0 + (size_t)w.h * D * D : nullptr;
+    const bool init = first && state && p.has_init[n] != 0;
+    const float* const begins = first || local ? nullptr : p.planes + (size_t)(plane - 2 * p.H) * D * D;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint32_t* const base = reinterpret_cast<uint32_t*>(smem + kSmMisc + 8);
     if (threadIdx.x == 0) {
         for (int i = 0; i < kNumBars; ++i)
             mbar_init(bar(i), i >= kVEmpty ? kMakers : i >= kOEmpty ? kWriters : i >= kTurned ? kTurners : 1);
         abort_flag() = 0;
+        End& end = *reinterpret_cast<End*>(smem + kSmEnd);
+        end.state = last && !local ? state : nullptr;
+        end.plane = local ? p.planes + (size_t)(plane + !w.values) * D * D : nullptr;
+        end.kept = w.values ? nullptr : p.kept + plane / 2;
         fence_mbar_init();
     }
     if (warp == kIssuer) tmem_alloc(base, kTmCols);
-    Walk w;
-    w.h = blockIdx.x % p.H;
-    const int n = p.long_list[blockIdx.x / p.H];
-    w.t0 = p.cu[n];
-    w.len = p.cu[n + 1] - w.t0;
-    w.chunks = (w.len + C - 1) / C;
-    w.step = (int64_t)p.H * kDeltaBlock;
-    w.blocks = p.blocks + ((int64_t)p.seq_off[n] * p.H + w.h) * kDeltaBlock;
-    w.outputs = w.values = true;
-    const int slot = p.idx[n];
-    S* const state = slot >= 0 && slot < p.num_slots
-                         ? static_cast<S*>(p.pool) + (size_t)slot * p.stride0 + (size_t)w.h * D * D : nullptr;
-    const bool init = state && p.has_init[n] != 0;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -683,9 +745,20 @@ kda_delta_walk(const __grid_constant__ DeltaParams p, const __grid_constant__ CU
         asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
         f2 s[kKeys / 2];
         bool cleared;
-        if (make<S>(w, p, tm, warp, lane, init ? state : nullptr, nullptr, s, cleared) && state) {
+        if (begins) grid_dep_wait();
+        const bool done = make<S>(w, p, tm, warp, lane, init ? state : nullptr, begins, s, cleared);
+        const End end = *reinterpret_cast<const End*>(smem + kSmEnd);
+        const int place = (32 * (warp & 3) + lane) * D + (warp >> 2) * kKeys;
+        if (done && end.plane) {
+#pragma unroll
+            for (int j = 0; j < kKeys / 2; j += 2) {
+                const float2 a = unpack2(s[j]), b = unpack2(s[j + 1]);
+                *reinterpret_cast<float4*>(end.plane + place + 2 * j) = make_float4(a.x, a.y, b.x, b.y);
+            }
+            if (end.kept && threadIdx.x == 0) *end.kept = cleared ? 1.f : 0.f;
+        } else if (done && end.state) {
             constexpr int N = 16 / sizeof(S);
-            S* to = state + (32 * (warp & 3) + lane) * D + (warp >> 2) * kKeys;
+            S* to = static_cast<S*>(end.state) + place;
 #pragma unroll
             for (int i = 0; i < kKeys; i += N) {
                 float f[N];
@@ -709,9 +782,9 @@ kda_delta_walk(const __grid_constant__ DeltaParams p, const __grid_constant__ CU
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 32;");
         if (warp == kIssuer) {
-            Issuer i{w, elect_one()};
-            i.go(tm);
-            i.finish();
+            Issuer issuer{w, elect_one()};
+            issuer.go(tm);
+            issuer.finish();
         } else if (w.values) {
             Turner t{w, &v_map, warp - kIssuer - 1, lane};
             t.go();
@@ -724,6 +797,91 @@ kda_delta_walk(const __grid_constant__ DeltaParams p, const __grid_constant__ CU
             if (abort_flag() && lane == 0) atomicOr(p.status, 1);
             tmem_dealloc(tm, kTmCols);
         }
+    }
+}
+
+// The states that the segments of a cut sequence start from: with a segment's N and Phi,
+// S <- S Phi + N, from its first one's end on. A CTA has 16 value rows of a (sequence, head), a
+// thread eight of them at one key; the transitions come by bulk copies, two at a time.
+// Bound by the chain: about 1 us a segment.
+constexpr int kChainThreads = 256;
+constexpr int kChainRows = 16;
+constexpr int kChainPlane = D * D * 4;
+constexpr int kChainSmem = 2 * kChainPlane + D * kChainRows * 4 + 16;
+__global__ void __launch_bounds__(kChainThreads, 1)
+kda_delta_chain(const __grid_constant__ DeltaParams p, const __grid_constant__ LinCuts cuts) {
+    if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    float* const phi = reinterpret_cast<float*>(smem);
+    float* const st = phi + 2 * D * D;  // [key][row]
+    uint64_t* const full = reinterpret_cast<uint64_t*>(st + D * kChainRows);
+    const int r = blockIdx.x / p.H, h = blockIdx.x % p.H, row0 = blockIdx.y * kChainRows;
+    const int key = threadIdx.x % D, half = threadIdx.x / D;
+    const int first = cuts.first[r], steps = cuts.first[r + 1] - first - 2;
+    auto plane = [&](int g) { return p.planes + ((size_t)(first + g) * p.H + h) * 2 * D * D; };
+    if (threadIdx.x == 0) {
+        mbar_init(full, 1);
+        mbar_init(full + 1, 1);
+        fence_mbar_init();
+    }
+    __syncthreads();
+    grid_dep_wait();
+    auto fetch = [&](int g) {
+        mbar_arrive_expect_tx(full + (g & 1), kChainPlane);
+        bulk_g2s(phi + (g & 1) * D * D, plane(g) + D * D, kChainPlane, full + (g & 1));
+    };
+    if (threadIdx.x == 0) {
+        if (steps >= 1) fetch(1);
+        if (steps >= 2) fetch(2);
+    }
+    const size_t at = (size_t)(row0 + 8 * half) * D + key;
+    f2 s[4];
+    auto keep = [&]() {
+#pragma unroll
+        for (int i = 0; i < 4; i += 2)
+            *reinterpret_cast<ulonglong2*>(st + key * kChainRows + 8 * half + 2 * i) = make_ulonglong2(s[i], s[i + 1]);
+    };
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[i] = pack2(plane(0)[at + 2 * i * D], plane(0)[at + (2 * i + 1) * D]);
+    keep();
+    for (int g = 1; g <= steps; ++g) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[i] = pack2(plane(g)[at + 2 * i * D], plane(g)[at + (2 * i + 1) * D]);
+        const bool cleared = p.kept[(size_t)(first + g) * p.H + h] != 0.f;
+        if (!__syncthreads_and(mbar_wait(full + (g & 1), ((g - 1) >> 1) & 1))) {
+            // report, and let the copies in flight land
+            if (threadIdx.x == 0) {
+                atomicOr(p.status, 1);
+                mbar_wait(full + (g & 1), ((g - 1) >> 1) & 1);
+                if (g < steps) mbar_wait(full + ((g + 1) & 1), (g >> 1) & 1);
+            }
+            return;
+        }
+        if (!cleared) {
+            const float* f = phi + (g & 1) * D * D + key;
+#pragma unroll 8
+            for (int j = 0; j < D; ++j) {
+                const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(st + j * kChainRows + 8 * half);
+                const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(st + j * kChainRows + 8 * half + 4);
+                const f2 t = pack2(f[j * D], f[j * D]);
+                s[0] = fma2(a.x, t, s[0]);
+                s[1] = fma2(a.y, t, s[1]);
+                s[2] = fma2(b.x, t, s[2]);
+                s[3] = fma2(b.y, t, s[3]);
+            }
+        }
+        __syncthreads();  // all are done with st and the transition
+        if (threadIdx.x == 0 && g + 2 <= steps) {
+            fence_proxy_async();
+            fetch(g + 2);
+        }
+        keep();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 y = unpack2(s[i]);
+            plane(g)[at + 2 * i * D] = y.x;
+            plane(g)[at + (2 * i + 1) * D] = y.y;
+        }
+        __syncthreads();
     }
 }
 
@@ -750,40 +908,110 @@ bool make_v_map(CUtensorMap* m, const DeltaParams& p) {
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Launches with programmatic stream serialization: set up while the last CTAs of the kernel
+// before still run.
+template <class... A>
+cudaError_t launch_after(void (*kernel)(A...), dim3 grid, int threads, size_t bytes, cudaStream_t s, const A&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = bytes;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 template <class S>
-cudaError_t launch(const DeltaParams& p, const CUtensorMap& v_map, cudaStream_t s) {
+cudaError_t launch(const DeltaParams& p, const LinCuts& cuts, const CUtensorMap& v_map, cudaStream_t s) {
     static unsigned configured = 0;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev >= 32 || !(configured & (1u << dev))) {
         e = cudaFuncSetAttribute(kda_delta_walk<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(kda_delta_chain, cudaFuncAttributeMaxDynamicSharedMemorySize, kChainSmem);
         if (e != cudaSuccess) return e;
         if (dev < 32) configured |= 1u << dev;
     }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(p.n_long * p.H));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSmemBytes;
-    cfg.stream = s;
-    // set up while the chunks' last CTAs still run
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kda_delta_walk<S>, p, v_map);
+    const int after = p.n_seg - p.n_cut;  // segments that are not their sequence's first
+    if (p.n_cut > 0) {
+        e = launch_after(kda_delta_walk<S>, dim3((unsigned)(2 * after * p.H)), kThreads, kSmemBytes, s, p, v_map, cuts, true);
+        if (e == cudaSuccess)
+            e = launch_after(kda_delta_chain, dim3((unsigned)(p.n_cut * p.H), D / kChainRows), kChainThreads, kChainSmem, s, p, cuts);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_after(kda_delta_walk<S>, dim3((unsigned)((after + p.n_long - p.n_cut) * p.H)), kThreads, kSmemBytes, s, p, v_map,
+                        cuts, false);
+}
+
+// How the longest sequences are cut, from the long sequences' lengths (longest first).  In
+// units of a chunk's time in the walk: uncut it takes as long as its longest sequence, or as
+// all chunks shared out.  Cut into k segments, the first pass walks all but the last one
+// twice (but for the first), the second all but the first; the chain between them takes
+// half a unit a segment, and the two more launches about four.
+struct Cut {
+    int seg = 0, n_cut = 0, n_seg = 0;
+};
+Cut cut_rule(const int32_t* lens, int n, int H, int sms, int64_t planes) {
+    Cut best;
+    if (n <= 0 || (int64_t)n * H > sms) return best;  // a wave of whole sequences fills the GPU
+    auto chunks_of = [](int len) { return (len + C - 1) / C; };
+    const int longest = chunks_of(lens[0]);
+    float least = (float)longest;
+    for (int k = 2; k <= 32; ++k) {
+        const int seg = (longest + k - 1) / k;
+        if (seg < kDeltaMinSeg) break;
+        Cut c;
+        c.seg = seg;
+        int64_t local = 0, rest = 0;
+        int most = 0;
+        for (int i = 0; i < n; ++i) {
+            const int m = (chunks_of(lens[i]) + seg - 1) / seg;
+            if (m < 2) {
+                rest += H;
+                continue;
+            }
+            ++c.n_cut, c.n_seg += m;
+            local += (int64_t)(2 * (m - 1) - 1) * H;
+            rest += (int64_t)(m - 1) * H;
+            most = m > most ? m : most;
+        }
+        if (c.n_cut > kLinCuts || (int64_t)c.n_seg * H > planes) break;
+        const auto waves = [&](int64_t items) { return (float)((items + sms - 1) / sms); };
+        const float time = (waves(local) + waves(rest)) * (float)seg + 0.5f * (float)(most - 2) + 4.f;
+        if (time < least) least = time, best = c;
+    }
+    return best;
 }
 
 }  // namespace
 
-cudaError_t launch_delta_walk(const DeltaParams& p, cudaStream_t s) {
+void delta_cut(DeltaParams& p, LinCuts& cuts, const SeqTables& t) {
+    const Cut c = cut_rule(t.long_lens, p.n_long, p.H, num_sms(), delta_planes(p.T, p.H));
+    p.seg_len = c.seg * C;
+    p.n_cut = c.n_cut;
+    p.n_seg = c.n_seg;
+    cuts.first[0] = 0;
+    for (int r = 0; r < c.n_cut; ++r) {
+        cuts.seq[r] = t.long_seqs[r];
+        cuts.t0[r] = t.bounds[t.long_seqs[r]];
+        cuts.len[r] = t.long_lens[r];
+        cuts.first[r + 1] = cuts.first[r] + (t.long_lens[r] + p.seg_len - 1) / p.seg_len;
+    }
+}
+
+cudaError_t launch_delta_walk(const DeltaParams& p, const LinCuts& cuts, cudaStream_t s) {
     if (p.n_long <= 0) return cudaSuccess;
+    if ((int64_t)p.n_long * p.H > INT32_MAX / 4) return cudaErrorInvalidValue;
     CUtensorMap v_map;
     if (!make_v_map(&v_map, p)) return cudaErrorInvalidValue;
-    if (p.st_dtype == KDA_STATE_F32) return launch<float>(p, v_map, s);
-    if (p.st_dtype == KDA_STATE_BF16) return launch<__nv_bfloat16>(p, v_map, s);
-    return launch<__half>(p, v_map, s);
+    if (p.st_dtype == KDA_STATE_F32) return launch<float>(p, cuts, v_map, s);
+    if (p.st_dtype == KDA_STATE_BF16) return launch<__nv_bfloat16>(p, cuts, v_map, s);
+    return launch<__half>(p, cuts, v_map, s);
 }
 
 }  // namespace kda

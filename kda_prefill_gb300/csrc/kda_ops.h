@@ -106,6 +106,9 @@ struct DeltaParams : LinParams {
     const int32_t *seq_off, *chunk_seq, *chunk_tok;
     int64_t n_chunks;
     uint8_t* blocks;  // [n_chunks][H] of kDeltaBlock bytes
+    // of the cut sequences' segments: `planes` has two of [128 x 128] for each segment and
+    // head, its state from zero (then the one that the next starts from) and its transition,
+    // `kept` whether a token of it clears the state
 };
 // What kda_delta_chunk leaves for the walk of a chunk and head: fp32 scalars, and fp16 tiles in
 // the swizzled layout of kda_device.cuh.
@@ -135,12 +138,23 @@ static_assert(sizeof(DeltaScalars) <= kDeltaK, "room for the scalars");
 inline int64_t delta_chunks(int64_t T, int64_t N) {
     return T / kC + (T / (kShortMax + 1) < N ? T / (kShortMax + 1) : N);
 }
+// Segments times heads that a call's workspace holds: as many as are ever cut, or as there
+// can be.  All segments but a sequence's last have kDeltaMinSeg chunks or more: m > 1
+// segments have at least (m - 1) kDeltaMinSeg chunks' tokens, half as many each.
+constexpr int kDeltaPlanes = 2 * 152;
+constexpr int kDeltaMinSeg = 3;
+inline int64_t delta_planes(int64_t T, int64_t H) {
+    const int64_t n = T / (kDeltaMinSeg * kC / 2) * H;
+    return n < kDeltaPlanes ? n : kDeltaPlanes;
+}
+// Chooses n_cut, n_seg, seg_len and the cuts.
+void delta_cut(DeltaParams& p, LinCuts& cuts, const SeqTables& t);
 // The short sequences token by token (kda_delta_step.cu).
 cudaError_t launch_delta_step(const DeltaParams& p, cudaStream_t s);
 // The long sequences' chunks, each for itself (kda_delta_chunk.cu), and the walk over them
 // (kda_delta_walk.cu).
 cudaError_t launch_delta_chunk(const DeltaParams& p, cudaStream_t s);
-cudaError_t launch_delta_walk(const DeltaParams& p, cudaStream_t s);
+cudaError_t launch_delta_walk(const DeltaParams& p, const LinCuts& cuts, cudaStream_t s);
 
 struct RopeTensor {
     const void* in;

@@ -259,8 +259,10 @@ int enqueue_delta(void* arg, const kda::SeqTables& t) {
     p.chunk_seq = t.chunk_seq;
     p.chunk_tok = t.chunk_tok;
     p.n_chunks = t.n_chunks;
+    kda::LinCuts cuts;
+    kda::delta_cut(p, cuts, t);
     cudaError_t e = kda::launch_delta_chunk(p, c.stream);
-    if (e == cudaSuccess) e = kda::launch_delta_walk(p, c.stream);
+    if (e == cudaSuccess) e = kda::launch_delta_walk(p, cuts, c.stream);
     if (e == cudaSuccess) e = kda::launch_delta_step(p, c.stream);
     return e == cudaSuccess ? KDA_OK : cuda_error(e, "kernel launch");
 }
@@ -377,7 +379,8 @@ int kda_lin_attn_fwd(const void* q, int64_t q_stride_t, int64_t q_stride_h, cons
 
 size_t kda_gated_delta_workspace_size(int64_t total_tokens, int32_t num_seqs, int32_t num_heads) {
     if (total_tokens < 0 || num_seqs <= 0 || num_heads <= 0) return 0;
-    return kda::kWsHeader + (size_t)kda::delta_chunks(total_tokens, num_seqs) * num_heads * kda::kDeltaBlock;
+    return kda::kWsHeader + (size_t)kda::delta_chunks(total_tokens, num_seqs) * num_heads * kda::kDeltaBlock +
+           (size_t)kda::delta_planes(total_tokens, num_heads) * (2 * kda::kD * kda::kD + 64) * sizeof(float);
 }
 
 int kda_gated_delta_fwd(const void* q, int64_t q_stride_t, int64_t q_stride_h, const void* k,
@@ -400,6 +403,9 @@ int kda_gated_delta_fwd(const void* q, int64_t q_stride_t, int64_t q_stride_h, c
     set_params(a, c.p);
     c.p.beta = beta;
     c.p.blocks = static_cast<uint8_t*>(workspace) + kda::kWsHeader;
+    c.p.planes = reinterpret_cast<float*>(
+        c.p.blocks + (size_t)kda::delta_chunks(total_tokens, num_seqs) * num_heads * kda::kDeltaBlock);
+    c.p.kept = c.p.planes + (size_t)kda::delta_planes(total_tokens, num_heads) * 2 * kda::kD * kda::kD;
     return kda::with_seq_tables(cu_seqlens, cu_seqlens_host, num_seqs, total_tokens, c.stream, enqueue_delta, &c);
 }
 
