@@ -9,15 +9,23 @@
 //
 // A CTA takes a chunk and head.  Rows of k and q are scaled by powers of two, so that they
 // are exact in fp16; their lengths are factors on sums.  The scores are products of 16-bit
-// MMAs, exact but for the sums.  T is solved in fp32: the two 32 x 32 blocks on the diagonal
-// column by column, a lane each (the block below them is T22 N21 T11, N = -A).  A power series of N
-// would cancel: with equal keys its terms grow to 10^18.
+// MMAs, exact but for the sums.  T is solved in the four 16 x 16 blocks on the diagonal in fp32,
+// column by column, a lane each, then in blocks twice as large from the two on their diagonal,
+// the one below being T22 N21 T11, N = -A: 16-bit MMAs of operands that are sums of two fp16 (22
+// bits, as T's in the end).  A power series of N would cancel: with equal keys its terms
+// grow to 10^18.
+//
+// The shared-memory port is the bound, then instructions: with the products of T's blocks in
+// fp32 a chunk took 7.6 K cycles of that port.
 //
 // q e^G would leave fp16's range where a chunk's decays are strong, while P T, at most one,
 // does not: rows of both are multiplied by a power of two, up to 2^15, that brings e^G near one.
 //
 // Decays are sums of the decays between two tokens, never differences of sums over the
-// chunk, which lose the bits of weak decays behind strong ones.
+// chunk, which lose the bits of weak decays behind strong ones.  In the 16 x 16 blocks on the
+// diagonal each sum is made; left of them e^{G_i - G_j} is e^{G_i - G_b} e^{G_b - G_j}, b the
+// last token of column j's block: both factors are at most one, the first is one a row and
+// block and the second one a token.
 
 #include "kda_device.cuh"
 #include "kda_ops.h"
@@ -30,25 +38,76 @@ using namespace dev;
 
 constexpr int D = kD;
 constexpr int C = kC;
+constexpr int B = 16;  // tokens of a block
 constexpr int kThreads = 256;
-constexpr int kLd = 68;  // floats of a row of the fp32 matrices
+constexpr int kLdE = 20; // floats of a row of the fp32 blocks on the diagonal
 
 // Shared memory.
-constexpr int kSmK = 0;                          // k, the block's tile
-constexpr int kSmQ = kSmK + C * D * 2;           // q; then T in fp32
-constexpr int kSmN = kSmQ + C * kLd * 4;         // transposed: e^{G_i - G_j}, then N; then T high
-constexpr int kSmP = kSmN + C * kLd * 4;         // P; then P T
-constexpr int kSmVec = kSmP + C * C * 2;         // a, ck, cq, beta, e^G up, up
-constexpr int kSmemBytes = kSmVec + 6 * C * 4;
-static_assert(C * kLd * 4 >= C * D * 2 && C * kLd * 4 >= 2 * C * C * 2 && kSmP % 1024 == 0 && kSmN % 1024 == 0, "room");
+constexpr int kTile = C * C * 2;
+constexpr int kSmK = 0;                   // k, the block's tile
+constexpr int kSmQ = kSmK + C * D * 2;    // q; then T, high and low part
+constexpr int kSmN = kSmQ + C * D * 2;    // N below the diagonal blocks, high and low part; above them Y
+constexpr int kSmP = kSmN + 2 * kTile;    // P; then P T
+constexpr int kSmE = kSmP + kTile;        // blocks on the diagonal, transposed: e^{G_i - G_j}; then N
+constexpr int kSmVec = kSmE + C * kLdE * 4;
+struct Vecs {
+    float a[C];       // decays in log2
+    float ck[C];      // what makes the scaled k's length one (0: not finite)
+    float rk[C];      // that and e^{G_b - G_j}
+    float cq[C];
+    float bk[C];      // beta ck
+    float eg[C];      // e^G up
+    float up[C];
+    float f[3][C];    // e^{G_i - G_b} of the blocks before token i's
+    float total[4];   // decays over a block
+    unsigned clears[2];
+    float strongest[2];
+};
+constexpr int kSmemBytes = kSmVec + (int)sizeof(Vecs);
+static_assert(3 * (kSmemBytes + 1024) <= 233472, "three CTAs on an SM");
+static_assert(2 * kTile <= C * D * 2 && kSmP % 1024 == 0 && kSmN % 1024 == 0 && kSmVec % 16 == 0, "room");
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+__device__ __forceinline__ float zero_if_nan(float x) { return x == x ? x : 0.f; }
+
+// Two fp32 values in one 64-bit register.
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 pack2(float a, float b) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2(f2 a) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+    return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint32_t half2_of(f2 x) {
+    const float2 f = unpack2(x);
+    return pack_half2(f.x, f.y);
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 // The fragments of rows r0 .. r0 + 15, columns c0 .. c0 + 15 of a swizzled tile of halves of
-// R rows: an A operand, or two B operands of eight rows each (r0 .. r0 + 7: b[0], b[2]).
+// R rows: an A operand, or two B operands of eight rows each (r0 .. r0 + 7: a[0], a[2]).
 __device__ __forceinline__ void frag(uint32_t tile, int r0, int c0, int R, int lane, uint32_t (&a)[4]) {
     const int r = r0 + (lane & 15), c = c0 + (lane >> 4) * 8;
     ldsm_x4(tile + sw128_off(r, c, R), a[0], a[1], a[2], a[3]);
@@ -61,49 +120,45 @@ struct RowPart {
     float ssq, scale;  // of the row
     bool fine;         // no infinities or NaN in the row
 };
-__device__ __forceinline__ RowPart scaled_row(const __nv_bfloat16* row, int part, bool live) {
-    rows::Piece<__nv_bfloat16, 8> p[4];
-    float m = 0.f;
-    bool fine = true;
+__device__ __forceinline__ void fetch(uint4 (&v)[4], const __nv_bfloat16* row, int part, bool live) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) p[i].v = live ? __ldg(reinterpret_cast<const uint4*>(row + (4 * i + part) * 8)) : make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < 4; ++i) v[i] = live ? __ldg(reinterpret_cast<const uint4*>(row + (4 * i + part) * 8)) : make_uint4(0, 0, 0, 0);
+}
+__device__ __forceinline__ RowPart scaled_row(const uint4 (&v)[4]) {
     RowPart r;
+    __nv_bfloat162 m2 = __float2bfloat162_rn(0.f);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        float f[8];
-        p[i].get(f);
+        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            m = fmaxf(m, fabsf(f[j]));
-            fine = fine && fabsf(f[j]) < INFINITY;
-        }
+        for (int j = 0; j < 4; ++j) m2 = __hmax2_nan(m2, __habs2(reinterpret_cast<const __nv_bfloat162&>(w[j])));
     }
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    int bad = !fine;
-    bad |= __shfl_xor_sync(0xffffffffu, bad, 1);
-    bad |= __shfl_xor_sync(0xffffffffu, bad, 2);
-    r.fine = bad == 0;
+    float m = max_nan(__low2float(m2), __high2float(m2));
+    m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    r.fine = m < INFINITY;
     // 2^-e with 2^(e-1) <= m < 2^e; values of the smallest exponents stay below 1/2
-    const int e = (int)(__float_as_uint(m) >> 23) - 126;
+    const int e = (int)(__float_as_uint(m) >> 23 & 255) - 126;
     r.scale = __uint_as_float((uint32_t)(127 - max(-126, min(e, 126))) << 23);
-    float s = 0.f;
+    const f2 sc = pack2(r.scale, r.scale);
+    f2 s = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        float f[8];
-        p[i].get(f);
+        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        uint32_t h[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            f[j] *= r.scale;
-            s = fmaf(f[j], f[j], s);
+        for (int j = 0; j < 4; ++j) {
+            const f2 x = mul2(pack2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xFFFF0000u)), sc);
+            s = fma2(x, x, s);
+            h[j] = half2_of(x);
         }
-        rows::Piece<__half, 8> h;
-        h.set(f);
-        r.h[i] = h.v;
+        r.h[i] = make_uint4(h[0], h[1], h[2], h[3]);
     }
-    s += __shfl_xor_sync(0xffffffffu, s, 1);
-    s += __shfl_xor_sync(0xffffffffu, s, 2);
-    r.ssq = s;
+    const float2 t = unpack2(s);
+    float sum = t.x + t.y;
+    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+    r.ssq = sum;
     return r;
 }
 // What a scaled row is multiplied by to have length one.
@@ -111,12 +166,40 @@ __device__ __forceinline__ float unit(const RowPart& r) {
     return 1.f / sqrtf(fmaf(1e-6f * r.scale, r.scale, r.ssq));
 }
 
+// Two values as the sum of two fp16 each.
+__device__ __forceinline__ void put_split(uint8_t* hi_tile, int i, int j, f2 x) {
+    const uint32_t at = sw64_off(i, j), hi = half2_of(x);
+    const float2 f = __half22float2(reinterpret_cast<const __half2&>(hi));
+    *reinterpret_cast<uint32_t*>(hi_tile + at) = hi;
+    *reinterpret_cast<uint32_t*>(hi_tile + kTile + at) = half2_of(fma2(pack2(f.x, f.y), pack2(-1.f, -1.f), x));
+}
+// 16 rows from r0 and 8 columns from n0 of a b, over K from a's column ca and b's row rb on, all
+// of them sums of two fp16; into the tile `to` at row r1, column n1.
+template <int K>
+__device__ __forceinline__ void block_product(uint8_t* a, int r0, int ca, uint8_t* b, int rb, int n0, uint8_t* to, int r1, int n1,
+                                              int lane) {
+    float d[4] = {};
+    const uint32_t at = smem_u32(a), bt = smem_u32(b);
+#pragma unroll
+    for (int ks = 0; ks < K; ks += 16) {
+        uint32_t hi[4], lo[4], x[4];  // x: b's high part, then its low one
+        frag(at, r0, ca + ks, C, lane, hi);
+        frag(at + kTile, r0, ca + ks, C, lane, lo);
+        ldsm_x4_t(bt + (lane >> 4) * kTile + sw64_off(rb + ks + (lane & 15), n0), x[0], x[1], x[2], x[3]);
+        mma_f16(d, lo, x[0], x[1]);
+        mma_f16(d, hi, x[2], x[3]);
+        mma_f16(d, hi, x[0], x[1]);
+    }
+    const int r = r1 + (lane >> 2), c = n1 + (lane & 3) * 2;
+    put_split(to, r, c, pack2(d[0], d[1]));
+    put_split(to, r + 8, c, pack2(d[2], d[3]));
+}
+
 __global__ void __launch_bounds__(kThreads, 3) kda_delta_chunk(const __grid_constant__ DeltaParams p) {
     extern __shared__ __align__(1024) uint8_t smem[];
-    float* const q32 = reinterpret_cast<float*>(smem + kSmQ);  // T
-    float* const n32 = reinterpret_cast<float*>(smem + kSmN);
-    float* const va = reinterpret_cast<float*>(smem + kSmVec);
-    float *const vck = va + C, *const vcq = vck + C, *const vb = vcq + C, *const veg = vb + C, *const vup = veg + C;
+    float* const e32 = reinterpret_cast<float*>(smem + kSmE);
+    uint8_t *const tt = smem + kSmQ, *const nt = smem + kSmN;
+    Vecs& vec = *reinterpret_cast<Vecs*>(smem + kSmVec);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t chunk = blockIdx.x / p.H;
     const int h = blockIdx.x % p.H;
@@ -126,166 +209,229 @@ __global__ void __launch_bounds__(kThreads, 3) kda_delta_chunk(const __grid_cons
     const int len = min(C, p.cu[n + 1] - t0);
     uint8_t* const blk = p.blocks + (chunk * p.H + h) * (int64_t)kDeltaBlock;
     DeltaScalars* const scal = reinterpret_cast<DeltaScalars*>(blk);
+    const int r = tid >> 2, part = tid & 3;  // of a row
 
-    // k and q
+    RowPart q;
+    float g = 0.f, beta = 0.f;
     {
-        const int r = tid >> 2, part = tid & 3;
-        const bool live = r < len;
         const int64_t t = t0 + r;
-        const RowPart k = scaled_row(p.k + t * p.k_st + (int64_t)(h / p.rep) * p.k_sh, part, live);
-        const RowPart q = scaled_row(p.q + t * p.q_st + (int64_t)(h / p.rep) * p.q_sh, part, live);
+        uint4 kv[4], qv[4];
+        // (rows past the sequence's end are another's: cleared once its end is there)
+        fetch(kv, p.k + t * p.k_st + (int64_t)(h / p.rep) * p.k_sh, part, t < p.T);
+        fetch(qv, p.q + t * p.q_st + (int64_t)(h / p.rep) * p.q_sh, part, t < p.T);
+        if (r >= len) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) kv[i] = qv[i] = make_uint4(0, 0, 0, 0);
+        }
+        if (tid < len) {
+            g = p.g[(int64_t)(t0 + tid) * p.g_st + h];
+            beta = p.beta[(int64_t)(t0 + tid) * p.H + h];
+        }
+        RowPart k = scaled_row(kv);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const uint32_t at = sw128_off(r, (4 * i + part) * 8, C);
             // (a row with infinities or NaN counts as zero, but for its own factor c)
-            const uint4 kv = k.fine ? k.h[i] : make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4*>(smem + kSmK + at) = kv;
-            *reinterpret_cast<uint4*>(blk + kDeltaK + at) = kv;
-            *reinterpret_cast<uint4*>(smem + kSmQ + at) = q.h[i];
+            const uint4 x = k.fine ? k.h[i] : make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(smem + kSmK + at) = x;
         }
-        if (part == 0) {
-            vck[r] = k.fine ? unit(k) : NAN;
-            vcq[r] = unit(q);
-        }
+        if (part == 0) vec.ck[r] = k.fine ? unit(k) : NAN;
+        q = scaled_row(qv);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(smem + kSmQ + sw128_off(r, (4 * i + part) * 8, C)) = q.h[i];
+        if (part == 0) vec.cq[r] = unit(q);
     }
+    // sums of decays within the block, up to the token and behind it
+    float pre = 0.f, suf = 0.f;
     if (tid < C) {
-        const bool live = tid < len;
-        const int64_t t = t0 + tid;
-        va[tid] = live ? p.g[t * p.g_st + h] : 0.f;
-        vb[tid] = live ? p.beta[t * p.H + h] : 0.f;
+        const int at = lane & 15;
+        pre = g, suf = g;
+#pragma unroll
+        for (int d = 1; d < B; d <<= 1) {
+            const float x = __shfl_up_sync(0xffffffffu, pre, d), y = __shfl_down_sync(0xffffffffu, suf, d);
+            if (at >= d) pre += x;
+            if (at + d < B) suf += y;
+        }
+        suf = __shfl_down_sync(0xffffffffu, suf, 1);
+        if (at == B - 1) {
+            suf = 0.f;
+            vec.total[tid / B] = pre;
+        }
+        vec.a[tid] = zero_if_nan(g) * 1.4426950408889634f;
+        const unsigned mask = __ballot_sync(0xffffffffu, g < kMinDecay);
+        float most = beta;
+#pragma unroll
+        for (int x = 16; x >= 1; x >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, x));
+        if (lane == 0) vec.clears[warp] = mask, vec.strongest[warp] = most;
     }
+    fence_proxy_async();
     __syncthreads();
-    // scalars: G from the chunk's start and to its end
-    if (tid < C) {
-        const float b = vb[tid], ck = vck[tid];
-        float g = 0.f, rest = 0.f;
-#pragma unroll 8
-        for (int m = 0; m < C; ++m) {
-            const float a = va[m];
-            g += m <= tid ? a : 0.f;
-            rest += m > tid ? a : 0.f;
+    if (tid == 0) {
+        bulk_s2g(blk + kDeltaK, smem + kSmK, C * D * 2);
+        bulk_commit();
+    }
+    // e^{G_i - G_j} on the diagonal: row j, column i - its block's first
+    {
+        const int j = r, o = j & ~(B - 1), i0 = 4 * part;
+        float sum = 0.f;
+        for (int m = 0; m < i0; m += 4) {
+            const float4 a = *reinterpret_cast<const float4*>(vec.a + o + m);
+            sum += o + m > j ? a.x : 0.f;
+            sum += o + m + 1 > j ? a.y : 0.f;
+            sum += o + m + 2 > j ? a.z : 0.f;
+            sum += o + m + 3 > j ? a.w : 0.f;
         }
-        const float eg = g > -0.5f ? 1.f + expm1f(g) : expf(g);
-        const bool clears = va[tid] < kMinDecay;
-        const unsigned mask = __ballot_sync(0xffffffffu, clears);
-        scal->c[tid] = eg * ck;
-        scal->beta[tid] = b;
-        scal->w[tid] = 0.5f * expf(rest) * (ck == ck ? ck : 0.f);
+        const float4 a = *reinterpret_cast<const float4*>(vec.a + o + i0);
+        const float aa[4] = {a.x, a.y, a.z, a.w};
+        float x[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int i = o + i0 + u;
+            sum += i > j ? aa[u] : 0.f;
+            x[u] = i >= j ? ex2(sum) : 0.f;
+        }
+        *reinterpret_cast<float4*>(e32 + j * kLdE + i0) = make_float4(x[0], x[1], x[2], x[3]);
+    }
+    if (tid < C) {
+        constexpr float kLog2e = 1.4426950408889634f;
+        const int blk_i = tid / B;
+        const float ck = vec.ck[tid], fine = zero_if_nan(ck);
+        // decays from each block's end up to the token, from the chunk's start, to its end
+        float upto = pre, rest = suf;
+#pragma unroll
+        for (int b = 2; b >= 0; --b) {
+            if (b < blk_i) {
+                vec.f[b][tid] = zero_if_nan(ex2(upto * kLog2e));
+                upto += vec.total[b];
+            }
+        }
+#pragma unroll
+        for (int b = 1; b < 4; ++b)
+            if (b > blk_i) rest += vec.total[b];
+        const float eg = upto > -0.5f ? 1.f + expm1f(upto) : expf(upto);
         // up: 2^-e with 2^e <= e^G < 2^(e+1), at most 2^15
         const int e = min(15, max(0, 127 - (int)(__float_as_uint(eg) >> 23)));
         const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+        scal->c[tid] = eg * ck;
+        scal->beta[tid] = beta;
+        scal->w[tid] = 0.5f * expf(rest) * fine;
         scal->down[tid] = __uint_as_float((uint32_t)(127 - e) << 23);
-        veg[tid] = eg * up;
-        vup[tid] = up;
-        if (tid == C - 1) scal->gamma = eg;
-        float most = b;
-#pragma unroll
-        for (int x = 16; x >= 1; x >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, x));
-        if (lane == 0) {
-            scal->clears[warp] = mask;
-            reinterpret_cast<volatile unsigned*>(smem + kSmP)[warp] = mask;
-            reinterpret_cast<volatile float*>(smem + kSmP)[2 + warp] = most;
-        }
-    }
-    // e^{G_i - G_j}, transposed: row j, column i
-    {
-        constexpr float kLog2e = 1.4426950408889634f;
-        const int j = tid & (C - 1), i0 = (tid >> 6) * 16;
-        float sum = 0.f;
-        for (int m = 0; m < i0; ++m) {
-            const float a = va[m];
-            sum += m > j && a == a ? a : 0.f;
-        }
-#pragma unroll
-        for (int i = 0; i < 16; i += 4) {
-            float x[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int ii = i0 + i + u;
-                const float a = va[ii];
-                sum += ii > j && a == a ? a : 0.f;
-                x[u] = ii >= j ? ex2(sum * kLog2e) : 0.f;
-            }
-            *reinterpret_cast<float4*>(n32 + j * kLd + i0 + i) = make_float4(x[0], x[1], x[2], x[3]);
+        vec.rk[tid] = zero_if_nan(ex2(suf * kLog2e)) * fine;
+        vec.bk[tid] = -zero_if_nan(beta * ck);
+        vec.eg[tid] = eg * up;
+        vec.up[tid] = up;
+        if (tid == C - 1) {
+            scal->gamma = eg;
+            const unsigned lo = vec.clears[0], hi = vec.clears[1];
+            scal->first_clear = lo ? __ffs(lo) - 1 : hi ? 31 + __ffs(hi) : C;
+            scal->clears[0] = lo, scal->clears[1] = hi;
+            scal->strongest = fmaxf(vec.strongest[0], vec.strongest[1]);
         }
     }
     __syncthreads();
-    if (tid == 0) {
-        const unsigned lo = reinterpret_cast<volatile unsigned*>(smem + kSmP)[0];
-        const unsigned hi = reinterpret_cast<volatile unsigned*>(smem + kSmP)[1];
-        scal->strongest = fmaxf(reinterpret_cast<volatile float*>(smem + kSmP)[2], reinterpret_cast<volatile float*>(smem + kSmP)[3]);
-        scal->first_clear = lo ? __ffs(lo) - 1 : hi ? 31 + __ffs(hi) : C;
-    }
     // q^ e^G
     {
-        const int r = tid >> 2, part = tid & 3;
-        const float f = vcq[r] * veg[r];
+        const float f = vec.cq[r] * vec.eg[r];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const uint32_t at = sw128_off(r, (4 * i + part) * 8, C);
-            rows::Piece<__half, 8> x;
-            x.v = *reinterpret_cast<const uint4*>(smem + kSmQ + at);
-            float y[8];
-            x.get(y);
+            const uint32_t w[4] = {q.h[i].x, q.h[i].y, q.h[i].z, q.h[i].w};
+            uint32_t y[4];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] *= f;
-            x.set(y);
-            *reinterpret_cast<uint4*>(blk + kDeltaQ + at) = x.v;
+            for (int j = 0; j < 4; ++j) {
+                const float2 x = __half22float2(reinterpret_cast<const __half2&>(w[j]));
+                y[j] = half2_of(mul2(pack2(x.x, x.y), pack2(f, f)));
+            }
+            *reinterpret_cast<uint4*>(blk + kDeltaQ + sw128_off(r, (4 * i + part) * 8, C)) = make_uint4(y[0], y[1], y[2], y[3]);
         }
     }
     // scores: 16 rows x 32 columns a warp
-    const int r0 = (warp & 3) * 16, c0 = (warp >> 2) * 32;
-    const bool below = c0 < r0 + 16;  // some column is not above the diagonal
+    const int bi = warp & 3, r0 = bi * B, c0 = (warp >> 2) * 32;
+    const bool below = c0 < r0 + B;  // some column is not above the diagonal
     {
         float kk[4][4] = {}, qk[4][4] = {};
         if (below) {
             const uint32_t kt = smem_u32(smem + kSmK), qt = smem_u32(smem + kSmQ);
 #pragma unroll
             for (int ks = 0; ks < D; ks += 16) {
-                uint32_t a[4], q[4], b[2][4];
+                uint32_t a[4], qa[4], b[4];
                 frag(kt, r0, ks, C, lane, a);
-                frag(qt, r0, ks, C, lane, q);
-                frag(kt, c0, ks, C, lane, b[0]);
-                frag(kt, c0 + 16, ks, C, lane, b[1]);
+                frag(qt, r0, ks, C, lane, qa);
 #pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    mma_f16(kk[t], a, b[t >> 1][t & 1], b[t >> 1][2 + (t & 1)]);
-                    mma_f16(qk[t], q, b[t >> 1][t & 1], b[t >> 1][2 + (t & 1)]);
+                for (int t = 0; t < 4; t += 2) {
+                    if (c0 + 8 * t > r0) continue;
+                    frag(kt, c0 + 8 * t, ks, C, lane, b);
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        mma_f16(kk[t + u], a, b[u], b[2 + u]);
+                        mma_f16(qk[t + u], qa, b[u], b[2 + u]);
+                    }
                 }
             }
         }
-        __syncthreads();  // these words are read
+        // e^{G_i - G_j} of the block on the diagonal, before N takes its place
+        const int ri = lane >> 2, cj = (lane & 3) * 2;
+        float e[2][2][2] = {};  // [columns][rows][column]
+        if (below && r0 - c0 < 32) {
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+            for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const int i = r0 + half * 8 + (lane >> 2), j = c0 + t * 8 + (lane & 3) * 2;
-                float pv[2];
-                const float b = vb[i], ci = vck[i], cq = vcq[i];
-                const float bi = b == b && ci == ci ? b * ci : 0.f;
+                for (int half = 0; half < 2; ++half)
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const float cj = vck[j + u];
-                    const float l = n32[(j + u) * kLd + i] * (cj == cj ? cj : 0.f);
-                    n32[(j + u) * kLd + i] = j + u < i ? -bi * l * kk[t][2 * half + u] : 0.f;
-                    pv[u] = j + u <= i ? cq * l * qk[t][2 * half + u] : 0.f;
+                    for (int u = 0; u < 2; ++u) e[t][half][u] = e32[(r0 + 8 * t + cj + u) * kLdE + 8 * half + ri];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int i = r0 + half * 8 + ri;
+            const float b = vec.bk[i], cq = vec.cq[i];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const int j = c0 + t * 8 + cj, bj = (c0 + t * 8) / B;
+                float nv[2] = {}, pv[2] = {};
+                if (bj < bi) {
+                    const float f = vec.f[bj][i];
+                    const float2 rk = *reinterpret_cast<const float2*>(vec.rk + j);
+                    const float l[2] = {f * rk.x, f * rk.y};
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) nv[u] = b * l[u] * kk[t][2 * half + u], pv[u] = cq * l[u] * qk[t][2 * half + u];
+                } else if (bj == bi) {
+                    const float2 ck = *reinterpret_cast<const float2*>(vec.ck + j);
+                    const float l[2] = {e[t & 1][half][0] * zero_if_nan(ck.x), e[t & 1][half][1] * zero_if_nan(ck.y)};
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        nv[u] = j + u < i ? b * l[u] * kk[t][2 * half + u] : 0.f;
+                        pv[u] = j + u <= i ? cq * l[u] * qk[t][2 * half + u] : 0.f;
+                    }
+                }
+                if (bj < bi) put_split(nt, i, j, pack2(nv[0], nv[1]));
+                if (bj == bi) {
+                    e32[j * kLdE + i - r0] = nv[0];
+                    e32[(j + 1) * kLdE + i - r0] = nv[1];
                 }
                 *reinterpret_cast<uint32_t*>(smem + kSmP + sw64_off(i, j)) = pack_half2(pv[0], pv[1]);
             }
+        }
+        // T is zero right of its diagonal blocks
+#pragma unroll
+        for (int x = tid; x < 2 * C * (C / 8); x += kThreads) {
+            const int row = x >> 3 & (C - 1), c = (x & 7) * 8;
+            if (c >= (row & ~(B - 1)) + B)
+                *reinterpret_cast<uint4*>(tt + (x >> 9) * kTile + sw64_off(row, c)) = make_uint4(0, 0, 0, 0);
+        }
     }
     __syncthreads();
-    // the diagonal blocks of T: lane j has column j; once row m is known its multiples go to
-    // the rows below
-    if (warp < 2) {
-        const int o = warp * 32;
-        float t[32];
+    // the diagonal blocks of T: a lane has a column; once row m is known its multiples go to
+    // the rows below.  Half a warp keeps the high parts, the other the low ones.
+    if (warp < 4) {
+        const int o = warp * B, col = lane & 15;
+        float t[B];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) t[i] = i == lane ? 1.f : 0.f;
+        for (int i = 0; i < B; ++i) t[i] = i == col ? 1.f : 0.f;
 #pragma unroll
-        for (int m = 0; m < 31; ++m) {
+        for (int m = 0; m < B - 1; ++m) {
 #pragma unroll
-            for (int i = (m + 1) & ~3; i < 32; i += 4) {
-                const float4 x = *reinterpret_cast<const float4*>(n32 + (o + m) * kLd + o + i);
+            for (int i = (m + 1) & ~3; i < B; i += 4) {
+                const float4 x = *reinterpret_cast<const float4*>(e32 + (o + m) * kLdE + i);
                 if (i > m) t[i] = fmaf(x.x, t[m], t[i]);
                 if (i + 1 > m) t[i + 1] = fmaf(x.y, t[m], t[i + 1]);
                 if (i + 2 > m) t[i + 2] = fmaf(x.z, t[m], t[i + 2]);
@@ -293,72 +439,39 @@ __global__ void __launch_bounds__(kThreads, 3) kda_delta_chunk(const __grid_cons
             }
         }
 #pragma unroll
-        for (int i = 0; i < 32; ++i) q32[(o + i) * kLd + o + lane] = t[i];
-    } else if (warp < 4) {  // above the diagonal
-        for (int i = warp - 2; i < 32; i += 2) q32[i * kLd + 32 + lane] = 0.f;
+        for (int i = 0; i < B; ++i) {
+            const __half hi = __float2half_rn(t[i]);
+            *reinterpret_cast<__half*>(tt + (lane >> 4) * kTile + sw64_off(o + i, o + col)) =
+                lane < B ? hi : __float2half_rn(t[i] - __half2float(hi));
+        }
     }
     __syncthreads();
-    // Y = N21 T11, four rows a warp, into N's place above the diagonal (row 32 + j, column r)
-    float* const y32 = n32 + 32 * kLd;
+    // blocks of 32: Y = N21 T11, then T21 = T22 Y
     {
-        float y[4] = {};
-#pragma unroll 8
-        for (int m = 0; m < 32; ++m) {
-            const float4 x = *reinterpret_cast<const float4*>(n32 + m * kLd + 32 + 4 * warp);
-            const float t = q32[m * kLd + lane];
-            y[0] = fmaf(x.x, t, y[0]), y[1] = fmaf(x.y, t, y[1]);
-            y[2] = fmaf(x.z, t, y[2]), y[3] = fmaf(x.w, t, y[3]);
-        }
-#pragma unroll
-        for (int u = 0; u < 4; ++u) y32[(4 * warp + u) * kLd + lane] = y[u];
+        const int o = (warp >> 1 & 1) * 32, n = (warp & 1) * 8;
+        if (warp < 4) block_product<B>(nt, o + B, o, tt, o, o + n, nt, o, o + B + n, lane);
+        __syncthreads();
+        if (warp < 4) block_product<B>(tt, o + B, o + B, nt, o, o + B + n, tt, o + B, o + n, lane);
     }
     __syncthreads();
-    {  // T21 = T22 Y
-        float y[4] = {};
-#pragma unroll
-        for (int m = 0; m < 32; m += 4) {
-            float4 x[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) x[u] = *reinterpret_cast<const float4*>(q32 + (32 + 4 * warp + u) * kLd + 32 + m);
-#pragma unroll
-            for (int v = 0; v < 4; ++v) {
-                const float t = y32[(m + v) * kLd + lane];
-#pragma unroll
-                for (int u = 0; u < 4; ++u) y[u] = fmaf(v == 0 ? x[u].x : v == 1 ? x[u].y : v == 2 ? x[u].z : x[u].w, t, y[u]);
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < 4; ++u) q32[(32 + 4 * warp + u) * kLd + lane] = y[u];
-    }
-    __syncthreads();
-    // T as the sum of two fp16
+    // and of 64
     {
-        const int r = tid >> 2, part = tid & 3;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int c = (4 * i + part) * 8;
-            float f[8], lo[8];
-            const float4 a = *reinterpret_cast<const float4*>(q32 + r * kLd + c);
-            const float4 b = *reinterpret_cast<const float4*>(q32 + r * kLd + c + 4);
-            f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-            rows::Piece<__half, 8> hi, rest;
-            hi.set(f);
-            hi.get(lo);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) lo[j] = f[j] - lo[j];
-            rest.set(lo);
-            const uint32_t at = sw64_off(r, c);
-            *reinterpret_cast<uint4*>(smem + kSmN + at) = hi.v;
-            *reinterpret_cast<uint4*>(blk + kDeltaT + at) = hi.v;
-            *reinterpret_cast<uint4*>(blk + kDeltaT + C * C * 2 + at) = rest.v;
-        }
+        const int o = (warp >> 2) * B, n = (warp & 3) * 8;
+        block_product<32>(nt, 32 + o, 0, tt, 0, n, nt, o, 32 + n, lane);
+        __syncthreads();
+        block_product<32>(tt, 32 + o, 32, nt, 0, 32 + n, tt, 32 + o, n, lane);
     }
+    fence_proxy_async();
     __syncthreads();
+    if (tid == 0) {
+        bulk_s2g(blk + kDeltaT, tt, 2 * kTile);
+        bulk_commit();
+    }
     // P T
     {
         float d[4][4] = {};
         if (below) {
-            const uint32_t pt = smem_u32(smem + kSmP), tt = smem_u32(smem + kSmN);
+            const uint32_t pt = smem_u32(smem + kSmP), th = smem_u32(tt);
 #pragma unroll
             for (int ks = 0; ks < C; ks += 16) {
                 if (ks < r0 + 16 && ks + 16 > c0) {
@@ -367,8 +480,8 @@ __global__ void __launch_bounds__(kThreads, 3) kda_delta_chunk(const __grid_cons
 #pragma unroll
                     for (int t = 0; t < 4; t += 2) {
                         // rows ks .. ks + 15 of T, columns c0 + 8 t .. + 15, transposed
-                        const int r = ks + (lane & 15), c = c0 + 8 * t + (lane >> 4) * 8;
-                        ldsm_x4_t(tt + sw64_off(r, c), b[0], b[1], b[2], b[3]);
+                        const int tr = ks + (lane & 15), tc = c0 + 8 * t + (lane >> 4) * 8;
+                        ldsm_x4_t(th + sw64_off(tr, tc), b[0], b[1], b[2], b[3]);
                         mma_f16(d[t], a, b[0], b[1]);
                         mma_f16(d[t + 1], a, b[2], b[3]);
                     }
@@ -377,17 +490,23 @@ __global__ void __launch_bounds__(kThreads, 3) kda_delta_chunk(const __grid_cons
         }
         __syncthreads();
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+        for (int half = 0; half < 2; ++half) {
+            const int i = r0 + half * 8 + (lane >> 2);
+            const float up = vec.up[i];
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const int i = r0 + half * 8 + (lane >> 2), j = c0 + t * 8 + (lane & 3) * 2;
-                *reinterpret_cast<uint32_t*>(smem + kSmP + sw64_off(i, j)) = pack_half2(vup[i] * d[t][2 * half], vup[i] * d[t][2 * half + 1]);
+            for (int t = 0; t < 4; ++t) {
+                const int j = c0 + t * 8 + (lane & 3) * 2;
+                *reinterpret_cast<uint32_t*>(smem + kSmP + sw64_off(i, j)) = pack_half2(up * d[t][2 * half], up * d[t][2 * half + 1]);
             }
+        }
     }
+    fence_proxy_async();
     __syncthreads();
-#pragma unroll
-    for (int i = tid; i < C * C * 2 / 16; i += kThreads)
-        reinterpret_cast<uint4*>(blk + kDeltaPT)[i] = reinterpret_cast<const uint4*>(smem + kSmP)[i];
+    if (tid == 0) {
+        bulk_s2g(blk + kDeltaPT, smem + kSmP, kTile);
+        bulk_commit();
+        bulk_wait_all();
+    }
 }
 
 }  // namespace

@@ -580,8 +580,8 @@ __device__ __forceinline__ bool make(const Walk& w, const DeltaParams& p, uint32
         tc_fence_after();
         {
             f2 x[8];
-            load16(tm + kTmX + kToks * part, x);
             if (c > 0) was = of_row(c);
+            load16(tm + kTmX + kToks * part, x);
             const bool dead = !finite(was);
             const int mine = clear - kToks * part;  // among this thread's tokens
             if (mine < kToks) {
