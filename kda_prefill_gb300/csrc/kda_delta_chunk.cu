@@ -7,9 +7,9 @@
 // so that for an incoming state S, with R = beta (V - e^G K^ S^T), the chunk's writes are
 // U = T R and its outputs e^G Q^ S^T + (P T) R.
 //
-// A CTA takes a chunk and head.  Rows of k and q are scaled by powers of two, so that they
-// are exact in fp16; their lengths are factors on sums.  The scores are products of 16-bit
-// MMAs, exact but for the sums.  T is solved in the four 16 x 16 blocks on the diagonal in fp32,
+// A CTA takes a chunk and head.  The scores are products of k and q as they come, exact but
+// for the sums; their lengths are factors on them.  For the walk rows of k are scaled by powers
+// of two, so that they are exact in fp16.  T is solved in the four 16 x 16 blocks on the diagonal in fp32,
 // column by column, a lane each, then in blocks twice as large from the two on their diagonal,
 // the one below being T22 N21 T11, N = -A: 16-bit MMAs of operands that are sums of two fp16 (22
 // bits, as T's in the end).  A power series of N would cancel: with equal keys its terms
@@ -44,15 +44,15 @@ constexpr int kLdE = 20; // floats of a row of the fp32 blocks on the diagonal
 
 // Shared memory.
 constexpr int kTile = C * C * 2;
-constexpr int kSmK = 0;                   // k, the block's tile
+constexpr int kSmK = 0;                   // k; then N below the diagonal blocks, high and low part; above them Y
 constexpr int kSmQ = kSmK + C * D * 2;    // q; then T, high and low part
-constexpr int kSmN = kSmQ + C * D * 2;    // N below the diagonal blocks, high and low part; above them Y
-constexpr int kSmP = kSmN + 2 * kTile;    // P; then P T
+constexpr int kSmP = kSmQ + C * D * 2;    // P; then P T
 constexpr int kSmE = kSmP + kTile;        // blocks on the diagonal, transposed: e^{G_i - G_j}; then N
 constexpr int kSmVec = kSmE + C * kLdE * 4;
 struct Vecs {
     float a[C];       // decays in log2
-    float ck[C];      // what makes the scaled k's length one (0: not finite)
+    float ck[C];      // what makes k's length one (0 if k is not finite)
+    float ks[C];      // the same for the scaled k (NaN)
     float rk[C];      // that and e^{G_b - G_j}
     float cq[C];
     float bk[C];      // beta ck
@@ -64,8 +64,8 @@ struct Vecs {
     float strongest[2];
 };
 constexpr int kSmemBytes = kSmVec + (int)sizeof(Vecs);
-static_assert(3 * (kSmemBytes + 1024) <= 233472, "three CTAs on an SM");
-static_assert(2 * kTile <= C * D * 2 && kSmP % 1024 == 0 && kSmN % 1024 == 0 && kSmVec % 16 == 0, "room");
+static_assert(4 * (kSmemBytes + 1024) <= 233472, "four CTAs on an SM");
+static_assert(2 * kTile <= C * D * 2 && kSmP % 1024 == 0 && kSmVec % 16 == 0, "room");
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -100,10 +100,13 @@ __device__ __forceinline__ uint32_t half2_of(f2 x) {
     const float2 f = unpack2(x);
     return pack_half2(f.x, f.y);
 }
-__device__ __forceinline__ float max_nan(float a, float b) {
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
+// D += A (16x16, row) * B (16x8, col), bf16 inputs, fp32 accumulation.
+__device__ __forceinline__ void mma_bf16(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
 // The fragments of rows r0 .. r0 + 15, columns c0 .. c0 + 15 of a swizzled tile of halves of
@@ -113,57 +116,31 @@ __device__ __forceinline__ void frag(uint32_t tile, int r0, int c0, int R, int l
     ldsm_x4(tile + sw128_off(r, c, R), a[0], a[1], a[2], a[3]);
 }
 
-// One row's 32 values of this thread: scaled by a power of two so that the row's largest is
-// in [1/2, 1), as fp16; the sum of their squares over the row.  Four threads have a row.
-struct RowPart {
-    uint4 h[4];
-    float ssq, scale;  // of the row
-    bool fine;         // no infinities or NaN in the row
-};
+// Four threads have a row, 32 values each: four pieces of eight.
 __device__ __forceinline__ void fetch(uint4 (&v)[4], const __nv_bfloat16* row, int part, bool live) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = live ? __ldg(reinterpret_cast<const uint4*>(row + (4 * i + part) * 8)) : make_uint4(0, 0, 0, 0);
 }
-__device__ __forceinline__ RowPart scaled_row(const uint4 (&v)[4]) {
-    RowPart r;
-    __nv_bfloat162 m2 = __float2bfloat162_rn(0.f);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) m2 = __hmax2_nan(m2, __habs2(reinterpret_cast<const __nv_bfloat162&>(w[j])));
-    }
-    float m = max_nan(__low2float(m2), __high2float(m2));
-    m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    r.fine = m < INFINITY;
-    // 2^-e with 2^(e-1) <= m < 2^e; values of the smallest exponents stay below 1/2
-    const int e = (int)(__float_as_uint(m) >> 23 & 255) - 126;
-    r.scale = __uint_as_float((uint32_t)(127 - max(-126, min(e, 126))) << 23);
-    const f2 sc = pack2(r.scale, r.scale);
+__device__ __forceinline__ f2 pair(uint32_t w) { return pack2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)); }
+// The row's sum of squares.
+__device__ __forceinline__ float squares(const uint4 (&v)[4]) {
     f2 s = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-        uint32_t h[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const f2 x = mul2(pack2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xFFFF0000u)), sc);
-            s = fma2(x, x, s);
-            h[j] = half2_of(x);
-        }
-        r.h[i] = make_uint4(h[0], h[1], h[2], h[3]);
+        for (int j = 0; j < 4; ++j) s = fma2(pair(w[j]), pair(w[j]), s);
     }
     const float2 t = unpack2(s);
     float sum = t.x + t.y;
     sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-    r.ssq = sum;
-    return r;
+    return sum + __shfl_xor_sync(0xffffffffu, sum, 2);
 }
-// What a scaled row is multiplied by to have length one.
-__device__ __forceinline__ float unit(const RowPart& r) {
-    return 1.f / sqrtf(fmaf(1e-6f * r.scale, r.scale, r.ssq));
+// Eight values times f, as fp16.
+__device__ __forceinline__ uint4 times(uint4 v, float f) {
+    const f2 ff = pack2(f, f);
+    return make_uint4(half2_of(mul2(pair(v.x), ff)), half2_of(mul2(pair(v.y), ff)), half2_of(mul2(pair(v.z), ff)),
+                      half2_of(mul2(pair(v.w), ff)));
 }
 
 // Two values as the sum of two fp16 each.
@@ -195,10 +172,10 @@ __device__ __forceinline__ void block_product(uint8_t* a, int r0, int ca, uint8_
     put_split(to, r + 8, c, pack2(d[2], d[3]));
 }
 
-__global__ void __launch_bounds__(kThreads, 3) kda_delta_chunk(const __grid_constant__ DeltaParams p) {
+__global__ void __launch_bounds__(kThreads, 4) kda_delta_chunk(const __grid_constant__ DeltaParams p) {
     extern __shared__ __align__(1024) uint8_t smem[];
     float* const e32 = reinterpret_cast<float*>(smem + kSmE);
-    uint8_t *const tt = smem + kSmQ, *const nt = smem + kSmN;
+    uint8_t *const tt = smem + kSmQ, *const nt = smem + kSmK;
     Vecs& vec = *reinterpret_cast<Vecs*>(smem + kSmVec);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t chunk = blockIdx.x / p.H;
@@ -211,35 +188,41 @@ __global__ void __launch_bounds__(kThreads, 3) kda_delta_chunk(const __grid_cons
     DeltaScalars* const scal = reinterpret_cast<DeltaScalars*>(blk);
     const int r = tid >> 2, part = tid & 3;  // of a row
 
-    RowPart q;
+    uint4 q[4];
     float g = 0.f, beta = 0.f;
     {
         const int64_t t = t0 + r;
-        uint4 kv[4], qv[4];
+        uint4 k[4];
         // (rows past the sequence's end are another's: cleared once its end is there)
-        fetch(kv, p.k + t * p.k_st + (int64_t)(h / p.rep) * p.k_sh, part, t < p.T);
-        fetch(qv, p.q + t * p.q_st + (int64_t)(h / p.rep) * p.q_sh, part, t < p.T);
-        if (r >= len) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) kv[i] = qv[i] = make_uint4(0, 0, 0, 0);
-        }
+        fetch(k, p.k + t * p.k_st + (int64_t)(h / p.rep) * p.k_sh, part, t < p.T);
+        fetch(q, p.q + t * p.q_st + (int64_t)(h / p.rep) * p.q_sh, part, t < p.T);
         if (tid < len) {
             g = p.g[(int64_t)(t0 + tid) * p.g_st + h];
             beta = p.beta[(int64_t)(t0 + tid) * p.H + h];
         }
-        RowPart k = scaled_row(kv);
+        if (r >= len) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) k[i] = q[i] = make_uint4(0, 0, 0, 0);
+        }
+        const float kk = squares(k);
+        const bool fine = kk < INFINITY;
+        // 2^-e with |k| <= 2^e < 2 |k| or so; values of the smallest exponents stay smaller
+        const int e = ((int)(__float_as_uint(kk) >> 23) - 127 + 2) >> 1;
+        const float down = __uint_as_float((uint32_t)(127 - e) << 23), one = 1.f / sqrtf(kk + 1e-6f);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const uint32_t at = sw128_off(r, (4 * i + part) * 8, C);
             // (a row with infinities or NaN counts as zero, but for its own factor c)
-            const uint4 x = k.fine ? k.h[i] : make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4*>(smem + kSmK + at) = x;
+            *reinterpret_cast<uint4*>(smem + kSmK + at) = fine ? k[i] : make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(blk + kDeltaK + at) = fine ? times(k[i], down) : make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(smem + kSmQ + at) = q[i];
         }
-        if (part == 0) vec.ck[r] = k.fine ? unit(k) : NAN;
-        q = scaled_row(qv);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(smem + kSmQ + sw128_off(r, (4 * i + part) * 8, C)) = q.h[i];
-        if (part == 0) vec.cq[r] = unit(q);
+        const float qq = squares(q);
+        if (part == 0) {
+            vec.ck[r] = fine ? one : 0.f;
+            vec.ks[r] = fine ? one * __uint_as_float((uint32_t)(127 + e) << 23) : NAN;
+            vec.cq[r] = 1.f / sqrtf(qq + 1e-6f);
+        }
     }
     // sums of decays within the block, up to the token and behind it
     float pre = 0.f, suf = 0.f;
@@ -264,12 +247,7 @@ __global__ void __launch_bounds__(kThreads, 3) kda_delta_chunk(const __grid_cons
         for (int x = 16; x >= 1; x >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, x));
         if (lane == 0) vec.clears[warp] = mask, vec.strongest[warp] = most;
     }
-    fence_proxy_async();
     __syncthreads();
-    if (tid == 0) {
-        bulk_s2g(blk + kDeltaK, smem + kSmK, C * D * 2);
-        bulk_commit();
-    }
     // e^{G_i - G_j} on the diagonal: row j, column i - its block's first
     {
         const int j = r, o = j & ~(B - 1), i0 = 4 * part;
@@ -295,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 3) kda_delta_chunk(const __grid_cons
     if (tid < C) {
         constexpr float kLog2e = 1.4426950408889634f;
         const int blk_i = tid / B;
-        const float ck = vec.ck[tid], fine = zero_if_nan(ck);
+        const float ck = vec.ck[tid], ks = vec.ks[tid];
         // decays from each block's end up to the token, from the chunk's start, to its end
         float upto = pre, rest = suf;
 #pragma unroll
@@ -312,11 +290,11 @@ __global__ void __launch_bounds__(kThreads, 3) kda_delta_chunk(const __grid_cons
         // up: 2^-e with 2^e <= e^G < 2^(e+1), at most 2^15
         const int e = min(15, max(0, 127 - (int)(__float_as_uint(eg) >> 23)));
         const float up = __uint_as_float((uint32_t)(127 + e) << 23);
-        scal->c[tid] = eg * ck;
+        scal->c[tid] = eg * ks;
         scal->beta[tid] = beta;
-        scal->w[tid] = 0.5f * expf(rest) * fine;
+        scal->w[tid] = 0.5f * expf(rest) * zero_if_nan(ks);
         scal->down[tid] = __uint_as_float((uint32_t)(127 - e) << 23);
-        vec.rk[tid] = zero_if_nan(ex2(suf * kLog2e)) * fine;
+        vec.rk[tid] = zero_if_nan(ex2(suf * kLog2e)) * ck;
         vec.bk[tid] = -zero_if_nan(beta * ck);
         vec.eg[tid] = eg * up;
         vec.up[tid] = up;
@@ -333,16 +311,8 @@ __global__ void __launch_bounds__(kThreads, 3) kda_delta_chunk(const __grid_cons
     {
         const float f = vec.cq[r] * vec.eg[r];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t w[4] = {q.h[i].x, q.h[i].y, q.h[i].z, q.h[i].w};
-            uint32_t y[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 x = __half22float2(reinterpret_cast<const __half2&>(w[j]));
-                y[j] = half2_of(mul2(pack2(x.x, x.y), pack2(f, f)));
-            }
-            *reinterpret_cast<uint4*>(blk + kDeltaQ + sw128_off(r, (4 * i + part) * 8, C)) = make_uint4(y[0], y[1], y[2], y[3]);
-        }
+        for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<uint4*>(blk + kDeltaQ + sw128_off(r, (4 * i + part) * 8, C)) = times(q[i], f);
     }
     // scores: 16 rows x 32 columns a warp
     const int bi = warp & 3, r0 = bi * B, c0 = (warp >> 2) * 32;
@@ -362,8 +332,8 @@ __global__ void __launch_bounds__(kThreads, 3) kda_delta_chunk(const __grid_cons
                     frag(kt, c0 + 8 * t, ks, C, lane, b);
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
-                        mma_f16(kk[t + u], a, b[u], b[2 + u]);
-                        mma_f16(qk[t + u], qa, b[u], b[2 + u]);
+                        mma_bf16(kk[t + u], a, b[u], b[2 + u]);
+                        mma_bf16(qk[t + u], qa, b[u], b[2 + u]);
                     }
                 }
             }
@@ -396,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 3) kda_delta_chunk(const __grid_cons
                     for (int u = 0; u < 2; ++u) nv[u] = b * l[u] * kk[t][2 * half + u], pv[u] = cq * l[u] * qk[t][2 * half + u];
                 } else if (bj == bi) {
                     const float2 ck = *reinterpret_cast<const float2*>(vec.ck + j);
-                    const float l[2] = {e[t & 1][half][0] * zero_if_nan(ck.x), e[t & 1][half][1] * zero_if_nan(ck.y)};
+                    const float l[2] = {e[t & 1][half][0] * ck.x, e[t & 1][half][1] * ck.y};
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
                         nv[u] = j + u < i ? b * l[u] * kk[t][2 * half + u] : 0.f;
