@@ -801,21 +801,25 @@ kda_delta_walk(const __grid_constant__ DeltaParams p, const __grid_constant__ CU
 }
 
 // The states that the segments of a cut sequence start from: with a segment's N and Phi,
-// S <- S Phi + N, from its first one's end on. A CTA has 16 value rows of a (sequence, head), a
-// thread eight of them at one key; the transitions come by bulk copies, two at a time.
-// Bound by the chain: about 1 us a segment.
+// S <- S Phi + N, from its first one's end on.  A CTA has 16 value rows of a (sequence, head).
+// Its warps share out the sum: two for each 32 of the 128 terms, a lane with all rows at two
+// keys, so that a transition is read from shared memory once, and the state, the same
+// for all lanes, in wide loads; the four parts are then added up with N.  Transitions come by
+// bulk copies, two at a time, N a step ahead.
 constexpr int kChainThreads = 256;
 constexpr int kChainRows = 16;
 constexpr int kChainPlane = D * D * 4;
-constexpr int kChainSmem = 2 * kChainPlane + D * kChainRows * 4 + 16;
+constexpr int kChainParts = 4;
+constexpr int kChainLd = kChainRows + 4;
+constexpr int kChainSmem = 2 * kChainPlane + D * kChainRows * 4 + kChainParts * D * kChainLd * 4 + 16;
 __global__ void __launch_bounds__(kChainThreads, 1)
 kda_delta_chain(const __grid_constant__ DeltaParams p, const __grid_constant__ LinCuts cuts) {
     if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     float* const phi = reinterpret_cast<float*>(smem);
-    float* const st = phi + 2 * D * D;  // [key][row]
-    uint64_t* const full = reinterpret_cast<uint64_t*>(st + D * kChainRows);
+    float* const st = phi + 2 * D * D;            // [key][row]
+    float* const sums = st + D * kChainRows;      // [part][key][row]
+    uint64_t* const full = reinterpret_cast<uint64_t*>(sums + kChainParts * D * kChainLd);
     const int r = blockIdx.x / p.H, h = blockIdx.x % p.H, row0 = blockIdx.y * kChainRows;
-    const int key = threadIdx.x % D, half = threadIdx.x / D;
     const int first = cuts.first[r], steps = cuts.first[r + 1] - first - 2;
     auto plane = [&](int g) { return p.planes + ((size_t)(first + g) * p.H + h) * 2 * D * D; };
     if (threadIdx.x == 0) {
@@ -833,20 +837,28 @@ kda_delta_chain(const __grid_constant__ DeltaParams p, const __grid_constant__ L
         if (steps >= 1) fetch(1);
         if (steps >= 2) fetch(2);
     }
+    // of the state: key `key`, rows 8 half .. + 7
+    const int key = threadIdx.x % D, half = threadIdx.x / D;
     const size_t at = (size_t)(row0 + 8 * half) * D + key;
-    f2 s[4];
+    float s[8], next[8];
+    bool cleared = false;
     auto keep = [&]() {
+        float* to = st + key * kChainRows + 8 * half;
+        *reinterpret_cast<float4*>(to) = make_float4(s[0], s[1], s[2], s[3]);
+        *reinterpret_cast<float4*>(to + 4) = make_float4(s[4], s[5], s[6], s[7]);
+    };
+    auto fetch_n = [&](int g) {
+        if (g > steps) return;
 #pragma unroll
-        for (int i = 0; i < 4; i += 2)
-            *reinterpret_cast<ulonglong2*>(st + key * kChainRows + 8 * half + 2 * i) = make_ulonglong2(s[i], s[i + 1]);
+        for (int i = 0; i < 8; ++i) next[i] = plane(g)[at + i * D];
+        cleared = p.kept[(size_t)(first + g) * p.H + h] != 0.f;
     };
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s[i] = pack2(plane(0)[at + 2 * i * D], plane(0)[at + (2 * i + 1) * D]);
+    for (int i = 0; i < 8; ++i) s[i] = plane(0)[at + i * D];
     keep();
+    fetch_n(1);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp >> 1, two = ((warp & 1) * 32 + lane) * 2;
     for (int g = 1; g <= steps; ++g) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s[i] = pack2(plane(g)[at + 2 * i * D], plane(g)[at + (2 * i + 1) * D]);
-        const bool cleared = p.kept[(size_t)(first + g) * p.H + h] != 0.f;
         if (!__syncthreads_and(mbar_wait(full + (g & 1), ((g - 1) >> 1) & 1))) {
             // report, and let the copies in flight land
             if (threadIdx.x == 0) {
@@ -856,32 +868,51 @@ kda_delta_chain(const __grid_constant__ DeltaParams p, const __grid_constant__ L
             }
             return;
         }
-        if (!cleared) {
-            const float* f = phi + (g & 1) * D * D + key;
+        f2 acc[2][kChainRows / 2] = {};  // pairs of rows
+        const float* f = phi + (g & 1) * D * D + part * (D / kChainParts) * D + two;
+        const float* x = st + part * (D / kChainParts) * kChainRows;
 #pragma unroll 8
-            for (int j = 0; j < D; ++j) {
-                const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(st + j * kChainRows + 8 * half);
-                const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(st + j * kChainRows + 8 * half + 4);
-                const f2 t = pack2(f[j * D], f[j * D]);
-                s[0] = fma2(a.x, t, s[0]);
-                s[1] = fma2(a.y, t, s[1]);
-                s[2] = fma2(b.x, t, s[2]);
-                s[3] = fma2(b.y, t, s[3]);
+        for (int j = 0; j < D / kChainParts; ++j) {
+            const float2 t = *reinterpret_cast<const float2*>(f + j * D);
+            const f2 t0 = pack2(t.x, t.x), t1 = pack2(t.y, t.y);
+#pragma unroll
+            for (int i = 0; i < kChainRows / 4; ++i) {
+                const ulonglong2 y = *reinterpret_cast<const ulonglong2*>(x + j * kChainRows + 4 * i);
+                acc[0][2 * i] = fma2(y.x, t0, acc[0][2 * i]);
+                acc[0][2 * i + 1] = fma2(y.y, t0, acc[0][2 * i + 1]);
+                acc[1][2 * i] = fma2(y.x, t1, acc[1][2 * i]);
+                acc[1][2 * i + 1] = fma2(y.y, t1, acc[1][2 * i + 1]);
             }
         }
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int i = 0; i < kChainRows / 4; ++i)
+                *reinterpret_cast<ulonglong2*>(sums + (part * D + two + u) * kChainLd + 4 * i) = make_ulonglong2(acc[u][2 * i], acc[u][2 * i + 1]);
         __syncthreads();  // all are done with st and the transition
         if (threadIdx.x == 0 && g + 2 <= steps) {
             fence_proxy_async();
             fetch(g + 2);
         }
-        keep();
+        if (cleared) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 y = unpack2(s[i]);
-            plane(g)[at + 2 * i * D] = y.x;
-            plane(g)[at + (2 * i + 1) * D] = y.y;
+            for (int i = 0; i < 8; ++i) s[i] = next[i];
+        } else {
+            float y[8] = {};
+#pragma unroll
+            for (int u = 0; u < kChainParts; ++u) {
+                const float* from = sums + (u * D + key) * kChainLd + 8 * half;
+                const float4 a = *reinterpret_cast<const float4*>(from), b = *reinterpret_cast<const float4*>(from + 4);
+                y[0] += a.x, y[1] += a.y, y[2] += a.z, y[3] += a.w;
+                y[4] += b.x, y[5] += b.y, y[6] += b.z, y[7] += b.w;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s[i] = y[i] + next[i];
         }
-        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) plane(g)[at + i * D] = s[i];
+        keep();
+        fetch_n(g + 1);
     }
 }
 

@@ -31,13 +31,65 @@ __device__ __forceinline__ void load_weights(float (&w)[VE], const float* p) {
     for (int j = 0; j < VE; ++j) w[j] = p ? p[j] : 1.f;
 }
 
+// Two fp32 values in one 64-bit register.
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 pack2(float a, float b) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2(f2 a) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+    return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+template <int VE>
+__device__ __forceinline__ void pairs(f2 (&x)[VE / 2], const float (&f)[VE]) {
+#pragma unroll
+    for (int j = 0; j < VE / 2; ++j) x[j] = pack2(f[2 * j], f[2 * j + 1]);
+}
+template <int VE>
+__device__ __forceinline__ void values(float (&f)[VE], const f2 (&x)[VE / 2]) {
+#pragma unroll
+    for (int j = 0; j < VE / 2; ++j) {
+        const float2 y = unpack2(x[j]);
+        f[2 * j] = y.x, f[2 * j + 1] = y.y;
+    }
+}
+
+// The table's entries of two pairs, 16 bytes: (c, c, s, s) for the half layout, (c, s, c, s)
+// for pairs beside each other. Units lie beside each other in it, so that a row's lanes
+// read it without conflicts.
+template <int VE, bool IL>
+struct Entry {
+    static constexpr int kPairs = IL ? VE / 2 : VE;  // of a unit
+    static __device__ __forceinline__ void put(float* table, int j, int rot_units, float2 cs) {
+        const int u = j / kPairs, k = j % kPairs, e = k & 1;
+        float* at = table + ((k >> 1) * rot_units + u) * 4;
+        at[IL ? 2 * e : e] = cs.x;
+        at[IL ? 2 * e + 1 : 2 + e] = cs.y;
+    }
+};
+
 // `units` units a row, at most LANES, the first rot_units of them turned.
 template <class E, int VE, bool IL, int LANES>
-__global__ void __launch_bounds__(kMaxThreads)
+__global__ void __maxnreg__(80)
 kda_qk_norm_rope(const __grid_constant__ NormRopeParams p, int tokens, int rot_units, int units) {
     using U = Unit<E, VE, IL>;
-    __shared__ float2 table[kMaxTable];
-    constexpr int kAhead = 2;
+    using T = Entry<VE, IL>;
+    __shared__ __align__(16) float table[2 * kMaxTable];
+    __shared__ unsigned long long fraction[rope::kMaxPairs];
+    constexpr int kAhead = 2, kH = VE / 2;
     const int half = p.rot >> 1;
     const int64_t t0 = (int64_t)blockIdx.x * tokens;
     const int nt = (int)min((int64_t)tokens, p.T - t0);
@@ -63,50 +115,82 @@ kda_qk_norm_rope(const __grid_constant__ NormRopeParams p, int tokens, int rot_u
 #pragma unroll
         for (int i = 0; i < kAhead; ++i)
             if (i < n) x[i].load(in + i * in_st, at, at2, turned);
-        float w1[VE], w2[VE];
-        const float* weight = live && p.weight[which] ? p.weight[which] + (int64_t)h * p.weight_sh[which] : nullptr;
-        load_weights<VE>(w1, weight ? weight + at : nullptr);
-        load_weights<VE>(w2, weight && two ? weight + at2 : nullptr);
+        f2 w1[kH], w2[kH];
+        {
+            const float* weight = live && p.weight[which] ? p.weight[which] + (int64_t)h * p.weight_sh[which] : nullptr;
+            float w[VE];
+            load_weights<VE>(w, weight ? weight + at : nullptr);
+            pairs<VE>(w1, w);
+            load_weights<VE>(w, weight && two ? weight + at2 : nullptr);
+            pairs<VE>(w2, w);
+        }
         if (!made) {
+            for (int j = threadIdx.x; j < half; j += blockDim.x) fraction[j] = rope::fraction_of(p, j);
+            __syncthreads();
             for (int i = threadIdx.x; i < nt * half; i += blockDim.x) {
                 const int t = i / half, j = i - t * half;
-                table[i] = rope::turn_of(p, t0 + t, j);
+                T::put(table + 2 * t * half, j, rot_units, rope::turn_of(p, t0 + t, fraction[j]));
             }
             __syncthreads();
             made = true;
         }
-        const float2* cs = table + (U::kPaired ? u * VE : u * VE / 2);
+        const float4* cs = reinterpret_cast<const float4*>(table) + u;
         for (int t = 0; t < nt; t += kAhead) {
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) {
-                float f[VE], g[VE];
-                x[i].a.get(f);
-                if constexpr (U::kPaired) x[i].b.get(g);
-                float sum = 0.f;
+                f2 f[kH], g[kH];
+                float v[VE];
+                x[i].a.get(v);
+                pairs<VE>(f, v);
+                f2 sum = 0;
 #pragma unroll
-                for (int j = 0; j < VE; ++j) sum = fmaf(f[j], f[j], sum);
+                for (int j = 0; j < kH; ++j) sum = fma2(f[j], f[j], sum);
                 if constexpr (U::kPaired) {
+                    x[i].b.get(v);
+                    pairs<VE>(g, v);
                     if (two) {
 #pragma unroll
-                        for (int j = 0; j < VE; ++j) sum = fmaf(g[j], g[j], sum);
+                        for (int j = 0; j < kH; ++j) sum = fma2(g[j], g[j], sum);
                     }
                 }
-                sum = group_sum<LANES>(live ? sum : 0.f);
-                const float inv = 1.f / sqrtf(fmaf(sum, per, p.eps));
+                const float2 both = unpack2(sum);
+                const float all = group_sum<LANES>(live ? both.x + both.y : 0.f);
+                const float inv = 1.f / sqrtf(fmaf(all, per, p.eps));
+                const f2 inv2 = pack2(inv, inv);
                 if (t + i < n) {
 #pragma unroll
-                    for (int j = 0; j < VE; ++j) f[j] *= inv * w1[j];
+                    for (int j = 0; j < kH; ++j) f[j] = mul2(f[j], mul2(inv2, w1[j]));
                     if constexpr (U::kPaired) {
 #pragma unroll
-                        for (int j = 0; j < VE; ++j) g[j] *= inv * w2[j];
+                        for (int j = 0; j < kH; ++j) g[j] = mul2(g[j], mul2(inv2, w2[j]));
                     }
-                    if (turned) U::turn(f, g, cs + i * half);
-                    x[i].a.set(f);
-                    if constexpr (U::kPaired) x[i].b.set(g);
+                    if (turned) {
+                        const float4* k = cs + i * (half / 2);
+#pragma unroll
+                        for (int j = 0; j < T::kPairs / 2; ++j) {
+                            const float4 y = k[j * rot_units];
+                            if constexpr (U::kPaired) {
+                                const f2 c = pack2(y.x, y.y), s = pack2(y.z, y.w), ms = pack2(-y.z, -y.w);
+                                const f2 a = f[j];
+                                f[j] = fma2(g[j], ms, mul2(a, c));
+                                g[j] = fma2(a, s, mul2(g[j], c));
+                            } else {
+                                const float2 a = unpack2(f[2 * j]), b = unpack2(f[2 * j + 1]);
+                                f[2 * j] = fma2(pack2(a.y, a.x), pack2(-y.y, y.y), mul2(f[2 * j], pack2(y.x, y.x)));
+                                f[2 * j + 1] = fma2(pack2(b.y, b.x), pack2(-y.w, y.w), mul2(f[2 * j + 1], pack2(y.z, y.z)));
+                            }
+                        }
+                    }
+                    values<VE>(v, f);
+                    x[i].a.set(v);
+                    if constexpr (U::kPaired) {
+                        values<VE>(v, g);
+                        x[i].b.set(v);
+                    }
                     x[i].store(out + i * out_st, at, at2, turned);
                 }
             }
-            cs += kAhead * half;
+            cs += kAhead * (half / 2);
             in += kAhead * in_st;
             out += kAhead * out_st;
 #pragma unroll
@@ -122,12 +206,15 @@ __global__ void __launch_bounds__(kMaxThreads)
 kda_qk_norm_rope_long(const __grid_constant__ NormRopeParams p, int tokens, int rot_units, int units) {
     using U = Unit<E, VE, IL>;
     __shared__ float2 table[kMaxTable];
+    __shared__ unsigned long long fraction[rope::kMaxPairs];
     const int half = p.rot >> 1;
     const int64_t t0 = (int64_t)blockIdx.x * tokens;
     const int nt = (int)min((int64_t)tokens, p.T - t0);
+    for (int j = threadIdx.x; j < half; j += blockDim.x) fraction[j] = rope::fraction_of(p, j);
+    __syncthreads();
     for (int i = threadIdx.x; i < nt * half; i += blockDim.x) {
         const int t = i / half, j = i - t * half;
-        table[i] = rope::turn_of(p, t0 + t, j);
+        table[i] = rope::turn_of(p, t0 + t, fraction[j]);
     }
     __syncthreads();
     const int h0 = p.x[0].heads, heads = h0 + p.x[1].heads, lane = threadIdx.x & 31;

@@ -24,6 +24,7 @@ constexpr int kMaxTable = 2048;  // pairs times tokens a CTA holds (16 KB)
 template <class E, int VE, bool IL>
 __global__ void __maxnreg__(56) kda_rope(RopeParams p, int tokens, int rot_units, int units) {
     __shared__ float2 table[kMaxTable];
+    __shared__ unsigned long long fraction[rope::kMaxPairs];
     constexpr int kAhead = 4;
     const int half = p.rot >> 1;
     const int64_t t0 = (int64_t)blockIdx.x * tokens;
@@ -48,9 +49,11 @@ __global__ void __maxnreg__(56) kda_rope(RopeParams p, int tokens, int rot_units
         for (int i = 0; i < kAhead; ++i)
             if (i < n) x[i].load(in + i * in_st, at, at2, turned);
         if (!made) {
+            for (int j = threadIdx.x; j < half; j += blockDim.x) fraction[j] = rope::fraction_of(p, j);
+            __syncthreads();
             for (int i = threadIdx.x; i < nt * half; i += blockDim.x) {
                 const int t = i / half, j = i - t * half;
-                table[i] = rope::turn_of(p, t0 + t, j);
+                table[i] = rope::turn_of(p, t0 + t, fraction[j]);
             }
             __syncthreads();
             made = true;

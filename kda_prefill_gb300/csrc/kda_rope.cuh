@@ -13,18 +13,22 @@
 namespace kda {
 namespace rope {
 
-// (c, s) of token t and pair j.
-__device__ __forceinline__ float2 turn_of(const RopeParams& p, int64_t t, int j) {
+// F of pair j.  (64-bit floating point is slow: one for each pair and CTA, not for each token.)
+__device__ __forceinline__ unsigned long long fraction_of(const RopeParams& p, int j) {
+    const double turns = p.inv_freq[j] * 0.15915494309189533577;  // 1 / 2 pi
+    return (unsigned long long)__double2ll_rn((turns - rint(turns)) * 18446744073709551616.0);
+}
+// (c, s) of token t and a pair.
+__device__ __forceinline__ float2 turn_of(const RopeParams& p, int64_t t, unsigned long long fraction) {
     const int64_t pos = p.pos64 ? static_cast<const int64_t*>(p.pos)[t]
                                 : (int64_t) static_cast<const int32_t*>(p.pos)[t];
-    const double turns = p.inv_freq[j] * 0.15915494309189533577;  // 1 / 2 pi
-    const long long F = __double2ll_rn((turns - rint(turns)) * 18446744073709551616.0);
-    const unsigned long long phase = (unsigned long long)pos * (unsigned long long)F;
+    const unsigned long long phase = (unsigned long long)pos * fraction;
     const float a = (float)(int)(phase >> 32) * 4.656612873077392578125e-10f;  // 2^-31
     float s, c;
     sincospif(a, &s, &c);
     return make_float2(c * p.factor, s * p.factor * p.sign);
 }
+constexpr int kMaxPairs = 512;  // of a head
 
 // One unit of a row: 16 bytes, and for pairs of the half layout (and for the narrow
 // form's pairs) the partner's.
