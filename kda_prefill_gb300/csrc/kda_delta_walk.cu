@@ -483,10 +483,10 @@ __device__ __forceinline__ bool write(const Walk& w, const DeltaParams& p, uint3
 
 // Warps 0-15: a thread has a quarter of value row `row`: 32 keys, 16 of a chunk's tokens.
 // Starts from `state` (fp32 values if it is a plane, S if of the pool; 0: from zero, or from
-// the identity) and leaves the state there.
+// the identity) and leaves the state there, whether a token cleared it and the decay over all.
 template <class S>
 __device__ __forceinline__ bool make(const Walk& w, const DeltaParams& p, uint32_t base, int warp, int lane, const S* from,
-                                     const float* plane, f2 (&s)[kKeys / 2], bool& cleared) {
+                                     const float* plane, f2 (&s)[kKeys / 2], bool& cleared, float& decay) {
     const int part = warp >> 2, row = 32 * (warp & 3) + lane;
     const uint32_t tm = base + ((uint32_t)(32 * (warp & 3)) << 16);
     const int at = row * D + part * kKeys;
@@ -515,6 +515,7 @@ __device__ __forceinline__ bool make(const Walk& w, const DeltaParams& p, uint32
         }
     }
     cleared = false;
+    decay = 1.f;
     float smax = 0.f;
 #pragma unroll
     for (int i = 0; i < kKeys / 2; ++i) smax = max_abs(smax, s[i]);
@@ -633,6 +634,7 @@ __device__ __forceinline__ bool make(const Walk& w, const DeltaParams& p, uint32
         arrive_warp(kUReady, lane);
         // S
         const bool more = c + 1 < w.chunks;
+        decay *= sc->gamma;
         const f2 gamma = pack2(sc->gamma, sc->gamma), back = pack2(2.f * inv, 2.f * inv);
         if (clear < C) {
 #pragma unroll
@@ -680,6 +682,10 @@ __device__ __forceinline__ bool make(const Walk& w, const DeltaParams& p, uint32
     }
     return true;
 }
+
+// An entry of a transition's plane: row j's columns by eights in another order for every two
+// rows, so that a fragment's rows lie in different banks.
+__host__ __device__ constexpr int phi_at(int j, int k) { return j * D + (k ^ ((j >> 1 & 3) * 8)); }
 
 template <class S>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -745,17 +751,39 @@ kda_delta_walk(const __grid_constant__ DeltaParams p, const __grid_constant__ CU
         asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
         f2 s[kKeys / 2];
         bool cleared;
+        float decay;
         if (begins) grid_dep_wait();
-        const bool done = make<S>(w, p, tm, warp, lane, init ? state : nullptr, begins, s, cleared);
+        const bool done = make<S>(w, p, tm, warp, lane, init ? state : nullptr, begins, s, cleared, decay);
         const End end = *reinterpret_cast<const End*>(smem + kSmEnd);
         const int place = (32 * (warp & 3) + lane) * D + (warp >> 2) * kKeys;
-        if (done && end.plane) {
+        if (done && end.plane && !end.kept) {
 #pragma unroll
             for (int j = 0; j < kKeys / 2; j += 2) {
                 const float2 a = unpack2(s[j]), b = unpack2(s[j + 1]);
                 *reinterpret_cast<float4*>(end.plane + place + 2 * j) = make_float4(a.x, a.y, b.x, b.y);
             }
-            if (end.kept && threadIdx.x == 0) *end.kept = cleared ? 1.f : 0.f;
+        } else if (done && end.plane) {
+            // a transition, its entries at most the decay: for the chain as sums of two fp16
+            float undo;
+            const float up = scale_of(fminf(decay, 1.f), undo);
+            const int j = 32 * (warp & 3) + lane;
+#pragma unroll
+            for (int i = 0; i < kKeys; i += 4) {
+                uint32_t e[4];
+#pragma unroll
+                for (int u = 0; u < 4; u += 2) {
+                    const float2 a = unpack2(s[(i + u) / 2]);
+                    const float x = a.x * up, y = a.y * up;
+                    const __half2 hi = __floats2half2_rn(x, y);
+                    const float2 f = __half22float2(hi);
+                    const uint32_t h = reinterpret_cast<const uint32_t&>(hi), l = pack_half2(x - f.x, y - f.y);
+                    e[u] = __byte_perm(h, l, 0x5410);
+                    e[u + 1] = __byte_perm(h, l, 0x7632);
+                }
+                *reinterpret_cast<uint4*>(reinterpret_cast<uint32_t*>(end.plane) + phi_at(j, (warp >> 2) * kKeys + i)) =
+                    make_uint4(e[0], e[1], e[2], e[3]);
+            }
+            if (threadIdx.x == 0) *end.kept = cleared ? -1.f : undo;
         } else if (done && end.state) {
             constexpr int N = 16 / sizeof(S);
             S* to = static_cast<S*>(end.state) + place;
@@ -801,24 +829,27 @@ kda_delta_walk(const __grid_constant__ DeltaParams p, const __grid_constant__ CU
 }
 
 // The states that the segments of a cut sequence start from: with a segment's N and Phi,
-// S <- S Phi + N, from its first one's end on.  A CTA has 16 value rows of a (sequence, head).
-// Its warps share out the sum: two for each 32 of the 128 terms, a lane with all rows at two
-// keys, so that a transition is read from shared memory once, and the state, the same
-// for all lanes, in wide loads; the four parts are then added up with N.  Transitions come by
-// bulk copies, two at a time, N a step ahead.
+// S <- S Phi + N, from its first one's end on.  A CTA has 16 value rows of a (sequence, head), a
+// warp 16 of the keys.  S and Phi are sums of two fp16, S's rows scaled by a power of two,
+// Phi by one for all, from its largest possible entry, the decay over the segment.
+// Transitions come by bulk copies, two at a time, N a step ahead.
+// Bound by the chain, about 1 us a segment; with fp32 products it took 2.7, the FMA units' rate
+// being half of that.
 constexpr int kChainThreads = 256;
 constexpr int kChainRows = 16;
 constexpr int kChainPlane = D * D * 4;
-constexpr int kChainParts = 4;
-constexpr int kChainLd = kChainRows + 4;
-constexpr int kChainSmem = 2 * kChainPlane + D * kChainRows * 4 + kChainParts * D * kChainLd * 4 + 16;
+constexpr int kChainTile = kChainRows * D * 2;
+constexpr int kChainS = 2 * kChainPlane;                    // S, high and low part
+constexpr int kChainMax = kChainS + 2 * kChainTile;         // [8][16] largest of a row, by warp
+constexpr int kChainBar = kChainMax + 8 * kChainRows * 4;
+constexpr int kChainSmem = kChainBar + 16;
 __global__ void __launch_bounds__(kChainThreads, 1)
 kda_delta_chain(const __grid_constant__ DeltaParams p, const __grid_constant__ LinCuts cuts) {
     if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    float* const phi = reinterpret_cast<float*>(smem);
-    float* const st = phi + 2 * D * D;            // [key][row]
-    float* const sums = st + D * kChainRows;      // [part][key][row]
-    uint64_t* const full = reinterpret_cast<uint64_t*>(sums + kChainParts * D * kChainLd);
+    const uint32_t* const phi = reinterpret_cast<const uint32_t*>(smem);
+    uint8_t* const tile = smem + kChainS;
+    float* const most = reinterpret_cast<float*>(smem + kChainMax);
+    uint64_t* const full = reinterpret_cast<uint64_t*>(smem + kChainBar);
     const int r = blockIdx.x / p.H, h = blockIdx.x % p.H, row0 = blockIdx.y * kChainRows;
     const int first = cuts.first[r], steps = cuts.first[r + 1] - first - 2;
     auto plane = [&](int g) { return p.planes + ((size_t)(first + g) * p.H + h) * 2 * D * D; };
@@ -831,33 +862,58 @@ kda_delta_chain(const __grid_constant__ DeltaParams p, const __grid_constant__ L
     grid_dep_wait();
     auto fetch = [&](int g) {
         mbar_arrive_expect_tx(full + (g & 1), kChainPlane);
-        bulk_g2s(phi + (g & 1) * D * D, plane(g) + D * D, kChainPlane, full + (g & 1));
+        bulk_g2s(smem + (g & 1) * kChainPlane, plane(g) + D * D, kChainPlane, full + (g & 1));
     };
     if (threadIdx.x == 0) {
         if (steps >= 1) fetch(1);
         if (steps >= 2) fetch(2);
     }
-    // of the state: key `key`, rows 8 half .. + 7
-    const int key = threadIdx.x % D, half = threadIdx.x / D;
-    const size_t at = (size_t)(row0 + 8 * half) * D + key;
-    float s[8], next[8];
-    bool cleared = false;
-    auto keep = [&]() {
-        float* to = st + key * kChainRows + 8 * half;
-        *reinterpret_cast<float4*>(to) = make_float4(s[0], s[1], s[2], s[3]);
-        *reinterpret_cast<float4*>(to + 4) = make_float4(s[4], s[5], s[6], s[7]);
-    };
+    // a thread has rows `row` and row + 8 at keys col, col + 1, col + 8, col + 9: s[8's][row][key]
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = lane >> 2, col = warp * 16 + (lane & 3) * 2;
+    const size_t at = (size_t)(row0 + row) * D + col;
+    float2 s[2][2], next[2][2];
+    float kept = 0.f, scale[2], inv[2];
     auto fetch_n = [&](int g) {
         if (g > steps) return;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) next[i] = plane(g)[at + i * D];
-        cleared = p.kept[(size_t)(first + g) * p.H + h] != 0.f;
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) next[t][u] = *reinterpret_cast<const float2*>(plane(g) + at + 8 * u * D + 8 * t);
+        kept = p.kept[(size_t)(first + g) * p.H + h];
+    };
+    // S's rows' scales and operand; all have the state of a step behind them
+    auto keep = [&]() {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            float m = fmaxf(fmaxf(fabsf(s[0][u].x), fabsf(s[0][u].y)), fmaxf(fabsf(s[1][u].x), fabsf(s[1][u].y)));
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+            if ((lane & 3) == 0) most[warp * kChainRows + row + 8 * u] = m;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            float m = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) m = fmaxf(m, most[i * kChainRows + row + 8 * u]);
+            scale[u] = scale_of(m, inv[u]);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const uint32_t to = sw128_off(row + 8 * u, col + 8 * t, kChainRows);
+                const float x = s[t][u].x * scale[u], y = s[t][u].y * scale[u];
+                const __half2 hi = __floats2half2_rn(x, y);
+                const float2 f = __half22float2(hi);
+                *reinterpret_cast<__half2*>(tile + to) = hi;
+                *reinterpret_cast<uint32_t*>(tile + kChainTile + to) = pack_half2(x - f.x, y - f.y);
+            }
+        }
     };
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s[i] = plane(0)[at + i * D];
-    keep();
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) s[t][u] = *reinterpret_cast<const float2*>(plane(0) + at + 8 * u * D + 8 * t);
     fetch_n(1);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp >> 1, two = ((warp & 1) * 32 + lane) * 2;
+    keep();
     for (int g = 1; g <= steps; ++g) {
         if (!__syncthreads_and(mbar_wait(full + (g & 1), ((g - 1) >> 1) & 1))) {
             // report, and let the copies in flight land
@@ -868,51 +924,47 @@ kda_delta_chain(const __grid_constant__ DeltaParams p, const __grid_constant__ L
             }
             return;
         }
-        f2 acc[2][kChainRows / 2] = {};  // pairs of rows
-        const float* f = phi + (g & 1) * D * D + part * (D / kChainParts) * D + two;
-        const float* x = st + part * (D / kChainParts) * kChainRows;
-#pragma unroll 8
-        for (int j = 0; j < D / kChainParts; ++j) {
-            const float2 t = *reinterpret_cast<const float2*>(f + j * D);
-            const f2 t0 = pack2(t.x, t.x), t1 = pack2(t.y, t.y);
+        float d[2][4] = {};
+        const uint32_t* f = phi + (g & 1) * D * D;
+        const uint32_t ta = smem_u32(tile) + sw128_off(lane & 15, 0, kChainRows);
+        const int swap = lane & 7;
 #pragma unroll
-            for (int i = 0; i < kChainRows / 4; ++i) {
-                const ulonglong2 y = *reinterpret_cast<const ulonglong2*>(x + j * kChainRows + 4 * i);
-                acc[0][2 * i] = fma2(y.x, t0, acc[0][2 * i]);
-                acc[0][2 * i + 1] = fma2(y.y, t0, acc[0][2 * i + 1]);
-                acc[1][2 * i] = fma2(y.x, t1, acc[1][2 * i]);
-                acc[1][2 * i + 1] = fma2(y.y, t1, acc[1][2 * i + 1]);
+        for (int ks = 0; ks < D; ks += 16) {
+            uint32_t hi[4], lo[4];
+            const uint32_t o = (ks >> 6) * (kChainRows * 128) + ((((ks & 63) / 8 + (lane >> 4)) ^ swap) << 4) - (swap << 4);
+            ldsm_x4(ta + o, hi[0], hi[1], hi[2], hi[3]);
+            ldsm_x4(ta + kChainTile + o, lo[0], lo[1], lo[2], lo[3]);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const int j = ks + (lane & 3) * 2, k = warp * 16 + 8 * t + row;
+                uint32_t bh[2], bl[2];
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const uint32_t x = f[phi_at(j + 8 * u, k)], y = f[phi_at(j + 8 * u + 1, k)];
+                    bh[u] = __byte_perm(x, y, 0x5410);
+                    bl[u] = __byte_perm(x, y, 0x7632);
+                }
+                mma_f16(d[t], lo, bh[0], bh[1]);
+                mma_f16(d[t], hi, bl[0], bl[1]);
+                mma_f16(d[t], hi, bh[0], bh[1]);
             }
         }
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int i = 0; i < kChainRows / 4; ++i)
-                *reinterpret_cast<ulonglong2*>(sums + (part * D + two + u) * kChainLd + 4 * i) = make_ulonglong2(acc[u][2 * i], acc[u][2 * i + 1]);
-        __syncthreads();  // all are done with st and the transition
+            for (int u = 0; u < 2; ++u) {
+                const float back = kept * inv[u];
+                float2 y = next[t][u];
+                if (kept >= 0.f) y.x = fmaf(d[t][2 * u], back, y.x), y.y = fmaf(d[t][2 * u + 1], back, y.y);
+                s[t][u] = y;
+                *reinterpret_cast<float2*>(plane(g) + at + 8 * u * D + 8 * t) = y;
+            }
+        fetch_n(g + 1);
+        keep();  // (its barrier: all are done with the operand and the transition)
         if (threadIdx.x == 0 && g + 2 <= steps) {
             fence_proxy_async();
             fetch(g + 2);
         }
-        if (cleared) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) s[i] = next[i];
-        } else {
-            float y[8] = {};
-#pragma unroll
-            for (int u = 0; u < kChainParts; ++u) {
-                const float* from = sums + (u * D + key) * kChainLd + 8 * half;
-                const float4 a = *reinterpret_cast<const float4*>(from), b = *reinterpret_cast<const float4*>(from + 4);
-                y[0] += a.x, y[1] += a.y, y[2] += a.z, y[3] += a.w;
-                y[4] += b.x, y[5] += b.y, y[6] += b.z, y[7] += b.w;
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) s[i] = y[i] + next[i];
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) plane(g)[at + i * D] = s[i];
-        keep();
-        fetch_n(g + 1);
     }
 }
 

@@ -108,7 +108,7 @@ struct DeltaParams : LinParams {
     uint8_t* blocks;  // [n_chunks][H] of kDeltaBlock bytes
     // of the cut sequences' segments: `planes` has two of [128 x 128] for each segment and
     // head, its state from zero (then the one that the next starts from) and its transition,
-    // `kept` whether a token of it clears the state
+    // `kept` what the transition is to be multiplied by, or -1 where a token clears the state
 };
 // What kda_delta_chunk leaves for the walk of a chunk and head: fp32 scalars, and fp16 tiles in
 // the swizzled layout of kda_device.cuh.
