@@ -1032,19 +1032,24 @@ cudaError_t launch(const DeltaParams& p, const LinCuts& cuts, const CUtensorMap&
 }
 
 // How the longest sequences are cut, from the long sequences' lengths (longest first).  In
-// units of a chunk's time in the walk: uncut it takes as long as its longest sequence, or as
-// all chunks shared out.  Cut into k segments, the first pass walks all but the last one
-// twice (but for the first), the second all but the first; the chain between them takes
-// half a unit a segment, and the two more launches about four.
+// units of a chunk's time in the walk: uncut it takes as long as its longest sequence.  Cut into
+// k segments, the first pass walks all but the last one twice (but for the first), the
+// second all but the first; the chain between them takes half a unit a segment, and the two
+// more launches about four.  `single` is the time of the single tokens, on all SMs: they run beside
+// the last walk on the SMs that it leaves, and then on all.
 struct Cut {
     int seg = 0, n_cut = 0, n_seg = 0;
 };
-Cut cut_rule(const int32_t* lens, int n, int H, int sms, int64_t planes) {
+Cut cut_rule(const int32_t* lens, int n, int H, int sms, int64_t planes, float single) {
     Cut best;
     if (n <= 0 || (int64_t)n * H > sms) return best;  // a wave of whole sequences fills the GPU
     auto chunks_of = [](int len) { return (len + C - 1) / C; };
+    const auto left = [&](int64_t items, int length) {  // of the single tokens, after the walk
+        const float beside = items < sms ? (float)length * (float)(sms - items) / (float)sms : 0.f;
+        return single > beside ? single - beside : 0.f;
+    };
     const int longest = chunks_of(lens[0]);
-    float least = (float)longest;
+    float least = (float)longest + left((int64_t)n * H, longest);
     for (int k = 2; k <= 32; ++k) {
         const int seg = (longest + k - 1) / k;
         if (seg < kDeltaMinSeg) break;
@@ -1065,7 +1070,7 @@ Cut cut_rule(const int32_t* lens, int n, int H, int sms, int64_t planes) {
         }
         if (c.n_cut > kLinCuts || (int64_t)c.n_seg * H > planes) break;
         const auto waves = [&](int64_t items) { return (float)((items + sms - 1) / sms); };
-        const float time = (waves(local) + waves(rest)) * (float)seg + 0.5f * (float)(most - 2) + 4.f;
+        const float time = (waves(local) + waves(rest)) * (float)seg + 0.5f * (float)(most - 2) + 4.f + left(rest, seg);
         if (time < least) least = time, best = c;
     }
     return best;
@@ -1074,7 +1079,9 @@ Cut cut_rule(const int32_t* lens, int n, int H, int sms, int64_t planes) {
 }  // namespace
 
 void delta_cut(DeltaParams& p, LinCuts& cuts, const SeqTables& t) {
-    const Cut c = cut_rule(t.long_lens, p.n_long, p.H, num_sms(), delta_planes(p.T, p.H));
+    // a single token's state of a head goes there and back at 6.6 TB/s, a chunk takes 2.6 us
+    const float state = p.st_dtype == KDA_STATE_F32 ? 0.0076f : 0.0045f;
+    const Cut c = cut_rule(t.long_lens, p.n_long, p.H, num_sms(), delta_planes(p.T, p.H), state * (float)p.n_short * (float)p.H);
     p.seg_len = c.seg * C;
     p.n_cut = c.n_cut;
     p.n_seg = c.n_seg;
