@@ -74,8 +74,8 @@ enum Bar {
     kTurned,                // [2] v turned over, its largest found
     kOEmpty = kTurned + 2,  // [2] O read
     kVEmpty = kOEmpty + 2,  // [2] v's rows read
-    kSReady = kVEmpty + 2,
-    kRReady,
+    kSReady = kVEmpty + 2,  // [2] half of each part's keys
+    kRReady = kSReady + 2,
     kUReady,
     kNumBars
 };
@@ -279,19 +279,24 @@ struct Issuer {
 #pragma unroll 1
         for (int c = 0; c < w.chunks; ++c) {
             const uint32_t at = smem_u32(block(c)), o = tm + kTmO + (c & 1) * C;
-            if (!wait(kFull + (c & 1), c >> 1) || !wait(kSReady, c)) return false;
-            tc_fence_after();
-            if (lead) {
-                const uint64_t kd = sw128_desc(at + kDeltaK, 0, 1024);
+            if (!wait(kFull + (c & 1), c >> 1)) return false;
+            // each maker's first 16 keys, then its others
+            const uint64_t kd = sw128_desc(at + kDeltaK, 0, 1024);
 #pragma unroll
-                for (int s = 0; s < 8; ++s)
+            for (int b = 0; b < 2; ++b) {
+                if (!wait(kSReady + b, c)) return false;
+                tc_fence_after();
+                if (lead) {
 #pragma unroll
-                    for (int part = 0; part < 2; ++part)
-                        mma_f16_ts(tm + kTmX, tm + kTmS + 16 * s + 8 * part, kd + (s >> 2) * kHalf + (s & 3) * 2, kIdescKK,
-                                   s > 0 || part > 0);
-                mma_commit(bar(kXDone));
+                    for (int s = b; s < 8; s += 2)
+#pragma unroll
+                        for (int part = 0; part < 2; ++part)
+                            mma_f16_ts(tm + kTmX, tm + kTmS + 16 * s + 8 * part, kd + (s >> 2) * kHalf + (s & 3) * 2, kIdescKK,
+                                       s > 0 || part > 0);
+                    if (b == 1) mma_commit(bar(kXDone));
+                }
+                __syncwarp();
             }
-            __syncwarp();
             // the chunk before's products are over, and its outputs read
             if (w.outputs && c >= 1 && !wait(kOEmpty + ((c - 1) & 1), (c - 1) >> 1)) return false;
             if (c >= 1 && c + 1 < w.chunks) load(c + 1);
@@ -546,6 +551,7 @@ __device__ __forceinline__ bool make(const Walk& w, const DeltaParams& p, uint32
     store_s(1, finite(smax));
     tmem_wait_st();
     arrive_warp(kSReady, lane);
+    arrive_warp(kSReady + 1, lane);
 
 #pragma unroll 1
     for (int c = 0; c < w.chunks; ++c) {
@@ -661,23 +667,28 @@ __device__ __forceinline__ bool make(const Walk& w, const DeltaParams& p, uint32
                 smax = max_abs(smax, s[i]);
             }
         }
-        if (more) {
-            store_s(0, true);
-            store_s(1, true);
-        }
+        if (lost) smax = NAN;
+        // (rare, and before the operand is given away: rows with infinities or NaN)
+        const bool strange = __any_sync(0xffffffffu, !finite(smax));
         if (lost) {
-            smax = NAN;
 #pragma unroll
             for (int i = 0; i < kKeys / 2; ++i) s[i] = pack2(NAN, NAN);
         }
         if (more) {
-            if (__any_sync(0xffffffffu, !finite(smax))) {
+            smax_of(c + 1, part)[row] = smax;
+            if (!strange) {
+                store_s(0, true);
+                tmem_wait_st();
+                arrive_warp(kSReady, lane);
+                store_s(1, true);
+            } else {
                 store_s(0, finite(smax));
+                tmem_wait_st();
+                arrive_warp(kSReady, lane);
                 store_s(1, finite(smax));
             }
-            smax_of(c + 1, part)[row] = smax;
             tmem_wait_st();
-            arrive_warp(kSReady, lane);
+            arrive_warp(kSReady + 1, lane);
         }
     }
     return true;

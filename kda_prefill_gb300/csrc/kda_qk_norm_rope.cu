@@ -81,15 +81,19 @@ struct Entry {
     }
 };
 
-// `units` units a row, at most LANES, the first rot_units of them turned.
+// `units` units a row, at most LANES, the first rot_units of them turned.  Rows ahead and
+// registers: a unit and its partner with their weights take 80 registers for two rows, a unit
+// alone 64 for four (16384 tokens, 12 + 12 heads, half layout: 39.3 us, 41.1 with four rows,
+// 43.6 with 64 registers; 12 + 2 heads, pairs beside each other: 28.1 us, 34.9 with two rows
+// and 80 registers, 30.3 with two and 64).
 template <class E, int VE, bool IL, int LANES>
-__global__ void __maxnreg__(80)
+__global__ void __maxnreg__(IL ? 64 : 80)
 kda_qk_norm_rope(const __grid_constant__ NormRopeParams p, int tokens, int rot_units, int units) {
     using U = Unit<E, VE, IL>;
     using T = Entry<VE, IL>;
     __shared__ __align__(16) float table[2 * kMaxTable];
     __shared__ unsigned long long fraction[rope::kMaxPairs];
-    constexpr int kAhead = 2, kH = VE / 2;
+    constexpr int kAhead = IL ? 4 : 2, kH = VE / 2;
     const int half = p.rot >> 1;
     const int64_t t0 = (int64_t)blockIdx.x * tokens;
     const int nt = (int)min((int64_t)tokens, p.T - t0);
