@@ -11,10 +11,10 @@
 // registers, and everything it rounds or scales belongs to that row.  Rows are independent of
 // each other but for the keys, so nothing has to be summed across threads.
 //
-// A CTA walks one (sequence, head), its warps in roles:
+// A CTA walks its share of the (sequence, head) pairs one after the other, its warps in roles:
 //   0-15   operands: four warps for each 32 rows
 //   16-19  the output rows
-//   20     issues the products and the blocks' copies
+//   20     issues the products and the blocks' copies, and says what comes next
 //   21-23  turn v over, so that a value row's tokens lie beside each other, and find its
 //          largest
 // The chain X, R, U, dS, S of one chunk after the other is the bound: the roles keep all
@@ -77,16 +77,25 @@ enum Bar {
     kSReady = kVEmpty + 2,  // [2] half of each part's keys
     kRReady = kSReady + 2,
     kUReady,
-    kNumBars
+    kMax,                   // an item's first state's largest values there
+    kItem,                  // [2] item there
+    kItemFree = kItem + 2,  // [2] and done with
+    kNumBars = kItemFree + 2
 };
 constexpr int kSmMisc = kSmBar + kNumBars * 8;   // abort flag, tensor-memory base
-struct End {  // what happens to the state in the end
-    void* state;   // of the pool, or nullptr
-    float* plane;  // a segment's
-    float* kept;   // whether a transition is of cleared states, or nullptr
+// A sequence and head, or a segment of one, to be walked.
+struct Item {
+    int h, t0, len, chunks;
+    bool outputs, values;  // makes outputs; has values (not the rows of a transition)
+    const uint8_t* blocks; // of the first chunk
+    const void* from;      // the pool's state that it starts from, or nullptr
+    const float* begins;   // a segment's
+    void* state;           // where its state goes: the pool, or nullptr
+    float* plane;          // or the segment's
+    float* kept;           // what a transition is to be multiplied by, or nullptr
 };
-constexpr int kSmEnd = kSmMisc + 16;
-constexpr int kSmemBytes = kSmEnd + (int)sizeof(End);
+constexpr int kSmItem = kSmMisc + 16;
+constexpr int kSmemBytes = kSmItem + 2 * (int)sizeof(Item);
 static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
 static_assert(kDeltaBlock % 1024 == 0 && kDeltaK % 1024 == 0 && kSmV % 1024 == 0 && kSmVT % 1024 == 0 && kSmBar % 8 == 0, "alignment");
 
@@ -249,100 +258,181 @@ __device__ __forceinline__ volatile uint2* bad_of(int c, int row) {
 }
 __device__ __forceinline__ volatile float* inv_of(int c) { return reinterpret_cast<volatile float*>(smem + kSmInv) + (c & 1) * D; }
 
-struct Walk {
-    int h, t0, len, chunks;
-    const uint8_t* blocks;  // of the first chunk
-    int64_t step;           // bytes between chunks' blocks
-    bool outputs, values;   // makes outputs; has values (not the rows of a transition)
-};
+__device__ __forceinline__ volatile const Item& ring(int k) { return *(reinterpret_cast<const Item*>(smem + kSmItem) + (k & 1)); }
 
-// Warp 20: products, and the copies of the chunks' blocks.
+// This CTA's items: the list, longest first, dealt out in turns of alternating direction.
+__device__ __forceinline__ int item_of(int k) {
+    const int g = gridDim.x, b = blockIdx.x;
+    return k * g + (k & 1 ? g - 1 - b : b);
+}
+__device__ __forceinline__ bool next_item(int k, int total) { return item_of(k) < total && wait(kItem + (k & 1), k >> 1); }
+__device__ __forceinline__ void done_with(int k, int lane) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(kItemFree + (k & 1)));
+}
+
+// Item i of the walk over all sequences, or (local) of the segments' first pass: all of a cut
+// sequence but its last segment from zero, then all but its first and last from the identity.
+template <class S>
+__device__ __forceinline__ Item item_at(const DeltaParams& p, const LinCuts& cuts, bool local, int i) {
+    Item w;
+    const int after = p.n_seg - p.n_cut;  // segments that are not their sequence's first
+    w.h = i % p.H;
+    i /= p.H;
+    w.values = !local || i < after;
+    bool first = true, last = true;
+    int n, at = 0, plane = 0, r = 0;
+    if (i < after || local) {
+        const int skip = w.values ? 1 : 2;  // segments of each sequence that have no such item
+        if (!w.values) i -= after;
+        while (i >= cuts.first[r + 1] - skip * (r + 1)) ++r;
+        const int g = i - (cuts.first[r] - skip * r) + (local && w.values ? 0 : 1);
+        n = cuts.seq[r];
+        w.t0 = cuts.t0[r] + g * p.seg_len;
+        w.len = min(p.seg_len, cuts.len[r] - g * p.seg_len);
+        at = g * (p.seg_len / C);
+        first = g == 0;
+        last = g + 1 == cuts.first[r + 1] - cuts.first[r];
+        plane = ((cuts.first[r] + g) * p.H + w.h) * 2;
+    } else {
+        n = p.long_list[p.n_cut + i - after];
+        w.t0 = p.cu[n];
+        w.len = p.cu[n + 1] - w.t0;
+    }
+    w.outputs = first || !local;
+    w.chunks = (w.len + C - 1) / C;
+    w.blocks = p.blocks + (((int64_t)p.seq_off[n] + at) * p.H + w.h) * kDeltaBlock;
+    const int slot = p.idx[n];
+    S* const state = slot >= 0 && slot < p.num_slots
+                         ? static_cast<S*>(p.pool) + (size_t)slot * p.stride0 + (size_t)w.h * D * D : nullptr;
+    w.from = first && state && p.has_init[n] != 0 ? state : nullptr;
+    w.begins = first || local ? nullptr : p.planes + (size_t)(plane - 2 * p.H) * D * D;
+    w.state = last && !local ? state : nullptr;
+    w.plane = local ? p.planes + (size_t)(plane + !w.values) * D * D : nullptr;
+    w.kept = w.values ? nullptr : p.kept + plane / 2;
+    return w;
+}
+
+// Warp 20: items, products, and the copies of the chunks' blocks.  Chunks are counted over all
+// items here as elsewhere: n.
+template <class S>
 struct Issuer {
-    const Walk& w;
-    const bool lead;
-    int loads = 0;
+    const DeltaParams& p;
+    const LinCuts& cuts;
+    const bool local, lead;
+    const int total;
+    int loads = 0, at_item = 0, at_chunk = 0, outs = 0;
 
-    __device__ __forceinline__ void load(int c) {
+    __device__ __forceinline__ void publish(int k) {
+        if (item_of(k) >= total) return;
         if (lead) {
+            const Item w = item_at<S>(p, cuts, local, item_of(k));
+            *(reinterpret_cast<Item*>(smem + kSmItem) + (k & 1)) = w;
+            if (w.from) {
+                const char* from = static_cast<const char*>(w.from);
+                asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"((uint32_t)(D * D * sizeof(S))) : "memory");
+            }
+            mbar_arrive(bar(kItem + (k & 1)));
+        }
+        __syncwarp();
+    }
+    // The next chunk's block, if its item is known.
+    __device__ __forceinline__ void load(int known) {
+        if (at_item > known || item_of(at_item) >= total) return;
+        if (lead) {
+            const volatile Item& w = ring(at_item);
             const uint32_t bytes = w.outputs ? kDeltaBlock : kDeltaQ;
-            mbar_arrive_expect_tx(bar(kFull + (c & 1)), bytes);
-            bulk_g2s(block(c), w.blocks + c * w.step, bytes, bar(kFull + (c & 1)));
+            mbar_arrive_expect_tx(bar(kFull + (loads & 1)), bytes);
+            bulk_g2s(block(loads), w.blocks + (int64_t)at_chunk * p.H * kDeltaBlock, bytes, bar(kFull + (loads & 1)));
         }
         __syncwarp();
         ++loads;
+        if (++at_chunk == ring(at_item).chunks) at_chunk = 0, ++at_item;
     }
     __device__ __forceinline__ bool go(uint32_t tm) {
         constexpr uint64_t kHalf = kTile / 2 >> 4;  // descriptors' addresses count 16 bytes
+        publish(0);
         grid_dep_wait();                            // the blocks are written
         load(0);
-        if (w.chunks > 1) load(1);
+        load(0);
+        int n = 0;
 #pragma unroll 1
-        for (int c = 0; c < w.chunks; ++c) {
-            const uint32_t at = smem_u32(block(c)), o = tm + kTmO + (c & 1) * C;
-            if (!wait(kFull + (c & 1), c >> 1)) return false;
-            // each maker's first 16 keys, then its others
-            const uint64_t kd = sw128_desc(at + kDeltaK, 0, 1024);
+        for (int k = 0; item_of(k) < total; ++k) {
+            const int chunks = ring(k).chunks;
+            const bool outputs = ring(k).outputs;
+#pragma unroll 1
+            for (int c = 0; c < chunks; ++c, ++n) {
+                const uint32_t at = smem_u32(block(n)), o = tm + kTmO + (outs & 1) * C;
+                if (!wait(kFull + (n & 1), n >> 1)) return false;
+                // each maker's first 16 keys, then its others
+                const uint64_t kd = sw128_desc(at + kDeltaK, 0, 1024);
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                if (!wait(kSReady + b, c)) return false;
+                for (int b = 0; b < 2; ++b) {
+                    if (!wait(kSReady + b, n)) return false;
+                    tc_fence_after();
+                    if (lead) {
+#pragma unroll
+                        for (int s = b; s < 8; s += 2)
+#pragma unroll
+                            for (int part = 0; part < 2; ++part)
+                                mma_f16_ts(tm + kTmX, tm + kTmS + 16 * s + 8 * part, kd + (s >> 2) * kHalf + (s & 3) * 2, kIdescKK,
+                                           s > 0 || part > 0);
+                        if (b == 1) mma_commit(bar(kXDone));
+                    }
+                    __syncwarp();
+                }
+                // the chunk before's products are over, and its outputs read
+                if (outs > 0 && !wait(kOEmpty + ((outs - 1) & 1), (outs - 1) >> 1)) return false;
+                if (c == 0) {
+                    if (k > 0 && item_of(k + 1) < total && !wait(kItemFree + ((k - 1) & 1), (k - 1) >> 1)) return false;
+                    publish(k + 1);
+                }
+                if (loads < n + 2) load(k + 1);
+                if (outputs) {
+                    tc_fence_after();
+                    if (lead) {
+                        const uint64_t qd = sw128_desc(at + kDeltaQ, 0, 1024);
+#pragma unroll
+                        for (int s = 0; s < 8; ++s)
+                            mma_f16_ts(o, tm + kTmS + 16 * s, qd + (s >> 2) * kHalf + (s & 3) * 2, kIdescKK, s > 0);
+                    }
+                    __syncwarp();
+                }
+                if (!wait(kRReady, n)) return false;
                 tc_fence_after();
                 if (lead) {
+                    const uint64_t td = sw128_desc(at + kDeltaT, 0, 1024);
 #pragma unroll
-                    for (int s = b; s < 8; s += 2)
+                    for (int s = 0; s < 4; ++s) {
+                        const uint64_t hi = td + 2 * s, lo = hi + (C * C * 2 >> 4);
+                        mma_f16_ts(tm + kTmUAcc, tm + kTmR + 16 * s, lo, kIdescKK, s > 0);
+                        mma_f16_ts(tm + kTmUAcc, tm + kTmR + 16 * s + 8, hi, kIdescKK, 1);
+                        mma_f16_ts(tm + kTmUAcc, tm + kTmR + 16 * s, hi, kIdescKK, 1);
+                    }
+                    mma_commit(bar(kUDone));
+                    if (outputs) {
+                        const uint64_t pd = sw128_desc(at + kDeltaPT, 0, 1024);
 #pragma unroll
-                        for (int part = 0; part < 2; ++part)
-                            mma_f16_ts(tm + kTmX, tm + kTmS + 16 * s + 8 * part, kd + (s >> 2) * kHalf + (s & 3) * 2, kIdescKK,
-                                       s > 0 || part > 0);
-                    if (b == 1) mma_commit(bar(kXDone));
+                        for (int s = 0; s < 4; ++s) mma_f16_ts(o, tm + kTmR + 16 * s, pd + 2 * s, kIdescKK, 1);
+                        mma_commit(bar(kODone + (outs & 1)));
+                    }
+                }
+                __syncwarp();
+                if (outputs) ++outs;
+                if (!wait(kUReady, n)) return false;
+                tc_fence_after();
+                if (lead) {
+                    const uint64_t km = sw128_desc(at + kDeltaK, kTile / 2, 1024);
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) {
+                        const uint64_t b = km + s * (2048 >> 4);
+                        mma_f16_ts(tm + kTmDS, tm + kTmU + 16 * s + 8, b, kIdescKM, s > 0);
+                        mma_f16_ts(tm + kTmDS, tm + kTmU + 16 * s, b, kIdescKM, 1);
+                    }
+                    mma_commit(bar(kDDone));
                 }
                 __syncwarp();
             }
-            // the chunk before's products are over, and its outputs read
-            if (w.outputs && c >= 1 && !wait(kOEmpty + ((c - 1) & 1), (c - 1) >> 1)) return false;
-            if (c >= 1 && c + 1 < w.chunks) load(c + 1);
-            if (w.outputs) {
-                tc_fence_after();
-                if (lead) {
-                    const uint64_t qd = sw128_desc(at + kDeltaQ, 0, 1024);
-#pragma unroll
-                    for (int s = 0; s < 8; ++s)
-                        mma_f16_ts(o, tm + kTmS + 16 * s, qd + (s >> 2) * kHalf + (s & 3) * 2, kIdescKK, s > 0);
-                }
-                __syncwarp();
-            }
-            if (!wait(kRReady, c)) return false;
-            tc_fence_after();
-            if (lead) {
-                const uint64_t td = sw128_desc(at + kDeltaT, 0, 1024);
-#pragma unroll
-                for (int s = 0; s < 4; ++s) {
-                    const uint64_t hi = td + 2 * s, lo = hi + (C * C * 2 >> 4);
-                    mma_f16_ts(tm + kTmUAcc, tm + kTmR + 16 * s, lo, kIdescKK, s > 0);
-                    mma_f16_ts(tm + kTmUAcc, tm + kTmR + 16 * s + 8, hi, kIdescKK, 1);
-                    mma_f16_ts(tm + kTmUAcc, tm + kTmR + 16 * s, hi, kIdescKK, 1);
-                }
-                mma_commit(bar(kUDone));
-                if (w.outputs) {
-                    const uint64_t pd = sw128_desc(at + kDeltaPT, 0, 1024);
-#pragma unroll
-                    for (int s = 0; s < 4; ++s) mma_f16_ts(o, tm + kTmR + 16 * s, pd + 2 * s, kIdescKK, 1);
-                    mma_commit(bar(kODone + (c & 1)));
-                }
-            }
-            __syncwarp();
-            if (!wait(kUReady, c)) return false;
-            tc_fence_after();
-            if (lead) {
-                const uint64_t km = sw128_desc(at + kDeltaK, kTile / 2, 1024);
-#pragma unroll
-                for (int s = 0; s < 4; ++s) {
-                    const uint64_t b = km + s * (2048 >> 4);
-                    mma_f16_ts(tm + kTmDS, tm + kTmU + 16 * s + 8, b, kIdescKM, s > 0);
-                    mma_f16_ts(tm + kTmDS, tm + kTmU + 16 * s, b, kIdescKM, 1);
-                }
-                mma_commit(bar(kDDone));
-            }
-            __syncwarp();
         }
         return true;
     }
@@ -362,69 +452,83 @@ struct Issuer {
 // Warps 21-23: v by value rows, and each row's largest finite |v|.  Tokens past the sequence's
 // end are zeros.
 struct Turner {
-    const Walk& w;
     const CUtensorMap* map;
-    const int which, lane;
+    const int total, which, lane;
     int loads = 0;
 
-    __device__ __forceinline__ void load_v(int c) {
+    __device__ __forceinline__ void load_v(const volatile Item& w, int c) {
         if (lane == 0) {
+            const int h = w.h, t = w.t0 + c * C;
             mbar_arrive_expect_tx(bar(kFullV), kTile);
-            tma_load_3d(smem + kSmV, map, bar(kFullV), 0, w.h, w.t0 + c * C);
-            tma_load_3d(smem + kSmV + kTile / 2, map, bar(kFullV), 64, w.h, w.t0 + c * C);
+            tma_load_3d(smem + kSmV, map, bar(kFullV), 0, h, t);
+            tma_load_3d(smem + kSmV + kTile / 2, map, bar(kFullV), 64, h, t);
         }
         __syncwarp();
         ++loads;
     }
     __device__ __forceinline__ bool go() {
-        if (which == 0) load_v(0);
+        int n = 0;
 #pragma unroll 1
-        for (int c = 0; c < w.chunks; ++c) {
-            if (!wait(kFullV, c) || (c > 1 && !wait(kVEmpty + (c & 1), (c >> 1) - 1))) return false;
-            const int live = w.len - c * C;
-            const uint32_t from = smem_u32(smem + kSmV), to = smem_u32(smem + kSmVT) + (c & 1) * kTile;
+        for (int k = 0; item_of(k) < total; ++k) {
+            if (!wait(kItem + (k & 1), k >> 1)) return false;
+            const volatile Item& w = ring(k);
+            const int chunks = w.values ? w.chunks : 0, len = w.len;
 #pragma unroll 1
-            for (int g = which; g < D / 8; g += kTurners) {
-                uint32_t r[8];
-                const int piece = ((g & 7) ^ (lane & 7)) << 4;
-                const uint32_t a = from + (g >> 3) * (kTile / 2) + lane * 128 + piece;
-                ldsm_x4_t(a, r[0], r[1], r[2], r[3]);
-                ldsm_x4_t(a + 32 * 128, r[4], r[5], r[6], r[7]);
-                const int t = 2 * (lane & 3);
-                if (live < C) {
+            for (int c = 0; c < chunks; ++c, ++n) {
+                if (which == 0 && loads == n) load_v(w, c);
+                if (!wait(kFullV, n) || (n > 1 && !wait(kVEmpty + (n & 1), (n >> 1) - 1))) return false;
+                const int live = len - c * C;
+                const uint32_t from = smem_u32(smem + kSmV), to = smem_u32(smem + kSmVT) + (n & 1) * kTile;
+#pragma unroll 1
+                for (int g = which; g < D / 8; g += kTurners) {
+                    uint32_t r[8];
+                    const int piece = ((g & 7) ^ (lane & 7)) << 4;
+                    const uint32_t a = from + (g >> 3) * (kTile / 2) + lane * 128 + piece;
+                    ldsm_x4_t(a, r[0], r[1], r[2], r[3]);
+                    ldsm_x4_t(a + 32 * 128, r[4], r[5], r[6], r[7]);
+                    const int t = 2 * (lane & 3);
+                    if (live < C) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        if (8 * i + t >= live) r[i] &= 0xFFFF0000u;
-                        if (8 * i + t + 1 >= live) r[i] &= 0x0000FFFFu;
+                        for (int i = 0; i < 8; ++i) {
+                            if (8 * i + t >= live) r[i] &= 0xFFFF0000u;
+                            if (8 * i + t + 1 >= live) r[i] &= 0x0000FFFFu;
+                        }
+                    }
+                    const int row = 8 * g + (lane & 7);
+                    const uint32_t b = to + row * 128;
+                    stsm_x4(b + (((lane >> 3) ^ (lane & 7)) << 4), r[0], r[1], r[2], r[3]);
+                    stsm_x4(b + (((4 + (lane >> 3)) ^ (lane & 7)) << 4), r[4], r[5], r[6], r[7]);
+                    __nv_bfloat162 m = __float2bfloat162_rn(0.f);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) m = __hmax2_nan(m, __habs2(reinterpret_cast<const __nv_bfloat162&>(r[i])));
+                    float f = max_nan(__low2float(m), __high2float(m));
+                    if (__any_sync(0xffffffffu, !finite(f))) {
+                        f = 0.f;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float x = fabsf(__uint_as_float(r[i] << 16)), y = fabsf(__uint_as_float(r[i] & 0xFFFF0000u));
+                            f = fmaxf(f, finite(x) ? x : 0.f);
+                            f = fmaxf(f, finite(y) ? y : 0.f);
+                        }
+                    }
+                    f = fmaxf(f, __shfl_xor_sync(0xffffffffu, f, 1));
+                    f = fmaxf(f, __shfl_xor_sync(0xffffffffu, f, 2));
+                    if ((lane & 3) == 0) vmax(n)[8 * g + (lane >> 2)] = f;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(kTurned + (n & 1)));
+                if (which == 0) {
+                    // all have read v: the next chunk's, of this item or the one after
+                    if (!wait(kTurned + (n & 1), n >> 1)) return false;
+                    if (c + 1 < chunks) {
+                        load_v(w, c + 1);
+                    } else if (item_of(k + 1) < total) {
+                        if (!wait(kItem + ((k + 1) & 1), (k + 1) >> 1)) return false;
+                        if (ring(k + 1).values) load_v(ring(k + 1), 0);
                     }
                 }
-                const int row = 8 * g + (lane & 7);
-                const uint32_t b = to + row * 128;
-                stsm_x4(b + (((lane >> 3) ^ (lane & 7)) << 4), r[0], r[1], r[2], r[3]);
-                stsm_x4(b + (((4 + (lane >> 3)) ^ (lane & 7)) << 4), r[4], r[5], r[6], r[7]);
-                __nv_bfloat162 m = __float2bfloat162_rn(0.f);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) m = __hmax2_nan(m, __habs2(reinterpret_cast<const __nv_bfloat162&>(r[i])));
-                float f = max_nan(__low2float(m), __high2float(m));
-                if (__any_sync(0xffffffffu, !finite(f))) {
-                    f = 0.f;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float x = fabsf(__uint_as_float(r[i] << 16)), y = fabsf(__uint_as_float(r[i] & 0xFFFF0000u));
-                        f = fmaxf(f, finite(x) ? x : 0.f);
-                        f = fmaxf(f, finite(y) ? y : 0.f);
-                    }
-                }
-                f = fmaxf(f, __shfl_xor_sync(0xffffffffu, f, 1));
-                f = fmaxf(f, __shfl_xor_sync(0xffffffffu, f, 2));
-                if ((lane & 3) == 0) vmax(c)[8 * g + (lane >> 2)] = f;
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(kTurned + (c & 1)));
-            if (which == 0 && c + 1 < w.chunks) {
-                if (!wait(kTurned + (c & 1), c >> 1)) return false;
-                load_v(c + 1);
-            }
+            done_with(k, lane);
         }
         return true;
     }
@@ -447,57 +551,75 @@ __device__ __noinline__ uint2 poisoned(uint2 bad, uint2 clears) {
     return r;
 }
 
-// Warps 16-19: a thread has an output row's 64 tokens.
-__device__ __forceinline__ bool write(const Walk& w, const DeltaParams& p, uint32_t base, int warp, int lane) {
+// Warps 16-19: a thread has an output row's 64 tokens.  n counts the chunks with outputs, all
+// the chunks of all items.
+__device__ __forceinline__ bool write(const DeltaParams& p, int total, uint32_t base, int warp, int lane) {
     const int row = 32 * (warp & 3) + lane;
     const uint32_t tm = base + ((uint32_t)(32 * (warp & 3)) << 16) + kTmO;
     const int64_t st = (int64_t)p.H * D;
+    int n = 0, all = 0;
 #pragma unroll 1
-    for (int c = 0; c < w.chunks; ++c) {
-        if (!wait(kODone + (c & 1), c >> 1)) return false;
-        tc_fence_after();
-        const DeltaScalars* sc = scalars(c);
-        uint2 spoils = make_uint2(bad_of(c, row)->x, bad_of(c, row)->y);
-        if (__any_sync(0xffffffffu, (spoils.x | spoils.y) != 0)) spoils = poisoned(spoils, make_uint2(sc->clears[0], sc->clears[1]));
-        const int live = w.len - c * C;
-        const float f = inv_of(c)[row] * p.scale;
-        __nv_bfloat16* o = p.out + ((int64_t)(w.t0 + c * C) * p.H + w.h) * D + row;
-#pragma unroll 1
-        for (int b = 0; b < C; b += 16) {
-            f2 x[8];
-            load16(tm + (c & 1) * C + b, x);
-#pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-                const float4 d = *reinterpret_cast<const float4*>(sc->down + b + 2 * i);
-                x[i] = mul2(mul2(x[i], pack2(d.x, d.y)), pack2(f, f));
-                x[i + 1] = mul2(mul2(x[i + 1], pack2(d.z, d.w)), pack2(f, f));
-            }
-            const unsigned lost = (b < 32 ? spoils.x : spoils.y) >> (b & 31);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float2 y = unpack2(x[i]);
-                if (b + 2 * i < live) o[0] = __float2bfloat16_rn(lost >> (2 * i) & 1 ? NAN : y.x);
-                if (b + 2 * i + 1 < live) o[st] = __float2bfloat16_rn(lost >> (2 * i + 1) & 1 ? NAN : y.y);
-                o += 2 * st;
-            }
+    for (int k = 0; item_of(k) < total; ++k) {
+        if (!wait(kItem + (k & 1), k >> 1)) return false;
+        const int h = ring(k).h, t0 = ring(k).t0, len = ring(k).len, chunks = ring(k).chunks;
+        const bool outputs = ring(k).outputs;
+        done_with(k, lane);
+        if (!outputs) {
+            all += chunks;
+            continue;
         }
-        arrive_warp(kOEmpty + (c & 1), lane);
+#pragma unroll 1
+        for (int c = 0; c < chunks; ++c, ++n, ++all) {
+            if (!wait(kODone + (n & 1), n >> 1)) return false;
+            tc_fence_after();
+            const DeltaScalars* sc = scalars(all);
+            uint2 spoils = make_uint2(bad_of(all, row)->x, bad_of(all, row)->y);
+            if (__any_sync(0xffffffffu, (spoils.x | spoils.y) != 0))
+                spoils = poisoned(spoils, make_uint2(sc->clears[0], sc->clears[1]));
+            const int live = len - c * C;
+            const float f = inv_of(all)[row] * p.scale;
+            __nv_bfloat16* o = p.out + ((int64_t)(t0 + c * C) * p.H + h) * D + row;
+#pragma unroll 1
+            for (int b = 0; b < C; b += 16) {
+                f2 x[8];
+                load16(tm + (n & 1) * C + b, x);
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) {
+                    const float4 d = *reinterpret_cast<const float4*>(sc->down + b + 2 * i);
+                    x[i] = mul2(mul2(x[i], pack2(d.x, d.y)), pack2(f, f));
+                    x[i + 1] = mul2(mul2(x[i + 1], pack2(d.z, d.w)), pack2(f, f));
+                }
+                const unsigned lost = (b < 32 ? spoils.x : spoils.y) >> (b & 31);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float2 y = unpack2(x[i]);
+                    if (b + 2 * i < live) o[0] = __float2bfloat16_rn(lost >> (2 * i) & 1 ? NAN : y.x);
+                    if (b + 2 * i + 1 < live) o[st] = __float2bfloat16_rn(lost >> (2 * i + 1) & 1 ? NAN : y.y);
+                    o += 2 * st;
+                }
+            }
+            arrive_warp(kOEmpty + (n & 1), lane);
+        }
     }
     return true;
 }
 
 // Warps 0-15: a thread has a quarter of value row `row`: 32 keys, 16 of a chunk's tokens.
-// Starts from `state` (fp32 values if it is a plane, S if of the pool; 0: from zero, or from
-// the identity) and leaves the state there, whether a token cleared it and the decay over all.
+// Walks an item, the CTA's chunks n on and its chunks with values nv on, and leaves the state
+// in s, whether a token cleared it and the decay over all.
 template <class S>
-__device__ __forceinline__ bool make(const Walk& w, const DeltaParams& p, uint32_t base, int warp, int lane, const S* from,
-                                     const float* plane, f2 (&s)[kKeys / 2], bool& cleared, float& decay) {
+__device__ __forceinline__ bool make(const DeltaParams& p, int k, int& n, int& nv, uint32_t base, int warp, int lane,
+                                     f2 (&s)[kKeys / 2], bool& cleared, float& decay) {
+    const int chunks = ring(k).chunks;
+    const bool values = ring(k).values;
     const int part = warp >> 2, row = 32 * (warp & 3) + lane;
     const uint32_t tm = base + ((uint32_t)(32 * (warp & 3)) << 16);
     const int at = row * D + part * kKeys;
     constexpr int N = 16 / sizeof(S);
 #pragma unroll
     for (int i = 0; i < kKeys / 2; ++i) s[i] = 0;
+    const S* const from = static_cast<const S*>(ring(k).from);
+    const float* const begins = ring(k).begins;
     if (from) {
 #pragma unroll
         for (int i = 0; i < kKeys; i += N) {
@@ -506,13 +628,14 @@ __device__ __forceinline__ bool make(const Walk& w, const DeltaParams& p, uint32
 #pragma unroll
             for (int j = 0; j < N; j += 2) s[(i + j) / 2] = pack2(f[j], f[j + 1]);
         }
-    } else if (plane) {
+    } else if (begins) {
+        grid_dep_wait();
 #pragma unroll
         for (int i = 0; i < kKeys; i += 4) {
-            const float4 f = *reinterpret_cast<const float4*>(plane + at + i);
+            const float4 f = *reinterpret_cast<const float4*>(begins + at + i);
             s[i / 2] = pack2(f.x, f.y), s[i / 2 + 1] = pack2(f.z, f.w);
         }
-    } else if (!w.values) {
+    } else if (!values) {
 #pragma unroll
         for (int i = 0; i < kKeys; i += 2) {
             const int key = part * kKeys + i;
@@ -524,16 +647,18 @@ __device__ __forceinline__ bool make(const Walk& w, const DeltaParams& p, uint32
     float smax = 0.f;
 #pragma unroll
     for (int i = 0; i < kKeys / 2; ++i) smax = max_abs(smax, s[i]);
-    smax_of(0, part)[row] = smax;
-    asm volatile("bar.sync 1, %0;" ::"n"(kMakers * 32) : "memory");
+    smax_of(n, part)[row] = smax;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(kMax));
+    if (!wait(kMax, k)) return false;
     // the largest |S| of the row a chunk ago; what a chunk adds to |S| at most
     auto of_row = [&](int c) {
         return max_nan(max_nan(smax_of(c, 0)[row], smax_of(c, 1)[row]), max_nan(smax_of(c, 2)[row], smax_of(c, 3)[row]));
     };
-    float was = of_row(0), adds, scale, inv;
-    auto rescale = [&](int c, float grown) {
+    float was = of_row(n), adds, scale, inv;
+    auto rescale = [&](int at, int at_v, float grown) {
         const float l = 11.32f * (finite(was) ? was : 0.f) + grown;  // |S| <= sqrt(128) max
-        const float b = scalars(c)->strongest, m = w.values ? vmax(c)[row] : 0.f;
+        const float b = scalars(at)->strongest, m = values ? vmax(at_v)[row] : 0.f;
         adds = 64.f * b * m;
         // (v itself has to stay finite when it is scaled)
         scale = scale_of(fmaxf(fmaxf(l, b * (m + l + adds)), 0x1p-60f * m), inv);
@@ -545,8 +670,8 @@ __device__ __forceinline__ bool make(const Walk& w, const DeltaParams& p, uint32
         for (int i = 0; i < 8; ++i) x[i] = live ? mul2(s[8 * b + i], pack2(scale, scale)) : 0;
         store_split(tm + kTmS + kKeys * part + 16 * b, x);
     };
-    if ((w.values && !wait(kTurned, 0)) || !wait(kFull, 0)) return false;
-    rescale(0, 0.f);
+    if ((values && !wait(kTurned + (nv & 1), nv >> 1)) || !wait(kFull + (n & 1), n >> 1)) return false;
+    rescale(n, nv, 0.f);
     store_s(0, finite(smax));
     store_s(1, finite(smax));
     tmem_wait_st();
@@ -554,8 +679,8 @@ __device__ __forceinline__ bool make(const Walk& w, const DeltaParams& p, uint32
     arrive_warp(kSReady + 1, lane);
 
 #pragma unroll 1
-    for (int c = 0; c < w.chunks; ++c) {
-        const DeltaScalars* sc = scalars(c);
+    for (int c = 0; c < chunks; ++c, ++n) {
+        const DeltaScalars* sc = scalars(n);
         // R
         const int clear = sc->first_clear;
         cleared = cleared || clear < C;
@@ -563,10 +688,10 @@ __device__ __forceinline__ bool make(const Walk& w, const DeltaParams& p, uint32
         f2 y0[8], bc[8];
         {
             uint4 v[2] = {};
-            if (w.values) {
+            if (values) {
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
-                    v[j] = *reinterpret_cast<const uint4*>(smem + kSmVT + (c & 1) * kTile + row * 128 + (((2 * part + j) ^ (row & 7)) << 4));
+                    v[j] = *reinterpret_cast<const uint4*>(smem + kSmVT + (nv & 1) * kTile + row * 128 + (((2 * part + j) ^ (row & 7)) << 4));
             }
             const uint32_t vw[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
 #pragma unroll
@@ -583,11 +708,11 @@ __device__ __forceinline__ bool make(const Walk& w, const DeltaParams& p, uint32
                 }
             }
         }
-        if (!wait(kXDone, c)) return false;
+        if (!wait(kXDone, n)) return false;
         tc_fence_after();
         {
             f2 x[8];
-            if (c > 0) was = of_row(c);
+            if (c > 0) was = of_row(n);
             load16(tm + kTmX + kToks * part, x);
             const bool dead = !finite(was);
             const int mine = clear - kToks * part;  // among this thread's tokens
@@ -616,14 +741,17 @@ __device__ __forceinline__ bool make(const Walk& w, const DeltaParams& p, uint32
                 }
             }
             store_split(tm + kTmR + kToks * part, x);
-            reinterpret_cast<volatile uint16_t*>(bad_of(c, row))[part] = (uint16_t)bad;
-            if (part == 0) inv_of(c)[row] = inv;
+            reinterpret_cast<volatile uint16_t*>(bad_of(n, row))[part] = (uint16_t)bad;
+            if (part == 0) inv_of(n)[row] = inv;
         }
         tmem_wait_st();
         arrive_warp(kRReady, lane);
-        if (w.values && lane == 0) mbar_arrive(bar(kVEmpty + (c & 1)));
+        if (values) {
+            if (lane == 0) mbar_arrive(bar(kVEmpty + (nv & 1)));
+            ++nv;
+        }
         // U
-        if (!wait(kUDone, c)) return false;
+        if (!wait(kUDone, n)) return false;
         tc_fence_after();
         {
             f2 x[8];
@@ -639,7 +767,7 @@ __device__ __forceinline__ bool make(const Walk& w, const DeltaParams& p, uint32
         tmem_wait_st();
         arrive_warp(kUReady, lane);
         // S
-        const bool more = c + 1 < w.chunks;
+        const bool more = c + 1 < chunks;
         decay *= sc->gamma;
         const f2 gamma = pack2(sc->gamma, sc->gamma), back = pack2(2.f * inv, 2.f * inv);
         if (clear < C) {
@@ -648,14 +776,14 @@ __device__ __forceinline__ bool make(const Walk& w, const DeltaParams& p, uint32
         }
         bool lost = false;
         {
-            const uint2 bad = make_uint2(bad_of(c, row)->x, bad_of(c, row)->y);
+            const uint2 bad = make_uint2(bad_of(n, row)->x, bad_of(n, row)->y);
             if (__any_sync(0xffffffffu, (bad.x | bad.y) != 0)) lost = poisoned(bad, make_uint2(sc->clears[0], sc->clears[1])).y >> 31;
         }
         if (more) {
-            if ((w.values && !wait(kTurned + ((c + 1) & 1), (c + 1) >> 1)) || !wait(kFull + ((c + 1) & 1), (c + 1) >> 1)) return false;
-            rescale(c + 1, adds);
+            if ((values && !wait(kTurned + (nv & 1), nv >> 1)) || !wait(kFull + ((n + 1) & 1), (n + 1) >> 1)) return false;
+            rescale(n + 1, nv, adds);
         }
-        if (!wait(kDDone, c)) return false;
+        if (!wait(kDDone, n)) return false;
         tc_fence_after();
         smax = 0.f;
         {
@@ -675,7 +803,7 @@ __device__ __forceinline__ bool make(const Walk& w, const DeltaParams& p, uint32
             for (int i = 0; i < kKeys / 2; ++i) s[i] = pack2(NAN, NAN);
         }
         if (more) {
-            smax_of(c + 1, part)[row] = smax;
+            smax_of(n + 1, part)[row] = smax;
             if (!strange) {
                 store_s(0, true);
                 tmem_wait_st();
@@ -701,55 +829,15 @@ __host__ __device__ constexpr int phi_at(int j, int k) { return j * D + (k ^ ((j
 template <class S>
 __global__ void __launch_bounds__(kThreads, 1)
 kda_delta_walk(const __grid_constant__ DeltaParams p, const __grid_constant__ CUtensorMap v_map,
-               const __grid_constant__ LinCuts cuts, bool local) {
-    if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    // the item: a long sequence, or a segment of one that is cut
-    Walk w;
-    w.h = blockIdx.x % p.H;
-    int i = blockIdx.x / p.H;
-    bool first = true, last = true;
-    int n, at = 0, plane = 0;
-    w.outputs = w.values = true;
-    if (local) {  // all segments but the last: from zero, and from the identity
-        w.values = (i & 1) == 0;
-        i >>= 1;
-    }
-    int r = 0;  // cut sequence r's segments after its first follow those of the ones before
-    if (i < p.n_seg - p.n_cut) {
-        while (i >= cuts.first[r + 1] - (r + 1)) ++r;
-        int g = i - (cuts.first[r] - r) + (local ? 0 : 1);
-        n = cuts.seq[r];
-        w.t0 = cuts.t0[r] + g * p.seg_len;
-        w.len = min(p.seg_len, cuts.len[r] - g * p.seg_len);
-        at = g * (p.seg_len / C);
-        first = g == 0;
-        last = g + 1 == cuts.first[r + 1] - cuts.first[r];
-        plane = ((cuts.first[r] + g) * p.H + w.h) * 2;
-        w.outputs = first || !local;
-    } else {
-        n = p.long_list[p.n_cut + i - (p.n_seg - p.n_cut)];
-        w.t0 = p.cu[n];
-        w.len = p.cu[n + 1] - w.t0;
-    }
-    w.chunks = (w.len + C - 1) / C;
-    w.step = (int64_t)p.H * kDeltaBlock;
-    w.blocks = p.blocks + (((int64_t)p.seq_off[n] + at) * p.H + w.h) * kDeltaBlock;
-    if (local && first && !w.values) return;  // its state is its sequence's
-    const int slot = p.idx[n];
-    S* const state = slot >= 0 && slot < p.num_slots
-                         ? static_cast<S*>(p.pool) + (size_t)slot * p.stride0 + (size_t)w.h * D * D : nullptr;
-    const bool init = first && state && p.has_init[n] != 0;
-    const float* const begins = first || local ? nullptr : p.planes + (size_t)(plane - 2 * p.H) * D * D;
+               const __grid_constant__ LinCuts cuts, bool local, int total) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint32_t* const base = reinterpret_cast<uint32_t*>(smem + kSmMisc + 8);
     if (threadIdx.x == 0) {
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
         for (int i = 0; i < kNumBars; ++i)
-            mbar_init(bar(i), i >= kVEmpty ? kMakers : i >= kOEmpty ? kWriters : i >= kTurned ? kTurners : 1);
+            mbar_init(bar(i), i >= kItemFree ? kMakers + kWriters + kTurners : i >= kItem ? 1 : i >= kVEmpty ? kMakers
+                              : i >= kOEmpty ? kWriters : i >= kTurned ? kTurners : 1);
         abort_flag() = 0;
-        End& end = *reinterpret_cast<End*>(smem + kSmEnd);
-        end.state = last && !local ? state : nullptr;
-        end.plane = local ? p.planes + (size_t)(plane + !w.values) * D * D : nullptr;
-        end.kept = w.values ? nullptr : p.kept + plane / 2;
         fence_mbar_init();
     }
     if (warp == kIssuer) tmem_alloc(base, kTmCols);
@@ -760,72 +848,76 @@ kda_delta_walk(const __grid_constant__ DeltaParams p, const __grid_constant__ CU
     // registers: 512 x 96 + 128 x 64 + 128 x 32 of the launch's 768 x 80
     if (warp < kMakers) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
-        f2 s[kKeys / 2];
-        bool cleared;
-        float decay;
-        if (begins) grid_dep_wait();
-        const bool done = make<S>(w, p, tm, warp, lane, init ? state : nullptr, begins, s, cleared, decay);
-        const End end = *reinterpret_cast<const End*>(smem + kSmEnd);
-        const int place = (32 * (warp & 3) + lane) * D + (warp >> 2) * kKeys;
-        if (done && end.plane && !end.kept) {
+        int n = 0, nv = 0;
+#pragma unroll 1
+        for (int k = 0; next_item(k, total); ++k) {
+            f2 s[kKeys / 2];
+            bool cleared;
+            float decay;
+            if (!make<S>(p, k, n, nv, tm, warp, lane, s, cleared, decay)) break;
+            S* const state = static_cast<S*>(ring(k).state);
+            float *const plane = ring(k).plane, *const kept = ring(k).kept;
+            const int place = (32 * (warp & 3) + lane) * D + (warp >> 2) * kKeys;
+            if (plane && !kept) {
 #pragma unroll
-            for (int j = 0; j < kKeys / 2; j += 2) {
-                const float2 a = unpack2(s[j]), b = unpack2(s[j + 1]);
-                *reinterpret_cast<float4*>(end.plane + place + 2 * j) = make_float4(a.x, a.y, b.x, b.y);
-            }
-        } else if (done && end.plane) {
-            // a transition, its entries at most the decay: for the chain as sums of two fp16
-            float undo;
-            const float up = scale_of(fminf(decay, 1.f), undo);
-            const int j = 32 * (warp & 3) + lane;
-#pragma unroll
-            for (int i = 0; i < kKeys; i += 4) {
-                uint32_t e[4];
-#pragma unroll
-                for (int u = 0; u < 4; u += 2) {
-                    const float2 a = unpack2(s[(i + u) / 2]);
-                    const float x = a.x * up, y = a.y * up;
-                    const __half2 hi = __floats2half2_rn(x, y);
-                    const float2 f = __half22float2(hi);
-                    const uint32_t h = reinterpret_cast<const uint32_t&>(hi), l = pack_half2(x - f.x, y - f.y);
-                    e[u] = __byte_perm(h, l, 0x5410);
-                    e[u + 1] = __byte_perm(h, l, 0x7632);
+                for (int j = 0; j < kKeys / 2; j += 2) {
+                    const float2 a = unpack2(s[j]), b = unpack2(s[j + 1]);
+                    *reinterpret_cast<float4*>(plane + place + 2 * j) = make_float4(a.x, a.y, b.x, b.y);
                 }
-                *reinterpret_cast<uint4*>(reinterpret_cast<uint32_t*>(end.plane) + phi_at(j, (warp >> 2) * kKeys + i)) =
-                    make_uint4(e[0], e[1], e[2], e[3]);
-            }
-            if (threadIdx.x == 0) *end.kept = cleared ? -1.f : undo;
-        } else if (done && end.state) {
-            constexpr int N = 16 / sizeof(S);
-            S* to = static_cast<S*>(end.state) + place;
+            } else if (plane) {
+                // a transition, its entries at most the decay: for the chain as sums of two fp16
+                float undo;
+                const float up = scale_of(fminf(decay, 1.f), undo);
+                const int j = 32 * (warp & 3) + lane;
 #pragma unroll
-            for (int i = 0; i < kKeys; i += N) {
-                float f[N];
+                for (int i = 0; i < kKeys; i += 4) {
+                    uint32_t e[4];
 #pragma unroll
-                for (int j = 0; j < N; j += 2) {
-                    const float2 y = unpack2(s[(i + j) / 2]);
-                    f[j] = y.x, f[j + 1] = y.y;
+                    for (int u = 0; u < 4; u += 2) {
+                        const float2 a = unpack2(s[(i + u) / 2]);
+                        const float x = a.x * up, y = a.y * up;
+                        const __half2 hi = __floats2half2_rn(x, y);
+                        const float2 f = __half22float2(hi);
+                        const uint32_t h = reinterpret_cast<const uint32_t&>(hi), l = pack_half2(x - f.x, y - f.y);
+                        e[u] = __byte_perm(h, l, 0x5410);
+                        e[u + 1] = __byte_perm(h, l, 0x7632);
+                    }
+                    *reinterpret_cast<uint4*>(reinterpret_cast<uint32_t*>(plane) + phi_at(j, (warp >> 2) * kKeys + i)) =
+                        make_uint4(e[0], e[1], e[2], e[3]);
                 }
-                rows::Piece<S, N> x;
-                x.set(f);
-                rows::store<S, N>(to + i, x);
+                if (threadIdx.x == 0) *kept = cleared ? -1.f : undo;
+            } else if (state) {
+                constexpr int N = 16 / sizeof(S);
+#pragma unroll
+                for (int i = 0; i < kKeys; i += N) {
+                    float f[N];
+#pragma unroll
+                    for (int j = 0; j < N; j += 2) {
+                        const float2 y = unpack2(s[(i + j) / 2]);
+                        f[j] = y.x, f[j + 1] = y.y;
+                    }
+                    rows::Piece<S, N> x;
+                    x.set(f);
+                    rows::store<S, N>(state + place + i, x);
+                }
             }
+            done_with(k, lane);
         }
         tc_fence_before();
         __syncthreads();
     } else if (warp < kIssuer) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-        if (w.outputs) write(w, p, tm, warp, lane);
+        write(p, total, tm, warp, lane);
         tc_fence_before();
         __syncthreads();
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 32;");
         if (warp == kIssuer) {
-            Issuer issuer{w, elect_one()};
+            Issuer<S> issuer{p, cuts, local, elect_one(), total};
             issuer.go(tm);
             issuer.finish();
-        } else if (w.values) {
-            Turner t{w, &v_map, warp - kIssuer - 1, lane};
+        } else {
+            Turner t{&v_map, total, warp - kIssuer - 1, lane};
             t.go();
             t.finish();
         }
@@ -1031,15 +1123,18 @@ cudaError_t launch(const DeltaParams& p, const LinCuts& cuts, const CUtensorMap&
         if (e != cudaSuccess) return e;
         if (dev < 32) configured |= 1u << dev;
     }
-    const int after = p.n_seg - p.n_cut;  // segments that are not their sequence's first
+    const auto walk = [&](bool local, int segments) {
+        const int items = segments * p.H, sms = num_sms();
+        return launch_after(kda_delta_walk<S>, dim3((unsigned)(items < sms ? items : sms)), kThreads, kSmemBytes, s, p, v_map, cuts,
+                            local, items);
+    };
     if (p.n_cut > 0) {
-        e = launch_after(kda_delta_walk<S>, dim3((unsigned)(2 * after * p.H)), kThreads, kSmemBytes, s, p, v_map, cuts, true);
+        e = walk(true, 2 * p.n_seg - 3 * p.n_cut);
         if (e == cudaSuccess)
             e = launch_after(kda_delta_chain, dim3((unsigned)(p.n_cut * p.H), D / kChainRows), kChainThreads, kChainSmem, s, p, cuts);
         if (e != cudaSuccess) return e;
     }
-    return launch_after(kda_delta_walk<S>, dim3((unsigned)((after + p.n_long - p.n_cut) * p.H)), kThreads, kSmemBytes, s, p, v_map,
-                        cuts, false);
+    return walk(false, p.n_seg - 2 * p.n_cut + p.n_long);
 }
 
 // How the longest sequences are cut, from the long sequences' lengths (longest first).  In
