@@ -109,12 +109,23 @@ __device__ __forceinline__ void mma_bf16(float* d, const uint32_t* a, uint32_t b
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// The fragments of rows r0 .. r0 + 15, columns c0 .. c0 + 15 of a swizzled tile of halves of
-// R rows: an A operand, or two B operands of eight rows each (r0 .. r0 + 7: a[0], a[2]).
-__device__ __forceinline__ void frag(uint32_t tile, int r0, int c0, int R, int lane, uint32_t (&a)[4]) {
-    const int r = r0 + (lane & 15), c = c0 + (lane >> 4) * 8;
-    ldsm_x4(tile + sw128_off(r, c, R), a[0], a[1], a[2], a[3]);
-}
+// A lane's places in 16 rows of a swizzled tile: its row's bytes, and its 16 bytes for each 16
+// of 64 columns.
+struct Lanes {
+    uint32_t row, x[4];
+    __device__ __forceinline__ explicit Lanes(int lane) : row((lane & 15) * 128) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = ((2 * i + (lane >> 4)) ^ (lane & 7)) << 4;
+    }
+    // Rows r0 .. r0 + 15 (r0 a multiple of 8), columns c0 .. c0 + 15 (of 16) of a tile.
+    __device__ __forceinline__ uint32_t at(uint32_t tile, int r0, int c0) const {
+        return tile + r0 * 128 + (c0 >> 6) * kTile + row + x[c0 >> 4 & 3];
+    }
+    // Its fragments: an A operand, or two B operands of eight rows each (the first: a[0], a[2]).
+    __device__ __forceinline__ void load(uint32_t tile, int r0, int c0, uint32_t (&a)[4]) const {
+        ldsm_x4(at(tile, r0, c0), a[0], a[1], a[2], a[3]);
+    }
+};
 
 // Four threads have a row, 32 values each: four pieces of eight.
 __device__ __forceinline__ void fetch(uint4 (&v)[4], const __nv_bfloat16* row, int part, bool live) {
@@ -144,32 +155,34 @@ __device__ __forceinline__ uint4 times(uint4 v, float f) {
 }
 
 // Two values as the sum of two fp16 each.
-__device__ __forceinline__ void put_split(uint8_t* hi_tile, int i, int j, f2 x) {
-    const uint32_t at = sw64_off(i, j), hi = half2_of(x);
+__device__ __forceinline__ void put_split(uint8_t* at, f2 x) {
+    const uint32_t hi = half2_of(x);
     const float2 f = __half22float2(reinterpret_cast<const __half2&>(hi));
-    *reinterpret_cast<uint32_t*>(hi_tile + at) = hi;
-    *reinterpret_cast<uint32_t*>(hi_tile + kTile + at) = half2_of(fma2(pack2(f.x, f.y), pack2(-1.f, -1.f), x));
+    *reinterpret_cast<uint32_t*>(at) = hi;
+    *reinterpret_cast<uint32_t*>(at + kTile) = half2_of(fma2(pack2(f.x, f.y), pack2(-1.f, -1.f), x));
 }
 // 16 rows from r0 and 8 columns from n0 of a b, over K from a's column ca and b's row rb on, all
 // of them sums of two fp16; into the tile `to` at row r1, column n1.
 template <int K>
-__device__ __forceinline__ void block_product(uint8_t* a, int r0, int ca, uint8_t* b, int rb, int n0, uint8_t* to, int r1, int n1,
-                                              int lane) {
+__device__ __forceinline__ void block_product(const Lanes& ln, uint8_t* a, int r0, int ca, uint8_t* b, int rb, int n0, uint8_t* to,
+                                              int r1, int n1, int lane) {
     float d[4] = {};
-    const uint32_t at = smem_u32(a), bt = smem_u32(b);
+    const uint32_t at = smem_u32(a);
+    const uint32_t bt = smem_u32(b) + (lane >> 4) * kTile + rb * 128 + ln.row + (((n0 >> 3) ^ (lane & 7)) << 4);
 #pragma unroll
     for (int ks = 0; ks < K; ks += 16) {
         uint32_t hi[4], lo[4], x[4];  // x: b's high part, then its low one
-        frag(at, r0, ca + ks, C, lane, hi);
-        frag(at + kTile, r0, ca + ks, C, lane, lo);
-        ldsm_x4_t(bt + (lane >> 4) * kTile + sw64_off(rb + ks + (lane & 15), n0), x[0], x[1], x[2], x[3]);
+        ln.load(at, r0, ca + ks, hi);
+        ln.load(at + kTile, r0, ca + ks, lo);
+        ldsm_x4_t(bt + ks * 128, x[0], x[1], x[2], x[3]);
         mma_f16(d, lo, x[0], x[1]);
         mma_f16(d, hi, x[2], x[3]);
         mma_f16(d, hi, x[0], x[1]);
     }
-    const int r = r1 + (lane >> 2), c = n1 + (lane & 3) * 2;
-    put_split(to, r, c, pack2(d[0], d[1]));
-    put_split(to, r + 8, c, pack2(d[2], d[3]));
+    const int r = lane >> 2;
+    uint8_t* const y = to + (r1 + r) * 128 + (((n1 >> 3) ^ r) << 4) + (lane & 3) * 4;
+    put_split(y, pack2(d[0], d[1]));
+    put_split(y + 8 * 128, pack2(d[2], d[3]));
 }
 
 __global__ void __launch_bounds__(kThreads, 4) kda_delta_chunk(const __grid_constant__ DeltaParams p) {
@@ -178,6 +191,7 @@ __global__ void __launch_bounds__(kThreads, 4) kda_delta_chunk(const __grid_cons
     uint8_t *const tt = smem + kSmQ, *const nt = smem + kSmK;
     Vecs& vec = *reinterpret_cast<Vecs*>(smem + kSmVec);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const Lanes ln(lane);
     const int64_t chunk = blockIdx.x / p.H;
     const int h = blockIdx.x % p.H;
     if (tid == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -196,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, 4) kda_delta_chunk(const __grid_cons
         // (rows past the sequence's end are another's: cleared once its end is there)
         fetch(k, p.k + t * p.k_st + (int64_t)(h / p.rep) * p.k_sh, part, t < p.T);
         fetch(q, p.q + t * p.q_st + (int64_t)(h / p.rep) * p.q_sh, part, t < p.T);
-        if (tid < len) {
+        if (tid < C && t0 + tid < p.T) {
             g = p.g[(int64_t)(t0 + tid) * p.g_st + h];
             beta = p.beta[(int64_t)(t0 + tid) * p.H + h];
         }
@@ -204,17 +218,22 @@ __global__ void __launch_bounds__(kThreads, 4) kda_delta_chunk(const __grid_cons
 #pragma unroll
             for (int i = 0; i < 4; ++i) k[i] = q[i] = make_uint4(0, 0, 0, 0);
         }
+        if (tid >= len) g = beta = 0.f;
         const float kk = squares(k);
         const bool fine = kk < INFINITY;
         // 2^-e with |k| <= 2^e < 2 |k| or so; values of the smallest exponents stay smaller
         const int e = ((int)(__float_as_uint(kk) >> 23) - 127 + 2) >> 1;
         const float down = __uint_as_float((uint32_t)(127 - e) << 23), one = 1.f / sqrtf(kk + 1e-6f);
+        // (a row with infinities or NaN counts as zero, but for its own factor c)
+        if (!fine) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) k[i] = make_uint4(0, 0, 0, 0);
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const uint32_t at = sw128_off(r, (4 * i + part) * 8, C);
-            // (a row with infinities or NaN counts as zero, but for its own factor c)
-            *reinterpret_cast<uint4*>(smem + kSmK + at) = fine ? k[i] : make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4*>(blk + kDeltaK + at) = fine ? times(k[i], down) : make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(smem + kSmK + at) = k[i];
+            *reinterpret_cast<uint4*>(blk + kDeltaK + at) = times(k[i], down);
             *reinterpret_cast<uint4*>(smem + kSmQ + at) = q[i];
         }
         const float qq = squares(q);
@@ -249,26 +268,22 @@ __global__ void __launch_bounds__(kThreads, 4) kda_delta_chunk(const __grid_cons
     }
     __syncthreads();
     // e^{G_i - G_j} on the diagonal: row j, column i - its block's first
-    {
-        const int j = r, o = j & ~(B - 1), i0 = 4 * part;
+    if (tid >= C && tid < 2 * C) {
+        const int j = tid - C, o = j & ~(B - 1);
         float sum = 0.f;
-        for (int m = 0; m < i0; m += 4) {
-            const float4 a = *reinterpret_cast<const float4*>(vec.a + o + m);
-            sum += o + m > j ? a.x : 0.f;
-            sum += o + m + 1 > j ? a.y : 0.f;
-            sum += o + m + 2 > j ? a.z : 0.f;
-            sum += o + m + 3 > j ? a.w : 0.f;
-        }
-        const float4 a = *reinterpret_cast<const float4*>(vec.a + o + i0);
-        const float aa[4] = {a.x, a.y, a.z, a.w};
-        float x[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int i = o + i0 + u;
-            sum += i > j ? aa[u] : 0.f;
-            x[u] = i >= j ? ex2(sum) : 0.f;
+        for (int i0 = 0; i0 < B; i0 += 4) {
+            const float4 a = *reinterpret_cast<const float4*>(vec.a + o + i0);
+            const float aa[4] = {a.x, a.y, a.z, a.w};
+            float x[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int i = i0 + u;
+                sum += o + i > j ? aa[u] : 0.f;
+                x[u] = o + i >= j ? ex2(sum) : 0.f;
+            }
+            *reinterpret_cast<float4*>(e32 + j * kLdE + i0) = make_float4(x[0], x[1], x[2], x[3]);
         }
-        *reinterpret_cast<float4*>(e32 + j * kLdE + i0) = make_float4(x[0], x[1], x[2], x[3]);
     }
     if (tid < C) {
         constexpr float kLog2e = 1.4426950408889634f;
@@ -324,12 +339,12 @@ __global__ void __launch_bounds__(kThreads, 4) kda_delta_chunk(const __grid_cons
 #pragma unroll
             for (int ks = 0; ks < D; ks += 16) {
                 uint32_t a[4], qa[4], b[4];
-                frag(kt, r0, ks, C, lane, a);
-                frag(qt, r0, ks, C, lane, qa);
+                ln.load(kt, r0, ks, a);
+                ln.load(qt, r0, ks, qa);
 #pragma unroll
                 for (int t = 0; t < 4; t += 2) {
                     if (c0 + 8 * t > r0) continue;
-                    frag(kt, c0 + 8 * t, ks, C, lane, b);
+                    ln.load(kt, c0 + 8 * t, ks, b);
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
                         mma_bf16(kk[t + u], a, b[u], b[2 + u]);
@@ -350,35 +365,33 @@ __global__ void __launch_bounds__(kThreads, 4) kda_delta_chunk(const __grid_cons
                     for (int u = 0; u < 2; ++u) e[t][half][u] = e32[(r0 + 8 * t + cj + u) * kLdE + 8 * half + ri];
         }
         __syncthreads();
+        uint32_t y[4];  // in a row of a tile
+#pragma unroll
+        for (int t = 0; t < 4; ++t) y[t] = (((c0 >> 3) + t) ^ ri) << 4 | cj * 2;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             const int i = r0 + half * 8 + ri;
             const float b = vec.bk[i], cq = vec.cq[i];
+            const f2 bb = pack2(b, b), cc = pack2(cq, cq);
+            uint8_t *const nrow = nt + i * 128, *const prow = smem + kSmP + i * 128;
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 const int j = c0 + t * 8 + cj, bj = (c0 + t * 8) / B;
-                float nv[2] = {}, pv[2] = {};
+                uint32_t pv = 0;
                 if (bj < bi) {
                     const float f = vec.f[bj][i];
-                    const float2 rk = *reinterpret_cast<const float2*>(vec.rk + j);
-                    const float l[2] = {f * rk.x, f * rk.y};
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) nv[u] = b * l[u] * kk[t][2 * half + u], pv[u] = cq * l[u] * qk[t][2 * half + u];
+                    const f2 l = mul2(pack2(f, f), *reinterpret_cast<const f2*>(vec.rk + j));
+                    put_split(nrow + y[t], mul2(mul2(bb, l), pack2(kk[t][2 * half], kk[t][2 * half + 1])));
+                    pv = half2_of(mul2(mul2(cc, l), pack2(qk[t][2 * half], qk[t][2 * half + 1])));
                 } else if (bj == bi) {
-                    const float2 ck = *reinterpret_cast<const float2*>(vec.ck + j);
-                    const float l[2] = {e[t & 1][half][0] * ck.x, e[t & 1][half][1] * ck.y};
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        nv[u] = j + u < i ? b * l[u] * kk[t][2 * half + u] : 0.f;
-                        pv[u] = j + u <= i ? cq * l[u] * qk[t][2 * half + u] : 0.f;
-                    }
+                    const f2 l = mul2(pack2(e[t & 1][half][0], e[t & 1][half][1]), *reinterpret_cast<const f2*>(vec.ck + j));
+                    const float2 nv = unpack2(mul2(mul2(bb, l), pack2(kk[t][2 * half], kk[t][2 * half + 1])));
+                    const float2 q = unpack2(mul2(mul2(cc, l), pack2(qk[t][2 * half], qk[t][2 * half + 1])));
+                    e32[j * kLdE + i - r0] = j < i ? nv.x : 0.f;
+                    e32[(j + 1) * kLdE + i - r0] = j + 1 < i ? nv.y : 0.f;
+                    pv = pack_half2(j <= i ? q.x : 0.f, j + 1 <= i ? q.y : 0.f);
                 }
-                if (bj < bi) put_split(nt, i, j, pack2(nv[0], nv[1]));
-                if (bj == bi) {
-                    e32[j * kLdE + i - r0] = nv[0];
-                    e32[(j + 1) * kLdE + i - r0] = nv[1];
-                }
-                *reinterpret_cast<uint32_t*>(smem + kSmP + sw64_off(i, j)) = pack_half2(pv[0], pv[1]);
+                *reinterpret_cast<uint32_t*>(prow + y[t]) = pv;
             }
         }
         // T is zero right of its diagonal blocks
@@ -390,10 +403,10 @@ __global__ void __launch_bounds__(kThreads, 4) kda_delta_chunk(const __grid_cons
         }
     }
     __syncthreads();
-    // the diagonal blocks of T: a lane has a column; once row m is known its multiples go to
-    // the rows below.  Half a warp keeps the high parts, the other the low ones.
-    if (warp < 4) {
-        const int o = warp * B, col = lane & 15;
+    // the diagonal blocks of T, two a warp: a lane has a column; once row m is known its
+    // multiples go to the rows below
+    if (warp < 2) {
+        const int o = (2 * warp + (lane >> 4)) * B, col = lane & 15;
         float t[B];
 #pragma unroll
         for (int i = 0; i < B; ++i) t[i] = i == col ? 1.f : 0.f;
@@ -408,28 +421,31 @@ __global__ void __launch_bounds__(kThreads, 4) kda_delta_chunk(const __grid_cons
                 if (i + 3 > m) t[i + 3] = fmaf(x.w, t[m], t[i + 3]);
             }
         }
+        const uint32_t piece = (o >> 3) + (col >> 3);
+        uint8_t* const to = tt + o * 128 + (col & 7) * 2;
 #pragma unroll
         for (int i = 0; i < B; ++i) {
             const __half hi = __float2half_rn(t[i]);
-            *reinterpret_cast<__half*>(tt + (lane >> 4) * kTile + sw64_off(o + i, o + col)) =
-                lane < B ? hi : __float2half_rn(t[i] - __half2float(hi));
+            uint8_t* const at = to + i * 128 + ((piece ^ (i & 7)) << 4);
+            *reinterpret_cast<__half*>(at) = hi;
+            *reinterpret_cast<__half*>(at + kTile) = __float2half_rn(t[i] - __half2float(hi));
         }
     }
     __syncthreads();
     // blocks of 32: Y = N21 T11, then T21 = T22 Y
     {
         const int o = (warp >> 1 & 1) * 32, n = (warp & 1) * 8;
-        if (warp < 4) block_product<B>(nt, o + B, o, tt, o, o + n, nt, o, o + B + n, lane);
+        if (warp < 4) block_product<B>(ln, nt, o + B, o, tt, o, o + n, nt, o, o + B + n, lane);
         __syncthreads();
-        if (warp < 4) block_product<B>(tt, o + B, o + B, nt, o, o + B + n, tt, o + B, o + n, lane);
+        if (warp < 4) block_product<B>(ln, tt, o + B, o + B, nt, o, o + B + n, tt, o + B, o + n, lane);
     }
     __syncthreads();
     // and of 64
     {
         const int o = (warp >> 2) * B, n = (warp & 3) * 8;
-        block_product<32>(nt, 32 + o, 0, tt, 0, n, nt, o, 32 + n, lane);
+        block_product<32>(ln, nt, 32 + o, 0, tt, 0, n, nt, o, 32 + n, lane);
         __syncthreads();
-        block_product<32>(tt, 32 + o, 32, nt, 0, 32 + n, tt, 32 + o, n, lane);
+        block_product<32>(ln, tt, 32 + o, 32, nt, 0, 32 + n, tt, 32 + o, n, lane);
     }
     fence_proxy_async();
     __syncthreads();
@@ -446,12 +462,11 @@ __global__ void __launch_bounds__(kThreads, 4) kda_delta_chunk(const __grid_cons
             for (int ks = 0; ks < C; ks += 16) {
                 if (ks < r0 + 16 && ks + 16 > c0) {
                     uint32_t a[4], b[4];
-                    frag(pt, r0, ks, C, lane, a);
+                    ln.load(pt, r0, ks, a);
 #pragma unroll
                     for (int t = 0; t < 4; t += 2) {
                         // rows ks .. ks + 15 of T, columns c0 + 8 t .. + 15, transposed
-                        const int tr = ks + (lane & 15), tc = c0 + 8 * t + (lane >> 4) * 8;
-                        ldsm_x4_t(th + sw64_off(tr, tc), b[0], b[1], b[2], b[3]);
+                        ldsm_x4_t(ln.at(th, ks, c0 + 8 * t), b[0], b[1], b[2], b[3]);
                         mma_f16(d[t], a, b[0], b[1]);
                         mma_f16(d[t + 1], a, b[2], b[3]);
                     }
@@ -461,13 +476,12 @@ __global__ void __launch_bounds__(kThreads, 4) kda_delta_chunk(const __grid_cons
         __syncthreads();
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-            const int i = r0 + half * 8 + (lane >> 2);
+            const int ri = lane >> 2, i = r0 + half * 8 + ri;
             const float up = vec.up[i];
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                const int j = c0 + t * 8 + (lane & 3) * 2;
-                *reinterpret_cast<uint32_t*>(smem + kSmP + sw64_off(i, j)) = pack_half2(up * d[t][2 * half], up * d[t][2 * half + 1]);
-            }
+            for (int t = 0; t < 4; ++t)
+                *reinterpret_cast<uint32_t*>(smem + kSmP + i * 128 + ((((c0 >> 3) + t) ^ ri) << 4) + (lane & 3) * 4) =
+                    pack_half2(up * d[t][2 * half], up * d[t][2 * half + 1]);
         }
     }
     fence_proxy_async();
