@@ -95,7 +95,8 @@ struct Item {
     float* kept;           // what a transition is to be multiplied by, or nullptr
 };
 constexpr int kSmItem = kSmMisc + 16;
-constexpr int kSmemBytes = kSmItem + 2 * (int)sizeof(Item);
+constexpr int kSmStage = (kSmItem + 2 * (int)sizeof(Item) + 127) / 128 * 128;  // [16][32][64 bytes] for each maker warp
+constexpr int kSmemBytes = kSmStage + kMakers * 2048;
 static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
 static_assert(kDeltaBlock % 1024 == 0 && kDeltaK % 1024 == 0 && kSmV % 1024 == 0 && kSmVT % 1024 == 0 && kSmBar % 8 == 0, "alignment");
 
@@ -604,6 +605,68 @@ __device__ __forceinline__ bool write(const DeltaParams& p, int total, uint32_t 
     return true;
 }
 
+// Where a segment's state has an entry: a thread's 32 keys by fours, those of all threads beside
+// each other.
+__host__ __device__ constexpr int state_at(int row, int key) { return ((key % kKeys / 4) * 4 * D + key / kKeys * D + row) * 4 + key % 4; }
+// And a transition: row j's fours in another order, so that the chain's fragments, of eight
+// columns and rows two apart, lie in different banks.
+__host__ __device__ constexpr int phi_at(int j, int k) { return state_at(j ^ (k / 4 & 1), k); }
+
+// 32 rows' keys of a warp between its threads, a row each, and the pool: 64 bytes of a row by
+// four lanes (by threads, an access has 32 lines: 2 us each way).
+__device__ __forceinline__ uint8_t* staged(int warp, int row, int piece) {
+    return smem + kSmStage + warp * 2048 + row * 64 + ((piece ^ (row >> 1 & 3)) << 4);
+}
+template <class S>
+__device__ __forceinline__ void load_state(const S* from, int warp, int lane, f2 (&s)[kKeys / 2]) {
+    constexpr int N = 16 / sizeof(S), H = 4 * N;  // values of a piece, of 64 bytes
+    from += (32 * (warp & 3) + (lane >> 2)) * D + (warp >> 2) * kKeys + (lane & 3) * N;
+    uint4 x[kKeys / H][4];
+#pragma unroll
+    for (int b = 0; b < kKeys / H; ++b)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[b][i] = *reinterpret_cast<const uint4*>(from + 8 * i * D + b * H);
+#pragma unroll
+    for (int b = 0; b < kKeys / H; ++b) {
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(staged(warp, 8 * i + (lane >> 2), lane & 3)) = x[b][i];
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float f[N];
+            rows::load<S, N>(reinterpret_cast<const S*>(staged(warp, lane, i))).get(f);
+#pragma unroll
+            for (int j = 0; j < N; j += 2) s[(b * H + i * N + j) / 2] = pack2(f[j], f[j + 1]);
+        }
+    }
+}
+template <class S>
+__device__ __forceinline__ void store_state(S* to, int warp, int lane, const f2 (&s)[kKeys / 2]) {
+    constexpr int N = 16 / sizeof(S), H = 4 * N;
+    to += (32 * (warp & 3) + (lane >> 2)) * D + (warp >> 2) * kKeys + (lane & 3) * N;
+#pragma unroll
+    for (int b = 0; b < kKeys / H; ++b) {
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float f[N];
+#pragma unroll
+            for (int j = 0; j < N; j += 2) {
+                const float2 y = unpack2(s[(b * H + i * N + j) / 2]);
+                f[j] = y.x, f[j + 1] = y.y;
+            }
+            rows::Piece<S, N> x;
+            x.set(f);
+            rows::store<S, N>(reinterpret_cast<S*>(staged(warp, lane, i)), x);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<uint4*>(to + 8 * i * D + b * H) = *reinterpret_cast<const uint4*>(staged(warp, 8 * i + (lane >> 2), lane & 3));
+    }
+}
+
 // Warps 0-15: a thread has a quarter of value row `row`: 32 keys, 16 of a chunk's tokens.
 // Walks an item, the CTA's chunks n on and its chunks with values nv on, and leaves the state
 // in s, whether a token cleared it and the decay over all.
@@ -614,25 +677,17 @@ __device__ __forceinline__ bool make(const DeltaParams& p, int k, int& n, int& n
     const bool values = ring(k).values;
     const int part = warp >> 2, row = 32 * (warp & 3) + lane;
     const uint32_t tm = base + ((uint32_t)(32 * (warp & 3)) << 16);
-    const int at = row * D + part * kKeys;
-    constexpr int N = 16 / sizeof(S);
 #pragma unroll
     for (int i = 0; i < kKeys / 2; ++i) s[i] = 0;
     const S* const from = static_cast<const S*>(ring(k).from);
     const float* const begins = ring(k).begins;
     if (from) {
-#pragma unroll
-        for (int i = 0; i < kKeys; i += N) {
-            float f[N];
-            rows::load<S, N>(from + at + i).get(f);
-#pragma unroll
-            for (int j = 0; j < N; j += 2) s[(i + j) / 2] = pack2(f[j], f[j + 1]);
-        }
+        load_state(from, warp, lane, s);
     } else if (begins) {
         grid_dep_wait();
 #pragma unroll
         for (int i = 0; i < kKeys; i += 4) {
-            const float4 f = *reinterpret_cast<const float4*>(begins + at + i);
+            const float4 f = *reinterpret_cast<const float4*>(begins + state_at(row, part * kKeys + i));
             s[i / 2] = pack2(f.x, f.y), s[i / 2 + 1] = pack2(f.z, f.w);
         }
     } else if (!values) {
@@ -822,10 +877,6 @@ __device__ __forceinline__ bool make(const DeltaParams& p, int k, int& n, int& n
     return true;
 }
 
-// An entry of a transition's plane: row j's columns by eights in another order for every two
-// rows, so that a fragment's rows lie in different banks.
-__host__ __device__ constexpr int phi_at(int j, int k) { return j * D + (k ^ ((j >> 1 & 3) * 8)); }
-
 template <class S>
 __global__ void __launch_bounds__(kThreads, 1)
 kda_delta_walk(const __grid_constant__ DeltaParams p, const __grid_constant__ CUtensorMap v_map,
@@ -857,18 +908,17 @@ kda_delta_walk(const __grid_constant__ DeltaParams p, const __grid_constant__ CU
             if (!make<S>(p, k, n, nv, tm, warp, lane, s, cleared, decay)) break;
             S* const state = static_cast<S*>(ring(k).state);
             float *const plane = ring(k).plane, *const kept = ring(k).kept;
-            const int place = (32 * (warp & 3) + lane) * D + (warp >> 2) * kKeys;
+            const int row = 32 * (warp & 3) + lane, keys = (warp >> 2) * kKeys;
             if (plane && !kept) {
 #pragma unroll
                 for (int j = 0; j < kKeys / 2; j += 2) {
                     const float2 a = unpack2(s[j]), b = unpack2(s[j + 1]);
-                    *reinterpret_cast<float4*>(plane + place + 2 * j) = make_float4(a.x, a.y, b.x, b.y);
+                    *reinterpret_cast<float4*>(plane + state_at(row, keys + 2 * j)) = make_float4(a.x, a.y, b.x, b.y);
                 }
             } else if (plane) {
                 // a transition, its entries at most the decay: for the chain as sums of two fp16
                 float undo;
                 const float up = scale_of(fminf(decay, 1.f), undo);
-                const int j = 32 * (warp & 3) + lane;
 #pragma unroll
                 for (int i = 0; i < kKeys; i += 4) {
                     uint32_t e[4];
@@ -882,24 +932,12 @@ kda_delta_walk(const __grid_constant__ DeltaParams p, const __grid_constant__ CU
                         e[u] = __byte_perm(h, l, 0x5410);
                         e[u + 1] = __byte_perm(h, l, 0x7632);
                     }
-                    *reinterpret_cast<uint4*>(reinterpret_cast<uint32_t*>(plane) + phi_at(j, (warp >> 2) * kKeys + i)) =
+                    *reinterpret_cast<uint4*>(reinterpret_cast<uint32_t*>(plane) + phi_at(row, keys + i)) =
                         make_uint4(e[0], e[1], e[2], e[3]);
                 }
                 if (threadIdx.x == 0) *kept = cleared ? -1.f : undo;
             } else if (state) {
-                constexpr int N = 16 / sizeof(S);
-#pragma unroll
-                for (int i = 0; i < kKeys; i += N) {
-                    float f[N];
-#pragma unroll
-                    for (int j = 0; j < N; j += 2) {
-                        const float2 y = unpack2(s[(i + j) / 2]);
-                        f[j] = y.x, f[j + 1] = y.y;
-                    }
-                    rows::Piece<S, N> x;
-                    x.set(f);
-                    rows::store<S, N>(state + place + i, x);
-                }
+                store_state(state, warp, lane, s);
             }
             done_with(k, lane);
         }
@@ -973,7 +1011,7 @@ kda_delta_chain(const __grid_constant__ DeltaParams p, const __grid_constant__ L
     }
     // a thread has rows `row` and row + 8 at keys col, col + 1, col + 8, col + 9: s[8's][row][key]
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = lane >> 2, col = warp * 16 + (lane & 3) * 2;
-    const size_t at = (size_t)(row0 + row) * D + col;
+    auto at = [&](int t, int u) { return state_at(row0 + row + 8 * u, col + 8 * t); };
     float2 s[2][2], next[2][2];
     float kept = 0.f, scale[2], inv[2];
     auto fetch_n = [&](int g) {
@@ -981,7 +1019,7 @@ kda_delta_chain(const __grid_constant__ DeltaParams p, const __grid_constant__ L
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int u = 0; u < 2; ++u) next[t][u] = *reinterpret_cast<const float2*>(plane(g) + at + 8 * u * D + 8 * t);
+            for (int u = 0; u < 2; ++u) next[t][u] = *reinterpret_cast<const float2*>(plane(g) + at(t, u));
         kept = p.kept[(size_t)(first + g) * p.H + h];
     };
     // S's rows' scales and operand; all have the state of a step behind them
@@ -1014,7 +1052,7 @@ kda_delta_chain(const __grid_constant__ DeltaParams p, const __grid_constant__ L
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int u = 0; u < 2; ++u) s[t][u] = *reinterpret_cast<const float2*>(plane(0) + at + 8 * u * D + 8 * t);
+        for (int u = 0; u < 2; ++u) s[t][u] = *reinterpret_cast<const float2*>(plane(0) + at(t, u));
     fetch_n(1);
     keep();
     for (int g = 1; g <= steps; ++g) {
@@ -1060,7 +1098,7 @@ kda_delta_chain(const __grid_constant__ DeltaParams p, const __grid_constant__ L
                 float2 y = next[t][u];
                 if (kept >= 0.f) y.x = fmaf(d[t][2 * u], back, y.x), y.y = fmaf(d[t][2 * u + 1], back, y.y);
                 s[t][u] = y;
-                *reinterpret_cast<float2*>(plane(g) + at + 8 * u * D + 8 * t) = y;
+                *reinterpret_cast<float2*>(plane(g) + at(t, u)) = y;
             }
         fetch_n(g + 1);
         keep();  // (its barrier: all are done with the operand and the transition)
