@@ -48,7 +48,7 @@ constexpr int kSmK = 0;                   // k; then N below the diagonal blocks
 constexpr int kSmQ = kSmK + C * D * 2;    // q; then T, high and low part
 constexpr int kSmP = kSmQ + C * D * 2;    // P; then P T
 constexpr int kSmE = kSmP + kTile;        // blocks on the diagonal, transposed: e^{G_i - G_j}; then N
-constexpr int kSmVec = kSmE + C * kLdE * 4;
+constexpr int kSmVec = kSmE + (C * kLdE + 4 * C / B) * 4;
 struct Vecs {
     float a[C];       // decays in log2
     float ck[C];      // what makes k's length one (0 if k is not finite)
@@ -127,26 +127,39 @@ struct Lanes {
     }
 };
 
-// Four threads have a row, 32 values each: four pieces of eight.
-__device__ __forceinline__ void fetch(uint4 (&v)[4], const __nv_bfloat16* row, int part, bool live) {
+// Row j of the fp32 blocks: two blocks' same rows in different banks.
+__device__ __forceinline__ int e_at(int j) { return j * kLdE + j / B * 4; }
+
+// Eight threads have two rows, four apart: of each two pieces of eight values, v[2 row + half].
+// (With four threads a row every access is of half lines.)
+__device__ __forceinline__ void fetch(uint4 (&v)[4], const __nv_bfloat16* from, int64_t st, int64_t rows) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = live ? __ldg(reinterpret_cast<const uint4*>(row + (4 * i + part) * 8)) : make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < 4; ++i)
+        v[i] = 4 * (i >> 1) < rows ? __ldg(reinterpret_cast<const uint4*>(from + 4 * (i >> 1) * st + 64 * (i & 1))) : make_uint4(0, 0, 0, 0);
 }
 __device__ __forceinline__ f2 pair(uint32_t w) { return pack2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)); }
-// The row's sum of squares.
-__device__ __forceinline__ float squares(const uint4 (&v)[4]) {
-    f2 s = 0;
+// A row's sum of squares: the first one's in even lanes, the second one's in odd ones.
+__device__ __forceinline__ float squares(const uint4 (&v)[4], int lane) {
+    float sum[2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+    for (int r = 0; r < 2; ++r) {
+        f2 s = 0;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s = fma2(pair(w[j]), pair(w[j]), s);
+        for (int i = 2 * r; i < 2 * r + 2; ++i) {
+            const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s = fma2(pair(w[j]), pair(w[j]), s);
+        }
+        const float2 t = unpack2(s);
+        sum[r] = t.x + t.y;
     }
-    const float2 t = unpack2(s);
-    float sum = t.x + t.y;
-    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-    return sum + __shfl_xor_sync(0xffffffffu, sum, 2);
+    const bool odd = lane & 1;
+    float x = (odd ? sum[1] : sum[0]) + __shfl_xor_sync(0xffffffffu, odd ? sum[0] : sum[1], 1);
+    x += __shfl_xor_sync(0xffffffffu, x, 2);
+    return x + __shfl_xor_sync(0xffffffffu, x, 4);
 }
+// e with |k| <= 2^e < 2 |k| or so, from k's square.
+__device__ __forceinline__ int length_of(float kk) { return ((int)(__float_as_uint(kk) >> 23) - 127 + 2) >> 1; }
 // Eight values times f, as fp16.
 __device__ __forceinline__ uint4 times(uint4 v, float f) {
     const f2 ff = pack2(f, f);
@@ -200,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, 4) kda_delta_chunk(const __grid_cons
     const int len = min(C, p.cu[n + 1] - t0);
     uint8_t* const blk = p.blocks + (chunk * p.H + h) * (int64_t)kDeltaBlock;
     DeltaScalars* const scal = reinterpret_cast<DeltaScalars*>(blk);
-    const int r = tid >> 2, part = tid & 3;  // of a row
+    const int r = warp * 8 + (lane >> 3), col = (lane & 7) * 8;  // of this thread's first piece
 
     uint4 q[4];
     float g = 0.f, beta = 0.f;
@@ -208,39 +221,37 @@ __global__ void __launch_bounds__(kThreads, 4) kda_delta_chunk(const __grid_cons
         const int64_t t = t0 + r;
         uint4 k[4];
         // (rows past the sequence's end are another's: cleared once its end is there)
-        fetch(k, p.k + t * p.k_st + (int64_t)(h / p.rep) * p.k_sh, part, t < p.T);
-        fetch(q, p.q + t * p.q_st + (int64_t)(h / p.rep) * p.q_sh, part, t < p.T);
+        fetch(k, p.k + t * p.k_st + (int64_t)(h / p.rep) * p.k_sh + col, p.k_st, p.T - t);
+        fetch(q, p.q + t * p.q_st + (int64_t)(h / p.rep) * p.q_sh + col, p.q_st, p.T - t);
         if (tid < C && t0 + tid < p.T) {
             g = p.g[(int64_t)(t0 + tid) * p.g_st + h];
             beta = p.beta[(int64_t)(t0 + tid) * p.H + h];
         }
-        if (r >= len) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) k[i] = q[i] = make_uint4(0, 0, 0, 0);
-        }
+        for (int i = 0; i < 4; ++i)
+            if (r + 4 * (i >> 1) >= len) k[i] = q[i] = make_uint4(0, 0, 0, 0);
         if (tid >= len) g = beta = 0.f;
-        const float kk = squares(k);
-        const bool fine = kk < INFINITY;
-        // 2^-e with |k| <= 2^e < 2 |k| or so; values of the smallest exponents stay smaller
-        const int e = ((int)(__float_as_uint(kk) >> 23) - 127 + 2) >> 1;
-        const float down = __uint_as_float((uint32_t)(127 - e) << 23), one = 1.f / sqrtf(kk + 1e-6f);
-        // (a row with infinities or NaN counts as zero, but for its own factor c)
-        if (!fine) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) k[i] = make_uint4(0, 0, 0, 0);
-        }
+        const float mine = squares(k, lane), other = __shfl_xor_sync(0xffffffffu, mine, 1);
+        const float kk[2] = {lane & 1 ? other : mine, lane & 1 ? mine : other};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const uint32_t at = sw128_off(r, (4 * i + part) * 8, C);
+            // (a row with infinities or NaN counts as zero, but for its own factor c; values of
+            // the smallest exponents stay smaller)
+            const float x = kk[i >> 1], down = __uint_as_float((uint32_t)(127 - length_of(x)) << 23);
+            if (!(x < INFINITY)) k[i] = make_uint4(0, 0, 0, 0);
+            const uint32_t at = sw128_off(r + 4 * (i >> 1), col + 64 * (i & 1), C);
             *reinterpret_cast<uint4*>(smem + kSmK + at) = k[i];
-            *reinterpret_cast<uint4*>(blk + kDeltaK + at) = times(k[i], down);
+            *reinterpret_cast<uint4*>(blk + kDeltaK + at) = x < INFINITY ? times(k[i], down) : make_uint4(0, 0, 0, 0);
             *reinterpret_cast<uint4*>(smem + kSmQ + at) = q[i];
         }
-        const float qq = squares(q);
-        if (part == 0) {
-            vec.ck[r] = fine ? one : 0.f;
-            vec.ks[r] = fine ? one * __uint_as_float((uint32_t)(127 + e) << 23) : NAN;
-            vec.cq[r] = 1.f / sqrtf(qq + 1e-6f);
+        const float qq = squares(q, lane);
+        if (col < 16) {
+            const int row = r + 4 * (lane & 1);
+            const bool fine = mine < INFINITY;
+            const float one = 1.f / sqrtf(mine + 1e-6f);
+            vec.ck[row] = fine ? one : 0.f;
+            vec.ks[row] = fine ? one * __uint_as_float((uint32_t)(127 + length_of(mine)) << 23) : NAN;
+            vec.cq[row] = 1.f / sqrtf(qq + 1e-6f);
         }
     }
     // sums of decays within the block, up to the token and behind it
@@ -282,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 4) kda_delta_chunk(const __grid_cons
                 sum += o + i > j ? aa[u] : 0.f;
                 x[u] = o + i >= j ? ex2(sum) : 0.f;
             }
-            *reinterpret_cast<float4*>(e32 + j * kLdE + i0) = make_float4(x[0], x[1], x[2], x[3]);
+            *reinterpret_cast<float4*>(e32 + e_at(j) + i0) = make_float4(x[0], x[1], x[2], x[3]);
         }
     }
     if (tid < C) {
@@ -324,10 +335,10 @@ __global__ void __launch_bounds__(kThreads, 4) kda_delta_chunk(const __grid_cons
     __syncthreads();
     // q^ e^G
     {
-        const float f = vec.cq[r] * vec.eg[r];
+        const float f[2] = {vec.cq[r] * vec.eg[r], vec.cq[r + 4] * vec.eg[r + 4]};
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<uint4*>(blk + kDeltaQ + sw128_off(r, (4 * i + part) * 8, C)) = times(q[i], f);
+            *reinterpret_cast<uint4*>(blk + kDeltaQ + sw128_off(r + 4 * (i >> 1), col + 64 * (i & 1), C)) = times(q[i], f[i >> 1]);
     }
     // scores: 16 rows x 32 columns a warp
     const int bi = warp & 3, r0 = bi * B, c0 = (warp >> 2) * 32;
@@ -362,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 4) kda_delta_chunk(const __grid_cons
 #pragma unroll
                 for (int half = 0; half < 2; ++half)
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) e[t][half][u] = e32[(r0 + 8 * t + cj + u) * kLdE + 8 * half + ri];
+                    for (int u = 0; u < 2; ++u) e[t][half][u] = e32[e_at(r0 + 8 * t + cj + u) + 8 * half + ri];
         }
         __syncthreads();
         uint32_t y[4];  // in a row of a tile
@@ -387,8 +398,8 @@ __global__ void __launch_bounds__(kThreads, 4) kda_delta_chunk(const __grid_cons
                     const f2 l = mul2(pack2(e[t & 1][half][0], e[t & 1][half][1]), *reinterpret_cast<const f2*>(vec.ck + j));
                     const float2 nv = unpack2(mul2(mul2(bb, l), pack2(kk[t][2 * half], kk[t][2 * half + 1])));
                     const float2 q = unpack2(mul2(mul2(cc, l), pack2(qk[t][2 * half], qk[t][2 * half + 1])));
-                    e32[j * kLdE + i - r0] = j < i ? nv.x : 0.f;
-                    e32[(j + 1) * kLdE + i - r0] = j + 1 < i ? nv.y : 0.f;
+                    e32[e_at(j) + i - r0] = j < i ? nv.x : 0.f;
+                    e32[e_at(j + 1) + i - r0] = j + 1 < i ? nv.y : 0.f;
                     pv = pack_half2(j <= i ? q.x : 0.f, j + 1 <= i ? q.y : 0.f);
                 }
                 *reinterpret_cast<uint32_t*>(prow + y[t]) = pv;
@@ -414,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, 4) kda_delta_chunk(const __grid_cons
         for (int m = 0; m < B - 1; ++m) {
 #pragma unroll
             for (int i = (m + 1) & ~3; i < B; i += 4) {
-                const float4 x = *reinterpret_cast<const float4*>(e32 + (o + m) * kLdE + i);
+                const float4 x = *reinterpret_cast<const float4*>(e32 + e_at(o + m) + i);
                 if (i > m) t[i] = fmaf(x.x, t[m], t[i]);
                 if (i + 1 > m) t[i + 1] = fmaf(x.y, t[m], t[i + 1]);
                 if (i + 2 > m) t[i + 2] = fmaf(x.z, t[m], t[i + 2]);
