@@ -575,9 +575,10 @@ __device__ __forceinline__ bool write(const DeltaParams& p, int total, uint32_t 
             tc_fence_after();
             const DeltaScalars* sc = scalars(all);
             uint2 spoils = make_uint2(bad_of(all, row)->x, bad_of(all, row)->y);
-            if (__any_sync(0xffffffffu, (spoils.x | spoils.y) != 0))
-                spoils = poisoned(spoils, make_uint2(sc->clears[0], sc->clears[1]));
+            const bool spoilt = __any_sync(0xffffffffu, (spoils.x | spoils.y) != 0);
+            if (spoilt) spoils = poisoned(spoils, make_uint2(sc->clears[0], sc->clears[1]));
             const int live = len - c * C;
+            const bool plain = !spoilt && live >= C;
             const float f = inv_of(all)[row] * p.scale;
             __nv_bfloat16* o = p.out + ((int64_t)(t0 + c * C) * p.H + h) * D + row;
 #pragma unroll 1
@@ -589,6 +590,16 @@ __device__ __forceinline__ bool write(const DeltaParams& p, int total, uint32_t 
                     const float4 d = *reinterpret_cast<const float4*>(sc->down + b + 2 * i);
                     x[i] = mul2(mul2(x[i], pack2(d.x, d.y)), pack2(f, f));
                     x[i + 1] = mul2(mul2(x[i + 1], pack2(d.z, d.w)), pack2(f, f));
+                }
+                if (plain) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float2 y = unpack2(x[i]);
+                        o[0] = __float2bfloat16_rn(y.x);
+                        o[st] = __float2bfloat16_rn(y.y);
+                        o += 2 * st;
+                    }
+                    continue;
                 }
                 const unsigned lost = (b < 32 ? spoils.x : spoils.y) >> (b & 31);
 #pragma unroll
