@@ -28,6 +28,7 @@
 // block and the second one a token.
 
 #include "kda_device.cuh"
+#include "kda_f32x2.cuh"
 #include "kda_ops.h"
 #include "kda_rows.cuh"
 
@@ -73,29 +74,6 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 __device__ __forceinline__ float zero_if_nan(float x) { return x == x ? x : 0.f; }
-
-// Two fp32 values in one 64-bit register.
-typedef unsigned long long f2;
-__device__ __forceinline__ f2 pack2(float a, float b) {
-    f2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ float2 unpack2(f2 a) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
-    return r;
-}
-__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
-    f2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
-    f2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
 __device__ __forceinline__ uint32_t half2_of(f2 x) {
     const float2 f = unpack2(x);
     return pack_half2(f.x, f.y);
@@ -137,7 +115,6 @@ __device__ __forceinline__ void fetch(uint4 (&v)[4], const __nv_bfloat16* from, 
     for (int i = 0; i < 4; ++i)
         v[i] = 4 * (i >> 1) < rows ? __ldg(reinterpret_cast<const uint4*>(from + 4 * (i >> 1) * st + 64 * (i & 1))) : make_uint4(0, 0, 0, 0);
 }
-__device__ __forceinline__ f2 pair(uint32_t w) { return pack2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)); }
 // A row's sum of squares: the first one's in even lanes, the second one's in odd ones.
 __device__ __forceinline__ float squares(const uint4 (&v)[4], int lane) {
     float sum[2];
@@ -148,7 +125,7 @@ __device__ __forceinline__ float squares(const uint4 (&v)[4], int lane) {
         for (int i = 2 * r; i < 2 * r + 2; ++i) {
             const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
-            for (int j = 0; j < 4; ++j) s = fma2(pair(w[j]), pair(w[j]), s);
+            for (int j = 0; j < 4; ++j) s = fma2(bf16x2(w[j]), bf16x2(w[j]), s);
         }
         const float2 t = unpack2(s);
         sum[r] = t.x + t.y;
@@ -163,8 +140,8 @@ __device__ __forceinline__ int length_of(float kk) { return ((int)(__float_as_ui
 // Eight values times f, as fp16.
 __device__ __forceinline__ uint4 times(uint4 v, float f) {
     const f2 ff = pack2(f, f);
-    return make_uint4(half2_of(mul2(pair(v.x), ff)), half2_of(mul2(pair(v.y), ff)), half2_of(mul2(pair(v.z), ff)),
-                      half2_of(mul2(pair(v.w), ff)));
+    return make_uint4(half2_of(mul2(bf16x2(v.x), ff)), half2_of(mul2(bf16x2(v.y), ff)), half2_of(mul2(bf16x2(v.z), ff)),
+                      half2_of(mul2(bf16x2(v.w), ff)));
 }
 
 // Two values as the sum of two fp16 each.

@@ -7,9 +7,16 @@
 // that is there, their sums over a row's lanes travel together, and the lengths are factors
 // on sums.
 //
-// A CTA of four warps holds 32 value rows of one (sequence, head) state, a warp eight rows,
-// sixteen lanes a row: a lane has eight key columns of every other row, in 16-byte pieces.
+// Memory is the bound for single tokens: 512 of them, 12 heads, take 122.8 us with an fp32 pool (97 %
+// of a copy's rate) and 67.6 us with a bf16 one (89 %); each further token costs about 15 us,
+// instructions.
+//
+// A CTA of four warps has 32 or 128 value rows of one (sequence, head) state, a warp eight
+// rows at a time, eight lanes a row: a lane has sixteen key columns of every fourth row, in 16-byte
+// pieces, and the next eight rows' pieces are on their way.  What belongs to a token is made once
+// a CTA, in shared memory: k, q and v in fp32, the lengths, the decay.
 
+#include "kda_f32x2.cuh"
 #include "kda_ops.h"
 #include "kda_rows.cuh"
 
@@ -19,162 +26,200 @@ namespace {
 constexpr int D = kD;
 constexpr int kWarps = 4;
 constexpr int kRows = 8;                      // value rows per warp
-constexpr int kSplit = D / (kWarps * kRows);  // CTAs per (sequence, head)
-constexpr int kAcross = 16;                   // lanes of a row
-constexpr int kHeld = kRows * kAcross / 32;   // rows a lane has part of
-constexpr int kCols = D / kAcross;            // columns of a row a lane has
+constexpr int kParts = D / (kWarps * kRows);  // a CTA's least share of a (sequence, head)
+constexpr int kAcross = 8;                    // lanes of a row
+constexpr int kStep = 32 / kAcross;           // rows between a lane's
+constexpr int kHeld = kRows / kStep;          // rows a lane has part of
+constexpr int kPairs = D / kAcross / 2;       // pairs of columns of a row a lane has
+constexpr int kToks = kShortMax;
 
-// A lane's eight columns of a state row: 16 bytes at its place in each 16 x 16 bytes.
+struct alignas(16) Token {
+    float k[D], q[D], v[D];
+    float d, one;  // e^g = one + d
+    float rk, rq;  // 1 / |k|, 1 / |q|
+    float kq, beta;
+    bool clears;
+};
+
+// A lane's columns of a state row: 16 bytes at its place in each 8 x 16 bytes.
 template <class S>
 struct Cols {
-    static constexpr int kN = 16 / sizeof(S), kPieces = kCols / kN;
-    static __device__ __forceinline__ int at(int lane, int i) { return i * kAcross * kN + lane * kN; }
+    static constexpr int kN = 16 / sizeof(S), kPieces = 2 * kPairs / kN;
+    static __device__ __forceinline__ int at(int lane, int i) { return (i * kAcross + lane) * kN; }
     static __device__ __forceinline__ void load(const S* row, int lane, uint4 (&raw)[kPieces]) {
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) raw[i] = __ldcs(reinterpret_cast<const uint4*>(row + at(lane, i)));
     }
-    static __device__ __forceinline__ void get(const uint4 (&raw)[kPieces], float (&f)[kCols]) {
+    static __device__ __forceinline__ void get(const uint4 (&raw)[kPieces], f2 (&f)[kPairs]) {
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
             float x[kN];
             reinterpret_cast<const rows::Piece<S, kN>&>(raw[i]).get(x);
 #pragma unroll
-            for (int j = 0; j < kN; ++j) f[i * kN + j] = x[j];
+            for (int j = 0; j < kN; j += 2) f[(i * kN + j) / 2] = pack2(x[j], x[j + 1]);
         }
     }
-    static __device__ __forceinline__ void store(S* row, int lane, const float (&f)[kCols]) {
+    static __device__ __forceinline__ void store(S* row, int lane, const f2 (&f)[kPairs]) {
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
             float x[kN];
 #pragma unroll
-            for (int j = 0; j < kN; ++j) x[j] = f[i * kN + j];
+            for (int j = 0; j < kN; j += 2) {
+                const float2 y = unpack2(f[(i * kN + j) / 2]);
+                x[j] = y.x, x[j + 1] = y.y;
+            }
             rows::Piece<S, kN> p;
             p.set(x);
             __stcs(reinterpret_cast<uint4*>(row + at(lane, i)), reinterpret_cast<const uint4&>(p));
         }
     }
-    // the same columns of a bf16 row of k or q
-    static __device__ __forceinline__ uint4 load16(const __nv_bfloat16* row, int lane) {
-        if constexpr (kPieces == 1) {
-            return __ldg(reinterpret_cast<const uint4*>(row + at(lane, 0)));
-        } else {
-            const uint2 a = __ldg(reinterpret_cast<const uint2*>(row + at(lane, 0)));
-            const uint2 b = __ldg(reinterpret_cast<const uint2*>(row + at(lane, 1)));
-            return make_uint4(a.x, a.y, b.x, b.y);
-        }
-    }
 };
 
-__device__ __forceinline__ float row_sum(float x) {  // over the lanes of a row
+// A lane's share of a token's rows; a warp makes the token of it.
+struct Rows {
+    uint2 k, q, v;
+    float g, beta;
+};
+__device__ __forceinline__ Rows load_token(const DeltaParams& p, int64_t t, int h, int lane) {
+    const auto row = [&](const __nv_bfloat16* x, int64_t st, int64_t off) {
+        return __ldg(reinterpret_cast<const uint2*>(x + t * st + off + 4 * lane));
+    };
+    return {row(p.k, p.k_st, (int64_t)(h / p.rep) * p.k_sh), row(p.q, p.q_st, (int64_t)(h / p.rep) * p.q_sh),
+            row(p.v, p.v_st, (int64_t)h * p.v_sh), p.g[t * p.g_st + h], p.beta[t * p.H + h]};
+}
+__device__ __forceinline__ void make_token(const Rows& x, int lane, Token& to) {
+    const auto row = [&](uint2 w, float* out, f2 (&f)[2]) {
+        f[0] = bf16x2(w.x), f[1] = bf16x2(w.y);
+        *reinterpret_cast<ulonglong2*>(out + 4 * lane) = make_ulonglong2(f[0], f[1]);
+    };
+    const float g = x.g;
+    f2 k[2], q[2], v[2];
+    row(x.k, to.k, k);
+    row(x.q, to.q, q);
+    row(x.v, to.v, v);
+    const auto dot = [](const f2 (&a)[2], const f2 (&b)[2]) {
+        const float2 s = unpack2(fma2(a[0], b[0], mul2(a[1], b[1])));
+        return s.x + s.y;
+    };
+    float kk = dot(k, k), qq = dot(q, q), kq = dot(k, q);
 #pragma unroll
-    for (int w = kAcross / 2; w >= 1; w >>= 1) x += __shfl_xor_sync(0xffffffffu, x, w);
-    return x;
+    for (int w = 16; w >= 1; w >>= 1) {
+        kk += __shfl_xor_sync(0xffffffffu, kk, w);
+        qq += __shfl_xor_sync(0xffffffffu, qq, w);
+        kq += __shfl_xor_sync(0xffffffffu, kq, w);
+    }
+    // a decay near one as 1 + expm1(g): rounded to fp32, e^g alone would be off
+    // by up to 2^-25 in the same direction at every token
+    const bool slow = g > -0.5f;
+    if (lane == 0) {
+        to.d = slow ? expm1f(g) : expf(g);
+        to.one = slow ? 1.f : 0.f;
+        to.rk = 1.f / sqrtf(kk + 1e-6f);
+        to.rq = 1.f / sqrtf(qq + 1e-6f);
+        to.kq = kq;
+        to.beta = x.beta;
+        to.clears = g < kMinDecay;
+    }
 }
 
-template <class S>
-__global__ void __launch_bounds__(kWarps * 32, 5)
+template <class S, int kPasses>
+__global__ void __launch_bounds__(kWarps * 32, kPasses == 1 ? 6 : sizeof(S) == 4 ? 4 : 5)
 kda_delta_step(const __grid_constant__ DeltaParams p) {
     using C = Cols<S>;
-    const int h = blockIdx.y;
-    const int n = p.short_list[blockIdx.x / kSplit];
+    __shared__ Token tokens[kToks];
+    const int h = blockIdx.y, ctas = kParts / kPasses;
+    const int n = p.short_list[blockIdx.x / ctas];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int at = lane % kAcross, part = lane / kAcross;  // rows part, part + 2, ... of the eight
+    const int at = lane % kAcross, part = lane / kAcross;  // rows part, part + 4 of the eight
     const int own = at % kHeld;                            // the held row whose output this lane makes
-    const int row0 = (blockIdx.x % kSplit) * (kWarps * kRows) + warp * kRows + part;
-    const int t0 = p.cu[n], t1 = p.cu[n + 1];
-    const int slot = p.idx[n];
-    const bool ok = slot >= 0 && slot < p.num_slots;
-    const bool init = ok && p.has_init[n] != 0;
-    S* state = static_cast<S*>(p.pool) + (ok ? (size_t)slot * p.stride0 : 0) + ((size_t)h * D + row0) * D;
-    const __nv_bfloat16* qp = p.q + (int64_t)(h / p.rep) * p.q_sh;
-    const __nv_bfloat16* kp = p.k + (int64_t)(h / p.rep) * p.k_sh;
-    const __nv_bfloat16* vp = p.v + (int64_t)h * p.v_sh + row0 + own * (32 / kAcross);
-    rows::Piece<__nv_bfloat16, 8> k8, q8;
-    __nv_bfloat16 v1;
-    float g = 0.f, beta = 0.f;
-    auto fetch = [&](int t) {
-        k8.v = C::load16(kp + (int64_t)t * p.k_st, at);
-        q8.v = C::load16(qp + (int64_t)t * p.q_st, at);
-        v1 = vp[(int64_t)t * p.v_st];
-        g = p.g[(int64_t)t * p.g_st + h];
-        beta = p.beta[(int64_t)t * p.H + h];
-    };
-    if (t0 < t1) fetch(t0);
+    int row = ((blockIdx.x % ctas) * kWarps + warp) * kRows * kPasses + part;
+    const int t0 = p.cu[n], t1 = p.cu[n + 1], slot = p.idx[n];
+    const bool has = p.has_init[n] != 0;
+    const bool ok = slot >= 0 && slot < p.num_slots, init = ok && has;
+    S* state = static_cast<S*>(p.pool) + (ok ? (size_t)slot * p.stride0 : 0) + ((size_t)h * D + row) * D;
     uint4 raw[kHeld][C::kPieces] = {};
-    if (init) {
+    const auto load = [&](const S* from) {
 #pragma unroll
-        for (int r = 0; r < kHeld; ++r) C::load(state + r * (32 / kAcross) * D, at, raw[r]);
+        for (int r = 0; r < kHeld; ++r) C::load(from + r * kStep * D, at, raw[r]);
+    };
+    // (the token's rows first: its sums are made while the state is on its way)
+    Rows rows = {};
+    if (t0 + warp < t1) rows = load_token(p, t0 + warp, h, lane);
+    if (init) load(state);
+    for (int t = t0 + warp; t < t1; t += kWarps) {
+        make_token(rows, lane, tokens[t - t0]);
+        if (t + kWarps < t1) rows = load_token(p, t + kWarps, h, lane);
     }
-    float s[kHeld][kCols];
+    __syncthreads();
+#pragma unroll 1
+    for (int pass = 0; pass < kPasses; ++pass, row += kRows, state += kRows * D) {
+        f2 s[kHeld][kPairs];
 #pragma unroll
-    for (int r = 0; r < kHeld; ++r) C::get(raw[r], s[r]);
-    for (int t = t0; t < t1; ++t) {
-        float k[kCols], q[kCols];
-        k8.get(k);
-        q8.get(q);
-        const float v = __bfloat162float(v1), b = beta;
-        // a decay near one as 1 + expm1(g): rounded to fp32, e^g alone would be off
-        // by up to 2^-25 in the same direction at every token
-        const bool slow = g > -0.5f;
-        const float d = slow ? expm1f(g) : expf(g);
-        const float one = slow ? 1.f : 0.f;
-        if (g < kMinDecay) {  // cleared, whatever it held
+        for (int r = 0; r < kHeld; ++r) C::get(raw[r], s[r]);
+        if (init && pass + 1 < kPasses) load(state + kRows * D);
+#pragma unroll 1
+        for (int t = t0; t < t1; ++t) {
+            const Token& x = tokens[t - t0];
+            if (x.clears) {  // whatever it held
 #pragma unroll
-            for (int r = 0; r < kHeld; ++r)
+                for (int r = 0; r < kHeld; ++r)
 #pragma unroll
-                for (int j = 0; j < kCols; ++j) s[r][j] = 0.f;
-        }
-        if (t + 1 < t1) fetch(t + 1);
-        float kk = 0.f, qq = 0.f, kq = 0.f;
+                    for (int j = 0; j < kPairs; ++j) s[r][j] = 0;
+            }
+            // the state's products with k for the held rows, then with q
+            f2 k[kPairs], sum[2 * kHeld] = {};
 #pragma unroll
-        for (int j = 0; j < kCols; ++j) {
-            kk = fmaf(k[j], k[j], kk);
-            qq = fmaf(q[j], q[j], qq);
-            kq = fmaf(k[j], q[j], kq);
-        }
-        // sums over a row's lanes: lane l keeps x[l % 8], the state's product with k for the
-        // held rows, then with q
-        float x[2 * kHeld];
+            for (int i = 0; i < kPairs; i += 2) {
+                const int c = C::at(at, 2 * i / C::kN) + 2 * i % C::kN;
+                const ulonglong2 kk = *reinterpret_cast<const ulonglong2*>(x.k + c), qq = *reinterpret_cast<const ulonglong2*>(x.q + c);
+                k[i] = kk.x, k[i + 1] = kk.y;
 #pragma unroll
-        for (int r = 0; r < kHeld; ++r) {
-            x[r] = x[kHeld + r] = 0.f;
+                for (int r = 0; r < kHeld; ++r) {
+                    sum[r] = fma2(s[r][i + 1], kk.y, fma2(s[r][i], kk.x, sum[r]));
+                    sum[kHeld + r] = fma2(s[r][i + 1], qq.y, fma2(s[r][i], qq.x, sum[kHeld + r]));
+                }
+            }
+            // summed over a row's lanes: lane l keeps y[l % 4]
+            float y[2 * kHeld];
 #pragma unroll
-            for (int j = 0; j < kCols; ++j) {
-                x[r] = fmaf(s[r][j], k[j], x[r]);
-                x[kHeld + r] = fmaf(s[r][j], q[j], x[kHeld + r]);
+            for (int i = 0; i < 2 * kHeld; ++i) {
+                const float2 f = unpack2(sum[i]);
+                y[i] = f.x + f.y;
+            }
+#pragma unroll
+            for (int w = kHeld; w >= 1; w >>= 1) {
+                const bool up = (lane & w) != 0;
+#pragma unroll
+                for (int j = 0; j < w; ++j) {
+                    const float give = up ? y[j] : y[j + w];
+                    const float keep = up ? y[j + w] : y[j];
+                    y[j] = keep + __shfl_xor_sync(0xffffffffu, give, w);
+                }
+            }
+            float all = y[0];
+#pragma unroll
+            for (int w = 2 * kHeld; w < kAcross; w <<= 1) all += __shfl_xor_sync(0xffffffffu, all, w);
+            const int first = lane - at;
+            const float sk = __shfl_sync(0xffffffffu, all, first + own);
+            const float sq = __shfl_sync(0xffffffffu, all, first + kHeld + own);
+            const int mine = row + own * kStep;
+            const float e = x.one + x.d;
+            const float uk = x.beta * (x.v[mine] - e * (x.rk * sk)) * x.rk;
+            if (at < kHeld)
+                p.out[((size_t)t * p.H + h) * D + mine] = __float2bfloat16_rn(p.scale * (x.rq * fmaf(uk, x.kq, e * sq)));
+            const f2 d = pack2(x.d, x.d), one = pack2(x.one, x.one);
+#pragma unroll
+            for (int r = 0; r < kHeld; ++r) {
+                const float ur = __shfl_sync(0xffffffffu, uk, first + r);
+                const f2 u = pack2(ur, ur);
+#pragma unroll
+                for (int j = 0; j < kPairs; ++j) s[r][j] = fma2(one, s[r][j], fma2(d, s[r][j], mul2(u, k[j])));
             }
         }
+        if (ok && !(init && t1 <= t0)) {
 #pragma unroll
-        for (int w = kHeld; w >= 1; w >>= 1) {
-            const bool up = (lane & w) != 0;
-#pragma unroll
-            for (int j = 0; j < w; ++j) {
-                const float give = up ? x[j] : x[j + w];
-                const float keep = up ? x[j + w] : x[j];
-                x[j] = keep + __shfl_xor_sync(0xffffffffu, give, w);
-            }
+            for (int r = 0; r < kHeld; ++r) C::store(state + r * kStep * D, at, s[r]);
         }
-        const float sum = x[0] + __shfl_xor_sync(0xffffffffu, x[0], 2 * kHeld);
-        const float rk = 1.f / sqrtf(row_sum(kk) + 1e-6f), rq = 1.f / sqrtf(row_sum(qq) + 1e-6f);
-        kq = row_sum(kq);
-        const int first = lane - at;
-        const float sk = __shfl_sync(0xffffffffu, sum, first + own);
-        const float sq = __shfl_sync(0xffffffffu, sum, first + kHeld + own);
-        const float e = one + d;
-        const float uk = b * (v - e * (rk * sk)) * rk;
-        if (at < kHeld)
-            p.out[((size_t)t * p.H + h) * D + row0 + own * (32 / kAcross)] =
-                __float2bfloat16_rn(p.scale * (rq * fmaf(uk, kq, e * sq)));
-#pragma unroll
-        for (int r = 0; r < kHeld; ++r) {
-            const float ur = __shfl_sync(0xffffffffu, uk, first + r);
-#pragma unroll
-            for (int j = 0; j < kCols; ++j) s[r][j] = fmaf(one, s[r][j], fmaf(d, s[r][j], ur * k[j]));
-        }
-    }
-    if (ok && !(init && t1 <= t0)) {
-#pragma unroll
-        for (int r = 0; r < kHeld; ++r) C::store(state + r * (32 / kAcross) * D, at, s[r]);
     }
     // Launched beside the walk, this grid may be over only once the walk is: its last CTA waits
     // (all of them waiting would keep their places on the SMs that the walk leaves free: 512
@@ -184,10 +229,10 @@ kda_delta_step(const __grid_constant__ DeltaParams p) {
     if (p.n_long == 0 && blockIdx.x == 0 && blockIdx.y == 0 && warp == 0) write_status(p, lane);
 }
 
-template <class S>
+template <class S, int kPasses>
 cudaError_t launch(const DeltaParams& p, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)p.n_short * kSplit, (unsigned)p.H);
+    cfg.gridDim = dim3((unsigned)p.n_short * (kParts / kPasses), (unsigned)p.H);
     cfg.blockDim = dim3(kWarps * 32);
     cfg.stream = s;
     // right behind the walk, beside its CTAs
@@ -196,7 +241,15 @@ cudaError_t launch(const DeltaParams& p, cudaStream_t s) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = p.n_long > 0 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kda_delta_step<S>, p);
+    return cudaLaunchKernelEx(&cfg, kda_delta_step<S, kPasses>, p);
+}
+template <class S>
+cudaError_t launch(const DeltaParams& p, cudaStream_t s) {
+    // Few states: 32 rows a CTA, for the latency; many: 128, whose loads overlap and which share
+    // what belongs to a token.  12 heads, fp32 pool: 16 sequences of 4 tokens 10.4 and 12.5 us, 50
+    // of them 18.6 and 16.8; 512 single tokens, bf16 pool: 82 and 68 us
+    if ((int64_t)p.n_short * p.H * kParts <= 8 * num_sms()) return launch<S, 1>(p, s);
+    return launch<S, kParts>(p, s);
 }
 
 }  // namespace

@@ -36,6 +36,7 @@
 // rows get NaN afterwards, until a token clears the state.
 
 #include "kda_device.cuh"
+#include "kda_f32x2.cuh"
 #include "kda_ops.h"
 #include "kda_rows.cuh"
 
@@ -130,29 +131,6 @@ __device__ __forceinline__ bool elect_one() {
 }
 __device__ __forceinline__ uint64_t* bar(int i) { return reinterpret_cast<uint64_t*>(smem + kSmBar) + i; }
 __device__ __forceinline__ volatile int& abort_flag() { return *reinterpret_cast<volatile int*>(smem + kSmMisc); }
-
-// Two fp32 values in one 64-bit register.
-typedef unsigned long long f2;
-__device__ __forceinline__ f2 pack2(float a, float b) {
-    f2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ float2 unpack2(f2 a) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
-    return r;
-}
-__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
-    f2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
-    f2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
 
 // Sixteen columns of this thread's lane, there on return.
 __device__ __forceinline__ void load16(uint32_t a, f2 (&v)[8]) {
@@ -1234,8 +1212,9 @@ Cut cut_rule(const int32_t* lens, int n, int H, int sms, int64_t planes, float s
 }  // namespace
 
 void delta_cut(DeltaParams& p, LinCuts& cuts, const SeqTables& t) {
-    // a single token's state of a head goes there and back at 6.6 TB/s, a chunk takes 2.6 us
-    const float state = p.st_dtype == KDA_STATE_F32 ? 0.0076f : 0.0045f;
+    // a single token's state of a head goes there and back at 6.6 TB/s (5.9 if of 2 bytes), a
+    // chunk takes 2.6 us
+    const float state = p.st_dtype == KDA_STATE_F32 ? 0.0077f : 0.0042f;
     const Cut c = cut_rule(t.long_lens, p.n_long, p.H, num_sms(), delta_planes(p.T, p.H), state * (float)p.n_short * (float)p.H);
     p.seg_len = c.seg * C;
     p.n_cut = c.n_cut;

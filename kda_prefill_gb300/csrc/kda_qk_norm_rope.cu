@@ -8,6 +8,7 @@
 // each other in a warp and sum its squares by shuffles; the row stays in registers.  Longer
 // rows, and rows that are not whole pieces, take a warp each, which reads them twice.
 
+#include "kda_f32x2.cuh"
 #include "kda_rope.cuh"
 
 namespace kda {
@@ -29,29 +30,6 @@ template <int VE>
 __device__ __forceinline__ void load_weights(float (&w)[VE], const float* p) {
 #pragma unroll
     for (int j = 0; j < VE; ++j) w[j] = p ? p[j] : 1.f;
-}
-
-// Two fp32 values in one 64-bit register.
-typedef unsigned long long f2;
-__device__ __forceinline__ f2 pack2(float a, float b) {
-    f2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ float2 unpack2(f2 a) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
-    return r;
-}
-__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
-    f2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
-    f2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
 }
 template <int VE>
 __device__ __forceinline__ void pairs(f2 (&x)[VE / 2], const float (&f)[VE]) {
