@@ -59,13 +59,15 @@ struct Entry {
     }
 };
 
-// `units` units a row, at most LANES, the first rot_units of them turned.  Rows ahead and
-// registers: a unit and its partner with their weights take 80 registers for two rows, a unit
-// alone 64 for four (16384 tokens, 12 + 12 heads, half layout: 39.3 us, 41.1 with four rows,
-// 43.6 with 64 registers; 12 + 2 heads, pairs beside each other: 28.1 us, 34.9 with two rows
-// and 80 registers, 30.3 with two and 64).
+// Rows ahead and registers: a unit and its partner with their weights take 80 registers for two
+// rows, a unit alone 56 for four (16384 tokens, 12 + 12 heads, half layout: 37.1 us, 39.1 with
+// 72 registers, 41.2 with 64; 12 + 2 heads, pairs beside each other: 21.7 us, 23.0 with 64
+// registers, 24.9 with 48; each with the tokens of a CTA that suit it).
+constexpr int regs_of(bool interleaved) { return interleaved ? 56 : 80; }
+
+// `units` units a row, at most LANES, the first rot_units of them turned.
 template <class E, int VE, bool IL, int LANES>
-__global__ void __maxnreg__(IL ? 64 : 80)
+__global__ void __maxnreg__(regs_of(IL))
 kda_qk_norm_rope(const __grid_constant__ NormRopeParams p, int tokens, int rot_units, int units) {
     using U = Unit<E, VE, IL>;
     using T = Entry<VE, IL>;
@@ -137,7 +139,7 @@ kda_qk_norm_rope(const __grid_constant__ NormRopeParams p, int tokens, int rot_u
                 }
                 const float2 both = unpack2(sum);
                 const float all = group_sum<LANES>(live ? both.x + both.y : 0.f);
-                const float inv = 1.f / sqrtf(fmaf(all, per, p.eps));
+                const float inv = rsqrtf(fmaf(all, per, p.eps));
                 const f2 inv2 = pack2(inv, inv);
                 if (t + i < n) {
 #pragma unroll
@@ -244,22 +246,26 @@ kda_qk_norm_rope_long(const __grid_constant__ NormRopeParams p, int tokens, int 
 
 template <class E, int VE, bool IL, int LANES>
 cudaError_t launch(const NormRopeParams& p, int rot_units, int units, cudaStream_t s) {
-    const int half = p.rot / 2;
-    // tokens per CTA: eight, at most what the table holds, and few enough that each SM
-    // has eight CTAs where there are so many tokens
-    int tokens = max(1, min(8, kMaxTable / max(1, half)));
-    tokens = (int)max((int64_t)1, min((int64_t)tokens, p.T / (8 * num_sms())));
-    const int64_t grid = (p.T + tokens - 1) / tokens;
+    const int most = kMaxTable / max(1, p.rot / 2);  // tokens that the table holds
     const int heads = p.x[0].heads + p.x[1].heads;
     if constexpr (LANES == 0) {
+        // eight tokens a CTA, and few enough that each SM has eight CTAs where there are so
+        // many tokens
+        const int tokens = (int)max((int64_t)1, min((int64_t)min(8, most), p.T / (8 * num_sms())));
         const int threads = (int)min((int64_t)kMaxThreads, (int64_t)heads * tokens * 32);
-        kda_qk_norm_rope_long<E, VE, IL><<<(unsigned)grid, max(128, threads), 0, s>>>(p, tokens, rot_units, units);
+        kda_qk_norm_rope_long<E, VE, IL><<<(unsigned)((p.T + tokens - 1) / tokens), max(128, threads), 0, s>>>(p, tokens, rot_units, units);
     } else {
         // threads: as many as a token's units in the fewest rounds, in whole warps
         const int items = heads * LANES;
         const int rounds = (items + kMaxThreads - 1) / kMaxThreads;
         const int threads = max(128, ((items + rounds - 1) / rounds + 31) / 32 * 32);
-        kda_qk_norm_rope<E, VE, IL, LANES><<<(unsigned)grid, threads, 0, s>>>(p, tokens, rot_units, units);
+        // tokens a CTA: all CTAs are on the SMs at once, or go there in the fewest whole waves
+        // (16384 tokens, 12 + 2 heads: 21.7 us with 22 tokens, one wave; 23.3 with 8, 24.8 with
+        // 16; 12 + 12 heads: 37.1 us with 27 tokens, 38.1 with 8, 47.5 with 24)
+        const int resident = max(1, min(65536 / (regs_of(IL) * threads), min(2048 / threads, 10)));
+        const int64_t ctas = (int64_t)resident * num_sms(), one = (p.T + ctas - 1) / ctas, waves = (one + most - 1) / most;
+        const int tokens = (int)max((int64_t)1, (p.T + waves * ctas - 1) / (waves * ctas));
+        kda_qk_norm_rope<E, VE, IL, LANES><<<(unsigned)((p.T + tokens - 1) / tokens), threads, 0, s>>>(p, tokens, rot_units, units);
     }
     return cudaGetLastError();
 }
