@@ -18,6 +18,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import math
+import struct
 from typing import Optional
 
 import torch
@@ -40,6 +41,12 @@ class _RopeTensor(ctypes.Structure):
 
 class _NormRopeTensor(ctypes.Structure):
     _fields_ = [("x", _RopeTensor), ("weight", ctypes.c_void_p), ("weight_stride_h", ctypes.c_int64)]
+
+
+# Two of them, as bytes: a third of the time that ctypes takes for their fields
+_NORM_ROPE_TENSORS = struct.Struct("@" + "PPqqqqi4xPq" * 2)
+assert _NORM_ROPE_TENSORS.size == 2 * ctypes.sizeof(_NormRopeTensor)
+_NO_TENSOR = (0,) * 9
 
 
 def _rows(x: torch.Tensor, name: str, dtype=None):
@@ -167,7 +174,11 @@ def gated_delta_fwd(q, k, v, log_decay, beta, cu_seqlens, *, state_cache, state_
         raise ValueError(f"beta must be a contiguous [1, T, H] tensor; got shape {tuple(bs)}")
     _on_current_device(at)
     host = None if cu_seqlens_cpu is None else _host_int32(cu_seqlens_cpu, N)
-    workspace, given = _packed_workspace(gated_delta_workspace_size(T, N, H), workspace, dev, stream)
+    given = gated_delta_workspace_size(T, N, H)
+    if workspace is None and given <= _HEADER:
+        workspace = _header(dev, stream)
+    else:
+        workspace, given = _packed_workspace(given, workspace, dev, stream)
     rc = lib.kda_gated_delta_fwd(
         q.data_ptr(), q_st, q_sh, k.data_ptr(), k_st, k_sh, v.data_ptr(), v_st, v_sh,
         log_decay.data_ptr(), log_decay.dim() > 1, beta.data_ptr(), cu_seqlens.data_ptr(),
@@ -220,6 +231,23 @@ def _packed(q, k, v, log_decay, cu_seqlens, state_cache, state_indices, hs, out)
         T, Hk, H, N, (q_st, q_sh, k_st, k_sh, v_st, v_sh) = _packed_args(
             q, k, v, log_decay, cu_seqlens, state_cache, state_indices, hs, out)
     return T, Hk, H, N, (q_st, q_sh, k_st, k_sh, v_st, v_sh)
+
+
+_HEADER = 256  # bytes of a workspace that holds a status word alone
+_headers = {}
+
+
+def _header(dev, stream):
+    """The workspace of a call that needs no other and whose caller cannot read its status:
+    one for each GPU, which any number of calls may write at once.  (An allocation takes 5 us
+    of such a call's 20 on the host.)"""
+    ws = _headers.get(dev.index)
+    if ws is None:
+        ws = _empty(_HEADER, torch.uint8, dev, stream)
+        # (memory of a graph's own is the graph's)
+        if not torch.cuda.is_current_stream_capturing() and stream is None:
+            _headers[dev.index] = ws
+    return ws
 
 
 def _packed_workspace(need, workspace, dev, stream):
@@ -333,12 +361,13 @@ def _rope_rows(q, k, positions, inv_freq, layout, q_out, k_out):
     if k is None and k_out is not None:
         raise ValueError("k_out is given without k")
     k_out = k if k_out is None else k_out
-    T, _, D, _, _ = _rows(q, "q")
     rows = []
     for name, x, y in (("q", q, q_out), ("k", k, k_out)):
         if x is None:
             continue
         Tx, H, Dx, st, sh = _rows(x, name, q.dtype)
+        if x is q:
+            T, D = Tx, Dx
         To, Ho, Do, ost, osh = (Tx, H, Dx, st, sh) if y is x else _rows(y, name + "_out", q.dtype)
         if Tx != T or Dx != D or To != Tx or Ho != H or Do != Dx:
             raise ValueError(f"{name} and {name}_out must be [1, T, H, D] with q's T and D")
@@ -383,10 +412,10 @@ def rope(q, k, positions, inv_freq, *, layout: str = "half", factor: float = 1.0
 def _head_weight(w, name, H, D):
     """(address, elements between heads) of a norm's weights."""
     if w is None:
-        return None, 0
+        return 0, 0
     if w.dtype != torch.float32 or not w.is_cuda:
         raise TypeError(f"{name} must be a float32 CUDA tensor")
-    if tuple(w.shape) not in ((D,), (H, D)) or not w.is_contiguous():
+    if w.shape not in ((D,), (H, D)) or not w.is_contiguous():
         raise ValueError(f"{name} must be a contiguous [{D}] or [{H}, {D}] tensor; got shape "
                          f"{tuple(w.shape)}")
     return w.data_ptr(), D if w.dim() == 2 else 0
@@ -404,12 +433,16 @@ def qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, *, layout: str =
     rows, D = _rope_rows(q, k, positions, inv_freq, layout, q_out, k_out)
     if k is None and k_weight is not None:
         raise ValueError("k_weight is given without k")
-    arr = (_NormRopeTensor * 2)()
-    for i, (w, name) in enumerate(((q_weight, "q_weight"), (k_weight, "k_weight"))[:len(rows)]):
-        arr[i] = (rows[i], *_head_weight(w, name, rows[i][6], D))
-        if w is not None and w.get_device() != q.get_device():
-            _same_device(q.device, **{name: w})
-    rc = lib.kda_qk_norm_rope(arr, len(rows), float(eps), positions.data_ptr(), positions.element_size(),
+    at = q.get_device()
+    fields = _NO_TENSOR
+    if k is not None:
+        fields = (*rows[1], *_head_weight(k_weight, "k_weight", rows[1][6], D))
+        if k_weight is not None and k_weight.get_device() != at:
+            _same_device(q.device, k_weight=k_weight)
+    tensors = _NORM_ROPE_TENSORS.pack(*rows[0], *_head_weight(q_weight, "q_weight", rows[0][6], D), *fields)
+    if q_weight is not None and q_weight.get_device() != at:
+        _same_device(q.device, q_weight=q_weight)
+    rc = lib.kda_qk_norm_rope(tensors, len(rows), float(eps), positions.data_ptr(), positions.element_size(),
                               inv_freq.data_ptr(), positions.numel(), D, 2 * inv_freq.numel(),
                               _LAYOUTS[layout], float(factor), _DTYPES[q.dtype], _stream(stream, q.device))
     if rc != KDA_OK:

@@ -151,3 +151,40 @@ def test_norms_and_turns_past_32_bits():
     view.copy_(x)
     kda.qk_norm_rope(view, None, None, None, pos, freq)
     assert torch.equal(view, want)
+
+
+def test_single_tokens_first_seen_in_a_capture():
+    """A call that needs no workspace but its header, made for the first time while a graph is
+    captured, on a stream of its own and eagerly afterwards."""
+    kda.ops._headers.clear()
+    c = make([1, 4], 2, seed=49, init=[True, True])
+    want, before = expected(c), c["storage"].clone()
+    go(dict(c, cache=c["cache"].clone()))  # the bounds' tables have to be there
+    kda.ops._headers.clear()
+    out = torch.empty(c["v"].shape, dtype=torch.bfloat16, device="cuda")
+    cu, idx, has = c["cu"].cuda(), c["idx"].cuda(), c["has"].cuda()
+
+    def call(**kw):
+        kda.gated_delta_fwd(c["q"], c["k"], c["v"], c["g"], c["beta"], cu, state_cache=c["cache"], state_indices=idx,
+                            has_initial_state=has, out=out, cu_seqlens_cpu=c["cu"], **kw)
+
+    graph, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=s):
+        call()
+    assert not kda.ops._headers
+    c["storage"].copy_(before)
+    graph.replay()
+    torch.cuda.synchronize()
+    check(c, out, want, before)
+    c["storage"].copy_(before)
+    torch.cuda.synchronize()
+    call(stream=s)
+    s.synchronize()
+    assert not kda.ops._headers
+    check(c, out, want, before)
+    for _ in range(2):
+        c["storage"].copy_(before)
+        call()
+        assert list(kda.ops._headers) == [torch.cuda.current_device()]
+        check(c, out, want, before)
