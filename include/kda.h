@@ -437,8 +437,23 @@ KDA_API size_t kda_lin_attn_workspace_size(int64_t total_tokens, int32_t num_seq
  *   workspace        at least kda_gated_delta_workspace_size() bytes, 256-byte
  *                    aligned; kda_check_status() reads its status word.
  *
- * Accumulation is in fp32; an fp32 pool receives the state to fp32 accuracy.
- * Graph capture, synchronisation and bounds follow kda_chunk_fwd.
+ * Sequences of at most 8 tokens go token by token, longer ones in chunks of 64, a
+ * few long ones in segments besides; a call's sums are made in the same order every
+ * time.  States are fp32 while they are carried, and the products' operands have 22
+ * bits or more; those of the outputs alone have 11 (out has 8).
+ *
+ * Decays are at most 0; one below -104 clears the state, whatever it held (e^g is zero
+ * in fp32).  beta outside 0 .. 2 lengthens the state and is not for this call: the
+ * chunks' scales are made for it.  |q|^2 and |k|^2 have to be finite in fp32: a row
+ * with one that is not counts as one that is not finite.  Such a k spoils its
+ * sequence and head, such a v or an entry of the state its value row, from its token
+ * on until a token clears the state; such a q spoils its own output.  A sequence
+ * without tokens keeps its slot's state, or has it zeroed where it starts from zero.
+ * Rows of out behind the last sequence stay as they were.
+ *
+ * Graph capture, synchronisation and bounds follow kda_chunk_fwd.  Calls on one
+ * workspace have to follow each other (one stream, or graphs replayed in turn), and so
+ * have calls on one slot; a slot may occur once in a call.
  */
 KDA_API int kda_gated_delta_fwd(const void* q, int64_t q_stride_t, int64_t q_stride_h,
                   const void* k, int64_t k_stride_t, int64_t k_stride_h,
@@ -453,7 +468,8 @@ KDA_API int kda_gated_delta_fwd(const void* q, int64_t q_stride_t, int64_t q_str
                   void* workspace, size_t workspace_bytes, kda_stream_t stream);
 
 /* Bytes of workspace a kda_gated_delta_fwd call with these sizes needs; 0 for
- * invalid sizes. */
+ * invalid sizes.  About 59 KB for 64 tokens and a head (223 MB for 16384 tokens of 12
+ * heads), whatever the sequences' lengths; 256 bytes below nine tokens. */
 KDA_API size_t kda_gated_delta_workspace_size(int64_t total_tokens, int32_t num_seqs,
                   int32_t num_heads);
 
@@ -502,6 +518,9 @@ KDA_API int kda_rope(const kda_rope_tensor* tensors, int32_t num_tensors,
  * mean square and multiplied by a weight, then turned as in kda_rope:
  *
  *     y = x / sqrt(mean(x^2) + eps) * weight,   y's first rot_dim dimensions turned
+ *
+ * All of it in fp32, rounded once.  A row that is not finite, or whose sum of squares
+ * is not, spoils itself alone; with eps = 0 a row of zeros does, too.
  *
  *   tensors       1 or 2 of them (q and k), their `x` as in kda_rope.  `weight`
  *                 is device fp32 [head_dim], or [num_heads][head_dim] with

@@ -17,9 +17,13 @@
 //   20     issues the products and the blocks' copies, and says what comes next
 //   21-23  turn v over, so that a value row's tokens lie beside each other, and find its
 //          largest
-// The chain X, R, U, dS, S of one chunk after the other is the bound: the roles keep all
-// else off it, and an SM has one CTA, whose registers then let a warp have all its values of a step
-// in flight (two CTAs of half as many registers took 10.7 K cycles a chunk).
+// The chain X, R, U, dS, S of one chunk after the other is the bound: 5 K cycles, 2.6 us, of which
+// the products are 1.8 K (46 cycles for one of 128 x 64 x 16, 65 for 128 x 128 x 16, A in tensor
+// memory) and their three round trips 1.1 K; the rest are the makers' instructions.  The roles
+// keep all else off the chain, and an SM has one CTA, whose registers then let a warp have all its
+// values of a step in flight (two CTAs of half as many registers took 10.7 K cycles a chunk).
+// An item's begin and end take 7 to 10 us.  12 heads: 16384 tokens in segments take 107 us (first
+// pass) and 62, 128 sequences of 117,555 tokens 488 us, the tensor pipe active for 24 % of the time.
 //
 // Rounding.  Operands are fp16: k exactly, up to its row's power of two; S, R, U and T as
 // the sum of two (22 bits; with one, a state would be off by 2^-12).  The outputs' own terms,

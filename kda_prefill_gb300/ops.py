@@ -158,9 +158,11 @@ def gated_delta_fwd(q, k, v, log_decay, beta, cu_seqlens, *, state_cache, state_
         S_t = exp(g_t) S_{t-1} (I - beta_t k_t k_t^T) + beta_t v_t k_t^T,  o_t = scale * S_t q_t
 
     with q and k divided by their lengths.  Tensors, pool and options are those of
-    ``lin_attn_fwd``; ``beta`` is contiguous fp32 [1, T, H] (or [T, H]), from 0 to 2.
-    Prompts, ragged batches and single tokens go in one call.  Writes ``out`` and
-    the selected pool slots in place and returns ``out``."""
+    ``lin_attn_fwd``; ``beta`` is contiguous fp32 [1, T, H] (or [T, H]), from 0 to 2,
+    ``log_decay`` at most 0 (below -104 a token clears the state).  Prompts, ragged
+    batches and single tokens go in one call.  The workspace holds what the chunks of
+    long sequences need, 59 KB for 64 tokens and a head.  Writes ``out`` and the
+    selected pool slots in place and returns ``out``."""
     lib = load_library()
     dev, at = q.device, q.get_device()
     T, Hk, H, N, (q_st, q_sh, k_st, k_sh, v_st, v_sh) = _packed(
