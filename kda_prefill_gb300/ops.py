@@ -432,6 +432,63 @@ def qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, *, layout: str =
     None.  The other arguments are those of ``rope``; without ``q_out`` and ``k_out``
     it works in place.  Returns (q_out, k_out)."""
     lib = load_library()
+    q_out = q if q_out is None else q_out
+    both = k is not None
+    tensors = None
+    if both:
+        k_out = k if k_out is None else k_out
+        tensors = _usual_turn(q, k, q_out, k_out, q_weight, k_weight, positions, inv_freq)
+    if tensors is None or layout not in _LAYOUTS:
+        tensors = _checked_turn(q, k, q_out, k_out, q_weight, k_weight, positions, inv_freq, layout)
+    _on_current_device(q.get_device())
+    freqs = inv_freq.numel()
+    rc = lib.kda_qk_norm_rope(tensors, 2 if both else 1, float(eps), positions.data_ptr(), positions.element_size(),
+                              inv_freq.data_ptr(), positions.numel(), q.shape[-1], 2 * freqs,
+                              _LAYOUTS[layout], float(factor), _DTYPES[q.dtype], _stream(stream, q.device))
+    if rc != KDA_OK:
+        _check(rc, lib)
+    return q_out, k_out
+
+
+def _usual_turn(q, k, q_out, k_out, q_weight, k_weight, positions, inv_freq):
+    """The tensors' fields of a ``qk_norm_rope`` call, packed, after one look at the usual
+    forms; None for any other, which ``_checked_turn`` takes or says what is wrong with."""
+    qs, ks = q.shape, k.shape
+    if len(qs) != 4 or len(ks) != 4:
+        return None
+    one, T, H, D = qs
+    one_k, Tk, Hk, Dk = ks
+    (_, q_st, q_sh, q_1), (_, k_st, k_sh, k_1) = q.stride(), k.stride()
+    at, dtype, f32 = q.get_device(), q.dtype, torch.float32
+    if not (at >= 0 and one == one_k == 1 and T == Tk > 1 and D == Dk and H > 1 and Hk > 1 and q_1 == k_1 == 1
+            and dtype in _DTYPES and k.dtype is dtype and k.get_device() == at
+            and positions.dtype in (torch.int64, torch.int32) and positions.get_device() == at
+            and positions.numel() == T and positions.is_contiguous()
+            and inv_freq.dtype is torch.float64 and inv_freq.get_device() == at and inv_freq.dim() == 1
+            and inv_freq.is_contiguous() and 2 * inv_freq.numel() <= D):
+        return None
+    out = (q_st, q_sh), (k_st, k_sh)
+    if q_out is not q or k_out is not k:
+        (_, qo_st, qo_sh, qo_1), (_, ko_st, ko_sh, ko_1) = (x.stride() if x.dim() == 4 else (0, 0, 0, 0) for x in (q_out, k_out))
+        if not (q_out.shape == qs and k_out.shape == ks and qo_1 == ko_1 == 1 and q_out.dtype is k_out.dtype is dtype
+                and q_out.get_device() == k_out.get_device() == at):
+            return None
+        out = (qo_st, qo_sh), (ko_st, ko_sh)
+    weights = []
+    for w, heads in ((q_weight, H), (k_weight, Hk)):
+        if w is None:
+            weights += 0, 0
+            continue
+        ws = w.shape
+        if not (w.dtype is f32 and w.get_device() == at and w.is_contiguous() and (ws == (D,) or ws == (heads, D))):
+            return None
+        weights += w.data_ptr(), D if len(ws) == 2 else 0
+    return _NORM_ROPE_TENSORS.pack(q.data_ptr(), q_out.data_ptr(), q_st, q_sh, *out[0], H, *weights[:2],
+                                   k.data_ptr(), k_out.data_ptr(), k_st, k_sh, *out[1], Hk, *weights[2:])
+
+
+def _checked_turn(q, k, q_out, k_out, q_weight, k_weight, positions, inv_freq, layout):
+    """The same, every argument checked for itself."""
     rows, D = _rope_rows(q, k, positions, inv_freq, layout, q_out, k_out)
     if k is None and k_weight is not None:
         raise ValueError("k_weight is given without k")
@@ -444,12 +501,7 @@ def qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, *, layout: str =
     tensors = _NORM_ROPE_TENSORS.pack(*rows[0], *_head_weight(q_weight, "q_weight", rows[0][6], D), *fields)
     if q_weight is not None and q_weight.get_device() != at:
         _same_device(q.device, q_weight=q_weight)
-    rc = lib.kda_qk_norm_rope(tensors, len(rows), float(eps), positions.data_ptr(), positions.element_size(),
-                              inv_freq.data_ptr(), positions.numel(), D, 2 * inv_freq.numel(),
-                              _LAYOUTS[layout], float(factor), _DTYPES[q.dtype], _stream(stream, q.device))
-    if rc != KDA_OK:
-        _check(rc, lib)
-    return q if q_out is None else q_out, k if k_out is None else k_out
+    return tensors
 
 
 def gated_norm(x, weight=None, *, gate=None, activation: str = "sigmoid", eps: float = 1e-6,

@@ -188,3 +188,33 @@ def test_single_tokens_first_seen_in_a_capture():
         call()
         assert list(kda.ops._headers) == [torch.cuda.current_device()]
         check(c, out, want, before)
+
+
+def test_the_quick_look_hands_over_what_the_checks_do():
+    """The binding's look at the usual forms gives the fields that the checks of each argument
+    give, and leaves every other form to them."""
+    ops = kda.ops
+    x = torch.randn(1, 6, 9, D, device="cuda").bfloat16()
+    q, k = x[:, :, :4], x[:, :, 4:6]
+    qo, ko = torch.empty(1, 6, 4, D, device="cuda").bfloat16(), torch.empty(1, 6, 2, D, device="cuda").bfloat16()
+    w, wq, wk = torch.ones(D, device="cuda"), torch.ones(4, D, device="cuda"), torch.ones(2, D, device="cuda")
+    pos, freq = torch.arange(6, device="cuda"), kda.rope_frequencies(D)[0]
+    taken = [(q, k, q, k, w, w, pos, freq), (q, k, qo, ko, None, wk, pos.int(), freq), (q, k, q, ko, wq, None, pos, freq[:8]),
+             (qo, ko, qo, ko, None, None, pos, freq)]
+    for a in taken:
+        assert ops._usual_turn(*a) == ops._checked_turn(*a, "half")
+    left = [(q[0], k[0], q[0], k[0], w, w, pos, freq), (q[:, :1], k[:, :1], q[:, :1], k[:, :1], w, w, pos[:1], freq),
+            (q[:, :, :1], k, q[:, :, :1], k, w, w, pos, freq), (q, k, qo, ko[0], w, w, pos, freq)]
+    for a in left:
+        assert ops._usual_turn(*a) is None
+        ops._checked_turn(*a, "half")
+    wrong = [(q, k.half(), q, k.half(), w, w, pos, freq), (q, k, qo.float(), ko, w, w, pos, freq),
+             (q, k, q, k, w.half(), w, pos, freq), (q, k, q, k, wk, w, pos, freq), (q, k, q, k, w, w[::2], pos, freq),
+             (q, k, q, k, w, w, pos[:5], freq), (q, k, q, k, w, w, pos.float(), freq), (q, k, q, k, w, w, pos, freq.float()),
+             (q, k, q, k, w, w, pos, torch.cat([freq, freq])), (q, k[:, :5], q, k[:, :5], w, w, pos, freq),
+             (q, k, qo[..., :64], ko, w, w, pos, freq), (q[..., ::2], k[..., ::2], q[..., ::2], k[..., ::2], None, None, pos, freq[:8]),
+             (q, k, q, k, w, w, pos.cpu(), freq), (q, k, q, k, w.cpu(), w, pos, freq)]
+    for i, a in enumerate(wrong):
+        assert ops._usual_turn(*a) is None, i
+        with pytest.raises((TypeError, ValueError)):
+            ops._checked_turn(*a, "half")
