@@ -437,7 +437,7 @@ KDA_API size_t kda_lin_attn_workspace_size(int64_t total_tokens, int32_t num_seq
  *   workspace        at least kda_gated_delta_workspace_size() bytes, 256-byte
  *                    aligned; kda_check_status() reads its status word.
  *
- * Sequences of at most 8 tokens go token by token, longer ones in chunks of 64, a
+ * Sequences of at most 16 tokens go token by token, longer ones in chunks of 64, a
  * few long ones in segments besides; a call's sums are made in the same order every
  * time.  States are fp32 while they are carried, and the products' operands have 22
  * bits or more; those of the outputs alone have 11 (out has 8).

@@ -8,8 +8,8 @@
 // on sums.
 //
 // Memory is the bound for single tokens: 512 of them, 12 heads, take 122.8 us with an fp32 pool (97 %
-// of a copy's rate) and 67.6 us with a bf16 one (89 %); each further token costs about 15 us,
-// instructions.
+// of a copy's rate) and 67.6 us with a bf16 one (89 %); each token after the
+// second costs about 20 us, instructions.
 //
 // A CTA of four warps has 32 or 128 value rows of one (sequence, head) state, a warp eight
 // rows at a time, eight lanes a row: a lane has sixteen key columns of every fourth row, in 16-byte
@@ -31,10 +31,10 @@ constexpr int kAcross = 8;                    // lanes of a row
 constexpr int kStep = 32 / kAcross;           // rows between a lane's
 constexpr int kHeld = kRows / kStep;          // rows a lane has part of
 constexpr int kPairs = D / kAcross / 2;       // pairs of columns of a row a lane has
-constexpr int kToks = kShortMax;
 
 struct alignas(16) Token {
-    float k[D], q[D], v[D];
+    float k[D], q[D];  // a row's lanes' first four columns beside each other, then their next
+    float v[D];
     float d, one;  // e^g = one + d
     float rk, rq;  // 1 / |k|, 1 / |q|
     float kq, beta;
@@ -87,16 +87,21 @@ __device__ __forceinline__ Rows load_token(const DeltaParams& p, int64_t t, int 
     return {row(p.k, p.k_st, (int64_t)(h / p.rep) * p.k_sh), row(p.q, p.q_st, (int64_t)(h / p.rep) * p.q_sh),
             row(p.v, p.v_st, (int64_t)h * p.v_sh), p.g[t * p.g_st + h], p.beta[t * p.H + h]};
 }
+template <class C>
 __device__ __forceinline__ void make_token(const Rows& x, int lane, Token& to) {
+    // its four columns are the `four`-th of lane `of`'s
+    constexpr int kFours = C::kN / 4;  // of a piece
+    const int piece = lane / (kFours * kAcross), of = lane / kFours % kAcross, four = piece * kFours + lane % kFours;
+    const int at = (four * kAcross + of) * 4;
     const auto row = [&](uint2 w, float* out, f2 (&f)[2]) {
         f[0] = bf16x2(w.x), f[1] = bf16x2(w.y);
-        *reinterpret_cast<ulonglong2*>(out + 4 * lane) = make_ulonglong2(f[0], f[1]);
+        *reinterpret_cast<ulonglong2*>(out) = make_ulonglong2(f[0], f[1]);
     };
     const float g = x.g;
     f2 k[2], q[2], v[2];
-    row(x.k, to.k, k);
-    row(x.q, to.q, q);
-    row(x.v, to.v, v);
+    row(x.k, to.k + at, k);
+    row(x.q, to.q + at, q);
+    row(x.v, to.v + 4 * lane, v);
     const auto dot = [](const f2 (&a)[2], const f2 (&b)[2]) {
         const float2 s = unpack2(fma2(a[0], b[0], mul2(a[1], b[1])));
         return s.x + s.y;
@@ -126,9 +131,9 @@ template <class S, int kPasses>
 __global__ void __launch_bounds__(kWarps * 32, kPasses == 1 ? 6 : sizeof(S) == 4 ? 4 : 5)
 kda_delta_step(const __grid_constant__ DeltaParams p) {
     using C = Cols<S>;
-    __shared__ Token tokens[kToks];
+    extern __shared__ Token tokens[];  // of a sequence
     const int h = blockIdx.y, ctas = kParts / kPasses;
-    const int n = p.short_list[blockIdx.x / ctas];
+    const int i = blockIdx.x / ctas, n = i < p.n_short ? p.short_list[i] : p.mid_list[i - p.n_short];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int at = lane % kAcross, part = lane / kAcross;  // rows part, part + 4 of the eight
     const int own = at % kHeld;                            // the held row whose output this lane makes
@@ -147,7 +152,7 @@ kda_delta_step(const __grid_constant__ DeltaParams p) {
     if (t0 + warp < t1) rows = load_token(p, t0 + warp, h, lane);
     if (init) load(state);
     for (int t = t0 + warp; t < t1; t += kWarps) {
-        make_token(rows, lane, tokens[t - t0]);
+        make_token<C>(rows, lane, tokens[t - t0]);
         if (t + kWarps < t1) rows = load_token(p, t + kWarps, h, lane);
     }
     __syncthreads();
@@ -170,7 +175,7 @@ kda_delta_step(const __grid_constant__ DeltaParams p) {
             f2 k[kPairs], sum[2 * kHeld] = {};
 #pragma unroll
             for (int i = 0; i < kPairs; i += 2) {
-                const int c = C::at(at, 2 * i / C::kN) + 2 * i % C::kN;
+                const int c = (i / 2 * kAcross + at) * 4;
                 const ulonglong2 kk = *reinterpret_cast<const ulonglong2*>(x.k + c), qq = *reinterpret_cast<const ulonglong2*>(x.q + c);
                 k[i] = kk.x, k[i + 1] = kk.y;
 #pragma unroll
@@ -232,8 +237,9 @@ kda_delta_step(const __grid_constant__ DeltaParams p) {
 template <class S, int kPasses>
 cudaError_t launch(const DeltaParams& p, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)p.n_short * (kParts / kPasses), (unsigned)p.H);
+    cfg.gridDim = dim3((unsigned)(p.n_short + p.n_mid) * (kParts / kPasses), (unsigned)p.H);
     cfg.blockDim = dim3(kWarps * 32);
+    cfg.dynamicSmemBytes = sizeof(Token) * (p.n_mid > 0 ? kDeltaStepMax : kShortMax);
     cfg.stream = s;
     // right behind the walk, beside its CTAs
     cudaLaunchAttribute attr[1];
@@ -248,14 +254,14 @@ cudaError_t launch(const DeltaParams& p, cudaStream_t s) {
     // Few states: 32 rows a CTA, for the latency; many: 128, whose loads overlap and which share
     // what belongs to a token.  12 heads, fp32 pool: 16 sequences of 4 tokens 10.4 and 12.5 us, 50
     // of them 18.6 and 16.8; 512 single tokens, bf16 pool: 82 and 68 us
-    if ((int64_t)p.n_short * p.H * kParts <= 8 * num_sms()) return launch<S, 1>(p, s);
+    if ((int64_t)(p.n_short + p.n_mid) * p.H * kParts <= 8 * num_sms()) return launch<S, 1>(p, s);
     return launch<S, kParts>(p, s);
 }
 
 }  // namespace
 
 cudaError_t launch_delta_step(const DeltaParams& p, cudaStream_t s) {
-    if (p.n_short <= 0) return cudaSuccess;
+    if (p.n_short + p.n_mid <= 0) return cudaSuccess;
     if (p.st_dtype == KDA_STATE_F32) return launch<float>(p, s);
     if (p.st_dtype == KDA_STATE_BF16) return launch<__nv_bfloat16>(p, s);
     return launch<__half>(p, s);

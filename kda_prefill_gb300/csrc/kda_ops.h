@@ -105,11 +105,17 @@ struct DeltaParams : LinParams {
     const float* beta;  // [T][H]
     const int32_t *seq_off, *chunk_seq, *chunk_tok;
     int64_t n_chunks;
+    const int32_t* mid_list;  // sequences beside short_list's that go token by token
+    int n_mid;
     uint8_t* blocks;  // [n_chunks][H] of kDeltaBlock bytes
     // of the cut sequences' segments: `planes` has two of [128 x 128] for each segment and
     // head, its state from zero (then the one that the next starts from) and its transition,
     // `kept` what the transition is to be multiplied by, or -1 where a token clears the state
 };
+// Sequences of at most so many tokens go token by token: 512 of 9, 12 and 16 tokens of 12 heads
+// take 250, 318 and 413 us (fp32 pool; bf16 232, 301 and 396) instead of 467 (401) in a chunk, one of
+// them 8.4 to 12.5 us instead of 15.
+constexpr int kDeltaStepMax = 16;
 // What kda_delta_chunk leaves for the walk of a chunk and head: fp32 scalars, and fp16 tiles in
 // the swizzled layout of kda_device.cuh.
 //   k   [64][128]  k times a power of two for each row
@@ -149,9 +155,9 @@ inline int64_t delta_planes(int64_t T, int64_t H) {
 }
 // Chooses n_cut, n_seg, seg_len and the cuts.
 void delta_cut(DeltaParams& p, LinCuts& cuts, const SeqTables& t);
-// The short sequences token by token (kda_delta_step.cu).
+// The sequences of at most kDeltaStepMax tokens (kda_delta_step.cu).
 cudaError_t launch_delta_step(const DeltaParams& p, cudaStream_t s);
-// The long sequences' chunks, each for itself (kda_delta_chunk.cu), and the walk over them
+// The other sequences' chunks, each for itself (kda_delta_chunk.cu), and the walk over them
 // (kda_delta_walk.cu).
 cudaError_t launch_delta_chunk(const DeltaParams& p, cudaStream_t s);
 cudaError_t launch_delta_walk(const DeltaParams& p, const LinCuts& cuts, cudaStream_t s);

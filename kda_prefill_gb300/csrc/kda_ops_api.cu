@@ -255,6 +255,9 @@ int enqueue_delta(void* arg, const kda::SeqTables& t) {
     p.short_list = t.short_list;
     p.n_long = t.n_long;
     p.n_short = t.n_short;
+    while (p.n_long > 0 && t.long_lens[p.n_long - 1] <= kda::kDeltaStepMax) --p.n_long;
+    p.mid_list = t.long_list + p.n_long;
+    p.n_mid = t.n_long - p.n_long;
     p.seq_off = t.seq_off;
     p.chunk_seq = t.chunk_seq;
     p.chunk_tok = t.chunk_tok;

@@ -218,3 +218,22 @@ def test_the_quick_look_hands_over_what_the_checks_do():
         assert ops._usual_turn(*a) is None, i
         with pytest.raises((TypeError, ValueError)):
             ops._checked_turn(*a, "half")
+
+
+@pytest.mark.parametrize("pool", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("lengths", [[16, 9, 17, 3, 12, 0, 100, 15, 1], [9] * 5, [16, 8, 16], [17, 16], [10] * 150 + [1] * 150])
+def test_lengths_about_where_chunks_begin(lengths, pool):
+    go(make(lengths, 3, 1, seed=50, pool=pool))
+
+
+def test_bad_slots_of_token_by_token_sequences():
+    c = make([12, 9, 2], 2, seed=51, init=[True] * 3)
+    c["idx"][0] = -1
+    before = c["storage"].clone()
+    ws = workspace(c, 0xFF)
+    run(c, workspace=ws)
+    torch.cuda.synchronize()
+    assert kda.check_status(ws) == kda.STATUS_BAD_SLOT
+    keep = torch.ones(len(before), dtype=torch.bool, device="cuda")
+    keep[c["idx"][1:].long().cuda()] = False
+    assert torch.equal(c["storage"][keep].view(torch.int32), before[keep].view(torch.int32))
