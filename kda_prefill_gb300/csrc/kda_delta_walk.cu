@@ -720,8 +720,9 @@ __device__ __forceinline__ bool make(const DeltaParams& p, int k, int& n, int& n
     };
     if ((values && !wait(kTurned + (nv & 1), nv >> 1)) || !wait(kFull + (n & 1), n >> 1)) return false;
     rescale(n, nv, 0.f);
-    store_s(0, finite(smax));
-    store_s(1, finite(smax));
+    // (the whole row's: with one entry that is not finite, the scale bounds none of the others)
+    store_s(0, finite(was));
+    store_s(1, finite(was));
     tmem_wait_st();
     arrive_warp(kSReady, lane);
     arrive_warp(kSReady + 1, lane);
