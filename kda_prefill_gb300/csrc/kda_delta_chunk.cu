@@ -59,7 +59,7 @@ struct Vecs {
     float ck[C];      // what makes k's length one (0 if k is not finite)
     float ks[C];      // the same for the scaled k (NaN)
     float rk[C];      // that and e^{G_b - G_j}
-    float cq[C];
+    float cq[C];      // what makes q's length one (NaN if q is not finite)
     float bk[C];      // beta ck
     float eg[C];      // e^G up
     float up[C];
@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, 4) kda_delta_chunk(const __grid_cons
             const float one = 1.f / sqrtf(mine + 1e-6f);
             vec.ck[row] = fine ? one : 0.f;
             vec.ks[row] = fine ? one * __uint_as_float((uint32_t)(127 + length_of(mine)) << 23) : NAN;
-            vec.cq[row] = 1.f / sqrtf(qq + 1e-6f);
+            vec.cq[row] = qq < INFINITY ? 1.f / sqrtf(qq + 1e-6f) : NAN;
         }
     }
     // sums of decays within the block, up to the token and behind it

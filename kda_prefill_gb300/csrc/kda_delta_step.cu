@@ -119,8 +119,9 @@ __device__ __forceinline__ void make_token(const Rows& x, int lane, Token& to) {
     if (lane == 0) {
         to.d = slow ? expm1f(g) : expf(g);
         to.one = slow ? 1.f : 0.f;
-        to.rk = 1.f / sqrtf(kk + 1e-6f);
-        to.rq = 1.f / sqrtf(qq + 1e-6f);
+        // (a sum that overflows has no length to divide by: as if the row were not finite)
+        to.rk = kk < INFINITY ? 1.f / sqrtf(kk + 1e-6f) : NAN;
+        to.rq = qq < INFINITY ? 1.f / sqrtf(qq + 1e-6f) : NAN;
         to.kq = kq;
         to.beta = x.beta;
         to.clears = g < kMinDecay;

@@ -5,7 +5,7 @@ bound as well."""
 import pytest
 import torch
 
-from tests.test_gpu_gated_delta import D, expected, make, run
+from tests.test_gpu_gated_delta import D, check, expected, make, run
 
 pytestmark = pytest.mark.gpu
 
@@ -42,3 +42,33 @@ def test_one_entry_beside_large_ones_and_an_early_clear(n, clear, silent, bad, p
     keep[slot] = False
     bits = torch.int16 if pool == torch.float16 else torch.int32
     assert torch.equal(c["storage"][keep].view(bits), before[keep].view(bits))
+
+
+@pytest.mark.parametrize("n", [1, 8, 16, 17, 200])
+@pytest.mark.parametrize("where", ["q", "k"])
+def test_finite_rows_whose_squares_are_not(n, where):
+    """Entries of 1e20: |q|^2 and |k|^2 are infinite in fp32, so such a row counts as one that is
+    not finite, however long its sequence."""
+    t, clear = n // 2, n - 1
+    g = torch.full((1, 2 * n, 2), -0.1)
+    if n > 4:
+        g[:, clear] = g[:, n + clear] = -torch.inf
+    c = make([n, n], 2, seed=61, g=g, init=[True, True])
+    want, before = expected(c), c["storage"].clone()
+    c[where][0, t, 0] = 1e20 * torch.sign(c[where][0, t, 0])
+    assert bool(torch.isfinite(c[where]).all())
+    out = run(c)[0].double()
+    torch.cuda.synchronize()
+    hit = torch.zeros_like(out, dtype=torch.bool)
+    if where == "q":
+        hit[t, 0] = True
+    else:
+        hit[t:clear if n > 4 else n, 0] = True
+    assert torch.isnan(out[hit]).all()
+    err, lim = (out - want[0]).abs(), 2.0 ** -8 * want[0].abs() + 2.0 ** -9 * want[2] + 1e-30
+    assert bool((err <= lim)[~hit].all())
+    if where == "q" or n > 4:
+        check(c, torch.where(hit, want[0], out)[None], want, before)
+    else:
+        got = c["cache"][c["idx"].long().cuda()]
+        assert torch.isnan(got[0, 0]).all() and torch.isfinite(got[1]).all() and torch.isfinite(got[0, 1]).all()
