@@ -520,7 +520,7 @@ KDA_API int kda_rope(const kda_rope_tensor* tensors, int32_t num_tensors,
  *     y = x / sqrt(mean(x^2) + eps) * weight,   y's first rot_dim dimensions turned
  *
  * All of it in fp32, rounded once.  A row that is not finite, or whose sum of squares
- * is not, spoils itself alone; with eps = 0 a row of zeros does, too.
+ * is not, becomes NaN, and it alone; with eps = 0 a row of zeros does, too.
  *
  *   tensors       1 or 2 of them (q and k), their `x` as in kda_rope.  `weight`
  *                 is device fp32 [head_dim], or [num_heads][head_dim] with

@@ -139,7 +139,8 @@ kda_qk_norm_rope(const __grid_constant__ NormRopeParams p, int tokens, int rot_u
                 }
                 const float2 both = unpack2(sum);
                 const float all = group_sum<LANES>(live ? both.x + both.y : 0.f);
-                const float inv = rsqrtf(fmaf(all, per, p.eps));
+                // (a sum that overflows leaves no row to give: infinity times zero makes it NaN, not zeros)
+                const float inv = rsqrtf(fmaf(all, 0.f, fmaf(all, per, p.eps)));
                 const f2 inv2 = pack2(inv, inv);
                 if (t + i < n) {
 #pragma unroll
@@ -218,7 +219,8 @@ kda_qk_norm_rope_long(const __grid_constant__ NormRopeParams p, int tokens, int 
 #pragma unroll
             for (int j = 0; j < VE; ++j) sum = fmaf(f[j], f[j], sum);
         }
-        const float inv = 1.f / sqrtf(group_sum<32>(sum) / (float)p.D + p.eps);
+        sum = group_sum<32>(sum);
+        const float inv = sum < INFINITY ? 1.f / sqrtf(sum / (float)p.D + p.eps) : NAN;
         __syncwarp();  // in place: all lanes have read the row
         for (int u = lane; u < units; u += 32) {
             const bool turned = u < rot_units;
