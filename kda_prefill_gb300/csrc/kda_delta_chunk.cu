@@ -2,14 +2,15 @@
 // not need the state.  With G the prefix sums of the log decays, k^ and q^ of length one:
 //
 //     A_ij = beta_i e^{G_i - G_j} k^_i . k^_j  (j < i)      T = (1 + A)^-1
-//     P_ij = e^{G_i - G_j} q^_i . k^_j  (j <= i)            P T
+//     P_ij = e^{G_i - G_j} q^_i . k^_j  (j <= i)
 //
 // so that for an incoming state S, with R = beta (V - e^G K^ S^T), the chunk's writes are
-// U = T R and its outputs e^G Q^ S^T + (P T) R.
+// U = T R and its outputs e^G Q^ S^T + P U.
 //
 // A CTA takes a chunk and head.  The scores are products of k and q as they come, exact but
-// for the sums; their lengths are factors on them.  For the walk rows of k are scaled by powers
-// of two, so that they are exact in fp16.  T is solved in the four 16 x 16 blocks on the diagonal in fp32,
+// for the sums; their lengths are factors on them.  For the walk rows of k and q are scaled by powers
+// of two: a bf16 value is exact in fp16 down to 2^-17 of its row's length, smaller ones are off
+// by at most 2^-24 of it.  T is solved in the four 16 x 16 blocks on the diagonal in fp32,
 // column by column, a lane each, then in blocks twice as large from the two on their diagonal,
 // the one below being T22 N21 T11, N = -A: 16-bit MMAs of operands that are sums of two fp16 (22
 // bits, as T's in the end).  A power series of N would cancel: with equal keys its terms
@@ -22,8 +23,13 @@
 // that port); four CTAs an SM fill each other's waits.  With k and q left to the walk, to make
 // the tiles itself, this kernel took 59 us, but the walk 176 instead of 140.
 //
-// q e^G would leave fp16's range where a chunk's decays are strong, while P T, at most one,
-// does not: rows of both are multiplied by a power of two, up to 2^15, that brings e^G near one.
+// An output's two terms may cancel (a large value overwritten by a small one), so neither is rounded to
+// 11 bits: q^ e^G is m 2^x q with 1 <= m < 2, and the row of q takes 2^x alone, P's row 1 / m and
+// the output m; P is the sum of two fp16.  q^ e^G would leave fp16's range where a chunk's decays are
+// strong, while P, at most one, does not: rows of both are multiplied by a power of two, up to
+// 2^15, that brings e^G near one.  The quarters of T and P above the diagonal are not read: P's low
+// part stands in them, so that the block is no larger for it (with 8 KB more this kernel took 72 us
+// instead of 61, the last walk 76 instead of 70).
 //
 // Decays are sums of the decays between two tokens, never differences of sums over the
 // chunk, which lose the bits of weak decays behind strong ones.  In the 16 x 16 blocks on the
@@ -51,7 +57,7 @@ constexpr int kLdE = 20; // floats of a row of the fp32 blocks on the diagonal
 constexpr int kTile = C * C * 2;
 constexpr int kSmK = 0;                   // k; then N below the diagonal blocks, high and low part; above them Y
 constexpr int kSmQ = kSmK + C * D * 2;    // q; then T, high and low part
-constexpr int kSmP = kSmQ + C * D * 2;    // P; then P T
+constexpr int kSmP = kSmQ + C * D * 2;    // P's high part
 constexpr int kSmE = kSmP + kTile;        // blocks on the diagonal, transposed: e^{G_i - G_j}; then N
 constexpr int kSmVec = kSmE + (C * kLdE + 4 * C / B) * 4;
 struct Vecs {
@@ -59,10 +65,9 @@ struct Vecs {
     float ck[C];      // what makes k's length one (0 if k is not finite)
     float ks[C];      // the same for the scaled k (NaN)
     float rk[C];      // that and e^{G_b - G_j}
-    float cq[C];      // what makes q's length one (NaN if q is not finite)
+    float cq[C];      // what makes q's length one (NaN if q is not finite); then P's rows' factor
     float bk[C];      // beta ck
-    float eg[C];      // e^G up
-    float up[C];
+    float two[C];     // q's rows' power of two
     float f[3][C];    // e^{G_i - G_b} of the blocks before token i's
     float total[4];   // decays over a block
     unsigned clears[2];
@@ -149,12 +154,13 @@ __device__ __forceinline__ uint4 times(uint4 v, float f) {
 }
 
 // Two values as the sum of two fp16 each.
-__device__ __forceinline__ void put_split(uint8_t* at, f2 x) {
+__device__ __forceinline__ void put_split(uint8_t* at, uint8_t* lo, f2 x) {
     const uint32_t hi = half2_of(x);
     const float2 f = __half22float2(reinterpret_cast<const __half2&>(hi));
     *reinterpret_cast<uint32_t*>(at) = hi;
-    *reinterpret_cast<uint32_t*>(at + kTile) = half2_of(fma2(pack2(f.x, f.y), pack2(-1.f, -1.f), x));
+    *reinterpret_cast<uint32_t*>(lo) = half2_of(fma2(pack2(f.x, f.y), pack2(-1.f, -1.f), x));
 }
+__device__ __forceinline__ void put_split(uint8_t* at, f2 x) { put_split(at, at + kTile, x); }
 // 16 rows from r0 and 8 columns from n0 of a b, over K from a's column ca and b's row rb on, all
 // of them sums of two fp16; into the tile `to` at row r1, column n1.
 template <int K>
@@ -301,11 +307,14 @@ __global__ void __launch_bounds__(kThreads, 4) kda_delta_chunk(const __grid_cons
         scal->c[tid] = eg * ks;
         scal->beta[tid] = beta;
         scal->w[tid] = 0.5f * expf(rest) * zero_if_nan(ks);
-        scal->down[tid] = __uint_as_float((uint32_t)(127 - e) << 23);
+        // q^ e^G up = m 2^x q, 1 <= m < 2: the row of q takes 2^x, those of P and the output take 1 / m and m
+        const uint32_t f = __float_as_uint(vec.cq[tid] * (eg * up));
+        const float m = f < 0x7F800000u ? __uint_as_float((f & 0x007FFFFFu) | 0x3F800000u) : NAN;
+        scal->down[tid] = m * __uint_as_float((uint32_t)(127 - e) << 23);
         vec.rk[tid] = zero_if_nan(ex2(suf * kLog2e)) * ck;
         vec.bk[tid] = -zero_if_nan(beta * ck);
-        vec.eg[tid] = eg * up;
-        vec.up[tid] = up;
+        vec.two[tid] = __uint_as_float(f & 0x7F800000u);
+        vec.cq[tid] = vec.cq[tid] * up / m;
         if (tid == C - 1) {
             scal->gamma = eg;
             const unsigned lo = vec.clears[0], hi = vec.clears[1];
@@ -315,9 +324,9 @@ __global__ void __launch_bounds__(kThreads, 4) kda_delta_chunk(const __grid_cons
         }
     }
     __syncthreads();
-    // q^ e^G
+    // q
     {
-        const float f[2] = {vec.cq[r] * vec.eg[r], vec.cq[r + 4] * vec.eg[r + 4]};
+        const float f[2] = {vec.two[r], vec.two[r + 4]};
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             *reinterpret_cast<uint4*>(blk + kDeltaQ + sw128_off(r + 4 * (i >> 1), col + 64 * (i & 1), C)) = times(q[i], f[i >> 1]);
@@ -367,35 +376,40 @@ __global__ void __launch_bounds__(kThreads, 4) kda_delta_chunk(const __grid_cons
             const float b = vec.bk[i], cq = vec.cq[i];
             const f2 bb = pack2(b, b), cc = pack2(cq, cq);
             uint8_t *const nrow = nt + i * 128, *const prow = smem + kSmP + i * 128;
+            // P's low part in the quarters above the diagonal
+            uint8_t* const lrow = (c0 ? smem + kSmP : r0 < 32 ? tt : tt + kTile) + (i & 31) * 128;
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 const int j = c0 + t * 8 + cj, bj = (c0 + t * 8) / B;
-                uint32_t pv = 0;
+                f2 pv = 0;
                 if (bj < bi) {
                     const float f = vec.f[bj][i];
                     const f2 l = mul2(pack2(f, f), *reinterpret_cast<const f2*>(vec.rk + j));
                     put_split(nrow + y[t], mul2(mul2(bb, l), pack2(kk[t][2 * half], kk[t][2 * half + 1])));
-                    pv = half2_of(mul2(mul2(cc, l), pack2(qk[t][2 * half], qk[t][2 * half + 1])));
+                    pv = mul2(mul2(cc, l), pack2(qk[t][2 * half], qk[t][2 * half + 1]));
                 } else if (bj == bi) {
                     const f2 l = mul2(pack2(e[t & 1][half][0], e[t & 1][half][1]), *reinterpret_cast<const f2*>(vec.ck + j));
                     const float2 nv = unpack2(mul2(mul2(bb, l), pack2(kk[t][2 * half], kk[t][2 * half + 1])));
                     const float2 q = unpack2(mul2(mul2(cc, l), pack2(qk[t][2 * half], qk[t][2 * half + 1])));
                     e32[e_at(j) + i - r0] = j < i ? nv.x : 0.f;
                     e32[e_at(j + 1) + i - r0] = j + 1 < i ? nv.y : 0.f;
-                    pv = pack_half2(j <= i ? q.x : 0.f, j + 1 <= i ? q.y : 0.f);
+                    pv = pack2(j <= i ? q.x : 0.f, j + 1 <= i ? q.y : 0.f);
                 }
-                *reinterpret_cast<uint32_t*>(prow + y[t]) = pv;
+                if (below) put_split(prow + y[t], lrow + (c0 ? y[t] : y[t] ^ 64), pv);
             }
         }
-        // T is zero right of its diagonal blocks
-#pragma unroll
-        for (int x = tid; x < 2 * C * (C / 8); x += kThreads) {
-            const int row = x >> 3 & (C - 1), c = (x & 7) * 8;
-            if (c >= (row & ~(B - 1)) + B)
-                *reinterpret_cast<uint4*>(tt + (x >> 9) * kTile + sw64_off(row, c)) = make_uint4(0, 0, 0, 0);
+        // T is zero right of its diagonal blocks, within the quarters that are read
+        if (tid < 128) {
+            const int row = (tid >> 1 & 15) + (tid >> 5 & 1) * 32, c = (row & 32) + 16 + (tid & 1) * 8;
+            *reinterpret_cast<uint4*>(tt + (tid >> 6) * kTile + sw64_off(row, c)) = make_uint4(0, 0, 0, 0);
         }
     }
+    fence_proxy_async();
     __syncthreads();
+    if (tid == kThreads - 1) {
+        bulk_s2g(blk + kDeltaP, smem + kSmP, kTile);
+        bulk_commit();
+    }
     // the diagonal blocks of T, two a warp: a lane has a column; once row m is known its
     // multiples go to the rows below
     if (warp < 2) {
@@ -442,45 +456,8 @@ __global__ void __launch_bounds__(kThreads, 4) kda_delta_chunk(const __grid_cons
     }
     fence_proxy_async();
     __syncthreads();
-    if (tid == 0) {
+    if (tid == kThreads - 1) {
         bulk_s2g(blk + kDeltaT, tt, 2 * kTile);
-        bulk_commit();
-    }
-    // P T
-    {
-        float d[4][4] = {};
-        if (below) {
-            const uint32_t pt = smem_u32(smem + kSmP), th = smem_u32(tt);
-#pragma unroll
-            for (int ks = 0; ks < C; ks += 16) {
-                if (ks < r0 + 16 && ks + 16 > c0) {
-                    uint32_t a[4], b[4];
-                    ln.load(pt, r0, ks, a);
-#pragma unroll
-                    for (int t = 0; t < 4; t += 2) {
-                        // rows ks .. ks + 15 of T, columns c0 + 8 t .. + 15, transposed
-                        ldsm_x4_t(ln.at(th, ks, c0 + 8 * t), b[0], b[1], b[2], b[3]);
-                        mma_f16(d[t], a, b[0], b[1]);
-                        mma_f16(d[t + 1], a, b[2], b[3]);
-                    }
-                }
-            }
-        }
-        __syncthreads();
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const int ri = lane >> 2, i = r0 + half * 8 + ri;
-            const float up = vec.up[i];
-#pragma unroll
-            for (int t = 0; t < 4; ++t)
-                *reinterpret_cast<uint32_t*>(smem + kSmP + i * 128 + ((((c0 >> 3) + t) ^ ri) << 4) + (lane & 3) * 4) =
-                    pack_half2(up * d[t][2 * half], up * d[t][2 * half + 1]);
-        }
-    }
-    fence_proxy_async();
-    __syncthreads();
-    if (tid == 0) {
-        bulk_s2g(blk + kDeltaPT, smem + kSmP, kTile);
         bulk_commit();
         bulk_wait_all();
     }

@@ -1,10 +1,10 @@
 // The gated delta rule's walk over a sequence's chunks on the tensor cores (tcgen05,
 // accumulators in tensor memory).  For a chunk of C = 64 tokens with incoming state S (V x K),
-// with kda_delta_chunk's k, q, T and P T:
+// with kda_delta_chunk's k, q, T and P:
 //
 //     X = S [k q]^T                   128 x 128 x 128
 //     R = beta (V - c X_k)            in registers
-//     U = R T^T,  O = X_q + R (P T)^T 128 x 64 x 64
+//     U = R T^T,  O = X_q + U P^T     128 x 64 x 64
 //     S' = e^{G_C} S + (w U) k        128 x 128 x 64
 //
 // All products have the value rows as their M: a thread keeps a quarter of a row of S in fp32
@@ -25,9 +25,10 @@
 // An item's begin and end take 7 to 10 us.  12 heads: 16384 tokens in segments take 107 us (first
 // pass) and 62, 128 sequences of 117,555 tokens 488 us, the tensor pipe active for 24 % of the time.
 //
-// Rounding.  Operands are fp16: k exactly, up to its row's power of two; S, R, U and T as
-// the sum of two (22 bits; with one, a state would be off by 2^-12).  The outputs' own terms,
-// q e^G and P T, have one: 11 bits, beside the 8 of out.  S, R and U of a row are scaled by
+// Rounding.  Operands are fp16: k and q exactly, up to their rows' powers of two and but for entries
+// below 2^-17 of a row's length; S, R, U, T and P as the sum of two (22 bits; with one, a state would
+// be off by 2^-12, and an output, whose terms may cancel, by as much of what the state held).
+// S, R and U of a row are scaled by
 // one power of two, from a bound that holds for all three: with |v| <= m and beta <= b in the
 // chunk, |R| <= b (m + |S|) and |U| <= b (m + |S| + 64 b m), since I - beta k k^T does not
 // lengthen a row for beta in [0, 2] and a token adds at most b m; |S| itself is bounded by
@@ -60,14 +61,16 @@ constexpr int kKeys = D / 4, kToks = C / 4;  // of a maker
 
 // Shared memory.
 constexpr int kTile = C * D * 2;
-constexpr int kSmBlock = 0;                      // [2] blocks of kda_delta_chunk
-constexpr int kSmV = kSmBlock + 2 * kDeltaBlock; // v as it comes
+constexpr int kTiles = kDeltaBlock - kDeltaK;
+constexpr int kSmTiles = 0;                      // [2] the tiles of kda_delta_chunk's blocks
+constexpr int kSmScalars = kSmTiles + 2 * kTiles; // [4] their scalars, which the output rows read last
+constexpr int kSmV = kSmScalars + 4 * kDeltaK;   // v as it comes
 constexpr int kSmVT = kSmV + kTile;              // [2][128][64] v by value rows, 16-byte pieces swizzled
 constexpr int kSmVMax = kSmVT + 2 * kTile;       // [2][128] largest |v| of a value row
 constexpr int kSmSMax = kSmVMax + 2 * D * 4;     // [2][4][128] largest |S| of a quarter of a row
-constexpr int kSmBad = kSmSMax + 8 * D * 4;      // [2][128][4] tokens whose R is not finite, 16 bits a maker
-constexpr int kSmInv = kSmBad + 2 * D * 8;       // [2][128] the rows' scales undone
-constexpr int kSmBar = kSmInv + 2 * D * 4;
+constexpr int kSmBad = kSmSMax + 8 * D * 4;      // [4][128][4] tokens whose R is not finite, 16 bits a maker
+constexpr int kSmInv = kSmBad + 4 * D * 8;       // [4][128] the rows' scales undone
+constexpr int kSmBar = kSmInv + 4 * D * 4;
 enum Bar {
     kFull = 0,              // [2] block there
     kFullV = kFull + 2,
@@ -82,6 +85,7 @@ enum Bar {
     kSReady = kVEmpty + 2,  // [2] half of each part's keys
     kRReady = kSReady + 2,
     kUReady,
+    kPReady,                // U itself there, in R's place
     kMax,                   // an item's first state's largest values there
     kItem,                  // [2] item there
     kItemFree = kItem + 2,  // [2] and done with
@@ -103,7 +107,7 @@ constexpr int kSmItem = kSmMisc + 16;
 constexpr int kSmStage = (kSmItem + 2 * (int)sizeof(Item) + 127) / 128 * 128;  // [16][32][64 bytes] for each maker warp
 constexpr int kSmemBytes = kSmStage + kMakers * 2048;
 static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
-static_assert(kDeltaBlock % 1024 == 0 && kDeltaK % 1024 == 0 && kSmV % 1024 == 0 && kSmVT % 1024 == 0 && kSmBar % 8 == 0, "alignment");
+static_assert(kTiles % 1024 == 0 && kDeltaK % 1024 == 0 && kSmV % 1024 == 0 && kSmVT % 1024 == 0 && kSmBar % 8 == 0, "alignment");
 
 // Tensor memory columns.  Operands have, for 16 of their K, 8 columns of the high part and 8
 // of the low one.
@@ -117,6 +121,7 @@ constexpr uint32_t kTmDS = 256;
 constexpr uint32_t kTmO = 384;    // [2]
 
 constexpr uint32_t kIdescKK = mma_idesc(0, 0, 0, 128, 64);  // B K-major
+constexpr uint32_t kIdescHalf = mma_idesc(0, 0, 0, 128, 32);
 constexpr uint32_t kIdescKM = mma_idesc(0, 0, 1, 128, 128); // B MN-major
 
 extern __shared__ __align__(1024) uint8_t smem[];
@@ -127,6 +132,13 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, u
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
         "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
+}
+// Sixteen of K, from 16 s on, of a lower triangle's columns: of the right half the lower rows alone.
+__device__ __forceinline__ void mma_lower(uint32_t d, uint32_t a, uint64_t b, int s, uint32_t accumulate) {
+    if (s < 2)
+        mma_f16_ts(d, a, b + 2 * s, kIdescKK, accumulate);
+    else
+        mma_f16_ts(d + C / 2, a, b + 2 * s + (C / 2 * 128 >> 4), kIdescHalf, accumulate);
 }
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;
@@ -230,16 +242,17 @@ __device__ __forceinline__ void arrive_warp(int b, int lane) {
     __syncwarp();
     if (lane == 0) mbar_arrive(bar(b));
 }
-__device__ __forceinline__ uint8_t* block(int c) { return smem + kSmBlock + (c & 1) * kDeltaBlock; }
-__device__ __forceinline__ const DeltaScalars* scalars(int c) { return reinterpret_cast<const DeltaScalars*>(block(c)); }
+__device__ __forceinline__ uint8_t* tiles(int c) { return smem + kSmTiles + (c & 1) * kTiles; }
+__device__ __forceinline__ uint8_t* scalars_at(int c) { return smem + kSmScalars + (c & 3) * kDeltaK; }
+__device__ __forceinline__ const DeltaScalars* scalars(int c) { return reinterpret_cast<const DeltaScalars*>(scalars_at(c)); }
 __device__ __forceinline__ volatile float* vmax(int c) { return reinterpret_cast<volatile float*>(smem + kSmVMax) + (c & 1) * D; }
 __device__ __forceinline__ volatile float* smax_of(int c, int part) {
     return reinterpret_cast<volatile float*>(smem + kSmSMax) + ((c & 1) * 4 + part) * D;
 }
 __device__ __forceinline__ volatile uint2* bad_of(int c, int row) {
-    return reinterpret_cast<volatile uint2*>(smem + kSmBad) + (c & 1) * D + row;
+    return reinterpret_cast<volatile uint2*>(smem + kSmBad) + (c & 3) * D + row;
 }
-__device__ __forceinline__ volatile float* inv_of(int c) { return reinterpret_cast<volatile float*>(smem + kSmInv) + (c & 1) * D; }
+__device__ __forceinline__ volatile float* inv_of(int c) { return reinterpret_cast<volatile float*>(smem + kSmInv) + (c & 3) * D; }
 
 __device__ __forceinline__ volatile const Item& ring(int k) { return *(reinterpret_cast<const Item*>(smem + kSmItem) + (k & 1)); }
 
@@ -326,7 +339,9 @@ struct Issuer {
             const volatile Item& w = ring(at_item);
             const uint32_t bytes = w.outputs ? kDeltaBlock : kDeltaQ;
             mbar_arrive_expect_tx(bar(kFull + (loads & 1)), bytes);
-            bulk_g2s(block(loads), w.blocks + (int64_t)at_chunk * p.H * kDeltaBlock, bytes, bar(kFull + (loads & 1)));
+            const uint8_t* from = w.blocks + (int64_t)at_chunk * p.H * kDeltaBlock;
+            bulk_g2s(scalars_at(loads), from, kDeltaK, bar(kFull + (loads & 1)));
+            bulk_g2s(tiles(loads), from + kDeltaK, bytes - kDeltaK, bar(kFull + (loads & 1)));
         }
         __syncwarp();
         ++loads;
@@ -345,10 +360,10 @@ struct Issuer {
             const bool outputs = ring(k).outputs;
 #pragma unroll 1
             for (int c = 0; c < chunks; ++c, ++n) {
-                const uint32_t at = smem_u32(block(n)), o = tm + kTmO + (outs & 1) * C;
+                const uint32_t at = smem_u32(tiles(n)), o = tm + kTmO + (outs & 1) * C;
                 if (!wait(kFull + (n & 1), n >> 1)) return false;
                 // each maker's first 16 keys, then its others
-                const uint64_t kd = sw128_desc(at + kDeltaK, 0, 1024);
+                const uint64_t kd = sw128_desc(at, 0, 1024);
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
                     if (!wait(kSReady + b, n)) return false;
@@ -364,17 +379,25 @@ struct Issuer {
                     }
                     __syncwarp();
                 }
-                // the chunk before's products are over, and its outputs read
-                if (outs > 0 && !wait(kOEmpty + ((outs - 1) & 1), (outs - 1) >> 1)) return false;
+                // the chunk before's products are over (without outputs they were with dS)
+                if (outs > 0 && !wait(kODone + ((outs - 1) & 1), (outs - 1) >> 1)) return false;
                 if (c == 0) {
                     if (k > 0 && item_of(k + 1) < total && !wait(kItemFree + ((k - 1) & 1), (k - 1) >> 1)) return false;
                     publish(k + 1);
                 }
                 if (loads < n + 2) load(k + 1);
+                // (the outputs' products fill the pipe's pauses: X_q's high part here, its low one behind U,
+                // P U behind dS)
+                constexpr uint64_t kNext = C * C * 2 >> 4;
+                const uint64_t qd = sw128_desc(at + kDeltaQ - kDeltaK, 0, 1024), pd = sw128_desc(at + kDeltaP - kDeltaK, 0, 1024);
+                const uint64_t td = sw128_desc(at + kDeltaT - kDeltaK, 0, 1024);
+                // The outputs of the chunk before last are read: O's place is free, and of the rings of four no
+                // place is written that a chunk of which outputs are still to be read has.
+                const int read = outputs ? outs - 1 : outs;
+                if (read > 0 && !wait(kOEmpty + ((read - 1) & 1), (read - 1) >> 1)) return false;
                 if (outputs) {
                     tc_fence_after();
                     if (lead) {
-                        const uint64_t qd = sw128_desc(at + kDeltaQ, 0, 1024);
 #pragma unroll
                         for (int s = 0; s < 8; ++s)
                             mma_f16_ts(o, tm + kTmS + 16 * s, qd + (s >> 2) * kHalf + (s & 3) * 2, kIdescKK, s > 0);
@@ -384,28 +407,24 @@ struct Issuer {
                 if (!wait(kRReady, n)) return false;
                 tc_fence_after();
                 if (lead) {
-                    const uint64_t td = sw128_desc(at + kDeltaT, 0, 1024);
 #pragma unroll
                     for (int s = 0; s < 4; ++s) {
-                        const uint64_t hi = td + 2 * s, lo = hi + (C * C * 2 >> 4);
-                        mma_f16_ts(tm + kTmUAcc, tm + kTmR + 16 * s, lo, kIdescKK, s > 0);
-                        mma_f16_ts(tm + kTmUAcc, tm + kTmR + 16 * s + 8, hi, kIdescKK, 1);
-                        mma_f16_ts(tm + kTmUAcc, tm + kTmR + 16 * s, hi, kIdescKK, 1);
+                        mma_lower(tm + kTmUAcc, tm + kTmR + 16 * s, td + kNext, s, s > 0);
+                        mma_lower(tm + kTmUAcc, tm + kTmR + 16 * s + 8, td, s, 1);
+                        mma_lower(tm + kTmUAcc, tm + kTmR + 16 * s, td, s, 1);
                     }
                     mma_commit(bar(kUDone));
                     if (outputs) {
-                        const uint64_t pd = sw128_desc(at + kDeltaPT, 0, 1024);
 #pragma unroll
-                        for (int s = 0; s < 4; ++s) mma_f16_ts(o, tm + kTmR + 16 * s, pd + 2 * s, kIdescKK, 1);
-                        mma_commit(bar(kODone + (outs & 1)));
+                        for (int s = 0; s < 8; ++s)
+                            mma_f16_ts(o, tm + kTmS + 16 * s + 8, qd + (s >> 2) * kHalf + (s & 3) * 2, kIdescKK, 1);
                     }
                 }
                 __syncwarp();
-                if (outputs) ++outs;
                 if (!wait(kUReady, n)) return false;
                 tc_fence_after();
                 if (lead) {
-                    const uint64_t km = sw128_desc(at + kDeltaK, kTile / 2, 1024);
+                    const uint64_t km = sw128_desc(at, kTile / 2, 1024);
 #pragma unroll
                     for (int s = 0; s < 4; ++s) {
                         const uint64_t b = km + s * (2048 >> 4);
@@ -415,6 +434,27 @@ struct Issuer {
                     mma_commit(bar(kDDone));
                 }
                 __syncwarp();
+                if (outputs) {
+                    if (!wait(kPReady, outs)) return false;
+                    tc_fence_after();
+                    if (lead) {
+#pragma unroll
+                        for (int s = 0; s < 2; ++s) {
+                            const uint64_t right = 2 * (2 + s);
+                            mma_f16_ts(o, tm + kTmR + 16 * s, td + right, kIdescHalf, 1);
+                            mma_f16_ts(o + C / 2, tm + kTmR + 16 * s, td + kNext + right, kIdescHalf, 1);
+                            mma_f16_ts(o + C / 2, tm + kTmR + 16 * (2 + s), pd + right, kIdescHalf, 1);
+                        }
+#pragma unroll
+                        for (int s = 0; s < 4; ++s) {
+                            mma_lower(o, tm + kTmR + 16 * s + 8, pd, s, 1);
+                            mma_lower(o, tm + kTmR + 16 * s, pd, s, 1);
+                        }
+                        mma_commit(bar(kODone + (outs & 1)));
+                    }
+                    __syncwarp();
+                    ++outs;
+                }
             }
         }
         return true;
@@ -667,7 +707,7 @@ template <class S>
 __device__ __forceinline__ bool make(const DeltaParams& p, int k, int& n, int& nv, uint32_t base, int warp, int lane,
                                      f2 (&s)[kKeys / 2], bool& cleared, float& decay) {
     const int chunks = ring(k).chunks;
-    const bool values = ring(k).values;
+    const bool values = ring(k).values, outputs = ring(k).outputs;
     const int part = warp >> 2, row = 32 * (warp & 3) + lane;
     const uint32_t tm = base + ((uint32_t)(32 * (warp & 3)) << 16);
 #pragma unroll
@@ -803,18 +843,24 @@ __device__ __forceinline__ bool make(const DeltaParams& p, int k, int& n, int& n
         if (!wait(kUDone, n)) return false;
         tc_fence_after();
         {
-            f2 x[8];
+            f2 x[8], y[8];
             load16(tm + kTmUAcc + kToks * part, x);
 #pragma unroll
             for (int i = 0; i < 8; i += 2) {
                 const float4 wi = *reinterpret_cast<const float4*>(sc->w + kToks * part + 2 * i);
-                x[i] = mul2(x[i], pack2(wi.x, wi.y));
-                x[i + 1] = mul2(x[i + 1], pack2(wi.z, wi.w));
+                y[i] = mul2(x[i], pack2(wi.x, wi.y));
+                y[i + 1] = mul2(x[i + 1], pack2(wi.z, wi.w));
             }
-            store_split(tm + kTmU + kToks * part, x);
+            store_split(tm + kTmU + kToks * part, y);
+            tmem_wait_st();
+            arrive_warp(kUReady, lane);
+            // for the outputs U itself, in R's place, while dS's products run
+            if (outputs) {
+                store_split(tm + kTmR + kToks * part, x);
+                tmem_wait_st();
+                arrive_warp(kPReady, lane);
+            }
         }
-        tmem_wait_st();
-        arrive_warp(kUReady, lane);
         // S
         const bool more = c + 1 < chunks;
         decay *= sc->gamma;

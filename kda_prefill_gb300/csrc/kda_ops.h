@@ -120,14 +120,15 @@ constexpr int kDeltaStepMax = 16;
 // the swizzled layout of kda_device.cuh.
 //   k   [64][128]  k times a power of two for each row
 //   t   [2][64][64] the triangular inverse's high and low part
-//   q   [64][128]  q^ e^G, each row times up
-//   pt  [64][64]   the scores times the inverse, each row times up
-// A walk without outputs needs the first kDeltaQ bytes.
+//   q   [64][128]  q times a power of two for each row
+//   p   [64][64]   the scores' high part, each row over down
+// The upper right quarters of t and p are not read as theirs: the scores' low part stands in them, its
+// upper left quarter in t's high part, the lower left one in t's low part, the lower right one in p.  A walk without outputs needs the first kDeltaQ bytes.
 struct DeltaScalars {
     float c[kC];      // e^{G_i} and k's length: k^ e^{G_i} = c k
     float beta[kC];
     float w[kC];      // half of e^{G_C - G_i} and k's length
-    float down[kC];   // 1 / up
+    float down[kC];   // of a token's output
     float gamma;      // e^{G_C}
     int first_clear;  // first token that clears the state, kC if none
     unsigned clears[2];  // all of them
@@ -137,8 +138,8 @@ struct DeltaScalars {
 constexpr int kDeltaK = 2048;
 constexpr int kDeltaT = kDeltaK + 16384;
 constexpr int kDeltaQ = kDeltaT + 16384;
-constexpr int kDeltaPT = kDeltaQ + 16384;
-constexpr int kDeltaBlock = kDeltaPT + 8192;
+constexpr int kDeltaP = kDeltaQ + 16384;
+constexpr int kDeltaBlock = kDeltaP + 8192;
 static_assert(sizeof(DeltaScalars) <= kDeltaK, "room for the scalars");
 // At most so many chunks: only sequences of more than kShortMax tokens have any.
 inline int64_t delta_chunks(int64_t T, int64_t N) {
