@@ -121,21 +121,24 @@ def lin_attn_fwd(q, k, v, log_decay, cu_seqlens, *, state_cache, state_indices,
     [H], or [1, T, H] for a decay of each token.  ``scale`` defaults to
     128 ** -0.5.  Prompts, ragged batches and single tokens go in one call; the
     pool arguments are those of ``chunk_fwd``.  ``workspace`` (uint8, at least
-    ``lin_attn_workspace_size`` bytes; one for each stream) saves the call its
-    allocation, about 5 us of the 18 that a call takes on the host.  Writes ``out``
+    ``lin_attn_workspace_size`` bytes; one for each stream) saves a call of more than
+    8 tokens its allocation, about 5 us of the 18 that it takes on the host.  Writes ``out``
     and the selected pool slots in place and returns ``out``."""
     lib = load_library()
     dev = q.device
-    T, Hk, H, N, (q_st, q_sh, k_st, k_sh, v_st, v_sh) = _packed(
+    T, Hk, H, N, q_st, q_sh, k_st, k_sh, v_st, v_sh, p_st, slots, per_token, at = _packed(
         q, k, v, log_decay, cu_seqlens, state_cache, state_indices, has_initial_state, out)
-    _on_current_device(q.get_device())
+    _on_current_device(at)
     host = None if cu_seqlens_cpu is None else _host_int32(cu_seqlens_cpu, N)
-    workspace, given = _packed_workspace(lin_attn_workspace_size(T, N, H), workspace, dev, stream)
+    if workspace is None and T <= _LIN_STEP_MAX:
+        workspace, given = _header(dev, stream), _HEADER
+    else:
+        workspace, given = _packed_workspace(lin_attn_workspace_size(T, N, H), workspace, dev, stream)
     rc = lib.kda_lin_attn_fwd(
         q.data_ptr(), q_st, q_sh, k.data_ptr(), k_st, k_sh, v.data_ptr(), v_st, v_sh,
-        log_decay.data_ptr(), log_decay.dim() > 1, cu_seqlens.data_ptr(),
+        log_decay.data_ptr(), per_token, cu_seqlens.data_ptr(),
         None if host is None else host.data_ptr(), N, T, H, Hk,
-        state_cache.data_ptr(), state_cache.stride(0), state_cache.shape[0],
+        state_cache.data_ptr(), p_st, slots,
         state_indices.data_ptr(), has_initial_state.data_ptr(), out.data_ptr(),
         0.08838834764831845 if scale is None else float(scale), STATE_DTYPES[state_cache.dtype],
         workspace.data_ptr(), given, _stream(stream, dev))
@@ -164,8 +167,8 @@ def gated_delta_fwd(q, k, v, log_decay, beta, cu_seqlens, *, state_cache, state_
     long sequences need, 59 KB for 64 tokens and a head.  Writes ``out`` and the
     selected pool slots in place and returns ``out``."""
     lib = load_library()
-    dev, at = q.device, q.get_device()
-    T, Hk, H, N, (q_st, q_sh, k_st, k_sh, v_st, v_sh) = _packed(
+    dev = q.device
+    T, Hk, H, N, q_st, q_sh, k_st, k_sh, v_st, v_sh, p_st, slots, per_token, at = _packed(
         q, k, v, log_decay, cu_seqlens, state_cache, state_indices, has_initial_state, out)
     if beta.dtype is not torch.float32 or not beta.is_cuda:
         raise TypeError("beta must be a float32 CUDA tensor")
@@ -183,9 +186,9 @@ def gated_delta_fwd(q, k, v, log_decay, beta, cu_seqlens, *, state_cache, state_
         workspace, given = _packed_workspace(given, workspace, dev, stream)
     rc = lib.kda_gated_delta_fwd(
         q.data_ptr(), q_st, q_sh, k.data_ptr(), k_st, k_sh, v.data_ptr(), v_st, v_sh,
-        log_decay.data_ptr(), log_decay.dim() > 1, beta.data_ptr(), cu_seqlens.data_ptr(),
+        log_decay.data_ptr(), per_token, beta.data_ptr(), cu_seqlens.data_ptr(),
         None if host is None else host.data_ptr(), N, T, H, Hk,
-        state_cache.data_ptr(), state_cache.stride(0), state_cache.shape[0],
+        state_cache.data_ptr(), p_st, slots,
         state_indices.data_ptr(), has_initial_state.data_ptr(), out.data_ptr(),
         0.08838834764831845 if scale is None else float(scale), STATE_DTYPES[state_cache.dtype],
         workspace.data_ptr(), given, _stream(stream, dev))
@@ -195,12 +198,13 @@ def gated_delta_fwd(q, k, v, log_decay, beta, cu_seqlens, *, state_cache, state_
 
 
 def _packed(q, k, v, log_decay, cu_seqlens, state_cache, state_indices, hs, out):
-    """(T, Hqk, H, N, strides of q, k and v) of a call over packed sequences and the pool
-    of their states, its arguments checked."""
+    """(T, Hqk, H, N, strides of q, k and v, slot stride, slots, whether each token has its
+    decay, GPU) of a call over packed sequences and the pool of their states, its arguments
+    checked."""
     bf16 = torch.bfloat16
     at = q.get_device()  # -1 without a GPU
     qs, vs, ps, gs = q.shape, v.shape, state_cache.shape, log_decay.shape
-    (_, q_st, q_sh, q_1), (_, k_st, k_sh, k_1), (_, v_st, v_sh, v_1), (_, *plane) = (
+    (_, q_st, q_sh, q_1), (_, k_st, k_sh, k_1), (_, v_st, v_sh, v_1), (p_st, *plane) = (
         x.stride() if x.dim() == 4 else (0, 0, 0, 0) for x in (q, k, v, state_cache))
     N = cu_seqlens.numel() - 1
     # One look at the usual forms; _packed_args looks at each argument, takes the others and
@@ -232,10 +236,13 @@ def _packed(q, k, v, log_decay, cu_seqlens, state_cache, state_indices, hs, out)
     else:
         T, Hk, H, N, (q_st, q_sh, k_st, k_sh, v_st, v_sh) = _packed_args(
             q, k, v, log_decay, cu_seqlens, state_cache, state_indices, hs, out)
-    return T, Hk, H, N, (q_st, q_sh, k_st, k_sh, v_st, v_sh)
+    return T, Hk, H, N, q_st, q_sh, k_st, k_sh, v_st, v_sh, p_st, ps[0], len(gs) > 1, at
 
 
 _HEADER = 256  # bytes of a workspace that holds a status word alone
+# With so few tokens every sequence of linear attention's goes token by token: nothing of the
+# workspace but the status word is used.  (Above, chunks may be dealt out by counters in it.)
+_LIN_STEP_MAX = 8
 _headers = {}
 
 
