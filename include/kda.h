@@ -435,7 +435,9 @@ KDA_API size_t kda_lin_attn_workspace_size(int64_t total_tokens, int32_t num_seq
  *                    strength of a token's write (with 1 the state then gives
  *                    v_t for k^_t).
  *   workspace        at least kda_gated_delta_workspace_size() bytes, 256-byte
- *                    aligned; kda_check_status() reads its status word.
+ *                    aligned; kda_check_status() reads its status word.  256 bytes
+ *                    are enough where cu_seqlens_host is given and no sequence has
+ *                    more than 16 tokens.
  *
  * Sequences of at most 16 tokens go token by token, longer ones in chunks of 64, a
  * few long ones in segments besides; a call's sums are made in the same order every
@@ -469,7 +471,7 @@ KDA_API int kda_gated_delta_fwd(const void* q, int64_t q_stride_t, int64_t q_str
 
 /* Bytes of workspace a kda_gated_delta_fwd call with these sizes needs; 0 for
  * invalid sizes.  About 59 KB for 64 tokens and a head (223 MB for 16384 tokens of 12
- * heads), whatever the sequences' lengths; 256 bytes below nine tokens. */
+ * heads), whatever the sequences' lengths; 256 bytes below 17 tokens. */
 KDA_API size_t kda_gated_delta_workspace_size(int64_t total_tokens, int32_t num_seqs,
                   int32_t num_heads);
 

@@ -46,10 +46,12 @@ constexpr int kChunk = kda::kC;
 constexpr int kD = kda::kD;
 
 inline int64_t chunks_of(int64_t len) { return (len + kChunk - 1) / kChunk; }
-// Chunks a sequence gets in the chunked kernels: none when it is short enough
-// for the token-by-token kernel.
-inline bool is_short(int64_t len) { return len <= kda::kShortMax; }
-inline int64_t routed_chunks(int64_t len) { return is_short(len) ? 0 : chunks_of(len); }
+// Chunks a sequence gets in the chunked kernels: none when it is short enough, at most
+// `step_max` tokens, for the token-by-token kernel.
+inline bool is_short(int64_t len, int step_max = kda::kShortMax) { return len <= step_max; }
+inline int64_t routed_chunks(int64_t len, int step_max = kda::kShortMax) {
+    return is_short(len, step_max) ? 0 : chunks_of(len);
+}
 
 int64_t max_chunks(int64_t T, int32_t N) { return (T + kChunk - 1) / kChunk + N; }
 
@@ -90,6 +92,7 @@ int check_host_bounds(const int32_t* cu, int32_t N, int64_t T) {
 struct MetaLayout {
     int64_t n_chunks = 0;
     int32_t n_long = 0, n_short = 0;
+    int32_t n_mid = 0;            // of the short ones, those of more than kShortMax tokens
     int32_t max_long_chunks = 0;  // chunks of the longest sequence the chunked kernels take
     // the sequences the chunked kernels take and their lengths, longest first
     std::vector<int32_t> long_seqs, long_lens;
@@ -101,18 +104,19 @@ struct MetaLayout {
 inline size_t align4(size_t w) { return (w + 3) & ~size_t(3); }  // 16-byte blocks
 
 // Chunk count and routing of the sequences from host bounds.
-MetaLayout meta_layout(const int32_t* cu, int32_t N) {
+MetaLayout meta_layout(const int32_t* cu, int32_t N, int step_max) {
     MetaLayout L;
     for (int32_t n = 0; n < N; ++n) {
         const int64_t len = (int64_t)cu[n + 1] - cu[n];
-        L.n_chunks += routed_chunks(len);
-        if (is_short(len)) {
+        L.n_chunks += routed_chunks(len, step_max);
+        if (is_short(len, step_max)) {
             ++L.n_short;
+            L.n_mid += !is_short(len);
         } else {
             ++L.n_long;
             L.long_seqs.push_back(n);
         }
-        L.max_long_chunks = std::max<int32_t>(L.max_long_chunks, (int32_t)routed_chunks(len));
+        L.max_long_chunks = std::max<int32_t>(L.max_long_chunks, (int32_t)routed_chunks(len, step_max));
     }
     std::stable_sort(L.long_seqs.begin(), L.long_seqs.end(), [&](int32_t a, int32_t b) {
         return cu[a + 1] - cu[a] > cu[b + 1] - cu[b];
@@ -129,7 +133,7 @@ MetaLayout meta_layout(const int32_t* cu, int32_t N) {
     return L;
 }
 
-void meta_fill(const int32_t* cu, int32_t N, const MetaLayout& L, int32_t* buf) {
+void meta_fill(const int32_t* cu, int32_t N, int step_max, const MetaLayout& L, int32_t* buf) {
     std::memset(buf, 0, L.words * sizeof(int32_t));
     int32_t* mcu = buf + L.off_cu;
     int32_t* off = buf + L.off_seq_off;
@@ -143,8 +147,8 @@ void meta_fill(const int32_t* cu, int32_t N, const MetaLayout& L, int32_t* buf) 
         mcu[n] = cu[n];
         off[n] = (int32_t)j;
         const int64_t len = (int64_t)cu[n + 1] - cu[n];
-        if (is_short(len)) sht[ns++] = n;
-        const int64_t nc = routed_chunks(len);
+        if (is_short(len, step_max)) sht[ns++] = n;
+        const int64_t nc = routed_chunks(len, step_max);
         for (int64_t c = 0; c < nc; ++c, ++j) {
             cseq[j] = n;
             ctok[j] = (int32_t)(cu[n] + c * kChunk);
@@ -251,7 +255,7 @@ class PinnedPool {
 };
 
 struct MetaEntry {
-    std::vector<int32_t> key;  // device, N, bounds
+    std::vector<int32_t> key;  // device, step_max, N, bounds
     int device = 0;
     MetaLayout layout;
     int32_t* dev = nullptr;
@@ -271,16 +275,17 @@ class MetaCache {
     PinnedPool ring;
     uint64_t clock = 0;
 
-    // Finds or builds the entry for these bounds; enqueues the upload on a miss
-    // and the cross-stream wait on a hit.
-    int get(const int32_t* cu, int32_t N, cudaStream_t stream, bool capturing, MetaEntry** out) {
+    // Finds or builds the entry for these bounds and this longest short sequence; enqueues
+    // the upload on a miss and the cross-stream wait on a hit.
+    int get(const int32_t* cu, int32_t N, int step_max, cudaStream_t stream, bool capturing,
+            MetaEntry** out) {
         int dev = 0;
         cudaError_t e = cudaGetDevice(&dev);
         if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
         std::vector<int32_t> key;
         key.reserve((size_t)N + 3);
         key.push_back(dev);
-        key.push_back(kChunk);
+        key.push_back(step_max);
         key.push_back(N);
         key.insert(key.end(), cu, cu + N + 1);
         auto it = map.find(key);
@@ -320,7 +325,7 @@ class MetaCache {
         auto* m = new MetaEntry();
         m->key = std::move(key);
         m->device = dev;
-        m->layout = meta_layout(cu, N);
+        m->layout = meta_layout(cu, N, step_max);
         const size_t bytes = m->layout.words * sizeof(int32_t);
         cudaEvent_t* done = nullptr;
         void* host = ring.acquire(bytes, &done);
@@ -328,7 +333,7 @@ class MetaCache {
             delete m;
             return fail(KDA_ERR_CUDA, "pinned staging allocation failed");
         }
-        meta_fill(cu, N, m->layout, static_cast<int32_t*>(host));
+        meta_fill(cu, N, step_max, m->layout, static_cast<int32_t*>(host));
         e = cudaMallocAsync(reinterpret_cast<void**>(&m->dev), bytes, stream);
         if (e != cudaSuccess) {
             cudaEventRecord(*done, stream);  // the staging region is free again
@@ -468,7 +473,7 @@ struct StateArgs {
 // The call's metadata entry, with the cache locked: reads the bounds back first
 // when the host does not have them.
 int find_tables(const int32_t* cu_dev, const int32_t* cu_host, int32_t N, int64_t T,
-                cudaStream_t stream, bool capturing, MetaEntry** m) {
+                int step_max, cudaStream_t stream, bool capturing, MetaEntry** m) {
     std::vector<int32_t> readback;
     if (!cu_host) {
         if (capturing)
@@ -489,7 +494,7 @@ int find_tables(const int32_t* cu_dev, const int32_t* cu_host, int32_t N, int64_
         int rc = check_host_bounds(cu_host, N, T);
         if (rc != KDA_OK) return rc;
     }
-    return cache().get(cu_host, N, stream, capturing, m);
+    return cache().get(cu_host, N, step_max, stream, capturing, m);
 }
 
 int run_forward(const void* q, const void* k, const void* v, const void* g_raw,
@@ -504,7 +509,7 @@ int run_forward(const void* q, const void* k, const void* v, const void* g_raw,
 
     std::lock_guard<std::mutex> lock(cache().mu);
     MetaEntry* m = nullptr;
-    int rc = find_tables(cu_dev, cu_host, N, T, stream, capturing, &m);
+    int rc = find_tables(cu_dev, cu_host, N, T, kda::kShortMax, stream, capturing, &m);
     if (rc != KDA_OK) return rc;
 
     uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -655,18 +660,18 @@ int check_bounds(const int32_t* cu_host, int32_t N, int64_t T) {
 }
 
 int with_seq_tables(const int32_t* cu_dev, const int32_t* cu_host, int32_t N, int64_t T,
-                    cudaStream_t stream, int (*enqueue)(void*, const SeqTables&), void* arg) {
+                    int step_max, cudaStream_t stream, int (*enqueue)(void*, const SeqTables&), void* arg) {
     cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
     cudaError_t e = cudaStreamIsCapturing(stream, &cap);
     if (e != cudaSuccess) return cuda_fail(e, "cudaStreamIsCapturing");
     const bool capturing = (cap != cudaStreamCaptureStatusNone);
     std::lock_guard<std::mutex> lock(cache().mu);
     MetaEntry* m = nullptr;
-    int rc = find_tables(cu_dev, cu_host, N, T, stream, capturing, &m);
+    int rc = find_tables(cu_dev, cu_host, N, T, step_max, stream, capturing, &m);
     if (rc != KDA_OK) return rc;
     const MetaLayout& L = m->layout;
     SeqTables t{m->dev + L.off_cu, m->dev + L.off_long, m->dev + L.off_short,
-                L.n_long,          L.n_short,           m->dev + L.off_seq_off,
+                L.n_long,          L.n_short,           L.n_mid, m->dev + L.off_seq_off,
                 m->dev + L.off_chunk_seq, m->dev + L.off_chunk_tok, L.n_chunks, m->key.data() + 3,
                 L.long_seqs.data(), L.long_lens.data()};
     rc = enqueue(arg, t);

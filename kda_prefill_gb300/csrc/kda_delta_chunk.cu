@@ -197,7 +197,6 @@ __global__ void __launch_bounds__(kThreads, 4) kda_delta_chunk(const __grid_cons
     if (tid == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (blockIdx.x == 0 && warp == 0) write_status(p, lane);
     const int n = p.chunk_seq[chunk], t0 = p.chunk_tok[chunk];
-    if (p.cu[n + 1] - p.cu[n] <= kDeltaStepMax) return;  // goes token by token
     const int len = min(C, p.cu[n + 1] - t0);
     uint8_t* const blk = p.blocks + (chunk * p.H + h) * (int64_t)kDeltaBlock;
     DeltaScalars* const scal = reinterpret_cast<DeltaScalars*>(blk);

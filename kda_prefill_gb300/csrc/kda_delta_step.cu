@@ -134,7 +134,7 @@ kda_delta_step(const __grid_constant__ DeltaParams p) {
     using C = Cols<S>;
     extern __shared__ Token tokens[];  // of a sequence
     const int h = blockIdx.y, ctas = kParts / kPasses;
-    const int i = blockIdx.x / ctas, n = i < p.n_short ? p.short_list[i] : p.mid_list[i - p.n_short];
+    const int n = p.short_list[blockIdx.x / ctas];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int at = lane % kAcross, part = lane / kAcross;  // rows part, part + 4 of the eight
     const int own = at % kHeld;                            // the held row whose output this lane makes
@@ -238,7 +238,7 @@ kda_delta_step(const __grid_constant__ DeltaParams p) {
 template <class S, int kPasses>
 cudaError_t launch(const DeltaParams& p, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(p.n_short + p.n_mid) * (kParts / kPasses), (unsigned)p.H);
+    cfg.gridDim = dim3((unsigned)p.n_short * (kParts / kPasses), (unsigned)p.H);
     cfg.blockDim = dim3(kWarps * 32);
     cfg.dynamicSmemBytes = sizeof(Token) * (p.n_mid > 0 ? kDeltaStepMax : kShortMax);
     cfg.stream = s;
@@ -255,14 +255,14 @@ cudaError_t launch(const DeltaParams& p, cudaStream_t s) {
     // Few states: 32 rows a CTA, for the latency; many: 128, whose loads overlap and which share
     // what belongs to a token.  12 heads, fp32 pool: 16 sequences of 4 tokens 10.4 and 12.5 us, 50
     // of them 18.6 and 16.8; 512 single tokens, bf16 pool: 82 and 68 us
-    if ((int64_t)(p.n_short + p.n_mid) * p.H * kParts <= 8 * num_sms()) return launch<S, 1>(p, s);
+    if ((int64_t)p.n_short * p.H * kParts <= 8 * num_sms()) return launch<S, 1>(p, s);
     return launch<S, kParts>(p, s);
 }
 
 }  // namespace
 
 cudaError_t launch_delta_step(const DeltaParams& p, cudaStream_t s) {
-    if (p.n_short + p.n_mid <= 0) return cudaSuccess;
+    if (p.n_short <= 0) return cudaSuccess;
     if (p.st_dtype == KDA_STATE_F32) return launch<float>(p, s);
     if (p.st_dtype == KDA_STATE_BF16) return launch<__nv_bfloat16>(p, s);
     return launch<__half>(p, s);

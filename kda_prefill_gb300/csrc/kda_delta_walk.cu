@@ -1266,7 +1266,7 @@ void delta_cut(DeltaParams& p, LinCuts& cuts, const SeqTables& t) {
     // a single token's state of a head goes there and back at 6.6 TB/s (5.9 if of 2 bytes), a
     // chunk takes 2.6 us; a sequence of more tokens takes some 30 ns more for a head
     const float state = p.st_dtype == KDA_STATE_F32 ? 0.0077f : 0.0042f;
-    const float single = state * (float)(p.n_short + p.n_mid) + 0.012f * (float)p.n_mid;
+    const float single = state * (float)p.n_short + 0.012f * (float)p.n_mid;
     const Cut c = cut_rule(t.long_lens, p.n_long, p.H, num_sms(), delta_planes(p.T, p.H), single * (float)p.H);
     p.seg_len = c.seg * C;
     p.n_cut = c.n_cut;

@@ -17,9 +17,10 @@ int set_error(int code, const char* fmt, ...);
 // on `stream` for work enqueued while the lock is held.
 struct SeqTables {
     const int32_t* cu;          // [N + 1]
-    const int32_t* long_list;   // sequences of more than kShortMax tokens, longest first
+    const int32_t* long_list;   // sequences of more than step_max tokens, longest first
     const int32_t* short_list;  // the others
     int n_long, n_short;
+    int n_mid;                  // of the others, those of more than kShortMax tokens
     // chunks of kC tokens of the long sequences: the first of each sequence [N + 1], and
     // each one's sequence and first token
     const int32_t *seq_off, *chunk_seq, *chunk_tok;
@@ -30,9 +31,10 @@ struct SeqTables {
     const int32_t* long_lens;
 };
 // Looks the bounds up (reading them back once without cu_host), calls
-// enqueue(arg, tables) with the cache locked and marks the tables' use.
+// enqueue(arg, tables) with the cache locked and marks the tables' use.  Sequences of at
+// most step_max tokens are the short ones.
 int with_seq_tables(const int32_t* cu_dev, const int32_t* cu_host, int32_t N, int64_t T,
-                    cudaStream_t stream, int (*enqueue)(void*, const SeqTables&), void* arg);
+                    int step_max, cudaStream_t stream, int (*enqueue)(void*, const SeqTables&), void* arg);
 // The bounds' host check (message set on failure).
 int check_bounds(const int32_t* cu_host, int32_t N, int64_t T);
 
@@ -105,8 +107,7 @@ struct DeltaParams : LinParams {
     const float* beta;  // [T][H]
     const int32_t *seq_off, *chunk_seq, *chunk_tok;
     int64_t n_chunks;
-    const int32_t* mid_list;  // sequences beside short_list's that go token by token
-    int n_mid;
+    int n_mid;  // short sequences of more than kShortMax tokens
     uint8_t* blocks;  // [n_chunks][H] of kDeltaBlock bytes
     // of the cut sequences' segments: `planes` has two of [128 x 128] for each segment and
     // head, its state from zero (then the one that the next starts from) and its transition,
@@ -141,9 +142,9 @@ constexpr int kDeltaQ = kDeltaT + 16384;
 constexpr int kDeltaP = kDeltaQ + 16384;
 constexpr int kDeltaBlock = kDeltaP + 8192;
 static_assert(sizeof(DeltaScalars) <= kDeltaK, "room for the scalars");
-// At most so many chunks: only sequences of more than kShortMax tokens have any.
+// At most so many chunks: only sequences of more than kDeltaStepMax tokens have any.
 inline int64_t delta_chunks(int64_t T, int64_t N) {
-    return T / kC + (T / (kShortMax + 1) < N ? T / (kShortMax + 1) : N);
+    return T / kC + (T / (kDeltaStepMax + 1) < N ? T / (kDeltaStepMax + 1) : N);
 }
 // Segments times heads that a call's workspace holds: as many as are ever cut, or as there
 // can be.  All segments but a sequence's last have kDeltaMinSeg chunks or more: m > 1

@@ -1,5 +1,6 @@
 // Host side of the operators beside the KDA forward: argument checks and launches.
 
+#include <algorithm>
 #include <numeric>
 
 #include "kda_ops.h"
@@ -247,6 +248,15 @@ struct DeltaCall {
     cudaStream_t stream;
 };
 
+// Whether the host's bounds say that no sequence has chunks, so that nothing of the workspace
+// but the header is used.
+bool token_by_token(const int32_t* cu_host, int32_t N) {
+    if (!cu_host) return false;
+    for (int32_t n = 0; n < N; ++n)
+        if ((int64_t)cu_host[n + 1] - cu_host[n] > kda::kDeltaStepMax) return false;
+    return true;
+}
+
 int enqueue_delta(void* arg, const kda::SeqTables& t) {
     DeltaCall& c = *static_cast<DeltaCall*>(arg);
     kda::DeltaParams& p = c.p;
@@ -255,9 +265,7 @@ int enqueue_delta(void* arg, const kda::SeqTables& t) {
     p.short_list = t.short_list;
     p.n_long = t.n_long;
     p.n_short = t.n_short;
-    while (p.n_long > 0 && t.long_lens[p.n_long - 1] <= kda::kDeltaStepMax) --p.n_long;
-    p.mid_list = t.long_list + p.n_long;
-    p.n_mid = t.n_long - p.n_long;
+    p.n_mid = t.n_mid;
     p.seq_off = t.seq_off;
     p.chunk_seq = t.chunk_seq;
     p.chunk_tok = t.chunk_tok;
@@ -377,7 +385,7 @@ int kda_lin_attn_fwd(const void* q, int64_t q_stride_t, int64_t q_stride_h, cons
     set_params(a, c.p);
     c.p.kept = reinterpret_cast<float*>(static_cast<char*>(workspace) + kda::kWsHeader);
     c.p.planes = c.p.kept + 64 * kda::kLinPlanes;
-    return kda::with_seq_tables(cu_seqlens, cu_seqlens_host, num_seqs, total_tokens, c.stream, enqueue_lin, &c);
+    return kda::with_seq_tables(cu_seqlens, cu_seqlens_host, num_seqs, total_tokens, kda::kShortMax, c.stream, enqueue_lin, &c);
 }
 
 size_t kda_gated_delta_workspace_size(int64_t total_tokens, int32_t num_seqs, int32_t num_heads) {
@@ -399,7 +407,9 @@ int kda_gated_delta_fwd(const void* q, int64_t q_stride_t, int64_t q_stride_h, c
                        log_decay, decay_per_token, beta, true, cu_seqlens, cu_seqlens_host, num_seqs,
                        total_tokens, num_heads, num_qk_heads, state_cache, state_stride0, num_slots,
                        state_indices, has_initial_state, out, scale, state_dtype, workspace, workspace_bytes};
-    const int rc = check_packed(a, kda_gated_delta_workspace_size(total_tokens, num_seqs, num_heads));
+    size_t need = kda_gated_delta_workspace_size(total_tokens, num_seqs, num_heads);
+    if (token_by_token(cu_seqlens_host, num_seqs)) need = std::min(need, (size_t)kda::kWsHeader);
+    const int rc = check_packed(a, need);
     if (rc != KDA_OK || num_seqs == 0) return rc;
     DeltaCall c{};
     c.stream = reinterpret_cast<cudaStream_t>(stream);
@@ -409,7 +419,7 @@ int kda_gated_delta_fwd(const void* q, int64_t q_stride_t, int64_t q_stride_h, c
     c.p.planes = reinterpret_cast<float*>(
         c.p.blocks + (size_t)kda::delta_chunks(total_tokens, num_seqs) * num_heads * kda::kDeltaBlock);
     c.p.kept = c.p.planes + (size_t)kda::delta_planes(total_tokens, num_heads) * 2 * kda::kD * kda::kD;
-    return kda::with_seq_tables(cu_seqlens, cu_seqlens_host, num_seqs, total_tokens, c.stream, enqueue_delta, &c);
+    return kda::with_seq_tables(cu_seqlens, cu_seqlens_host, num_seqs, total_tokens, kda::kDeltaStepMax, c.stream, enqueue_delta, &c);
 }
 
 int kda_rope(const kda_rope_tensor* tensors, int32_t num_tensors, const void* positions,

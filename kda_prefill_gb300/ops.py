@@ -23,7 +23,7 @@ from typing import Optional
 
 import torch
 
-from . import (KDA_OK, STATE_DTYPES, _check, _host_bounds, _on_current_device, _per_sequence,
+from . import (KDA_ERR_WORKSPACE, KDA_OK, STATE_DTYPES, _check, _host_bounds, _on_current_device, _per_sequence,
                _same_device, load_library)
 
 _DTYPES = STATE_DTYPES  # kda_dtype has the same values as kda_state_dtype
@@ -164,8 +164,9 @@ def gated_delta_fwd(q, k, v, log_decay, beta, cu_seqlens, *, state_cache, state_
     ``lin_attn_fwd``; ``beta`` is contiguous fp32 [1, T, H] (or [T, H]), from 0 to 2,
     ``log_decay`` at most 0 (below -104 a token clears the state).  Prompts, ragged
     batches and single tokens go in one call.  The workspace holds what the chunks of
-    long sequences need, 59 KB for 64 tokens and a head.  Writes ``out`` and the
-    selected pool slots in place and returns ``out``."""
+    long sequences need, 59 KB for 64 tokens and a head; where ``cu_seqlens_cpu`` says that
+    none has more than 16 tokens, a call allocates none.  Writes ``out`` and the selected
+    pool slots in place and returns ``out``."""
     lib = load_library()
     dev = q.device
     T, Hk, H, N, q_st, q_sh, k_st, k_sh, v_st, v_sh, p_st, slots, per_token, at = _packed(
@@ -179,19 +180,23 @@ def gated_delta_fwd(q, k, v, log_decay, beta, cu_seqlens, *, state_cache, state_
         raise ValueError(f"beta must be a contiguous [1, T, H] tensor; got shape {tuple(bs)}")
     _on_current_device(at)
     host = None if cu_seqlens_cpu is None else _host_int32(cu_seqlens_cpu, N)
-    given = gated_delta_workspace_size(T, N, H)
-    if workspace is None and given <= _HEADER:
-        workspace = _header(dev, stream)
-    else:
-        workspace, given = _packed_workspace(given, workspace, dev, stream)
-    rc = lib.kda_gated_delta_fwd(
-        q.data_ptr(), q_st, q_sh, k.data_ptr(), k_st, k_sh, v.data_ptr(), v_st, v_sh,
-        log_decay.data_ptr(), per_token, beta.data_ptr(), cu_seqlens.data_ptr(),
-        None if host is None else host.data_ptr(), N, T, H, Hk,
-        state_cache.data_ptr(), p_st, slots,
-        state_indices.data_ptr(), has_initial_state.data_ptr(), out.data_ptr(),
-        0.08838834764831845 if scale is None else float(scale), STATE_DTYPES[state_cache.dtype],
-        workspace.data_ptr(), given, _stream(stream, dev))
+    args = (q.data_ptr(), q_st, q_sh, k.data_ptr(), k_st, k_sh, v.data_ptr(), v_st, v_sh,
+            log_decay.data_ptr(), per_token, beta.data_ptr(), cu_seqlens.data_ptr(),
+            None if host is None else host.data_ptr(), N, T, H, Hk,
+            state_cache.data_ptr(), p_st, slots,
+            state_indices.data_ptr(), has_initial_state.data_ptr(), out.data_ptr(),
+            0.08838834764831845 if scale is None else float(scale), STATE_DTYPES[state_cache.dtype])
+    rc = KDA_ERR_WORKSPACE
+    if workspace is None and (T <= _DELTA_STEP_MAX or host is not None and T <= N * _DELTA_STEP_MAX):
+        # it has no chunks unless a sequence is longer than they are on average, which the library
+        # sees before it does anything
+        rc = lib.kda_gated_delta_fwd(*args, _header(dev, stream).data_ptr(), _HEADER, _stream(stream, dev))
+    if rc == KDA_ERR_WORKSPACE:
+        need = gated_delta_workspace_size(T, N, H)
+        if workspace is not None and host is not None and T <= N * _DELTA_STEP_MAX:
+            need = min(need, _HEADER)  # it may be enough: the library says
+        workspace, given = _packed_workspace(need, workspace, dev, stream)
+        rc = lib.kda_gated_delta_fwd(*args, workspace.data_ptr(), given, _stream(stream, dev))
     if rc != KDA_OK:
         _check(rc, lib)
     return out
@@ -243,6 +248,7 @@ _HEADER = 256  # bytes of a workspace that holds a status word alone
 # With so few tokens every sequence of linear attention's goes token by token: nothing of the
 # workspace but the status word is used.  (Above, chunks may be dealt out by counters in it.)
 _LIN_STEP_MAX = 8
+_DELTA_STEP_MAX = 16  # of each of the gated delta rule's, which has no counters
 _headers = {}
 
 

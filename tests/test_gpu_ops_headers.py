@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import kda_prefill_gb300 as kda
-from tests.test_gpu_lin_attn import D
+from tests.test_gpu_gated_delta import D, check, expected, make
 
 pytestmark = pytest.mark.gpu
 
@@ -80,3 +80,43 @@ def test_single_tokens_allocate_nothing():
     n = torch.cuda.memory_stats()["allocation.all.allocated"]
     call()
     assert torch.cuda.memory_stats()["allocation.all.allocated"] == n
+
+
+def allocations(f):
+    torch.cuda.synchronize()
+    n = torch.cuda.memory_stats()["allocation.all.allocated"]
+    f()
+    return torch.cuda.memory_stats()["allocation.all.allocated"] - n
+
+
+@pytest.mark.parametrize("lengths,few", [([1] * 300, True), ([4] * 90 + [16] * 2 + [0] * 5, True), ([9, 16, 12], True),
+                                         ([1] * 200 + [40], False), ([17], False), ([0] * 20 + [17, 100], False)])
+def test_the_delta_rule_without_a_workspace(lengths, few):
+    """Sequences of at most 16 tokens: nothing is allocated; with a longer one among them the call
+    takes its workspace as any other."""
+    c = make(lengths, 2, seed=91, init=[i % 3 != 0 for i in range(len(lengths))])
+    want, before = expected(c), c["storage"].clone()
+    out = torch.empty(c["v"].shape, dtype=torch.bfloat16, device="cuda")
+    args = c["q"], c["k"], c["v"], c["g"], c["beta"], c["cu"].cuda()
+    kw = dict(state_cache=c["cache"], state_indices=c["idx"].cuda(), has_initial_state=c["has"].cuda(), out=out)
+
+    def call(**more):
+        c["storage"].copy_(before)
+        return allocations(lambda: kda.gated_delta_fwd(*args, **kw, **more))
+
+    call(cu_seqlens_cpu=c["cu"])
+    check(c, out, want, before)
+    assert (call(cu_seqlens_cpu=c["cu"]) == 0) == few
+    check(c, out, want, before)
+    call()
+    check(c, out, want, before)
+    ws = torch.empty(256, dtype=torch.uint8, device="cuda")
+    if few:
+        call(cu_seqlens_cpu=c["cu"], workspace=ws)
+        check(c, out, want, before)
+        assert kda.check_status(ws) == 0
+        with pytest.raises(ValueError, match="too small"):
+            kda.gated_delta_fwd(*args, **kw, cu_seqlens_cpu=c["cu"], workspace=ws[:128])
+    else:
+        with pytest.raises((ValueError, kda.KDAError), match="workspace"):
+            kda.gated_delta_fwd(*args, **kw, cu_seqlens_cpu=c["cu"], workspace=ws)
