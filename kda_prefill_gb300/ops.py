@@ -122,15 +122,15 @@ def lin_attn_fwd(q, k, v, log_decay, cu_seqlens, *, state_cache, state_indices,
     128 ** -0.5.  Prompts, ragged batches and single tokens go in one call; the
     pool arguments are those of ``chunk_fwd``.  ``workspace`` (uint8, at least
     ``lin_attn_workspace_size`` bytes; one for each stream) saves a call of more than
-    8 tokens its allocation, about 5 us of the 18 that it takes on the host.  Writes ``out``
-    and the selected pool slots in place and returns ``out``."""
+    8 tokens, or with ``stream``, its allocation, about 5 us of the 18 that it takes on the
+    host.  Writes ``out`` and the selected pool slots in place and returns ``out``."""
     lib = load_library()
     dev = q.device
     T, Hk, H, N, q_st, q_sh, k_st, k_sh, v_st, v_sh, p_st, slots, per_token, at = _packed(
         q, k, v, log_decay, cu_seqlens, state_cache, state_indices, has_initial_state, out)
     _on_current_device(at)
     host = None if cu_seqlens_cpu is None else _host_int32(cu_seqlens_cpu, N)
-    if workspace is None and T <= _LIN_STEP_MAX:
+    if workspace is None and T <= _LIN_STEP_MAX and stream is None:
         workspace, given = _header(dev, stream), _HEADER
     else:
         workspace, given = _packed_workspace(lin_attn_workspace_size(T, N, H), workspace, dev, stream)
