@@ -249,19 +249,23 @@ _HEADER = 256  # bytes of a workspace that holds a status word alone
 # workspace but the status word is used.  (Above, chunks may be dealt out by counters in it.)
 _LIN_STEP_MAX = 8
 _DELTA_STEP_MAX = 16  # of each of the gated delta rule's, which has no counters
-_headers = {}
+_headers = {}  # of each GPU, by stream
 
 
 def _header(dev, stream):
     """The workspace of a call that needs no other and whose caller cannot read its status:
-    one for each GPU, which any number of calls may write at once.  (An allocation takes 5 us
-    of such a call's 20 on the host.)"""
-    ws = _headers.get(dev.index)
-    if ws is None:
-        ws = _empty(_HEADER, torch.uint8, dev, stream)
-        # (memory of a graph's own is the graph's)
-        if not torch.cuda.is_current_stream_capturing() and stream is None:
-            _headers[dev.index] = ws
+    one for each GPU and current stream, which any number of calls may write.  (An allocation
+    takes 5 us of such a call's 20 on the host.  Its memory may be what earlier work of the
+    stream that makes it still uses: other streams have their own.)"""
+    if stream is None:
+        on = _stream(None, dev)
+        ws = _headers.get(dev.index, {}).get(on)
+        if ws is not None:
+            return ws
+    ws = _empty(_HEADER, torch.uint8, dev, stream)
+    # (memory of a graph's own is the graph's)
+    if stream is None and not torch.cuda.is_current_stream_capturing():
+        _headers.setdefault(dev.index, {})[on] = ws
     return ws
 
 

@@ -82,6 +82,38 @@ def test_single_tokens_allocate_nothing():
     assert torch.cuda.memory_stats()["allocation.all.allocated"] == n
 
 
+@pytest.mark.parametrize("op", ["lin", "delta"])
+def test_a_header_is_not_memory_that_another_stream_still_reads(op):
+    """The word that a call on one stream makes may lie where that stream's earlier work still reads;
+    a call on another stream does not write it."""
+    if op == "lin":
+        calls = [lin_call([1], 92 + i)[0] for i in range(2)]
+    else:
+        calls = []
+        for i in range(2):
+            c = make([1], 2, seed=92 + i, init=[True])
+            cu, idx, has = c["cu"].cuda(), c["idx"].cuda(), c["has"].cuda()
+            out = torch.empty(c["v"].shape, dtype=torch.bfloat16, device="cuda")
+            calls.append(lambda c=c, cu=cu, idx=idx, has=has, out=out, **kw: kda.gated_delta_fwd(
+                c["q"], c["k"], c["v"], c["g"], c["beta"], cu, state_cache=c["cache"], state_indices=idx,
+                has_initial_state=has, out=out, cu_seqlens_cpu=c["cu"], **kw))
+    for call in calls:  # the bounds' tables
+        call(workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+    torch.cuda.synchronize()
+    kda.ops._headers.clear()
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    with torch.cuda.stream(a):
+        x = torch.full((256,), 7, dtype=torch.uint8, device="cuda")
+        torch.cuda._sleep(2 * 10 ** 8)  # a tenth of a second
+        y = x.clone()
+        del x
+        calls[0]()
+    with torch.cuda.stream(b):
+        calls[1]()
+    torch.cuda.synchronize()
+    assert bool((y == 7).all())
+
+
 def allocations(f):
     torch.cuda.synchronize()
     n = torch.cuda.memory_stats()["allocation.all.allocated"]
