@@ -386,8 +386,8 @@ struct Issuer {
                     publish(k + 1);
                 }
                 if (loads < n + 2) load(k + 1);
-                // (the outputs' products fill the pipe's pauses: X_q's high part here, its low one behind U,
-                // P U behind dS)
+                // (the outputs' products fill the pipe's pauses: X_q here, while R is made, P U behind dS; with
+                // half of X_q behind U 128 sequences' walk took 589 us instead of 584)
                 constexpr uint64_t kNext = C * C * 2 >> 4;
                 const uint64_t qd = sw128_desc(at + kDeltaQ - kDeltaK, 0, 1024), pd = sw128_desc(at + kDeltaP - kDeltaK, 0, 1024);
                 const uint64_t td = sw128_desc(at + kDeltaT - kDeltaK, 0, 1024);
@@ -399,8 +399,11 @@ struct Issuer {
                     tc_fence_after();
                     if (lead) {
 #pragma unroll
-                        for (int s = 0; s < 8; ++s)
-                            mma_f16_ts(o, tm + kTmS + 16 * s, qd + (s >> 2) * kHalf + (s & 3) * 2, kIdescKK, s > 0);
+                        for (int part = 0; part < 2; ++part)
+#pragma unroll
+                            for (int s = 0; s < 8; ++s)
+                                mma_f16_ts(o, tm + kTmS + 16 * s + 8 * part, qd + (s >> 2) * kHalf + (s & 3) * 2, kIdescKK,
+                                           s > 0 || part > 0);
                     }
                     __syncwarp();
                 }
@@ -414,11 +417,6 @@ struct Issuer {
                         mma_lower(tm + kTmUAcc, tm + kTmR + 16 * s, td, s, 1);
                     }
                     mma_commit(bar(kUDone));
-                    if (outputs) {
-#pragma unroll
-                        for (int s = 0; s < 8; ++s)
-                            mma_f16_ts(o, tm + kTmS + 16 * s + 8, qd + (s >> 2) * kHalf + (s & 3) * 2, kIdescKK, 1);
-                    }
                 }
                 __syncwarp();
                 if (!wait(kUReady, n)) return false;
@@ -854,12 +852,8 @@ __device__ __forceinline__ bool make(const DeltaParams& p, int k, int& n, int& n
             store_split(tm + kTmU + kToks * part, y);
             tmem_wait_st();
             arrive_warp(kUReady, lane);
-            // for the outputs U itself, in R's place, while dS's products run
-            if (outputs) {
-                store_split(tm + kTmR + kToks * part, x);
-                tmem_wait_st();
-                arrive_warp(kPReady, lane);
-            }
+            // for the outputs U itself, in R's place, on its way while dS's products run
+            if (outputs) store_split(tm + kTmR + kToks * part, x);
         }
         // S
         const bool more = c + 1 < chunks;
@@ -877,6 +871,10 @@ __device__ __forceinline__ bool make(const DeltaParams& p, int k, int& n, int& n
         if (more) {
             if ((values && !wait(kTurned + (nv & 1), nv >> 1)) || !wait(kFull + ((n + 1) & 1), (n + 1) >> 1)) return false;
             rescale(n + 1, nv, adds);
+        }
+        if (outputs) {
+            tmem_wait_st();
+            arrive_warp(kPReady, lane);
         }
         if (!wait(kDDone, n)) return false;
         tc_fence_after();
@@ -981,6 +979,7 @@ kda_delta_walk(const __grid_constant__ DeltaParams p, const __grid_constant__ CU
             }
             done_with(k, lane);
         }
+        tmem_wait_st();  // (of an item that was left)
         tc_fence_before();
         __syncthreads();
     } else if (warp < kIssuer) {
