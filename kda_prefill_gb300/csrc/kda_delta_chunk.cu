@@ -16,12 +16,12 @@
 // bits, as T's in the end).  A power series of N would cancel: with equal keys its terms
 // grow to 10^18.
 //
-// The shared-memory port (3.7 K of 6 K cycles a chunk) and instructions are the bound, with 59 KB
-// written a chunk: 16384 tokens of 12 heads take 61 us, 128 sequences of 117,555 tokens 400 us, 4.6
-// and 4.0 TB/s with what is read.  So all accesses are of whole lines, addresses of fragments come
+// Writing 59 KB a chunk (3.0 to 3.5 TB/s; 67 KB took 12 to 18 % longer), the shared-memory port (61 %
+// of the cycles) and instructions are the bound: 16384 tokens of 12 heads take 60 us, 128 sequences
+// of 117,555 tokens 388 us, 4.7 and 4.1 TB/s with what is read.  So all accesses are of whole lines, addresses of fragments come
 // from a lane's own few, and T's blocks are products of MMAs (in fp32 they took 7.6 K cycles of
 // that port); four CTAs an SM fill each other's waits.  With k and q left to the walk, to make
-// the tiles itself, this kernel took 59 us, but the walk 176 instead of 140.
+// the tiles itself, this kernel took 59 us instead of 69 then, but the walk 176 instead of 140.
 //
 // An output's two terms may cancel (a large value overwritten by a small one), so neither is rounded to
 // 11 bits: q^ e^G is m 2^x q with 1 <= m < 2, and the row of q takes 2^x alone, P's row 1 / m and

@@ -18,23 +18,24 @@
 //   21-23  turn v over, so that a value row's tokens lie beside each other, and find its
 //          largest
 // The chain X, R, U, dS, S of one chunk after the other is the bound: 5 K cycles, 2.6 us, of which
-// the products are 1.8 K (46 cycles for one of 128 x 64 x 16, 65 for 128 x 128 x 16, A in tensor
-// memory) and their three round trips 1.1 K; the rest are the makers' instructions.  The roles
-// keep all else off the chain, and an SM has one CTA, whose registers then let a warp have all its
-// values of a step in flight (two CTAs of half as many registers took 10.7 K cycles a chunk).
-// An item's begin and end take 7 to 10 us.  12 heads: 16384 tokens in segments take 107 us (first
-// pass) and 62, 128 sequences of 117,555 tokens 488 us, the tensor pipe active for 24 % of the time.
+// its products are 1.8 K (46 cycles for one of 128 x 64 x 16, 65 for 128 x 128 x 16, A in tensor
+// memory) and their three round trips 1.1 K; the rest are the makers' instructions.  The outputs'
+// products, about 1.3 K, run meanwhile.  The roles keep all else off the chain, and an SM has one
+// CTA, whose registers then let a warp have all its values of a step in flight (two CTAs of half as
+// many registers took 10.7 K cycles a chunk).
+// An item's begin and end take 7 to 10 us.  12 heads: 16384 tokens in segments take 106 us (first
+// pass) and 69, 128 sequences of 117,555 tokens 488 us, the tensor pipe active for 23 and 28 % of the time.
 //
 // Rounding.  Operands are fp16: k and q exactly, up to their rows' powers of two and but for entries
 // below 2^-17 of a row's length; S, R, U, T and P as the sum of two (22 bits; with one, a state would
 // be off by 2^-12, and an output, whose terms may cancel, by as much of what the state held).
-// S, R and U of a row are scaled by
-// one power of two, from a bound that holds for all three: with |v| <= m and beta <= b in the
-// chunk, |R| <= b (m + |S|) and |U| <= b (m + |S| + 64 b m), since I - beta k k^T does not
-// lengthen a row for beta in [0, 2] and a token adds at most b m; |S| itself is bounded by
-// that of a chunk before and 64 b m of that chunk, so that no thread waits for another's
-// maximum.  The bound is up to 2^10 too large; fp16's exponent has room for it: a term is kept to
-// 2^-25 of 2^14, the bound.
+// S, R and U of a row are scaled by one power of two, from a bound that holds for all three: with
+// |v| <= m and beta <= b in the chunk, |R| <= b (m + |S|) and |U| <= b (m + |S| + 64 b m), since
+// I - beta k k^T does not lengthen a row for beta in [0, 2] and a token adds at most b m; |S| itself
+// is bounded by that of a chunk before and 64 b m of that chunk, so that no thread waits for
+// another's maximum.  The bound is up to 2^10 too large; fp16's exponent has room for it: a term
+// is kept to 2^-25 of 2^14, the bound.  What is smaller than 2^-29 or so of the most that the
+// chunk writes is lost beside it.
 //
 // Infinities and NaN stay in their value row (in v or the state) or sequence and head (in k)
 // from their token on: R's entries that are not finite become zero for the products and their

@@ -62,7 +62,9 @@ struct Entry {
 // Rows ahead and registers: a unit and its partner with their weights take 80 registers for two
 // rows, a unit alone 56 for four (16384 tokens, 12 + 12 heads, half layout: 37.1 us, 39.1 with
 // 72 registers, 41.2 with 64; 12 + 2 heads, pairs beside each other: 21.7 us, 23.0 with 64
-// registers, 24.9 with 48; each with the tokens of a CTA that suit it).
+// registers, 24.9 with 48; each with the tokens of a CTA that suit it).  These times and those at
+// the launch are of calls on one set of buffers, part of which stays in the L2: on alternating
+// ones the same calls take 39.2 us for 37.1 and 25.1 for 21.7.
 constexpr int regs_of(bool interleaved) { return interleaved ? 56 : 80; }
 
 // `units` units a row, at most LANES, the first rot_units of them turned.

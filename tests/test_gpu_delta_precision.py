@@ -80,3 +80,22 @@ def test_keys_of_entries_of_many_magnitudes():
     compare(c, most=2.5e-3)
     c["k"][:, :, :, 1:] *= 1e-6
     compare(c, most=2.5e-3)
+
+
+@pytest.mark.parametrize("n", [17, 64, 300])
+@pytest.mark.parametrize("big", [1e2, 1e4, 1e6])
+def test_small_states_in_the_chunk_of_large_values(n, big):
+    """A value row has one scale in a chunk, made from a bound that is at most 2^10 too large, and
+    terms are kept to 2^-39 of it: 2^-29 of the most that the chunk writes for each of an output's 128
+    terms, whose factors, of a vector no longer than one, add up to less than 2^4."""
+    c = make([n], 2, seed=74, init=[True], g=torch.full((1, n, 2), -0.01), state=1e-4)
+    late = n // 2
+    c["v"][:, :late] *= 1e-4
+    c["v"][:, late:] *= big
+    o, S, emag, smag = expected(c)
+    out = run(c)[0].double()
+    most = torch.zeros_like(emag)
+    for a in range(0, n, 64):
+        most[a:a + 64] = emag[a:a + 64].amax(0, keepdim=True)
+    lim = 2.0 ** -8 * o.abs() + 2.0 ** -16 * emag + 2.0 ** -25 * most
+    assert bool(((out - o).abs() <= lim).all()), float(((out - o).abs() / lim).max())
