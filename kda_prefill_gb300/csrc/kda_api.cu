@@ -494,7 +494,13 @@ int find_tables(const int32_t* cu_dev, const int32_t* cu_host, int32_t N, int64_
         int rc = check_host_bounds(cu_host, N, T);
         if (rc != KDA_OK) return rc;
     }
-    return cache().get(cu_host, N, step_max, stream, capturing, m);
+    // without a sequence in between, the tables are the same as those of kShortMax
+    bool between = false;
+    for (int32_t n = 0; n < N && !between; ++n) {
+        const int64_t len = (int64_t)cu_host[n + 1] - cu_host[n];
+        between = !is_short(len) && is_short(len, step_max);
+    }
+    return cache().get(cu_host, N, between ? step_max : kda::kShortMax, stream, capturing, m);
 }
 
 int run_forward(const void* q, const void* k, const void* v, const void* g_raw,

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import kda_prefill_gb300 as kda
-from tests.test_gpu_gated_delta import D, check, expected, make
+from tests.test_gpu_gated_delta import D, check, expected, make, run
 
 pytestmark = pytest.mark.gpu
 
@@ -152,3 +152,32 @@ def test_the_delta_rule_without_a_workspace(lengths, few):
     else:
         with pytest.raises((ValueError, kda.KDAError), match="workspace"):
             kda.gated_delta_fwd(*args, **kw, cu_seqlens_cpu=c["cu"], workspace=ws)
+
+
+@pytest.mark.parametrize("lengths,shared", [([90, 3, 0, 17], True), ([1] * 9, True), ([90, 9], False), ([16, 1], False)])
+def test_operators_share_the_tables_of_a_batch(lengths, shared):
+    """A batch without sequences of 9 to 16 tokens, which linear attention takes in a chunk and the
+    delta rule token by token, has one set of tables for both: either may be captured once the other ran."""
+    kda.release_cache()
+    call, right = lin_call(lengths, 95, H=2)
+    assert right is not None  # (it ran once)
+    c = make(lengths, 2, seed=96, init=[True] * len(lengths))
+    want, before = expected(c), c["storage"].clone()
+    n = kda.cache_entries()
+    check(c, run(c), want, before)
+    assert kda.cache_entries() - n == (0 if shared else 1)
+    if shared:
+        kda.release_cache()
+        call()
+        c["storage"].copy_(before)
+        out = torch.empty(c["v"].shape, dtype=torch.bfloat16, device="cuda")
+        args = c["q"], c["k"], c["v"], c["g"], c["beta"], c["cu"].cuda()
+        kw = dict(state_cache=c["cache"], state_indices=c["idx"].cuda(), has_initial_state=c["has"].cuda(), out=out,
+                  cu_seqlens_cpu=c["cu"])
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            kda.gated_delta_fwd(*args, **kw)
+        graph.replay()
+        torch.cuda.synchronize()
+        check(c, out, want, before)
